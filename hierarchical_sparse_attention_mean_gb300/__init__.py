@@ -30,7 +30,10 @@ LLSA_ENRICH_ALLK = 2
 _RULES = {"top1": LLSA_ENRICH_TOP1, "ancestor": LLSA_ENRICH_ANCESTOR, "allk": LLSA_ENRICH_ALLK}
 LLSA_ORDER_TILE, LLSA_ORDER_RASTER = 0, 1
 _ORDERS = {"tile": LLSA_ORDER_TILE, "raster": LLSA_ORDER_RASTER}
-OP_POOL, OP_SELECT, OP_FWD, OP_TRANSPOSE, OP_BWD = range(5)
+OP_POOL, OP_SELECT, OP_FWD, OP_TRANSPOSE, OP_BWD, OP_DENSE_FWD, OP_DENSE_BWD = range(7)
+LLSA_ROPE_HALF, LLSA_ROPE_INTERLEAVED = 0, 1
+_ROPE_LAYOUTS = {"half": LLSA_ROPE_HALF, "interleaved": LLSA_ROPE_INTERLEAVED}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3}
 MAX_LEVELS = 8
 
 
@@ -59,6 +62,21 @@ class _Sizes(ctypes.Structure):
                 ("coarse_cols", ctypes.c_int), ("enrich_cols", ctypes.c_int)]
 
 
+class _DenseParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d", "dtype", "causal")] + [
+        ("scale", ctypes.c_float)]
+
+
+class _RopeParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "n", "d", "rot_dim", "layout", "axes", "width",
+                                            "token_order", "pos_offset", "pos_batched", "dtype", "scaling", "orig_len")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "low", "high", "amplitude")]
+
+
+class _RopeStrides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_longlong * 3) for n in ("q", "k", "q_out", "k_out")]
+
+
 def lib_path() -> str:
     return _LIB_PATH
 
@@ -83,6 +101,12 @@ def _load():
     lib.llsa_reorder.argtypes = [P, ctypes.c_int, ctypes.c_int, vp, vp, ctypes.c_int, vp]
     lib.llsa_select_exhaustive.argtypes = [P, vp, vp, vp]
     lib.llsa_bwd.argtypes = [P] + [vp] * 14 + [vp, sz, vp]
+    DP = ctypes.POINTER(_DenseParams)
+    lib.llsa_dense_workspace_bytes.argtypes = [DP, ctypes.c_int]
+    lib.llsa_dense_workspace_bytes.restype = sz
+    lib.llsa_dense_fwd.argtypes = [DP] + [vp] * 8 + [sz, vp]
+    lib.llsa_dense_bwd.argtypes = [DP] + [vp] * 12 + [sz, vp]
+    lib.llsa_rope.argtypes = [ctypes.POINTER(_RopeParams), ctypes.POINTER(_RopeStrides)] + [vp] * 5 + [ctypes.c_int, vp]
     lib.llsa_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     lib.llsa_strerror.argtypes = [ctypes.c_int]
     lib.llsa_strerror.restype = ctypes.c_char_p
@@ -141,6 +165,97 @@ class Params:
         if dtype is None:
             raise ValueError("q must be bfloat16 or float32")
         return Params(b, h, n, d, dtype=dtype, **kw)
+
+
+_DTYPES = {"bf16": LLSA_DTYPE_BF16, "fp32": LLSA_DTYPE_F32}
+
+
+def _choice(table, value, name):
+    got = table.get(value)
+    if got is None:
+        raise ValueError(f"{name} must be one of {', '.join(map(repr, table))}, not {value!r}")
+    return got
+
+
+def _dtype_name(t):
+    import torch
+    name = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(t.dtype)
+    if name is None:
+        raise ValueError("q must be bfloat16 or float32")
+    return name
+
+
+@dataclass(frozen=True)
+class DenseParams:
+    """A dense-attention problem; mirrors llsa_dense_params of include/llsa.h."""
+    batch: int
+    heads: int
+    nq: int
+    nk: int
+    d: int
+    kv_heads: int = 0          # 0: as many as heads
+    causal: bool = False       # the last query sees the last key
+    dtype: str = "bf16"        # "bf16" or "fp32"
+    scale: float = 0.0         # 0: 1/sqrt(d)
+
+    def __post_init__(self):
+        object.__setattr__(self, "_c", _DenseParams(
+            self.batch, self.heads, self.kv_heads, self.nq, self.nk, self.d, _choice(_DTYPES, self.dtype, "dtype"),
+            1 if self.causal else 0, self.scale))
+
+    def c(self) -> _DenseParams:
+        return self._c
+
+    @staticmethod
+    def like(q, k, **kw) -> "DenseParams":
+        b, h, n, d = q.shape
+        return DenseParams(b, h, n, k.shape[2], d, kv_heads=k.shape[1], dtype=_dtype_name(q), **kw)
+
+    def shapes(self):
+        """Shapes of q (and o, dout, dq), of k (and v, dk, dv) and of lse."""
+        return ((self.batch, self.heads, self.nq, self.d),
+                (self.batch, self.kv_heads or self.heads, self.nk, self.d), (self.batch, self.heads, self.nq))
+
+
+@dataclass(frozen=True)
+class RopeParams:
+    """Rotary positions of q and k; mirrors llsa_rope_params of include/llsa.h."""
+    batch: int
+    heads: int
+    n: int
+    d: int
+    kv_heads: int = 0            # heads of k; 0: no k
+    rot_dim: int = 0             # columns turned; 0: d
+    layout: str = "half"         # pairs: "half" (i, i + h) or "interleaved" (2i, 2i + 1)
+    axes: int = 1                # 1, or 2 (row and column, half of the columns each)
+    width: int = 0               # image width (axes 2; ignored with pos)
+    token_order: str = "raster"  # "raster" or "tile" (axes 2; ignored with pos)
+    pos_offset: int = 0          # position of token 0 (axes 1; ignored with pos)
+    base: float = 10000.0
+    scaling: str = "none"        # "none", "linear", "base" or "wavelength"
+    factor: float = 1.0
+    orig_len: int = 0            # "wavelength": positions the model was trained on
+    low: float = 1.0             # "wavelength": turns over orig_len below which a pair is stretched fully
+    high: float = 32.0           # and above which it is kept
+    amplitude: float = 0.0       # 0: 1, or 0.1 ln(factor) + 1 for "wavelength"
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        scaling, order = _choice(_ROPE_SCALINGS, self.scaling, "scaling"), _choice(_ORDERS, self.token_order, "token_order")
+        layout, dt = _choice(_ROPE_LAYOUTS, self.layout, "layout"), _choice(_DTYPES, self.dtype, "dtype")
+        for batched in (0, 1):
+            object.__setattr__(self, f"_c{batched}", _RopeParams(
+                self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width, order,
+                self.pos_offset, batched, dt, scaling, self.orig_len, self.base, self.factor, self.low, self.high,
+                self.amplitude))
+
+    def c(self, pos_batched: bool = False) -> _RopeParams:
+        return self._c1 if pos_batched else self._c0
+
+    @staticmethod
+    def like(q, k=None, **kw) -> "RopeParams":
+        b, h, n, d = q.shape
+        return RopeParams(b, h, n, d, kv_heads=0 if k is None else k.shape[1], dtype=_dtype_name(q), **kw)
 
 
 @dataclass(frozen=True)
@@ -280,6 +395,112 @@ def llsa_bwd(p: Params, q, k, v, o, lse, dout, pyr, sel_idx, coarse_idx, col_ptr
                             _ptr(sel_idx, "sel_idx", i32), _ptr(coarse_idx, "coarse_idx", i32),
                             _ptr(col_ptr, "col_ptr", i32), _ptr(row_idx, "row_idx", i32), _ptr(dq, "dq", td),
                             _ptr(dk, "dk", td), _ptr(dv, "dv", td), w, wb, _stream(stream)), "llsa_bwd")
+
+
+def _like(t, name, shape, dtype, device):
+    """Pointer of a contiguous tensor of exactly this shape, type and device."""
+    ptr = _ptr(t, name, dtype)
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return ptr
+
+
+def _on(t, name):
+    """The device of the call: that of its first tensor, which becomes the current one."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch.cuda.device(t.device)
+
+
+def dense_workspace_bytes(p: DenseParams, op: int) -> int:
+    """Workspace of llsa_dense_fwd (OP_DENSE_FWD) or llsa_dense_bwd (OP_DENSE_BWD)."""
+    return int(_load().llsa_dense_workspace_bytes(ctypes.byref(p.c()), op))
+
+
+def _lens(p, q_len, k_len, device):
+    import torch
+    return tuple(None if x is None else _like(x, name, (p.batch,), torch.int32, device)
+                 for x, name in ((q_len, "q_len"), (k_len, "k_len")))
+
+
+def llsa_dense_fwd(p: DenseParams, q, k, v, o, lse, q_len=None, k_len=None, ws=None, stream=None):
+    """Dense attention: o and lse of q over k, v (llsa_dense_fwd of include/llsa.h)."""
+    import torch
+    with _on(q, "q"):
+        td, dev, (sq, sk, sl) = _tok_dtype(p), q.device, p.shapes()
+        ql, kl = _lens(p, q_len, k_len, dev)
+        w, wb = _ws(ws)
+        _check(_load().llsa_dense_fwd(ctypes.byref(p.c()), _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
+                                      _like(v, "v", sk, td, dev), ql, kl, _like(o, "o", sq, td, dev),
+                                      _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_dense_fwd")
+
+
+def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None, k_len=None, ws=None, stream=None):
+    """Gradients of dense attention (llsa_dense_bwd of include/llsa.h)."""
+    import torch
+    with _on(q, "q"):
+        td, dev, (sq, sk, sl) = _tok_dtype(p), q.device, p.shapes()
+        ql, kl = _lens(p, q_len, k_len, dev)
+        w, wb = _ws(ws)
+        _check(_load().llsa_dense_bwd(ctypes.byref(p.c()), _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
+                                      _like(v, "v", sk, td, dev), _like(o, "o", sq, td, dev),
+                                      _like(lse, "lse", sl, torch.float32, dev), _like(dout, "dout", sq, td, dev), ql, kl,
+                                      _like(dq, "dq", sq, td, dev), _like(dk, "dk", sk, td, dev),
+                                      _like(dv, "dv", sk, td, dev), w, wb, _stream(stream)), "llsa_dense_bwd")
+
+
+def _strided(t, name, shape, dtype, device, out):
+    """Pointer of a [batch, heads, n, d] tensor whose columns are contiguous; its
+    batch, head and token strides go into `out`."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    out[0], out[1], out[2] = s[0], s[1], s[2]
+    return t.data_ptr()
+
+
+def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False, stream=None):
+    """Rotary positions of q and k (None where p.kv_heads is 0) into q_out and
+    k_out, in one launch. All may be strided views with contiguous columns, and
+    a tensor may be its own output. pos: int32 [n], [n, axes], or either with a
+    leading batch dimension. inverse: the negative angles (the gradient)."""
+    import torch
+    with _on(q, "q"):
+        td, dev, st = _tok_dtype(p), q.device, _RopeStrides()
+        shape = (p.batch, p.heads, p.n, p.d)
+        a, c = _strided(q, "q", shape, td, dev, st.q), _strided(q_out, "q_out", shape, td, dev, st.q_out)
+        b = d = None
+        if p.kv_heads:
+            shape = (p.batch, p.kv_heads, p.n, p.d)
+            b, d = _strided(k, "k", shape, td, dev, st.k), _strided(k_out, "k_out", shape, td, dev, st.k_out)
+        elif k is not None or k_out is not None:
+            raise ValueError("k and k_out must be None where kv_heads is 0")
+        at, batched = None, False
+        if pos is not None:
+            shape = tuple(pos.shape) + (1,) if p.axes == 1 and pos.ndim < 3 and pos.shape[-1:] == (p.n,) else tuple(pos.shape)
+            if shape == (p.batch, p.n, p.axes):
+                batched = True
+            elif shape != (p.n, p.axes):
+                raise ValueError(f"pos must have shape [n, axes] or [batch, n, axes], got {tuple(pos.shape)}")
+            at = _like(pos, "pos", pos.shape, torch.int32, dev)
+        _check(_load().llsa_rope(ctypes.byref(p.c(batched)), ctypes.byref(st), a, b, at, c, d, 1 if inverse else 0,
+                                 _stream(stream)), "llsa_rope")
 
 
 def llsa_get_status(stream=None) -> int:
@@ -422,6 +643,56 @@ def backward(p: Params, q, k, v, dout, b: Buffers, dq=None, dk=None, dv=None, st
     return dq, dk, dv
 
 
+def _dense_ws(p: DenseParams, op: int, device, stream):
+    """The workspace of one call (None where it needs none), kept until `stream` is done with it."""
+    import torch
+    need = dense_workspace_bytes(p, op)
+    if need == 0:
+        return None
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    if stream is not None:
+        ws.record_stream(_as_stream(stream, device))
+    return ws
+
+
+def dense_forward(p: DenseParams, q, k, v, q_len=None, k_len=None, o=None, lse=None, ws=None, stream=None):
+    """Dense attention of q over k, v. Returns (o, lse); what is not given is
+    allocated here."""
+    import torch
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty(p.shapes()[2], dtype=torch.float32, device=q.device) if lse is None else lse
+    ws = _dense_ws(p, OP_DENSE_FWD, q.device, stream) if ws is None else ws
+    llsa_dense_fwd(p, q, k, v, o, lse, q_len, k_len, ws, stream)
+    return o, lse
+
+
+def dense_backward(p: DenseParams, q, k, v, o, lse, dout, q_len=None, k_len=None, dq=None, dk=None, dv=None, ws=None,
+                   stream=None):
+    """Gradients of dense_forward(). Returns (dq, dk, dv)."""
+    import torch
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    ws = _dense_ws(p, OP_DENSE_BWD, q.device, stream) if ws is None else ws
+    llsa_dense_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, q_len, k_len, ws, stream)
+    return dq, dk, dv
+
+
+def _check_rope(p: RopeParams, q, k, name="rope"):
+    want = (p.batch, p.heads, p.n, p.d)
+    if tuple(q.shape) != want or (k is not None and tuple(k.shape) != (p.batch, p.kv_heads, p.n, p.d)):
+        raise ValueError(f"{name} is for q {want} and {p.kv_heads} heads of k, got q {tuple(q.shape)}"
+                         + ("" if k is None else f" and k {tuple(k.shape)}"))
+
+
+def _rope_view(t):
+    """t, or a contiguous copy where its strides are none that llsa_rope takes."""
+    unit = 16 // t.element_size()
+    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
+        t.stride(i) % unit == 0 for i in range(3) if t.shape[i] > 1)
+    return t if ok else t.contiguous()
+
+
 def _autograd_function():
     import torch
 
@@ -429,36 +700,129 @@ def _autograd_function():
         """Differentiable LLSA over [batch, heads, N, d] tensors."""
 
         @staticmethod
-        def forward(ctx, q, k, v, block, topk, levels, enrich_levels, scale, token_order):
-            q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        def forward(ctx, q, k, v, block, topk, levels, enrich_levels, scale, token_order, rope, pos):
+            ctx.rope = rope
+            if rope is None:
+                q, k = q.contiguous(), k.contiguous()
+            else:
+                q, k = _rotated(rope, q, k, pos)
+            v = v.contiguous()
             p = Params.like(q, block=block, topk=topk, levels=levels, enrich_levels=enrich_levels, scale=scale,
                             token_order=token_order)
             b = forward(p, q, k, v)
             ctx.p, ctx.b = p, b
-            ctx.save_for_backward(q, k, v)
+            ctx.save_for_backward(q, k, v, *([] if rope is None or pos is None else [pos]))
             return b.o
 
         @staticmethod
         def backward(ctx, do):
-            q, k, v = ctx.saved_tensors
+            q, k, v, *pos = ctx.saved_tensors
             dq, dk, dv = backward(ctx.p, q, k, v, do.contiguous(), ctx.b)
-            return dq, dk, dv, None, None, None, None, None, None
+            if ctx.rope is not None:
+                llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos[0] if pos else None, inverse=True)
+            return dq, dk, dv, None, None, None, None, None, None, None, None
 
     return LLSAFunction
+
+
+def _rotated(rope, q, k, pos, inverse=False):
+    """Head-major contiguous copies of q and k (None allowed) with their positions turned in."""
+    import torch
+    _check_rope(rope, q, k)
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    llsa_rope(rope, _rope_view(q), None if k is None else _rope_view(k), q_out, k_out, pos=pos, inverse=inverse)
+    return q_out, k_out
 
 
 _FN = None
 
 
 def llsa_attention(q, k, v, block: int = 16, topk: int = 8, levels: int = 0, enrich_levels: int = -1,
-                   scale: float = 0.0, token_order: str = "tile"):
+                   scale: float = 0.0, token_order: str = "tile", rope: RopeParams | None = None, pos=None):
     """Autograd entry point: o = LLSA(q, k, v). token_order "raster": q, k, v
     (and o, the gradients) are in the raster order of a square image, reordered
-    inside the kernels."""
+    inside the kernels. rope: rotary positions for q and k (with `pos`, or the
+    positions that the parameters imply; its token_order is its own)."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()
-    return _FN.apply(q, k, v, block, topk, levels, enrich_levels, scale, token_order)
+    return _FN.apply(q, k, v, block, topk, levels, enrich_levels, scale, token_order, rope, pos)
+
+
+def _dense_functions():
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class DenseFunction(torch.autograd.Function):
+        """Differentiable dense attention, with rotary positions if asked."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, causal, scale, q_len, k_len, rope, pos):
+            if rope is None:
+                q, k = q.contiguous(), k.contiguous()
+            else:
+                q, k = _rotated(rope, q, k, pos)
+            v = v.contiguous()
+            p = DenseParams.like(q, k, causal=causal, scale=scale)
+            o, lse = dense_forward(p, q, k, v, q_len, k_len)
+            ctx.p, ctx.rope = p, rope
+            ctx.save_for_backward(q, k, v, o, lse, q_len, k_len, pos)
+            return o
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, do):
+            q, k, v, o, lse, q_len, k_len, pos = ctx.saved_tensors
+            dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, do.contiguous(), q_len, k_len)
+            if ctx.rope is not None:
+                llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
+            return dq, dk, dv, None, None, None, None, None, None
+
+    class RotaryFunction(torch.autograd.Function):
+        """Differentiable rotary positions of q and k."""
+
+        @staticmethod
+        def forward(ctx, q, k, rope, pos):
+            ctx.rope = rope
+            ctx.save_for_backward(pos)
+            return _rotated(rope, q, k, pos)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dq, dk):
+            (pos,) = ctx.saved_tensors
+            dq, dk = _rotated(ctx.rope, dq, dk, pos, inverse=True)
+            return dq, dk, None, None
+
+    return DenseFunction, RotaryFunction
+
+
+_DENSE_FNS = None
+
+
+def _dense_fns():
+    global _DENSE_FNS
+    if _DENSE_FNS is None:
+        _DENSE_FNS = _dense_functions()
+    return _DENSE_FNS
+
+
+def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=None, k_len=None,
+                    rope: RopeParams | None = None, pos=None):
+    """Autograd entry point of dense attention: q [batch, heads, nq, d] over k, v
+    [batch, kv_heads, nk, d]. q_len, k_len: int32 [batch] valid tokens of a
+    padded batch. rope: rotary positions for q and k of the same tokens."""
+    return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)
+
+
+def rotary(q, k=None, rope: RopeParams | None = None, pos=None):
+    """Autograd entry point of rotary positions: (q, k) turned, head-major and
+    contiguous (k None: q alone). Strided inputs are read in place."""
+    if rope is None:
+        rope = RopeParams.like(q, k)
+    out = _dense_fns()[1].apply(q, k, rope, pos)
+    return out if k is not None else out[0]
 
 
 def default_scale(d: int) -> float:

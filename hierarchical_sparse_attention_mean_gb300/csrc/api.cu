@@ -5,13 +5,11 @@
 #include <string.h>
 
 #include <atomic>
-#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
 
-#include <nvtx3/nvToolsExt.h>
-
+#include "entry.h"
 #include "internal.h"
 #include "tc.cuh"
 
@@ -188,24 +186,7 @@ static int derive(const llsa_params* p, Shape* s) {
     return LLSA_OK;
 }
 
-static bool aligned(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
-
-static int check_ptrs(std::initializer_list<const void*> ptrs) {
-    for (const void* q : ptrs) {
-        if (!q) return LLSA_ERR_INVALID_ARG;
-        if (!aligned(q)) return LLSA_ERR_ALIGN;
-    }
-    return LLSA_OK;
-}
-
 static size_t transpose_ws(const Shape& s) { return (size_t)s.slices * s.T * sizeof(int32_t); }
-
-// An NVTX range around a C-ABI call (the call's name), so a profiler timeline
-// shows each library call with the kernels it enqueued.
-struct CallRange {
-    explicit CallRange(const char* name) { nvtxRangePushA(name); }
-    ~CallRange() { nvtxRangePop(); }
-};
 
 int wait_limit() {
     const int v = g_wait_limit.load();

@@ -1,0 +1,111 @@
+// dense.h -- what the dense attention kernels share: their arguments, the
+// mask's arithmetic and the launchers.
+//
+// Rows. The query heads that share a key head lie next to each other in
+// [batch, heads, nq, d], so the kernels see batch * kv_heads slices of
+// G * nq query rows (G = heads / kv_heads) over nk keys: row r of a slice is
+// token r % nq of the slice's head r / nq. One pass over K and V then serves
+// all heads that share them, a single token's G heads included, and dk, dv sum
+// over those heads in one place.
+//
+// Mask. Every rule of the call (lengths, padding, causal order) leaves row r
+// the keys 0 .. kend(r) - 1, so one number per row is the mask.
+#pragma once
+
+#include "internal.h"
+
+namespace llsa {
+
+constexpr float kDenseLog2e = 1.4426950408889634f;
+constexpr int kDenseRowPad = 128;  // rows of a slice in the per-row arrays: a multiple of this
+constexpr int kDenseMaxExtent = 1 << 30;  // rows of a slice, keys of a slice
+constexpr int kDenseSms = 152;  // splits, and so the workspace, go by the GB300's SMs
+
+struct DenseShape {
+    int batch, heads, kv_heads, G, nq, nk, d, dtype, causal;
+    int slices;   // batch * kv_heads
+    int R, Rp;    // rows per slice, and padded to kDenseRowPad
+    float scale;
+};
+
+struct DenseArgs {
+    const void *q, *k, *v, *o, *dout;
+    const float* lse;
+    const int *q_len, *k_len;
+    void *o_out, *dq, *dk, *dv;
+    float* lse_out;
+    float* l2;    // [slices][Rp]: lse * log2(e); +infinity for rows without keys
+    float* dsum;  // [slices][Rp]: D = dout . o
+    float* part;  // partial sums of a split axis (layout: see the kernels)
+    int splits, chunk;  // parts of the split axis, and how many of its elements each takes
+    int slices, kv_heads, nq, nk, R, Rp, d, causal;
+    float scale;
+    int* status;
+    int spin, test_flags;
+};
+
+struct DenseSpan {
+    int lq, lk;
+};
+
+// Valid query and key tokens of a slice's batch entry.
+__device__ __forceinline__ DenseSpan dense_span(const DenseArgs& a, int slice) {
+    const int b = slice / a.kv_heads;
+    DenseSpan s;
+    s.lq = a.nq;
+    s.lk = a.nk;
+    if (a.q_len) {
+        const int v = __ldg(a.q_len + b);
+        s.lq = min(max(v, 0), a.nq);
+        if (s.lq != v) set_status(a.status, LLSA_ERR_BAD_INDEX);
+    }
+    if (a.k_len) {
+        const int v = __ldg(a.k_len + b);
+        s.lk = min(max(v, 0), a.nk);
+        if (s.lk != v) set_status(a.status, LLSA_ERR_BAD_INDEX);
+    }
+    return s;
+}
+
+// Keys that token t of a head sees: 0 .. kend - 1.
+__device__ __forceinline__ int dense_kend(const DenseArgs& a, DenseSpan s, int t) {
+    if (t >= s.lq) return 0;
+    return a.causal ? min(max(t + s.lk - s.lq + 1, 0), s.lk) : s.lk;
+}
+
+// A bound on kend over `rows` consecutive rows whose first is token t0 of its
+// head (they may run into the next heads); 0 when none of them sees a key.
+__device__ __forceinline__ int dense_tile_kend(const DenseArgs& a, DenseSpan s, int t0, int rows) {
+    const bool wraps = t0 + rows > a.nq;
+    if (!wraps && t0 >= s.lq) return 0;
+    const int last = wraps ? s.lq - 1 : min(t0 + rows, s.lq) - 1;
+    return last < 0 ? 0 : dense_kend(a, s, last);
+}
+
+size_t dense_fwd_workspace(const DenseShape& s);
+size_t dense_bwd_workspace(const DenseShape& s);
+int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
+int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
+
+// How a long axis is split where the other one gives too few blocks: `blocks`
+// independent blocks, `units` tiles of the long axis, at least `least` tiles
+// per part.
+inline int dense_splits(long long blocks, long long units, long long least, int resident) {
+    if (blocks <= 0 || units <= 0) return 1;
+    long long s = resident / blocks;  // parts that still fit one wave
+    if (s > units / least) s = units / least;
+    return s < 2 ? 1 : s > 128 ? 128 : (int)s;
+}
+
+// dense_simt.cu: CUDA-core kernels (any type and head dimension).
+struct DenseSplit {
+    int splits, chunk;
+};
+DenseSplit dense_simt_fwd_split(const DenseShape& s);
+DenseSplit dense_simt_dq_split(const DenseShape& s);
+DenseSplit dense_simt_dkv_split(const DenseShape& s);
+int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+
+}  // namespace llsa

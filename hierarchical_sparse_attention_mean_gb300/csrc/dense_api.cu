@@ -1,0 +1,317 @@
+// dense_api.cu -- the C entries of dense attention: validation, workspace,
+// choice of kernels, and the passes around the attention kernels (the per-row
+// numbers of the backward pass, the joins of a split axis).
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "dense.h"
+#include "entry.h"
+
+namespace llsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// ------------------------------------------------------ per-row numbers --
+
+// l2 = lse * log2(e) and D = dout . o of every query row; rows that see no key
+// (and the padding to Rp) get l2 = +infinity, so that their probabilities are
+// 2^(s - l2) = 0, and D = 0. Eight lanes per row. Bound by HBM: dout and o are
+// read once.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dense_rows_kernel(DenseArgs a) {
+    const long long idx = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 3;
+    const int part = threadIdx.x & 7;
+    const int slice = (int)(idx / a.Rp), r = (int)(idx - (long long)slice * a.Rp);
+    if (slice >= a.slices) return;  // whole groups of eight lanes leave together
+    float lse = -INFINITY, sum = 0.f;
+    if (r < a.R && dense_kend(a, dense_span(a, slice), r % a.nq) > 0) {
+        const long long row = (long long)slice * a.R + r;
+        lse = __ldg(a.lse + row);
+        const T* g = static_cast<const T*>(a.dout) + row * a.d;
+        const T* o = static_cast<const T*>(a.o) + row * a.d;
+        for (int c = part * 8; c < a.d; c += 64) {
+            float x[8], y[8];
+            load8(g + c, x);
+            load8(o + c, y);
+#pragma unroll
+            for (int i = 0; i < 8; i++) sum = fmaf(x[i], y[i], sum);
+        }
+    }
+    const unsigned lanes = 0xffu << (threadIdx.x & 24);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
+    if (part == 0) {
+        a.l2[idx] = lse == -INFINITY ? INFINITY : lse * kDenseLog2e;
+        a.dsum[idx] = lse == -INFINITY ? 0.f : sum;
+    }
+}
+
+// ------------------------------------------------------- joins of a split --
+
+// o and lse of every query row from the parts of a split over the keys: a warp
+// per row, the parts in ascending order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(DenseArgs a) {
+    const long long rows = (long long)a.slices * a.R;
+    const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.part + (long long)a.splits * rows * a.d);
+    float m = -INFINITY;
+    for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[p * rows + row].x);
+    m = warp_max(m);
+    const float shift = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int p = 0; p < a.splits; p++) {
+        const float2 x = ml[p * rows + row];
+        l = fmaf(x.y, exp2f(x.x - shift), l);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    for (int c = lane * 4; c < a.d; c += 128) {
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < a.splits; p++) {
+            const float w = exp2f(ml[p * rows + row].x - shift);
+            const float4 x = *reinterpret_cast<const float4*>(a.part + (p * rows + row) * a.d + c);
+            acc[0] = fmaf(w, x.x, acc[0]);
+            acc[1] = fmaf(w, x.y, acc[1]);
+            acc[2] = fmaf(w, x.z, acc[2]);
+            acc[3] = fmaf(w, x.w, acc[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) acc[i] *= inv;
+        store4(static_cast<T*>(a.o_out) + row * a.d + c, acc);
+    }
+    if (lane == 0) a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+}
+
+// out = the sum of `parts` fp32 arrays of n values, in ascending order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dense_join_sum_kernel(const float* part, T* out, long long n, int parts) {
+    const long long i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 4;
+    if (i >= n) return;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < parts; p++) {
+        const float4 x = *reinterpret_cast<const float4*>(part + p * n + i);
+        acc[0] += x.x;
+        acc[1] += x.y;
+        acc[2] += x.z;
+        acc[3] += x.w;
+    }
+    store4(out + i, acc);
+}
+
+template <typename T>
+int join_sum(const float* part, void* out, long long n, int parts, cudaStream_t st) {
+    const long long blocks = (n / 4 + kThreads - 1) / kThreads;
+    LLSA_LAUNCH("dense_join_sum", st,
+                dense_join_sum_kernel<T><<<(unsigned)blocks, kThreads, 0, st>>>(part, static_cast<T*>(out), n, parts));
+    return LLSA_OK;
+}
+
+int derive_dense(const llsa_dense_params* p, DenseShape* s) {
+    if (!p) return LLSA_ERR_INVALID_ARG;
+    if (p->batch < 0 || p->heads < 0 || p->kv_heads < 0 || p->nq < 0 || p->nk < 0) return LLSA_ERR_INVALID_ARG;
+    if (p->dtype != LLSA_DTYPE_BF16 && p->dtype != LLSA_DTYPE_F32) return LLSA_ERR_DTYPE;
+    if (p->causal != 0 && p->causal != 1) return LLSA_ERR_INVALID_ARG;
+    if (!(p->scale >= 0.0f) || isinf(p->scale)) return LLSA_ERR_INVALID_ARG;
+    if (p->d < 8 || p->d > 256 || p->d % 8 != 0) return LLSA_ERR_SHAPE;
+    memset(s, 0, sizeof(*s));
+    s->batch = p->batch;
+    s->heads = p->heads;
+    s->kv_heads = p->kv_heads ? p->kv_heads : p->heads;
+    if (s->heads == 0) {
+        if (s->kv_heads != 0) return LLSA_ERR_SHAPE;
+    } else if (s->heads % s->kv_heads != 0) {
+        return LLSA_ERR_SHAPE;
+    }
+    s->G = s->heads ? s->heads / s->kv_heads : 0;
+    s->nq = p->nq;
+    s->nk = p->nk;
+    s->d = p->d;
+    s->dtype = p->dtype;
+    s->causal = p->causal;
+    s->scale = p->scale > 0.0f ? p->scale : 1.0f / sqrtf((float)p->d);
+    const long long slices = (long long)s->batch * s->kv_heads, R = (long long)s->G * s->nq;
+    if (slices > kDenseMaxExtent || R > kDenseMaxExtent || s->nk > kDenseMaxExtent) return LLSA_ERR_UNSUPPORTED;
+    s->slices = (int)slices;
+    s->R = (int)R;
+    s->Rp = (s->R + kDenseRowPad - 1) / kDenseRowPad * kDenseRowPad;
+    if (slices * std::max<long long>(s->Rp, s->nk) * s->d > (1LL << 40)) return LLSA_ERR_UNSUPPORTED;
+    return LLSA_OK;
+}
+
+DenseArgs dense_args(const DenseShape& s) {
+    DenseArgs a;
+    memset(&a, 0, sizeof(a));
+    a.splits = 1;
+    a.slices = s.slices;
+    a.kv_heads = s.kv_heads;
+    a.nq = s.nq;
+    a.nk = s.nk;
+    a.R = s.R;
+    a.Rp = s.Rp;
+    a.d = s.d;
+    a.causal = s.causal;
+    a.scale = s.scale;
+    a.status = status_ptr();
+    a.spin = wait_limit();
+    a.test_flags = test_flags();
+    return a;
+}
+
+int check_lens(const int32_t* q_len, const int32_t* k_len) {
+    if ((reinterpret_cast<uintptr_t>(q_len) | reinterpret_cast<uintptr_t>(k_len)) & 3u) return LLSA_ERR_ALIGN;
+    return LLSA_OK;
+}
+
+DenseSplit fwd_split(const DenseShape& s) { return dense_simt_fwd_split(s); }
+DenseSplit dq_split(const DenseShape& s) { return dense_simt_dq_split(s); }
+DenseSplit dkv_split(const DenseShape& s) { return dense_simt_dkv_split(s); }
+
+}  // namespace
+
+size_t dense_fwd_workspace(const DenseShape& s) {
+    const DenseSplit p = fwd_split(s);
+    return p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0;
+}
+
+size_t dense_bwd_workspace(const DenseShape& s) {
+    const DenseSplit pq = dq_split(s), pk = dkv_split(s);
+    const size_t dq = pq.splits > 1 ? (size_t)pq.splits * s.slices * s.R * s.d * sizeof(float) : 0;
+    const size_t dkv = pk.splits > 1 ? (size_t)pk.splits * 2 * s.slices * s.nk * s.d * sizeof(float) : 0;
+    return 2 * align_up((size_t)s.slices * s.Rp * sizeof(float)) + std::max(dq, dkv);
+}
+
+int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
+    if (s.R == 0) return LLSA_OK;
+    const DenseSplit p = fwd_split(s);
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.part = static_cast<float*>(ws);
+    LLSA_TRY(launch_dense_simt_fwd(s, a, st));
+    if (p.splits > 1) {
+        const long long rows = (long long)s.slices * s.R;
+        const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+        if (s.dtype == LLSA_DTYPE_BF16)
+            LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
+        else
+            LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<float><<<blocks, kThreads, 0, st>>>(a));
+    }
+    return LLSA_OK;
+}
+
+int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
+    const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
+    const size_t rows = align_up((size_t)s.slices * s.Rp * sizeof(float));
+    a.l2 = static_cast<float*>(ws);
+    a.dsum = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * rows);
+    if (s.R > 0) {
+        const long long blocks = (long long)s.slices * s.Rp / (kThreads / 8);
+        if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+        if (bf16)
+            LLSA_LAUNCH("dense_rows", st, dense_rows_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, st>>>(a));
+        else
+            LLSA_LAUNCH("dense_rows", st, dense_rows_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>(a));
+        const DenseSplit p = dq_split(s);
+        a.splits = p.splits;
+        a.chunk = p.chunk;
+        LLSA_TRY(launch_dense_simt_dq(s, a, st));
+        if (p.splits > 1) {
+            const long long n = (long long)s.slices * s.R * s.d;
+            LLSA_TRY(bf16 ? join_sum<__nv_bfloat16>(a.part, a.dq, n, p.splits, st)
+                          : join_sum<float>(a.part, a.dq, n, p.splits, st));
+        }
+    }
+    if (s.nk > 0) {
+        const DenseSplit p = dkv_split(s);
+        a.splits = p.splits;
+        a.chunk = p.chunk;
+        LLSA_TRY(launch_dense_simt_dkv(s, a, st));
+        if (p.splits > 1) {
+            const long long n = (long long)s.slices * s.nk * s.d;
+            const float* second = a.part + (long long)p.splits * n;
+            LLSA_TRY(bf16 ? join_sum<__nv_bfloat16>(a.part, a.dk, n, p.splits, st)
+                          : join_sum<float>(a.part, a.dk, n, p.splits, st));
+            LLSA_TRY(bf16 ? join_sum<__nv_bfloat16>(second, a.dv, n, p.splits, st)
+                          : join_sum<float>(second, a.dv, n, p.splits, st));
+        }
+    }
+    return LLSA_OK;
+}
+
+}  // namespace llsa
+
+using namespace llsa;
+
+extern "C" {
+
+size_t llsa_dense_workspace_bytes(const llsa_dense_params* p, int op) {
+    DenseShape s;
+    if (derive_dense(p, &s) != LLSA_OK || s.slices == 0) return 0;
+    switch (op) {
+        case LLSA_OP_DENSE_FWD: return dense_fwd_workspace(s);
+        case LLSA_OP_DENSE_BWD: return dense_bwd_workspace(s);
+        default: return 0;
+    }
+}
+
+int llsa_dense_fwd(const llsa_dense_params* p, const void* q, const void* k, const void* v, const int32_t* q_len,
+                   const int32_t* k_len, void* o, float* lse, void* ws, size_t ws_bytes, void* stream) {
+    CallRange range("llsa_dense_fwd");
+    DenseShape s;
+    LLSA_TRY(derive_dense(p, &s));
+    if (s.slices == 0 || s.R == 0) return LLSA_OK;
+    LLSA_TRY(check_ptrs({q, o, lse}));
+    if (s.nk > 0) LLSA_TRY(check_ptrs({k, v}));
+    LLSA_TRY(check_lens(q_len, k_len));
+    const size_t need = dense_fwd_workspace(s);
+    if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
+    if (need > 0) LLSA_TRY(check_ptrs({ws}));
+    LLSA_TRY(device_ready());
+    DenseArgs a = dense_args(s);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_len = q_len;
+    a.k_len = k_len;
+    a.o_out = o;
+    a.lse_out = lse;
+    return launch_dense_fwd(s, a, ws, static_cast<cudaStream_t>(stream));
+}
+
+int llsa_dense_bwd(const llsa_dense_params* p, const void* q, const void* k, const void* v, const void* o,
+                   const float* lse, const void* dout, const int32_t* q_len, const int32_t* k_len, void* dq,
+                   void* dk, void* dv, void* ws, size_t ws_bytes, void* stream) {
+    CallRange range("llsa_dense_bwd");
+    DenseShape s;
+    LLSA_TRY(derive_dense(p, &s));
+    if (s.slices == 0 || (s.R == 0 && s.nk == 0)) return LLSA_OK;
+    if (s.R > 0) LLSA_TRY(check_ptrs({q, o, lse, dout, dq}));
+    if (s.nk > 0) LLSA_TRY(check_ptrs({k, v, dk, dv}));
+    LLSA_TRY(check_lens(q_len, k_len));
+    const size_t need = dense_bwd_workspace(s);
+    if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
+    if (need > 0) LLSA_TRY(check_ptrs({ws}));
+    LLSA_TRY(device_ready());
+    DenseArgs a = dense_args(s);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.o = o;
+    a.lse = lse;
+    a.dout = dout;
+    a.q_len = q_len;
+    a.k_len = k_len;
+    a.dq = dq;
+    a.dk = dk;
+    a.dv = dv;
+    return launch_dense_bwd(s, a, ws, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

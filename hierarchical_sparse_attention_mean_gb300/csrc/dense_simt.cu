@@ -1,0 +1,425 @@
+// dense_simt.cu -- dense attention on the CUDA cores: every type and head
+// dimension; fp32 runs here, where its products keep 32 bits.
+//
+// Forward: one pass over the keys with the running maximum and sum of the
+// softmax. Backward: probabilities recomputed from lse; dq by blocks of query
+// rows, dk and dv by blocks of keys, so that every sum has one owner and a
+// fixed order.
+//
+// A block takes BM rows against tiles of BM rows of the other side, 256
+// threads as 16 x 16, each with an (BM / 16)^2 piece of the score tile and
+// BM / 16 rows of the output. Operands sit in shared memory as fp32, rows of
+// DP + 4 floats: the 16 rows that a quarter warp reads then fall on distinct
+// banks. Bound by the FMA pipes: per 4 columns of d a thread loads 8 vectors
+// for 64 FMAs.
+#include <algorithm>
+
+#include "dense.h"
+
+namespace llsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return __ldg(reinterpret_cast<const float4*>(p));
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// BM rows of a [rows][d] matrix from row r0 on into shared memory, zeros where
+// valid(row) fails and behind column d.
+template <typename T, int DP, int BM, typename F>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, int r0, int d, F valid) {
+    constexpr int C = DP / 4;
+    for (int x = threadIdx.x; x < BM * C; x += kThreads) {
+        const int r = x / C, c = (x - r * C) * 4;
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < d && valid(r0 + r)) f = load4<T>(src + (long long)(r0 + r) * d + c);
+        *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = f;
+    }
+}
+
+// acc[i][j] = A row (ty * N + i) . B row (tx + 16 j)
+template <int N, int DP>
+__device__ __forceinline__ void tile_dot(float (&acc)[N][N], const float* A, const float* B, int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < N; j++) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < DP; k += 4) {
+        float4 x[N], y[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) x[i] = *reinterpret_cast<const float4*>(A + (ty * N + i) * (DP + 4) + k);
+#pragma unroll
+        for (int j = 0; j < N; j++) y[j] = *reinterpret_cast<const float4*>(B + (tx + 16 * j) * (DP + 4) + k);
+#pragma unroll
+        for (int i = 0; i < N; i++)
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                acc[i][j] = fmaf(x[i].x, y[j].x, acc[i][j]);
+                acc[i][j] = fmaf(x[i].y, y[j].y, acc[i][j]);
+                acc[i][j] = fmaf(x[i].z, y[j].z, acc[i][j]);
+                acc[i][j] = fmaf(x[i].w, y[j].w, acc[i][j]);
+            }
+    }
+}
+
+// acc[i][c] (columns 4 tx + 64 c ..) += sum over the BM entries of P row (ty * N + i) times X's rows
+template <int N, int DP, int BM>
+__device__ __forceinline__ void tile_acc(float4 (&acc)[N][DP / 64], const float* P, const float* X, int ty, int tx) {
+#pragma unroll 2
+    for (int k = 0; k < BM; k += 4) {
+        float4 p[N];
+#pragma unroll
+        for (int i = 0; i < N; i++) p[i] = *reinterpret_cast<const float4*>(P + (ty * N + i) * (BM + 4) + k);
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++)
+#pragma unroll
+            for (int kk = 0; kk < 4; kk++) {
+                const float4 x = *reinterpret_cast<const float4*>(X + (k + kk) * (DP + 4) + 4 * tx + 64 * c);
+#pragma unroll
+                for (int i = 0; i < N; i++) {
+                    const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                    acc[i][c].x = fmaf(w, x.x, acc[i][c].x);
+                    acc[i][c].y = fmaf(w, x.y, acc[i][c].y);
+                    acc[i][c].z = fmaf(w, x.z, acc[i][c].z);
+                    acc[i][c].w = fmaf(w, x.w, acc[i][c].w);
+                }
+            }
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void store_p(float* P, const float (&v)[N][N], int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int j = 0; j < N; j++) P[(ty * N + i) * (16 * N + 4) + tx + 16 * j] = v[i][j];
+}
+
+// One row's columns of the result, times f.
+template <typename T, int DP>
+__device__ __forceinline__ void store_row(T* dst, const float4 (&acc)[DP / 64], float f, int d, int tx) {
+#pragma unroll
+    for (int c = 0; c < DP / 64; c++)
+        if (4 * tx + 64 * c < d) {
+            const float v[4] = {acc[c].x * f, acc[c].y * f, acc[c].z * f, acc[c].w * f};
+            store4(dst + 4 * tx + 64 * c, v);
+        }
+}
+
+// ---------------------------------------------------------------- forward --
+
+// Partial results of a split over the keys: o unnormalised [split][slice][R][d],
+// then (maximum, sum) pairs [split][slice][R].
+template <typename T, int DP, int BM>
+__global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
+    constexpr int N = BM / 16;
+    extern __shared__ float4 smem4[];
+    float* sQ = reinterpret_cast<float*>(smem4);
+    float* sK = sQ + BM * (DP + 4);
+    float* sV = sK + BM * (DP + 4);
+    float* sP = sV + BM * (DP + 4);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.R + BM - 1) / BM;
+    const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
+    const DenseSpan sp = dense_span(a, slice);
+    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
+    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
+    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
+    load_tile<T, DP, BM>(sQ, q, r0, a.d, [&](int r) { return r < a.R; });
+    int kend[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int r = r0 + ty * N + i;
+        kend[i] = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
+    }
+    const int j_first = part * a.chunk;
+    const int j_last = min(dense_tile_kend(a, sp, r0 % a.nq, BM), a.splits > 1 ? j_first + a.chunk : a.nk);
+    const float sl2 = a.scale * kDenseLog2e;
+    float m[N], l[N];
+    float4 acc[N][DP / 64];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int j0 = j_first; j0 < j_last; j0 += BM) {
+        __syncthreads();
+        load_tile<T, DP, BM>(sK, k, j0, a.d, [&](int j) { return j < sp.lk; });
+        load_tile<T, DP, BM>(sV, v, j0, a.d, [&](int j) { return j < sp.lk; });
+        __syncthreads();
+        float s[N][N];
+        tile_dot<N, DP>(s, sQ, sK, ty, tx);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            float top = m[i];
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                s[i][j] = j0 + tx + 16 * j < kend[i] ? s[i][j] * sl2 : -INFINITY;
+                top = fmaxf(top, s[i][j]);
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float shift = top == -INFINITY ? 0.f : top;  // no key yet: every weight below is exp2(-inf) = 0
+            const float f = exp2f(m[i] - shift);
+            m[i] = top;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                s[i][j] = exp2f(s[i][j] - shift);
+                sum += s[i][j];
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            l[i] = l[i] * f + sum;
+#pragma unroll
+            for (int c = 0; c < DP / 64; c++) {
+                acc[i][c].x *= f;
+                acc[i][c].y *= f;
+                acc[i][c].z *= f;
+                acc[i][c].w *= f;
+            }
+        }
+        store_p<N>(sP, s, ty, tx);
+        __syncthreads();
+        tile_acc<N, DP, BM>(acc, sP, sV, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int r = r0 + ty * N + i;
+        if (r >= a.R) continue;
+        const long long row = (long long)slice * a.R + r;
+        if (a.splits > 1) {
+            const long long prow = (long long)part * a.slices * a.R + row;
+            store_row<float, DP>(a.part + prow * a.d, acc[i], 1.f, a.d, tx);
+            float2* ml = reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d);
+            if (tx == 0) ml[prow] = make_float2(m[i], l[i]);
+        } else {
+            store_row<T, DP>(static_cast<T*>(a.o_out) + row * a.d, acc[i], l[i] > 0.f ? 1.f / l[i] : 0.f, a.d, tx);
+            if (tx == 0) a.lse_out[row] = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
+        }
+    }
+}
+
+// --------------------------------------------------------------- backward --
+
+// dq of BM query rows. Partial sums of a split over the keys: [split][slice][R][d].
+template <typename T, int DP, int BM>
+__global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
+    constexpr int N = BM / 16;
+    extern __shared__ float4 smem4[];
+    float* sQ = reinterpret_cast<float*>(smem4);
+    float* sG = sQ + BM * (DP + 4);
+    float* sK = sG + BM * (DP + 4);
+    float* sV = sK + BM * (DP + 4);
+    float* sP = sV + BM * (DP + 4);
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.R + BM - 1) / BM;
+    const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
+    const DenseSpan sp = dense_span(a, slice);
+    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
+    const T* g = static_cast<const T*>(a.dout) + (long long)slice * a.R * a.d;
+    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
+    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
+    auto row_ok = [&](int r) { return r < a.R && r % a.nq < sp.lq; };
+    load_tile<T, DP, BM>(sQ, q, r0, a.d, row_ok);
+    load_tile<T, DP, BM>(sG, g, r0, a.d, row_ok);
+    int kend[N];
+    float l2[N], dsum[N];
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int r = r0 + ty * N + i;
+        kend[i] = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
+        l2[i] = r < a.R ? a.l2[(long long)slice * a.Rp + r] : INFINITY;
+        dsum[i] = r < a.R ? a.dsum[(long long)slice * a.Rp + r] : 0.f;
+    }
+    const int j_first = part * a.chunk;
+    const int j_last = min(dense_tile_kend(a, sp, r0 % a.nq, BM), a.splits > 1 ? j_first + a.chunk : a.nk);
+    const float sl2 = a.scale * kDenseLog2e;
+    float4 acc[N][DP / 64];
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = j_first; j0 < j_last; j0 += BM) {
+        __syncthreads();
+        load_tile<T, DP, BM>(sK, k, j0, a.d, [&](int j) { return j < sp.lk; });
+        load_tile<T, DP, BM>(sV, v, j0, a.d, [&](int j) { return j < sp.lk; });
+        __syncthreads();
+        float s[N][N], dp[N][N];
+        tile_dot<N, DP>(s, sQ, sK, ty, tx);
+        tile_dot<N, DP>(dp, sG, sV, ty, tx);
+#pragma unroll
+        for (int i = 0; i < N; i++)
+#pragma unroll
+            for (int j = 0; j < N; j++) {
+                const float p = exp2f(fmaf(s[i][j], sl2, -l2[i]));
+                s[i][j] = j0 + tx + 16 * j < kend[i] ? p * (dp[i][j] - dsum[i]) : 0.f;
+            }
+        store_p<N>(sP, s, ty, tx);
+        __syncthreads();
+        tile_acc<N, DP, BM>(acc, sP, sK, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int r = r0 + ty * N + i;
+        if (r >= a.R) continue;
+        const long long row = (long long)slice * a.R + r;
+        if (a.splits > 1)
+            store_row<float, DP>(a.part + ((long long)part * a.slices * a.R + row) * a.d, acc[i], a.scale, a.d, tx);
+        else
+            store_row<T, DP>(static_cast<T*>(a.dq) + row * a.d, acc[i], a.scale, a.d, tx);
+    }
+}
+
+// dk and dv of BM keys, over the query rows of all heads that share them.
+// Partial sums of a split over the rows: dk [split][slice][nk][d], then dv.
+template <typename T, int DP, int BM>
+__global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
+    constexpr int N = BM / 16;
+    extern __shared__ float4 smem4[];
+    float* sK = reinterpret_cast<float*>(smem4);
+    float* sV = sK + BM * (DP + 4);
+    float* sQ = sV + BM * (DP + 4);
+    float* sG = sQ + BM * (DP + 4);
+    float* sP = sG + BM * (DP + 4);  // P^T
+    float* sS = sP + BM * (BM + 4);  // dS^T
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    const int tiles = (a.nk + BM - 1) / BM;
+    const int slice = blockIdx.x / tiles, j0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
+    const DenseSpan sp = dense_span(a, slice);
+    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
+    const T* g = static_cast<const T*>(a.dout) + (long long)slice * a.R * a.d;
+    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
+    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
+    auto key_ok = [&](int j) { return j < sp.lk; };
+    auto row_ok = [&](int r) { return r < a.R && r % a.nq < sp.lq; };
+    load_tile<T, DP, BM>(sK, k, j0, a.d, key_ok);
+    load_tile<T, DP, BM>(sV, v, j0, a.d, key_ok);
+    const int r_first = a.splits > 1 ? part * a.chunk : 0;
+    const int r_last = a.splits > 1 ? min(a.R, r_first + a.chunk) : a.R;
+    const float sl2 = a.scale * kDenseLog2e;
+    float4 dk[N][DP / 64], dv[N][DP / 64];
+#pragma unroll
+    for (int i = 0; i < N; i++)
+#pragma unroll
+        for (int c = 0; c < DP / 64; c++) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r0 = r_first; r0 < r_last; r0 += BM) {
+        if (dense_tile_kend(a, sp, r0 % a.nq, BM) <= j0) continue;
+        __syncthreads();
+        load_tile<T, DP, BM>(sQ, q, r0, a.d, row_ok);
+        load_tile<T, DP, BM>(sG, g, r0, a.d, row_ok);
+        __syncthreads();
+        float s[N][N], dp[N][N];
+        tile_dot<N, DP>(s, sK, sQ, ty, tx);
+        tile_dot<N, DP>(dp, sV, sG, ty, tx);
+#pragma unroll
+        for (int j = 0; j < N; j++) {
+            const int r = r0 + tx + 16 * j;
+            const int kend = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
+            const float l2 = r < a.R ? a.l2[(long long)slice * a.Rp + r] : INFINITY;
+            const float dsum = r < a.R ? a.dsum[(long long)slice * a.Rp + r] : 0.f;
+#pragma unroll
+            for (int i = 0; i < N; i++) {
+                const float p = j0 + ty * N + i < kend ? exp2f(fmaf(s[i][j], sl2, -l2)) : 0.f;
+                s[i][j] = p;
+                dp[i][j] = p * (dp[i][j] - dsum);
+            }
+        }
+        store_p<N>(sP, s, ty, tx);
+        store_p<N>(sS, dp, ty, tx);
+        __syncthreads();
+        tile_acc<N, DP, BM>(dv, sP, sG, ty, tx);
+        tile_acc<N, DP, BM>(dk, sS, sQ, ty, tx);
+    }
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int j = j0 + ty * N + i;
+        if (j >= a.nk) continue;
+        const long long row = (long long)slice * a.nk + j;
+        if (a.splits > 1) {
+            const long long all = (long long)a.slices * a.nk;
+            store_row<float, DP>(a.part + (part * all + row) * a.d, dk[i], a.scale, a.d, tx);
+            store_row<float, DP>(a.part + ((a.splits + part) * all + row) * a.d, dv[i], 1.f, a.d, tx);
+        } else {
+            store_row<T, DP>(static_cast<T*>(a.dk) + row * a.d, dk[i], a.scale, a.d, tx);
+            store_row<T, DP>(static_cast<T*>(a.dv) + row * a.d, dv[i], 1.f, a.d, tx);
+        }
+    }
+}
+
+int block_rows(const DenseShape& s) { return s.d > 128 ? 32 : 64; }
+
+DenseSplit make_split(long long blocks, int extent, int bm) {
+    const long long units = (extent + bm - 1) / bm;
+    const int n = dense_splits(blocks, units, 4, kDenseSms);
+    DenseSplit p;
+    p.chunk = (int)((units + n - 1) / n) * bm;
+    p.splits = extent > 0 ? (extent + p.chunk - 1) / p.chunk : 1;
+    return p;
+}
+
+enum { kFwd, kDq, kDkv };
+
+template <int OP, typename T, int DP, int BM>
+int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    const int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
+    const int smem = OP == kFwd ? 3 * tile + p : OP == kDq ? 4 * tile + p : 4 * tile + 2 * p;
+    const int extent = OP == kDkv ? s.nk : s.R;
+    const long long blocks = (long long)((extent + BM - 1) / BM) * s.slices;
+    if (blocks > 2147483647LL) return LLSA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, a.splits);
+    if constexpr (OP == kFwd) {
+        cudaFuncSetAttribute(dense_fwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        LLSA_LAUNCH("dense_fwd_simt", st, dense_fwd_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
+    } else if constexpr (OP == kDq) {
+        cudaFuncSetAttribute(dense_dq_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        LLSA_LAUNCH("dense_dq_simt", st, dense_dq_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
+    } else {
+        cudaFuncSetAttribute(dense_dkv_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        LLSA_LAUNCH("dense_dkv_simt", st, dense_dkv_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
+    }
+    return LLSA_OK;
+}
+
+template <int OP>
+int launch_op(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    if (s.dtype == LLSA_DTYPE_F32)
+        return s.d <= 64    ? launch<OP, float, 64, 64>(s, a, st)
+               : s.d <= 128 ? launch<OP, float, 128, 64>(s, a, st)
+                            : launch<OP, float, 256, 32>(s, a, st);
+    return s.d <= 64    ? launch<OP, __nv_bfloat16, 64, 64>(s, a, st)
+           : s.d <= 128 ? launch<OP, __nv_bfloat16, 128, 64>(s, a, st)
+                        : launch<OP, __nv_bfloat16, 256, 32>(s, a, st);
+}
+
+}  // namespace
+
+DenseSplit dense_simt_fwd_split(const DenseShape& s) {
+    const int bm = block_rows(s);
+    return make_split((long long)s.slices * ((s.R + bm - 1) / bm), s.nk, bm);
+}
+DenseSplit dense_simt_dq_split(const DenseShape& s) { return dense_simt_fwd_split(s); }
+DenseSplit dense_simt_dkv_split(const DenseShape& s) {
+    const int bm = block_rows(s);
+    return make_split((long long)s.slices * ((s.nk + bm - 1) / bm), s.R, bm);
+}
+
+int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) { return launch_op<kFwd>(s, a, st); }
+int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st) { return launch_op<kDq>(s, a, st); }
+int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st) { return launch_op<kDkv>(s, a, st); }
+
+}  // namespace llsa

@@ -288,6 +288,133 @@ int llsa_select_exhaustive(const llsa_params *p, const float *pyr, int32_t *sel_
  * image is s^m x s^m; LLSA_ERR_INVALID_ARG for inverse not 0 / 1 or in == out. */
 int llsa_reorder(const llsa_params *p, int height, int width, const void *in, void *out, int inverse, void *stream);
 
+/* Dense attention: every query token sees every key token that the mask
+ * leaves. The companion of the sparse path for the layers it does not take:
+ * images of fewer than B^2 tokens, keys that are not the queries' own tokens
+ * (a conditioning sequence, a pooling query), padded batches, causal order and
+ * key heads that several query heads share.
+ *
+ * For query token t of head h in batch entry b, with key head
+ * h / (heads / kv_heads), lq = q_len[b] and lk = k_len[b] (nq and nk where the
+ * pointer is NULL), key j is allowed when t < lq, j < lk and, if causal,
+ * j <= t + lk - lq (the last query sees the last key). With
+ * s_tj = scale * q_t . k_j,
+ *   lse_t = ln sum_j exp(s_tj),  o_t = sum_j exp(s_tj - lse_t) v_j.
+ * A query without an allowed key (t >= lq, lk = 0, or causal with too few
+ * keys) gets o = 0 and lse = -infinity, and adds nothing to any gradient.
+ * Tokens at or beyond a length may hold anything, NaN and infinities included;
+ * what is stored for them (o, dq, dk, dv) is zero. Values of tokens inside
+ * the lengths must be finite. A length outside [0, nq] or [0, nk] is clamped
+ * and reported through llsa_get_status (LLSA_ERR_BAD_INDEX). */
+typedef struct llsa_dense_params {
+    int batch;
+    int heads;          /* query heads: a multiple of kv_heads */
+    int kv_heads;       /* key / value heads; 0 selects heads */
+    int nq, nk;         /* query and key tokens per slice, padding included; 0 is allowed */
+    int d;              /* head dimension: multiple of 8, at most 256 */
+    int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int causal;         /* 0 or 1 */
+    float scale;        /* softmax scale; 0 selects 1/sqrt(d) */
+} llsa_dense_params;
+
+/* Workspace of llsa_dense_fwd (op LLSA_OP_DENSE_FWD) or llsa_dense_bwd
+ * (LLSA_OP_DENSE_BWD) in bytes; 0 when none, or when the parameters are
+ * invalid (the call then fails). Two calls that may run at the same time (two
+ * streams, two captured graphs) need a workspace each. */
+enum { LLSA_OP_DENSE_FWD = 5, LLSA_OP_DENSE_BWD = 6 };
+size_t llsa_dense_workspace_bytes(const llsa_dense_params *p, int op);
+
+/* Dense attention, forward.
+ *   q     : [batch, heads, nq, d]; k, v : [batch, kv_heads, nk, d] (p->dtype).
+ *   q_len, k_len : int32 [batch] on the device, or NULL (all tokens valid).
+ *   o     : output [batch, heads, nq, d] (p->dtype).
+ *   lse   : output fp32 [batch, heads, nq] (natural log).
+ * Limits: heads / kv_heads * nq and nk at most 2^30 (LLSA_ERR_UNSUPPORTED).
+ * Deterministic. */
+int llsa_dense_fwd(const llsa_dense_params *p, const void *q, const void *k, const void *v, const int32_t *q_len,
+                   const int32_t *k_len, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/* Dense attention, backward: gradients of sum_t dout_t . o_t. The
+ * probabilities are recomputed from lse:
+ *   P = exp(s - lse), D_t = dout_t . o_t, dS = P (dout_t . v_j - D_t),
+ *   dq_t = scale sum_j dS k_j, dk_j = scale sum_t dS q_t, dv_j = sum_t P dout_t,
+ * the last two over the query heads that share the key head too.
+ *   o, lse : from llsa_dense_fwd on the same inputs and lengths.
+ *   dout   : [batch, heads, nq, d]; dq, dk, dv : outputs, overwritten.
+ * Deterministic: every sum has one owner and a fixed order. */
+int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, const void *v, const void *o,
+                   const float *lse, const void *dout, const int32_t *q_len, const int32_t *k_len, void *dq,
+                   void *dk, void *dv, void *ws, size_t ws_bytes, void *stream);
+
+/* Rotary positions of q and k, in one launch.
+ *
+ * The first rot_dim columns of a head are `axes` equal segments; segment a is
+ * turned by the token's position on axis a. With seg = rot_dim / axes columns
+ * and h = seg / 2 pairs, pair i of a segment is its columns (2i, 2i + 1)
+ * (LLSA_ROPE_INTERLEAVED) or (i, i + h) (LLSA_ROPE_HALF), and becomes
+ *   (x cos - y sin, x sin + y cos) * amplitude,  angle = position * w_i.
+ * The other columns are copied. Frequencies w_i, i = 0 .. h - 1:
+ *   LLSA_ROPE_SCALE_NONE       base^(-2i / seg)
+ *   LLSA_ROPE_SCALE_LINEAR     the same / factor (positions pressed together)
+ *   LLSA_ROPE_SCALE_BASE       base replaced by base * factor^(seg / (seg - 2)):
+ *                              the slowest pair is stretched by factor, the
+ *                              fastest kept
+ *   LLSA_ROPE_SCALE_WAVELENGTH w (g + (1 - g) / factor), where g goes from 0
+ *                              to 1 as the turns that the pair makes over
+ *                              orig_len positions, orig_len * w / 2 pi, go
+ *                              from `low` to `high`
+ * amplitude 0 selects 1, or 0.1 ln(factor) + 1 under WAVELENGTH.
+ * Angles are exact to 2^-31 turns at every int32 position (the frequency is a
+ * 64-bit fraction of a turn, and the product keeps its fractional part).
+ * `inverse` turns by the negative angles: with amplitude 1 the inverse, and
+ * with any amplitude the gradient of the call.
+ *
+ *   q, k         : heads / kv_heads heads each, [batch, heads, n, d] through
+ *                  the strides; k and k_out are NULL where kv_heads is 0.
+ *   pos          : int32 [n][axes] on the device, or [batch][n][axes] with
+ *                  pos_batched; NULL: token t is at pos_offset + t (axes 1),
+ *                  or (axes 2) at row t / width, column t % width of the image
+ *                  under LLSA_ORDER_RASTER, and at the row and column of tile
+ *                  position t (llsa_reorder with B = 16; n = width^2, width a
+ *                  power of 4) under LLSA_ORDER_TILE.
+ *   q_out, k_out : outputs; a tensor may be its own output (same pointer and
+ *                  strides). Other overlaps are not allowed.
+ *   strides      : element strides of batch, head and token; NULL, or three
+ *                  zeros, stands for contiguous [batch, heads, n, d]. Columns are
+ *                  contiguous; every stride that is used spans a multiple of
+ *                  16 bytes (LLSA_ERR_ALIGN otherwise). */
+enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };
+enum { LLSA_ROPE_SCALE_NONE = 0, LLSA_ROPE_SCALE_LINEAR = 1, LLSA_ROPE_SCALE_BASE = 2, LLSA_ROPE_SCALE_WAVELENGTH = 3 };
+
+typedef struct llsa_rope_params {
+    int batch;
+    int heads;          /* heads of q */
+    int kv_heads;       /* heads of k; 0: no k */
+    int n;              /* tokens per slice */
+    int d;              /* head dimension: multiple of 8, at most 256 */
+    int rot_dim;        /* columns turned: a multiple of 2 * axes, at most d; 0 selects d */
+    int layout;         /* LLSA_ROPE_HALF or LLSA_ROPE_INTERLEAVED */
+    int axes;           /* 1 or 2 */
+    int width;          /* image width (axes 2); 0 for axes 1; ignored with pos */
+    int token_order;    /* LLSA_ORDER_RASTER or LLSA_ORDER_TILE (axes 2); ignored with pos */
+    int pos_offset;     /* position of token 0 (axes 1); 0 for axes 2; ignored with pos */
+    int pos_batched;    /* pos holds batch * n rows instead of n */
+    int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int scaling;        /* LLSA_ROPE_SCALE_* */
+    int orig_len;       /* WAVELENGTH: positions that the model was trained on */
+    double base;        /* > 1 */
+    double factor;      /* > 0 (ignored by SCALE_NONE) */
+    double low, high;   /* WAVELENGTH: low < high */
+    double amplitude;   /* 0 selects the default */
+} llsa_rope_params;
+
+typedef struct llsa_rope_strides {
+    long long q[3], k[3], q_out[3], k_out[3]; /* batch, head, token */
+} llsa_rope_strides;
+
+int llsa_rope(const llsa_rope_params *p, const llsa_rope_strides *strides, const void *q, const void *k,
+              const int32_t *pos, void *q_out, void *k_out, int inverse, void *stream);
+
 /* Reads (after synchronising `stream`) and clears the device status word of
  * the current device: LLSA_OK, LLSA_ERR_TIMEOUT or LLSA_ERR_BAD_INDEX. */
 int llsa_get_status(void *stream, int *device_status);

@@ -1,0 +1,331 @@
+"""Dense attention on the GPU against its formulas in 64 bits: values and
+gradients over types, head layouts, lengths, masks and padding, within bounds
+that count roundings; plus streams, captured graphs, splits of a long axis,
+offsets behind 32 bits, and a run together with rotary positions."""
+import math
+
+import pytest
+import torch
+
+import hierarchical_sparse_attention_mean_gb300 as llsa
+from hierarchical_sparse_attention_mean_gb300 import build
+
+import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+BAD_INDEX = -10
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def make(b, h, kv, nq, nk, d, dtype, q_len=None, k_len=None, seed=0, pad=float("nan")):
+    g = torch.Generator().manual_seed(seed * 1000 + nq * 7 + nk * 3 + d)
+    x = {n: torch.randn(b, hh, nn, d, generator=g).to(T[dtype])
+         for n, hh, nn in (("q", h, nq), ("k", kv, nk), ("v", kv, nk), ("dout", h, nq))}
+    for e in range(b):  # what lies behind the lengths must not matter
+        if q_len is not None:
+            x["q"][e, :, q_len[e]:] = pad
+            x["dout"][e, :, q_len[e]:] = pad
+        if k_len is not None:
+            x["k"][e, :, k_len[e]:] = pad
+            x["v"][e, :, k_len[e]:] = -pad
+    return x
+
+
+def lens(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def run(x, causal=False, scale=0.0, q_len=None, k_len=None, dtype="bf16"):
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DenseParams.like(c["q"], c["k"], causal=causal, scale=scale)
+    ql, kl = lens(q_len), lens(k_len)
+    o, lse = llsa.dense_forward(p, c["q"], c["k"], c["v"], ql, kl,
+                                o=torch.full_like(c["q"], 7.0))  # every row is written
+    full = [torch.full_like(c[n], 7.0) for n in ("q", "k", "v")]
+    dq, dk, dv = llsa.dense_backward(p, c["q"], c["k"], c["v"], o, lse, c["dout"], ql, kl, *full)
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    return {"o": o, "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+CASES = [
+    # b, h, kv, nq, nk, d, causal, q_len, k_len
+    (1, 1, 1, 1, 1, 8, False, None, None),
+    (2, 3, 3, 5, 1, 64, False, None, None),
+    (1, 2, 1, 1, 300, 64, False, None, None),             # one token, shared keys
+    (2, 8, 2, 3, 67, 128, True, None, None),
+    (1, 2, 2, 64, 64, 64, False, None, None),
+    (1, 2, 2, 128, 128, 64, True, None, None),
+    (1, 4, 2, 130, 129, 64, False, None, None),
+    (2, 2, 2, 257, 255, 128, True, None, None),
+    (1, 2, 2, 200, 77, 64, True, None, None),             # 123 rows see nothing
+    (1, 2, 1, 77, 200, 64, True, None, None),
+    (1, 6, 2, 100, 150, 64, True, None, None),            # tiles run over the ends of heads
+    (1, 6, 2, 100, 150, 128, True, [61], [149]),
+    (1, 8, 1, 17, 90, 64, False, [9], None),              # padding inside a tile, head after head
+    (3, 2, 2, 140, 190, 64, False, [140, 65, 1], [190, 1, 129]),
+    (3, 2, 2, 140, 190, 64, True, [140, 65, 0], [100, 0, 190]),
+    (2, 4, 4, 300, 333, 64, False, None, [333, 0]),       # one entry without keys
+    (2, 2, 1, 260, 270, 128, False, [0, 259], [270, 131]),
+    (1, 2, 2, 90, 100, 40, False, None, None),
+    (1, 2, 2, 90, 100, 72, True, None, [97]),
+    (1, 2, 2, 150, 140, 96, False, None, None),
+    (1, 2, 1, 70, 90, 136, True, None, None),             # behind 128 columns
+    (1, 1, 1, 40, 65, 256, False, [33], [64]),
+    (1, 2, 2, 1000, 1100, 64, False, None, None),
+    (1, 1, 1, 700, 900, 128, True, None, None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c[:6]) + ("-causal" if c[6] else "") +
+                         ("-len" if c[7] or c[8] else ""))
+def test_forward_and_backward(case, dtype):
+    b, h, kv, nq, nk, d, causal, ql, kl = case
+    x = make(b, h, kv, nq, nk, d, dtype, ql, kl)
+    want = ref.attention(**x, causal=causal, q_len=ql, k_len=kl, dtype=T[dtype])
+    got = run(x, causal, 0.0, ql, kl, dtype)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("amp,scale", [(8.0, 0.0), (1.0, 1.0), (0.01, 0.3)])
+def test_scales(amp, scale, dtype):
+    """Sharp and flat softmax: scores up to hundreds, where rows pass through many maxima."""
+    x = make(1, 2, 2, 150, 400, 64, dtype, seed=3)
+    x["q"] = (x["q"].float() * amp).to(T[dtype])
+    # keys that grow along the sequence: the maximum keeps moving
+    x["k"] = (x["k"].float() * torch.linspace(0.1, 2.0, 400)[:, None]).to(T[dtype])
+    want = ref.attention(**x, scale=scale, dtype=T[dtype])
+    got = run(x, scale=scale, dtype=dtype)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("bf16", 200)])
+@pytest.mark.parametrize("nq,nk,h,kv", [(1, 20000, 2, 2), (2, 9000, 8, 2), (5000, 33, 2, 1)])
+def test_long_axis_is_split(nq, nk, h, kv, dtype, d):
+    """Few rows over many keys (and few keys under many rows): the long axis runs in parts."""
+    x = make(1, h, kv, nq, nk, d, dtype, k_len=[nk - 3], seed=5)
+    want = ref.attention(**x, k_len=[nk - 3], dtype=T[dtype])
+    got = run(x, k_len=[nk - 3], dtype=dtype)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("nq,nk", [(0, 5), (5, 0), (0, 0)])
+def test_empty_sides(nq, nk, dtype):
+    x = make(2, 2, 2, nq, nk, 64, dtype)
+    got = run(x, dtype=dtype)
+    assert got["o"].shape == (2, 2, nq, 64) and not got["o"].any()
+    assert bool((got["lse"] == -math.inf).all())
+    for n in ("dq", "dk", "dv"):
+        assert not got[n].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_bad_lengths_are_clamped_and_reported(dtype):
+    x = {n: t.cuda() for n, t in make(2, 2, 2, 70, 80, 64, dtype).items()}
+    p = llsa.DenseParams.like(x["q"], x["k"])
+    o, lse = llsa.dense_forward(p, x["q"], x["k"], x["v"], lens([75, 70]), lens([80, -4]))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == BAD_INDEX
+    o2, lse2 = llsa.dense_forward(p, x["q"], x["k"], x["v"], lens([70, 70]), lens([80, 0]))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_repeats_are_bit_equal(dtype, d):
+    x = make(2, 8, 2, 333, 450, d, dtype, q_len=[333, 200], k_len=[450, 77])
+    a, b = (run(x, True, 0.0, [333, 200], [450, 77], dtype) for _ in range(2))
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_gradients_against_differences():
+    """Directional derivatives of the 64-bit loss sum(o dout), by central differences."""
+    x = make(1, 4, 2, 50, 60, 64, "fp32", seed=9)
+    got = run(x, causal=True, dtype="fp32")
+
+    def loss(**kw):
+        y = {n: t.double() for n, t in {**x, **kw}.items()}
+        return float((ref.attention(y["q"], y["k"], y["v"], causal=True)["o"][0] * y["dout"]).sum())
+
+    for n in ("q", "k", "v"):
+        u = torch.randn(x[n].shape, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+        u /= u.norm()
+        h = 1e-4  # truncation h^2, cancellation 2^-53 |loss| / h: both far below the fp32 gradient's error
+        diff = (loss(**{n: x[n].double() + h * u}) - loss(**{n: x[n].double() - h * u})) / (2 * h)
+        g = got["d" + n].double().cpu()
+        assert abs(float((g * u).sum()) - diff) <= 1e-5 * float(g.norm()) + 1e-6
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_other_stream_and_captured_graph(dtype):
+    """The call on a stream of its own, and captured with its backward pass and
+    replayed on new inputs, gives what it gives on the current stream."""
+    ql, kl = [200, 130], [190, 260]
+    x = make(2, 4, 2, 200, 260, 64, dtype, ql, kl)
+    y = make(2, 4, 2, 200, 260, 64, dtype, ql, kl, seed=4)
+    want_x, want_y = run(x, True, 0.0, ql, kl, dtype), run(y, True, 0.0, ql, kl, dtype)
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DenseParams.like(c["q"], c["k"], causal=True)
+    a, b = lens(ql), lens(kl)
+
+    def step():
+        o, lse = llsa.dense_forward(p, c["q"], c["k"], c["v"], a, b)
+        return dict(zip(("o", "lse", "dq", "dk", "dv"),
+                        (o, lse, *llsa.dense_backward(p, c["q"], c["k"], c["v"], o, lse, c["dout"], a, b))))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    torch.cuda.synchronize()
+    for n in got:
+        assert torch.equal(got[n], want_x[n]), n
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for source, want in ((x, want_x), (y, want_y)):
+        for n in c:
+            c[n].copy_(source[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in got:
+            assert torch.equal(got[n], want[n]), n
+
+
+def test_a_given_stream_orders_the_call():
+    """stream=: the work goes there, workspace included, whatever the current stream is."""
+    x = {n: t.cuda() for n, t in make(1, 2, 2, 1, 20000, 64, "bf16").items()}
+    p = llsa.DenseParams.like(x["q"], x["k"])
+    want, _ = llsa.dense_forward(p, x["q"], x["k"], x["v"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    o, lse = llsa.dense_forward(p, x["q"], x["k"], x["v"], stream=side)
+    side.synchronize()
+    assert torch.equal(o, want)
+
+
+def test_offsets_behind_32_bits():
+    """2^31 elements and more in each of k and v; the weight lies on the last keys."""
+    d, nk = 64, (1 << 25) + 77
+    k = torch.zeros(1, 1, nk, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() > 1 << 31
+    q = torch.ones(1, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    k[0, 0, -3:] = 8.0                  # scores 64 against 0: e^64 >> the number of keys
+    v[0, 0, -3:] = torch.tensor([[1.0], [2.0], [4.0]], device="cuda")
+    p = llsa.DenseParams.like(q, k)
+    o, lse = llsa.dense_forward(p, q, k, v)
+    dq, dk, dv = llsa.dense_backward(p, q, k, v, o, lse, q)
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    # the zero keys weigh nk e^-64: nothing
+    assert torch.allclose(o.float(), torch.full_like(o, 7.0 / 3).float(), rtol=2.0 ** -7, atol=0)
+    assert abs(float(lse) - (64 + math.log(3))) < 1e-3
+    third = torch.full((3, d), 1 / 3)
+    assert torch.allclose(dv[0, 0, -3:].float().cpu(), third, rtol=2.0 ** -7, atol=0)
+    # a zero key's value gets P dO = e^-64 / 3 = 5.346e-29, rounded to bf16 (exp2 and lse add 64 log2(e) 2^-23)
+    few = dv[0, 0, : nk // 2]
+    lo, hi = float(few.min()), float(few.max())
+    assert lo == hi and abs(lo / (math.exp(-64) / 3) - 1) < 2.0 ** -8 + 2.0 ** -15
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_autograd_matches_the_calls(dtype):
+    x = make(2, 4, 2, 64, 96, 64, dtype, seed=2)
+    want = run(x, causal=True, dtype=dtype)
+    leaves = [x[n].cuda().transpose(1, 2).contiguous().transpose(1, 2).requires_grad_() for n in ("q", "k", "v")]
+    o = llsa.dense_attention(*leaves, causal=True)
+    grads = torch.autograd.grad(o, leaves, x["dout"].cuda())
+    assert torch.equal(o, want["o"])
+    for g, n in zip(grads, ("dq", "dk", "dv")):
+        assert torch.equal(g, want[n]), n
+
+
+def test_shared_gradient_of_expanded_keys():
+    """Keys and values broadcast over the batch collect the gradients of every entry."""
+    x = make(3, 2, 2, 40, 50, 64, "fp32", seed=8)
+    k1, v1 = (x[n][:1].cuda().requires_grad_() for n in ("k", "v"))
+    o = llsa.dense_attention(x["q"].cuda(), k1.expand(3, -1, -1, -1), v1.expand(3, -1, -1, -1))
+    dk, dv = torch.autograd.grad(o, (k1, v1), x["dout"].cuda())
+    x["k"], x["v"] = (x[n][:1].expand(3, -1, -1, -1) for n in ("k", "v"))
+    want = ref.attention(**x, dtype=torch.float32)
+    for n, g in (("dk", dk), ("dv", dv)):
+        value, bound = (t.sum(0, keepdim=True) for t in want[n])
+        ref.check(n, g, (value, bound + 4 * 2.0 ** -24 * value.abs()))
+
+
+@pytest.mark.parametrize("axes,width,order", [(1, 0, "raster"), (2, 16, "raster"), (2, 16, "tile")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rotary_attention_and_gradients_together(dtype, axes, width, order):
+    """rotary positions -> attention -> both backward passes, against autograd of
+    the formulas in 64 bits."""
+    b, h, kv, n, d = 2, 4, 2, 256, 64
+    x = make(b, h, kv, n, n, d, dtype, seed=6)
+    leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v")]
+    rope = llsa.RopeParams.like(leaves[0], leaves[1], axes=axes, width=width, token_order=order)
+    o = llsa.dense_attention(*leaves, rope=rope)
+    got = dict(zip(("o", "dq", "dk", "dv"), (o, *torch.autograd.grad(o, leaves, x["dout"].cuda()))))
+    turned = llsa.rotary(leaves[0].detach(), leaves[1].detach(), rope)
+    torch.cuda.synchronize()
+    t = torch.arange(n)
+    if axes == 1:
+        pos = t[:, None]
+    elif order == "raster":
+        pos = torch.stack([t // width, t % width], -1)
+    else:
+        pos = torch.stack([((t >> 4) >> 2) * 4 + ((t & 15) >> 2), ((t >> 4) & 3) * 4 + (t & 3)], -1)
+    y = dict(x)
+    for m, z in zip(("q", "k"), turned):  # the attention sees them rounded to the type
+        ref.check(m, z, ref.rotary(x[m], pos[None], axes=axes, dtype=T[dtype]))
+        y[m] = z.cpu()
+    want = ref.attention(**y, dtype=T[dtype])
+    for m in ("o", "dv"):
+        ref.check(m, got[m], want[m])
+    u = ref.half_step(T[dtype])
+    for m in ("dq", "dk"):
+        value, bound = want[m]
+        back, turn = ref.rotary(value, pos[None], axes=axes, inverse=True)
+        # |cos|, |sin| <= 1: an error of either column of a pair reaches both, and the result is rounded once more
+        bound = _pair_sum(bound, axes) * (1 + u) + turn + u * back.abs()
+        ref.check(m, got[m], (back, bound))
+
+
+def _pair_sum(t, axes):
+    """For each column, its value plus its partner's (half layout)."""
+    seg = t.shape[-1] // axes
+    s = t.unflatten(-1, (axes, 2, seg // 2))
+    return (s + s.flip(-2)).flatten(-3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rotary_before_the_sparse_attention(dtype):
+    """llsa_attention with rope= is the sparse attention of the turned q and k, and
+    its gradients turned back."""
+    n, d = 256 if dtype == "fp32" else 4096, 64
+    x = make(1, 2, 2, n, n, d, dtype, seed=7)
+    side = math.isqrt(n)
+    q, k, v = (x[m].cuda().requires_grad_() for m in ("q", "k", "v"))
+    rope = llsa.RopeParams.like(q, k, axes=2, width=side, token_order="tile")
+    o = llsa.llsa_attention(q, k, v, topk=4, rope=rope)
+    got = torch.autograd.grad(o, (q, k, v), x["dout"].cuda())
+    qr, kr = (t.detach().requires_grad_() for t in llsa.rotary(q, k, rope))
+    o2 = llsa.llsa_attention(qr, kr, v, topk=4)
+    dqr, dkr, dv = torch.autograd.grad(o2, (qr, kr, v), x["dout"].cuda())
+    dq, dk = torch.empty_like(dqr), torch.empty_like(dkr)
+    llsa.llsa_rope(rope, dqr, dkr, dq, dk, inverse=True)
+    assert torch.equal(o, o2)
+    for a, b in zip(got, (dq, dk, dv)):
+        assert torch.equal(a, b)
