@@ -87,25 +87,35 @@ size_t dense_bwd_workspace(const DenseShape& s);
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
 
-// How a long axis is split where the other one gives too few blocks: `blocks`
-// independent blocks, `units` tiles of the long axis, at least `least` tiles
-// per part.
-inline int dense_splits(long long blocks, long long units, long long least, int resident) {
-    if (blocks <= 0 || units <= 0) return 1;
-    long long s = resident / blocks;  // parts that still fit one wave
-    if (s > units / least) s = units / least;
-    return s < 2 ? 1 : s > 128 ? 128 : (int)s;
+struct DenseSplit {
+    int splits, chunk;  // parts, and elements of the split axis per part (a multiple of `tile`)
+};
+
+// How a long axis of `extent` elements in tiles is split where the other axis
+// gives too few blocks: as many parts as still fit one wave of blocks, each of
+// `least` tiles at least.
+inline DenseSplit dense_make_split(long long blocks, int extent, int tile, int least) {
+    const long long units = (extent + tile - 1) / tile;
+    long long n = blocks > 0 ? kDenseSms / blocks : 1;
+    n = n > units / least ? units / least : n;
+    n = n < 1 ? 1 : n;
+    DenseSplit p;
+    p.chunk = (int)((units + n - 1) / n) * tile;
+    p.splits = extent > 0 ? (extent + p.chunk - 1) / p.chunk : 1;
+    return p;
 }
 
 // dense_simt.cu: CUDA-core kernels (any type and head dimension).
-struct DenseSplit {
-    int splits, chunk;
-};
 DenseSplit dense_simt_fwd_split(const DenseShape& s);
 DenseSplit dense_simt_dq_split(const DenseShape& s);
 DenseSplit dense_simt_dkv_split(const DenseShape& s);
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+
+// dense_fwd_tc.cu: tensor-core kernels (bf16, d <= 128).
+bool dense_tc_supported(const DenseShape& s);
+DenseSplit dense_tc_fwd_split(const DenseShape& s);
+int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
 }  // namespace llsa

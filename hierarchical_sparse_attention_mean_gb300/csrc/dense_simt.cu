@@ -363,15 +363,6 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
 
 int block_rows(const DenseShape& s) { return s.d > 128 ? 32 : 64; }
 
-DenseSplit make_split(long long blocks, int extent, int bm) {
-    const long long units = (extent + bm - 1) / bm;
-    const int n = dense_splits(blocks, units, 4, kDenseSms);
-    DenseSplit p;
-    p.chunk = (int)((units + n - 1) / n) * bm;
-    p.splits = extent > 0 ? (extent + p.chunk - 1) / p.chunk : 1;
-    return p;
-}
-
 enum { kFwd, kDq, kDkv };
 
 template <int OP, typename T, int DP, int BM>
@@ -410,12 +401,12 @@ int launch_op(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
 
 DenseSplit dense_simt_fwd_split(const DenseShape& s) {
     const int bm = block_rows(s);
-    return make_split((long long)s.slices * ((s.R + bm - 1) / bm), s.nk, bm);
+    return dense_make_split((long long)s.slices * ((s.R + bm - 1) / bm), s.nk, bm, 4);
 }
 DenseSplit dense_simt_dq_split(const DenseShape& s) { return dense_simt_fwd_split(s); }
 DenseSplit dense_simt_dkv_split(const DenseShape& s) {
     const int bm = block_rows(s);
-    return make_split((long long)s.slices * ((s.nk + bm - 1) / bm), s.R, bm);
+    return dense_make_split((long long)s.slices * ((s.nk + bm - 1) / bm), s.R, bm, 4);
 }
 
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) { return launch_op<kFwd>(s, a, st); }

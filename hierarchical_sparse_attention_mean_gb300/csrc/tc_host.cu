@@ -38,6 +38,19 @@ int make_tmap_bf16(CUtensorMap* map, const void* base, long long rows, int cols,
     return r == CUDA_SUCCESS ? LLSA_OK : LLSA_ERR_CUDA;
 }
 
+int make_tmap_rows(CUtensorMap* map, const void* base, long long slices, long long rows, int d, int box_rows) {
+    const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+    if (!enc) return LLSA_ERR_CUDA;
+    cuuint64_t gdim[3] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slices};
+    cuuint64_t gstride[2] = {(cuuint64_t)d * 2, (cuuint64_t)rows * d * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), gdim, gstride, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LLSA_OK : LLSA_ERR_CUDA;
+}
+
 int make_tmap_tokens(CUtensorMap* map, const void* base, const Shape& s) {
     if (!s.raster) return make_tmap_bf16(map, base, s.slices * (long long)s.n, s.d, 16);
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
