@@ -34,8 +34,8 @@ struct DenseArgs {
     const int *q_len, *k_len;
     void *o_out, *dq, *dk, *dv;
     float* lse_out;
-    float* l2;    // [slices][Rp]: lse * log2(e); +infinity for rows without keys
-    float* dsum;  // [slices][Rp]: D = dout . o
+    float* nl2;   // [slices][Rp]: -lse * log2(e); -infinity for rows without keys
+    float* nd;    // [slices][Rp]: -D = -dout . o; 0 for those rows
     float* part;  // partial sums of a split axis (layout: see the kernels)
     int splits, chunk;  // parts of the split axis, and how many of its elements each takes
     int slices, kv_heads, nq, nk, R, Rp, d, causal;
@@ -113,9 +113,13 @@ int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t 
 int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
-// dense_fwd_tc.cu: tensor-core kernels (bf16, d <= 128).
+// dense_fwd_tc.cu, dense_bwd_tc.cu: tensor-core kernels (bf16, d <= 128).
 bool dense_tc_supported(const DenseShape& s);
 DenseSplit dense_tc_fwd_split(const DenseShape& s);
+DenseSplit dense_tc_dq_split(const DenseShape& s);
+DenseSplit dense_tc_dkv_split(const DenseShape& s);
 int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_tc_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_tc_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
 }  // namespace llsa

@@ -18,9 +18,9 @@ size_t align_up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // ------------------------------------------------------ per-row numbers --
 
-// l2 = lse * log2(e) and D = dout . o of every query row; rows that see no key
-// (and the padding to Rp) get l2 = +infinity, so that their probabilities are
-// 2^(s - l2) = 0, and D = 0. Eight lanes per row. Bound by HBM: dout and o are
+// -lse * log2(e) and -D = -dout . o of every query row; rows that see no key
+// (and the padding to Rp) get -infinity, so that their probabilities are
+// 2^(s - inf) = 0, and D = 0. Eight lanes per row. Bound by HBM: dout and o are
 // read once.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dense_rows_kernel(DenseArgs a) {
@@ -46,8 +46,8 @@ __global__ void __launch_bounds__(kThreads) dense_rows_kernel(DenseArgs a) {
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(lanes, sum, o);
     if (part == 0) {
-        a.l2[idx] = lse == -INFINITY ? INFINITY : lse * kDenseLog2e;
-        a.dsum[idx] = lse == -INFINITY ? 0.f : sum;
+        a.nl2[idx] = lse == -INFINITY ? -INFINITY : -lse * kDenseLog2e;
+        a.nd[idx] = lse == -INFINITY ? 0.f : -sum;
     }
 }
 
@@ -172,8 +172,10 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
 DenseSplit fwd_split(const DenseShape& s) {
     return dense_tc_supported(s) ? dense_tc_fwd_split(s) : dense_simt_fwd_split(s);
 }
-DenseSplit dq_split(const DenseShape& s) { return dense_simt_dq_split(s); }
-DenseSplit dkv_split(const DenseShape& s) { return dense_simt_dkv_split(s); }
+DenseSplit dq_split(const DenseShape& s) { return dense_tc_supported(s) ? dense_tc_dq_split(s) : dense_simt_dq_split(s); }
+DenseSplit dkv_split(const DenseShape& s) {
+    return dense_tc_supported(s) ? dense_tc_dkv_split(s) : dense_simt_dkv_split(s);
+}
 
 }  // namespace
 
@@ -210,8 +212,8 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
     const size_t rows = align_up((size_t)s.slices * s.Rp * sizeof(float));
-    a.l2 = static_cast<float*>(ws);
-    a.dsum = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
+    a.nl2 = static_cast<float*>(ws);
+    a.nd = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * rows);
     if (s.R > 0) {
         const long long blocks = (long long)s.slices * s.Rp / (kThreads / 8);
@@ -223,7 +225,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         const DenseSplit p = dq_split(s);
         a.splits = p.splits;
         a.chunk = p.chunk;
-        LLSA_TRY(launch_dense_simt_dq(s, a, st));
+        LLSA_TRY(dense_tc_supported(s) ? launch_dense_tc_dq(s, a, st) : launch_dense_simt_dq(s, a, st));
         if (p.splits > 1) {
             const long long n = (long long)s.slices * s.R * s.d;
             LLSA_TRY(bf16 ? join_sum<__nv_bfloat16>(a.part, a.dq, n, p.splits, st)
@@ -234,7 +236,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         const DenseSplit p = dkv_split(s);
         a.splits = p.splits;
         a.chunk = p.chunk;
-        LLSA_TRY(launch_dense_simt_dkv(s, a, st));
+        LLSA_TRY(dense_tc_supported(s) ? launch_dense_tc_dkv(s, a, st) : launch_dense_simt_dkv(s, a, st));
         if (p.splits > 1) {
             const long long n = (long long)s.slices * s.nk * s.d;
             const float* second = a.part + (long long)p.splits * n;

@@ -1,0 +1,495 @@
+// dense_bwd_tc.cu -- dense attention backward on the tcgen05 tensor cores (bf16,
+// d <= 128; the tiles hold 64 or 128 columns, TMA fills the rest with zeros).
+//
+// Mathematics, with l2 = lse * log2(e) and D = dout . o of every query row from
+// the pass before: P = 2^(scale log2(e) q.k - l2), dS = P (dout.v - D),
+//   dq = scale dS K          one kernel, blocks own 128 query rows,
+//   dk = scale dS^T Q, dv = P^T dO   the other, blocks own 128 keys.
+// Every sum has one owner and a fixed order, so results repeat bit by bit. One
+// kernel for all three gradients would save two of seven matrix products per
+// tile, at the price of adding dq up across blocks in memory in whatever order
+// they run.
+//
+// Both kernels are one: 128 stationary rows (X1, X2) against a stream of tiles of
+// 128 rows (Y1, Y2), with (X1, X2, Y1, Y2) = (Q, dO, K, V) or (K, V, Q, dO). Per
+// item: S = X1 Y1^T, dP = X2 Y2^T (128 x 128 fp32 in tensor memory), then P and
+// dS as bf16 over dP's columns, then acc1 += dS Y1 and, for keys, acc2 += P Y2,
+// with P and dS as tensor-memory operands. An M = 128 product of two
+// shared-memory operands takes 64 clocks per 16 of K at N = 128 and 48 at N = 64
+// (shared memory feeds it then), so tiles of 128 are worth their tensor memory.
+//
+// The next item's S, and dP where there is room for two of them (all but keys at
+// 128 columns), are issued before this item's sums, so the tensor cores work
+// while the threads turn S and dP into P and dS. All eight softmax warps take one
+// item together, a thread per row and half of the columns.
+//
+// Roles: warps 0-7 elementwise and epilogue, warp 8 issues the MMAs, warps 9 and
+// 10 the copies of the two streams (one warp issues a 16 KB copy about every 500
+// clocks, less than the tensor cores eat).
+#include <algorithm>
+
+#include "dense.h"
+#include "tc.cuh"
+
+namespace llsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 384;
+constexpr int BT = 128;  // rows of every tile
+
+template <int D, bool KEYS>
+struct Cfg {
+    static constexpr int TILE = BT * D * 2;   // bytes of 128 rows
+    static constexpr int REGION = BT * 128;   // bytes of 128 rows x 64 columns
+    static constexpr int N1 = D == 64 ? 4 : 3, N2 = D == 64 ? 4 : 2;  // stages of the two streams
+    static constexpr int NB = D == 128 && KEYS ? 1 : 2;               // dP buffers
+    static constexpr int STATS = KEYS ? N2 * 2 * BT * 4 : 0;          // -l2 and -D of a row tile, with stream 2
+    static constexpr int SMEM = (2 + N1 + N2) * TILE + STATS + 512;
+    static constexpr int TM_DP = 128, TM_ACC = 128 + NB * 128;        // S at column 0
+};
+
+struct Bars {
+    uint64_t x_full[2], y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
+    uint64_t s_full, s_free, dp_full[2], ds_ready[2], acc_full, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, const DenseArgs& a) {
+    return __all_sync(0xffffffffu, mbar_wait(mbar, parity, abort_flag, a.status, a.spin));
+}
+
+// The items of a block: tiles of 128 rows of the streamed side, those that the
+// mask leaves nothing of skipped. Every role walks the same list.
+template <bool KEYS>
+struct Items {
+    int pos, t0, stop;  // first row of the tile; its token in its head (KEYS); end of the axis
+    int x0;             // the block's first stationary row
+    DenseSpan sp;
+
+    __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int first, int end)
+        : pos(first), t0(KEYS ? first % a.nq : 0), stop(end), x0(x0_), sp(s) {
+        settle(a);
+    }
+    __device__ __forceinline__ bool done() const { return pos >= stop; }
+    __device__ __forceinline__ void next(const DenseArgs& a) {
+        step(a);
+        settle(a);
+    }
+
+private:
+    __device__ __forceinline__ void step(const DenseArgs& a) {
+        pos += BT;
+        if constexpr (KEYS) {
+            t0 += BT;
+            if (t0 >= a.nq) t0 %= a.nq;
+        }
+    }
+    __device__ __forceinline__ void settle(const DenseArgs& a) {
+        if constexpr (KEYS)
+            while (pos < stop && dense_tile_kend(a, sp, t0, BT) <= x0) step(a);
+    }
+};
+
+template <int D, bool KEYS>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
+                    const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2,
+                    const __grid_constant__ DenseArgs a) {
+    using C = Cfg<D, KEYS>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char* sX = sm;  // X1, X2
+    unsigned char* ring1 = sm + 2 * C::TILE;
+    unsigned char* ring2 = ring1 + C::N1 * C::TILE;
+    float* stats = reinterpret_cast<float*>(ring2 + C::N2 * C::TILE);
+    Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * C::TILE + C::STATS);
+    volatile int* abort_flag = &bar->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
+        if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
+        return;
+    }
+
+    // causal order: the last rows see the most keys, the first keys the most rows; those blocks go first
+    const int extent = KEYS ? a.nk : a.R;
+    const int blocks = (extent + BT - 1) / BT;
+    const int slice = blockIdx.x / blocks;
+    const int idx = (int)(blockIdx.x - slice * blocks);
+    const int x0 = (KEYS ? idx : blocks - 1 - idx) * BT;
+    const int part = blockIdx.y;
+    const DenseSpan sp = dense_span(a, slice);
+    int first = a.splits > 1 ? part * a.chunk : 0, stop;
+    if constexpr (KEYS) {
+        stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
+    } else {
+        stop = dense_tile_kend(a, sp, x0 % a.nq, BT);
+        if (a.splits > 1) stop = min(stop, first + a.chunk);
+    }
+    const bool any = !Items<KEYS>(a, sp, x0, first, stop).done();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&bar->x_full[i]), 1);
+            mbar_init(smem_u32(&bar->dp_full[i]), 1);
+            mbar_init(smem_u32(&bar->ds_ready[i]), 256);
+        }
+        for (int i = 0; i < 4; i++) {
+            mbar_init(smem_u32(&bar->y1_full[i]), 1);
+            mbar_init(smem_u32(&bar->y1_empty[i]), 1);
+            mbar_init(smem_u32(&bar->y2_full[i]), 1);
+            mbar_init(smem_u32(&bar->y2_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->s_full), 1);
+        mbar_init(smem_u32(&bar->s_free), 256);
+        mbar_init(smem_u32(&bar->acc_full), 1);
+        mbar_init(smem_u32(&bar->drain), 1);
+        bar->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = bar->tmem_slot;
+
+    if (warp == 9 || warp == 10) {
+        // ----------------------------------------------------------- copies
+        if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+            const int k = warp - 9;  // stream
+            const int ns = k == 0 ? C::N1 : C::N2;
+            unsigned char* ring = k == 0 ? ring1 : ring2;
+            uint64_t* full = k == 0 ? bar->y1_full : bar->y2_full;
+            uint64_t* empty = k == 0 ? bar->y1_empty : bar->y2_empty;
+            const CUtensorMap* mx = k == 0 ? &mx1 : &mx2;
+            const CUtensorMap* my = k == 0 ? &my1 : &my2;
+            const uint32_t xb = smem_u32(&bar->x_full[k]);
+            mbar_arrive_expect_tx(xb, C::TILE);
+            for (int c = 0; c < D / 64; c++)
+                tma_load_3d(smem_u32(sX + k * C::TILE + c * C::REGION), mx, c * 64, x0, slice, xb);
+            int st = 0, n = 0;
+            uint32_t parity = 1;  // of the stage's release before its use `n / ns`
+            for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a)) {
+                if (n >= ns && !mbar_wait(smem_u32(&empty[st]), parity, abort_flag, a.status, a.spin)) break;
+                const uint32_t fb = smem_u32(&full[st]);
+                const bool with_stats = KEYS && k == 1;
+                mbar_arrive_expect_tx(fb, C::TILE + (with_stats ? 2 * BT * 4 : 0));
+                for (int c = 0; c < D / 64; c++)
+                    tma_load_3d(smem_u32(ring + st * C::TILE + c * C::REGION), my, c * 64, it.pos, slice, fb);
+                if (with_stats) {
+                    const long long row = (long long)slice * a.Rp + it.pos;
+                    bulk_load(smem_u32(stats + st * 2 * BT), a.nl2 + row, BT * 4, fb);
+                    bulk_load(smem_u32(stats + st * 2 * BT + BT), a.nd + row, BT * 4, fb);
+                }
+                n++;
+                if (++st == ns) {
+                    st = 0;
+                    parity ^= 1;
+                }
+            }
+            // copies still in flight must land before the block exits
+            for (int i = 0; i < kSpinLimit && !mbar_try(xb, 0); i++) {
+            }
+            for (int x = max(0, n - ns); x < n; x++)
+                for (int i = 0; i < kSpinLimit && !mbar_try(smem_u32(&full[x % ns]), (x / ns) & 1); i++) {
+                }
+        }
+    } else if (warp == 8) {
+        // ------------------------------------------------------- MMA issuer
+        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, D, 0, 1);
+        const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024);
+        const uint64_t dY1 = desc_sw128(smem_u32(ring1), 16, 1024), dY2 = desc_sw128(smem_u32(ring2), 16, 1024);
+        const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the same tiles read along their rows
+        const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
+        // Rows of the streamed tile whose P and dS are 0 by the mask of the
+        // lengths may hold anything: they meet those zeros in the sums, so
+        // they are cleared.
+        auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
+            if constexpr (KEYS) {
+                if (sp.lq == a.nq || it.t0 + BT <= sp.lq) return;
+                int t = it.t0 + lane;
+                for (int x = lane; x < BT; x += 32, t += 32)
+                    if (t % a.nq >= sp.lq)
+                        for (int c = 0; c < D / 64; c++)
+                            for (int e = 0; e < 8; e++)
+                                reinterpret_cast<uint4*>(tile + c * C::REGION + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                const int live = sp.lk - it.pos;
+                if (live >= BT) return;
+                for (int c = 0; c < D / 64; c++)
+                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
+                        reinterpret_cast<uint4*>(tile + c * C::REGION)[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            __syncwarp();
+        };
+        auto issue_S = [&](int n, const Items<KEYS>& it) -> bool {
+            const int st = n % C::N1;
+            if (!warp_wait(smem_u32(&bar->y1_full[st]), (n / C::N1) & 1, abort_flag, a)) return false;
+            clear_rows(ring1 + st * C::TILE, it);
+            if (n > 0 && !warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a)) return false;
+            tc_fence_after();
+            const uint32_t y0 = (uint32_t)(st * C::TILE);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks++) {
+                const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                mma_bf16_warp(tbase, dX + (off >> 4), dY1 + ((y0 + off) >> 4), idS, ks > 0);
+            }
+            mma_commit_warp(smem_u32(&bar->s_full));
+            return true;
+        };
+        auto issue_dP = [&](int n, const Items<KEYS>& it) -> bool {
+            const int st = n % C::N2, b = n % C::NB;
+            if (!warp_wait(smem_u32(&bar->y2_full[st]), (n / C::N2) & 1, abort_flag, a)) return false;
+            if (KEYS) clear_rows(ring2 + st * C::TILE, it);  // V only enters dP, which the mask covers
+            tc_fence_after();
+            const uint32_t y0 = (uint32_t)(st * C::TILE);
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ks++) {
+                const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                mma_bf16_warp(tbase + C::TM_DP + b * 128, dX + ((C::TILE + off) >> 4), dY2 + ((y0 + off) >> 4), idS, ks > 0);
+            }
+            mma_commit_warp(smem_u32(&bar->dp_full[b]));
+            if (!KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[st]));
+            return true;
+        };
+        auto issue_sums = [&](int n) -> bool {
+            const int s1 = n % C::N1, s2 = n % C::N2, b = n % C::NB;
+            if (!warp_wait(smem_u32(&bar->ds_ready[b]), (n / C::NB) & 1, abort_flag, a)) return false;
+            tc_fence_after();
+            const uint32_t p0 = tbase + C::TM_DP + b * 128;
+#pragma unroll
+            for (int ks = 0; ks < BT / 16; ks++) {
+                const uint32_t op = p0 + (ks / 4) * 64 + (ks % 4) * 8;  // each half of the columns: P, then dS, 32 columns each
+                if constexpr (KEYS) {
+                    mma_bf16_ts_warp(tbase + C::TM_ACC + D, op, dM2 + ((s2 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
+                    mma_bf16_ts_warp(tbase + C::TM_ACC, op + 32, dM1 + ((s1 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
+                } else {
+                    mma_bf16_ts_warp(tbase + C::TM_ACC, op, dM1 + ((s1 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
+                }
+            }
+            mma_commit_warp(smem_u32(&bar->y1_empty[s1]));
+            if (KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2]));
+            return true;
+        };
+        if (any) {
+            Items<KEYS> it(a, sp, x0, first, stop);
+            bool ok = warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
+                      warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
+            ok = ok && issue_S(0, it) && issue_dP(0, it);
+            it.next(a);
+            for (int n = 0; ok; n++) {  // item n is under way, `it` is item n + 1
+                const bool more = !it.done();
+                if (more) ok = issue_S(n + 1, it);
+                if (ok && more && C::NB == 2) ok = issue_dP(n + 1, it);
+                ok = ok && issue_sums(n);
+                if (ok && more && C::NB == 1) ok = issue_dP(n + 1, it);
+                if (!more) break;
+                it.next(a);
+            }
+            if (ok) mma_commit_warp(smem_u32(&bar->acc_full));
+        }
+        // no MMA may be in flight when tensor memory is released
+        mma_commit_warp(smem_u32(&bar->drain));
+        if (lane == 0)
+            for (int i = 0; i < kSpinLimit && !mbar_try(smem_u32(&bar->drain), 0); i++) {
+            }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ---------------------------------------- elementwise, epilogue
+        const int w = warp >> 2;  // half of the columns
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int x = x0 + (warp & 3) * 32 + lane;  // stationary row
+        const float sl2 = a.scale * kDenseLog2e;
+        const uint64_t sl2x2 = pack2(sl2, sl2);
+        uint64_t nl2x2 = 0, ndx2 = 0;
+        int kend = 0;
+        if constexpr (!KEYS) {
+            const long long row = (long long)slice * a.Rp + x;  // Rp is a multiple of 128
+            const float nl2 = a.nl2[row], nd = a.nd[row];
+            nl2x2 = pack2(nl2, nl2);
+            ndx2 = pack2(nd, nd);
+            kend = x < a.R ? dense_kend(a, sp, x % a.nq) : 0;
+        }
+        int n = 0;
+        for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a), n++) {
+            const int b = n % C::NB;
+            const uint32_t tP = tbase + C::TM_DP + b * 128 + w * 64 + lanes;
+            const float* st = stats + (n % C::N2) * 2 * BT + w * 64;  // KEYS: -l2 of this half's rows; -D follows BT later
+            mbar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a.status, a.spin);
+            tc_fence_after();
+            uint32_t s[64];
+            tmem_ld32_nowait(tbase + lanes + w * 64, s);
+            tmem_ld32_nowait(tbase + lanes + w * 64 + 32, s + 32);
+            if constexpr (KEYS) mbar_wait(smem_u32(&bar->y2_full[n % C::N2]), (n / C::N2) & 1, abort_flag, a.status, a.spin);
+            tmem_wait_ld();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&bar->s_free));
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                uint64_t l0 = nl2x2, l1 = nl2x2;
+                if constexpr (KEYS) {
+                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + c);
+                    l0 = u.x;
+                    l1 = u.y;
+                }
+                float e0, e1, e2, e3;
+                unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2x2, l0), e0, e1);
+                unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2x2, l1), e2, e3);
+                s[c] = __float_as_uint(ex2(e0));
+                s[c + 1] = __float_as_uint(ex2(e1));
+                s[c + 2] = __float_as_uint(ex2(e2));
+                s[c + 3] = __float_as_uint(ex2(e3));
+            }
+            // which of this thread's columns the mask leaves
+            bool masked;
+            if constexpr (KEYS) {
+                // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
+                masked = a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT);
+                if (masked) {
+                    int t = (it.t0 + w * 64) % a.nq;
+#pragma unroll
+                    for (int c = 0; c < 64; c++) {
+                        if (x > t + sp.lk - sp.lq) s[c] = 0u;
+                        if (++t == a.nq) t = 0;
+                    }
+                }
+            } else {
+                masked = __any_sync(0xffffffffu, kend - it.pos < BT);
+                if (masked) {
+#pragma unroll
+                    for (int c = 0; c < 64; c++)
+                        if (w * 64 + c >= kend - it.pos) s[c] = 0u;
+                }
+            }
+            mbar_wait(smem_u32(&bar->dp_full[b]), (n / C::NB) & 1, abort_flag, a.status, a.spin);
+            tc_fence_after();
+            uint32_t g[64];
+            tmem_ld32_nowait(tP, g);
+            tmem_ld32_nowait(tP + 32, g + 32);
+            tmem_wait_ld();
+            uint32_t o[32];
+            if constexpr (KEYS) {
+#pragma unroll
+                for (int c = 0; c < 64; c += 2) o[c >> 1] = pack_bf16x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                tmem_st32(tP, o);
+            }
+#pragma unroll
+            for (int c = 0; c < 64; c += 4) {
+                uint64_t d0 = ndx2, d1 = ndx2;
+                if constexpr (KEYS) {
+                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + BT + c);
+                    d0 = u.x;
+                    d1 = u.y;
+                }
+                float e0, e1, e2, e3;
+                unpack2(mul2(add2(pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), d0),
+                             pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]))), e0, e1);
+                unpack2(mul2(add2(pack2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), d1),
+                             pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]))), e2, e3);
+                if (!KEYS && masked) {  // dP of a key behind the lengths may be anything
+                    const int lim = kend - it.pos - w * 64;
+                    e0 = c < lim ? e0 : 0.f;
+                    e1 = c + 1 < lim ? e1 : 0.f;
+                    e2 = c + 2 < lim ? e2 : 0.f;
+                    e3 = c + 3 < lim ? e3 : 0.f;
+                }
+                o[c >> 1] = pack_bf16x2(e0, e1);
+                o[(c >> 1) + 1] = pack_bf16x2(e2, e3);
+            }
+            tmem_st32(KEYS ? tP + 32 : tP, o);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&bar->ds_ready[b]));
+        }
+        if (any) {
+            mbar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a.status, a.spin);
+            tc_fence_after();
+        }
+        // rows without a gradient hold whatever their padding made: zero
+        const bool live = any && (KEYS ? x < sp.lk : kend > 0);
+        const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
+#pragma unroll
+        for (int k = 0; k < (KEYS ? 2 : 1); k++) {
+            const float f = k == 0 ? a.scale : 1.f;
+#pragma unroll
+            for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
+                uint32_t o[32];
+                if (any) {
+                    tmem_ld32_nowait(tbase + C::TM_ACC + k * D + c + lanes, o);
+                    tmem_wait_ld();
+                }
+                if (x < extent) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 8) {
+                        if (c + i >= a.d) break;
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) v[e] = live ? __uint_as_float(o[i + e]) * f : 0.f;
+                        if (a.splits > 1) {
+                            float* dst = a.part + ((k * a.splits + part) * all + row) * a.d + c + i;
+                            store4(dst, v);
+                            store4(dst + 4, v + 4);
+                        } else {
+                            uint4 u;
+                            u.x = pack_bf16x2(v[0], v[1]);
+                            u.y = pack_bf16x2(v[2], v[3]);
+                            u.z = pack_bf16x2(v[4], v[5]);
+                            u.w = pack_bf16x2(v[6], v[7]);
+                            void* base = KEYS ? (k == 0 ? a.dk : a.dv) : a.dq;
+                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + row * a.d + c + i) = u;
+                        }
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+template <int D, bool KEYS>
+int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    using C = Cfg<D, KEYS>;
+    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
+    CUtensorMap mq, mk, mv, mg;
+    LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mg, a.dout, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mv, a.v, s.slices, s.nk, s.d, BT));
+    cudaFuncSetAttribute(dense_bwd_tc_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const int extent = KEYS ? s.nk : s.R;
+    const long long blocks = (long long)((extent + BT - 1) / BT) * s.slices;
+    if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, a.splits);
+    if constexpr (KEYS)
+        LLSA_LAUNCH("dense_dkv_tc", st,
+                    dense_bwd_tc_kernel<D, true><<<grid, kThreads, C::SMEM, st>>>(mk, mv, mq, mg, a));
+    else
+        LLSA_LAUNCH("dense_dq_tc", st,
+                    dense_bwd_tc_kernel<D, false><<<grid, kThreads, C::SMEM, st>>>(mq, mg, mk, mv, a));
+    return LLSA_OK;
+}
+
+}  // namespace
+
+DenseSplit dense_tc_dq_split(const DenseShape& s) {
+    return dense_make_split((long long)s.slices * ((s.R + BT - 1) / BT), s.nk, BT, 2);
+}
+DenseSplit dense_tc_dkv_split(const DenseShape& s) {
+    return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT), s.R, BT, 2);
+}
+
+int launch_dense_tc_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    return s.d <= 64 ? launch<64, false>(s, a, st) : launch<128, false>(s, a, st);
+}
+int launch_dense_tc_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    return s.d <= 64 ? launch<64, true>(s, a, st) : launch<128, true>(s, a, st);
+}
+
+}  // namespace llsa

@@ -238,13 +238,13 @@ __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
     load_tile<T, DP, BM>(sQ, q, r0, a.d, row_ok);
     load_tile<T, DP, BM>(sG, g, r0, a.d, row_ok);
     int kend[N];
-    float l2[N], dsum[N];
+    float nl2[N], nd[N];
 #pragma unroll
     for (int i = 0; i < N; i++) {
         const int r = r0 + ty * N + i;
         kend[i] = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
-        l2[i] = r < a.R ? a.l2[(long long)slice * a.Rp + r] : INFINITY;
-        dsum[i] = r < a.R ? a.dsum[(long long)slice * a.Rp + r] : 0.f;
+        nl2[i] = r < a.R ? a.nl2[(long long)slice * a.Rp + r] : -INFINITY;
+        nd[i] = r < a.R ? a.nd[(long long)slice * a.Rp + r] : 0.f;
     }
     const int j_first = part * a.chunk;
     const int j_last = min(dense_tile_kend(a, sp, r0 % a.nq, BM), a.splits > 1 ? j_first + a.chunk : a.nk);
@@ -266,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
         for (int i = 0; i < N; i++)
 #pragma unroll
             for (int j = 0; j < N; j++) {
-                const float p = exp2f(fmaf(s[i][j], sl2, -l2[i]));
-                s[i][j] = j0 + tx + 16 * j < kend[i] ? p * (dp[i][j] - dsum[i]) : 0.f;
+                const float p = exp2f(fmaf(s[i][j], sl2, nl2[i]));
+                s[i][j] = j0 + tx + 16 * j < kend[i] ? p * (dp[i][j] + nd[i]) : 0.f;
             }
         store_p<N>(sP, s, ty, tx);
         __syncthreads();
@@ -330,13 +330,13 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
         for (int j = 0; j < N; j++) {
             const int r = r0 + tx + 16 * j;
             const int kend = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
-            const float l2 = r < a.R ? a.l2[(long long)slice * a.Rp + r] : INFINITY;
-            const float dsum = r < a.R ? a.dsum[(long long)slice * a.Rp + r] : 0.f;
+            const float nl2 = r < a.R ? a.nl2[(long long)slice * a.Rp + r] : -INFINITY;
+            const float nd = r < a.R ? a.nd[(long long)slice * a.Rp + r] : 0.f;
 #pragma unroll
             for (int i = 0; i < N; i++) {
-                const float p = j0 + ty * N + i < kend ? exp2f(fmaf(s[i][j], sl2, -l2)) : 0.f;
+                const float p = j0 + ty * N + i < kend ? exp2f(fmaf(s[i][j], sl2, nl2)) : 0.f;
                 s[i][j] = p;
-                dp[i][j] = p * (dp[i][j] - dsum);
+                dp[i][j] = p * (dp[i][j] + nd);
             }
         }
         store_p<N>(sP, s, ty, tx);
