@@ -14,6 +14,7 @@ Transformers" (arXiv 2512.16615), as described on its Pith review page
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -243,14 +244,13 @@ class RopeParams:
     def __post_init__(self):
         scaling, order = _choice(_ROPE_SCALINGS, self.scaling, "scaling"), _choice(_ORDERS, self.token_order, "token_order")
         layout, dt = _choice(_ROPE_LAYOUTS, self.layout, "layout"), _choice(_DTYPES, self.dtype, "dtype")
-        for batched in (0, 1):
-            object.__setattr__(self, f"_c{batched}", _RopeParams(
-                self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width, order,
-                self.pos_offset, batched, dt, scaling, self.orig_len, self.base, self.factor, self.low, self.high,
-                self.amplitude))
+        object.__setattr__(self, "_names", (layout, order, dt, scaling))
 
     def c(self, pos_batched: bool = False) -> _RopeParams:
-        return self._c1 if pos_batched else self._c0
+        layout, order, dt, scaling = self._names
+        return _RopeParams(self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width,
+                           order, self.pos_offset, 1 if pos_batched else 0, dt, scaling, self.orig_len, self.base, self.factor,
+                           self.low, self.high, self.amplitude)
 
     @staticmethod
     def like(q, k=None, **kw) -> "RopeParams":
@@ -307,7 +307,7 @@ def _ptr(t, name, dtype=None):
 def _stream(stream):
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -399,14 +399,20 @@ def llsa_bwd(p: Params, q, k, v, o, lse, dout, pyr, sel_idx, coarse_idx, col_ptr
 
 def _like(t, name, shape, dtype, device):
     """Pointer of a contiguous tensor of exactly this shape, type and device."""
-    ptr = _ptr(t, name, dtype)
+    import torch
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
+    ptr = _ptr(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     return ptr
+
+
+_HERE = contextlib.nullcontext()
 
 
 def _on(t, name):
@@ -416,7 +422,7 @@ def _on(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
 
 
 def dense_workspace_bytes(p: DenseParams, op: int) -> int:
@@ -471,7 +477,7 @@ def _strided(t, name, shape, dtype, device, out):
     s = t.stride()
     if s[3] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    out[0], out[1], out[2] = s[0], s[1], s[2]
+    out[:] = s[:3]
     return t.data_ptr()
 
 

@@ -20,23 +20,24 @@
 //
 // The next item's S, and dP where there is room for two of them (all but keys at
 // 128 columns), are issued before this item's sums, so the tensor cores work
-// while the threads turn S and dP into P and dS. All eight softmax warps take one
-// item together, a thread per row and half of the columns.
+// while the threads turn S and dP into P and dS. All sixteen elementwise warps
+// take one item together, a thread per row and quarter of the columns.
 //
-// Roles: warps 0-7 elementwise and epilogue, warp 8 issues the MMAs, warps 9 and
-// 10 the copies of the two streams (one warp issues a 16 KB copy about every 500
-// clocks, less than the tensor cores eat).
+// Roles: warps 0-15 elementwise and epilogue, warp 16 issues S and dP, warp 17
+// the sums, warps 18 and 19 the copies of the two streams. Waits and the issue of a
+// dozen MMAs add up to some thousand clocks per item, so one warp for all of them
+// would be what the kernel waits for.
 #include <algorithm>
 
-#include "dense.h"
-#include "tc.cuh"
+#include "dense_tc.cuh"
 
 namespace llsa {
 namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kWarps = 16, kCols = 32;  // elementwise warps: a thread takes one row and kCols columns of an item
+constexpr int kThreads = (kWarps + 4) * 32;
 constexpr int BT = 128;  // rows of every tile
 
 template <int D, bool KEYS>
@@ -52,14 +53,10 @@ struct Cfg {
 
 struct Bars {
     uint64_t x_full[2], y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
-    uint64_t s_full, s_free, dp_full[2], ds_ready[2], acc_full, drain;
+    uint64_t s_full, s_free, dp_full[2], ds_ready[2], dp_free[2], acc_full, drain[2];
     uint32_t tmem_slot;
     int abort_flag;
 };
-
-__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, const DenseArgs& a) {
-    return __all_sync(0xffffffffu, mbar_wait(mbar, parity, abort_flag, a.status, a.spin));
-}
 
 // The items of a block: tiles of 128 rows of the streamed side, those that the
 // mask leaves nothing of skipped. Every role walks the same list.
@@ -67,29 +64,33 @@ template <bool KEYS>
 struct Items {
     int pos, t0, stop;  // first row of the tile; its token in its head (KEYS); end of the axis
     int x0;             // the block's first stationary row
+    bool all;           // no tile to skip, no row to clear
     DenseSpan sp;
 
     __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int first, int end)
-        : pos(first), t0(KEYS ? first % a.nq : 0), stop(end), x0(x0_), sp(s) {
+        : pos(first), t0(0), stop(end), x0(x0_), all(!KEYS || (!a.causal && s.lq == a.nq)), sp(s) {
+        if (all) return;
+        t0 = first % a.nq;
         settle(a);
     }
     __device__ __forceinline__ bool done() const { return pos >= stop; }
     __device__ __forceinline__ void next(const DenseArgs& a) {
-        step(a);
+        pos += BT;
+        if (all) return;
+        turn(a);
         settle(a);
     }
 
 private:
-    __device__ __forceinline__ void step(const DenseArgs& a) {
-        pos += BT;
-        if constexpr (KEYS) {
-            t0 += BT;
-            if (t0 >= a.nq) t0 %= a.nq;
-        }
+    __device__ __forceinline__ void turn(const DenseArgs& a) {
+        t0 += BT;
+        if (t0 >= a.nq) t0 = t0 - a.nq < a.nq ? t0 - a.nq : t0 % a.nq;
     }
     __device__ __forceinline__ void settle(const DenseArgs& a) {
-        if constexpr (KEYS)
-            while (pos < stop && dense_tile_kend(a, sp, t0, BT) <= x0) step(a);
+        while (pos < stop && dense_tile_kend(a, sp, t0, BT) <= x0) {
+            pos += BT;
+            turn(a);
+        }
     }
 };
 
@@ -133,7 +134,9 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&bar->x_full[i]), 1);
             mbar_init(smem_u32(&bar->dp_full[i]), 1);
-            mbar_init(smem_u32(&bar->ds_ready[i]), 256);
+            mbar_init(smem_u32(&bar->ds_ready[i]), kWarps);
+            mbar_init(smem_u32(&bar->dp_free[i]), 1);
+            mbar_init(smem_u32(&bar->drain[i]), 1);
         }
         for (int i = 0; i < 4; i++) {
             mbar_init(smem_u32(&bar->y1_full[i]), 1);
@@ -142,22 +145,21 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             mbar_init(smem_u32(&bar->y2_empty[i]), 1);
         }
         mbar_init(smem_u32(&bar->s_full), 1);
-        mbar_init(smem_u32(&bar->s_free), 256);
+        mbar_init(smem_u32(&bar->s_free), kWarps);
         mbar_init(smem_u32(&bar->acc_full), 1);
-        mbar_init(smem_u32(&bar->drain), 1);
         bar->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = bar->tmem_slot;
 
-    if (warp == 9 || warp == 10) {
+    if (warp >= kWarps + 2) {
         // ----------------------------------------------------------- copies
         if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
-            const int k = warp - 9;  // stream
+            const int k = warp - kWarps - 2;  // stream
             const int ns = k == 0 ? C::N1 : C::N2;
             unsigned char* ring = k == 0 ? ring1 : ring2;
             uint64_t* full = k == 0 ? bar->y1_full : bar->y2_full;
@@ -169,9 +171,9 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             for (int c = 0; c < D / 64; c++)
                 tma_load_3d(smem_u32(sX + k * C::TILE + c * C::REGION), mx, c * 64, x0, slice, xb);
             int st = 0, n = 0;
-            uint32_t parity = 1;  // of the stage's release before its use `n / ns`
+            uint32_t parity = 1;  // of the release that the stage's next use waits for
             for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a)) {
-                if (n >= ns && !mbar_wait(smem_u32(&empty[st]), parity, abort_flag, a.status, a.spin)) break;
+                if (n >= ns && !bar_wait(smem_u32(&empty[st]), parity, abort_flag, a)) break;
                 const uint32_t fb = smem_u32(&full[st]);
                 const bool with_stats = KEYS && k == 1;
                 mbar_arrive_expect_tx(fb, C::TILE + (with_stats ? 2 * BT * 4 : 0));
@@ -188,26 +190,20 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                     parity ^= 1;
                 }
             }
-            // copies still in flight must land before the block exits
-            for (int i = 0; i < kSpinLimit && !mbar_try(xb, 0); i++) {
-            }
-            for (int x = max(0, n - ns); x < n; x++)
-                for (int i = 0; i < kSpinLimit && !mbar_try(smem_u32(&full[x % ns]), (x / ns) & 1); i++) {
-                }
+            land(xb, 0);
+            for (int x = max(0, n - ns); x < n; x++) land(smem_u32(&full[x % ns]), (x / ns) & 1);
         }
-    } else if (warp == 8) {
-        // ------------------------------------------------------- MMA issuer
-        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, D, 0, 1);
+    } else if (warp == kWarps) {
+        // --------------------------------------------------- S and dP issuer
+        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0);
         const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024);
         const uint64_t dY1 = desc_sw128(smem_u32(ring1), 16, 1024), dY2 = desc_sw128(smem_u32(ring2), 16, 1024);
-        const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the same tiles read along their rows
-        const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
         // Rows of the streamed tile whose P and dS are 0 by the mask of the
         // lengths may hold anything: they meet those zeros in the sums, so
         // they are cleared.
         auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
             if constexpr (KEYS) {
-                if (sp.lq == a.nq || it.t0 + BT <= sp.lq) return;
+                if (it.all || it.t0 + BT <= sp.lq) return;
                 int t = it.t0 + lane;
                 for (int x = lane; x < BT; x += 32, t += 32)
                     if (t % a.nq >= sp.lq)
@@ -224,81 +220,93 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             fence_async_smem();
             __syncwarp();
         };
-        auto issue_S = [&](int n, const Items<KEYS>& it) -> bool {
-            const int st = n % C::N1;
-            if (!warp_wait(smem_u32(&bar->y1_full[st]), (n / C::N1) & 1, abort_flag, a)) return false;
-            clear_rows(ring1 + st * C::TILE, it);
-            if (n > 0 && !warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a)) return false;
-            tc_fence_after();
-            const uint32_t y0 = (uint32_t)(st * C::TILE);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ks++) {
-                const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                mma_bf16_warp(tbase, dX + (off >> 4), dY1 + ((y0 + off) >> 4), idS, ks > 0);
-            }
-            mma_commit_warp(smem_u32(&bar->s_full));
-            return true;
-        };
-        auto issue_dP = [&](int n, const Items<KEYS>& it) -> bool {
-            const int st = n % C::N2, b = n % C::NB;
-            if (!warp_wait(smem_u32(&bar->y2_full[st]), (n / C::N2) & 1, abort_flag, a)) return false;
-            if (KEYS) clear_rows(ring2 + st * C::TILE, it);  // V only enters dP, which the mask covers
-            tc_fence_after();
-            const uint32_t y0 = (uint32_t)(st * C::TILE);
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ks++) {
-                const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                mma_bf16_warp(tbase + C::TM_DP + b * 128, dX + ((C::TILE + off) >> 4), dY2 + ((y0 + off) >> 4), idS, ks > 0);
-            }
-            mma_commit_warp(smem_u32(&bar->dp_full[b]));
-            if (!KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[st]));
-            return true;
-        };
-        auto issue_sums = [&](int n) -> bool {
-            const int s1 = n % C::N1, s2 = n % C::N2, b = n % C::NB;
-            if (!warp_wait(smem_u32(&bar->ds_ready[b]), (n / C::NB) & 1, abort_flag, a)) return false;
-            tc_fence_after();
-            const uint32_t p0 = tbase + C::TM_DP + b * 128;
-#pragma unroll
-            for (int ks = 0; ks < BT / 16; ks++) {
-                const uint32_t op = p0 + (ks / 4) * 64 + (ks % 4) * 8;  // each half of the columns: P, then dS, 32 columns each
-                if constexpr (KEYS) {
-                    mma_bf16_ts_warp(tbase + C::TM_ACC + D, op, dM2 + ((s2 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
-                    mma_bf16_ts_warp(tbase + C::TM_ACC, op + 32, dM1 + ((s1 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
-                } else {
-                    mma_bf16_ts_warp(tbase + C::TM_ACC, op, dM1 + ((s1 * C::TILE + ks * 2048) >> 4), idA, n > 0 || ks > 0);
-                }
-            }
-            mma_commit_warp(smem_u32(&bar->y1_empty[s1]));
-            if (KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2]));
-            return true;
-        };
         if (any) {
-            Items<KEYS> it(a, sp, x0, first, stop);
             bool ok = warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
                       warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
-            ok = ok && issue_S(0, it) && issue_dP(0, it);
-            it.next(a);
-            for (int n = 0; ok; n++) {  // item n is under way, `it` is item n + 1
-                const bool more = !it.done();
-                if (more) ok = issue_S(n + 1, it);
-                if (ok && more && C::NB == 2) ok = issue_dP(n + 1, it);
-                ok = ok && issue_sums(n);
-                if (ok && more && C::NB == 1) ok = issue_dP(n + 1, it);
-                if (!more) break;
-                it.next(a);
+            Stage<C::N1> s1;
+            Stage<C::N2> s2;
+            Stage<C::NB> sb;
+            uint32_t n = 0;
+            for (Items<KEYS> it(a, sp, x0, first, stop); ok && !it.done(); it.next(a), n++) {
+                ok = warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a);
+                if (!ok) break;
+                clear_rows(ring1 + s1.st * C::TILE, it);
+                if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t y1 = (uint32_t)(s1.st * C::TILE);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                    mma_bf16_warp(tbase, dX + (off >> 4), dY1 + ((y1 + off) >> 4), idS, ks > 0);
+                }
+                mma_commit_warp(smem_u32(&bar->s_full));
+                ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
+                if (!ok) break;
+                if (KEYS) clear_rows(ring2 + s2.st * C::TILE, it);  // V only enters dP, which the mask covers
+                if (n >= C::NB) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t y2 = (uint32_t)(s2.st * C::TILE);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                    mma_bf16_warp(tbase + C::TM_DP + sb.st * 128, dX + ((C::TILE + off) >> 4), dY2 + ((y2 + off) >> 4), idS,
+                                  ks > 0);
+                }
+                mma_commit_warp(smem_u32(&bar->dp_full[sb.st]));
+                if (!KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2.st]));
+                s1.next();
+                s2.next();
+                sb.next();
+            }
+        }
+        // no MMA may be in flight when tensor memory is released
+        mma_commit_warp(smem_u32(&bar->drain[0]));
+        if (lane == 0) land(smem_u32(&bar->drain[0]), 0);
+        __syncwarp();
+    } else if (warp == kWarps + 1) {
+        // ------------------------------------------------------- sums issuer
+        constexpr uint32_t idA = idesc_bf16(BT, D, 0, 1);
+        const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the tiles read along their rows
+        const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
+        if (any) {
+            bool ok = true;
+            Stage<C::N1> s1;
+            Stage<C::N2> s2;
+            Stage<C::NB> sb;
+            uint32_t n = 0;
+            for (Items<KEYS> it(a, sp, x0, first, stop); ok && !it.done(); it.next(a), n++) {
+                ok = warp_wait(smem_u32(&bar->ds_ready[sb.st]), sb.parity, abort_flag, a);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t p0 = tbase + C::TM_DP + sb.st * 128;
+#pragma unroll
+                for (int ks = 0; ks < BT / 16; ks++) {
+                    const uint32_t op = p0 + (ks / 2) * 32 + (ks % 2) * 8;  // each quarter of the columns: P, then dS, 16 columns each
+                    const uint64_t m1 = dM1 + ((s1.st * C::TILE + ks * 2048) >> 4), m2 = dM2 + ((s2.st * C::TILE + ks * 2048) >> 4);
+                    if constexpr (KEYS) {
+                        mma_bf16_ts_warp(tbase + C::TM_ACC + D, op, m2, idA, n > 0 || ks > 0);
+                        mma_bf16_ts_warp(tbase + C::TM_ACC, op + 16, m1, idA, n > 0 || ks > 0);
+                    } else {
+                        mma_bf16_ts_warp(tbase + C::TM_ACC, op, m1, idA, n > 0 || ks > 0);
+                    }
+                }
+                mma_commit_warp(smem_u32(&bar->dp_free[sb.st]));
+                mma_commit_warp(smem_u32(&bar->y1_empty[s1.st]));
+                if (KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2.st]));
+                s1.next();
+                s2.next();
+                sb.next();
             }
             if (ok) mma_commit_warp(smem_u32(&bar->acc_full));
         }
-        // no MMA may be in flight when tensor memory is released
-        mma_commit_warp(smem_u32(&bar->drain));
-        if (lane == 0)
-            for (int i = 0; i < kSpinLimit && !mbar_try(smem_u32(&bar->drain), 0); i++) {
-            }
+        mma_commit_warp(smem_u32(&bar->drain[1]));
+        if (lane == 0) land(smem_u32(&bar->drain[1]), 0);
         __syncwarp();
-    } else if (warp < 8) {
+    } else if (warp < kWarps) {
         // ---------------------------------------- elementwise, epilogue
-        const int w = warp >> 2;  // half of the columns
+        const int w = warp >> 2;  // quarter of the columns
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int x = x0 + (warp & 3) * 32 + lane;  // stationary row
         const float sl2 = a.scale * kDenseLog2e;
@@ -312,22 +320,22 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             ndx2 = pack2(nd, nd);
             kend = x < a.R ? dense_kend(a, sp, x % a.nq) : 0;
         }
-        int n = 0;
+        uint32_t n = 0;
+        Stage<C::N2> s2;
+        Stage<C::NB> sb;
         for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a), n++) {
-            const int b = n % C::NB;
-            const uint32_t tP = tbase + C::TM_DP + b * 128 + w * 64 + lanes;
-            const float* st = stats + (n % C::N2) * 2 * BT + w * 64;  // KEYS: -l2 of this half's rows; -D follows BT later
-            mbar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a.status, a.spin);
+            const uint32_t tP = tbase + C::TM_DP + sb.st * 128 + w * kCols + lanes;
+            const float* st = stats + s2.st * 2 * BT + w * kCols;  // KEYS: -l2 of these columns' rows; -D BT further
+            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
             tc_fence_after();
-            uint32_t s[64];
-            tmem_ld32_nowait(tbase + lanes + w * 64, s);
-            tmem_ld32_nowait(tbase + lanes + w * 64 + 32, s + 32);
-            if constexpr (KEYS) mbar_wait(smem_u32(&bar->y2_full[n % C::N2]), (n / C::N2) & 1, abort_flag, a.status, a.spin);
+            uint32_t s[kCols];
+            tmem_ld32_nowait(tbase + lanes + w * kCols, s);
+            if constexpr (KEYS) bar_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
             tmem_wait_ld();
             tc_fence_before();
-            mbar_arrive(smem_u32(&bar->s_free));
+            warp_arrive(smem_u32(&bar->s_free), lane);
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kCols; c += 4) {
                 uint64_t l0 = nl2x2, l1 = nl2x2;
                 if constexpr (KEYS) {
                     const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + c);
@@ -348,9 +356,9 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
                 masked = a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT);
                 if (masked) {
-                    int t = (it.t0 + w * 64) % a.nq;
+                    int t = (it.t0 + w * kCols) % a.nq;
 #pragma unroll
-                    for (int c = 0; c < 64; c++) {
+                    for (int c = 0; c < kCols; c++) {
                         if (x > t + sp.lk - sp.lq) s[c] = 0u;
                         if (++t == a.nq) t = 0;
                     }
@@ -359,24 +367,24 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 masked = __any_sync(0xffffffffu, kend - it.pos < BT);
                 if (masked) {
 #pragma unroll
-                    for (int c = 0; c < 64; c++)
-                        if (w * 64 + c >= kend - it.pos) s[c] = 0u;
+                    for (int c = 0; c < kCols; c++)
+                        if (w * kCols + c >= kend - it.pos) s[c] = 0u;
                 }
             }
-            mbar_wait(smem_u32(&bar->dp_full[b]), (n / C::NB) & 1, abort_flag, a.status, a.spin);
+            bar_wait(smem_u32(&bar->dp_full[sb.st]), sb.parity, abort_flag, a);
             tc_fence_after();
-            uint32_t g[64];
+            uint32_t g[kCols];
             tmem_ld32_nowait(tP, g);
-            tmem_ld32_nowait(tP + 32, g + 32);
             tmem_wait_ld();
-            uint32_t o[32];
+            uint32_t o[kCols / 2];
             if constexpr (KEYS) {
 #pragma unroll
-                for (int c = 0; c < 64; c += 2) o[c >> 1] = pack_bf16x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                tmem_st32(tP, o);
+                for (int c = 0; c < kCols; c += 2)
+                    o[c >> 1] = pack_bf16x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                tmem_st16(tP, o);
             }
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
+            for (int c = 0; c < kCols; c += 4) {
                 uint64_t d0 = ndx2, d1 = ndx2;
                 if constexpr (KEYS) {
                     const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + BT + c);
@@ -389,7 +397,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 unpack2(mul2(add2(pack2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), d1),
                              pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]))), e2, e3);
                 if (!KEYS && masked) {  // dP of a key behind the lengths may be anything
-                    const int lim = kend - it.pos - w * 64;
+                    const int lim = kend - it.pos - w * kCols;
                     e0 = c < lim ? e0 : 0.f;
                     e1 = c + 1 < lim ? e1 : 0.f;
                     e2 = c + 2 < lim ? e2 : 0.f;
@@ -398,13 +406,15 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 o[c >> 1] = pack_bf16x2(e0, e1);
                 o[(c >> 1) + 1] = pack_bf16x2(e2, e3);
             }
-            tmem_st32(KEYS ? tP + 32 : tP, o);
+            tmem_st16(KEYS ? tP + kCols / 2 : tP, o);
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&bar->ds_ready[b]));
+            warp_arrive(smem_u32(&bar->ds_ready[sb.st]), lane);
+            s2.next();
+            sb.next();
         }
         if (any) {
-            mbar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a.status, a.spin);
+            bar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a);
             tc_fence_after();
         }
         // rows without a gradient hold whatever their padding made: zero
@@ -414,19 +424,16 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         for (int k = 0; k < (KEYS ? 2 : 1); k++) {
             const float f = k == 0 ? a.scale : 1.f;
 #pragma unroll
-            for (int c = w * (D / 2); c < (w + 1) * (D / 2); c += 32) {
-                uint32_t o[32];
-                if (any) {
-                    tmem_ld32_nowait(tbase + C::TM_ACC + k * D + c + lanes, o);
-                    tmem_wait_ld();
-                }
+            for (int c = w * 16; c < D; c += 64) {
+                float o[16];
+                if (any) tmem_ld16(tbase + C::TM_ACC + k * D + c + lanes, o);
                 if (x < extent) {
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {
+                    for (int i = 0; i < 16; i += 8) {
                         if (c + i >= a.d) break;
                         float v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; e++) v[e] = live ? __uint_as_float(o[i + e]) * f : 0.f;
+                        for (int e = 0; e < 8; e++) v[e] = live ? o[i + e] * f : 0.f;
                         if (a.splits > 1) {
                             float* dst = a.part + ((k * a.splits + part) * all + row) * a.d + c + i;
                             store4(dst, v);
@@ -447,7 +454,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kWarps) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }

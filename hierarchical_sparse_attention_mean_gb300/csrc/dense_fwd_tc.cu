@@ -10,18 +10,20 @@
 // precision; it saves reading O back for almost every tile.
 //
 // A block takes 256 query rows as two tiles of 128 against a shared stream of
-// key and value tiles. While the softmax of one tile runs, the tensor cores
-// work for the other: per tile, in one in-order stream, O += P V, then the next
-// S. S and P share tensor memory (a thread holds its whole row of S in
-// registers before it writes P); 2 x 128 columns S / P and 2 x D columns O.
+// key and value tiles; an item is one row tile's turn at one key tile, and the
+// two alternate. S and P share a tensor-memory buffer of 128 columns (a thread
+// holds its whole row of S in registers before it writes P). At 64 columns of d
+// there is room for three buffers: the next S of a row tile is then ready when its
+// softmax is, and the tensor cores and the exponentials (8 a clock and scheduler
+// on this part, 1,024 clocks for two tiles, as long as their products) both stay
+// busy. At 128 columns the two outputs leave room for two.
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue (a thread per row of their
-// tile), warp 8 issues the MMAs, warp 9 the copies; warps 10 and 11 only fill
-// the warpgroup whose registers the softmax takes over.
+// tile), warp 8 issues S = Q K^T, warp 9 O += P V, warps 10 and 11 the copies of
+// K and V.
 #include <algorithm>
 
-#include "dense.h"
-#include "tc.cuh"
+#include "dense_tc.cuh"
 
 namespace llsa {
 namespace {
@@ -37,21 +39,18 @@ template <int D>
 struct Cfg {
     static constexpr int TILE = 128 * D * 2;  // bytes of 128 rows
     static constexpr int REGION = 128 * 128;  // bytes of 128 rows x 64 columns
-    static constexpr int STAGES = D == 64 ? 8 : 4;
-    static constexpr int SMEM = 1024 + (2 + STAGES) * TILE + 1024;
-    static constexpr int TM_O = 256;          // tensor-memory columns: S / P at 0 and 128, O behind them
+    static constexpr int STAGES = D == 64 ? 4 : 2;  // of K, and of V
+    static constexpr int NS = D == 64 ? 3 : 2;      // S / P buffers
+    static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE + 512;
+    static constexpr int TM_O = NS * 128;     // tensor-memory columns: S / P first, O behind them
 };
 
 struct Bars {
-    uint64_t full[8], empty[8], q_full[2], s_full[2], p_full[2], o_full[2], drain;
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2];
+    uint64_t s_full[3], p_full[3], s_free[3], drain[2];
     uint32_t tmem_slot;
     int abort_flag;
 };
-
-// A whole warp waits; false as soon as any wait of the block gave up.
-__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, const DenseArgs& a) {
-    return __all_sync(0xffffffffu, mbar_wait(mbar, parity, abort_flag, a.status, a.spin));
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
@@ -63,8 +62,9 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     unsigned char* sQ = sm;
-    unsigned char* ring = sm + 2 * C::TILE;
-    Bars* bar = reinterpret_cast<Bars*>(ring + C::STAGES * C::TILE);
+    unsigned char* sK = sm + 2 * C::TILE;
+    unsigned char* sV = sK + C::STAGES * C::TILE;
+    Bars* bar = reinterpret_cast<Bars*>(sV + C::STAGES * C::TILE);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -86,17 +86,21 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     const int nt = max(n[0], n[1]);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < C::STAGES; s++) {
-            mbar_init(smem_u32(&bar->full[s]), 1);
-            mbar_init(smem_u32(&bar->empty[s]), 1);
+        for (int i = 0; i < 4; i++) {
+            mbar_init(smem_u32(&bar->k_full[i]), 1);
+            mbar_init(smem_u32(&bar->k_empty[i]), 1);
+            mbar_init(smem_u32(&bar->v_full[i]), 1);
+            mbar_init(smem_u32(&bar->v_empty[i]), 1);
+        }
+        for (int i = 0; i < 3; i++) {
+            mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->p_full[i]), 4);
+            mbar_init(smem_u32(&bar->s_free[i]), 1);
         }
         for (int w = 0; w < 2; w++) {
             mbar_init(smem_u32(&bar->q_full[w]), 1);
-            mbar_init(smem_u32(&bar->s_full[w]), 1);
-            mbar_init(smem_u32(&bar->p_full[w]), 128);
-            mbar_init(smem_u32(&bar->o_full[w]), 1);
+            mbar_init(smem_u32(&bar->drain[w]), 1);
         }
-        mbar_init(smem_u32(&bar->drain), 1);
         bar->abort_flag = 0;
         fence_mbar_init();
     }
@@ -106,128 +110,123 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     tc_fence_after();
     const uint32_t tbase = bar->tmem_slot;
 
+    // Items in order: for each key tile, row tile 0 then 1, each as long as it has
+    // key tiles left. Item i uses buffer i % NS.
     if (warp >= 8) {
         regs_dec<kRegsOther>();
-        if (warp == 9) {
-            // ----------------------------------------------------------- copies
-            // tile sequence K(0), V(0), K(1), V(1), ... through one ring
-            if (lane == 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
-                for (int w = 0; w < 2; w++)
-                    if (n[w] > 0) {
-                        mbar_arrive_expect_tx(smem_u32(&bar->q_full[w]), C::TILE);
-                        for (int c = 0; c < D / 64; c++)
-                            tma_load_3d(smem_u32(sQ + w * C::TILE + c * C::REGION), &mq, c * 64, r0 + w * BM, slice,
-                                        smem_u32(&bar->q_full[w]));
-                    }
-                int s = 0;
-                for (; s < 2 * nt; s++) {
-                    const int st = s % C::STAGES, use = s / C::STAGES;
-                    if (use > 0 && !mbar_wait(smem_u32(&bar->empty[st]), (use - 1) & 1, abort_flag, a.status, a.spin)) break;
-                    const uint32_t fb = smem_u32(&bar->full[st]);
+        if (warp >= 10) {
+            // ------------------------------------------------------- copies
+            if (lane == 0 && nt > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+                const bool keys = warp == 10;
+                if (keys)
+                    for (int w = 0; w < 2; w++)
+                        if (n[w] > 0) {
+                            mbar_arrive_expect_tx(smem_u32(&bar->q_full[w]), C::TILE);
+                            for (int c = 0; c < D / 64; c++)
+                                tma_load_3d(smem_u32(sQ + w * C::TILE + c * C::REGION), &mq, c * 64, r0 + w * BM, slice,
+                                            smem_u32(&bar->q_full[w]));
+                        }
+                unsigned char* ring = keys ? sK : sV;
+                uint64_t* full = keys ? bar->k_full : bar->v_full;
+                uint64_t* empty = keys ? bar->k_empty : bar->v_empty;
+                const CUtensorMap* map = keys ? &mk : &mv;
+                Stage<C::STAGES> s;
+                int t = 0;
+                for (; t < nt; t++, s.next()) {
+                    if (t >= C::STAGES && !bar_wait(smem_u32(&empty[s.st]), s.parity ^ 1, abort_flag, a)) break;
+                    const uint32_t fb = smem_u32(&full[s.st]);
                     mbar_arrive_expect_tx(fb, C::TILE);
                     for (int c = 0; c < D / 64; c++)
-                        tma_load_3d(smem_u32(ring + st * C::TILE + c * C::REGION), (s & 1) ? &mv : &mk, c * 64,
-                                    j_first + (s >> 1) * BN, slice, fb);
+                        tma_load_3d(smem_u32(ring + s.st * C::TILE + c * C::REGION), map, c * 64, j_first + t * BN, slice, fb);
                 }
-                // copies still in flight must land before the block exits
-                for (int w = 0; w < 2; w++)
-                    if (n[w] > 0)
-                        for (int it = 0; it < kSpinLimit && !mbar_try(smem_u32(&bar->q_full[w]), 0); it++) {
-                        }
-                for (int x = max(0, s - C::STAGES); x < s; x++)
-                    for (int it = 0; it < kSpinLimit && !mbar_try(smem_u32(&bar->full[x % C::STAGES]), (x / C::STAGES) & 1);
-                         it++) {
-                    }
+                if (keys)
+                    for (int w = 0; w < 2; w++)
+                        if (n[w] > 0) land(smem_u32(&bar->q_full[w]), 0);
+                for (int x = max(0, t - C::STAGES); x < t; x++)
+                    land(smem_u32(&full[x % C::STAGES]), (x / C::STAGES) & 1);
             }
         } else if (warp == 8) {
-            // ------------------------------------------------------- MMA issuer
-            constexpr uint32_t idS = idesc_bf16(BM, BN, 0, 0), idO = idesc_bf16(BM, D, 0, 1);
-            const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024);
-            const uint64_t dK = desc_sw128(smem_u32(ring), 16, 1024);
-            const uint64_t dV = desc_sw128(smem_u32(ring), C::REGION, 1024);
-            auto ring_wait = [&](int s) {
-                return warp_wait(smem_u32(&bar->full[s % C::STAGES]), (s / C::STAGES) & 1, abort_flag, a);
-            };
-            auto issue_S = [&](int w, int t) {
-                const uint32_t k0 = (uint32_t)((2 * t) % C::STAGES * C::TILE);
-    #pragma unroll
-                for (int ks = 0; ks < D / 16; ks++) {
-                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                    mma_bf16_warp(tbase + w * 128, dQ + ((w * C::TILE + off) >> 4), dK + ((k0 + off) >> 4), idS, ks > 0);
-                }
-                mma_commit_warp(smem_u32(&bar->s_full[w]));
-            };
-            auto issue_O = [&](int w, int t) {
-                const uint32_t v0 = (uint32_t)((2 * t + 1) % C::STAGES * C::TILE);
-    #pragma unroll
-                for (int ks = 0; ks < BN / 16; ks++)
-                    mma_bf16_ts_warp(tbase + C::TM_O + w * D, tbase + w * 128 + 8 * ks, dV + ((v0 + ks * 2048) >> 4), idO,
-                                     t > 0 || ks > 0);
-            };
+            // ----------------------------------------------------- S issuer
+            constexpr uint32_t idS = idesc_bf16(BM, BN, 0, 0);
+            const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024), dK = desc_sw128(smem_u32(sK), 16, 1024);
             bool ok = true;
-            if (nt > 0) {
-                for (int w = 0; w < 2 && ok; w++)
-                    if (n[w] > 0) ok = warp_wait(smem_u32(&bar->q_full[w]), 0, abort_flag, a);
-                ok = ok && ring_wait(0);
-                if (ok) {
+            for (int w = 0; w < 2 && ok; w++)
+                if (n[w] > 0) ok = warp_wait(smem_u32(&bar->q_full[w]), 0, abort_flag, a);
+            Stage<C::STAGES> s;
+            Stage<C::NS> b;
+            int i = 0;
+            for (int t = 0; t < nt && ok; t++, s.next()) {
+                ok = warp_wait(smem_u32(&bar->k_full[s.st]), s.parity, abort_flag, a);
+                const uint32_t k0 = (uint32_t)(s.st * C::TILE);
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    if (t >= n[w] || !ok) continue;
+                    if (i >= C::NS) ok = warp_wait(smem_u32(&bar->s_free[b.st]), b.parity ^ 1, abort_flag, a);
+                    if (!ok) continue;
                     tc_fence_after();
-                    for (int w = 0; w < 2; w++)
-                        if (n[w] > 0) issue_S(w, 0);
-                    mma_commit_warp(smem_u32(&bar->empty[0]));
-                }
-            }
-            for (int t = 0; t < nt && ok; t++) {
-                bool have_v = false, have_k = false;
-                for (int w = 0; w < 2 && ok; w++) {
-                    if (t >= n[w]) continue;
-                    ok = warp_wait(smem_u32(&bar->p_full[w]), t & 1, abort_flag, a);
-                    if (!ok) break;
-                    if (!have_v) {
-                        ok = ring_wait(2 * t + 1);
-                        if (!ok) break;
-                        // values behind the last valid key may be anything: their weights are 0, so they must be finite
-                        const int live = sp.lk - (j_first + t * BN);
-                        if (live < BN) {
-                            unsigned char* v0 = ring + (2 * t + 1) % C::STAGES * C::TILE;
-                            for (int c = 0; c < D / 64; c++)
-                                for (int x = live * 8 + lane; x < BN * 8; x += 32)
-                                    *reinterpret_cast<uint4*>(v0 + c * C::REGION + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_async_smem();
-                            __syncwarp();
-                        }
-                        have_v = true;
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ks++) {
+                        const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                        mma_bf16_warp(tbase + b.st * 128, dQ + ((w * C::TILE + off) >> 4), dK + ((k0 + off) >> 4), idS, ks > 0);
                     }
-                    tc_fence_after();
-                    issue_O(w, t);
-                    if (t + 1 == n[w]) {
-                        mma_commit_warp(smem_u32(&bar->o_full[w]));
-                    } else {
-                        if (!have_k) {
-                            ok = ring_wait(2 * t + 2);
-                            if (!ok) break;
-                            tc_fence_after();
-                            have_k = true;
-                        }
-                        issue_S(w, t + 1);
-                    }
+                    mma_commit_warp(smem_u32(&bar->s_full[b.st]));
+                    i++;
+                    b.next();
                 }
-                if (!ok) break;
-                mma_commit_warp(smem_u32(&bar->empty[(2 * t + 1) % C::STAGES]));
-                if (t + 1 < nt) mma_commit_warp(smem_u32(&bar->empty[(2 * t + 2) % C::STAGES]));
+                if (ok) mma_commit_warp(smem_u32(&bar->k_empty[s.st]));
             }
             // no MMA may be in flight when tensor memory is released
-            mma_commit_warp(smem_u32(&bar->drain));
-            if (lane == 0)
-                for (int it = 0; it < kSpinLimit && !mbar_try(smem_u32(&bar->drain), 0); it++) {
-                }
+            mma_commit_warp(smem_u32(&bar->drain[0]));
+            if (lane == 0) land(smem_u32(&bar->drain[0]), 0);
             __syncwarp();
-    }
+        } else {
+            // ----------------------------------------------------- O issuer
+            constexpr uint32_t idO = idesc_bf16(BM, D, 0, 1);
+            const uint64_t dV = desc_sw128(smem_u32(sV), C::REGION, 1024);
+            bool ok = true;
+            Stage<C::STAGES> s;
+            Stage<C::NS> b;
+            for (int t = 0; t < nt && ok; t++, s.next()) {
+                ok = warp_wait(smem_u32(&bar->v_full[s.st]), s.parity, abort_flag, a);
+                if (!ok) break;
+                // values behind the last valid key may be anything: their weights are 0, so they must be finite
+                const int live = sp.lk - (j_first + t * BN);
+                if (live < BN) {
+                    unsigned char* v0 = sV + s.st * C::TILE;
+                    for (int c = 0; c < D / 64; c++)
+                        for (int x = live * 8 + lane; x < BN * 8; x += 32)
+                            *reinterpret_cast<uint4*>(v0 + c * C::REGION + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                const uint32_t v0 = (uint32_t)(s.st * C::TILE);
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    if (t >= n[w] || !ok) continue;
+                    ok = warp_wait(smem_u32(&bar->p_full[b.st]), b.parity, abort_flag, a);
+                    if (!ok) continue;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < BN / 16; ks++)
+                        mma_bf16_ts_warp(tbase + C::TM_O + w * D, tbase + b.st * 128 + 8 * ks, dV + ((v0 + ks * 2048) >> 4), idO,
+                                         t > 0 || ks > 0);
+                    mma_commit_warp(smem_u32(&bar->s_free[b.st]));
+                    b.next();
+                }
+                if (ok) mma_commit_warp(smem_u32(&bar->v_empty[s.st]));
+            }
+            mma_commit_warp(smem_u32(&bar->drain[1]));
+            if (lane == 0) land(smem_u32(&bar->drain[1]), 0);
+            __syncwarp();
+        }
     } else {
         // ----------------------------------------------- softmax, epilogue
         regs_inc<kRegsSoftmax>();
         const int w = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t tS = tbase + w * 128 + lanes, tO = tbase + C::TM_O + w * D + lanes;
+        const uint32_t tO = tbase + C::TM_O + w * D + lanes;
+        const int n_other = n[1 - w];
+        auto item = [&](int t) { return t + min(t + w, n_other); };  // number of this row tile's turn t
         const int r = r0 + w * BM + (warp & 3) * 32 + lane;
         const int kend = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
         const float sl2 = a.scale * kDenseLog2e;
@@ -235,7 +234,10 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         float m = -INFINITY;
         uint64_t l4[2] = {0ull, 0ull};  // the row's sum in four parts
         for (int t = 0; t < n[w]; t++) {
-            mbar_wait(smem_u32(&bar->s_full[w]), t & 1, abort_flag, a.status, a.spin);
+            const int i = item(t);
+            const int b = i % C::NS;
+            const uint32_t tS = tbase + b * 128 + lanes;
+            bar_wait(smem_u32(&bar->s_full[b]), (i / C::NS) & 1, abort_flag, a);
             tc_fence_after();
             uint32_t s[128];
 #pragma unroll
@@ -261,7 +263,10 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 l4[0] = mul2(l4[0], f2);
                 l4[1] = mul2(l4[1], f2);
                 if (t > 0) {
-                    // S(t) is there, and with it everything issued before it: O is at rest
+                    // O is at rest once this row tile's last item gave its buffer back
+                    const int prev = item(t - 1);
+                    bar_wait(smem_u32(&bar->s_free[prev % C::NS]), (prev / C::NS) & 1, abort_flag, a);
+                    tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
                         uint32_t o[32];
@@ -291,14 +296,15 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&bar->p_full[w]));
+            warp_arrive(smem_u32(&bar->p_full[b]), lane);
         }
         float l0, l1, l2, l3;
         unpack2(l4[0], l0, l1);
         unpack2(l4[1], l2, l3);
         const float l = (l0 + l1) + (l2 + l3);
         if (n[w] > 0) {
-            mbar_wait(smem_u32(&bar->o_full[w]), 0, abort_flag, a.status, a.spin);
+            const int last = item(n[w] - 1);
+            bar_wait(smem_u32(&bar->s_free[last % C::NS]), (last / C::NS) & 1, abort_flag, a);
             tc_fence_after();
         }
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
@@ -350,7 +356,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 template <int D>
 int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
     using C = Cfg<D>;
-    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
+    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
     CUtensorMap mq, mk, mv;
     LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BM));
     LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BN));

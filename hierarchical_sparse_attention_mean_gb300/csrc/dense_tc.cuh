@@ -1,0 +1,48 @@
+// dense_tc.cuh -- waits and arrivals of the dense tensor-core kernels.
+#pragma once
+
+#include "dense.h"
+#include "tc.cuh"
+
+namespace llsa {
+namespace tc {
+
+// A bounded wait that first looks: a phase that has completed costs one test
+// (about 24 clocks) instead of a try_wait.
+__device__ __forceinline__ bool bar_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, const DenseArgs& a) {
+    if (mbar_test(mbar, parity)) return true;
+    return mbar_wait(mbar, parity, abort_flag, a.status, a.spin);
+}
+
+// A whole warp waits; false as soon as any wait of the block gave up.
+__device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volatile int* abort_flag, const DenseArgs& a) {
+    return __all_sync(0xffffffffu, bar_wait(mbar, parity, abort_flag, a));
+}
+
+// One arrival for the whole warp, after what all its lanes did.
+__device__ __forceinline__ void warp_arrive(uint32_t mbar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(mbar);
+}
+
+// Copies in flight must land before a block exits.
+__device__ __forceinline__ void land(uint32_t mbar, uint32_t parity) {
+    for (int i = 0; i < kSpinLimit && !mbar_try(mbar, parity); i++) {
+    }
+}
+
+// A stage of a ring and the parity of its current use.
+template <int N>
+struct Stage {
+    int st = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++st == N) {
+            st = 0;
+            parity ^= 1;
+        }
+    }
+};
+
+}  // namespace tc
+}  // namespace llsa
