@@ -98,6 +98,7 @@ template <int D, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
                     const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2,
+                    const __grid_constant__ CUtensorMap mz1, const __grid_constant__ CUtensorMap mz2,
                     const __grid_constant__ DenseArgs a) {
     using C = Cfg<D, KEYS>;
     extern __shared__ __align__(1024) unsigned char sm[];
@@ -417,9 +418,11 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             bar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a);
             tc_fence_after();
         }
-        // rows without a gradient hold whatever their padding made: zero
+        // rows without a gradient hold whatever their padding made: zero. The
+        // stationary tiles have been used up: their places take the results
         const bool live = any && (KEYS ? x < sp.lk : kend > 0);
         const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
+        const int lr = (warp & 3) * 32 + lane;
 #pragma unroll
         for (int k = 0; k < (KEYS ? 2 : 1); k++) {
             const float f = k == 0 ? a.scale : 1.f;
@@ -427,28 +430,30 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             for (int c = w * 16; c < D; c += 64) {
                 float o[16];
                 if (any) tmem_ld16(tbase + C::TM_ACC + k * D + c + lanes, o);
-                if (x < extent) {
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) {
-                        if (c + i >= a.d) break;
-                        float v[8];
+                for (int i = 0; i < 16; i++) o[i] = live ? o[i] * f : 0.f;
+                if (a.splits == 1) {
+                    unsigned char* region = sX + k * C::TILE + (c / 64) * C::REGION;
+                    put_chunk(region, lr, w * 2, o);
+                    put_chunk(region, lr, w * 2 + 1, o + 8);
+                } else if (x < extent) {
+                    float* dst = a.part + ((k * a.splits + part) * all + row) * a.d + c;
 #pragma unroll
-                        for (int e = 0; e < 8; e++) v[e] = live ? o[i + e] * f : 0.f;
-                        if (a.splits > 1) {
-                            float* dst = a.part + ((k * a.splits + part) * all + row) * a.d + c + i;
-                            store4(dst, v);
-                            store4(dst + 4, v + 4);
-                        } else {
-                            uint4 u;
-                            u.x = pack_bf16x2(v[0], v[1]);
-                            u.y = pack_bf16x2(v[2], v[3]);
-                            u.z = pack_bf16x2(v[4], v[5]);
-                            u.w = pack_bf16x2(v[6], v[7]);
-                            void* base = KEYS ? (k == 0 ? a.dk : a.dv) : a.dq;
-                            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + row * a.d + c + i) = u;
-                        }
-                    }
+                    for (int i = 0; i < 16; i += 4)
+                        if (c + i < a.d) store4(dst + i, o + i);
                 }
+            }
+        }
+        if (a.splits == 1) {
+            fence_async_smem();
+            named_barrier(1 + (warp & 3), 128);  // the four warps of these 32 rows
+            if (w == 0 && lane == 0 && x < extent) {
+                for (int k = 0; k < (KEYS ? 2 : 1); k++)
+                    for (int c = 0; c < D / 64; c++)
+                        tma_store_3d(k == 0 ? &mz1 : &mz2, smem_u32(sX + k * C::TILE + c * C::REGION + lr * 128), c * 64, x,
+                                     slice);
+                bulk_commit();
+                bulk_wait_read();
             }
         }
     }
@@ -464,11 +469,13 @@ template <int D, bool KEYS>
 int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
     using C = Cfg<D, KEYS>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
-    CUtensorMap mq, mk, mv, mg;
+    CUtensorMap mq, mk, mv, mg, z1, z2;
     LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mg, a.dout, s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mv, a.v, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&z1, KEYS ? a.dk : a.dq, s.slices, KEYS ? s.nk : s.R, s.d, 32));
+    LLSA_TRY(make_tmap_rows(&z2, KEYS ? a.dv : a.dq, s.slices, KEYS ? s.nk : s.R, s.d, 32));
     cudaFuncSetAttribute(dense_bwd_tc_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const int extent = KEYS ? s.nk : s.R;
     const long long blocks = (long long)((extent + BT - 1) / BT) * s.slices;
@@ -476,10 +483,10 @@ int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
     const dim3 grid((unsigned)blocks, a.splits);
     if constexpr (KEYS)
         LLSA_LAUNCH("dense_dkv_tc", st,
-                    dense_bwd_tc_kernel<D, true><<<grid, kThreads, C::SMEM, st>>>(mk, mv, mq, mg, a));
+                    dense_bwd_tc_kernel<D, true><<<grid, kThreads, C::SMEM, st>>>(mk, mv, mq, mg, z1, z2, a));
     else
         LLSA_LAUNCH("dense_dq_tc", st,
-                    dense_bwd_tc_kernel<D, false><<<grid, kThreads, C::SMEM, st>>>(mq, mg, mk, mv, a));
+                    dense_bwd_tc_kernel<D, false><<<grid, kThreads, C::SMEM, st>>>(mq, mg, mk, mv, z1, z2, a));
     return LLSA_OK;
 }
 

@@ -10,13 +10,12 @@
 // precision; it saves reading O back for almost every tile.
 //
 // A block takes 256 query rows as two tiles of 128 against a shared stream of
-// key and value tiles; an item is one row tile's turn at one key tile, and the
-// two alternate. S and P share a tensor-memory buffer of 128 columns (a thread
-// holds its whole row of S in registers before it writes P). At 64 columns of d
-// there is room for three buffers: the next S of a row tile is then ready when its
-// softmax is, and the tensor cores and the exponentials (8 a clock and scheduler
-// on this part, 1,024 clocks for two tiles, as long as their products) both stay
-// busy. At 128 columns the two outputs leave room for two.
+// key and value tiles, the two taking turns on the tensor cores. A thread holds
+// its whole row of S in registers, so S may be overwritten as soon as it is read.
+// At 64 columns of d tensor memory has room for P beside S (2 x (128 + 64) columns
+// and 2 x 64 of O): the next S of a row tile is made while its softmax runs, and
+// neither waits for the other. At 128 columns P lies over S, and goes to the
+// tensor cores in two halves, so that P V begins while the second half is made.
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue (a thread per row of their
 // tile), warp 8 issues S = Q K^T, warp 9 O += P V, warps 10 and 11 the copies of
@@ -40,14 +39,16 @@ struct Cfg {
     static constexpr int TILE = 128 * D * 2;  // bytes of 128 rows
     static constexpr int REGION = 128 * 128;  // bytes of 128 rows x 64 columns
     static constexpr int STAGES = D == 64 ? 4 : 2;  // of K, and of V
-    static constexpr int NS = D == 64 ? 3 : 2;      // S / P buffers
+    static constexpr bool APART = D == 64;          // P beside S
+    static constexpr int HALVES = APART ? 1 : 2;    // parts in which P is handed over
     static constexpr int SMEM = 1024 + (2 + 2 * STAGES) * TILE + 512;
-    static constexpr int TM_O = NS * 128;     // tensor-memory columns: S / P first, O behind them
+    // tensor-memory columns: S of row tile w at 128 w
+    static constexpr int TM_P = APART ? 256 : 0, P_STEP = APART ? 64 : 128, TM_O = APART ? 384 : 256;
 };
 
 struct Bars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2];
-    uint64_t s_full[3], p_full[3], s_free[3], drain[2];
+    uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], drain[2];
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -57,7 +58,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ DenseArgs a) {
+                    const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo,
+                    const __grid_constant__ DenseArgs a) {
     using C = Cfg<D>;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -92,13 +94,13 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             mbar_init(smem_u32(&bar->v_full[i]), 1);
             mbar_init(smem_u32(&bar->v_empty[i]), 1);
         }
-        for (int i = 0; i < 3; i++) {
-            mbar_init(smem_u32(&bar->s_full[i]), 1);
-            mbar_init(smem_u32(&bar->p_full[i]), 4);
-            mbar_init(smem_u32(&bar->s_free[i]), 1);
-        }
         for (int w = 0; w < 2; w++) {
             mbar_init(smem_u32(&bar->q_full[w]), 1);
+            mbar_init(smem_u32(&bar->s_full[w]), 1);
+            mbar_init(smem_u32(&bar->s_free[w]), 4);
+            mbar_init(smem_u32(&bar->p_full[w][0]), 4);
+            mbar_init(smem_u32(&bar->p_full[w][1]), 4);
+            mbar_init(smem_u32(&bar->o_done[w]), 1);
             mbar_init(smem_u32(&bar->drain[w]), 1);
         }
         bar->abort_flag = 0;
@@ -110,8 +112,6 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     tc_fence_after();
     const uint32_t tbase = bar->tmem_slot;
 
-    // Items in order: for each key tile, row tile 0 then 1, each as long as it has
-    // key tiles left. Item i uses buffer i % NS.
     if (warp >= 8) {
         regs_dec<kRegsOther>();
         if (warp >= 10) {
@@ -153,25 +153,22 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             for (int w = 0; w < 2 && ok; w++)
                 if (n[w] > 0) ok = warp_wait(smem_u32(&bar->q_full[w]), 0, abort_flag, a);
             Stage<C::STAGES> s;
-            Stage<C::NS> b;
-            int i = 0;
             for (int t = 0; t < nt && ok; t++, s.next()) {
                 ok = warp_wait(smem_u32(&bar->k_full[s.st]), s.parity, abort_flag, a);
                 const uint32_t k0 = (uint32_t)(s.st * C::TILE);
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
                     if (t >= n[w] || !ok) continue;
-                    if (i >= C::NS) ok = warp_wait(smem_u32(&bar->s_free[b.st]), b.parity ^ 1, abort_flag, a);
+                    // S is read, or P that lies over it is used up
+                    if (t > 0) ok = warp_wait(smem_u32(C::APART ? &bar->s_free[w] : &bar->o_done[w]), (t - 1) & 1, abort_flag, a);
                     if (!ok) continue;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ks++) {
                         const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                        mma_bf16_warp(tbase + b.st * 128, dQ + ((w * C::TILE + off) >> 4), dK + ((k0 + off) >> 4), idS, ks > 0);
+                        mma_bf16_warp(tbase + w * 128, dQ + ((w * C::TILE + off) >> 4), dK + ((k0 + off) >> 4), idS, ks > 0);
                     }
-                    mma_commit_warp(smem_u32(&bar->s_full[b.st]));
-                    i++;
-                    b.next();
+                    mma_commit_warp(smem_u32(&bar->s_full[w]));
                 }
                 if (ok) mma_commit_warp(smem_u32(&bar->k_empty[s.st]));
             }
@@ -185,7 +182,6 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             const uint64_t dV = desc_sw128(smem_u32(sV), C::REGION, 1024);
             bool ok = true;
             Stage<C::STAGES> s;
-            Stage<C::NS> b;
             for (int t = 0; t < nt && ok; t++, s.next()) {
                 ok = warp_wait(smem_u32(&bar->v_full[s.st]), s.parity, abort_flag, a);
                 if (!ok) break;
@@ -203,15 +199,17 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 #pragma unroll
                 for (int w = 0; w < 2; w++) {
                     if (t >= n[w] || !ok) continue;
-                    ok = warp_wait(smem_u32(&bar->p_full[b.st]), b.parity, abort_flag, a);
-                    if (!ok) continue;
-                    tc_fence_after();
 #pragma unroll
-                    for (int ks = 0; ks < BN / 16; ks++)
-                        mma_bf16_ts_warp(tbase + C::TM_O + w * D, tbase + b.st * 128 + 8 * ks, dV + ((v0 + ks * 2048) >> 4), idO,
-                                         t > 0 || ks > 0);
-                    mma_commit_warp(smem_u32(&bar->s_free[b.st]));
-                    b.next();
+                    for (int h = 0; h < C::HALVES; h++) {
+                        ok = ok && warp_wait(smem_u32(&bar->p_full[w][h]), t & 1, abort_flag, a);
+                        if (!ok) continue;
+                        tc_fence_after();
+#pragma unroll
+                        for (int ks = h * 8 / C::HALVES; ks < (h + 1) * 8 / C::HALVES; ks++)
+                            mma_bf16_ts_warp(tbase + C::TM_O + w * D, tbase + C::TM_P + w * C::P_STEP + 8 * ks,
+                                             dV + ((v0 + ks * 2048) >> 4), idO, t > 0 || ks > 0);
+                    }
+                    if (ok) mma_commit_warp(smem_u32(&bar->o_done[w]));
                 }
                 if (ok) mma_commit_warp(smem_u32(&bar->v_empty[s.st]));
             }
@@ -224,9 +222,8 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         regs_inc<kRegsSoftmax>();
         const int w = warp >> 2;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tbase + w * 128 + lanes, tP = tbase + C::TM_P + w * C::P_STEP + lanes;
         const uint32_t tO = tbase + C::TM_O + w * D + lanes;
-        const int n_other = n[1 - w];
-        auto item = [&](int t) { return t + min(t + w, n_other); };  // number of this row tile's turn t
         const int r = r0 + w * BM + (warp & 3) * 32 + lane;
         const int kend = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
         const float sl2 = a.scale * kDenseLog2e;
@@ -234,15 +231,16 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         float m = -INFINITY;
         uint64_t l4[2] = {0ull, 0ull};  // the row's sum in four parts
         for (int t = 0; t < n[w]; t++) {
-            const int i = item(t);
-            const int b = i % C::NS;
-            const uint32_t tS = tbase + b * 128 + lanes;
-            bar_wait(smem_u32(&bar->s_full[b]), (i / C::NS) & 1, abort_flag, a);
+            bar_wait(smem_u32(&bar->s_full[w]), t & 1, abort_flag, a);
             tc_fence_after();
             uint32_t s[128];
 #pragma unroll
             for (int c = 0; c < 4; c++) tmem_ld32_nowait(tS + 32 * c, s + 32 * c);
             tmem_wait_ld();
+            if (C::APART) {
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->s_free[w]), lane);
+            }
             const int lim = kend - (j_first + t * BN);
             if (__any_sync(0xffffffffu, lim < BN)) {
 #pragma unroll
@@ -263,9 +261,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 l4[0] = mul2(l4[0], f2);
                 l4[1] = mul2(l4[1], f2);
                 if (t > 0) {
-                    // O is at rest once this row tile's last item gave its buffer back
-                    const int prev = item(t - 1);
-                    bar_wait(smem_u32(&bar->s_free[prev % C::NS]), (prev / C::NS) & 1, abort_flag, a);
+                    bar_wait(smem_u32(&bar->o_done[w]), (t - 1) & 1, abort_flag, a);  // O is at rest
                     tc_fence_after();
 #pragma unroll
                     for (int c = 0; c < D; c += 32) {
@@ -280,35 +276,40 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             }
             const float shift = m == -INFINITY ? 0.f : -m;
             const uint64_t shift2 = pack2(shift, shift);
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-                uint32_t p[16];
-#pragma unroll
-                for (int i = 0; i < 32; i += 2) {
-                    float e0, e1;
-                    unpack2(fma2(pack2(__uint_as_float(s[c + i]), __uint_as_float(s[c + i + 1])), sl2x2, shift2), e0, e1);
-                    e0 = ex2(e0);
-                    e1 = ex2(e1);
-                    l4[(i >> 1) & 1] = add2(l4[(i >> 1) & 1], pack2(e0, e1));
-                    p[i >> 1] = pack_bf16x2(e0, e1);
-                }
-                tmem_st16(tS + (c >> 1), p);
+            if (C::APART && t > 0) {  // the last P is used up
+                bar_wait(smem_u32(&bar->o_done[w]), (t - 1) & 1, abort_flag, a);
+                tc_fence_after();
             }
-            tmem_wait_st();
-            tc_fence_before();
-            warp_arrive(smem_u32(&bar->p_full[b]), lane);
+            uint32_t p[64];
+#pragma unroll
+            for (int c = 0; c < 64; c++) {
+                float e0, e1;
+                unpack2(fma2(pack2(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1])), sl2x2, shift2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                l4[c & 1] = add2(l4[c & 1], pack2(e0, e1));
+                p[c] = pack_bf16x2(e0, e1);
+                if (c % 16 == 15) tmem_st16(tP + c - 15, p + c - 15);
+                if ((c + 1) % (64 / C::HALVES) == 0) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    warp_arrive(smem_u32(&bar->p_full[w][c / (64 / C::HALVES)]), lane);
+                }
+            }
         }
         float l0, l1, l2, l3;
         unpack2(l4[0], l0, l1);
         unpack2(l4[1], l2, l3);
         const float l = (l0 + l1) + (l2 + l3);
         if (n[w] > 0) {
-            const int last = item(n[w] - 1);
-            bar_wait(smem_u32(&bar->s_free[last % C::NS]), (last / C::NS) & 1, abort_flag, a);
+            bar_wait(smem_u32(&bar->o_done[w]), (n[w] - 1) & 1, abort_flag, a);
             tc_fence_after();
         }
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
         const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
+        // the query tile has been used up: its place takes the output rows, 32 of them per warp
+        unsigned char* out = sQ + w * C::TILE;
+        const int lr = (warp & 3) * 32 + lane;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
@@ -316,26 +317,27 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 tmem_ld32_nowait(tO + c, o);
                 tmem_wait_ld();
             }
-            if (r < a.R) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
-                    if (c + i >= a.d) break;
-                    float f[8];
+            for (int i = 0; i < 32; i += 8) {
+                float f[8];
 #pragma unroll
-                    for (int e = 0; e < 8; e++) f[e] = n[w] > 0 ? __uint_as_float(o[i + e]) * inv : 0.f;
-                    if (a.splits > 1) {
-                        float* dst = a.part + prow * a.d + c + i;
-                        store4(dst, f);
-                        store4(dst + 4, f + 4);
-                    } else {
-                        uint4 u;
-                        u.x = pack_bf16x2(f[0], f[1]);
-                        u.y = pack_bf16x2(f[2], f[3]);
-                        u.z = pack_bf16x2(f[4], f[5]);
-                        u.w = pack_bf16x2(f[6], f[7]);
-                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o_out) + row * a.d + c + i) = u;
-                    }
+                for (int e = 0; e < 8; e++) f[e] = n[w] > 0 ? __uint_as_float(o[i + e]) * inv : 0.f;
+                if (a.splits == 1) {
+                    put_chunk(out + (c / 64) * C::REGION, lr, (c % 64 + i) / 8, f);
+                } else if (r < a.R && c + i < a.d) {
+                    float* dst = a.part + prow * a.d + c + i;
+                    store4(dst, f);
+                    store4(dst + 4, f + 4);
                 }
+            }
+        }
+        if (a.splits == 1) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0 && r < a.R) {
+                for (int c = 0; c < D / 64; c++)
+                    tma_store_3d(&mo, smem_u32(out + c * C::REGION + lr * 128), c * 64, r, slice);
+                bulk_commit();
             }
         }
         if (r < a.R) {
@@ -344,6 +346,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             else
                 a.lse_out[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
         }
+        if (lane == 0) bulk_wait_read();
     }
     tc_fence_before();
     __syncthreads();
@@ -357,15 +360,16 @@ template <int D>
 int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
     using C = Cfg<D>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BM));
     LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BN));
     LLSA_TRY(make_tmap_rows(&mv, a.v, s.slices, s.nk, s.d, BN));
+    LLSA_TRY(make_tmap_rows(&mo, a.o_out, s.slices, s.R, s.d, 32));
     cudaFuncSetAttribute(dense_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const long long blocks = (long long)((s.R + 2 * BM - 1) / (2 * BM)) * s.slices;
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("dense_fwd_tc", st,
-                dense_fwd_tc_kernel<D><<<dim3((unsigned)blocks, a.splits), kThreads, C::SMEM, st>>>(mq, mk, mv, a));
+                dense_fwd_tc_kernel<D><<<dim3((unsigned)blocks, a.splits), kThreads, C::SMEM, st>>>(mq, mk, mv, mo, a));
     return LLSA_OK;
 }
 

@@ -31,6 +31,17 @@ __device__ __forceinline__ void land(uint32_t mbar, uint32_t parity) {
     }
 }
 
+// Eight fp32 values as bf16 into chunk `chunk` (16 bytes) of row `row` of a tile
+// region of 128-byte rows with the 128-byte swizzle.
+__device__ __forceinline__ void put_chunk(unsigned char* region, int row, int chunk, const float* v) {
+    uint4 u;
+    u.x = pack_bf16x2(v[0], v[1]);
+    u.y = pack_bf16x2(v[2], v[3]);
+    u.z = pack_bf16x2(v[4], v[5]);
+    u.w = pack_bf16x2(v[6], v[7]);
+    *reinterpret_cast<uint4*>(region + row * 128 + ((chunk ^ (row & 7)) << 4)) = u;
+}
+
 // A stage of a ring and the parity of its current use.
 template <int N>
 struct Stage {
