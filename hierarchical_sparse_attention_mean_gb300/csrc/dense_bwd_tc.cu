@@ -108,7 +108,8 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
     float* stats = reinterpret_cast<float*>(ring2 + C::N2 * C::TILE);
     Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * C::TILE + C::STATS);
     volatile int* abort_flag = &bar->abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // broadcast, so that the compiler knows these as the same in a whole warp
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
         if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
         return;
@@ -155,7 +156,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bar->tmem_slot;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
 
     if (warp >= kWarps + 2) {
         // ----------------------------------------------------------- copies

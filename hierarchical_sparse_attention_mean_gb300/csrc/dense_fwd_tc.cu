@@ -68,7 +68,8 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     unsigned char* sV = sK + C::STAGES * C::TILE;
     Bars* bar = reinterpret_cast<Bars*>(sV + C::STAGES * C::TILE);
     volatile int* abort_flag = &bar->abort_flag;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // broadcast, so that the compiler knows these as the same in a whole warp
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     // blocks of a slice from its last rows to its first: causal order gives those the most keys
     const int blocks = (a.R + 2 * BM - 1) / (2 * BM);
@@ -110,7 +111,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tbase = bar->tmem_slot;
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
 
     if (warp >= 8) {
         regs_dec<kRegsOther>();
