@@ -38,6 +38,7 @@ struct DenseArgs {
     float* nd;    // [slices][Rp]: -D = -dout . o; 0 for those rows
     float* part;  // partial sums of a split axis (layout: see the kernels)
     int splits, chunk;  // parts of the split axis, and how many of its elements each takes
+    int pieces;         // pieces of work that the resident blocks share (tensor-core kernels)
     int slices, kv_heads, nq, nk, R, Rp, d, causal;
     float scale;
     int* status;
@@ -80,6 +81,34 @@ __device__ __forceinline__ int dense_tile_kend(const DenseArgs& a, DenseSpan s, 
     if (!wraps && t0 >= s.lq) return 0;
     const int last = wraps ? s.lq - 1 : min(t0 + rows, s.lq) - 1;
     return last < 0 ? 0 : dense_kend(a, s, last);
+}
+
+// Piece `id` of a call's work: block `block` of `blocks` along the owned axis of
+// a slice, part `part` of the split one. In causal order blocks differ in
+// work: all slices' first blocks come first, so the heaviest ones are dealt out
+// evenly before the light ones. Otherwise the blocks of a slice stay together
+// and share its keys in L2.
+struct DenseWork {
+    int slice, part, block, blocks;
+};
+
+constexpr long long kDenseMaxPieces = 0x7fffffffLL - 1024;
+
+__device__ __forceinline__ DenseWork dense_work(const DenseArgs& a, int id, int blocks) {
+    DenseWork w;
+    w.blocks = blocks;
+    const int sets = a.slices * a.splits;
+    int set;
+    if (a.causal) {
+        w.block = id / sets;
+        set = id - w.block * sets;
+    } else {
+        set = id / blocks;
+        w.block = id - set * blocks;
+    }
+    w.slice = a.splits > 1 ? set / a.splits : set;
+    w.part = set - w.slice * a.splits;
+    return w;
 }
 
 size_t dense_fwd_workspace(const DenseShape& s);

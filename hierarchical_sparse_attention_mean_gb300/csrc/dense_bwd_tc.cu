@@ -23,6 +23,11 @@
 // while the threads turn S and dP into P and dS. All sixteen elementwise warps
 // take one item together, a thread per row and quarter of the columns.
 //
+// At 64 columns one block per SM stays for the whole call and takes its share of
+// the work: while the elementwise warps finish one piece, the others load and
+// multiply for the next. At 128 columns shared memory holds one pair of
+// stationary tiles, and every piece gets a block of its own.
+//
 // Roles: warps 0-15 elementwise and epilogue, warp 16 issues S and dP, warp 17
 // the sums, warps 18 and 19 the copies of the two streams. Waits and the issue of a
 // dozen MMAs add up to some thousand clocks per item, so one warp for all of them
@@ -37,7 +42,9 @@ namespace {
 using namespace tc;
 
 constexpr int kWarps = 16, kCols = 32;  // elementwise warps: a thread takes one row and kCols columns of an item
-constexpr int kThreads = (kWarps + 4) * 32;
+// 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
+// 104 of them, the 128 others keep 64.
+constexpr int kThreads = (kWarps + 4) * 32, kRegsElementwise = 104, kRegsOther = 64;
 constexpr int BT = 128;  // rows of every tile
 
 template <int D, bool KEYS>
@@ -45,15 +52,16 @@ struct Cfg {
     static constexpr int TILE = BT * D * 2;   // bytes of 128 rows
     static constexpr int REGION = BT * 128;   // bytes of 128 rows x 64 columns
     static constexpr int N1 = D == 64 ? 4 : 3, N2 = D == 64 ? 4 : 2;  // stages of the two streams
+    static constexpr int NX = D == 64 ? 2 : 1;                        // pairs of stationary tiles
     static constexpr int NB = D == 128 && KEYS ? 1 : 2;               // dP buffers
     static constexpr int STATS = KEYS ? N2 * 2 * BT * 4 : 0;          // -l2 and -D of a row tile, with stream 2
-    static constexpr int SMEM = (2 + N1 + N2) * TILE + STATS + 512;
+    static constexpr int SMEM = (2 * NX + N1 + N2) * TILE + STATS + 512;
     static constexpr int TM_DP = 128, TM_ACC = 128 + NB * 128;        // S at column 0
 };
 
 struct Bars {
-    uint64_t x_full[2], y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
-    uint64_t s_full, s_free, dp_full[2], ds_ready[2], dp_free[2], acc_full, drain[2];
+    uint64_t x_full[2][2], x_free[2], y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
+    uint64_t s_full, s_free, dp_full[2], ds_ready[2], dp_free[2], acc_full, acc_free, drain[2];
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -94,6 +102,30 @@ private:
     }
 };
 
+// One piece of work: 128 stationary rows of a slice against a part of the stream.
+template <bool KEYS>
+struct Piece {
+    int slice, x0, part, first, stop;
+    DenseSpan sp;
+
+    __device__ __forceinline__ Piece(const DenseArgs& a, int id) {
+        const DenseWork w = dense_work(a, id, ((KEYS ? a.nk : a.R) + BT - 1) / BT);
+        slice = w.slice;
+        part = w.part;
+        // causal order: the last rows see the most keys, the first keys the most rows; those come first
+        x0 = (a.causal && !KEYS ? w.blocks - 1 - w.block : w.block) * BT;
+        sp = dense_span(a, slice);
+        first = a.splits > 1 ? part * a.chunk : 0;
+        if constexpr (KEYS) {
+            stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
+        } else {
+            stop = dense_tile_kend(a, sp, x0 < a.nq ? x0 : x0 % a.nq, BT);
+            if (a.splits > 1) stop = min(stop, first + a.chunk);
+        }
+    }
+    __device__ __forceinline__ Items<KEYS> items(const DenseArgs& a) const { return Items<KEYS>(a, sp, x0, first, stop); }
+};
+
 template <int D, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
@@ -102,8 +134,8 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                     const __grid_constant__ DenseArgs a) {
     using C = Cfg<D, KEYS>;
     extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char* sX = sm;  // X1, X2
-    unsigned char* ring1 = sm + 2 * C::TILE;
+    unsigned char* sX = sm;  // [NX] X1, X2
+    unsigned char* ring1 = sm + 2 * C::NX * C::TILE;
     unsigned char* ring2 = ring1 + C::N1 * C::TILE;
     float* stats = reinterpret_cast<float*>(ring2 + C::N2 * C::TILE);
     Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * C::TILE + C::STATS);
@@ -114,27 +146,14 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
         return;
     }
-
-    // causal order: the last rows see the most keys, the first keys the most rows; those blocks go first
     const int extent = KEYS ? a.nk : a.R;
-    const int blocks = (extent + BT - 1) / BT;
-    const int slice = blockIdx.x / blocks;
-    const int idx = (int)(blockIdx.x - slice * blocks);
-    const int x0 = (KEYS ? idx : blocks - 1 - idx) * BT;
-    const int part = blockIdx.y;
-    const DenseSpan sp = dense_span(a, slice);
-    int first = a.splits > 1 ? part * a.chunk : 0, stop;
-    if constexpr (KEYS) {
-        stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
-    } else {
-        stop = dense_tile_kend(a, sp, x0 % a.nq, BT);
-        if (a.splits > 1) stop = min(stop, first + a.chunk);
-    }
-    const bool any = !Items<KEYS>(a, sp, x0, first, stop).done();
+    const Piece<KEYS> start(a, blockIdx.x);  // worked out while the barriers and tensor memory come up
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
-            mbar_init(smem_u32(&bar->x_full[i]), 1);
+            mbar_init(smem_u32(&bar->x_full[0][i]), 1);
+            mbar_init(smem_u32(&bar->x_full[1][i]), 1);
+            mbar_init(smem_u32(&bar->x_free[i]), 4);
             mbar_init(smem_u32(&bar->dp_full[i]), 1);
             mbar_init(smem_u32(&bar->ds_ready[i]), kWarps);
             mbar_init(smem_u32(&bar->dp_free[i]), 1);
@@ -149,314 +168,385 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         mbar_init(smem_u32(&bar->s_full), 1);
         mbar_init(smem_u32(&bar->s_free), kWarps);
         mbar_init(smem_u32(&bar->acc_full), 1);
+        mbar_init(smem_u32(&bar->acc_free), kWarps);
         bar->abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    if (warp >= kWarps + 2 && lane == 0) {
+        prefetch_map(warp == kWarps + 2 ? &mx1 : &mx2);
+        prefetch_map(warp == kWarps + 2 ? &my1 : &my2);
+        prefetch_map(warp == kWarps + 2 ? &mz1 : &mz2);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
 
-    if (warp >= kWarps + 2) {
-        // ----------------------------------------------------------- copies
-        if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
-            const int k = warp - kWarps - 2;  // stream
-            const int ns = k == 0 ? C::N1 : C::N2;
-            unsigned char* ring = k == 0 ? ring1 : ring2;
-            uint64_t* full = k == 0 ? bar->y1_full : bar->y2_full;
-            uint64_t* empty = k == 0 ? bar->y1_empty : bar->y2_empty;
-            const CUtensorMap* mx = k == 0 ? &mx1 : &mx2;
-            const CUtensorMap* my = k == 0 ? &my1 : &my2;
-            const uint32_t xb = smem_u32(&bar->x_full[k]);
-            mbar_arrive_expect_tx(xb, C::TILE);
-            for (int c = 0; c < D / 64; c++)
-                tma_load_3d(smem_u32(sX + k * C::TILE + c * C::REGION), mx, c * 64, x0, slice, xb);
-            int st = 0, n = 0;
-            uint32_t parity = 1;  // of the release that the stage's next use waits for
-            for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a)) {
-                if (n >= ns && !bar_wait(smem_u32(&empty[st]), parity, abort_flag, a)) break;
-                const uint32_t fb = smem_u32(&full[st]);
-                const bool with_stats = KEYS && k == 1;
-                mbar_arrive_expect_tx(fb, C::TILE + (with_stats ? 2 * BT * 4 : 0));
-                for (int c = 0; c < D / 64; c++)
-                    tma_load_3d(smem_u32(ring + st * C::TILE + c * C::REGION), my, c * 64, it.pos, slice, fb);
-                if (with_stats) {
-                    const long long row = (long long)slice * a.Rp + it.pos;
-                    bulk_load(smem_u32(stats + st * 2 * BT), a.nl2 + row, BT * 4, fb);
-                    bulk_load(smem_u32(stats + st * 2 * BT + BT), a.nd + row, BT * 4, fb);
-                }
-                n++;
-                if (++st == ns) {
-                    st = 0;
-                    parity ^= 1;
-                }
-            }
-            land(xb, 0);
-            for (int x = max(0, n - ns); x < n; x++) land(smem_u32(&full[x % ns]), (x / ns) & 1);
-        }
-    } else if (warp == kWarps) {
-        // --------------------------------------------------- S and dP issuer
-        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0);
-        const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024);
-        const uint64_t dY1 = desc_sw128(smem_u32(ring1), 16, 1024), dY2 = desc_sw128(smem_u32(ring2), 16, 1024);
-        // Rows of the streamed tile whose P and dS are 0 by the mask of the
-        // lengths may hold anything: they meet those zeros in the sums, so
-        // they are cleared.
-        auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
-            if constexpr (KEYS) {
-                if (it.all || it.t0 + BT <= sp.lq) return;
-                int t = it.t0 + lane;
-                for (int x = lane; x < BT; x += 32, t += 32)
-                    if (t % a.nq >= sp.lq)
+    // Every role walks the block's pieces. Counted on through them: the stages of
+    // the rings and buffers, the items (n), and the pieces that have any (v).
+    if (warp >= kWarps) {
+        regs_dec<kRegsOther>();
+        if (warp >= kWarps + 2) {
+            // ----------------------------------------------------------- copies
+            if (lane == 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+                const int k = warp - kWarps - 2;  // stream
+                const int ns = k == 0 ? C::N1 : C::N2;
+                unsigned char* ring = k == 0 ? ring1 : ring2;
+                uint64_t* full = k == 0 ? bar->y1_full : bar->y2_full;
+                uint64_t* empty = k == 0 ? bar->y1_empty : bar->y2_empty;
+                const CUtensorMap* mx = k == 0 ? &mx1 : &mx2;
+                const CUtensorMap* my = k == 0 ? &my1 : &my2;
+                int st = 0, n = 0, v = 0;
+                uint32_t parity = 1;  // of the release that the stage's next use waits for
+                bool ok = true;
+                Piece<KEYS> pc = start;
+                for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
+                    if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
+                    Items<KEYS> it = pc.items(a);
+                    if (it.done()) continue;
+                    const int xb = v % C::NX;
+                    if (v >= C::NX) ok = bar_wait(smem_u32(&bar->x_free[xb]), (v / C::NX - 1) & 1, abort_flag, a);
+                    if (!ok) break;
+                    const uint32_t fx = smem_u32(&bar->x_full[k][xb]);
+                    mbar_arrive_expect_tx(fx, C::TILE);
+                    for (int c = 0; c < D / 64; c++)
+                        tma_load_3d(smem_u32(sX + (2 * xb + k) * C::TILE + c * C::REGION), mx, c * 64, pc.x0, pc.slice, fx);
+                    v++;
+                    for (; !it.done(); it.next(a)) {
+                        if (n >= ns) ok = bar_wait(smem_u32(&empty[st]), parity, abort_flag, a);
+                        if (!ok) break;
+                        const uint32_t fb = smem_u32(&full[st]);
+                        const bool with_stats = KEYS && k == 1;
+                        mbar_arrive_expect_tx(fb, C::TILE + (with_stats ? 2 * BT * 4 : 0));
                         for (int c = 0; c < D / 64; c++)
-                            for (int e = 0; e < 8; e++)
-                                reinterpret_cast<uint4*>(tile + c * C::REGION + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                const int live = sp.lk - it.pos;
-                if (live >= BT) return;
-                for (int c = 0; c < D / 64; c++)
-                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
-                        reinterpret_cast<uint4*>(tile + c * C::REGION)[x] = make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_async_smem();
-            __syncwarp();
-        };
-        if (any) {
-            bool ok = warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
-                      warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
-            Stage<C::N1> s1;
-            Stage<C::N2> s2;
-            Stage<C::NB> sb;
-            uint32_t n = 0;
-            for (Items<KEYS> it(a, sp, x0, first, stop); ok && !it.done(); it.next(a), n++) {
-                ok = warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a);
-                if (!ok) break;
-                clear_rows(ring1 + s1.st * C::TILE, it);
-                if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t y1 = (uint32_t)(s1.st * C::TILE);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ks++) {
-                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                    mma_bf16_warp(tbase, dX + (off >> 4), dY1 + ((y1 + off) >> 4), idS, ks > 0);
+                            tma_load_3d(smem_u32(ring + st * C::TILE + c * C::REGION), my, c * 64, it.pos, pc.slice, fb);
+                        if (with_stats) {
+                            const long long row = (long long)pc.slice * a.Rp + it.pos;
+                            bulk_load(smem_u32(stats + st * 2 * BT), a.nl2 + row, BT * 4, fb);
+                            bulk_load(smem_u32(stats + st * 2 * BT + BT), a.nd + row, BT * 4, fb);
+                        }
+                        n++;
+                        if (++st == ns) {
+                            st = 0;
+                            parity ^= 1;
+                        }
+                    }
                 }
-                mma_commit_warp(smem_u32(&bar->s_full));
-                ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
-                if (!ok) break;
-                if (KEYS) clear_rows(ring2 + s2.st * C::TILE, it);  // V only enters dP, which the mask covers
-                if (n >= C::NB) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t y2 = (uint32_t)(s2.st * C::TILE);
-#pragma unroll
-                for (int ks = 0; ks < D / 16; ks++) {
-                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                    mma_bf16_warp(tbase + C::TM_DP + sb.st * 128, dX + ((C::TILE + off) >> 4), dY2 + ((y2 + off) >> 4), idS,
-                                  ks > 0);
-                }
-                mma_commit_warp(smem_u32(&bar->dp_full[sb.st]));
-                if (!KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2.st]));
-                s1.next();
-                s2.next();
-                sb.next();
+                // copies still in flight must land before the block exits
+                for (int x = max(0, v - C::NX); x < v; x++) land(smem_u32(&bar->x_full[k][x % C::NX]), (x / C::NX) & 1);
+                for (int x = max(0, n - ns); x < n; x++) land(smem_u32(&full[x % ns]), (x / ns) & 1);
             }
-        }
-        // no MMA may be in flight when tensor memory is released
-        mma_commit_warp(smem_u32(&bar->drain[0]));
-        if (lane == 0) land(smem_u32(&bar->drain[0]), 0);
-        __syncwarp();
-    } else if (warp == kWarps + 1) {
-        // ------------------------------------------------------- sums issuer
-        constexpr uint32_t idA = idesc_bf16(BT, D, 0, 1);
-        const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the tiles read along their rows
-        const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
-        if (any) {
+        } else if (warp == kWarps) {
+            // --------------------------------------------------- S and dP issuer
+            const uint32_t leader = elect_lane();
+            constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0);
+            const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024);
+            const uint64_t dY1 = desc_sw128(smem_u32(ring1), 16, 1024), dY2 = desc_sw128(smem_u32(ring2), 16, 1024);
+            // Rows of the streamed tile whose P and dS are 0 by the mask of the
+            // lengths may hold anything: they meet those zeros in the sums, so
+            // they are cleared.
+            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
+                if constexpr (KEYS) {
+                    if (it.all || it.t0 + BT <= it.sp.lq) return;
+                    int t = it.t0 + lane;
+                    for (int x = lane; x < BT; x += 32, t += 32)
+                        if (t % a.nq >= it.sp.lq)
+                            for (int c = 0; c < D / 64; c++)
+                                for (int e = 0; e < 8; e++)
+                                    reinterpret_cast<uint4*>(tile + c * C::REGION + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const int live = it.sp.lk - it.pos;
+                    if (live >= BT) return;
+                    for (int c = 0; c < D / 64; c++)
+                        for (int x = live * 8 + lane; x < BT * 8; x += 32)
+                            reinterpret_cast<uint4*>(tile + c * C::REGION)[x] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                __syncwarp();
+            };
             bool ok = true;
             Stage<C::N1> s1;
             Stage<C::N2> s2;
             Stage<C::NB> sb;
+            Stage<C::NX> sx;
             uint32_t n = 0;
-            for (Items<KEYS> it(a, sp, x0, first, stop); ok && !it.done(); it.next(a), n++) {
-                ok = warp_wait(smem_u32(&bar->ds_ready[sb.st]), sb.parity, abort_flag, a);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t p0 = tbase + C::TM_DP + sb.st * 128;
+            Piece<KEYS> pc = start;
+            for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
+                if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
+                Items<KEYS> it = pc.items(a);
+                if (it.done()) continue;
+                ok = warp_wait(smem_u32(&bar->x_full[0][sx.st]), sx.parity, abort_flag, a) &&
+                     warp_wait(smem_u32(&bar->x_full[1][sx.st]), sx.parity, abort_flag, a);
+                const uint64_t dX1 = dX + (2 * sx.st * C::TILE >> 4), dX2 = dX1 + (C::TILE >> 4);
+                for (; ok && !it.done(); it.next(a), n++) {
+                    ok = warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a);
+                    if (!ok) break;
+                    clear_rows(ring1 + s1.st * C::TILE, it);
+                    if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dT1 = dY1 + (s1.st * C::TILE >> 4);
 #pragma unroll
-                for (int ks = 0; ks < BT / 16; ks++) {
-                    const uint32_t op = p0 + (ks / 2) * 32 + (ks % 2) * 8;  // each quarter of the columns: P, then dS, 16 columns each
-                    const uint64_t m1 = dM1 + ((s1.st * C::TILE + ks * 2048) >> 4), m2 = dM2 + ((s2.st * C::TILE + ks * 2048) >> 4);
+                    for (int ks = 0; ks < D / 16; ks++) {
+                        const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                        mma_ss(leader, tbase, dX1 + (off >> 4), dT1 + (off >> 4), idS, ks > 0);
+                    }
+                    commit(leader, smem_u32(&bar->s_full));
+                    ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
+                    if (!ok) break;
+                    if (KEYS) clear_rows(ring2 + s2.st * C::TILE, it);  // V only enters dP, which the mask covers
+                    if (n >= C::NB) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dT2 = dY2 + (s2.st * C::TILE >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ks++) {
+                        const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                        mma_ss(leader, tbase + C::TM_DP + sb.st * 128, dX2 + (off >> 4), dT2 + (off >> 4), idS,
+                                      ks > 0);
+                    }
+                    commit(leader, smem_u32(&bar->dp_full[sb.st]));
+                    if (!KEYS) commit(leader, smem_u32(&bar->y2_empty[s2.st]));
+                    s1.next();
+                    s2.next();
+                    sb.next();
+                }
+                sx.next();
+            }
+            // no MMA may be in flight when tensor memory is released
+            commit(leader, smem_u32(&bar->drain[0]));
+            if (lane == 0) land(smem_u32(&bar->drain[0]), 0);
+            __syncwarp();
+        } else if (warp == kWarps + 1) {
+            // ------------------------------------------------------- sums issuer
+            const uint32_t leader = elect_lane();
+            constexpr uint32_t idA = idesc_bf16(BT, D, 0, 1);
+            const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the tiles read along their rows
+            const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
+            bool ok = true;
+            Stage<C::N1> s1;
+            Stage<C::N2> s2;
+            Stage<C::NB> sb;
+            int v = 0;
+            Piece<KEYS> pc = start;
+            for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
+                if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
+                Items<KEYS> it = pc.items(a);
+                if (it.done()) continue;
+                if (v > 0) ok = warp_wait(smem_u32(&bar->acc_free), (v - 1) & 1, abort_flag, a);
+                uint32_t n = 0;
+                for (; ok && !it.done(); it.next(a), n++) {
+                    ok = warp_wait(smem_u32(&bar->ds_ready[sb.st]), sb.parity, abort_flag, a);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t p0 = tbase + C::TM_DP + sb.st * 128;
+                    const uint64_t dT1 = dM1 + (s1.st * C::TILE >> 4), dT2 = dM2 + (s2.st * C::TILE >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < BT / 16; ks++) {
+                        const uint32_t op = p0 + (ks / 2) * 32 + (ks % 2) * 8;  // each quarter of the columns: P, then dS, 16 columns each
+                        const uint64_t m1 = dT1 + (ks * 2048 >> 4), m2 = dT2 + (ks * 2048 >> 4);
+                        if constexpr (KEYS) {
+                            mma_ts(leader, tbase + C::TM_ACC + D, op, m2, idA, n > 0 || ks > 0);
+                            mma_ts(leader, tbase + C::TM_ACC, op + 16, m1, idA, n > 0 || ks > 0);
+                        } else {
+                            mma_ts(leader, tbase + C::TM_ACC, op, m1, idA, n > 0 || ks > 0);
+                        }
+                    }
+                    commit(leader, smem_u32(&bar->dp_free[sb.st]));
+                    commit(leader, smem_u32(&bar->y1_empty[s1.st]));
+                    if (KEYS) commit(leader, smem_u32(&bar->y2_empty[s2.st]));
+                    s1.next();
+                    s2.next();
+                    sb.next();
+                }
+                if (ok) commit(leader, smem_u32(&bar->acc_full));
+                v++;
+            }
+            commit(leader, smem_u32(&bar->drain[1]));
+            if (lane == 0) land(smem_u32(&bar->drain[1]), 0);
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------- elementwise, epilogue
+        regs_inc<kRegsElementwise>();
+        const int w = warp >> 2;  // quarter of the columns
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int lr = (warp & 3) * 32 + lane;  // row of the tile
+        const float sl2 = a.scale * kDenseLog2e;
+        const uint64_t sl2x2 = pack2(sl2, sl2);
+        uint32_t n = 0;
+        int v = 0;
+        Stage<C::N2> s2;
+        Stage<C::NB> sb;
+        const bool storer = w == 0 && lane == 0;  // sends the results of this quarter of the rows
+        bool storing = false;                     // and has some on their way, from stationary pair (v - 1) % NX
+        auto stored = [&]() {
+            if (storer && storing) {
+                bulk_wait_read();
+                mbar_arrive(smem_u32(&bar->x_free[(v - 1) % C::NX]));
+            }
+            storing = false;
+        };
+        for (int id = blockIdx.x; id < a.pieces; id += gridDim.x) {
+            const Piece<KEYS> pc(a, id);
+            const DenseSpan sp = pc.sp;
+            const int x = pc.x0 + lr;  // stationary row
+            uint64_t nl2x2 = 0, ndx2 = 0;
+            int kend = 0;
+            if constexpr (!KEYS) {
+                const long long row = (long long)pc.slice * a.Rp + x;  // Rp is a multiple of 128
+                const float nl2 = a.nl2[row], nd = a.nd[row];
+                nl2x2 = pack2(nl2, nl2);
+                ndx2 = pack2(nd, nd);
+                kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
+            }
+            Items<KEYS> it = pc.items(a);
+            const bool any = !it.done();
+            for (; !it.done(); it.next(a), n++) {
+                const uint32_t tP = tbase + C::TM_DP + sb.st * 128 + w * kCols + lanes;
+                const float* st = stats + s2.st * 2 * BT + w * kCols;  // KEYS: -l2 of these columns' rows; -D BT further
+                bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
+                tc_fence_after();
+                uint32_t s[kCols];
+                tmem_ld32_nowait(tbase + lanes + w * kCols, s);
+                if constexpr (KEYS) bar_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
+                tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->s_free), lane);
+                stored();
+#pragma unroll
+                for (int c = 0; c < kCols; c += 4) {
+                    uint64_t l0 = nl2x2, l1 = nl2x2;
                     if constexpr (KEYS) {
-                        mma_bf16_ts_warp(tbase + C::TM_ACC + D, op, m2, idA, n > 0 || ks > 0);
-                        mma_bf16_ts_warp(tbase + C::TM_ACC, op + 16, m1, idA, n > 0 || ks > 0);
-                    } else {
-                        mma_bf16_ts_warp(tbase + C::TM_ACC, op, m1, idA, n > 0 || ks > 0);
+                        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + c);
+                        l0 = u.x;
+                        l1 = u.y;
+                    }
+                    float e0, e1, e2, e3;
+                    unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2x2, l0), e0, e1);
+                    unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2x2, l1), e2, e3);
+                    s[c] = __float_as_uint(ex2(e0));
+                    s[c + 1] = __float_as_uint(ex2(e1));
+                    s[c + 2] = __float_as_uint(ex2(e2));
+                    s[c + 3] = __float_as_uint(ex2(e3));
+                }
+                // which of this thread's columns the mask leaves
+                bool masked;
+                if constexpr (KEYS) {
+                    // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
+                    masked = a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < pc.x0 + BT);
+                    if (masked) {
+                        int t = (it.t0 + w * kCols) % a.nq;
+#pragma unroll
+                        for (int c = 0; c < kCols; c++) {
+                            if (x > t + sp.lk - sp.lq) s[c] = 0u;
+                            if (++t == a.nq) t = 0;
+                        }
+                    }
+                } else {
+                    masked = __any_sync(0xffffffffu, kend - it.pos < BT);
+                    if (masked) {
+#pragma unroll
+                        for (int c = 0; c < kCols; c++)
+                            if (w * kCols + c >= kend - it.pos) s[c] = 0u;
                     }
                 }
-                mma_commit_warp(smem_u32(&bar->dp_free[sb.st]));
-                mma_commit_warp(smem_u32(&bar->y1_empty[s1.st]));
-                if (KEYS) mma_commit_warp(smem_u32(&bar->y2_empty[s2.st]));
-                s1.next();
+                bar_wait(smem_u32(&bar->dp_full[sb.st]), sb.parity, abort_flag, a);
+                tc_fence_after();
+                uint32_t g[kCols];
+                tmem_ld32_nowait(tP, g);
+                tmem_wait_ld();
+                uint32_t o[kCols / 2];
+                if constexpr (KEYS) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 2)
+                        o[c >> 1] = pack_bf16x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
+                    tmem_st16(tP, o);
+                }
+#pragma unroll
+                for (int c = 0; c < kCols; c += 4) {
+                    uint64_t d0 = ndx2, d1 = ndx2;
+                    if constexpr (KEYS) {
+                        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + BT + c);
+                        d0 = u.x;
+                        d1 = u.y;
+                    }
+                    float e0, e1, e2, e3;
+                    unpack2(mul2(add2(pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), d0),
+                                 pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]))), e0, e1);
+                    unpack2(mul2(add2(pack2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), d1),
+                                 pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]))), e2, e3);
+                    if (!KEYS && masked) {  // dP of a key behind the lengths may be anything
+                        const int lim = kend - it.pos - w * kCols;
+                        e0 = c < lim ? e0 : 0.f;
+                        e1 = c + 1 < lim ? e1 : 0.f;
+                        e2 = c + 2 < lim ? e2 : 0.f;
+                        e3 = c + 3 < lim ? e3 : 0.f;
+                    }
+                    o[c >> 1] = pack_bf16x2(e0, e1);
+                    o[(c >> 1) + 1] = pack_bf16x2(e2, e3);
+                }
+                tmem_st16(KEYS ? tP + kCols / 2 : tP, o);
+                tmem_wait_st();
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->ds_ready[sb.st]), lane);
                 s2.next();
                 sb.next();
             }
-            if (ok) mma_commit_warp(smem_u32(&bar->acc_full));
-        }
-        mma_commit_warp(smem_u32(&bar->drain[1]));
-        if (lane == 0) land(smem_u32(&bar->drain[1]), 0);
-        __syncwarp();
-    } else if (warp < kWarps) {
-        // ---------------------------------------- elementwise, epilogue
-        const int w = warp >> 2;  // quarter of the columns
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int x = x0 + (warp & 3) * 32 + lane;  // stationary row
-        const float sl2 = a.scale * kDenseLog2e;
-        const uint64_t sl2x2 = pack2(sl2, sl2);
-        uint64_t nl2x2 = 0, ndx2 = 0;
-        int kend = 0;
-        if constexpr (!KEYS) {
-            const long long row = (long long)slice * a.Rp + x;  // Rp is a multiple of 128
-            const float nl2 = a.nl2[row], nd = a.nd[row];
-            nl2x2 = pack2(nl2, nl2);
-            ndx2 = pack2(nd, nd);
-            kend = x < a.R ? dense_kend(a, sp, x % a.nq) : 0;
-        }
-        uint32_t n = 0;
-        Stage<C::N2> s2;
-        Stage<C::NB> sb;
-        for (Items<KEYS> it(a, sp, x0, first, stop); !it.done(); it.next(a), n++) {
-            const uint32_t tP = tbase + C::TM_DP + sb.st * 128 + w * kCols + lanes;
-            const float* st = stats + s2.st * 2 * BT + w * kCols;  // KEYS: -l2 of these columns' rows; -D BT further
-            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
-            tc_fence_after();
-            uint32_t s[kCols];
-            tmem_ld32_nowait(tbase + lanes + w * kCols, s);
-            if constexpr (KEYS) bar_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
-            tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(smem_u32(&bar->s_free), lane);
-#pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                uint64_t l0 = nl2x2, l1 = nl2x2;
-                if constexpr (KEYS) {
-                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + c);
-                    l0 = u.x;
-                    l1 = u.y;
-                }
-                float e0, e1, e2, e3;
-                unpack2(fma2(pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sl2x2, l0), e0, e1);
-                unpack2(fma2(pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sl2x2, l1), e2, e3);
-                s[c] = __float_as_uint(ex2(e0));
-                s[c + 1] = __float_as_uint(ex2(e1));
-                s[c + 2] = __float_as_uint(ex2(e2));
-                s[c + 3] = __float_as_uint(ex2(e3));
+            const long long row = (long long)pc.slice * extent + x, all = (long long)a.slices * extent;
+            // rows without a gradient hold whatever their padding made: zero
+            const bool live = any && (KEYS ? x < sp.lk : kend > 0);
+            unsigned char* out = sX + 2 * (v % C::NX) * C::TILE;  // the stationary tiles have been used up
+            if (any) {
+                bar_wait(smem_u32(&bar->acc_full), v & 1, abort_flag, a);
+                tc_fence_after();
             }
-            // which of this thread's columns the mask leaves
-            bool masked;
-            if constexpr (KEYS) {
-                // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
-                masked = a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT);
-                if (masked) {
-                    int t = (it.t0 + w * kCols) % a.nq;
 #pragma unroll
-                    for (int c = 0; c < kCols; c++) {
-                        if (x > t + sp.lk - sp.lq) s[c] = 0u;
-                        if (++t == a.nq) t = 0;
+            for (int k = 0; k < (KEYS ? 2 : 1); k++) {
+                const float f = k == 0 ? a.scale : 1.f;
+#pragma unroll
+                for (int c = w * 16; c < D; c += 64) {
+                    float o[16];
+                    if (any) tmem_ld16(tbase + C::TM_ACC + k * D + c + lanes, o);
+#pragma unroll
+                    for (int i = 0; i < 16; i++) o[i] = live ? o[i] * f : 0.f;
+                    if (a.splits > 1) {
+                        float* dst = a.part + ((k * a.splits + pc.part) * all + row) * a.d + c;
+                        if (x < extent)
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                if (c + i < a.d) store4(dst + i, o + i);
+                    } else if (any) {
+                        put_chunk(out + k * C::TILE + (c / 64) * C::REGION, lr, w * 2, o);
+                        put_chunk(out + k * C::TILE + (c / 64) * C::REGION, lr, w * 2 + 1, o + 8);
+                    } else if (x < extent) {  // nothing here: zeros, past the tiles that the next piece may be using
+                        __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(KEYS ? (k == 0 ? a.dk : a.dv) : a.dq) + row * a.d + c;
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4)
+                            if (c + i < a.d) store4(dst + i, o + i);
                     }
                 }
-            } else {
-                masked = __any_sync(0xffffffffu, kend - it.pos < BT);
-                if (masked) {
-#pragma unroll
-                    for (int c = 0; c < kCols; c++)
-                        if (w * kCols + c >= kend - it.pos) s[c] = 0u;
-                }
             }
-            bar_wait(smem_u32(&bar->dp_full[sb.st]), sb.parity, abort_flag, a);
-            tc_fence_after();
-            uint32_t g[kCols];
-            tmem_ld32_nowait(tP, g);
-            tmem_wait_ld();
-            uint32_t o[kCols / 2];
-            if constexpr (KEYS) {
-#pragma unroll
-                for (int c = 0; c < kCols; c += 2)
-                    o[c >> 1] = pack_bf16x2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                tmem_st16(tP, o);
-            }
-#pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                uint64_t d0 = ndx2, d1 = ndx2;
-                if constexpr (KEYS) {
-                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + BT + c);
-                    d0 = u.x;
-                    d1 = u.y;
-                }
-                float e0, e1, e2, e3;
-                unpack2(mul2(add2(pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1])), d0),
-                             pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]))), e0, e1);
-                unpack2(mul2(add2(pack2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3])), d1),
-                             pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]))), e2, e3);
-                if (!KEYS && masked) {  // dP of a key behind the lengths may be anything
-                    const int lim = kend - it.pos - w * kCols;
-                    e0 = c < lim ? e0 : 0.f;
-                    e1 = c + 1 < lim ? e1 : 0.f;
-                    e2 = c + 2 < lim ? e2 : 0.f;
-                    e3 = c + 3 < lim ? e3 : 0.f;
-                }
-                o[c >> 1] = pack_bf16x2(e0, e1);
-                o[(c >> 1) + 1] = pack_bf16x2(e2, e3);
-            }
-            tmem_st16(KEYS ? tP + kCols / 2 : tP, o);
-            tmem_wait_st();
+            if (!any) continue;
             tc_fence_before();
-            warp_arrive(smem_u32(&bar->ds_ready[sb.st]), lane);
-            s2.next();
-            sb.next();
-        }
-        if (any) {
-            bar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a);
-            tc_fence_after();
-        }
-        // rows without a gradient hold whatever their padding made: zero. The
-        // stationary tiles have been used up: their places take the results
-        const bool live = any && (KEYS ? x < sp.lk : kend > 0);
-        const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
-        const int lr = (warp & 3) * 32 + lane;
-#pragma unroll
-        for (int k = 0; k < (KEYS ? 2 : 1); k++) {
-            const float f = k == 0 ? a.scale : 1.f;
-#pragma unroll
-            for (int c = w * 16; c < D; c += 64) {
-                float o[16];
-                if (any) tmem_ld16(tbase + C::TM_ACC + k * D + c + lanes, o);
-#pragma unroll
-                for (int i = 0; i < 16; i++) o[i] = live ? o[i] * f : 0.f;
-                if (a.splits == 1) {
-                    unsigned char* region = sX + k * C::TILE + (c / 64) * C::REGION;
-                    put_chunk(region, lr, w * 2, o);
-                    put_chunk(region, lr, w * 2 + 1, o + 8);
-                } else if (x < extent) {
-                    float* dst = a.part + ((k * a.splits + part) * all + row) * a.d + c;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4)
-                        if (c + i < a.d) store4(dst + i, o + i);
+            warp_arrive(smem_u32(&bar->acc_free), lane);
+            if (a.splits == 1) {
+                fence_async_smem();
+                named_barrier(1 + (warp & 3), 128);  // the four warps of these 32 rows
+                if (storer && x < extent) {
+                    for (int k = 0; k < (KEYS ? 2 : 1); k++)
+                        for (int c = 0; c < D / 64; c++)
+                            tma_store_3d(k == 0 ? &mz1 : &mz2, smem_u32(out + k * C::TILE + c * C::REGION + lr * 128), c * 64, x,
+                                         pc.slice);
+                    bulk_commit();
                 }
             }
+            v++;
+            storing = true;
+            if (C::NX == 1) stored();
         }
-        if (a.splits == 1) {
-            fence_async_smem();
-            named_barrier(1 + (warp & 3), 128);  // the four warps of these 32 rows
-            if (w == 0 && lane == 0 && x < extent) {
-                for (int k = 0; k < (KEYS ? 2 : 1); k++)
-                    for (int c = 0; c < D / 64; c++)
-                        tma_store_3d(k == 0 ? &mz1 : &mz2, smem_u32(sX + k * C::TILE + c * C::REGION + lr * 128), c * 64, x,
-                                     slice);
-                bulk_commit();
-                bulk_wait_read();
-            }
-        }
+        stored();
     }
     tc_fence_before();
     __syncthreads();
@@ -467,7 +557,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
 }
 
 template <int D, bool KEYS>
-int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     using C = Cfg<D, KEYS>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
     CUtensorMap mq, mk, mv, mg, z1, z2;
@@ -479,9 +569,10 @@ int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
     LLSA_TRY(make_tmap_rows(&z2, KEYS ? a.dv : a.dq, s.slices, KEYS ? s.nk : s.R, s.d, 32));
     cudaFuncSetAttribute(dense_bwd_tc_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const int extent = KEYS ? s.nk : s.R;
-    const long long blocks = (long long)((extent + BT - 1) / BT) * s.slices;
-    if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks, a.splits);
+    const long long pieces = (long long)((extent + BT - 1) / BT) * s.slices * a.splits;
+    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    a.pieces = (int)pieces;
+    const int grid = C::NX > 1 ? (int)std::min<long long>(pieces, sm_count()) : (int)pieces;
     if constexpr (KEYS)
         LLSA_LAUNCH("dense_dkv_tc", st,
                     dense_bwd_tc_kernel<D, true><<<grid, kThreads, C::SMEM, st>>>(mk, mv, mq, mg, z1, z2, a));

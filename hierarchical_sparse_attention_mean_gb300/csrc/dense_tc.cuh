@@ -19,6 +19,30 @@ __device__ __forceinline__ bool warp_wait(uint32_t mbar, uint32_t parity, volati
     return __all_sync(0xffffffffu, bar_wait(mbar, parity, abort_flag, a));
 }
 
+// The lane of a warp that issues, chosen once per role: 1 in that lane, 0 elsewhere.
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t r;
+    asm volatile("{\n.reg .pred e;\nelect.sync _|e, 0xffffffff;\nselp.u32 %0, 1, 0, e;\n}\n" : "=r"(r));
+    return r;
+}
+
+// MMAs and commits of a converged warp, issued by the chosen lane.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n.reg .pred p, e;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 e, %5, 0;\n"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader));
+}
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t mbar) {
+    asm volatile("{\n.reg .pred e;\nsetp.ne.b32 e, %1, 0;\n"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n"
+                 :: "r"(mbar), "r"(leader) : "memory");
+}
+
 // One arrival for the whole warp, after what all its lanes did.
 __device__ __forceinline__ void warp_arrive(uint32_t mbar, int lane) {
     __syncwarp();
