@@ -28,10 +28,8 @@
 // multiply for the next. At 128 columns shared memory holds one pair of
 // stationary tiles, and every piece gets a block of its own.
 //
-// Roles: warps 0-15 elementwise and epilogue, warp 16 issues S and dP, warp 17
-// the sums, warps 18 and 19 the copies of the two streams. Waits and the issue of a
-// dozen MMAs add up to some thousand clocks per item, so one warp for all of them
-// would be what the kernel waits for.
+// Roles: warps 0-15 elementwise and epilogue, warps 16 and 17 issue the MMAs,
+// warps 18 and 19 the copies of the two streams.
 #include <algorithm>
 
 #include "dense_tc.cuh"
@@ -237,12 +235,18 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 for (int x = max(0, v - C::NX); x < v; x++) land(smem_u32(&bar->x_full[k][x % C::NX]), (x / C::NX) & 1);
                 for (int x = max(0, n - ns); x < n; x++) land(smem_u32(&full[x % ns]), (x / ns) & 1);
             }
-        } else if (warp == kWarps) {
-            // --------------------------------------------------- S and dP issuer
+        } else {
+            // ----------------------------------------------------- MMA issuers
+            // With two dP buffers warp kWarps issues S and dP, the next warp the
+            // sums. With one, dP of the next item goes where this item's P and
+            // dS are, so one warp issues all, dP right behind the sums that use
+            // those up.
             const uint32_t leader = elect_lane();
-            constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0);
+            constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, D, 0, 1);
             const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024);
             const uint64_t dY1 = desc_sw128(smem_u32(ring1), 16, 1024), dY2 = desc_sw128(smem_u32(ring2), 16, 1024);
+            const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the tiles read along their rows
+            const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
             // Rows of the streamed tile whose P and dS are 0 by the mask of the
             // lengths may hold anything: they meet those zeros in the sums, so
             // they are cleared.
@@ -265,106 +269,111 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 fence_async_smem();
                 __syncwarp();
             };
-            bool ok = true;
-            Stage<C::N1> s1;
-            Stage<C::N2> s2;
-            Stage<C::NB> sb;
+            // stages and buffers of the next S (s1), dP (s2, sb) and sums (t1, t2, tb)
+            Stage<C::N1> s1, t1;
+            Stage<C::N2> s2, t2;
+            Stage<C::NB> sb, tb;
             Stage<C::NX> sx;
-            uint32_t n = 0;
+            uint32_t n = 0, nd = 0;  // S and dP issued
+            int v = 0;
+            uint64_t dX1 = 0, dX2 = 0;
+            auto take_x = [&]() {
+                dX1 = dX + (2 * sx.st * C::TILE >> 4);
+                dX2 = dX1 + (C::TILE >> 4);
+                return warp_wait(smem_u32(&bar->x_full[0][sx.st]), sx.parity, abort_flag, a) &&
+                       warp_wait(smem_u32(&bar->x_full[1][sx.st]), sx.parity, abort_flag, a);
+            };
+            auto issue_S = [&](const Items<KEYS>& it) {
+                if (!warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a)) return false;
+                clear_rows(ring1 + s1.st * C::TILE, it);
+                if (n > 0 && !warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a)) return false;
+                tc_fence_after();
+                const uint64_t dT = dY1 + (s1.st * C::TILE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                    mma_ss(leader, tbase, dX1 + (off >> 4), dT + (off >> 4), idS, ks > 0);
+                }
+                commit(leader, smem_u32(&bar->s_full));
+                s1.next();
+                n++;
+                return true;
+            };
+            auto issue_dP = [&](const Items<KEYS>& it) {
+                if (!warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a)) return false;
+                if (KEYS) clear_rows(ring2 + s2.st * C::TILE, it);  // V only enters dP, which the mask covers
+                if (C::NB > 1 && nd >= C::NB && !warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a))
+                    return false;
+                tc_fence_after();
+                const uint64_t dT = dY2 + (s2.st * C::TILE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ks++) {
+                    const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
+                    mma_ss(leader, tbase + C::TM_DP + sb.st * 128, dX2 + (off >> 4), dT + (off >> 4), idS, ks > 0);
+                }
+                commit(leader, smem_u32(&bar->dp_full[sb.st]));
+                if (!KEYS) commit(leader, smem_u32(&bar->y2_empty[s2.st]));
+                s2.next();
+                sb.next();
+                nd++;
+                return true;
+            };
+            auto issue_sums = [&](bool fresh) {
+                if (!warp_wait(smem_u32(&bar->ds_ready[tb.st]), tb.parity, abort_flag, a)) return false;
+                tc_fence_after();
+                const uint32_t p0 = tbase + C::TM_DP + tb.st * 128;
+                const uint64_t dT1 = dM1 + (t1.st * C::TILE >> 4), dT2 = dM2 + (t2.st * C::TILE >> 4);
+#pragma unroll
+                for (int ks = 0; ks < BT / 16; ks++) {
+                    const uint32_t op = p0 + (ks / 2) * 32 + (ks % 2) * 8;  // of every 32 columns: P, then dS, 16 words each
+                    if constexpr (KEYS) {
+                        mma_ts(leader, tbase + C::TM_ACC + D, op, dT2 + (ks * 2048 >> 4), idA, !fresh || ks > 0);
+                        mma_ts(leader, tbase + C::TM_ACC, op + 16, dT1 + (ks * 2048 >> 4), idA, !fresh || ks > 0);
+                    } else {
+                        mma_ts(leader, tbase + C::TM_ACC, op, dT1 + (ks * 2048 >> 4), idA, !fresh || ks > 0);
+                    }
+                }
+                if (C::NB > 1) commit(leader, smem_u32(&bar->dp_free[tb.st]));
+                commit(leader, smem_u32(&bar->y1_empty[t1.st]));
+                if (KEYS) commit(leader, smem_u32(&bar->y2_empty[t2.st]));
+                t1.next();
+                t2.next();
+                tb.next();
+                return true;
+            };
+            bool ok = C::NB > 1 || warp == kWarps;
             Piece<KEYS> pc = start;
             for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
                 if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
                 Items<KEYS> it = pc.items(a);
                 if (it.done()) continue;
-                ok = warp_wait(smem_u32(&bar->x_full[0][sx.st]), sx.parity, abort_flag, a) &&
-                     warp_wait(smem_u32(&bar->x_full[1][sx.st]), sx.parity, abort_flag, a);
-                const uint64_t dX1 = dX + (2 * sx.st * C::TILE >> 4), dX2 = dX1 + (C::TILE >> 4);
-                for (; ok && !it.done(); it.next(a), n++) {
-                    ok = warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a);
-                    if (!ok) break;
-                    clear_rows(ring1 + s1.st * C::TILE, it);
-                    if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dT1 = dY1 + (s1.st * C::TILE >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ks++) {
-                        const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                        mma_ss(leader, tbase, dX1 + (off >> 4), dT1 + (off >> 4), idS, ks > 0);
+                if (C::NB > 1 && warp == kWarps) {
+                    ok = take_x();
+                    for (; ok && !it.done(); it.next(a)) ok = issue_S(it) && issue_dP(it);
+                } else if (C::NB > 1) {
+                    if (v > 0) ok = warp_wait(smem_u32(&bar->acc_free), (v - 1) & 1, abort_flag, a);
+                    for (bool fresh = true; ok && !it.done(); it.next(a), fresh = false) ok = issue_sums(fresh);
+                    if (ok) commit(leader, smem_u32(&bar->acc_full));
+                } else {
+                    ok = take_x() && issue_S(it) && issue_dP(it);
+                    if (ok && v > 0) ok = warp_wait(smem_u32(&bar->acc_free), (v - 1) & 1, abort_flag, a);
+                    it.next(a);
+                    for (bool fresh = true; ok; fresh = false) {
+                        const bool more = !it.done();
+                        if (more) ok = issue_S(it);
+                        ok = ok && issue_sums(fresh);
+                        if (!more) break;
+                        ok = ok && issue_dP(it);
+                        it.next(a);
                     }
-                    commit(leader, smem_u32(&bar->s_full));
-                    ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
-                    if (!ok) break;
-                    if (KEYS) clear_rows(ring2 + s2.st * C::TILE, it);  // V only enters dP, which the mask covers
-                    if (n >= C::NB) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t dT2 = dY2 + (s2.st * C::TILE >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < D / 16; ks++) {
-                        const uint32_t off = (ks / 4) * C::REGION + (ks % 4) * 32;
-                        mma_ss(leader, tbase + C::TM_DP + sb.st * 128, dX2 + (off >> 4), dT2 + (off >> 4), idS,
-                                      ks > 0);
-                    }
-                    commit(leader, smem_u32(&bar->dp_full[sb.st]));
-                    if (!KEYS) commit(leader, smem_u32(&bar->y2_empty[s2.st]));
-                    s1.next();
-                    s2.next();
-                    sb.next();
+                    if (ok) commit(leader, smem_u32(&bar->acc_full));
                 }
                 sx.next();
-            }
-            // no MMA may be in flight when tensor memory is released
-            commit(leader, smem_u32(&bar->drain[0]));
-            if (lane == 0) land(smem_u32(&bar->drain[0]), 0);
-            __syncwarp();
-        } else if (warp == kWarps + 1) {
-            // ------------------------------------------------------- sums issuer
-            const uint32_t leader = elect_lane();
-            constexpr uint32_t idA = idesc_bf16(BT, D, 0, 1);
-            const uint64_t dM1 = desc_sw128(smem_u32(ring1), C::REGION, 1024);  // the tiles read along their rows
-            const uint64_t dM2 = desc_sw128(smem_u32(ring2), C::REGION, 1024);
-            bool ok = true;
-            Stage<C::N1> s1;
-            Stage<C::N2> s2;
-            Stage<C::NB> sb;
-            int v = 0;
-            Piece<KEYS> pc = start;
-            for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
-                if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
-                Items<KEYS> it = pc.items(a);
-                if (it.done()) continue;
-                if (v > 0) ok = warp_wait(smem_u32(&bar->acc_free), (v - 1) & 1, abort_flag, a);
-                uint32_t n = 0;
-                for (; ok && !it.done(); it.next(a), n++) {
-                    ok = warp_wait(smem_u32(&bar->ds_ready[sb.st]), sb.parity, abort_flag, a);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t p0 = tbase + C::TM_DP + sb.st * 128;
-                    const uint64_t dT1 = dM1 + (s1.st * C::TILE >> 4), dT2 = dM2 + (s2.st * C::TILE >> 4);
-#pragma unroll
-                    for (int ks = 0; ks < BT / 16; ks++) {
-                        const uint32_t op = p0 + (ks / 2) * 32 + (ks % 2) * 8;  // each quarter of the columns: P, then dS, 16 columns each
-                        const uint64_t m1 = dT1 + (ks * 2048 >> 4), m2 = dT2 + (ks * 2048 >> 4);
-                        if constexpr (KEYS) {
-                            mma_ts(leader, tbase + C::TM_ACC + D, op, m2, idA, n > 0 || ks > 0);
-                            mma_ts(leader, tbase + C::TM_ACC, op + 16, m1, idA, n > 0 || ks > 0);
-                        } else {
-                            mma_ts(leader, tbase + C::TM_ACC, op, m1, idA, n > 0 || ks > 0);
-                        }
-                    }
-                    commit(leader, smem_u32(&bar->dp_free[sb.st]));
-                    commit(leader, smem_u32(&bar->y1_empty[s1.st]));
-                    if (KEYS) commit(leader, smem_u32(&bar->y2_empty[s2.st]));
-                    s1.next();
-                    s2.next();
-                    sb.next();
-                }
-                if (ok) commit(leader, smem_u32(&bar->acc_full));
                 v++;
             }
-            commit(leader, smem_u32(&bar->drain[1]));
-            if (lane == 0) land(smem_u32(&bar->drain[1]), 0);
+            // no MMA may be in flight when tensor memory is released
+            commit(leader, smem_u32(&bar->drain[warp - kWarps]));
+            if (lane == 0) land(smem_u32(&bar->drain[warp - kWarps]), 0);
             __syncwarp();
         }
     } else {
