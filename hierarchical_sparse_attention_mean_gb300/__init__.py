@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -200,22 +201,28 @@ class DenseParams:
     scale: float = 0.0         # 0: 1/sqrt(d)
 
     def __post_init__(self):
-        object.__setattr__(self, "_c", _DenseParams(
-            self.batch, self.heads, self.kv_heads, self.nq, self.nk, self.d, _choice(_DTYPES, self.dtype, "dtype"),
-            1 if self.causal else 0, self.scale))
+        c = _DenseParams(self.batch, self.heads, self.kv_heads, self.nq, self.nk, self.d,
+                         _choice(_DTYPES, self.dtype, "dtype"), 1 if self.causal else 0, self.scale)
+        self.__dict__.update(_c=c, _ref=ctypes.byref(c), _ws={})
 
     def c(self) -> _DenseParams:
         return self._c
 
     @staticmethod
-    def like(q, k, **kw) -> "DenseParams":
-        b, h, n, d = q.shape
-        return DenseParams(b, h, n, k.shape[2], d, kv_heads=k.shape[1], dtype=_dtype_name(q), **kw)
+    def like(q, k, causal: bool = False, scale: float = 0.0) -> "DenseParams":
+        """The parameters of a call on q and k (equal calls share one object)."""
+        return _dense_params(tuple(q.shape), tuple(k.shape), _dtype_name(q), bool(causal), float(scale))
 
     def shapes(self):
         """Shapes of q (and o, dout, dq), of k (and v, dk, dv) and of lse."""
         return ((self.batch, self.heads, self.nq, self.d),
                 (self.batch, self.kv_heads or self.heads, self.nk, self.d), (self.batch, self.heads, self.nq))
+
+
+@functools.lru_cache(maxsize=256)
+def _dense_params(q, k, dtype, causal, scale):
+    b, h, n, d = q
+    return DenseParams(b, h, n, k[2], d, kv_heads=k[1], causal=causal, dtype=dtype, scale=scale)
 
 
 @dataclass(frozen=True)
@@ -244,13 +251,17 @@ class RopeParams:
     def __post_init__(self):
         scaling, order = _choice(_ROPE_SCALINGS, self.scaling, "scaling"), _choice(_ORDERS, self.token_order, "token_order")
         layout, dt = _choice(_ROPE_LAYOUTS, self.layout, "layout"), _choice(_DTYPES, self.dtype, "dtype")
-        object.__setattr__(self, "_names", (layout, order, dt, scaling))
+        self.__dict__.update(_names=(layout, order, dt, scaling), _c={})
 
     def c(self, pos_batched: bool = False) -> _RopeParams:
-        layout, order, dt, scaling = self._names
-        return _RopeParams(self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width,
-                           order, self.pos_offset, 1 if pos_batched else 0, dt, scaling, self.orig_len, self.base, self.factor,
-                           self.low, self.high, self.amplitude)
+        got = self._c.get(pos_batched)
+        if got is None:
+            layout, order, dt, scaling = self._names
+            got = self._c[pos_batched] = _RopeParams(
+                self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width, order,
+                self.pos_offset, 1 if pos_batched else 0, dt, scaling, self.orig_len, self.base, self.factor, self.low,
+                self.high, self.amplitude)
+        return got
 
     @staticmethod
     def like(q, k=None, **kw) -> "RopeParams":
@@ -398,17 +409,18 @@ def llsa_bwd(p: Params, q, k, v, o, lse, dout, pyr, sel_idx, coarse_idx, col_ptr
 
 
 def _like(t, name, shape, dtype, device):
-    """Pointer of a contiguous tensor of exactly this shape, type and device."""
+    """Pointer of a contiguous tensor of exactly this shape and type on device number `device`."""
     import torch
-    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+    if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device
+            and t.is_contiguous()):
         return t.data_ptr()
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
     ptr = _ptr(t, name, dtype)
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     return ptr
 
 
@@ -422,12 +434,15 @@ def _on(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    return _HERE if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+    return _HERE if t.get_device() == torch._C._cuda_getDevice() else torch.cuda.device(t.device)
 
 
 def dense_workspace_bytes(p: DenseParams, op: int) -> int:
     """Workspace of llsa_dense_fwd (OP_DENSE_FWD) or llsa_dense_bwd (OP_DENSE_BWD)."""
-    return int(_load().llsa_dense_workspace_bytes(ctypes.byref(p.c()), op))
+    got = p._ws.get(op)
+    if got is None:
+        got = p._ws[op] = int(_load().llsa_dense_workspace_bytes(p._ref, op))
+    return got
 
 
 def _lens(p, q_len, k_len, device):
@@ -440,10 +455,10 @@ def llsa_dense_fwd(p: DenseParams, q, k, v, o, lse, q_len=None, k_len=None, ws=N
     """Dense attention: o and lse of q over k, v (llsa_dense_fwd of include/llsa.h)."""
     import torch
     with _on(q, "q"):
-        td, dev, (sq, sk, sl) = _tok_dtype(p), q.device, p.shapes()
-        ql, kl = _lens(p, q_len, k_len, dev)
+        td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws(ws)
-        _check(_load().llsa_dense_fwd(ctypes.byref(p.c()), _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
+        _check(_load().llsa_dense_fwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
                                       _like(v, "v", sk, td, dev), ql, kl, _like(o, "o", sq, td, dev),
                                       _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_dense_fwd")
 
@@ -452,33 +467,47 @@ def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None
     """Gradients of dense attention (llsa_dense_bwd of include/llsa.h)."""
     import torch
     with _on(q, "q"):
-        td, dev, (sq, sk, sl) = _tok_dtype(p), q.device, p.shapes()
-        ql, kl = _lens(p, q_len, k_len, dev)
+        td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws(ws)
-        _check(_load().llsa_dense_bwd(ctypes.byref(p.c()), _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
+        _check(_load().llsa_dense_bwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
                                       _like(v, "v", sk, td, dev), _like(o, "o", sq, td, dev),
                                       _like(lse, "lse", sl, torch.float32, dev), _like(dout, "dout", sq, td, dev), ql, kl,
                                       _like(dq, "dq", sq, td, dev), _like(dk, "dk", sk, td, dev),
                                       _like(dv, "dv", sk, td, dev), w, wb, _stream(stream)), "llsa_dense_bwd")
 
 
-def _strided(t, name, shape, dtype, device, out):
-    """Pointer of a [batch, heads, n, d] tensor whose columns are contiguous; its
-    batch, head and token strides go into `out`."""
+def _strided(t, name, shape, dtype, device):
+    """Pointer of a [batch, heads, n, d] tensor whose columns are contiguous, and
+    its batch, head and token strides (None: contiguous throughout)."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} must be on cuda:{device}, got {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
     s = t.stride()
     if s[3] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    out[:] = s[:3]
-    return t.data_ptr()
+    if not any(s[:3]):  # one row for all tokens: zeros mean contiguous to the library
+        raise ValueError(f"{name} must not be one row expanded over all tokens")
+    return t.data_ptr(), s[:3]
+
+
+def _rope_strides(views):
+    """The C structure of the strides of q, k, q_out, k_out; None where all are contiguous."""
+    if not any(views):
+        return None
+    st = _RopeStrides()
+    for field, s in zip((st.q, st.k, st.q_out, st.k_out), views):
+        if s is not None:
+            field[:] = s
+    return ctypes.byref(st)
 
 
 def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False, stream=None):
@@ -488,13 +517,15 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
     leading batch dimension. inverse: the negative angles (the gradient)."""
     import torch
     with _on(q, "q"):
-        td, dev, st = _tok_dtype(p), q.device, _RopeStrides()
+        td, dev = _tok_dtype(p), q.get_device()
         shape = (p.batch, p.heads, p.n, p.d)
-        a, c = _strided(q, "q", shape, td, dev, st.q), _strided(q_out, "q_out", shape, td, dev, st.q_out)
-        b = d = None
+        a, sa = _strided(q, "q", shape, td, dev)
+        c, sc = _strided(q_out, "q_out", shape, td, dev)
+        b = d = sb = sd = None
         if p.kv_heads:
             shape = (p.batch, p.kv_heads, p.n, p.d)
-            b, d = _strided(k, "k", shape, td, dev, st.k), _strided(k_out, "k_out", shape, td, dev, st.k_out)
+            b, sb = _strided(k, "k", shape, td, dev)
+            d, sd = _strided(k_out, "k_out", shape, td, dev)
         elif k is not None or k_out is not None:
             raise ValueError("k and k_out must be None where kv_heads is 0")
         at, batched = None, False
@@ -505,7 +536,7 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
             elif shape != (p.n, p.axes):
                 raise ValueError(f"pos must have shape [n, axes] or [batch, n, axes], got {tuple(pos.shape)}")
             at = _like(pos, "pos", pos.shape, torch.int32, dev)
-        _check(_load().llsa_rope(ctypes.byref(p.c(batched)), ctypes.byref(st), a, b, at, c, d, 1 if inverse else 0,
+        _check(_load().llsa_rope(p.c(batched), _rope_strides((sa, sb, sc, sd)), a, b, at, c, d, 1 if inverse else 0,
                                  _stream(stream)), "llsa_rope")
 
 
@@ -651,10 +682,10 @@ def backward(p: Params, q, k, v, dout, b: Buffers, dq=None, dk=None, dv=None, st
 
 def _dense_ws(p: DenseParams, op: int, device, stream):
     """The workspace of one call (None where it needs none), kept until `stream` is done with it."""
-    import torch
     need = dense_workspace_bytes(p, op)
     if need == 0:
         return None
+    import torch
     ws = torch.empty(need, dtype=torch.uint8, device=device)
     if stream is not None:
         ws.record_stream(_as_stream(stream, device))
@@ -693,8 +724,10 @@ def _check_rope(p: RopeParams, q, k, name="rope"):
 
 def _rope_view(t):
     """t, or a contiguous copy where its strides are none that llsa_rope takes."""
+    if t.is_contiguous() and t.data_ptr() % 16 == 0:
+        return t
     unit = 16 // t.element_size()
-    ok = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
+    ok = any(t.stride()[:3]) and t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
         t.stride(i) % unit == 0 for i in range(3) if t.shape[i] > 1)
     return t if ok else t.contiguous()
 

@@ -233,8 +233,9 @@ int check_rope(const llsa_rope_params* p, int has_pos) {
     return LLSA_OK;
 }
 
-// The strides of one tensor: the caller's, or the contiguous ones.
-int take_strides(const long long* given, const llsa_rope_params* p, int heads, long long* out) {
+// The strides of one tensor: the caller's, or the contiguous ones. An output's
+// rows must not lie over one another.
+int take_strides(const long long* given, const llsa_rope_params* p, int heads, bool output, long long* out) {
     const long long want = p->dtype == LLSA_DTYPE_BF16 ? 8 : 4;  // elements in 16 bytes
     if (!given || (given[0] == 0 && given[1] == 0 && given[2] == 0)) {
         out[0] = (long long)heads * p->n * p->d;
@@ -246,6 +247,7 @@ int take_strides(const long long* given, const llsa_rope_params* p, int heads, l
     for (int i = 0; i < 3; i++) {
         out[i] = extent[i] > 1 ? given[i] : 0;  // one entry: the stride is never walked
         if (out[i] % want != 0) return LLSA_ERR_ALIGN;
+        if (output && extent[i] > 1 && out[i] == 0) return LLSA_ERR_INVALID_ARG;
     }
     return LLSA_OK;
 }
@@ -302,10 +304,10 @@ extern "C" int llsa_rope(const llsa_rope_params* p, const llsa_rope_strides* str
     if (p->heads > 0) LLSA_TRY(check_ptrs({q, q_out}));
     if (p->kv_heads > 0) LLSA_TRY(check_ptrs({k, k_out}));
     if (pos && (reinterpret_cast<uintptr_t>(pos) & 3u)) return LLSA_ERR_ALIGN;
-    LLSA_TRY(take_strides(strides ? strides->q : nullptr, p, p->heads, a.in_stride[0]));
-    LLSA_TRY(take_strides(strides ? strides->k : nullptr, p, p->kv_heads, a.in_stride[1]));
-    LLSA_TRY(take_strides(strides ? strides->q_out : nullptr, p, p->heads, a.out_stride[0]));
-    LLSA_TRY(take_strides(strides ? strides->k_out : nullptr, p, p->kv_heads, a.out_stride[1]));
+    LLSA_TRY(take_strides(strides ? strides->q : nullptr, p, p->heads, false, a.in_stride[0]));
+    LLSA_TRY(take_strides(strides ? strides->k : nullptr, p, p->kv_heads, false, a.in_stride[1]));
+    LLSA_TRY(take_strides(strides ? strides->q_out : nullptr, p, p->heads, true, a.out_stride[0]));
+    LLSA_TRY(take_strides(strides ? strides->k_out : nullptr, p, p->kv_heads, true, a.out_stride[1]));
     // a tensor may be its own output only if every element goes back to its own place
     if (p->heads > 0 && q == q_out && memcmp(a.in_stride[0], a.out_stride[0], sizeof(a.in_stride[0])) != 0)
         return LLSA_ERR_INVALID_ARG;

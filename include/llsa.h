@@ -382,7 +382,8 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  *   strides      : element strides of batch, head and token; NULL, or three
  *                  zeros, stands for contiguous [batch, heads, n, d]. Columns are
  *                  contiguous; every stride that is used spans a multiple of
- *                  16 bytes (LLSA_ERR_ALIGN otherwise). */
+ *                  16 bytes (LLSA_ERR_ALIGN otherwise), and an output's are
+ *                  not 0 (LLSA_ERR_INVALID_ARG): its rows must not overlap. */
 enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };
 enum { LLSA_ROPE_SCALE_NONE = 0, LLSA_ROPE_SCALE_LINEAR = 1, LLSA_ROPE_SCALE_BASE = 2, LLSA_ROPE_SCALE_WAVELENGTH = 3 };
 

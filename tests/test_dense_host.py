@@ -133,6 +133,9 @@ def test_rope_pointers_and_strides_refused(lib):
     assert rope(lib, p, strides=ctypes.byref(st)) == ALIGN
     st.q[:] = [51200, 64, 512]       # in place, other strides: rows would overwrite rows not yet read
     assert rope(lib, p, ptrs=(16, 16), outs=(16, 32), strides=ctypes.byref(st)) == INVALID
+    st = llsa._RopeStrides()
+    st.q_out[:] = [25600, 0, 64]     # all heads into one
+    assert rope(lib, p, strides=ctypes.byref(st)) == INVALID
     assert rope(lib, llsa.RopeParams(0, 4, 100, 64), (None, None), outs=(None, None)) == 0
     assert rope(lib, llsa.RopeParams(2, 4, 0, 64), (None, None), outs=(None, None)) == 0
     assert lib.llsa_rope(None, None, 16, 16, None, 32, 32, 0, None) == INVALID

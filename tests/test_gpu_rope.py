@@ -145,6 +145,20 @@ def test_packed_projection_in_and_out(dtype):
     assert bool((bv[:, h + kv:] == 5.0).all())
 
 
+def test_broadcast_inputs():
+    """Rows shared by heads or batch entries are read in place; one row for all is copied first."""
+    x = rand((2, 1, 19, 64), "fp32", 21)
+    pos = torch.arange(19)[None, :, None]
+    q = x.cuda().expand(2, 3, 19, 64)
+    p = llsa.RopeParams.like(q)
+    ref.check("q", llsa.rotary(q, rope=p), ref.rotary(x.expand(2, 3, 19, 64), pos, dtype=torch.float32))
+    row = rand((64,), "fp32", 22)
+    one = row.cuda().expand(2, 3, 19, 64)
+    ref.check("one", llsa.rotary(one, rope=p), ref.rotary(row.expand(2, 3, 19, 64), pos, dtype=torch.float32))
+    with pytest.raises(ValueError, match="expanded"):
+        llsa.llsa_rope(p, one, None, torch.empty(2, 3, 19, 64, device="cuda"), None)
+
+
 def test_columns_behind_the_turned_ones_may_hold_anything():
     x = rand((1, 1, 8, 16), "bf16", 11)
     x[..., 6:] = float("inf")
