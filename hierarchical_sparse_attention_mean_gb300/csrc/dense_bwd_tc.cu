@@ -53,13 +53,14 @@ struct Cfg {
     static constexpr int NX = D == 64 ? 2 : 1;                        // pairs of stationary tiles
     static constexpr int NB = D == 128 && KEYS ? 1 : 2;               // dP buffers
     static constexpr int STATS = KEYS ? N2 * 2 * BT * 4 : 0;          // -l2 and -D of a row tile, with stream 2
-    static constexpr int SMEM = (2 * NX + N1 + N2) * TILE + STATS + 512;
+    static constexpr int SMEM = (2 * NX + N1 + N2) * TILE + STATS + 1024;
     static constexpr int TM_DP = 128, TM_ACC = 128 + NB * 128;        // S at column 0
 };
 
 struct Bars {
     uint64_t x_full[2][2], x_free[2], y1_full[4], y1_empty[4], y2_full[4], y2_empty[4];
     uint64_t s_full, s_free, dp_full[2], ds_ready[2], dp_free[2], acc_full, acc_free, drain[2];
+    PieceRing pieces;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -73,10 +74,11 @@ struct Items {
     bool all;           // no tile to skip, no row to clear
     DenseSpan sp;
 
-    __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int first, int end)
-        : pos(first), t0(0), stop(end), x0(x0_), all(!KEYS || (!a.causal && s.lq == a.nq)), sp(s) {
+    __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int pos_, int t0_, int end)
+        : pos(pos_), t0(t0_), stop(end), x0(x0_), all(!KEYS || (!a.causal && s.lq == a.nq)), sp(s) {}
+    __device__ __forceinline__ void start(const DenseArgs& a) {
         if (all) return;
-        t0 = first % a.nq;
+        t0 = pos % a.nq;
         settle(a);
     }
     __device__ __forceinline__ bool done() const { return pos >= stop; }
@@ -103,25 +105,47 @@ private:
 // One piece of work: 128 stationary rows of a slice against a part of the stream.
 template <bool KEYS>
 struct Piece {
-    int slice, x0, part, first, stop;
+    int slice, x0, part, pos, t0, stop;  // pos, t0: the first item
     DenseSpan sp;
 
-    __device__ __forceinline__ Piece(const DenseArgs& a, int id) {
+    __device__ __forceinline__ void make(const DenseArgs& a, int id) {
         const DenseWork w = dense_work(a, id, ((KEYS ? a.nk : a.R) + BT - 1) / BT);
         slice = w.slice;
         part = w.part;
         // causal order: the last rows see the most keys, the first keys the most rows; those come first
         x0 = (a.causal && !KEYS ? w.blocks - 1 - w.block : w.block) * BT;
         sp = dense_span(a, slice);
-        first = a.splits > 1 ? part * a.chunk : 0;
+        pos = a.splits > 1 ? part * a.chunk : 0;
         if constexpr (KEYS) {
-            stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
+            stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, pos + a.chunk) : a.R) : 0;
         } else {
             stop = dense_tile_kend(a, sp, x0 < a.nq ? x0 : x0 % a.nq, BT);
-            if (a.splits > 1) stop = min(stop, first + a.chunk);
+            if (a.splits > 1) stop = min(stop, pos + a.chunk);
         }
+        t0 = 0;
+        Items<KEYS> it = items(a);
+        it.start(a);
+        pos = it.pos;
+        t0 = it.t0;
     }
-    __device__ __forceinline__ Items<KEYS> items(const DenseArgs& a) const { return Items<KEYS>(a, sp, x0, first, stop); }
+    __device__ __forceinline__ Items<KEYS> items(const DenseArgs& a) const { return Items<KEYS>(a, sp, x0, pos, t0, stop); }
+    __device__ __forceinline__ bool put(PieceRing* ring, int i, volatile int* abort_flag, const DenseArgs& a) const {
+        return piece_put(ring, i, make_int4(slice, x0, part, pos), make_int4(t0, stop, sp.lq, sp.lk), abort_flag, a);
+    }
+    template <int LANES>
+    __device__ __forceinline__ bool get(PieceRing* ring, int i, int lane, volatile int* abort_flag, const DenseArgs& a) {
+        int4 x, y;
+        if (!piece_get<LANES>(ring, i, x, y, lane, abort_flag, a)) return false;
+        slice = x.x;
+        x0 = x.y;
+        part = x.z;
+        pos = x.w;
+        t0 = y.x;
+        stop = y.y;
+        sp.lq = y.z;
+        sp.lk = y.w;
+        return true;
+    }
 };
 
 template <int D, bool KEYS>
@@ -145,7 +169,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         return;
     }
     const int extent = KEYS ? a.nk : a.R;
-    const Piece<KEYS> start(a, blockIdx.x);  // worked out while the barriers and tensor memory come up
+    const int mine = (a.pieces - blockIdx.x + gridDim.x - 1) / gridDim.x;  // pieces blockIdx.x, + gridDim.x, ...
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
@@ -167,6 +191,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         mbar_init(smem_u32(&bar->s_free), kWarps);
         mbar_init(smem_u32(&bar->acc_full), 1);
         mbar_init(smem_u32(&bar->acc_free), kWarps);
+        piece_ring_init(&bar->pieces, kWarps + (C::NB > 1 ? 3 : 2));  // elementwise warps, issuers, the copies of stream 2
         bar->abort_flag = 0;
         fence_mbar_init();
     }
@@ -198,9 +223,15 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 int st = 0, n = 0, v = 0;
                 uint32_t parity = 1;  // of the release that the stage's next use waits for
                 bool ok = true;
-                Piece<KEYS> pc = start;
-                for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
-                    if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
+                for (int i = 0; ok && i < mine; i++) {
+                    Piece<KEYS> pc;
+                    if (k == 0) {
+                        pc.make(a, blockIdx.x + i * gridDim.x);
+                        ok = pc.put(&bar->pieces, i, abort_flag, a);
+                    } else {
+                        ok = pc.template get<1>(&bar->pieces, i, lane, abort_flag, a);
+                    }
+                    if (!ok) break;
                     Items<KEYS> it = pc.items(a);
                     if (it.done()) continue;
                     const int xb = v % C::NX;
@@ -342,9 +373,10 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 return true;
             };
             bool ok = C::NB > 1 || warp == kWarps;
-            Piece<KEYS> pc = start;
-            for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
-                if (id != blockIdx.x) pc = Piece<KEYS>(a, id);
+            for (int i = 0; ok && i < mine; i++) {
+                Piece<KEYS> pc;
+                ok = pc.template get<32>(&bar->pieces, i, lane, abort_flag, a);
+                if (!ok) break;
                 Items<KEYS> it = pc.items(a);
                 if (it.done()) continue;
                 if (C::NB > 1 && warp == kWarps) {
@@ -397,8 +429,9 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
             }
             storing = false;
         };
-        for (int id = blockIdx.x; id < a.pieces; id += gridDim.x) {
-            const Piece<KEYS> pc(a, id);
+        for (int i = 0; i < mine; i++) {
+            Piece<KEYS> pc;
+            if (!pc.template get<32>(&bar->pieces, i, lane, abort_flag, a)) break;
             const DenseSpan sp = pc.sp;
             const int x = pc.x0 + lr;  // stationary row
             uint64_t nl2x2 = 0, ndx2 = 0;
@@ -568,7 +601,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
 template <int D, bool KEYS>
 int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     using C = Cfg<D, KEYS>;
-    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
+    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
     CUtensorMap mq, mk, mv, mg, z1, z2;
     LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mg, a.dout, s.slices, s.R, s.d, BT));

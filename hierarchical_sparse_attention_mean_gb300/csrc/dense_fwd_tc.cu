@@ -47,7 +47,7 @@ struct Cfg {
     static constexpr int NQ = D == 64 ? 2 : 1;      // query tiles kept per row tile: the next piece's comes in early
     static constexpr bool APART = D == 64;          // P beside S
     static constexpr int HALVES = APART ? 1 : 2;    // parts in which P is handed over
-    static constexpr int SMEM = 1024 + (2 * NQ + 2 * STAGES) * TILE + 512;
+    static constexpr int SMEM = 1024 + (2 * NQ + 2 * STAGES) * TILE + 1024;
     // tensor-memory columns: S of row tile w at 128 w
     static constexpr int TM_P = APART ? 256 : 0, P_STEP = APART ? 64 : 128, TM_O = APART ? 384 : 256;
 };
@@ -55,6 +55,7 @@ struct Cfg {
 struct Bars {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], q_full[2][2], q_free[2][2];
     uint64_t s_full[2], s_free[2], p_full[2][2], o_done[2], o_free[2], drain[2];
+    PieceRing pieces;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -63,11 +64,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 
 // One piece of work: 256 query rows of a slice against a part of its keys.
 struct Piece {
-    int slice, r0, part, j_first;
-    int n[2], nt;  // key tiles of each row tile, and of both
+    int slice, r0, part, j_first, n[2], nt;  // n: key tiles of each row tile, nt: of both
     DenseSpan sp;
 
-    __device__ __forceinline__ Piece(const DenseArgs& a, int id) {
+    __device__ __forceinline__ void make(const DenseArgs& a, int id) {
         const DenseWork w = dense_work(a, id, (a.R + 2 * BM - 1) / (2 * BM));
         slice = w.slice;
         part = w.part;
@@ -83,6 +83,24 @@ struct Piece {
             n[w] = end > j_first ? (end - j_first + BN - 1) / BN : 0;
         }
         nt = max(n[0], n[1]);
+    }
+    __device__ __forceinline__ bool put(PieceRing* ring, int i, volatile int* abort_flag, const DenseArgs& a) const {
+        return piece_put(ring, i, make_int4(slice, r0, part, j_first), make_int4(n[0], n[1], sp.lq, sp.lk), abort_flag, a);
+    }
+    template <int LANES>
+    __device__ __forceinline__ bool get(PieceRing* ring, int i, int lane, volatile int* abort_flag, const DenseArgs& a) {
+        int4 x, y;
+        if (!piece_get<LANES>(ring, i, x, y, lane, abort_flag, a)) return false;
+        slice = x.x;
+        r0 = x.y;
+        part = x.z;
+        j_first = x.w;
+        n[0] = y.x;
+        n[1] = y.y;
+        nt = max(n[0], n[1]);
+        sp.lq = y.z;
+        sp.lk = y.w;
+        return true;
     }
 };
 
@@ -102,7 +120,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     // broadcast, so that the compiler knows these as the same in a whole warp
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    const Piece first(a, blockIdx.x);  // worked out while the barriers and tensor memory come up
+    const int mine = (a.pieces - blockIdx.x + gridDim.x - 1) / gridDim.x;  // pieces blockIdx.x, + gridDim.x, ...
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; i++) {
             mbar_init(smem_u32(&bar->k_full[i]), 1);
@@ -122,6 +140,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             mbar_init(smem_u32(&bar->o_free[w]), 4);
             mbar_init(smem_u32(&bar->drain[w]), 1);
         }
+        piece_ring_init(&bar->pieces, C::APART ? 11 : 10);  // softmax warps, issuers, the copies of V
         bar->abort_flag = 0;
         fence_mbar_init();
     }
@@ -153,9 +172,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 Stage<C::STAGES> s;
                 int filled = 0, v[2] = {0, 0};
                 bool ok = true;
-                Piece pc = first;
-                for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
-                    if (id != blockIdx.x) pc = Piece(a, id);
+                for (int i = 0; ok && i < mine; i++) {
+                    Piece pc;
+                    if (keys) {
+                        pc.make(a, blockIdx.x + i * gridDim.x);
+                        ok = pc.put(&bar->pieces, i, abort_flag, a);
+                    } else {
+                        ok = pc.get<1>(&bar->pieces, i, lane, abort_flag, a);
+                    }
                     if (keys)
 #pragma unroll
                         for (int w = 0; w < 2; w++) {
@@ -215,9 +239,10 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                     }
                     commit(leader, smem_u32(&bar->s_full[w]));
                 };
-                Piece pc = first;
-                for (int id = blockIdx.x; ok && id < a.pieces; id += gridDim.x) {
-                    if (id != blockIdx.x) pc = Piece(a, id);
+                for (int i = 0; ok && i < mine; i++) {
+                    Piece pc;
+                    ok = pc.get<32>(&bar->pieces, i, lane, abort_flag, a);
+                    if (!ok) break;
                     // key tile t: its S (APART), or its O and the S of tile t + 1
                     for (int t = C::APART ? 0 : -1; ok && t < pc.nt; t++) {
                         const int ts = C::APART ? t : t + 1;  // tile of S
@@ -307,8 +332,9 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             }
             storing = false;
         };
-        for (int id = blockIdx.x; id < a.pieces; id += gridDim.x) {
-            const Piece pc(a, id);
+        for (int i = 0; i < mine; i++) {
+            Piece pc;
+            if (!pc.get<32>(&bar->pieces, i, lane, abort_flag, a)) break;
             const int n = w == 0 ? pc.n[0] : pc.n[1];
             const int r = pc.r0 + w * BM + lr;
             const int kend = r < a.R ? dense_kend(a, pc.sp, r % a.nq) : 0;
@@ -329,7 +355,10 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 const int lim = kend - (pc.j_first + t * BN);
                 if (__any_sync(0xffffffffu, lim < BN)) {
 #pragma unroll
-                    for (int c = 0; c < 128; c++) s[c] = c < lim ? s[c] : 0xff800000u;
+                    for (int q = 0; q < 128; q += 32)
+                        if (__any_sync(0xffffffffu, lim < q + 32))
+#pragma unroll
+                            for (int c = q; c < q + 32; c++) s[c] = c < lim ? s[c] : 0xff800000u;
                 }
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -460,7 +489,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
 template <int D>
 int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     using C = Cfg<D>;
-    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
+    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
     CUtensorMap mq, mk, mv, mo;
     LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BM));
     LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BN));

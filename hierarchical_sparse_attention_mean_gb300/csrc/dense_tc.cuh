@@ -79,5 +79,47 @@ struct Stage {
     }
 };
 
+// The pieces of a resident block, worked out by one copying thread (divisions and
+// loads of the lengths: some 1,500 clocks) ahead of the roles that read them.
+constexpr int kPieceSlots = 4;
+
+struct PieceRing {
+    int4 slot[kPieceSlots][2];
+    uint64_t full[kPieceSlots], free[kPieceSlots];
+};
+
+// One thread.
+__device__ __forceinline__ void piece_ring_init(PieceRing* r, int readers) {
+    for (int i = 0; i < kPieceSlots; i++) {
+        mbar_init(smem_u32(&r->full[i]), 1);
+        mbar_init(smem_u32(&r->free[i]), readers);
+    }
+}
+
+// The writing thread: piece number i.
+__device__ __forceinline__ bool piece_put(PieceRing* r, int i, int4 x, int4 y, volatile int* abort_flag, const DenseArgs& a) {
+    const int s = i % kPieceSlots, use = i / kPieceSlots;
+    if (use > 0 && !bar_wait(smem_u32(&r->free[s]), (use - 1) & 1, abort_flag, a)) return false;
+    r->slot[s][0] = x;
+    r->slot[s][1] = y;
+    mbar_arrive(smem_u32(&r->full[s]));
+    return true;
+}
+
+// A reading warp (`lanes` 32) or thread (1): piece number i; one arrival per reader.
+template <int LANES>
+__device__ __forceinline__ bool piece_get(PieceRing* r, int i, int4& x, int4& y, int lane, volatile int* abort_flag,
+                                          const DenseArgs& a) {
+    const int s = i % kPieceSlots;
+    const bool ok = LANES == 32 ? warp_wait(smem_u32(&r->full[s]), (i / kPieceSlots) & 1, abort_flag, a)
+                                : bar_wait(smem_u32(&r->full[s]), (i / kPieceSlots) & 1, abort_flag, a);
+    if (!ok) return false;
+    x = r->slot[s][0];
+    y = r->slot[s][1];
+    if (LANES == 32) warp_arrive(smem_u32(&r->free[s]), lane);
+    else mbar_arrive(smem_u32(&r->free[s]));
+    return true;
+}
+
 }  // namespace tc
 }  // namespace llsa
