@@ -39,6 +39,7 @@ struct DenseArgs {
     float* part;  // partial sums of a split axis (layout: see the kernels)
     int splits, chunk;  // parts of the split axis, and how many of its elements each takes
     int pieces;         // pieces of work that the resident blocks share (tensor-core kernels)
+    int whole;          // of them, those before the halved ones (forward)
     int slices, kv_heads, nq, nk, R, Rp, d, causal;
     float scale;
     int* status;

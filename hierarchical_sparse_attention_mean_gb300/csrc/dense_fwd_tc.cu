@@ -62,17 +62,19 @@ struct Bars {
 
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
-// One piece of work: 256 query rows of a slice against a part of its keys.
+// One piece of work: 256 query rows of a slice against a part of its keys, or
+// 128 of them where halves fill a round of blocks better.
 struct Piece {
-    int slice, r0, part, j_first, n[2], nt;  // n: key tiles of each row tile, nt: of both
+    int slice, r0, part, j_first, n[2], nt;  // n: key tiles of each row tile (-1: not there), nt: of both
     DenseSpan sp;
 
     __device__ __forceinline__ void make(const DenseArgs& a, int id) {
-        const DenseWork w = dense_work(a, id, (a.R + 2 * BM - 1) / (2 * BM));
+        const bool half = id >= a.whole;
+        const DenseWork w = dense_work(a, half ? a.whole + (id - a.whole) / 2 : id, (a.R + 2 * BM - 1) / (2 * BM));
         slice = w.slice;
         part = w.part;
         // causal order gives the last rows the most keys: those come first
-        r0 = (a.causal ? w.blocks - 1 - w.block : w.block) * 2 * BM;
+        r0 = (a.causal ? w.blocks - 1 - w.block : w.block) * 2 * BM + (half ? ((id - a.whole) & 1) * BM : 0);
         sp = dense_span(a, slice);
         j_first = part * a.chunk;
         const int j_stop = a.splits > 1 ? j_first + a.chunk : a.nk;
@@ -82,6 +84,7 @@ struct Piece {
             const int end = row < a.R ? min(dense_tile_kend(a, sp, row < a.nq ? row : row % a.nq, BM), j_stop) : 0;
             n[w] = end > j_first ? (end - j_first + BN - 1) / BN : 0;
         }
+        if (half) n[1] = -1;
         nt = max(n[0], n[1]);
     }
     __device__ __forceinline__ bool put(PieceRing* ring, int i, volatile int* abort_flag, const DenseArgs& a) const {
@@ -324,23 +327,29 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
         const float sl2 = a.scale * kDenseLog2e;
         const uint64_t sl2x2 = pack2(sl2, sl2);
         int u = 0, v = 0;
-        bool storing = false;  // this warp's last results are on their way out of query buffer (v - 1) % NQ
-        auto stored = [&]() {
-            if (lane == 0 && storing) {
+        auto stored = [&]() {  // the last results have left query buffer (v - 1) % NQ
+            if (lane == 0) {
                 bulk_wait_read();
                 mbar_arrive(smem_u32(&bar->q_free[w][(v - 1) % C::NQ]));
             }
-            storing = false;
         };
         for (int i = 0; i < mine; i++) {
-            Piece pc;
-            if (!pc.get<32>(&bar->pieces, i, lane, abort_flag, a)) break;
-            const int n = w == 0 ? pc.n[0] : pc.n[1];
-            const int r = pc.r0 + w * BM + lr;
-            const int kend = r < a.R ? dense_kend(a, pc.sp, r % a.nq) : 0;
+            // what only the epilogue needs is read again there: the registers hold a row of S
+            const int slot = i % kPieceSlots;
+            if (!warp_wait(smem_u32(&bar->pieces.full[slot]), (i / kPieceSlots) & 1, abort_flag, a)) break;
+            const int4 head = bar->pieces.slot[slot][0], tail = bar->pieces.slot[slot][1];
+            const int n = w == 0 ? tail.x : tail.y;
+            int lim;  // keys that this row sees from the current tile on
+            {
+                const int r = head.y + w * BM + lr;
+                DenseSpan sp;
+                sp.lq = tail.z;
+                sp.lk = tail.w;
+                lim = (r < a.R ? dense_kend(a, sp, r < a.nq ? r : r % a.nq) : 0) - head.w;
+            }
             float m = -INFINITY;
             uint64_t l4[2] = {0ull, 0ull};  // the row's sum in four parts
-            for (int t = 0; t < n; t++, u++) {
+            for (int t = 0; t < n; t++, u++, lim -= BN) {
                 bar_wait(smem_u32(&bar->s_full[w]), u & 1, abort_flag, a);
                 tc_fence_after();
                 uint32_t s[128];
@@ -351,8 +360,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                     tc_fence_before();
                     warp_arrive(smem_u32(&bar->s_free[w]), lane);
                 }
-                if (t == 0) stored();
-                const int lim = kend - (pc.j_first + t * BN);
+                if (C::NQ > 1 && t == 0 && v > 0) stored();
                 if (__any_sync(0xffffffffu, lim < BN)) {
 #pragma unroll
                     for (int q = 0; q < 128; q += 32)
@@ -416,7 +424,11 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             unpack2(l4[1], l2, l3);
             const float l = (l0 + l1) + (l2 + l3);
             const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
-            const long long row = (long long)pc.slice * a.R + r, prow = (long long)pc.part * a.slices * a.R + row;
+            const int4 piece = bar->pieces.slot[slot][0];  // slice, first row, part
+            const int r = piece.y + w * BM + lr;
+            const long long row = (long long)piece.x * a.R + r, prow = (long long)piece.z * a.slices * a.R + row;
+            warp_arrive(smem_u32(&bar->pieces.free[slot]), lane);
+            if (n < 0) continue;  // half a piece: the other half's rows
             if (r < a.R) {
                 if (a.splits > 1)
                     reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
@@ -468,15 +480,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 __syncwarp();
                 if (lane == 0 && r < a.R) {
                     for (int c = 0; c < D / 64; c++)
-                        tma_store_3d(&mo, smem_u32(out + c * C::REGION + lr * 128), c * 64, r, pc.slice);
+                        tma_store_3d(&mo, smem_u32(out + c * C::REGION + lr * 128), c * 64, r, piece.x);
                     bulk_commit();
                 }
             }
             v++;
-            storing = true;
             if (C::NQ == 1) stored();  // the next query tile waits for the place
         }
-        stored();
+        if (C::NQ > 1 && v > 0) stored();
     }
     tc_fence_before();
     __syncthreads();
@@ -496,8 +507,13 @@ int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     LLSA_TRY(make_tmap_rows(&mv, a.v, s.slices, s.nk, s.d, BN));
     LLSA_TRY(make_tmap_rows(&mo, a.o_out, s.slices, s.R, s.d, 32));
     cudaFuncSetAttribute(dense_fwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    const long long pieces = (long long)((s.R + 2 * BM - 1) / (2 * BM)) * s.slices * a.splits;
-    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    long long pieces = (long long)((s.R + 2 * BM - 1) / (2 * BM)) * s.slices * a.splits;
+    if (pieces > kDenseMaxPieces / 2) return LLSA_ERR_UNSUPPORTED;
+    // A last round that leaves half of the SMs idle is dealt out in halves: a row
+    // tile alone takes about 3/4 of the time of two.
+    const long long rest = pieces % kDenseSms;
+    a.whole = (int)(2 * rest <= kDenseSms && a.splits == 1 ? pieces - rest : pieces);
+    pieces += pieces - a.whole;
     a.pieces = (int)pieces;
     // At 128 columns there is one query tile per row tile, so a resident block would wait for its next one:
     // a block per piece there (12 heads x 4,096 tokens 105 us against 107; at 64 columns 74 against 70).
@@ -513,7 +529,7 @@ bool dense_tc_supported(const DenseShape& s) {
 }
 
 DenseSplit dense_tc_fwd_split(const DenseShape& s) {
-    return dense_make_split((long long)s.slices * ((s.R + 2 * BM - 1) / (2 * BM)), s.nk, BN, 2);
+    return dense_make_split((long long)s.slices * ((s.R + 2 * BM - 1) / (2 * BM)), s.nk, BN, 8);
 }
 
 int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
