@@ -170,7 +170,7 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
 }
 
 DenseSplit fwd_split(const DenseShape& s) {
-    return dense_tc_supported(s) ? dense_tc_fwd_split(s) : dense_simt_fwd_split(s);
+    return dense_few_supported(s) ? dense_few_split(s) : dense_tc_supported(s) ? dense_tc_fwd_split(s) : dense_simt_fwd_split(s);
 }
 DenseSplit dq_split(const DenseShape& s) { return dense_tc_supported(s) ? dense_tc_dq_split(s) : dense_simt_dq_split(s); }
 DenseSplit dkv_split(const DenseShape& s) {
@@ -197,7 +197,9 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.part = static_cast<float*>(ws);
-    LLSA_TRY(dense_tc_supported(s) ? launch_dense_tc_fwd(s, a, st) : launch_dense_simt_fwd(s, a, st));
+    LLSA_TRY(dense_few_supported(s)  ? launch_dense_few(s, a, st)
+             : dense_tc_supported(s) ? launch_dense_tc_fwd(s, a, st)
+                                     : launch_dense_simt_fwd(s, a, st));
     if (p.splits > 1) {
         const long long rows = (long long)s.slices * s.R;
         const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));

@@ -43,7 +43,7 @@ constexpr int kWarps = 16, kCols = 32;  // elementwise warps: a thread takes one
 // 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
 // 104 of them, the 128 others keep 64.
 constexpr int kThreads = (kWarps + 4) * 32, kRegsElementwise = 104, kRegsOther = 64;
-constexpr int BT = 128;  // rows of every tile
+constexpr int BT = kTileRows;
 
 template <int D, bool KEYS>
 struct Cfg {
@@ -63,43 +63,6 @@ struct Bars {
     PieceRing pieces;
     uint32_t tmem_slot;
     int abort_flag;
-};
-
-// The items of a block: tiles of 128 rows of the streamed side, those that the
-// mask leaves nothing of skipped. Every role walks the same list.
-template <bool KEYS>
-struct Items {
-    int pos, t0, stop;  // first row of the tile; its token in its head (KEYS); end of the axis
-    int x0;             // the block's first stationary row
-    bool all;           // no tile to skip, no row to clear
-    DenseSpan sp;
-
-    __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int pos_, int t0_, int end)
-        : pos(pos_), t0(t0_), stop(end), x0(x0_), all(!KEYS || (!a.causal && s.lq == a.nq)), sp(s) {}
-    __device__ __forceinline__ void start(const DenseArgs& a) {
-        if (all) return;
-        t0 = pos % a.nq;
-        settle(a);
-    }
-    __device__ __forceinline__ bool done() const { return pos >= stop; }
-    __device__ __forceinline__ void next(const DenseArgs& a) {
-        pos += BT;
-        if (all) return;
-        turn(a);
-        settle(a);
-    }
-
-private:
-    __device__ __forceinline__ void turn(const DenseArgs& a) {
-        t0 += BT;
-        if (t0 >= a.nq) t0 = t0 - a.nq < a.nq ? t0 - a.nq : t0 % a.nq;
-    }
-    __device__ __forceinline__ void settle(const DenseArgs& a) {
-        while (pos < stop && dense_tile_kend(a, sp, t0, BT) <= x0) {
-            pos += BT;
-            turn(a);
-        }
-    }
 };
 
 // One piece of work: 128 stationary rows of a slice against a part of the stream.

@@ -48,6 +48,64 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, int r0, int 
     }
 }
 
+// The same, fp32, through asynchronous copies: in shared memory after async_wait
+// and a barrier.
+template <int DP, int BM, typename F>
+__device__ __forceinline__ void fetch_tile(float* dst, const float* src, int r0, int d, F valid) {
+    constexpr int C = DP / 4;
+    for (int x = threadIdx.x; x < BM * C; x += kThreads) {
+        const int r = x / C, c = (x - r * C) * 4;
+        const bool on = c < d && valid(r0 + r);
+        const float* from = on ? src + (long long)(r0 + r) * d + c : src;
+        const uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(dst + r * (DP + 4) + c));
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" :: "r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+    }
+}
+__device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+__device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group 0;\n" ::: "memory"); }
+
+// The forward keeps two buffers for the tiles of the streamed side where the type
+// needs no conversion on the way: the next tile comes in during this one's work (4
+// heads x 200 queries x 8,000 keys 92 -> 73 us). The backward kernels lose more to
+// the block that no longer fits beside (2 x 8 x 1,023 tokens 476 -> 552 us).
+template <typename T, bool FWD>
+constexpr int buffers() {
+    return sizeof(T) == 4 && FWD ? 2 : 1;
+}
+
+// Tiles of two streamed operands, one after the other.
+template <typename T, int DP, int BM, int NBUF, typename F>
+struct Stream {
+    float *x, *y;  // NBUF tiles each
+    const T *gx, *gy;
+    int d, buf;
+    F valid;
+
+    __device__ __forceinline__ void fetch(int r0) {  // NBUF 2: into the buffer that is not in use
+        if constexpr (NBUF == 2) {
+            fetch_tile<DP, BM>(x + buf * BM * (DP + 4), gx, r0, d, valid);
+            fetch_tile<DP, BM>(y + buf * BM * (DP + 4), gy, r0, d, valid);
+            async_commit();
+        }
+    }
+    // The tile at r0 becomes the current one; `next` (or -1) is asked for. Ends with a barrier.
+    __device__ __forceinline__ void turn(int r0, int next) {
+        if constexpr (NBUF == 2) {
+            async_wait();
+            __syncthreads();
+            buf ^= 1;
+            if (next >= 0) fetch(next);
+        } else {
+            __syncthreads();
+            load_tile<T, DP, BM>(x, gx, r0, d, valid);
+            load_tile<T, DP, BM>(y, gy, r0, d, valid);
+            __syncthreads();
+        }
+    }
+    __device__ __forceinline__ const float* cx() const { return x + (NBUF == 2 ? (buf ^ 1) * BM * (DP + 4) : 0); }
+    __device__ __forceinline__ const float* cy() const { return y + (NBUF == 2 ? (buf ^ 1) * BM * (DP + 4) : 0); }
+};
+
 // acc[i][j] = A row (ty * N + i) . B row (tx + 16 j)
 template <int N, int DP>
 __device__ __forceinline__ void tile_dot(float (&acc)[N][N], const float* A, const float* B, int ty, int tx) {
@@ -124,12 +182,12 @@ __device__ __forceinline__ void store_row(T* dst, const float4 (&acc)[DP / 64], 
 // then (maximum, sum) pairs [split][slice][R].
 template <typename T, int DP, int BM>
 __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
-    constexpr int N = BM / 16;
+    constexpr int N = BM / 16, NBUF = buffers<T, true>();
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sK = sQ + BM * (DP + 4);
-    float* sV = sK + BM * (DP + 4);
-    float* sP = sV + BM * (DP + 4);
+    float* sV = sK + NBUF * BM * (DP + 4);
+    float* sP = sV + NBUF * BM * (DP + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.R + BM - 1) / BM;
     const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
@@ -156,13 +214,13 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
 #pragma unroll
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    auto key_ok = [&](int j) { return j < sp.lk; };
+    Stream<T, DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
-        __syncthreads();
-        load_tile<T, DP, BM>(sK, k, j0, a.d, [&](int j) { return j < sp.lk; });
-        load_tile<T, DP, BM>(sV, v, j0, a.d, [&](int j) { return j < sp.lk; });
-        __syncthreads();
+        stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
         float s[N][N];
-        tile_dot<N, DP>(s, sQ, sK, ty, tx);
+        tile_dot<N, DP>(s, sQ, stream.cx(), ty, tx);
 #pragma unroll
         for (int i = 0; i < N; i++) {
             float top = m[i];
@@ -195,7 +253,7 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
         }
         store_p<N>(sP, s, ty, tx);
         __syncthreads();
-        tile_acc<N, DP, BM>(acc, sP, sV, ty, tx);
+        tile_acc<N, DP, BM>(acc, sP, stream.cy(), ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -219,13 +277,13 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
 // dq of BM query rows. Partial sums of a split over the keys: [split][slice][R][d].
 template <typename T, int DP, int BM>
 __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
-    constexpr int N = BM / 16;
+    constexpr int N = BM / 16, NBUF = buffers<T, false>();
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sG = sQ + BM * (DP + 4);
     float* sK = sG + BM * (DP + 4);
-    float* sV = sK + BM * (DP + 4);
-    float* sP = sV + BM * (DP + 4);
+    float* sV = sK + NBUF * BM * (DP + 4);
+    float* sP = sV + NBUF * BM * (DP + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.R + BM - 1) / BM;
     const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
@@ -254,14 +312,14 @@ __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto key_ok = [&](int j) { return j < sp.lk; };
+    Stream<T, DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
-        __syncthreads();
-        load_tile<T, DP, BM>(sK, k, j0, a.d, [&](int j) { return j < sp.lk; });
-        load_tile<T, DP, BM>(sV, v, j0, a.d, [&](int j) { return j < sp.lk; });
-        __syncthreads();
+        stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
         float s[N][N], dp[N][N];
-        tile_dot<N, DP>(s, sQ, sK, ty, tx);
-        tile_dot<N, DP>(dp, sG, sV, ty, tx);
+        tile_dot<N, DP>(s, sQ, stream.cx(), ty, tx);
+        tile_dot<N, DP>(dp, sG, stream.cy(), ty, tx);
 #pragma unroll
         for (int i = 0; i < N; i++)
 #pragma unroll
@@ -271,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
             }
         store_p<N>(sP, s, ty, tx);
         __syncthreads();
-        tile_acc<N, DP, BM>(acc, sP, sK, ty, tx);
+        tile_acc<N, DP, BM>(acc, sP, stream.cx(), ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -289,13 +347,13 @@ __global__ void __launch_bounds__(kThreads) dense_dq_simt_kernel(DenseArgs a) {
 // Partial sums of a split over the rows: dk [split][slice][nk][d], then dv.
 template <typename T, int DP, int BM>
 __global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
-    constexpr int N = BM / 16;
+    constexpr int N = BM / 16, NBUF = buffers<T, false>();
     extern __shared__ float4 smem4[];
     float* sK = reinterpret_cast<float*>(smem4);
     float* sV = sK + BM * (DP + 4);
     float* sQ = sV + BM * (DP + 4);
-    float* sG = sQ + BM * (DP + 4);
-    float* sP = sG + BM * (DP + 4);  // P^T
+    float* sG = sQ + NBUF * BM * (DP + 4);
+    float* sP = sG + NBUF * BM * (DP + 4);  // P^T
     float* sS = sP + BM * (BM + 4);  // dS^T
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.nk + BM - 1) / BM;
@@ -317,15 +375,20 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
     for (int i = 0; i < N; i++)
 #pragma unroll
         for (int c = 0; c < DP / 64; c++) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int r0 = r_first; r0 < r_last; r0 += BM) {
-        if (dense_tile_kend(a, sp, r0 % a.nq, BM) <= j0) continue;
-        __syncthreads();
-        load_tile<T, DP, BM>(sQ, q, r0, a.d, row_ok);
-        load_tile<T, DP, BM>(sG, g, r0, a.d, row_ok);
-        __syncthreads();
+    auto settle = [&](int r0) {  // the first tile from r0 on that sees any of these keys, or -1
+        while (r0 < r_last && dense_tile_kend(a, sp, r0 % a.nq, BM) <= j0) r0 += BM;
+        return r0 < r_last ? r0 : -1;
+    };
+    Stream<T, DP, BM, NBUF, decltype(row_ok)> stream{sQ, sG, q, g, a.d, 0, row_ok};
+    int next = settle(r_first);
+    if (next >= 0) stream.fetch(next);
+    while (next >= 0) {
+        const int r0 = next;
+        next = settle(r0 + BM);
+        stream.turn(r0, next);
         float s[N][N], dp[N][N];
-        tile_dot<N, DP>(s, sK, sQ, ty, tx);
-        tile_dot<N, DP>(dp, sV, sG, ty, tx);
+        tile_dot<N, DP>(s, sK, stream.cx(), ty, tx);
+        tile_dot<N, DP>(dp, sV, stream.cy(), ty, tx);
 #pragma unroll
         for (int j = 0; j < N; j++) {
             const int r = r0 + tx + 16 * j;
@@ -342,8 +405,8 @@ __global__ void __launch_bounds__(kThreads) dense_dkv_simt_kernel(DenseArgs a) {
         store_p<N>(sP, s, ty, tx);
         store_p<N>(sS, dp, ty, tx);
         __syncthreads();
-        tile_acc<N, DP, BM>(dv, sP, sG, ty, tx);
-        tile_acc<N, DP, BM>(dk, sS, sQ, ty, tx);
+        tile_acc<N, DP, BM>(dv, sP, stream.cy(), ty, tx);
+        tile_acc<N, DP, BM>(dk, sS, stream.cx(), ty, tx);
     }
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -367,8 +430,9 @@ enum { kFwd, kDq, kDkv };
 
 template <int OP, typename T, int DP, int BM>
 int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    const int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
-    const int smem = OP == kFwd ? 3 * tile + p : OP == kDq ? 4 * tile + p : 4 * tile + 2 * p;
+    constexpr int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, NBUF = buffers<T, OP == kFwd>();
+    constexpr int smem = OP == kFwd ? (1 + 2 * NBUF) * tile + p : (2 + 2 * NBUF) * tile + (OP == kDq ? p : 2 * p);
+    static_assert(smem <= 227 * 1024, "shared memory budget");
     const int extent = OP == kDkv ? s.nk : s.R;
     const long long blocks = (long long)((extent + BM - 1) / BM) * s.slices;
     if (blocks > 2147483647LL) return LLSA_ERR_UNSUPPORTED;

@@ -79,6 +79,45 @@ struct Stage {
     }
 };
 
+constexpr int kTileRows = 128;  // rows of every tile of the backward kernels
+
+// The items of a block: tiles of 128 rows of the streamed side, those that the
+// mask leaves nothing of skipped. Every role walks the same list.
+template <bool KEYS>
+struct Items {
+    int pos, t0, stop;  // first row of the tile; its token in its head (KEYS); end of the axis
+    int x0;             // the block's first stationary row
+    bool all;           // no tile to skip, no row to clear
+    DenseSpan sp;
+
+    __device__ __forceinline__ Items(const DenseArgs& a, DenseSpan s, int x0_, int pos_, int t0_, int end)
+        : pos(pos_), t0(t0_), stop(end), x0(x0_), all(!KEYS || (!a.causal && s.lq == a.nq)), sp(s) {}
+    __device__ __forceinline__ void start(const DenseArgs& a) {
+        if (all) return;
+        t0 = pos % a.nq;
+        settle(a);
+    }
+    __device__ __forceinline__ bool done() const { return pos >= stop; }
+    __device__ __forceinline__ void next(const DenseArgs& a) {
+        pos += kTileRows;
+        if (all) return;
+        turn(a);
+        settle(a);
+    }
+
+private:
+    __device__ __forceinline__ void turn(const DenseArgs& a) {
+        t0 += kTileRows;
+        if (t0 >= a.nq) t0 = t0 - a.nq < a.nq ? t0 - a.nq : t0 % a.nq;
+    }
+    __device__ __forceinline__ void settle(const DenseArgs& a) {
+        while (pos < stop && dense_tile_kend(a, sp, t0, kTileRows) <= x0) {
+            pos += kTileRows;
+            turn(a);
+        }
+    }
+};
+
 // The pieces of a resident block, worked out by one copying thread (divisions and
 // loads of the lengths: some 1,500 clocks) ahead of the roles that read them.
 constexpr int kPieceSlots = 4;
