@@ -157,4 +157,15 @@ int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st
 int launch_dense_tc_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_tc_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
+// dense_split_tc.cu: fp32 on the tensor cores, d <= 64 (planes: three bf16 planes
+// of q, k, v, or of q, dout, k, v, at the start of the workspace).
+bool dense_split_supported(const DenseShape& s);
+DenseSplit dense_split_fwd_split(const DenseShape& s);  // dq: the same
+DenseSplit dense_split_dkv_split(const DenseShape& s);
+size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes
+int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st);
+int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st);
+int launch_dense_split_dq(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st);
+int launch_dense_split_dkv(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st);
+
 }  // namespace llsa

@@ -169,26 +169,56 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
     return LLSA_OK;
 }
 
-DenseSplit fwd_split(const DenseShape& s) {
-    return dense_few_supported(s) ? dense_few_split(s) : dense_tc_supported(s) ? dense_tc_fwd_split(s) : dense_simt_fwd_split(s);
+// Which kernels take a call.
+enum class Path { kFew, kTc, kSplit, kSimt };
+
+Path fwd_path(const DenseShape& s) {
+    return dense_few_supported(s)     ? Path::kFew
+           : dense_tc_supported(s)    ? Path::kTc
+           : dense_split_supported(s) ? Path::kSplit
+                                      : Path::kSimt;
 }
-DenseSplit dq_split(const DenseShape& s) { return dense_tc_supported(s) ? dense_tc_dq_split(s) : dense_simt_dq_split(s); }
+Path bwd_path(const DenseShape& s) {
+    return dense_tc_supported(s) ? Path::kTc : dense_split_supported(s) ? Path::kSplit : Path::kSimt;
+}
+
+DenseSplit fwd_split(const DenseShape& s) {
+    switch (fwd_path(s)) {
+        case Path::kFew: return dense_few_split(s);
+        case Path::kTc: return dense_tc_fwd_split(s);
+        case Path::kSplit: return dense_split_fwd_split(s);
+        default: return dense_simt_fwd_split(s);
+    }
+}
+DenseSplit dq_split(const DenseShape& s) {
+    switch (bwd_path(s)) {
+        case Path::kTc: return dense_tc_dq_split(s);
+        case Path::kSplit: return dense_split_fwd_split(s);
+        default: return dense_simt_dq_split(s);
+    }
+}
 DenseSplit dkv_split(const DenseShape& s) {
-    return dense_tc_supported(s) ? dense_tc_dkv_split(s) : dense_simt_dkv_split(s);
+    switch (bwd_path(s)) {
+        case Path::kTc: return dense_tc_dkv_split(s);
+        case Path::kSplit: return dense_split_dkv_split(s);
+        default: return dense_simt_dkv_split(s);
+    }
 }
 
 }  // namespace
 
 size_t dense_fwd_workspace(const DenseShape& s) {
     const DenseSplit p = fwd_split(s);
-    return p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0;
+    return (fwd_path(s) == Path::kSplit ? dense_split_planes(s, false) : 0) +
+           (p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0);
 }
 
 size_t dense_bwd_workspace(const DenseShape& s) {
     const DenseSplit pq = dq_split(s), pk = dkv_split(s);
     const size_t dq = pq.splits > 1 ? (size_t)pq.splits * s.slices * s.R * s.d * sizeof(float) : 0;
     const size_t dkv = pk.splits > 1 ? (size_t)pk.splits * 2 * s.slices * s.nk * s.d * sizeof(float) : 0;
-    return 2 * align_up((size_t)s.slices * s.Rp * sizeof(float)) + std::max(dq, dkv);
+    return (bwd_path(s) == Path::kSplit ? dense_split_planes(s, true) : 0) +
+           2 * align_up((size_t)s.slices * s.Rp * sizeof(float)) + std::max(dq, dkv);
 }
 
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
@@ -196,10 +226,14 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     const DenseSplit p = fwd_split(s);
     a.splits = p.splits;
     a.chunk = p.chunk;
-    a.part = static_cast<float*>(ws);
-    LLSA_TRY(dense_few_supported(s)  ? launch_dense_few(s, a, st)
-             : dense_tc_supported(s) ? launch_dense_tc_fwd(s, a, st)
-                                     : launch_dense_simt_fwd(s, a, st));
+    const Path path = fwd_path(s);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + (path == Path::kSplit ? dense_split_planes(s, false) : 0));
+    switch (path) {
+        case Path::kFew: LLSA_TRY(launch_dense_few(s, a, st)); break;
+        case Path::kTc: LLSA_TRY(launch_dense_tc_fwd(s, a, st)); break;
+        case Path::kSplit: LLSA_TRY(launch_dense_split_fwd(s, a, ws, st)); break;
+        default: LLSA_TRY(launch_dense_simt_fwd(s, a, st));
+    }
     if (p.splits > 1) {
         const long long rows = (long long)s.slices * s.R;
         const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
@@ -213,7 +247,13 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
 
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
+    const Path path = bwd_path(s);
     const size_t rows = align_up((size_t)s.slices * s.Rp * sizeof(float));
+    void* planes[4];
+    if (path == Path::kSplit) {
+        LLSA_TRY(make_dense_split_planes(s, a, ws, planes, st));
+        ws = static_cast<char*>(ws) + dense_split_planes(s, true);
+    }
     a.nl2 = static_cast<float*>(ws);
     a.nd = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * rows);
@@ -227,7 +267,9 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         const DenseSplit p = dq_split(s);
         a.splits = p.splits;
         a.chunk = p.chunk;
-        LLSA_TRY(dense_tc_supported(s) ? launch_dense_tc_dq(s, a, st) : launch_dense_simt_dq(s, a, st));
+        LLSA_TRY(path == Path::kTc      ? launch_dense_tc_dq(s, a, st)
+                 : path == Path::kSplit ? launch_dense_split_dq(s, a, planes, st)
+                                        : launch_dense_simt_dq(s, a, st));
         if (p.splits > 1) {
             const long long n = (long long)s.slices * s.R * s.d;
             LLSA_TRY(bf16 ? join_sum<__nv_bfloat16>(a.part, a.dq, n, p.splits, st)
@@ -238,7 +280,9 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         const DenseSplit p = dkv_split(s);
         a.splits = p.splits;
         a.chunk = p.chunk;
-        LLSA_TRY(dense_tc_supported(s) ? launch_dense_tc_dkv(s, a, st) : launch_dense_simt_dkv(s, a, st));
+        LLSA_TRY(path == Path::kTc      ? launch_dense_tc_dkv(s, a, st)
+                 : path == Path::kSplit ? launch_dense_split_dkv(s, a, planes, st)
+                                        : launch_dense_simt_dkv(s, a, st));
         if (p.splits > 1) {
             const long long n = (long long)s.slices * s.nk * s.d;
             const float* second = a.part + (long long)p.splits * n;

@@ -1,0 +1,669 @@
+// dense_split_tc.cu -- dense attention in fp32 on the tcgen05 tensor cores (d <=
+// 64), forward and backward.
+//
+// Mathematics. Each fp32 operand x is written as x1 + x2 + x3 with x1 = bf16(x),
+// x2 = bf16(x - x1), x3 = bf16(x - x1 - x2): 8 bits and a sign each, so what is
+// left of x is at most 2^-26 of it. A product keeps the six terms x1 y1, x1 y2,
+// x2 y1, x2 y2, x1 y3, x3 y1; the dropped ones are 2^-25 of it and less, as small
+// as fp32's own rounding. Products are exact in fp32 and summed in fp32 in tensor
+// memory. Probabilities and dS, computed in fp32 from fp32 scores, are split the
+// same way in registers.
+//
+// Six bf16 products take 6 / 2,250 of the tensor cores' time against 1 / 80 on the
+// CUDA cores, whose kernel moreover gets half of that rate (an operand from shared
+// memory costs them as much as two of its FMAs). The kernels are bound by the
+// tensor cores: 1,530 clocks per 128 x 128 x 64 product.
+//
+// A pass before writes the three planes of q, k, v (and dout) to the workspace,
+// plane by plane, where TMA fetches them as ordinary bf16 tiles of 64 columns
+// (zeros behind d); a tile is three planes of 16 KB.
+#include <algorithm>
+
+#include "dense_tc.cuh"
+
+namespace llsa {
+namespace {
+
+using namespace tc;
+
+constexpr int kPlane = kTileRows * 128;  // bytes of 128 rows x 64 bf16
+constexpr int kTile = 3 * kPlane;
+constexpr int BT = kTileRows;
+
+// The six terms, small ones first: plane of the first operand, of the second.
+__device__ __forceinline__ constexpr int term_a(int i) { return i == 0 ? 2 : i == 1 ? 0 : i == 2 ? 1 : i == 3 ? 1 : 0; }
+__device__ __forceinline__ constexpr int term_b(int i) { return i == 0 ? 0 : i == 1 ? 2 : i == 2 ? 1 : i == 3 ? 0 : i == 4 ? 1 : 0; }
+
+// ----------------------------------------------------------------- planes --
+
+struct PlaneArgs {
+    const float* x[4];
+    __nv_bfloat16* out[4];  // plane p at out + p * n
+    long long n[4];
+};
+
+// Eight values per thread, blockIdx.y the tensor. Bound by HBM: 4 bytes in, 6 out.
+__global__ void __launch_bounds__(256) dense_planes_kernel(const __grid_constant__ PlaneArgs a) {
+    const int t = blockIdx.y;
+    const long long n = a.n[t];
+    for (long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 8; i < n; i += (long long)gridDim.x * 2048) {
+        float f[8];
+        load8(a.x[t] + i, f);
+#pragma unroll
+        for (int p = 0; p < 3; p++) {
+            uint4 u;
+            uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+                w[c >> 1] = pack_bf16x2(f[c], f[c + 1]);
+                f[c] -= __uint_as_float(w[c >> 1] << 16);
+                f[c + 1] -= __uint_as_float(w[c >> 1] & 0xffff0000u);
+            }
+            *reinterpret_cast<uint4*>(a.out[t] + p * n + i) = u;
+        }
+    }
+}
+
+// Two fp32 values as three packed bf16 pairs.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+    p1 = pack_bf16x2(x, y);
+    x -= __uint_as_float(p1 << 16);
+    y -= __uint_as_float(p1 & 0xffff0000u);
+    p2 = pack_bf16x2(x, y);
+    x -= __uint_as_float(p2 << 16);
+    y -= __uint_as_float(p2 & 0xffff0000u);
+    p3 = pack_bf16x2(x, y);
+}
+
+// One thread: the three planes of the 128 rows at `row` of a tensor of `slices` slices.
+__device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, int slices,
+                                            uint32_t mbar) {
+    mbar_arrive_expect_tx(mbar, kTile);
+    for (int p = 0; p < 3; p++) tma_load_3d(smem_u32(dst + p * kPlane), map, 0, row, p * slices + slice, mbar);
+}
+
+__device__ __forceinline__ void store_rowpart(float* dst, const uint32_t* o, float f, int c0, int cols, int d) {
+    for (int c = 0; c < cols; c += 4)
+        if (c0 + c < d) {
+            const float v[4] = {__uint_as_float(o[c]) * f, __uint_as_float(o[c + 1]) * f, __uint_as_float(o[c + 2]) * f,
+                                __uint_as_float(o[c + 3]) * f};
+            store4(dst + c0 + c, v);
+        }
+}
+
+// ---------------------------------------------------------------- forward --
+
+// A block takes 128 query rows against a stream of key and value tiles. S has two
+// buffers (columns 0 and 128), so the next S runs beside this one's softmax; the
+// planes of P lie at 256, O at 448.
+constexpr int kFwdThreads = 256;
+constexpr int kFwdSmem = kTile * 4 + 1024;  // Q, two K, one V
+
+struct FwdBars {
+    uint64_t q_full, k_full[2], k_empty[2], v_full, v_empty, s_full[2], s_free[2], p_full, o_done, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+__global__ void __launch_bounds__(kFwdThreads, 1)
+dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const __grid_constant__ DenseArgs a) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *sQ = sm, *sK = sm + kTile, *sV = sm + 3 * kTile;
+    FwdBars* bar = reinterpret_cast<FwdBars*>(sm + 4 * kTile);
+    volatile int* abort_flag = &bar->abort_flag;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
+        if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
+        return;
+    }
+    const DenseWork work = dense_work(a, blockIdx.x, (a.R + BT - 1) / BT);
+    const int slice = work.slice, part = work.part;
+    const int r0 = (a.causal ? work.blocks - 1 - work.block : work.block) * BT;
+    const DenseSpan sp = dense_span(a, slice);
+    const int j_first = part * a.chunk;
+    const int end = min(dense_tile_kend(a, sp, r0 < a.nq ? r0 : r0 % a.nq, BT), a.splits > 1 ? j_first + a.chunk : a.nk);
+    const int n = end > j_first ? (end - j_first + BT - 1) / BT : 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&bar->k_full[i]), 1);
+            mbar_init(smem_u32(&bar->k_empty[i]), 1);
+            mbar_init(smem_u32(&bar->s_full[i]), 1);
+            mbar_init(smem_u32(&bar->s_free[i]), 4);
+        }
+        mbar_init(smem_u32(&bar->q_full), 1);
+        mbar_init(smem_u32(&bar->v_full), 1);
+        mbar_init(smem_u32(&bar->v_empty), 1);
+        mbar_init(smem_u32(&bar->p_full), 4);
+        mbar_init(smem_u32(&bar->o_done), 1);
+        mbar_init(smem_u32(&bar->drain), 1);
+        bar->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 4) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
+    const uint32_t tP = tbase + 256, tO = tbase + 448;
+
+    if (warp == 5 || warp == 6) {
+        // ----------------------------------------------------------- copies
+        if (lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+            const bool keys = warp == 5;
+            if (keys) load_planes(sQ, &mq, r0, slice, a.slices, smem_u32(&bar->q_full));
+            int t = 0;
+            for (; t < n; t++) {
+                const int st = keys ? t & 1 : 0, use = keys ? t >> 1 : t;
+                const uint32_t full = smem_u32(keys ? &bar->k_full[st] : &bar->v_full);
+                if (use > 0 && !bar_wait(smem_u32(keys ? &bar->k_empty[st] : &bar->v_empty), (use - 1) & 1, abort_flag, a)) break;
+                load_planes(keys ? sK + st * kTile : sV, keys ? &mk : &mv, j_first + t * BT, slice, a.slices, full);
+            }
+            // copies still in flight must land before the block exits
+            if (keys) land(smem_u32(&bar->q_full), 0);
+            if (keys)
+                for (int x = max(0, t - 2); x < t; x++) land(smem_u32(&bar->k_full[x & 1]), (x >> 1) & 1);
+            else if (t > 0)
+                land(smem_u32(&bar->v_full), (t - 1) & 1);
+        }
+    } else if (warp == 4) {
+        // ------------------------------------------------------- MMA issuer
+        const uint32_t leader = elect_lane();
+        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idO = idesc_bf16(BT, 64, 0, 1);
+        const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024), dK = desc_sw128(smem_u32(sK), 16, 1024);
+        const uint64_t dV = desc_sw128(smem_u32(sV), kPlane, 1024);
+        auto issue_S = [&](int t) {
+            const int b = t & 1;
+            if (!warp_wait(smem_u32(&bar->k_full[b]), (t >> 1) & 1, abort_flag, a)) return false;
+            if (t > 1 && !warp_wait(smem_u32(&bar->s_free[b]), ((t >> 1) - 1) & 1, abort_flag, a)) return false;
+            tc_fence_after();
+            const uint64_t dT = dK + (b * kTile >> 4);
+#pragma unroll
+            for (int i = 0; i < 6; i++)
+#pragma unroll
+                for (int ks = 0; ks < 4; ks++)
+                    mma_ss(leader, tbase + b * 128, dQ + ((term_a(i) * kPlane + ks * 32) >> 4),
+                           dT + ((term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+            commit(leader, smem_u32(&bar->s_full[b]));
+            commit(leader, smem_u32(&bar->k_empty[b]));
+            return true;
+        };
+        bool ok = n > 0 && warp_wait(smem_u32(&bar->q_full), 0, abort_flag, a) && issue_S(0);
+        for (int t = 0; t < n && ok; t++) {
+            if (t + 1 < n) ok = issue_S(t + 1);
+            ok = ok && warp_wait(smem_u32(&bar->p_full), t & 1, abort_flag, a);
+            ok = ok && warp_wait(smem_u32(&bar->v_full), t & 1, abort_flag, a);
+            if (!ok) break;
+            // values behind the last valid key may be anything: their weights are 0, so they must be finite
+            const int live = sp.lk - (j_first + t * BT);
+            if (live < BT) {
+                for (int p = 0; p < 3; p++)
+                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
+                        reinterpret_cast<uint4*>(sV + p * kPlane)[x] = make_uint4(0u, 0u, 0u, 0u);
+                fence_async_smem();
+                __syncwarp();
+            }
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 6; i++)
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++)
+                    mma_ts(leader, tO, tP + term_a(i) * 64 + ks * 8, dV + ((term_b(i) * kPlane + ks * 2048) >> 4), idO,
+                           t > 0 || i > 0 || ks > 0);
+            commit(leader, smem_u32(&bar->o_done));
+            commit(leader, smem_u32(&bar->v_empty));
+        }
+        // no MMA may be in flight when tensor memory is released
+        commit(leader, smem_u32(&bar->drain));
+        if (lane == 0) land(smem_u32(&bar->drain), 0);
+        __syncwarp();
+    } else if (warp < 4) {
+        // ------------------------------------------------ softmax, epilogue
+        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
+        const int r = r0 + warp * 32 + lane;
+        int lim = (r < a.R ? dense_kend(a, sp, r < a.nq ? r : r % a.nq) : 0) - j_first;
+        const float sl2 = a.scale * kDenseLog2e;
+        float m = -INFINITY, l = 0.f;
+        for (int t = 0; t < n; t++, lim -= BT) {
+            const int b = t & 1;
+            bar_wait(smem_u32(&bar->s_full[b]), (t >> 1) & 1, abort_flag, a);
+            tc_fence_after();
+            uint32_t s[128];
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) tmem_ld32_nowait(tbase + b * 128 + lanes + c, s + c);
+            tmem_wait_ld();
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->s_free[b]), lane);
+            if (__any_sync(0xffffffffu, lim < BT)) {
+#pragma unroll
+                for (int c = 0; c < 128; c++) s[c] = c < lim ? s[c] : 0xff800000u;
+            }
+            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
+            // the reference follows the row's maximum exactly here: reading O back costs little beside six products
+            const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2);
+            const bool grow = top > m;
+            const float f = grow ? ex2(m - top) : 1.f;
+            m = top;
+            l *= f;
+            if (t > 0) {  // O and the planes of P are at rest
+                bar_wait(smem_u32(&bar->o_done), (t - 1) & 1, abort_flag, a);
+                tc_fence_after();
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_nowait(tO + lanes + c, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        tmem_st32(tO + lanes + c, o);
+                    }
+                }
+            }
+            const float shift = m == -INFINITY ? 0.f : -m;
+#pragma unroll
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t p1[16], p2[16], p3[16];
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    const float e0 = exp2f(fmaf(__uint_as_float(s[c + i]), sl2, shift));
+                    const float e1 = exp2f(fmaf(__uint_as_float(s[c + i + 1]), sl2, shift));
+                    sum += e0 + e1;
+                    split2(e0, e1, p1[i >> 1], p2[i >> 1], p3[i >> 1]);
+                }
+                l += sum;
+                tmem_st16(tP + lanes + (c >> 1), p1);
+                tmem_st16(tP + lanes + 64 + (c >> 1), p2);
+                tmem_st16(tP + lanes + 128 + (c >> 1), p3);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->p_full), lane);
+        }
+        if (n > 0) {
+            bar_wait(smem_u32(&bar->o_done), (n - 1) & 1, abort_flag, a);
+            tc_fence_after();
+        }
+        const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
+        const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+            uint32_t o[32];
+#pragma unroll
+            for (int i = 0; i < 32; i++) o[i] = 0u;
+            if (n > 0) {
+                tmem_ld32_nowait(tO + lanes + c, o);
+                tmem_wait_ld();
+            }
+            if (r < a.R)
+                store_rowpart(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, o, inv, c, 32, a.d);
+        }
+        if (r < a.R) {
+            if (a.splits > 1)
+                reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
+            else
+                a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 4) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// --------------------------------------------------------------- backward --
+
+// As the bf16 kernel: 128 stationary rows (X1, X2) = (Q, dO) or (K, V) against a
+// stream (Y1, Y2) of the others. Shared memory holds one tile of each, so an item's
+// copies, its S and dP, the elementwise work and its sums follow one another; the
+// tensor cores carry most of that time. Tensor memory: S at 0, dP at 128, both
+// covered by planes 1 and 2 of P and of dS once they are read, their planes 3 at
+// 256 and 320, the sums at 384.
+constexpr int kBwdWarps = 16, kCols = 32;
+constexpr int kBwdThreads = (kBwdWarps + 4) * 32;
+constexpr int kBwdSmem = kTile * 4 + 2 * BT * 4 + 512;
+
+struct BwdBars {
+    uint64_t x_full[2], y_full[2], y_empty[2], s_full, dp_full, ds_ready, acc_full, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+template <bool KEYS>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
+                       const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2,
+                       const __grid_constant__ DenseArgs a) {
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *sX = sm, *sY = sm + 2 * kTile;
+    float* stats = reinterpret_cast<float*>(sm + 4 * kTile);  // KEYS: -l2 and -D of the item's rows
+    BwdBars* bar = reinterpret_cast<BwdBars*>(sm + 4 * kTile + 2 * BT * 4);
+    volatile int* abort_flag = &bar->abort_flag;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
+        if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
+        return;
+    }
+    const int extent = KEYS ? a.nk : a.R;
+    const DenseWork work = dense_work(a, blockIdx.x, (extent + BT - 1) / BT);
+    const int slice = work.slice, part = work.part;
+    const int x0 = (a.causal && !KEYS ? work.blocks - 1 - work.block : work.block) * BT;
+    const DenseSpan sp = dense_span(a, slice);
+    const int first = a.splits > 1 ? part * a.chunk : 0;
+    int stop;
+    if constexpr (KEYS) {
+        stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
+    } else {
+        stop = dense_tile_kend(a, sp, x0 < a.nq ? x0 : x0 % a.nq, BT);
+        if (a.splits > 1) stop = min(stop, first + a.chunk);
+    }
+    Items<KEYS> start(a, sp, x0, first, 0, stop);
+    start.start(a);
+    const bool any = !start.done();
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&bar->x_full[i]), 1);
+            mbar_init(smem_u32(&bar->y_full[i]), 1);
+            mbar_init(smem_u32(&bar->y_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->s_full), 1);
+        mbar_init(smem_u32(&bar->dp_full), 1);
+        mbar_init(smem_u32(&bar->ds_ready), kBwdWarps);
+        mbar_init(smem_u32(&bar->acc_full), 1);
+        mbar_init(smem_u32(&bar->drain), 1);
+        bar->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kBwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
+    const uint32_t tDP = tbase + 128, tP3 = tbase + 256, tS3 = tbase + 320, tAcc = tbase + 384;
+
+    if (warp == kBwdWarps + 1 || warp == kBwdWarps + 2) {
+        // ----------------------------------------------------------- copies
+        if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+            const int k = warp - kBwdWarps - 1;
+            load_planes(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
+            const uint32_t full = smem_u32(&bar->y_full[k]);
+            int n = 0;
+            for (Items<KEYS> it = start; !it.done(); it.next(a)) {
+                if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
+                if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
+                    const long long row = (long long)slice * a.Rp + it.pos;
+                    mbar_arrive_expect_tx(full, kTile + 2 * BT * 4);
+                    for (int p = 0; p < 3; p++)
+                        tma_load_3d(smem_u32(sY + kTile + p * kPlane), &my2, 0, it.pos, p * a.slices + slice, full);
+                    bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
+                    bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
+                } else {
+                    load_planes(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                }
+                n++;
+            }
+            // copies still in flight must land before the block exits
+            land(smem_u32(&bar->x_full[k]), 0);
+            if (n > 0) land(full, (n - 1) & 1);
+        }
+    } else if (warp == kBwdWarps) {
+        // ------------------------------------------------------- MMA issuer
+        const uint32_t leader = elect_lane();
+        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, 64, 0, 1);
+        const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024), dY = desc_sw128(smem_u32(sY), 16, 1024);
+        const uint64_t dM = desc_sw128(smem_u32(sY), kPlane, 1024);  // the streamed tiles read along their rows
+        // rows whose P and dS are 0 by the lengths may hold anything: cleared, as they meet those zeros in the sums
+        auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
+            if constexpr (KEYS) {
+                if (it.all || it.t0 + BT <= it.sp.lq) return;
+                int t = it.t0 + lane;
+                for (int x = lane; x < BT; x += 32, t += 32)
+                    if (t % a.nq >= it.sp.lq)
+                        for (int p = 0; p < 3; p++)
+                            for (int e = 0; e < 8; e++)
+                                reinterpret_cast<uint4*>(tile + p * kPlane + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+            } else {
+                const int live = it.sp.lk - it.pos;
+                if (live >= BT) return;
+                for (int p = 0; p < 3; p++)
+                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
+                        reinterpret_cast<uint4*>(tile + p * kPlane)[x] = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_async_smem();
+            __syncwarp();
+        };
+        bool ok = any && warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
+                  warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
+        int n = 0;
+        for (Items<KEYS> it = start; ok && !it.done(); it.next(a), n++) {
+            // S and dP: the sums that used up what lies over them were issued before
+            for (int k = 0; k < 2 && ok; k++) {
+                ok = warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a);
+                if (!ok) break;
+                if (k == 0 || KEYS) clear_rows(sY + k * kTile, it);  // V only enters dP, which the mask covers
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 6; i++)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ks++)
+                        mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
+                               dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+            }
+            ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int i = 0; i < 6; i++) {
+                const int pa = term_a(i);
+                const uint32_t opP = pa == 2 ? tP3 : tbase + pa * 64, opS = pa == 2 ? tS3 : tDP + pa * 64;
+#pragma unroll
+                for (int ks = 0; ks < 8; ks++) {
+                    const uint64_t m = dM + ((term_b(i) * kPlane + ks * 2048) >> 4);
+                    mma_ts(leader, tAcc, opS + ks * 8, m, idA, n > 0 || i > 0 || ks > 0);
+                    if (KEYS) mma_ts(leader, tAcc + 64, opP + ks * 8, m + (kTile >> 4), idA, n > 0 || i > 0 || ks > 0);
+                }
+            }
+            commit(leader, smem_u32(&bar->y_empty[0]));
+            commit(leader, smem_u32(&bar->y_empty[1]));
+        }
+        if (ok) commit(leader, smem_u32(&bar->acc_full));
+        // no MMA may be in flight when tensor memory is released
+        commit(leader, smem_u32(&bar->drain));
+        if (lane == 0) land(smem_u32(&bar->drain), 0);
+        __syncwarp();
+    } else if (warp < kBwdWarps) {
+        // ---------------------------------------- elementwise, epilogue
+        const int w = warp >> 2, q4 = warp & 3;  // quarter of the columns, of the rows
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const int x = x0 + q4 * 32 + lane;       // stationary row
+        const float sl2 = a.scale * kDenseLog2e;
+        float nl2 = 0.f, nd = 0.f;
+        int kend = 0;
+        if constexpr (!KEYS) {
+            nl2 = a.nl2[(long long)slice * a.Rp + x];  // Rp is a multiple of 128
+            nd = a.nd[(long long)slice * a.Rp + x];
+            kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
+        }
+        int n = 0;
+        for (Items<KEYS> it = start; !it.done(); it.next(a), n++) {
+            uint32_t s[kCols], g[kCols];
+            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
+            tc_fence_after();
+            tmem_ld32_nowait(tbase + lanes + w * kCols, s);
+            bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);  // with it the streamed tile's numbers
+            tc_fence_after();
+            tmem_ld32_nowait(tDP + lanes + w * kCols, g);
+            tmem_wait_ld();
+            tc_fence_before();
+            named_barrier(1 + q4, 128);  // the four warps of these rows have read S and dP
+            tc_fence_after();
+            const int lim = KEYS ? 0 : kend - it.pos - w * kCols;
+            const bool cut = KEYS ? a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)
+                                  : __any_sync(0xffffffffu, lim < kCols);
+            int t = KEYS && cut ? (it.t0 + w * kCols) % a.nq : 0;
+#pragma unroll
+            for (int c = 0; c < kCols; c++) {
+                const float l = KEYS ? stats[w * kCols + c] : nl2, D = KEYS ? stats[BT + w * kCols + c] : nd;
+                float p = exp2f(fmaf(__uint_as_float(s[c]), sl2, l));
+                float ds = p * (__uint_as_float(g[c]) + D);
+                if (cut) {
+                    const bool out = KEYS ? x > t + sp.lk - sp.lq : c >= lim;
+                    p = out ? 0.f : p;
+                    ds = out ? 0.f : ds;
+                    if (KEYS && ++t == a.nq) t = 0;
+                }
+                s[c] = __float_as_uint(p);
+                g[c] = __float_as_uint(ds);
+            }
+#pragma unroll
+            for (int k = KEYS ? 0 : 1; k < 2; k++) {  // planes of P, of dS
+                uint32_t p1[16], p2[16], p3[16];
+#pragma unroll
+                for (int c = 0; c < kCols; c += 2)
+                    split2(__uint_as_float(k == 0 ? s[c] : g[c]), __uint_as_float(k == 0 ? s[c + 1] : g[c + 1]), p1[c >> 1],
+                           p2[c >> 1], p3[c >> 1]);
+                const uint32_t t1 = tbase + k * 128 + lanes + w * 16;
+                tmem_st16(t1, p1);
+                tmem_st16(t1 + 64, p2);
+                tmem_st16((k == 0 ? tP3 : tS3) + lanes + w * 16, p3);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->ds_ready), lane);
+        }
+        if (any) {
+            bar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a);
+            tc_fence_after();
+        }
+        // rows without a gradient hold whatever their padding made: zero
+        const bool live = any && (KEYS ? x < sp.lk : kend > 0);
+        const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
+#pragma unroll
+        for (int k = 0; k < (KEYS ? 2 : 1); k++) {
+            float o[16];
+            if (any) tmem_ld16(tAcc + k * 64 + w * 16 + lanes, o);
+            uint32_t u[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) u[i] = live ? __float_as_uint(o[i]) : 0u;
+            float* base = a.splits > 1 ? a.part + (k * a.splits + part) * all * a.d
+                                       : static_cast<float*>(KEYS ? (k == 0 ? a.dk : a.dv) : a.dq);
+            if (x < extent) store_rowpart(base + row * a.d, u, k == 0 ? a.scale : 1.f, w * 16, 16, a.d);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kBwdWarps) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Planes of `n` tensors of sizes q_elems (first `nq` ones) or k_elems, laid out one after the other.
+int write_planes(const float* const* x, const long long* elems, int n, void* ws, __nv_bfloat16** planes, cudaStream_t st) {
+    PlaneArgs p;
+    char* at = static_cast<char*>(ws);
+    long long most = 0;
+    for (int i = 0; i < 4; i++) {
+        p.x[i] = i < n ? x[i] : nullptr;
+        p.n[i] = i < n ? elems[i] : 0;
+        p.out[i] = reinterpret_cast<__nv_bfloat16*>(at);
+        if (i < n) {
+            planes[i] = p.out[i];
+            at += up((size_t)elems[i] * 6);
+            most = std::max(most, elems[i]);
+        }
+    }
+    const dim3 grid((unsigned)std::min<long long>((most + 2047) / 2048, 8LL * kDenseSms), (unsigned)n);
+    LLSA_LAUNCH("dense_planes", st, dense_planes_kernel<<<grid, 256, 0, st>>>(p));
+    return LLSA_OK;
+}
+
+}  // namespace
+
+// From 2^14 (row, key) pairs per slice on: below, the passes before cost more than
+// the CUDA-core kernel.
+bool dense_split_supported(const DenseShape& s) {
+    return s.dtype == LLSA_DTYPE_F32 && s.d <= 64 && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent &&
+           (long long)s.R * s.nk >= (1 << 14);
+}
+
+DenseSplit dense_split_fwd_split(const DenseShape& s) {
+    return dense_make_split((long long)s.slices * ((s.R + BT - 1) / BT), s.nk, BT, 2);
+}
+DenseSplit dense_split_dkv_split(const DenseShape& s) {
+    return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT), s.R, BT, 2);
+}
+
+size_t dense_split_planes(const DenseShape& s, bool backward) {
+    const size_t q = up((size_t)s.slices * s.R * s.d * 6), k = up((size_t)s.slices * s.nk * s.d * 6);
+    return backward ? 2 * q + 2 * k : q + 2 * k;
+}
+
+int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st) {
+    const float* x[3] = {static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v)};
+    const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
+    const long long elems[3] = {nq, nk, nk};
+    __nv_bfloat16* p[3];
+    LLSA_TRY(write_planes(x, elems, 3, ws, p, st));
+    CUtensorMap mq, mk, mv;
+    LLSA_TRY(make_tmap_rows(&mq, p[0], 3LL * s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mk, p[1], 3LL * s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mv, p[2], 3LL * s.slices, s.nk, s.d, BT));
+    static_assert(kFwdSmem <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
+    cudaFuncSetAttribute(dense_fwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem);
+    const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
+    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("dense_fwd_split", st,
+                dense_fwd_split_kernel<<<(unsigned)pieces, kFwdThreads, kFwdSmem, st>>>(mq, mk, mv, a));
+    return LLSA_OK;
+}
+
+int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st) {
+    const float* x[4] = {static_cast<const float*>(a.q), static_cast<const float*>(a.dout), static_cast<const float*>(a.k),
+                         static_cast<const float*>(a.v)};
+    const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
+    const long long elems[4] = {nq, nq, nk, nk};
+    __nv_bfloat16* p[4];
+    LLSA_TRY(write_planes(x, elems, 4, ws, p, st));
+    for (int i = 0; i < 4; i++) planes[i] = p[i];
+    return LLSA_OK;
+}
+
+template <bool KEYS>
+static int launch_bwd(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
+    CUtensorMap mq, mg, mk, mv;
+    LLSA_TRY(make_tmap_rows(&mq, planes[0], 3LL * s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mg, planes[1], 3LL * s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mk, planes[2], 3LL * s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mv, planes[3], 3LL * s.slices, s.nk, s.d, BT));
+    static_assert(kBwdSmem <= 227 * 1024 && sizeof(BwdBars) <= 512, "shared memory budget");
+    cudaFuncSetAttribute(dense_bwd_split_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    const long long pieces = (long long)(((KEYS ? s.nk : s.R) + BT - 1) / BT) * s.slices * a.splits;
+    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    if constexpr (KEYS)
+        LLSA_LAUNCH("dense_dkv_split", st,
+                    dense_bwd_split_kernel<true><<<(unsigned)pieces, kBwdThreads, kBwdSmem, st>>>(mk, mv, mq, mg, a));
+    else
+        LLSA_LAUNCH("dense_dq_split", st,
+                    dense_bwd_split_kernel<false><<<(unsigned)pieces, kBwdThreads, kBwdSmem, st>>>(mq, mg, mk, mv, a));
+    return LLSA_OK;
+}
+
+int launch_dense_split_dq(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
+    return launch_bwd<false>(s, a, planes, st);
+}
+int launch_dense_split_dkv(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
+    return launch_bwd<true>(s, a, planes, st);
+}
+
+}  // namespace llsa
