@@ -84,10 +84,19 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     constexpr int V = 16 / sizeof(T);
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (idx >= a.rows * a.units) return;
-    const long long row = idx / a.units;
-    const int u = (int)(idx - row * a.units);
-    const long long b = row / a.n;
-    const int t = (int)(row - b * a.n);
+    int u, t;
+    long long b;
+    if (a.rows * a.units <= 0x7fffffffLL) {  // 64-bit divisions cost more than the rest of the thread's set-up
+        const uint32_t i = (uint32_t)idx, row = i / (uint32_t)a.units;
+        u = (int)(i - row * a.units);
+        b = row / (uint32_t)a.n;
+        t = (int)(row - (uint32_t)b * a.n);
+    } else {
+        const long long row = idx / a.units;
+        u = (int)(idx - row * a.units);
+        b = row / a.n;
+        t = (int)(row - b * a.n);
+    }
     const int seg = a.rot / a.axes, half = seg / 2;
     constexpr int P = MODE == kInterleaved ? V / 2 : MODE == kHalfVector ? V : 1;  // pairs of a unit
     float c[P], s[P];
@@ -122,47 +131,58 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     }
     const int total = a.heads[0] + a.heads[1];
     const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(h0 + a.heads_per_thread, total);
-#pragma unroll 4
-    for (int h = h0; h < h1; h++) {
+    auto place = [&](int h, const T*& in, T*& out) {
         const int w = h >= a.heads[0] ? 1 : 0;
         const int hh = h - w * a.heads[0];
-        const T* in = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] + hh * a.in_stride[w][1] +
-                      t * a.in_stride[w][2];
-        T* out = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + hh * a.out_stride[w][1] +
-                 t * a.out_stride[w][2];
-        if constexpr (MODE == kHalfScalar) {
-            const float x = to_float(in[col0]);
+        in = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] + hh * a.in_stride[w][1] + t * a.in_stride[w][2];
+        out = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + hh * a.out_stride[w][1] + t * a.out_stride[w][2];
+    };
+    if constexpr (MODE == kHalfScalar) {
+        for (int h = h0; h < h1; h++) {
+            const T* in;
+            T* out;
+            place(h, in, out);
             if (copy) {
                 out[col0] = in[col0];
             } else {
-                const float y = to_float(in[col1]);
+                const float x = to_float(in[col0]), y = to_float(in[col1]);
                 out[col0] = from_float<T>(x * c[0] - y * s[0]);
                 out[col1] = from_float<T>(x * s[0] + y * c[0]);
             }
-        } else {
-            Vec<T> x, y;
-            x.u = *reinterpret_cast<const uint4*>(in + col0);
-            if (copy) {
-                *reinterpret_cast<uint4*>(out + col0) = x.u;
-            } else if constexpr (MODE == kInterleaved) {
+        }
+    } else {
+        // Outputs may be the inputs, so loads do not move over stores by
+        // themselves. In fp32 two heads are loaded before the first is stored; in
+        // bf16, where a vector is twice the arithmetic, the registers are worth more
+        // as occupancy (12 heads x 65,536 tokens 69 us, with two 76, with four 87).
+        constexpr int HB = sizeof(T) == 2 ? 1 : 2;
+        for (int h = h0; h < h1; h += HB) {
+            Vec<T> x[HB], y[HB];
+            T* out[HB];
 #pragma unroll
-                for (int i = 0; i < P; i++) {
-                    if (col0 + 2 * i >= a.rot) break;  // rot_dim may end inside the vector
-                    const float p = to_float(x.e[2 * i]), q = to_float(x.e[2 * i + 1]);
-                    x.e[2 * i] = from_float<T>(p * c[i] - q * s[i]);
-                    x.e[2 * i + 1] = from_float<T>(p * s[i] + q * c[i]);
+            for (int k = 0; k < HB; k++)
+                if (h + k < h1) {
+                    const T* in;
+                    place(h + k, in, out[k]);
+                    x[k].u = *reinterpret_cast<const uint4*>(in + col0);
+                    if (MODE == kHalfVector && !copy) y[k].u = *reinterpret_cast<const uint4*>(in + col1);
                 }
-                *reinterpret_cast<uint4*>(out + col0) = x.u;
-            } else {
-                y.u = *reinterpret_cast<const uint4*>(in + col1);
 #pragma unroll
-                for (int i = 0; i < P; i++) {
-                    const float p = to_float(x.e[i]), q = to_float(y.e[i]);
-                    x.e[i] = from_float<T>(p * c[i] - q * s[i]);
-                    y.e[i] = from_float<T>(p * s[i] + q * c[i]);
+            for (int k = 0; k < HB; k++) {
+                if (h + k >= h1) break;
+                if (!copy) {
+#pragma unroll
+                    for (int i = 0; i < P; i++) {
+                        T& first = x[k].e[MODE == kInterleaved ? 2 * i : i];
+                        T& second = MODE == kInterleaved ? x[k].e[2 * i + 1] : y[k].e[i];
+                        if (MODE == kInterleaved && col0 + 2 * i >= a.rot) break;  // rot_dim may end inside the vector
+                        const float p = to_float(first), q = to_float(second);
+                        first = from_float<T>(p * c[i] - q * s[i]);
+                        second = from_float<T>(p * s[i] + q * c[i]);
+                    }
+                    if (MODE == kHalfVector) *reinterpret_cast<uint4*>(out[k] + col1) = y[k].u;
                 }
-                *reinterpret_cast<uint4*>(out + col0) = x.u;
-                *reinterpret_cast<uint4*>(out + col1) = y.u;
+                *reinterpret_cast<uint4*>(out[k] + col0) = x[k].u;
             }
         }
     }
@@ -271,11 +291,12 @@ int launch_rope(const llsa_rope_params* p, RopeArgs& a, cudaStream_t st) {
     const int total = a.heads[0] + a.heads[1];
     const long long threads = a.rows * units;
     // As many heads per thread (the sines are computed once for them) as leave
-    // two waves of resident threads.
-    const long long want = (long long)sm_count() * 2048 * 2;
+    // one wave of resident threads (6 heads x 10,785 tokens in fp32 14 us; two waves, 22).
+    const long long want = (long long)sm_count() * 2048;
     a.heads_per_thread = (int)std::min<long long>(total, std::max<long long>(1, threads * total / want));
     const long long gx = (threads + kThreads - 1) / kThreads;
     const int gy = (total + a.heads_per_thread - 1) / a.heads_per_thread;
+    a.heads_per_thread = (total + gy - 1) / gy;  // the same share for all
     if (gx > 2147483647LL || gy > 65535) return LLSA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)gx, (unsigned)gy);
     if (mode == kInterleaved) LLSA_LAUNCH("rope", st, rope_kernel<T, kInterleaved><<<grid, kThreads, 0, st>>>(a));

@@ -14,7 +14,7 @@ import dense_ref as ref
 
 pytestmark = pytest.mark.gpu
 T = {"bf16": torch.bfloat16, "fp32": torch.float32}
-BAD_INDEX = -10
+TIMEOUT, BAD_INDEX = -9, -10
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -203,6 +203,30 @@ def test_other_stream_and_captured_graph(dtype):
         torch.cuda.synchronize()
         for n in got:
             assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("fp32", 64, 300)])
+def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d, nq):
+    """With the copying warps switched off every consumer's first wait runs out: the
+    status reads TIMEOUT once, the kernels end, and the next calls are right."""
+    x = make(1, 2, 2, nq, 400, d, dtype, seed=12)
+    want = run(x, dtype=dtype)
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DenseParams.like(c["q"], c["k"])
+    o, lse = want["o"], want["lse"]
+    for call in (lambda: llsa.dense_forward(p, c["q"], c["k"], c["v"]),
+                 lambda: llsa.dense_backward(p, c["q"], c["k"], c["v"], o, lse, c["dout"])):
+        llsa.test_set_wait_limit(256, llsa.LLSA_TEST_NO_COPIES)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            llsa.test_set_wait_limit(0, 0)
+        assert llsa.llsa_get_status() == TIMEOUT
+        assert llsa.llsa_get_status() == 0
+    got = run(x, dtype=dtype)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
 
 
 def test_a_given_stream_orders_the_call():
