@@ -82,11 +82,12 @@ __device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMa
     for (int p = 0; p < 3; p++) tma_load_3d(smem_u32(dst + p * kPlane), map, 0, row, p * slices + slice, mbar);
 }
 
-__device__ __forceinline__ void store_rowpart(float* dst, const uint32_t* o, float f, int c0, int cols, int d) {
-    for (int c = 0; c < cols; c += 4)
+template <int COLS>
+__device__ __forceinline__ void store_rowpart(float* dst, const float* o, float f, int c0, int d) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 4)
         if (c0 + c < d) {
-            const float v[4] = {__uint_as_float(o[c]) * f, __uint_as_float(o[c + 1]) * f, __uint_as_float(o[c + 2]) * f,
-                                __uint_as_float(o[c + 3]) * f};
+            const float v[4] = {o[c] * f, o[c + 1] * f, o[c + 2] * f, o[c + 3] * f};
             store4(dst + c0 + c, v);
         }
 }
@@ -210,7 +211,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 #pragma unroll
                 for (int ks = 0; ks < 8; ks++)
                     mma_ts(leader, tO, tP + term_a(i) * 64 + ks * 8, dV + ((term_b(i) * kPlane + ks * 2048) >> 4), idO,
-                           t > 0 || i > 0 || ks > 0);
+                           i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->o_done));
             commit(leader, smem_u32(&bar->v_empty));
         }
@@ -224,56 +225,64 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const int r = r0 + warp * 32 + lane;
         int lim = (r < a.R ? dense_kend(a, sp, r < a.nq ? r : r % a.nq) : 0) - j_first;
         const float sl2 = a.scale * kDenseLog2e;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, acc[64];
+#pragma unroll
+        for (int i = 0; i < 64; i++) acc[i] = 0.f;
+        auto take_O = [&](int t) {  // adds the product of tile t to this row's sums
+            bar_wait(smem_u32(&bar->o_done), t & 1, abort_flag, a);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_nowait(tO + lanes + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i++) acc[c + i] += __uint_as_float(o[i]);
+            }
+            tc_fence_before();
+        };
         for (int t = 0; t < n; t++, lim -= BT) {
             const int b = t & 1;
+            const uint32_t tS = tbase + b * 128 + lanes;
             bar_wait(smem_u32(&bar->s_full[b]), (t >> 1) & 1, abort_flag, a);
             tc_fence_after();
-            uint32_t s[128];
+            const bool cut = __any_sync(0xffffffffu, lim < BT);
+            float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) tmem_ld32_nowait(tbase + b * 128 + lanes + c, s + c);
-            tmem_wait_ld();
-            tc_fence_before();
-            warp_arrive(smem_u32(&bar->s_free[b]), lane);
-            if (__any_sync(0xffffffffu, lim < BT)) {
+            for (int c = 0; c < 128; c += 32) {
+                uint32_t s[32];
+                tmem_ld32_nowait(tS + c, s);
+                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 128; c++) s[c] = c < lim ? s[c] : 0xff800000u;
+                for (int i = 0; i < 32; i++)
+                    if (!cut || c + i < lim) top = fmaxf(top, __uint_as_float(s[i]));
             }
-            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 128; c++) x[c & 3] = fmaxf(x[c & 3], __uint_as_float(s[c]));
-            // the reference follows the row's maximum exactly here: reading O back costs little beside six products
-            const float top = fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl2);
-            const bool grow = top > m;
-            const float f = grow ? ex2(m - top) : 1.f;
+            top = fmaxf(m, top * sl2);
+            const float f = top > m ? ex2(m - top) : 1.f;  // 2^-inf = 0 at a row's first keys
             m = top;
             l *= f;
-            if (t > 0) {  // O and the planes of P are at rest
-                bar_wait(smem_u32(&bar->o_done), (t - 1) & 1, abort_flag, a);
-                tc_fence_after();
-                if (__any_sync(0xffffffffu, grow)) {
+            if (t > 0) {  // then the planes of P may be written again
+                take_O(t - 1);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32_nowait(tO + lanes + c, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(tO + lanes + c, o);
-                    }
-                }
+                for (int i = 0; i < 64; i++) acc[i] *= f;
             }
             const float shift = m == -INFINITY ? 0.f : -m;
 #pragma unroll
             for (int c = 0; c < 128; c += 32) {
-                uint32_t p1[16], p2[16], p3[16];
+                uint32_t s[32], p1[16], p2[16], p3[16];
+                tmem_ld32_nowait(tS + c, s);
+                tmem_wait_ld();
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 32; i += 2) {
-                    const float e0 = exp2f(fmaf(__uint_as_float(s[c + i]), sl2, shift));
-                    const float e1 = exp2f(fmaf(__uint_as_float(s[c + i + 1]), sl2, shift));
-                    sum += e0 + e1;
-                    split2(e0, e1, p1[i >> 1], p2[i >> 1], p3[i >> 1]);
+                    float e[2];
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        e[k] = exp2f(fmaf(__uint_as_float(s[i + k]), sl2, shift));
+                        if (cut) e[k] = c + i + k < lim ? e[k] : 0.f;
+                    }
+                    sum += e[0] + e[1];
+                    split2(e[0], e[1], p1[i >> 1], p2[i >> 1], p3[i >> 1]);
                 }
                 l += sum;
                 tmem_st16(tP + lanes + (c >> 1), p1);
@@ -282,26 +291,14 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             }
             tmem_wait_st();
             tc_fence_before();
+            warp_arrive(smem_u32(&bar->s_free[b]), lane);
             warp_arrive(smem_u32(&bar->p_full), lane);
         }
-        if (n > 0) {
-            bar_wait(smem_u32(&bar->o_done), (n - 1) & 1, abort_flag, a);
-            tc_fence_after();
-        }
+        if (n > 0) take_O(n - 1);
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
         const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-            uint32_t o[32];
-#pragma unroll
-            for (int i = 0; i < 32; i++) o[i] = 0u;
-            if (n > 0) {
-                tmem_ld32_nowait(tO + lanes + c, o);
-                tmem_wait_ld();
-            }
-            if (r < a.R)
-                store_rowpart(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, o, inv, c, 32, a.d);
-        }
+        if (r < a.R)
+            store_rowpart<64>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv, 0, a.d);
         if (r < a.R) {
             if (a.splits > 1)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
@@ -326,11 +323,13 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 // covered by planes 1 and 2 of P and of dS once they are read, their planes 3 at
 // 256 and 320, the sums at 384.
 constexpr int kBwdWarps = 16, kCols = 32;
-constexpr int kBwdThreads = (kBwdWarps + 4) * 32;
+// 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
+// 104 of them, the 128 others keep 64.
+constexpr int kBwdThreads = (kBwdWarps + 4) * 32, kRegsElementwise = 104, kRegsOther = 64;
 constexpr int kBwdSmem = kTile * 4 + 2 * BT * 4 + 512;
 
 struct BwdBars {
-    uint64_t x_full[2], y_full[2], y_empty[2], s_full, dp_full, ds_ready, acc_full, drain;
+    uint64_t x_full[2], y_full[2], y_empty[2], s_full, dp_full, ds_ready, acc_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -377,6 +376,7 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
         mbar_init(smem_u32(&bar->dp_full), 1);
         mbar_init(smem_u32(&bar->ds_ready), kBwdWarps);
         mbar_init(smem_u32(&bar->acc_full), 1);
+        mbar_init(smem_u32(&bar->acc_free), kBwdWarps);
         mbar_init(smem_u32(&bar->drain), 1);
         bar->abort_flag = 0;
         fence_mbar_init();
@@ -388,99 +388,104 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t tDP = tbase + 128, tP3 = tbase + 256, tS3 = tbase + 320, tAcc = tbase + 384;
 
-    if (warp == kBwdWarps + 1 || warp == kBwdWarps + 2) {
-        // ----------------------------------------------------------- copies
-        if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
-            const int k = warp - kBwdWarps - 1;
-            load_planes(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
-            const uint32_t full = smem_u32(&bar->y_full[k]);
-            int n = 0;
-            for (Items<KEYS> it = start; !it.done(); it.next(a)) {
-                if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
-                if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
-                    const long long row = (long long)slice * a.Rp + it.pos;
-                    mbar_arrive_expect_tx(full, kTile + 2 * BT * 4);
-                    for (int p = 0; p < 3; p++)
-                        tma_load_3d(smem_u32(sY + kTile + p * kPlane), &my2, 0, it.pos, p * a.slices + slice, full);
-                    bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
-                    bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
-                } else {
-                    load_planes(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
-                }
-                n++;
-            }
-            // copies still in flight must land before the block exits
-            land(smem_u32(&bar->x_full[k]), 0);
-            if (n > 0) land(full, (n - 1) & 1);
-        }
-    } else if (warp == kBwdWarps) {
-        // ------------------------------------------------------- MMA issuer
-        const uint32_t leader = elect_lane();
-        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, 64, 0, 1);
-        const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024), dY = desc_sw128(smem_u32(sY), 16, 1024);
-        const uint64_t dM = desc_sw128(smem_u32(sY), kPlane, 1024);  // the streamed tiles read along their rows
-        // rows whose P and dS are 0 by the lengths may hold anything: cleared, as they meet those zeros in the sums
-        auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
-            if constexpr (KEYS) {
-                if (it.all || it.t0 + BT <= it.sp.lq) return;
-                int t = it.t0 + lane;
-                for (int x = lane; x < BT; x += 32, t += 32)
-                    if (t % a.nq >= it.sp.lq)
+    if (warp >= kBwdWarps) {
+        regs_dec<kRegsOther>();
+        if (warp == kBwdWarps + 1 || warp == kBwdWarps + 2) {
+            // ----------------------------------------------------------- copies
+            if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+                const int k = warp - kBwdWarps - 1;
+                load_planes(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
+                const uint32_t full = smem_u32(&bar->y_full[k]);
+                int n = 0;
+                for (Items<KEYS> it = start; !it.done(); it.next(a)) {
+                    if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
+                    if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
+                        const long long row = (long long)slice * a.Rp + it.pos;
+                        mbar_arrive_expect_tx(full, kTile + 2 * BT * 4);
                         for (int p = 0; p < 3; p++)
-                            for (int e = 0; e < 8; e++)
-                                reinterpret_cast<uint4*>(tile + p * kPlane + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                const int live = it.sp.lk - it.pos;
-                if (live >= BT) return;
-                for (int p = 0; p < 3; p++)
-                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
-                        reinterpret_cast<uint4*>(tile + p * kPlane)[x] = make_uint4(0u, 0u, 0u, 0u);
+                            tma_load_3d(smem_u32(sY + kTile + p * kPlane), &my2, 0, it.pos, p * a.slices + slice, full);
+                        bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
+                        bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
+                    } else {
+                        load_planes(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                    }
+                    n++;
+                }
+                // copies still in flight must land before the block exits
+                land(smem_u32(&bar->x_full[k]), 0);
+                if (n > 0) land(full, (n - 1) & 1);
             }
-            fence_async_smem();
-            __syncwarp();
-        };
-        bool ok = any && warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
-                  warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
-        int n = 0;
-        for (Items<KEYS> it = start; ok && !it.done(); it.next(a), n++) {
-            // S and dP: the sums that used up what lies over them were issued before
-            for (int k = 0; k < 2 && ok; k++) {
-                ok = warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a);
+        } else if (warp == kBwdWarps) {
+            // ------------------------------------------------------- MMA issuer
+            const uint32_t leader = elect_lane();
+            constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idA = idesc_bf16(BT, 64, 0, 1);
+            const uint64_t dX = desc_sw128(smem_u32(sX), 16, 1024), dY = desc_sw128(smem_u32(sY), 16, 1024);
+            const uint64_t dM = desc_sw128(smem_u32(sY), kPlane, 1024);  // the streamed tiles read along their rows
+            // rows whose P and dS are 0 by the lengths may hold anything: cleared, as they meet those zeros in the sums
+            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
+                if constexpr (KEYS) {
+                    if (it.all || it.t0 + BT <= it.sp.lq) return;
+                    int t = it.t0 + lane;
+                    for (int x = lane; x < BT; x += 32, t += 32)
+                        if (t % a.nq >= it.sp.lq)
+                            for (int p = 0; p < 3; p++)
+                                for (int e = 0; e < 8; e++)
+                                    reinterpret_cast<uint4*>(tile + p * kPlane + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const int live = it.sp.lk - it.pos;
+                    if (live >= BT) return;
+                    for (int p = 0; p < 3; p++)
+                        for (int x = live * 8 + lane; x < BT * 8; x += 32)
+                            reinterpret_cast<uint4*>(tile + p * kPlane)[x] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                __syncwarp();
+            };
+            bool ok = any && warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
+                      warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
+            int n = 0;
+            for (Items<KEYS> it = start; ok && !it.done(); it.next(a), n++) {
+                // S and dP: the sums that used up what lies over them were issued before
+                for (int k = 0; k < 2 && ok; k++) {
+                    ok = warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a);
+                    if (!ok) break;
+                    if (k == 0 || KEYS) clear_rows(sY + k * kTile, it);  // V only enters dP, which the mask covers
+                    tc_fence_after();
+#pragma unroll
+                    for (int i = 0; i < 6; i++)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ks++)
+                            mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
+                                   dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+                    commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+                }
+                ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
+                if (ok && n > 0) ok = warp_wait(smem_u32(&bar->acc_free), (n - 1) & 1, abort_flag, a);
                 if (!ok) break;
-                if (k == 0 || KEYS) clear_rows(sY + k * kTile, it);  // V only enters dP, which the mask covers
                 tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < 6; i++)
+                for (int i = 0; i < 6; i++) {
+                    const int pa = term_a(i);
+                    const uint32_t opP = pa == 2 ? tP3 : tbase + pa * 64, opS = pa == 2 ? tS3 : tDP + pa * 64;
 #pragma unroll
-                    for (int ks = 0; ks < 4; ks++)
-                        mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
-                               dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
-                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
-            }
-            ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll
-            for (int i = 0; i < 6; i++) {
-                const int pa = term_a(i);
-                const uint32_t opP = pa == 2 ? tP3 : tbase + pa * 64, opS = pa == 2 ? tS3 : tDP + pa * 64;
-#pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    const uint64_t m = dM + ((term_b(i) * kPlane + ks * 2048) >> 4);
-                    mma_ts(leader, tAcc, opS + ks * 8, m, idA, n > 0 || i > 0 || ks > 0);
-                    if (KEYS) mma_ts(leader, tAcc + 64, opP + ks * 8, m + (kTile >> 4), idA, n > 0 || i > 0 || ks > 0);
+                    for (int ks = 0; ks < 8; ks++) {
+                        const uint64_t m = dM + ((term_b(i) * kPlane + ks * 2048) >> 4);
+                        mma_ts(leader, tAcc, opS + ks * 8, m, idA, i > 0 || ks > 0);
+                        if (KEYS) mma_ts(leader, tAcc + 64, opP + ks * 8, m + (kTile >> 4), idA, i > 0 || ks > 0);
+                    }
                 }
+                commit(leader, smem_u32(&bar->y_empty[0]));
+                commit(leader, smem_u32(&bar->y_empty[1]));
+                commit(leader, smem_u32(&bar->acc_full));
             }
-            commit(leader, smem_u32(&bar->y_empty[0]));
-            commit(leader, smem_u32(&bar->y_empty[1]));
+            // no MMA may be in flight when tensor memory is released
+            commit(leader, smem_u32(&bar->drain));
+            if (lane == 0) land(smem_u32(&bar->drain), 0);
+            __syncwarp();
         }
-        if (ok) commit(leader, smem_u32(&bar->acc_full));
-        // no MMA may be in flight when tensor memory is released
-        commit(leader, smem_u32(&bar->drain));
-        if (lane == 0) land(smem_u32(&bar->drain), 0);
-        __syncwarp();
-    } else if (warp < kBwdWarps) {
+    } else {
         // ---------------------------------------- elementwise, epilogue
+        regs_inc<kRegsElementwise>();
         const int w = warp >> 2, q4 = warp & 3;  // quarter of the columns, of the rows
         const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
         const int x = x0 + q4 * 32 + lane;       // stationary row
@@ -492,8 +497,27 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
             nd = a.nd[(long long)slice * a.Rp + x];
             kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
         }
+        float acc[KEYS ? 2 : 1][16];  // this row's sums, 16 columns of each
+#pragma unroll
+        for (int k = 0; k < (KEYS ? 2 : 1); k++)
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc[k][i] = 0.f;
+        auto take_sums = [&](int item) {
+            bar_wait(smem_u32(&bar->acc_full), item & 1, abort_flag, a);
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < (KEYS ? 2 : 1); k++) {
+                float o[16];
+                tmem_ld16(tAcc + k * 64 + w * 16 + lanes, o);
+#pragma unroll
+                for (int i = 0; i < 16; i++) acc[k][i] += o[i];
+            }
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->acc_free), lane);
+        };
         int n = 0;
         for (Items<KEYS> it = start; !it.done(); it.next(a), n++) {
+            if (n > 0) take_sums(n - 1);  // while S and dP of this item are made
             uint32_t s[kCols], g[kCols];
             bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
             tc_fence_after();
@@ -539,23 +563,17 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
             tc_fence_before();
             warp_arrive(smem_u32(&bar->ds_ready), lane);
         }
-        if (any) {
-            bar_wait(smem_u32(&bar->acc_full), 0, abort_flag, a);
-            tc_fence_after();
-        }
+        if (n > 0) take_sums(n - 1);
         // rows without a gradient hold whatever their padding made: zero
         const bool live = any && (KEYS ? x < sp.lk : kend > 0);
         const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
 #pragma unroll
         for (int k = 0; k < (KEYS ? 2 : 1); k++) {
-            float o[16];
-            if (any) tmem_ld16(tAcc + k * 64 + w * 16 + lanes, o);
-            uint32_t u[16];
 #pragma unroll
-            for (int i = 0; i < 16; i++) u[i] = live ? __float_as_uint(o[i]) : 0u;
+            for (int i = 0; i < 16; i++) acc[k][i] = live ? acc[k][i] : 0.f;
             float* base = a.splits > 1 ? a.part + (k * a.splits + part) * all * a.d
                                        : static_cast<float*>(KEYS ? (k == 0 ? a.dk : a.dv) : a.dq);
-            if (x < extent) store_rowpart(base + row * a.d, u, k == 0 ? a.scale : 1.f, w * 16, 16, a.d);
+            if (x < extent) store_rowpart<16>(base + row * a.d, acc[k], k == 0 ? a.scale : 1.f, w * 16, a.d);
         }
     }
     tc_fence_before();
