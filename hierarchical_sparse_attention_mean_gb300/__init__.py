@@ -205,6 +205,10 @@ class DenseParams:
                          _choice(_DTYPES, self.dtype, "dtype"), 1 if self.causal else 0, self.scale)
         self.__dict__.update(_c=c, _ref=ctypes.byref(c), _ws={})
 
+    def __reduce__(self):  # copies and pickles build their own C structure
+        return DenseParams, (self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, self.causal, self.dtype,
+                             self.scale)
+
     def c(self) -> _DenseParams:
         return self._c
 
@@ -530,7 +534,9 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
             raise ValueError("k and k_out must be None where kv_heads is 0")
         at, batched = None, False
         if pos is not None:
-            shape = tuple(pos.shape) + (1,) if p.axes == 1 and pos.ndim < 3 and pos.shape[-1:] == (p.n,) else tuple(pos.shape)
+            shape = tuple(pos.shape)
+            if p.axes == 1 and shape in ((p.n,), (p.batch, p.n)) and shape != (p.n, 1):
+                shape += (1,)
             if shape == (p.batch, p.n, p.axes):
                 batched = True
             elif shape != (p.n, p.axes):
@@ -680,26 +686,31 @@ def backward(p: Params, q, k, v, dout, b: Buffers, dq=None, dk=None, dv=None, st
     return dq, dk, dv
 
 
-def _dense_ws(p: DenseParams, op: int, device, stream):
-    """The workspace of one call (None where it needs none), kept until `stream` is done with it."""
+def _dense_ws(p: DenseParams, op: int, device):
+    """The workspace of one call (None where it needs none)."""
     need = dense_workspace_bytes(p, op)
     if need == 0:
         return None
     import torch
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    if stream is not None:
-        ws.record_stream(_as_stream(stream, device))
-    return ws
+    return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def _under(stream, device):
+    """What is allocated for a call belongs to the call's stream, whose order then
+    keeps it from being used again too early."""
+    import torch
+    return _HERE if stream is None else torch.cuda.stream(_as_stream(stream, device))
 
 
 def dense_forward(p: DenseParams, q, k, v, q_len=None, k_len=None, o=None, lse=None, ws=None, stream=None):
     """Dense attention of q over k, v. Returns (o, lse); what is not given is
-    allocated here."""
+    allocated here, on `stream` (None: the current one)."""
     import torch
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty(p.shapes()[2], dtype=torch.float32, device=q.device) if lse is None else lse
-    ws = _dense_ws(p, OP_DENSE_FWD, q.device, stream) if ws is None else ws
-    llsa_dense_fwd(p, q, k, v, o, lse, q_len, k_len, ws, stream)
+    with _under(stream, q.device):
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty(p.shapes()[2], dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _dense_ws(p, OP_DENSE_FWD, q.device) if ws is None else ws
+        llsa_dense_fwd(p, q, k, v, o, lse, q_len, k_len, ws, stream)
     return o, lse
 
 
@@ -707,11 +718,12 @@ def dense_backward(p: DenseParams, q, k, v, o, lse, dout, q_len=None, k_len=None
                    stream=None):
     """Gradients of dense_forward(). Returns (dq, dk, dv)."""
     import torch
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    ws = _dense_ws(p, OP_DENSE_BWD, q.device, stream) if ws is None else ws
-    llsa_dense_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, q_len, k_len, ws, stream)
+    with _under(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        ws = _dense_ws(p, OP_DENSE_BWD, q.device) if ws is None else ws
+        llsa_dense_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, q_len, k_len, ws, stream)
     return dq, dk, dv
 
 

@@ -162,3 +162,16 @@ def test_binding_refuses_host_tensors(lib):
         llsa.rotary(x, x)
     with pytest.raises(TypeError):
         llsa.llsa_rope(llsa.RopeParams.like(x), None, None, x, None)
+
+
+def test_parameters_copy_and_pickle(lib):
+    import copy
+    import dataclasses
+    import pickle
+    p = llsa.DenseParams(2, 4, 100, 90, 64, kv_heads=2, causal=True, scale=0.5)
+    r = llsa.RopeParams(2, 4, 256, 64, kv_heads=2, axes=2, width=16, token_order="tile")
+    r.c(), r.c(True), llsa.dense_workspace_bytes(p, llsa.OP_DENSE_BWD)
+    for x in (p, r):
+        for y in (copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x)), dataclasses.replace(x)):
+            assert y == x and bytes(y.c()) == bytes(x.c())
+    assert dataclasses.replace(p, nq=7).c().nq == 7 and p.c().nq == 100

@@ -204,3 +204,14 @@ def test_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_one_token_positions():
+    """[n, axes] with one token serves every entry; [batch, n] gives each its own."""
+    q = rand((3, 2, 1, 64), "fp32", 30)
+    qc = q.cuda()
+    p = llsa.RopeParams.like(qc)
+    for pos, full in (([[7]], [[[7]]]), ([7], [[[7]]]), ([[7], [8], [-9]], [[[7]], [[8]], [[-9]]])):
+        out = torch.empty_like(qc)
+        llsa.llsa_rope(p, qc, None, out, None, pos=torch.tensor(pos, dtype=torch.int32, device="cuda"))
+        ref.check("out", out, ref.rotary(q, torch.tensor(full), dtype=torch.float32))
