@@ -353,3 +353,116 @@ def test_rotary_before_the_sparse_attention(dtype):
     assert torch.equal(o, o2)
     for a, b in zip(got, (dq, dk, dv)):
         assert torch.equal(a, b)
+
+
+SEVERAL = [
+    # b, h, kv, nq, nk, d, causal: more pieces of work than SMs, so resident blocks take several one after the other
+    (8, 16, 16, 300, 333, 64, False),
+    (16, 12, 12, 200, 260, 64, True),      # one piece per slice forward: a last round in halves
+    (10, 16, 16, 256, 130, 64, False),
+    (20, 16, 8, 70, 70, 40, True),
+    (10, 16, 16, 150, 140, 128, True),
+    (4, 40, 40, 260, 129, 96, False),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("b,h,kv,nq,nk,d,causal", SEVERAL)
+def test_blocks_take_several_pieces(b, h, kv, nq, nk, d, causal, ragged, dtype):
+    """Also with lengths that leave pieces of every kind between the full ones:
+    empty ones, ones without queries or without keys, and partial tiles."""
+    ql = [(nq, 0, 1, nq - 1, nq // 2)[e % 5] for e in range(b)] if ragged else None
+    kl = [(nk - 1, nk, nk // 3, 0, nk, 1, nk)[e % 7] for e in range(b)] if ragged else None
+    x = make(b, h, kv, nq, nk, d, dtype, ql, kl, seed=11)
+    want = ref.attention(**x, causal=causal, q_len=ql, k_len=kl, dtype=T[dtype])
+    got = run(x, causal, 0.0, ql, kl, dtype)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [8, 64, 128, 136, 256])
+@pytest.mark.parametrize("h,kv,nq", [(1, 1, 1), (2, 2, 1), (2, 1, 1), (3, 1, 1), (4, 2, 2), (5, 1, 1), (2, 1, 4), (3, 1, 3)])
+def test_few_rows(h, kv, nq, d, dtype):
+    """One to nine rows per key head, where the choice of kernels changes."""
+    x = make(2, h, kv, nq, 700, d, dtype, None, [700, 531], seed=13)
+    want = ref.attention(**x, causal=True, k_len=[700, 531], dtype=T[dtype])
+    got = run(x, True, 0.0, None, [700, 531], dtype)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("d", [8, 24, 40, 64])
+@pytest.mark.parametrize("nq,nk", [(127, 129), (128, 128), (129, 128), (5, 3277), (3277, 5), (1, 16384)])
+def test_fp32_around_the_choice_of_kernels(nq, nk, d):
+    """Pairs of a slice just below and above the number from which fp32 runs on the tensor cores."""
+    x = make(1, 2, 2, nq, nk, d, "fp32", seed=14)
+    want = ref.attention(**x, dtype=torch.float32)
+    got = run(x, dtype="fp32")
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+def test_fp32_magnitudes():
+    """The bf16 pieces of fp32 operands keep the exponent range: large, small and mixed values."""
+    x = make(1, 2, 2, 200, 150, 64, "fp32", seed=15)
+    big = torch.tensor([2.0 ** 60, 2.0 ** -60]).repeat(75)[:, None]
+    x["v"] = x["v"] * big
+    x["q"], x["k"] = x["q"] * 2.0 ** 40, x["k"] * 2.0 ** -40
+    x["dout"] = x["dout"] * 2.0 ** -20
+    want = ref.attention(**x, dtype=torch.float32)
+    got = run(x, dtype="fp32")
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_two_streams_at_once(dtype, d):
+    """Calls on two streams, workspaces of their own, give what they give alone."""
+    xs = [make(2, 8, 4, 260, 3000, d, dtype, seed=s) for s in (20, 21)]
+    want = [run(x, dtype=dtype) for x in xs]
+    cs = [{n: t.cuda() for n, t in x.items()} for x in xs]
+    p = llsa.DenseParams.like(cs[0]["q"], cs[0]["k"])
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for c, st, out in zip(cs, streams, got):
+            o, lse = llsa.dense_forward(p, c["q"], c["k"], c["v"], stream=st)
+            # a stream may be given by its number too
+            out.append((o, lse, *llsa.dense_backward(p, c["q"], c["k"], c["v"], o, lse, c["dout"], stream=st.cuda_stream)))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    for outs, w in zip(got, want):
+        for out in outs:
+            for t, n in zip(out, ("o", "lse", "dq", "dk", "dv")):
+                assert torch.equal(t, w[n]), n
+
+
+def test_captured_autograd_step():
+    """rope, attention and their gradients captured on leaves of the capture's own,
+    replayed on new inputs, while an eager graph of the same tensors lives."""
+    x, y = (make(2, 4, 2, 256, 256, 64, "bf16", seed=s) for s in (22, 23))
+    c = {n: t.cuda() for n, t in x.items()}
+    rope = llsa.RopeParams.like(c["q"], c["k"], axes=2, width=16, token_order="tile")
+
+    def step(c):
+        leaves = [c[n].detach().requires_grad_() for n in ("q", "k", "v")]
+        o = llsa.dense_attention(*leaves, rope=rope)
+        return (o, *torch.autograd.grad(o, leaves, c["dout"]))
+
+    want = [[t.detach().clone() for t in step({n: t.cuda() for n, t in z.items()})] for z in (x, y)]
+    alive = llsa.dense_attention(*(c[n].detach().requires_grad_() for n in ("q", "k", "v")), rope=rope)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(c)
+    for z, w in zip((x, y), want):
+        for n in c:
+            c[n].copy_(z[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
+    assert torch.equal(alive, want[0][0])
