@@ -154,8 +154,7 @@ DenseSplit dense_tc_fwd_split(const DenseShape& s);
 DenseSplit dense_tc_dq_split(const DenseShape& s);
 DenseSplit dense_tc_dkv_split(const DenseShape& s);
 int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
-int launch_dense_tc_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
-int launch_dense_tc_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st);
 
 // dense_split_tc.cu: fp32 on the tensor cores, d <= 64 (planes: three bf16 planes
 // of q, k, v, or of q, dout, k, v, at the start of the workspace).
@@ -165,7 +164,7 @@ DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st);
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st);
-int launch_dense_split_dq(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st);
-int launch_dense_split_dkv(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st);
+int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
+                           cudaStream_t st);
 
 }  // namespace llsa

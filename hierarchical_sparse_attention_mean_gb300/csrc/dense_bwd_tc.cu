@@ -3,14 +3,16 @@
 //
 // Mathematics, with l2 = lse * log2(e) and D = dout . o of every query row from
 // the pass before: P = 2^(scale log2(e) q.k - l2), dS = P (dout.v - D),
-//   dq = scale dS K          one kernel, blocks own 128 query rows,
-//   dk = scale dS^T Q, dv = P^T dO   the other, blocks own 128 keys.
+//   dq = scale dS K          by blocks that own 128 query rows,
+//   dk = scale dS^T Q, dv = P^T dO   by blocks that own 128 keys.
 // Every sum has one owner and a fixed order, so results repeat bit by bit. One
-// kernel for all three gradients would save two of seven matrix products per
+// pass for all three gradients would save two of seven matrix products per
 // tile, at the price of adding dq up across blocks in memory in whatever order
 // they run.
 //
-// Both kernels are one: 128 stationary rows (X1, X2) against a stream of tiles of
+// Both kinds of blocks run in one launch, so that one kind fills the SMs that the
+// other leaves (12 heads x 4,096 tokens 170 us in two launches, 154 in one; d = 128,
+// 16 heads over 4 of 4,095 tokens, causal, 275 and 197). Their code is one: 128 stationary rows (X1, X2) against a stream of tiles of
 // 128 rows (Y1, Y2), with (X1, X2, Y1, Y2) = (Q, dO, K, V) or (K, V, Q, dO). Per
 // item: S = X1 Y1^T, dP = X2 Y2^T (128 x 128 fp32 in tensor memory), then P and
 // dS as bf16 over dP's columns, then acc1 += dS Y1 and, for keys, acc2 += P Y2,
@@ -27,6 +29,11 @@
 // the work: while the elementwise warps finish one piece, the others load and
 // multiply for the next. At 128 columns shared memory holds one pair of
 // stationary tiles, and every piece gets a block of its own.
+//
+// Bound by the chain of an item at 64 columns (S, exp, dP, dS, stores; 0.72 us against
+// 0.40 us of the tensor cores' time for an item of rows) and by the tensor cores at 128.
+// 19 slices of 16,384 tokens: 3.2 ms at d = 64 (1,020 TFLOP/s of the 10 d
+// operations per pair), 5.1 ms at d = 128 (1,270).
 //
 // Roles: warps 0-15 elementwise and epilogue, warps 16 and 17 issue the MMAs,
 // warps 18 and 19 the copies of the two streams.
@@ -111,12 +118,11 @@ struct Piece {
     }
 };
 
+// Block `block` of the `blocks` that share the pieces of rows or of keys.
 template <int D, bool KEYS>
-__global__ void __launch_bounds__(kThreads, 1)
-dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
-                    const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2,
-                    const __grid_constant__ CUtensorMap mz1, const __grid_constant__ CUtensorMap mz2,
-                    const __grid_constant__ DenseArgs a) {
+__device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorMap& mx2, const CUtensorMap& my1,
+                                         const CUtensorMap& my2, const CUtensorMap& mz1, const CUtensorMap& mz2,
+                                         const DenseArgs& a, int block, int blocks) {
     using C = Cfg<D, KEYS>;
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char* sX = sm;  // [NX] X1, X2
@@ -132,7 +138,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
         return;
     }
     const int extent = KEYS ? a.nk : a.R;
-    const int mine = (a.pieces - blockIdx.x + gridDim.x - 1) / gridDim.x;  // pieces blockIdx.x, + gridDim.x, ...
+    const int mine = dealt_pieces(a, block, blocks);
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
@@ -189,7 +195,7 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
                 for (int i = 0; ok && i < mine; i++) {
                     Piece<KEYS> pc;
                     if (k == 0) {
-                        pc.make(a, blockIdx.x + i * gridDim.x);
+                        pc.make(a, dealt(a, i, block, blocks));
                         ok = pc.put(&bar->pieces, i, abort_flag, a);
                     } else {
                         ok = pc.template get<1>(&bar->pieces, i, lane, abort_flag, a);
@@ -561,29 +567,78 @@ dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_consta
     }
 }
 
-template <int D, bool KEYS>
-int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
-    using C = Cfg<D, KEYS>;
-    static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
-    CUtensorMap mq, mk, mv, mg, z1, z2;
-    LLSA_TRY(make_tmap_rows(&mq, a.q, s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mg, a.dout, s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mk, a.k, s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mv, a.v, s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&z1, KEYS ? a.dk : a.dq, s.slices, KEYS ? s.nk : s.R, s.d, 32));
-    LLSA_TRY(make_tmap_rows(&z2, KEYS ? a.dv : a.dq, s.slices, KEYS ? s.nk : s.R, s.d, 32));
-    cudaFuncSetAttribute(dense_bwd_tc_kernel<D, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    const int extent = KEYS ? s.nk : s.R;
-    const long long pieces = (long long)((extent + BT - 1) / BT) * s.slices * a.splits;
-    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    a.pieces = (int)pieces;
-    const int grid = C::NX > 1 ? (int)std::min<long long>(pieces, sm_count()) : (int)pieces;
-    if constexpr (KEYS)
-        LLSA_LAUNCH("dense_dkv_tc", st,
-                    dense_bwd_tc_kernel<D, true><<<grid, kThreads, C::SMEM, st>>>(mk, mv, mq, mg, z1, z2, a));
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                    const __grid_constant__ CUtensorMap zq, const __grid_constant__ CUtensorMap zk,
+                    const __grid_constant__ CUtensorMap zv, const __grid_constant__ DenseArgs aq,
+                    const __grid_constant__ DenseArgs ak, int key_blocks) {
+    const int block = blockIdx.x;
+    if (block < key_blocks)
+        bwd_side<D, true>(mk, mv, mq, mg, zk, zv, ak, block, key_blocks);
     else
-        LLSA_LAUNCH("dense_dq_tc", st,
-                    dense_bwd_tc_kernel<D, false><<<grid, kThreads, C::SMEM, st>>>(mq, mg, mk, mv, z1, z2, a));
+        bwd_side<D, false>(mq, mg, mk, mv, zq, zq, aq, block - key_blocks, (int)gridDim.x - key_blocks);
+}
+
+// Resident blocks for the pieces of keys (pk, of ck each) beside those for the pieces
+// of rows (pq, of cq): the share under which the last of both ends first. All of
+// them, for two launches one after the other, where each side's pieces fill their
+// rounds so well that this takes less than the share, `gap` included. In causal
+// order pieces differ and even each other out over the rounds.
+int share_blocks(long long pk, long long ck, long long pq, long long cq, long long gap, int blocks, bool causal) {
+    if (pk + pq <= blocks) return (int)pk;
+    auto time = [&](long long pieces, long long each, int b) {
+        return causal ? (pieces * each + b - 1) / b : (pieces + b - 1) / b * each;
+    };
+    int best = blocks;
+    long long least = time(pk, ck, blocks) + time(pq, cq, blocks) + gap;
+    for (int b = 1; b < blocks; b++) {
+        const long long t = std::max(time(pk, ck, b), time(pq, cq, blocks - b));
+        if (t < least) {
+            least = t;
+            best = b;
+        }
+    }
+    return best;
+}
+
+template <int D>
+int launch(const DenseShape& s, DenseArgs aq, DenseArgs ak, cudaStream_t st) {
+    using K = Cfg<D, true>;
+    using Q = Cfg<D, false>;
+    constexpr int smem = K::SMEM > Q::SMEM ? K::SMEM : Q::SMEM;
+    static_assert(smem <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
+    CUtensorMap mq, mk, mv, mg, zq, zk, zv;
+    LLSA_TRY(make_tmap_rows(&mq, aq.q, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mg, aq.dout, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mk, aq.k, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mv, aq.v, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&zq, aq.dq, s.slices, s.R, s.d, 32));
+    LLSA_TRY(make_tmap_rows(&zk, aq.dk, s.slices, s.nk, s.d, 32));
+    LLSA_TRY(make_tmap_rows(&zv, aq.dv, s.slices, s.nk, s.d, 32));
+    cudaFuncSetAttribute(dense_bwd_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;
+    const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.splits;
+    if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    aq.pieces = (int)pq;
+    ak.pieces = (int)pk;
+    if constexpr (K::NX == 1) {
+        LLSA_LAUNCH("dense_bwd_tc", st, dense_bwd_tc_kernel<D><<<(unsigned)(pq + pk), kThreads, smem, st>>>(
+                                            mq, mg, mk, mv, zq, zk, zv, aq, ak, (int)pk));
+        return LLSA_OK;
+    }
+    // An item of keys takes 0.77 us, one of rows 0.72 us (19 slices of 16,384 tokens), a
+    // piece about three items' time more (152 slices with one item per piece), and
+    // a second launch that of seven.
+    const long long ck = 16 * ((std::min(ak.chunk, s.R) + BT - 1) / BT + 3), cq = 15 * ((std::min(aq.chunk, s.nk) + BT - 1) / BT + 3);
+    const int grid = (int)std::min<long long>(pq + pk, sm_count());
+    const int share = share_blocks(pk, ck, pq, cq, 7 * 16, grid, s.causal);
+    LLSA_LAUNCH("dense_bwd_tc", st,
+                dense_bwd_tc_kernel<D><<<grid, kThreads, smem, st>>>(mq, mg, mk, mv, zq, zk, zv, aq, ak, share));
+    if (share == grid)
+        LLSA_LAUNCH("dense_bwd_tc", st,
+                    dense_bwd_tc_kernel<D><<<grid, kThreads, smem, st>>>(mq, mg, mk, mv, zq, zk, zv, aq, ak, 0));
     return LLSA_OK;
 }
 
@@ -596,11 +651,8 @@ DenseSplit dense_tc_dkv_split(const DenseShape& s) {
     return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT), s.R, BT, 2);
 }
 
-int launch_dense_tc_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    return s.d <= 64 ? launch<64, false>(s, a, st) : launch<128, false>(s, a, st);
-}
-int launch_dense_tc_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    return s.d <= 64 ? launch<64, true>(s, a, st) : launch<128, true>(s, a, st);
+int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
+    return s.d <= 64 ? launch<64>(s, aq, ak, st) : launch<128>(s, aq, ak, st);
 }
 
 }  // namespace llsa

@@ -123,7 +123,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
     // broadcast, so that the compiler knows these as the same in a whole warp
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-    const int mine = (a.pieces - blockIdx.x + gridDim.x - 1) / gridDim.x;  // pieces blockIdx.x, + gridDim.x, ...
+    const int mine = dealt_pieces(a, blockIdx.x, gridDim.x);
     if (threadIdx.x == 0) {
         for (int i = 0; i < 4; i++) {
             mbar_init(smem_u32(&bar->k_full[i]), 1);
@@ -178,7 +178,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 for (int i = 0; ok && i < mine; i++) {
                     Piece pc;
                     if (keys) {
-                        pc.make(a, blockIdx.x + i * gridDim.x);
+                        pc.make(a, dealt(a, i, blockIdx.x, gridDim.x));
                         ok = pc.put(&bar->pieces, i, abort_flag, a);
                     } else {
                         ok = pc.get<1>(&bar->pieces, i, lane, abort_flag, a);

@@ -316,7 +316,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 
 // --------------------------------------------------------------- backward --
 
-// As the bf16 kernel: 128 stationary rows (X1, X2) = (Q, dO) or (K, V) against a
+// As the bf16 kernel, rows and keys in one launch too: 128 stationary rows (X1, X2) = (Q, dO) or (K, V) against a
 // stream (Y1, Y2) of the others. Shared memory holds one tile of each, so an item's
 // copies, its S and dP, the elementwise work and its sums follow one another; the
 // tensor cores carry most of that time. Tensor memory: S at 0, dP at 128, both
@@ -335,10 +335,8 @@ struct BwdBars {
 };
 
 template <bool KEYS>
-__global__ void __launch_bounds__(kBwdThreads, 1)
-dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_constant__ CUtensorMap mx2,
-                       const __grid_constant__ CUtensorMap my1, const __grid_constant__ CUtensorMap my2,
-                       const __grid_constant__ DenseArgs a) {
+__device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorMap& mx2, const CUtensorMap& my1,
+                                         const CUtensorMap& my2, const DenseArgs& a, int piece) {
     extern __shared__ __align__(1024) unsigned char sm[];
     unsigned char *sX = sm, *sY = sm + 2 * kTile;
     float* stats = reinterpret_cast<float*>(sm + 4 * kTile);  // KEYS: -l2 and -D of the item's rows
@@ -350,7 +348,7 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
         return;
     }
     const int extent = KEYS ? a.nk : a.R;
-    const DenseWork work = dense_work(a, blockIdx.x, (extent + BT - 1) / BT);
+    const DenseWork work = dense_work(a, piece, (extent + BT - 1) / BT);
     const int slice = work.slice, part = work.part;
     const int x0 = (a.causal && !KEYS ? work.blocks - 1 - work.block : work.block) * BT;
     const DenseSpan sp = dense_span(a, slice);
@@ -584,6 +582,17 @@ dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mx1, const __grid_con
     }
 }
 
+__global__ void __launch_bounds__(kBwdThreads, 1)
+dense_bwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
+                       const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                       const __grid_constant__ DenseArgs aq, const __grid_constant__ DenseArgs ak, int key_pieces) {
+    const int piece = blockIdx.x;
+    if (piece < key_pieces)
+        bwd_side<true>(mk, mv, mq, mg, ak, piece);
+    else
+        bwd_side<false>(mq, mg, mk, mv, aq, piece - key_pieces);
+}
+
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 // Planes of `n` tensors of sizes q_elems (first `nq` ones) or k_elems, laid out one after the other.
@@ -657,31 +666,21 @@ int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, v
     return LLSA_OK;
 }
 
-template <bool KEYS>
-static int launch_bwd(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
+int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
+                           cudaStream_t st) {
     CUtensorMap mq, mg, mk, mv;
     LLSA_TRY(make_tmap_rows(&mq, planes[0], 3LL * s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mg, planes[1], 3LL * s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mk, planes[2], 3LL * s.slices, s.nk, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mv, planes[3], 3LL * s.slices, s.nk, s.d, BT));
     static_assert(kBwdSmem <= 227 * 1024 && sizeof(BwdBars) <= 512, "shared memory budget");
-    cudaFuncSetAttribute(dense_bwd_split_kernel<KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
-    const long long pieces = (long long)(((KEYS ? s.nk : s.R) + BT - 1) / BT) * s.slices * a.splits;
-    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    if constexpr (KEYS)
-        LLSA_LAUNCH("dense_dkv_split", st,
-                    dense_bwd_split_kernel<true><<<(unsigned)pieces, kBwdThreads, kBwdSmem, st>>>(mk, mv, mq, mg, a));
-    else
-        LLSA_LAUNCH("dense_dq_split", st,
-                    dense_bwd_split_kernel<false><<<(unsigned)pieces, kBwdThreads, kBwdSmem, st>>>(mq, mg, mk, mv, a));
+    cudaFuncSetAttribute(dense_bwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+    const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;
+    const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.splits;
+    if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("dense_bwd_split", st,
+                dense_bwd_split_kernel<<<(unsigned)(pq + pk), kBwdThreads, kBwdSmem, st>>>(mq, mg, mk, mv, aq, ak, (int)pk));
     return LLSA_OK;
-}
-
-int launch_dense_split_dq(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
-    return launch_bwd<false>(s, a, planes, st);
-}
-int launch_dense_split_dkv(const DenseShape& s, const DenseArgs& a, void* const* planes, cudaStream_t st) {
-    return launch_bwd<true>(s, a, planes, st);
 }
 
 }  // namespace llsa

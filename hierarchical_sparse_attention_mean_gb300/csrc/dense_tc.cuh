@@ -118,6 +118,18 @@ private:
     }
 };
 
+// Pieces are dealt to the resident blocks in rounds. In causal order they get
+// lighter and lighter, so every other round goes backwards there: forwards alone
+// the first block would get the heaviest of every round (12 heads x 4,096 tokens
+// at d = 64, forward 42.6 us so and 35.8 in turns).
+__device__ __forceinline__ int dealt(const DenseArgs& a, int i, int block, int blocks) {
+    return i * blocks + (a.causal && (i & 1) ? blocks - 1 - block : block);
+}
+__device__ __forceinline__ int dealt_pieces(const DenseArgs& a, int block, int blocks) {
+    const int full = a.pieces / blocks;
+    return full + (dealt(a, full, block, blocks) < a.pieces ? 1 : 0);
+}
+
 // The pieces of a resident block, worked out by one copying thread (divisions and
 // loads of the lengths: some 1,500 clocks) ahead of the roles that read them.
 constexpr int kPieceSlots = 4;
