@@ -143,10 +143,12 @@ int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t 
 int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
-// dense_few.cu: forward of a handful of rows per key head.
+// dense_few.cu: a handful of rows per key head.
 bool dense_few_supported(const DenseShape& s);
-DenseSplit dense_few_split(const DenseShape& s);
+bool dense_few_bwd_supported(const DenseShape& s);
+DenseSplit dense_few_split(const DenseShape& s);  // of the keys, in both directions
 int launch_dense_few(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_few_bwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
 // dense_fwd_tc.cu, dense_bwd_tc.cu: tensor-core kernels (bf16, d <= 128).
 bool dense_tc_supported(const DenseShape& s);

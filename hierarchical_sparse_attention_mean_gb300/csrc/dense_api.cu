@@ -213,7 +213,10 @@ Path fwd_path(const DenseShape& s) {
                                       : Path::kSimt;
 }
 Path bwd_path(const DenseShape& s) {
-    return dense_tc_supported(s) ? Path::kTc : dense_split_supported(s) ? Path::kSplit : Path::kSimt;
+    return dense_few_bwd_supported(s) ? Path::kFew
+           : dense_tc_supported(s)    ? Path::kTc
+           : dense_split_supported(s) ? Path::kSplit
+                                      : Path::kSimt;
 }
 
 DenseSplit fwd_split(const DenseShape& s) {
@@ -226,6 +229,7 @@ DenseSplit fwd_split(const DenseShape& s) {
 }
 DenseSplit dq_split(const DenseShape& s) {
     switch (bwd_path(s)) {
+        case Path::kFew: return dense_few_split(s);
         case Path::kTc: return dense_tc_dq_split(s);
         case Path::kSplit: return dense_split_fwd_split(s);
         default: return dense_simt_dq_split(s);
@@ -233,6 +237,7 @@ DenseSplit dq_split(const DenseShape& s) {
 }
 DenseSplit dkv_split(const DenseShape& s) {
     switch (bwd_path(s)) {
+        case Path::kFew: return {1, s.nk};  // dk, dv: of the blocks that own the keys
         case Path::kTc: return dense_tc_dkv_split(s);
         case Path::kSplit: return dense_split_dkv_split(s);
         default: return dense_simt_dkv_split(s);
@@ -247,12 +252,18 @@ size_t dense_fwd_workspace(const DenseShape& s) {
            (p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0);
 }
 
+// The per-row numbers of the backward pass, one array of the two (the kernels for
+// a handful of rows work them out).
+static size_t dense_rows_bytes(const DenseShape& s) {
+    return bwd_path(s) == Path::kFew ? 0 : align_up((size_t)s.slices * s.Rp * sizeof(float));
+}
+
 size_t dense_bwd_workspace(const DenseShape& s) {
     const DenseSplit pq = dq_split(s), pk = dkv_split(s);
     const size_t dq = pq.splits > 1 ? (size_t)pq.splits * s.slices * s.R * s.d * sizeof(float) : 0;
     const size_t dkv = pk.splits > 1 ? (size_t)pk.splits * 2 * s.slices * s.nk * s.d * sizeof(float) : 0;
     return (bwd_path(s) == Path::kSplit ? dense_split_planes(s, true) : 0) +
-           2 * align_up((size_t)s.slices * s.Rp * sizeof(float)) + align_up(dq) + dkv;
+           2 * dense_rows_bytes(s) + align_up(dq) + dkv;
 }
 
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
@@ -282,7 +293,7 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
     const Path path = bwd_path(s);
-    const size_t rows = align_up((size_t)s.slices * s.Rp * sizeof(float));
+    const size_t rows = dense_rows_bytes(s);
     void* planes[4];
     if (path == Path::kSplit) {
         LLSA_TRY(make_dense_split_planes(s, a, ws, planes, st));
@@ -290,7 +301,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     }
     a.nl2 = static_cast<float*>(ws);
     a.nd = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
-    if (s.R > 0) {
+    if (s.R > 0 && path != Path::kFew) {
         const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
         if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
         if (bf16)
@@ -309,6 +320,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     aq.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * rows);
     ak.part = aq.part + (pq.splits > 1 ? align_up((size_t)pq.splits * nq * sizeof(float)) / sizeof(float) : 0);
     switch (path) {
+        case Path::kFew: LLSA_TRY(launch_dense_few_bwd(s, aq, st)); break;
         case Path::kTc: LLSA_TRY(launch_dense_tc_bwd(s, aq, ak, st)); break;
         case Path::kSplit: LLSA_TRY(launch_dense_split_bwd(s, aq, ak, planes, st)); break;
         default:
