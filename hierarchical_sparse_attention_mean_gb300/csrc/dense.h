@@ -140,8 +140,7 @@ DenseSplit dense_simt_fwd_split(const DenseShape& s);
 DenseSplit dense_simt_dq_split(const DenseShape& s);
 DenseSplit dense_simt_dkv_split(const DenseShape& s);
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
-int launch_dense_simt_dq(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
-int launch_dense_simt_dkv(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st);
 
 // dense_few.cu: a handful of rows per key head.
 bool dense_few_supported(const DenseShape& s);
@@ -160,7 +159,8 @@ int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArg
 
 // dense_split_tc.cu: fp32 on the tensor cores, d <= 64 (planes: three bf16 planes
 // of q, k, v, or of q, dout, k, v, at the start of the workspace).
-bool dense_split_supported(const DenseShape& s);
+bool dense_split_fwd_supported(const DenseShape& s);
+bool dense_split_bwd_supported(const DenseShape& s);
 DenseSplit dense_split_fwd_split(const DenseShape& s);  // dq: the same
 DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes

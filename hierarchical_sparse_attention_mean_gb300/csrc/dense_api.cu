@@ -207,16 +207,16 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
 enum class Path { kFew, kTc, kSplit, kSimt };
 
 Path fwd_path(const DenseShape& s) {
-    return dense_few_supported(s)     ? Path::kFew
-           : dense_tc_supported(s)    ? Path::kTc
-           : dense_split_supported(s) ? Path::kSplit
-                                      : Path::kSimt;
+    return dense_few_supported(s)         ? Path::kFew
+           : dense_tc_supported(s)        ? Path::kTc
+           : dense_split_fwd_supported(s) ? Path::kSplit
+                                          : Path::kSimt;
 }
 Path bwd_path(const DenseShape& s) {
-    return dense_few_bwd_supported(s) ? Path::kFew
-           : dense_tc_supported(s)    ? Path::kTc
-           : dense_split_supported(s) ? Path::kSplit
-                                      : Path::kSimt;
+    return dense_few_bwd_supported(s)     ? Path::kFew
+           : dense_tc_supported(s)        ? Path::kTc
+           : dense_split_bwd_supported(s) ? Path::kSplit
+                                          : Path::kSimt;
 }
 
 DenseSplit fwd_split(const DenseShape& s) {
@@ -323,9 +323,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         case Path::kFew: LLSA_TRY(launch_dense_few_bwd(s, aq, st)); break;
         case Path::kTc: LLSA_TRY(launch_dense_tc_bwd(s, aq, ak, st)); break;
         case Path::kSplit: LLSA_TRY(launch_dense_split_bwd(s, aq, ak, planes, st)); break;
-        default:
-            if (s.R > 0) LLSA_TRY(launch_dense_simt_dq(s, aq, st));
-            if (s.nk > 0) LLSA_TRY(launch_dense_simt_dkv(s, ak, st));
+        default: LLSA_TRY(launch_dense_simt_bwd(s, aq, ak, st));
     }
     JoinArgs join;
     int outs = 0;
