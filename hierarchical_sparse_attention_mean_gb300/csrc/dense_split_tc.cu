@@ -96,11 +96,13 @@ __device__ __forceinline__ void store_rowpart(float* dst, const float* o, float 
 
 // A block takes 128 query rows against a stream of key and value tiles. S has two
 // buffers (columns 0 and 128), so the next S runs beside this one's softmax; the
-// planes of P lie at 256, O at 448.
-constexpr int kFwdThreads = 256;
+// planes of P lie at 256, O at 448. Two threads share a row: each reads all of its
+// scores for the maximum, then takes half of the weights and half of the output.
+constexpr int kFwdWarps = 8, kFwdThreads = (kFwdWarps + 3) * 32;
 constexpr int kFwdSmem = kTile * 4 + 1024;  // Q, two K, one V
 
 struct FwdBars {
+    float l[BT];  // the second half's sum of a row
     uint64_t q_full, k_full[2], k_empty[2], v_full, v_empty, s_full[2], s_free[2], p_full, o_done, drain;
     uint32_t tmem_slot;
     int abort_flag;
@@ -131,28 +133,28 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             mbar_init(smem_u32(&bar->k_full[i]), 1);
             mbar_init(smem_u32(&bar->k_empty[i]), 1);
             mbar_init(smem_u32(&bar->s_full[i]), 1);
-            mbar_init(smem_u32(&bar->s_free[i]), 4);
+            mbar_init(smem_u32(&bar->s_free[i]), kFwdWarps);
         }
         mbar_init(smem_u32(&bar->q_full), 1);
         mbar_init(smem_u32(&bar->v_full), 1);
         mbar_init(smem_u32(&bar->v_empty), 1);
-        mbar_init(smem_u32(&bar->p_full), 4);
+        mbar_init(smem_u32(&bar->p_full), kFwdWarps);
         mbar_init(smem_u32(&bar->o_done), 1);
         mbar_init(smem_u32(&bar->drain), 1);
         bar->abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 4) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    if (warp == kFwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t tP = tbase + 256, tO = tbase + 448;
 
-    if (warp == 5 || warp == 6) {
+    if (warp > kFwdWarps) {
         // ----------------------------------------------------------- copies
         if (lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
-            const bool keys = warp == 5;
+            const bool keys = warp == kFwdWarps + 1;
             if (keys) load_planes(sQ, &mq, r0, slice, a.slices, smem_u32(&bar->q_full));
             int t = 0;
             for (; t < n; t++) {
@@ -168,7 +170,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             else if (t > 0)
                 land(smem_u32(&bar->v_full), (t - 1) & 1);
         }
-    } else if (warp == 4) {
+    } else if (warp == kFwdWarps) {
         // ------------------------------------------------------- MMA issuer
         const uint32_t leader = elect_lane();
         constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idO = idesc_bf16(BT, 64, 0, 1);
@@ -219,26 +221,24 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         commit(leader, smem_u32(&bar->drain));
         if (lane == 0) land(smem_u32(&bar->drain), 0);
         __syncwarp();
-    } else if (warp < 4) {
+    } else {
         // ------------------------------------------------ softmax, epilogue
-        const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-        const int r = r0 + warp * 32 + lane;
+        const int lr = (warp & 3) * 32 + lane, half = warp >> 2;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int r = r0 + lr;
         int lim = (r < a.R ? dense_kend(a, sp, r < a.nq ? r : r % a.nq) : 0) - j_first;
         const float sl2 = a.scale * kDenseLog2e;
-        float m = -INFINITY, l = 0.f, acc[64];
+        float m = -INFINITY, l = 0.f, acc[32];  // l: of this half of the keys
 #pragma unroll
-        for (int i = 0; i < 64; i++) acc[i] = 0.f;
+        for (int i = 0; i < 32; i++) acc[i] = 0.f;
         auto take_O = [&](int t) {  // adds the product of tile t to this row's sums
             bar_wait(smem_u32(&bar->o_done), t & 1, abort_flag, a);
             tc_fence_after();
+            uint32_t o[32];
+            tmem_ld32_nowait(tO + lanes + half * 32, o);
+            tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                uint32_t o[32];
-                tmem_ld32_nowait(tO + lanes + c, o);
-                tmem_wait_ld();
-#pragma unroll
-                for (int i = 0; i < 32; i++) acc[c + i] += __uint_as_float(o[i]);
-            }
+            for (int i = 0; i < 32; i++) acc[i] += __uint_as_float(o[i]);
             tc_fence_before();
         };
         for (int t = 0; t < n; t++, lim -= BT) {
@@ -264,11 +264,12 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             if (t > 0) {  // then the planes of P may be written again
                 take_O(t - 1);
 #pragma unroll
-                for (int i = 0; i < 64; i++) acc[i] *= f;
+                for (int i = 0; i < 32; i++) acc[i] *= f;
             }
             const float shift = m == -INFINITY ? 0.f : -m;
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
+            for (int c0 = 0; c0 < 64; c0 += 32) {
+                const int c = half * 64 + c0;
                 uint32_t s[32], p1[16], p2[16], p3[16];
                 tmem_ld32_nowait(tS + c, s);
                 tmem_wait_ld();
@@ -295,20 +296,29 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             warp_arrive(smem_u32(&bar->p_full), lane);
         }
         if (n > 0) take_O(n - 1);
+        if (half == 1) bar->l[lr] = l;
+        named_barrier(1, kFwdWarps * 32);
+        // both threads of a row need its sum, added in the same order
+        if (half == 0) {
+            l += bar->l[lr];
+            bar->l[lr] = l;
+        }
+        named_barrier(1, kFwdWarps * 32);
+        l = bar->l[lr];
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
         const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
-        if (r < a.R)
-            store_rowpart<64>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv, 0, a.d);
         if (r < a.R) {
-            if (a.splits > 1)
+            store_rowpart<32>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv, half * 32,
+                              a.d);
+            if (half == 0 && a.splits > 1)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
-            else
+            else if (half == 0)
                 a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
         }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 4) {
+    if (warp == kFwdWarps) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
@@ -316,12 +326,14 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 
 // --------------------------------------------------------------- backward --
 
-// As the bf16 kernel, rows and keys in one launch too: 128 stationary rows (X1, X2) = (Q, dO) or (K, V) against a
-// stream (Y1, Y2) of the others. Shared memory holds one tile of each, so an item's
-// copies, its S and dP, the elementwise work and its sums follow one another; the
-// tensor cores carry most of that time. Tensor memory: S at 0, dP at 128, both
-// covered by planes 1 and 2 of P and of dS once they are read, their planes 3 at
-// 256 and 320, the sums at 384.
+// As the bf16 kernel, rows and keys in one launch too: 128 stationary rows (X1, X2) =
+// (Q, dO) or (K, V) against a stream (Y1, Y2) of the others. Shared memory holds one
+// tile of each, so what can overlap is ordered by when a tile comes free: the sums
+// over P (keys) free Y2 and those over dS then Y1, whose next tiles come in while
+// the tensor cores are at the next product. The elementwise work of an item stays
+// in their way. Tensor memory: S at 0 and dP at 128; planes 1 and 2 of dS lie over
+// S and those of P over dP once these are read, their planes 3 at 320 and 256, the
+// sums at 384.
 constexpr int kBwdWarps = 16, kCols = 32;
 // 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
 // 104 of them, the 128 others keep 64.
@@ -441,40 +453,46 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             };
             bool ok = any && warp_wait(smem_u32(&bar->x_full[0]), 0, abort_flag, a) &&
                       warp_wait(smem_u32(&bar->x_full[1]), 0, abort_flag, a);
-            int n = 0;
-            for (Items<KEYS> it = start; ok && !it.done(); it.next(a), n++) {
-                // S and dP: the sums that used up what lies over them were issued before
-                for (int k = 0; k < 2 && ok; k++) {
-                    ok = warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a);
-                    if (!ok) break;
-                    if (k == 0 || KEYS) clear_rows(sY + k * kTile, it);  // V only enters dP, which the mask covers
-                    tc_fence_after();
+            // S (k 0) or dP (k 1) of item n; what lies over it was used up by sums issued before
+            auto issue_tile = [&](const Items<KEYS>& it, int k, int n) {
+                if (!warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a)) return false;
+                if (k == 0 || KEYS) clear_rows(sY + k * kTile, it);  // V only enters dP, which the mask covers
+                tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 6; i++)
+                for (int i = 0; i < 6; i++)
 #pragma unroll
-                        for (int ks = 0; ks < 4; ks++)
-                            mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
-                                   dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
-                    commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+                    for (int ks = 0; ks < 4; ks++)
+                        mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
+                               dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+                if (!KEYS && k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
+                return true;
+            };
+            // acc += (dS or P, planes at t1, t1 + 64 and t3) (streamed tile k, read along its rows)
+            auto issue_sum = [&](uint32_t acc, uint32_t t1, uint32_t t3, int k) {
+#pragma unroll
+                for (int i = 0; i < 6; i++) {
+                    const uint32_t op = term_a(i) == 2 ? t3 : t1 + term_a(i) * 64;
+#pragma unroll
+                    for (int ks = 0; ks < 8; ks++)
+                        mma_ts(leader, acc, op + ks * 8, dM + ((k * kTile + term_b(i) * kPlane + ks * 2048) >> 4), idA,
+                               i > 0 || ks > 0);
                 }
-                ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
+                if (KEYS || k == 0) commit(leader, smem_u32(&bar->y_empty[k]));
+            };
+            ok = ok && issue_tile(start, 1, 0) && issue_tile(start, 0, 0);
+            Items<KEYS> it = start;
+            for (int n = 0; ok; n++) {
+                ok = warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
                 if (ok && n > 0) ok = warp_wait(smem_u32(&bar->acc_free), (n - 1) & 1, abort_flag, a);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int i = 0; i < 6; i++) {
-                    const int pa = term_a(i);
-                    const uint32_t opP = pa == 2 ? tP3 : tbase + pa * 64, opS = pa == 2 ? tS3 : tDP + pa * 64;
-#pragma unroll
-                    for (int ks = 0; ks < 8; ks++) {
-                        const uint64_t m = dM + ((term_b(i) * kPlane + ks * 2048) >> 4);
-                        mma_ts(leader, tAcc, opS + ks * 8, m, idA, i > 0 || ks > 0);
-                        if (KEYS) mma_ts(leader, tAcc + 64, opP + ks * 8, m + (kTile >> 4), idA, i > 0 || ks > 0);
-                    }
-                }
-                commit(leader, smem_u32(&bar->y_empty[0]));
-                commit(leader, smem_u32(&bar->y_empty[1]));
+                if (KEYS) issue_sum(tAcc + 64, tDP, tP3, 1);
+                issue_sum(tAcc, tbase, tS3, 0);
                 commit(leader, smem_u32(&bar->acc_full));
+                it.next(a);
+                if (it.done()) break;
+                ok = issue_tile(it, 1, n + 1) && issue_tile(it, 0, n + 1);
             }
             // no MMA may be in flight when tensor memory is released
             commit(leader, smem_u32(&bar->drain));
@@ -520,7 +538,8 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
             tc_fence_after();
             tmem_ld32_nowait(tbase + lanes + w * kCols, s);
-            bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);  // with it the streamed tile's numbers
+            bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);
+            if (KEYS) bar_wait(smem_u32(&bar->y_full[1]), n & 1, abort_flag, a);  // the streamed rows' numbers
             tc_fence_after();
             tmem_ld32_nowait(tDP + lanes + w * kCols, g);
             tmem_wait_ld();
@@ -552,7 +571,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
                 for (int c = 0; c < kCols; c += 2)
                     split2(__uint_as_float(k == 0 ? s[c] : g[c]), __uint_as_float(k == 0 ? s[c + 1] : g[c + 1]), p1[c >> 1],
                            p2[c >> 1], p3[c >> 1]);
-                const uint32_t t1 = tbase + k * 128 + lanes + w * 16;
+                const uint32_t t1 = (k == 0 ? tDP : tbase) + lanes + w * 16;
                 tmem_st16(t1, p1);
                 tmem_st16(t1 + 64, p2);
                 tmem_st16((k == 0 ? tP3 : tS3) + lanes + w * 16, p3);
