@@ -279,7 +279,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                     float e[2];
 #pragma unroll
                     for (int k = 0; k < 2; k++) {
-                        e[k] = exp2f(fmaf(__uint_as_float(s[i + k]), sl2, shift));
+                        e[k] = ex2(fmaf(__uint_as_float(s[i + k]), sl2, shift));
                         if (cut) e[k] = c + i + k < lim ? e[k] : 0.f;
                     }
                     sum += e[0] + e[1];
@@ -332,8 +332,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 // over P (keys) free Y2 and those over dS then Y1, whose next tiles come in while
 // the tensor cores are at the next product. The elementwise work of an item stays
 // in their way. Tensor memory: S at 0 and dP at 128; planes 1 and 2 of dS lie over
-// S and those of P over dP once these are read, their planes 3 at 320 and 256, the
-// sums at 384.
+// S and those of P over dP, 16 columns over the same 16, so that a warp overwrites
+// only what it has read; their planes 3 at 320 and 256, the sums at 384.
 constexpr int kBwdWarps = 16, kCols = 32;
 // 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
 // 104 of them, the 128 others keep 64.
@@ -468,14 +468,14 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
                 if (!KEYS && k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
                 return true;
             };
-            // acc += (dS or P, planes at t1, t1 + 64 and t3) (streamed tile k, read along its rows)
+            // acc += (dS or P) (streamed tile k, read along its rows): of every 16 columns at t1 plane 1, then plane 2, 8 words each
             auto issue_sum = [&](uint32_t acc, uint32_t t1, uint32_t t3, int k) {
 #pragma unroll
                 for (int i = 0; i < 6; i++) {
-                    const uint32_t op = term_a(i) == 2 ? t3 : t1 + term_a(i) * 64;
+                    const uint32_t op = term_a(i) == 2 ? t3 : t1 + term_a(i) * 8, step = term_a(i) == 2 ? 8 : 16;
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++)
-                        mma_ts(leader, acc, op + ks * 8, dM + ((k * kTile + term_b(i) * kPlane + ks * 2048) >> 4), idA,
+                        mma_ts(leader, acc, op + ks * step, dM + ((k * kTile + term_b(i) * kPlane + ks * 2048) >> 4), idA,
                                i > 0 || ks > 0);
                 }
                 if (KEYS || k == 0) commit(leader, smem_u32(&bar->y_empty[k]));
@@ -534,47 +534,46 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
         int n = 0;
         for (Items<KEYS> it = start; !it.done(); it.next(a), n++) {
             if (n > 0) take_sums(n - 1);  // while S and dP of this item are made
-            uint32_t s[kCols], g[kCols];
-            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
-            tc_fence_after();
-            tmem_ld32_nowait(tbase + lanes + w * kCols, s);
             bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);
             if (KEYS) bar_wait(smem_u32(&bar->y_full[1]), n & 1, abort_flag, a);  // the streamed rows' numbers
-            tc_fence_after();
-            tmem_ld32_nowait(tDP + lanes + w * kCols, g);
-            tmem_wait_ld();
-            tc_fence_before();
-            named_barrier(1 + q4, 128);  // the four warps of these rows have read S and dP
+            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
             tc_fence_after();
             const int lim = KEYS ? 0 : kend - it.pos - w * kCols;
             const bool cut = KEYS ? a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)
                                   : __any_sync(0xffffffffu, lim < kCols);
             int t = KEYS && cut ? (it.t0 + w * kCols) % a.nq : 0;
 #pragma unroll
-            for (int c = 0; c < kCols; c++) {
-                const float l = KEYS ? stats[w * kCols + c] : nl2, D = KEYS ? stats[BT + w * kCols + c] : nd;
-                float p = exp2f(fmaf(__uint_as_float(s[c]), sl2, l));
-                float ds = p * (__uint_as_float(g[c]) + D);
-                if (cut) {
-                    const bool out = KEYS ? x > t + sp.lk - sp.lq : c >= lim;
-                    p = out ? 0.f : p;
-                    ds = out ? 0.f : ds;
-                    if (KEYS && ++t == a.nq) t = 0;
+            for (int c0 = 0; c0 < kCols; c0 += 16) {
+                const uint32_t at = lanes + w * kCols + c0;
+                uint32_t s[16], g[16];
+                tmem_ld16_nowait(tbase + at, s);
+                tmem_ld16_nowait(tDP + at, g);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 16; c++) {
+                    const int col = w * kCols + c0 + c;
+                    const float l = KEYS ? stats[col] : nl2, D = KEYS ? stats[BT + col] : nd;
+                    float p = ex2(fmaf(__uint_as_float(s[c]), sl2, l));
+                    float ds = p * (__uint_as_float(g[c]) + D);
+                    if (cut) {
+                        const bool out = KEYS ? x > t + sp.lk - sp.lq : c0 + c >= lim;
+                        p = out ? 0.f : p;
+                        ds = out ? 0.f : ds;
+                        if (KEYS && ++t == a.nq) t = 0;
+                    }
+                    s[c] = __float_as_uint(p);
+                    g[c] = __float_as_uint(ds);
                 }
-                s[c] = __float_as_uint(p);
-                g[c] = __float_as_uint(ds);
-            }
 #pragma unroll
-            for (int k = KEYS ? 0 : 1; k < 2; k++) {  // planes of P, of dS
-                uint32_t p1[16], p2[16], p3[16];
+                for (int k = KEYS ? 0 : 1; k < 2; k++) {  // planes of P, of dS
+                    uint32_t p12[16], p3[8];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 2)
-                    split2(__uint_as_float(k == 0 ? s[c] : g[c]), __uint_as_float(k == 0 ? s[c + 1] : g[c + 1]), p1[c >> 1],
-                           p2[c >> 1], p3[c >> 1]);
-                const uint32_t t1 = (k == 0 ? tDP : tbase) + lanes + w * 16;
-                tmem_st16(t1, p1);
-                tmem_st16(t1 + 64, p2);
-                tmem_st16((k == 0 ? tP3 : tS3) + lanes + w * 16, p3);
+                    for (int c = 0; c < 16; c += 2)
+                        split2(__uint_as_float(k == 0 ? s[c] : g[c]), __uint_as_float(k == 0 ? s[c + 1] : g[c + 1]),
+                               p12[c >> 1], p12[8 + (c >> 1)], p3[c >> 1]);
+                    tmem_st16((k == 0 ? tDP : tbase) + at, p12);
+                    tmem_st8((k == 0 ? tP3 : tS3) + lanes + (w * kCols + c0) / 2, p3);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
