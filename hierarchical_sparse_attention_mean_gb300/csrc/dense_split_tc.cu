@@ -542,7 +542,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             const bool cut = KEYS ? a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)
                                   : __any_sync(0xffffffffu, lim < kCols);
             int t = KEYS && cut ? (it.t0 + w * kCols) % a.nq : 0;
-#pragma unroll
+#pragma unroll 1  // both at once would spill the sums
             for (int c0 = 0; c0 < kCols; c0 += 16) {
                 const uint32_t at = lanes + w * kCols + c0;
                 uint32_t s[16], g[16];
