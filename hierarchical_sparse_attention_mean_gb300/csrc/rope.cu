@@ -321,7 +321,9 @@ extern "C" int llsa_rope(const llsa_rope_params* p, const llsa_rope_strides* str
     a.rot = p->rot_dim ? p->rot_dim : p->d;
     a.axes = p->axes;
     LLSA_TRY(derive_rope(p, &a));
-    if (p->batch == 0 || p->n == 0 || p->heads + p->kv_heads == 0) return LLSA_OK;
+    const long long total = (long long)p->heads + p->kv_heads;
+    if (p->batch == 0 || p->n == 0 || total == 0) return LLSA_OK;
+    if ((double)p->batch * p->n * total * p->d > (double)(1LL << 40)) return LLSA_ERR_UNSUPPORTED;
     if (p->heads > 0) LLSA_TRY(check_ptrs({q, q_out}));
     if (p->kv_heads > 0) LLSA_TRY(check_ptrs({k, k_out}));
     if (pos && (reinterpret_cast<uintptr_t>(pos) & 3u)) return LLSA_ERR_ALIGN;

@@ -330,7 +330,8 @@ size_t llsa_dense_workspace_bytes(const llsa_dense_params *p, int op);
  *   q_len, k_len : int32 [batch] on the device, or NULL (all tokens valid).
  *   o     : output [batch, heads, nq, d] (p->dtype).
  *   lse   : output fp32 [batch, heads, nq] (natural log).
- * Limits: heads / kv_heads * nq and nk at most 2^30 (LLSA_ERR_UNSUPPORTED).
+ * Limits: heads / kv_heads * nq, nk and batch * kv_heads at most 2^30, 2^40 elements
+ * in each of q and k (LLSA_ERR_UNSUPPORTED).
  * Deterministic. */
 int llsa_dense_fwd(const llsa_dense_params *p, const void *q, const void *k, const void *v, const int32_t *q_len,
                    const int32_t *k_len, void *o, float *lse, void *ws, size_t ws_bytes, void *stream);
@@ -384,7 +385,8 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  *                  zeros, stands for contiguous [batch, heads, n, d]. Columns are
  *                  contiguous; every stride that is used spans a multiple of
  *                  16 bytes (LLSA_ERR_ALIGN otherwise), and an output's are
- *                  not 0 (LLSA_ERR_INVALID_ARG): its rows must not overlap. */
+ *                  not 0 (LLSA_ERR_INVALID_ARG): its rows must not overlap.
+ * Limits: 2^40 elements of q and k together, 65,535 heads (LLSA_ERR_UNSUPPORTED). */
 enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };
 enum { LLSA_ROPE_SCALE_NONE = 0, LLSA_ROPE_SCALE_LINEAR = 1, LLSA_ROPE_SCALE_BASE = 2, LLSA_ROPE_SCALE_WAVELENGTH = 3 };
 

@@ -175,3 +175,10 @@ def test_parameters_copy_and_pickle(lib):
         for y in (copy.copy(x), copy.deepcopy(x), pickle.loads(pickle.dumps(x)), dataclasses.replace(x)):
             assert y == x and bytes(y.c()) == bytes(x.c())
     assert dataclasses.replace(p, nq=7).c().nq == 7 and p.c().nq == 100
+
+
+@pytest.mark.parametrize("kw", [dict(heads=(1 << 31) - 1, kv_heads=(1 << 31) - 1), dict(batch=(1 << 31) - 1, n=(1 << 31) - 1),
+                                dict(batch=1 << 20, n=1 << 15)])
+def test_rope_sizes_refused(lib, kw):
+    p = llsa.RopeParams(**{**dict(batch=2, heads=4, n=100, d=64, kv_heads=2), **kw})
+    assert rope(lib, p) == UNSUPPORTED
