@@ -201,9 +201,8 @@ class DenseParams:
     scale: float = 0.0         # 0: 1/sqrt(d)
 
     def __post_init__(self):
-        c = _DenseParams(self.batch, self.heads, self.kv_heads, self.nq, self.nk, self.d,
-                         _choice(_DTYPES, self.dtype, "dtype"), 1 if self.causal else 0, self.scale)
-        self.__dict__.update(_c=c, _ref=ctypes.byref(c), _ws={})
+        self.__dict__.update(_dense_native(self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, bool(self.causal),
+                                           self.dtype, float(self.scale)))
 
     def __reduce__(self):  # copies and pickles build their own C structure
         return DenseParams, (self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, self.causal, self.dtype,
@@ -219,8 +218,15 @@ class DenseParams:
 
     def shapes(self):
         """Shapes of q (and o, dout, dq), of k (and v, dk, dv) and of lse."""
-        return ((self.batch, self.heads, self.nq, self.d),
-                (self.batch, self.kv_heads or self.heads, self.nk, self.d), (self.batch, self.heads, self.nq))
+        return self._shapes
+
+
+@functools.lru_cache(maxsize=256)
+def _dense_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, scale):
+    """What equal parameters share: the C structure, the workspace sizes, the tensors' shapes."""
+    c = _DenseParams(batch, heads, kv_heads, nq, nk, d, _choice(_DTYPES, dtype, "dtype"), 1 if causal else 0, scale)
+    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {},
+            "_shapes": ((batch, heads, nq, d), (batch, kv_heads or heads, nk, d), (batch, heads, nq))}
 
 
 @functools.lru_cache(maxsize=256)
@@ -253,24 +259,27 @@ class RopeParams:
     dtype: str = "bf16"
 
     def __post_init__(self):
-        scaling, order = _choice(_ROPE_SCALINGS, self.scaling, "scaling"), _choice(_ORDERS, self.token_order, "token_order")
-        layout, dt = _choice(_ROPE_LAYOUTS, self.layout, "layout"), _choice(_DTYPES, self.dtype, "dtype")
-        self.__dict__.update(_names=(layout, order, dt, scaling), _c={})
+        self.__dict__["_c"] = _rope_native(
+            self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, self.layout, self.axes, self.width,
+            self.token_order, self.pos_offset, self.dtype, self.scaling, self.orig_len, float(self.base), float(self.factor),
+            float(self.low), float(self.high), float(self.amplitude))
 
     def c(self, pos_batched: bool = False) -> _RopeParams:
-        got = self._c.get(pos_batched)
-        if got is None:
-            layout, order, dt, scaling = self._names
-            got = self._c[pos_batched] = _RopeParams(
-                self.batch, self.heads, self.kv_heads, self.n, self.d, self.rot_dim, layout, self.axes, self.width, order,
-                self.pos_offset, 1 if pos_batched else 0, dt, scaling, self.orig_len, self.base, self.factor, self.low,
-                self.high, self.amplitude)
-        return got
+        return self._c[1 if pos_batched else 0]
 
     @staticmethod
     def like(q, k=None, **kw) -> "RopeParams":
         b, h, n, d = q.shape
         return RopeParams(b, h, n, d, kv_heads=0 if k is None else k.shape[1], dtype=_dtype_name(q), **kw)
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_native(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, order, offset, dtype, scaling, orig_len, *real):
+    """The C structures of equal parameters, for positions without and with a batch dimension."""
+    layout, order = _choice(_ROPE_LAYOUTS, layout, "layout"), _choice(_ORDERS, order, "token_order")
+    dtype, scaling = _choice(_DTYPES, dtype, "dtype"), _choice(_ROPE_SCALINGS, scaling, "scaling")
+    return tuple(_RopeParams(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, order, offset, batched, dtype,
+                             scaling, orig_len, *real) for batched in (0, 1))
 
 
 @dataclass(frozen=True)
