@@ -28,7 +28,7 @@
 // At 64 columns one block per SM stays for the whole call and takes its share of
 // the work: while the elementwise warps finish one piece, the others load and
 // multiply for the next. At 128 columns shared memory holds one pair of
-// stationary tiles, and every piece gets a block of its own.
+// stationary tiles, and every piece gets a block of its own (figures at the launch).
 //
 // Bound by the chain of an item at 64 columns (S, exp, dP, dS, stores; 0.72 us against
 // 0.40 us of the tensor cores' time for an item of rows) and by the tensor cores at 128.
@@ -623,6 +623,9 @@ int launch(const DenseShape& s, DenseArgs aq, DenseArgs ak, cudaStream_t st) {
     if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     aq.pieces = (int)pq;
     ak.pieces = (int)pk;
+    // A block per piece, dealt out by the hardware, where a resident one would wait for its
+    // next stationary tiles: 16 heads over 4 of 4,095 tokens 312 us against 379, 19 slices of
+    // 16,384 5,121 against 5,154 (4 x 12 heads x 4,096 queries x 333 keys 161 against 152).
     if constexpr (K::NX == 1) {
         LLSA_LAUNCH("dense_bwd_tc", st, dense_bwd_tc_kernel<D><<<(unsigned)(pq + pk), kThreads, smem, st>>>(
                                             mq, mg, mk, mv, zq, zk, zv, aq, ak, (int)pk));

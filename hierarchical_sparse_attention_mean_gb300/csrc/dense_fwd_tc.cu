@@ -19,8 +19,12 @@
 //
 // One block per SM stays for the whole call and takes its share of the work:
 // while the softmax warps finish one piece (the last sums, the division, the
-// stores), the others load and multiply for the next. Starting a block anew for
-// every 256 rows costs some 10,000 clocks each, five key tiles' worth.
+// stores), the others load and multiply for the next (figures at the launch).
+//
+// Bound by the tensor cores and the exponentials, which at 64 columns take the same
+// time (an exponential is 4 clocks per warp and quarter of an SM: 512 clocks per 128 x
+// 128 scores, as its two products do). 19 slices of 16,384 tokens: 988 us at d = 64
+// (1,322 TFLOP/s of the 4 d operations per pair), 1,560 us at d = 128 (1,670).
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue (a thread per row of their
 // tile), warps 8 and 9 issue the MMAs, warps 10 and 11 the copies of K and V.
@@ -515,9 +519,9 @@ int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     a.whole = (int)(2 * rest <= kDenseSms && a.splits == 1 ? pieces - rest : pieces);
     pieces += pieces - a.whole;
     a.pieces = (int)pieces;
-    // At 128 columns there is one query tile per row tile, so a resident block would wait for its next one:
-    // a block per piece there (12 heads x 4,096 tokens 105 us against 107; at 64 columns 74 against 70).
-    const int grid = D == 64 ? (int)std::min<long long>(pieces, sm_count()) : (int)pieces;
+    // resident blocks against one per piece: 12 heads x 4,096 tokens 61.0 us and 63.3, 4 x 12 heads x 4,096
+    // queries x 333 keys 33.7 and 43.1; at 128 columns 88.0 and 88.7, 50.6 and 58.0
+    const int grid = (int)std::min<long long>(pieces, sm_count());
     LLSA_LAUNCH("dense_fwd_tc", st, dense_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(mq, mk, mv, mo, a));
     return LLSA_OK;
 }
