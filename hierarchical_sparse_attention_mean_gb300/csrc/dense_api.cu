@@ -85,38 +85,56 @@ __global__ void __launch_bounds__(kThreads, 4) dense_rows_kernel(const __grid_co
 
 // ------------------------------------------------------- joins of a split --
 
-// o and lse of every query row from the parts of a split over the keys: a warp
-// per row, the parts in ascending order.
+// o and lse of every query row from the parts of a split over the keys: a warp per
+// row. The weights of 32 parts are worked out at once, a lane each; then each half of
+// the warp (d <= 64) or all of it takes every second or every part, many loads at a
+// time: with few rows the latency of the parts is what this costs.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(DenseArgs a) {
+__global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(const __grid_constant__ DenseArgs a) {
     const long long rows = (long long)a.slices * a.R;
     const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
     const float2* ml = reinterpret_cast<const float2*>(a.part + (long long)a.splits * rows * a.d);
-    float m = -INFINITY;
+    float m = -INFINITY, l = 0.f;
     for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[p * rows + row].x);
     m = warp_max(m);
     const float shift = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int p = 0; p < a.splits; p++) {
+    for (int p = lane; p < a.splits; p += 32) {
         const float2 x = ml[p * rows + row];
         l = fmaf(x.y, exp2f(x.x - shift), l);
     }
+    l = warp_sum(l);
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    for (int c = lane * 4; c < a.d; c += 128) {
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int p = 0; p < a.splits; p++) {
-            const float w = exp2f(ml[p * rows + row].x - shift);
-            const float4 x = *reinterpret_cast<const float4*>(a.part + (p * rows + row) * a.d + c);
-            acc[0] = fmaf(w, x.x, acc[0]);
-            acc[1] = fmaf(w, x.y, acc[1]);
-            acc[2] = fmaf(w, x.z, acc[2]);
-            acc[3] = fmaf(w, x.w, acc[3]);
-        }
+    const int at_once = a.d <= 64 ? 2 : 1, sub = at_once == 2 ? lane >> 4 : 0;
+    const int c = (at_once == 2 ? lane & 15 : lane) * 4;  // and c + 128 behind 128 columns
+    float acc[2][4] = {};
+    for (int p0 = 0; p0 < a.splits; p0 += 32) {
+        const float w = p0 + lane < a.splits ? exp2f(ml[(p0 + lane) * rows + row].x - shift) : 0.f;
+        const int n = min(32, a.splits - p0);
+#pragma unroll 8
+        for (int i = 0; i < n; i += at_once) {
+            const float wi = __shfl_sync(0xffffffffu, w, (i + sub) & 31);
+            const float* from = a.part + ((p0 + i + sub) * rows + row) * a.d + c;
 #pragma unroll
-        for (int i = 0; i < 4; i++) acc[i] *= inv;
-        store4(static_cast<T*>(a.o_out) + row * a.d + c, acc);
+            for (int k = 0; k < 2; k++)
+                if (c + 128 * k < a.d && i + sub < n) {
+                    const float4 x = *reinterpret_cast<const float4*>(from + 128 * k);
+                    acc[k][0] = fmaf(wi, x.x, acc[k][0]);
+                    acc[k][1] = fmaf(wi, x.y, acc[k][1]);
+                    acc[k][2] = fmaf(wi, x.z, acc[k][2]);
+                    acc[k][3] = fmaf(wi, x.w, acc[k][3]);
+                }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            if (at_once == 2) acc[k][i] += __shfl_xor_sync(0xffffffffu, acc[k][i], 16);
+            acc[k][i] *= inv;
+        }
+        if (sub == 0 && c + 128 * k < a.d) store4(static_cast<T*>(a.o_out) + row * a.d + c + 128 * k, acc[k]);
     }
     if (lane == 0) a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
 }
@@ -137,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) dense_join_sum_kernel(const __grid_c
     if (i >= n) return;
     const float* part = a.part[t];
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
     for (int p = 0; p < a.parts[t]; p++) {
         const float4 x = *reinterpret_cast<const float4*>(part + p * n + i);
         acc[0] += x.x;
