@@ -11,7 +11,7 @@
 // of 8 to 32 lanes holds one key, 8 columns per lane, so that a warp reads whole
 // rows; four keys per group are in flight before the first is used. The
 // tensor-core kernel would leave 120 of its 128 rows empty and wait for a softmax
-// of full tiles (12 heads x 65,536 keys, one query: 65 us there, 42 here, 30 at
+// of full tiles (12 heads x 65,536 keys, one query: 60 us there, 38 here, 30 at
 // HBM's rate; backward 167 and 70, at HBM's rate 59).
 #include <algorithm>
 
@@ -375,8 +375,8 @@ int launch_rows(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Two rows where the tensor cores could take them (12 heads x 65,536 keys 51 us
-// against 65; at four rows their kernel is the faster one, 65 us against 72, and 57
+// Two rows where the tensor cores could take them (12 heads x 65,536 keys 49 us
+// against 61; at four rows their kernel is the faster one, 61 us against 72, and 57
 // against 91 at 8 x 4 key heads x 16,383 keys of 128 columns), four where the other choice is the CUDA-core kernel with its 64-row tiles.
 bool dense_few_supported(const DenseShape& s) { return s.R > 0 && s.R <= (dense_tc_supported(s) ? 2 : 4); }
 

@@ -12,7 +12,11 @@
 // Six bf16 products take 6 / 2,250 of the tensor cores' time against 1 / 80 on the
 // CUDA cores, whose kernel moreover gets half of that rate (an operand from shared
 // memory costs them as much as two of its FMAs). The kernels are bound by the
-// tensor cores: 1,530 clocks per 128 x 128 x 64 product.
+// tensor cores and the work on the scores between two products: a product of 128 x
+// 128 x 64 takes 1,530 clocks, and there is shared memory for one tile of each
+// operand. 2 x 8 heads x 1,023 tokens: forward 28 us, backward 95 us with the pass
+// before (44 and 115 with a thread per row and the sums' order as it falls; CUDA
+// cores 134 and 475).
 //
 // A pass before writes the three planes of q, k, v (and dout) to the workspace,
 // plane by plane, where TMA fetches them as ordinary bf16 tiles of 64 columns
@@ -42,7 +46,8 @@ struct PlaneArgs {
     long long n[4];
 };
 
-// Eight values per thread, blockIdx.y the tensor. Bound by HBM: 4 bytes in, 6 out.
+// Eight values per thread, blockIdx.y the tensor. Bound by HBM: 4 bytes in, 6 out (three
+// tensors of 2 x 8 x 1,023 x 64 values 6 us of 5).
 __global__ void __launch_bounds__(256) dense_planes_kernel(const __grid_constant__ PlaneArgs a) {
     const int t = blockIdx.y;
     const long long n = a.n[t];
@@ -639,8 +644,8 @@ bool dense_split_bwd_supported(const DenseShape& s) {
     return s.dtype == LLSA_DTYPE_F32 && s.d <= 64 && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
 }
 // The CUDA-core kernel is the faster one where the keys are one of its tiles and the
-// rows few (12 heads x 64 tokens 8.4 us against 10.8; 4 heads x 5 queries x 300 keys 26.6
-// against 17.9); backward it is not even there (28 against 15).
+// rows few (12 heads x 64 tokens 8.4 us against 9.5; 4 heads x 5 queries x 300 keys 26.6
+// against 13.8); backward it is not even there (28 against 14).
 bool dense_split_fwd_supported(const DenseShape& s) {
     return dense_split_bwd_supported(s) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
 }
