@@ -21,6 +21,8 @@ import math
 import os
 from dataclasses import dataclass
 
+import torch
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_PKG, "_build", "libllsa.so")
 _lib = None
@@ -161,7 +163,6 @@ class Params:
 
     @staticmethod
     def like(q, **kw) -> "Params":
-        import torch
         b, h, n, d = q.shape
         dtype = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(q.dtype)
         if dtype is None:
@@ -180,7 +181,6 @@ def _choice(table, value, name):
 
 
 def _dtype_name(t):
-    import torch
     name = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(t.dtype)
     if name is None:
         raise ValueError("q must be bfloat16 or float32")
@@ -314,7 +314,6 @@ def workspace_bytes(p: Params, op: int) -> int:
 
 
 def _ptr(t, name, dtype=None):
-    import torch
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
@@ -329,7 +328,6 @@ def _ptr(t, name, dtype=None):
 
 
 def _stream(stream):
-    import torch
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
@@ -342,14 +340,12 @@ def _ws(ws):
 
 
 def _tok_dtype(p: Params):
-    import torch
     return torch.bfloat16 if p.dtype == "bf16" else torch.float32
 
 
 # ------------------------------------------------------------------ C calls
 
 def llsa_pool(p: Params, q, k, v, pyr, ws=None, stream=None):
-    import torch
     td = _tok_dtype(p)
     w, wb = _ws(ws)
     _check(_load().llsa_pool(ctypes.byref(p.c()), _ptr(q, "q", td), _ptr(k, "k", td), _ptr(v, "v", td),
@@ -357,7 +353,6 @@ def llsa_pool(p: Params, q, k, v, pyr, ws=None, stream=None):
 
 
 def llsa_select(p: Params, pyr, sel_idx, coarse_idx, level_idx=None, ws=None, stream=None):
-    import torch
     w, wb = _ws(ws)
     _check(_load().llsa_select(ctypes.byref(p.c()), _ptr(pyr, "pyr", torch.float32),
                                _ptr(sel_idx, "sel_idx", torch.int32), _ptr(coarse_idx, "coarse_idx", torch.int32),
@@ -365,7 +360,6 @@ def llsa_select(p: Params, pyr, sel_idx, coarse_idx, level_idx=None, ws=None, st
 
 
 def llsa_fwd(p: Params, q, k, v, pyr, sel_idx, coarse_idx, o, lse, ws=None, stream=None):
-    import torch
     td = _tok_dtype(p)
     w, wb = _ws(ws)
     _check(_load().llsa_fwd(ctypes.byref(p.c()), _ptr(q, "q", td), _ptr(k, "k", td), _ptr(v, "v", td),
@@ -375,7 +369,6 @@ def llsa_fwd(p: Params, q, k, v, pyr, sel_idx, coarse_idx, o, lse, ws=None, stre
 
 
 def llsa_index_transpose(p: Params, sel_idx, col_ptr, row_idx, ws, stream=None):
-    import torch
     w, wb = _ws(ws)
     _check(_load().llsa_index_transpose(ctypes.byref(p.c()), _ptr(sel_idx, "sel_idx", torch.int32),
                                         _ptr(col_ptr, "col_ptr", torch.int32), _ptr(row_idx, "row_idx", torch.int32),
@@ -384,7 +377,6 @@ def llsa_index_transpose(p: Params, sel_idx, col_ptr, row_idx, ws, stream=None):
 
 def llsa_select_exhaustive(p: Params, pyr, sel_idx, stream=None):
     """Exhaustive level-1 Top-K: sel_idx int32 [batch*heads, T, min(K, T)]."""
-    import torch
     _check(_load().llsa_select_exhaustive(ctypes.byref(p.c()), _ptr(pyr, "pyr", torch.float32),
                                           _ptr(sel_idx, "sel_idx", torch.int32), _stream(stream)),
            "llsa_select_exhaustive")
@@ -393,7 +385,6 @@ def llsa_select_exhaustive(p: Params, pyr, sel_idx, stream=None):
 def routing_recall(hier_sel, exhaustive_sel) -> float:
     """Share of the exhaustive level-1 Top-K entries that the hierarchical
     selection also holds, over all rows (both int32 [.., T, K] tensors)."""
-    import torch
     h = hier_sel.reshape(-1, hier_sel.shape[-1]).long()
     e = exhaustive_sel.reshape(-1, exhaustive_sel.shape[-1]).long()
     hit = (e[:, :, None] == h[:, None, :]).any(-1)
@@ -410,7 +401,6 @@ def llsa_reorder(p: Params, height: int, width: int, x, out, inverse: bool = Fal
 
 def llsa_bwd(p: Params, q, k, v, o, lse, dout, pyr, sel_idx, coarse_idx, col_ptr, row_idx, dq, dk, dv, ws,
              stream=None):
-    import torch
     td = _tok_dtype(p)
     w, wb = _ws(ws)
     i32, f32 = torch.int32, torch.float32
@@ -423,7 +413,6 @@ def llsa_bwd(p: Params, q, k, v, o, lse, dout, pyr, sel_idx, coarse_idx, col_ptr
 
 def _like(t, name, shape, dtype, device):
     """Pointer of a contiguous tensor of exactly this shape and type on device number `device`."""
-    import torch
     if (isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.get_device() == device
             and t.is_contiguous()):
         return t.data_ptr()
@@ -442,7 +431,6 @@ _HERE = contextlib.nullcontext()
 
 def _on(t, name):
     """The device of the call: that of its first tensor, which becomes the current one."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -459,14 +447,12 @@ def dense_workspace_bytes(p: DenseParams, op: int) -> int:
 
 
 def _lens(p, q_len, k_len, device):
-    import torch
     return tuple(None if x is None else _like(x, name, (p.batch,), torch.int32, device)
                  for x, name in ((q_len, "q_len"), (k_len, "k_len")))
 
 
 def llsa_dense_fwd(p: DenseParams, q, k, v, o, lse, q_len=None, k_len=None, ws=None, stream=None):
     """Dense attention: o and lse of q over k, v (llsa_dense_fwd of include/llsa.h)."""
-    import torch
     with _on(q, "q"):
         td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
@@ -478,7 +464,6 @@ def llsa_dense_fwd(p: DenseParams, q, k, v, o, lse, q_len=None, k_len=None, ws=N
 
 def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None, k_len=None, ws=None, stream=None):
     """Gradients of dense attention (llsa_dense_bwd of include/llsa.h)."""
-    import torch
     with _on(q, "q"):
         td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
@@ -493,7 +478,6 @@ def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None
 def _strided(t, name, shape, dtype, device):
     """Pointer of a [batch, heads, n, d] tensor whose columns are contiguous, and
     its batch, head and token strides (None: contiguous throughout)."""
-    import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != device:
@@ -528,7 +512,6 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
     k_out, in one launch. All may be strided views with contiguous columns, and
     a tensor may be its own output. pos: int32 [n], [n, axes], or either with a
     leading batch dimension. inverse: the negative angles (the gradient)."""
-    import torch
     with _on(q, "q"):
         td, dev = _tok_dtype(p), q.get_device()
         shape = (p.batch, p.heads, p.n, p.d)
@@ -604,7 +587,6 @@ class Buffers:
     """Device buffers of one problem (allocated by torch, owned here)."""
 
     def __init__(self, p: Params, device="cuda"):
-        import torch
         s = get_sizes(p)
         self.p, self.s = p, s
         bh = s.slices
@@ -628,7 +610,6 @@ class Buffers:
         self._pending = False      # a transpose was issued that backward() has not waited for
 
     def side_stream(self):
-        import torch
         if self._side is None:
             self._side = torch.cuda.Stream(device=self.sel_idx.device)
             self._sel_ready = torch.cuda.Event()
@@ -645,7 +626,6 @@ class Buffers:
 
 
 def _as_stream(stream, device):
-    import torch
     if stream is None:
         return torch.cuda.current_stream(device)
     if isinstance(stream, torch.cuda.Stream):
@@ -679,7 +659,6 @@ def forward(p: Params, q, k, v, bufs: Buffers | None = None, stream=None) -> Buf
 
 def backward(p: Params, q, k, v, dout, b: Buffers, dq=None, dk=None, dv=None, stream=None):
     """bwd after forward() (and its index transpose). Returns (dq, dk, dv)."""
-    import torch
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
@@ -700,21 +679,18 @@ def _dense_ws(p: DenseParams, op: int, device):
     need = dense_workspace_bytes(p, op)
     if need == 0:
         return None
-    import torch
     return torch.empty(need, dtype=torch.uint8, device=device)
 
 
 def _under(stream, device):
     """What is allocated for a call belongs to the call's stream, whose order then
     keeps it from being used again too early."""
-    import torch
     return _HERE if stream is None else torch.cuda.stream(_as_stream(stream, device))
 
 
 def dense_forward(p: DenseParams, q, k, v, q_len=None, k_len=None, o=None, lse=None, ws=None, stream=None):
     """Dense attention of q over k, v. Returns (o, lse); what is not given is
     allocated here, on `stream` (None: the current one)."""
-    import torch
     with _under(stream, q.device):
         o = torch.empty_like(q) if o is None else o
         lse = torch.empty(p.shapes()[2], dtype=torch.float32, device=q.device) if lse is None else lse
@@ -726,7 +702,6 @@ def dense_forward(p: DenseParams, q, k, v, q_len=None, k_len=None, o=None, lse=N
 def dense_backward(p: DenseParams, q, k, v, o, lse, dout, q_len=None, k_len=None, dq=None, dk=None, dv=None, ws=None,
                    stream=None):
     """Gradients of dense_forward(). Returns (dq, dk, dv)."""
-    import torch
     with _under(stream, q.device):
         dq = torch.empty_like(q) if dq is None else dq
         dk = torch.empty_like(k) if dk is None else dk
@@ -754,7 +729,6 @@ def _rope_view(t):
 
 
 def _autograd_function():
-    import torch
 
     class LLSAFunction(torch.autograd.Function):
         """Differentiable LLSA over [batch, heads, N, d] tensors."""
@@ -787,7 +761,6 @@ def _autograd_function():
 
 def _rotated(rope, q, k, pos, inverse=False):
     """Head-major contiguous copies of q and k (None allowed) with their positions turned in."""
-    import torch
     _check_rope(rope, q, k)
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
@@ -811,7 +784,6 @@ def llsa_attention(q, k, v, block: int = 16, topk: int = 8, levels: int = 0, enr
 
 
 def _dense_functions():
-    import torch
     from torch.autograd.function import once_differentiable
 
     class DenseFunction(torch.autograd.Function):
