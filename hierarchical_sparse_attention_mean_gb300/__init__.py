@@ -844,7 +844,10 @@ def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=Non
                     rope: RopeParams | None = None, pos=None):
     """Autograd entry point of dense attention: q [batch, heads, nq, d] over k, v
     [batch, kv_heads, nk, d]. q_len, k_len: int32 [batch] valid tokens of a
-    padded batch. rope: rotary positions for q and k of the same tokens."""
+    padded batch. rope: rotary positions for q and k of the same tokens; the turned
+    q and k are rounded to their type before the scores, as rotary() returns them.
+    A backward pass that a CUDA graph captures wants leaves made inside the capture
+    (x.detach().requires_grad_()), as every autograd function does."""
     return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)
 
 

@@ -16,7 +16,9 @@
 // 128 rows (Y1, Y2), with (X1, X2, Y1, Y2) = (Q, dO, K, V) or (K, V, Q, dO). Per
 // item: S = X1 Y1^T, dP = X2 Y2^T (128 x 128 fp32 in tensor memory), then P and
 // dS as bf16 over dP's columns, then acc1 += dS Y1 and, for keys, acc2 += P Y2,
-// with P and dS as tensor-memory operands. An M = 128 product of two
+// with P and dS as tensor-memory operands. P and dS are rounded to bf16 there, the type
+// that these products have beside bf16 inputs (2^-9 of each, independent from key to
+// key; statistics, D and all sums stay in fp32). An M = 128 product of two
 // shared-memory operands takes 64 clocks per 16 of K at N = 128 and 48 at N = 64
 // (shared memory feeds it then), so tiles of 128 are worth their tensor memory.
 //

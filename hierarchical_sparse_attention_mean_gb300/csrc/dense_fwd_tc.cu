@@ -7,7 +7,8 @@
 // the maximum has passed it by more than 2^8, and l and O are rescaled then.
 // Softmax does not depend on m, P = 2^(s - m) <= 2^8 has the same relative
 // rounding in bf16 whatever its size, and sums are fp32, so this costs no
-// precision; it saves reading O back for almost every tile.
+// precision; it saves reading O back for almost every tile. P is rounded to bf16,
+// the type that P V has beside bf16 inputs; l sums it before that.
 //
 // A block takes 256 query rows as two tiles of 128 against a shared stream of
 // key and value tiles, the two taking turns on the tensor cores. A thread holds
