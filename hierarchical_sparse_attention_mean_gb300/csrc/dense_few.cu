@@ -9,9 +9,9 @@
 //
 // Bound by HBM: 4 d flops per key and row against 4 d bytes per key (bf16). A group
 // of 8 to 32 lanes holds one key, 8 columns per lane, so that a warp reads whole
-// rows; four keys per group are in flight before the first is used. The
+// rows; several keys per group are in flight before the first is used. The
 // tensor-core kernel would leave 120 of its 128 rows empty and wait for a softmax
-// of full tiles (12 heads x 65,536 keys, one query: 60 us there, 38 here, 30 at
+// of full tiles (12 heads x 65,536 keys, one query: 60 us there, 37 here, 30 at
 // HBM's rate; backward 167 and 70, at HBM's rate 59).
 #include <algorithm>
 
@@ -62,7 +62,8 @@ __device__ __forceinline__ float ex2(float x) {
 template <typename T, int RR, int LANES>
 __global__ void __launch_bounds__(kThreads) dense_fwd_few_kernel(DenseArgs a) {
     constexpr int GROUPS = 32 / LANES;
-    constexpr int U = sizeof(T) == 2 ? 4 : 2;  // keys per group of lanes, in use and in flight
+    // keys per group of lanes, in use and in flight (one row: 8 x 4 key heads x 16,383 keys 45.3 us, with half as many 47.2)
+    constexpr int U = (sizeof(T) == 2 ? 4 : 2) * (RR == 1 ? 2 : 1);
     __shared__ float sO[kWarps][RR][LANES * 8];
     __shared__ float2 sML[kWarps][RR];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
