@@ -8,6 +8,10 @@ library's CUDA kernels on the caller's current torch stream. PyTorch supplies
 device memory and streams. There is no CPU fallback: if the library is not
 built or the device is not a GB300, calls raise.
 
+Beside the sparse path: dense attention (``llsa_dense_fwd``, ``llsa_dense_bwd``;
+``dense_attention`` with autograd) and rotary positions (``llsa_rope``;
+``rotary``, or ``rope=`` of either attention).
+
 Method: "Trainable Log-linear Sparse Attention for Efficient Diffusion
 Transformers" (arXiv 2512.16615), as described on its Pith review page
 ("Core claim", "What carries the argument").
