@@ -80,11 +80,15 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& p1, uint32_t&
     p3 = pack_bf16x2(x, y);
 }
 
-// One thread: the three planes of the 128 rows at `row` of a tensor of `slices` slices.
+// One thread: the three planes of ROWS rows from `row` on of a tensor of `slices`
+// slices, as regions of 64 columns.
+template <int ROWS, int D>
 __device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, int slices,
                                             uint32_t mbar) {
-    mbar_arrive_expect_tx(mbar, kTile);
-    for (int p = 0; p < 3; p++) tma_load_3d(smem_u32(dst + p * kPlane), map, 0, row, p * slices + slice, mbar);
+    mbar_arrive_expect_tx(mbar, 3 * ROWS * D * 2);
+    for (int p = 0; p < 3; p++)
+        for (int c = 0; c < D / 64; c++)
+            tma_load_3d(smem_u32(dst + (p * (D / 64) + c) * ROWS * 128), map, c * 64, row, p * slices + slice, mbar);
 }
 
 template <int COLS>
@@ -99,12 +103,20 @@ __device__ __forceinline__ void store_rowpart(float* dst, const float* o, float 
 
 // ---------------------------------------------------------------- forward --
 
-// A block takes 128 query rows against a stream of key and value tiles. S has two
-// buffers (columns 0 and 128), so the next S runs beside this one's softmax; the
-// planes of P lie at 256, O at 448. Two threads share a row: each reads all of its
-// scores for the maximum, then takes half of the weights and half of the output.
+// A block takes 128 query rows against a stream of key and value tiles, of 128 keys
+// at 64 columns and 64 keys at 128 columns. S has two buffers, so the next S runs
+// beside this one's softmax. Two threads share a row: each reads all of its scores
+// for the maximum, then takes half of the weights and half of the output.
 constexpr int kFwdWarps = 8, kFwdThreads = (kFwdWarps + 3) * 32;
-constexpr int kFwdSmem = kTile * 4 + 1024;  // Q, two K, one V
+
+template <int D>
+struct FwdCfg {
+    static constexpr int BN = D == 64 ? 128 : 64, NC = D / 64;
+    static constexpr int PQ = BT * D * 2, PK = BN * D * 2, RK = BN * 128;  // bytes: a plane of Q, of K or V; 64 columns of that
+    static constexpr int KST = D == 64 ? 2 : 1;                           // K tiles
+    static constexpr int SMEM = 3 * (PQ + (KST + 1) * PK) + 1024;
+    static constexpr int TM_P = 2 * BN, TM_O = D == 64 ? 448 : 256;       // tensor memory: S at 0 and BN
+};
 
 struct FwdBars {
     float l[BT];  // the second half's sum of a row
@@ -113,12 +125,15 @@ struct FwdBars {
     int abort_flag;
 };
 
+template <int D>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ DenseArgs a) {
+    using C = FwdCfg<D>;
+    constexpr int BN = C::BN;
     extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char *sQ = sm, *sK = sm + kTile, *sV = sm + 3 * kTile;
-    FwdBars* bar = reinterpret_cast<FwdBars*>(sm + 4 * kTile);
+    unsigned char *sQ = sm, *sK = sm + 3 * C::PQ, *sV = sK + C::KST * 3 * C::PK;
+    FwdBars* bar = reinterpret_cast<FwdBars*>(sV + 3 * C::PK);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
@@ -131,7 +146,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     const DenseSpan sp = dense_span(a, slice);
     const int j_first = part * a.chunk;
     const int end = min(dense_tile_kend(a, sp, r0 < a.nq ? r0 : r0 % a.nq, BT), a.splits > 1 ? j_first + a.chunk : a.nk);
-    const int n = end > j_first ? (end - j_first + BT - 1) / BT : 0;
+    const int n = end > j_first ? (end - j_first + BN - 1) / BN : 0;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; i++) {
@@ -154,47 +169,47 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
-    const uint32_t tP = tbase + 256, tO = tbase + 448;
+    const uint32_t tP = tbase + C::TM_P, tO = tbase + C::TM_O;
 
     if (warp > kFwdWarps) {
         // ----------------------------------------------------------- copies
         if (lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
             const bool keys = warp == kFwdWarps + 1;
-            if (keys) load_planes(sQ, &mq, r0, slice, a.slices, smem_u32(&bar->q_full));
+            if (keys) load_planes<BT, D>(sQ, &mq, r0, slice, a.slices, smem_u32(&bar->q_full));
             int t = 0;
             for (; t < n; t++) {
-                const int st = keys ? t & 1 : 0, use = keys ? t >> 1 : t;
+                const int st = keys ? t % C::KST : 0, use = keys ? t / C::KST : t;
                 const uint32_t full = smem_u32(keys ? &bar->k_full[st] : &bar->v_full);
                 if (use > 0 && !bar_wait(smem_u32(keys ? &bar->k_empty[st] : &bar->v_empty), (use - 1) & 1, abort_flag, a)) break;
-                load_planes(keys ? sK + st * kTile : sV, keys ? &mk : &mv, j_first + t * BT, slice, a.slices, full);
+                load_planes<BN, D>(keys ? sK + st * 3 * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, a.slices, full);
             }
             // copies still in flight must land before the block exits
             if (keys) land(smem_u32(&bar->q_full), 0);
             if (keys)
-                for (int x = max(0, t - 2); x < t; x++) land(smem_u32(&bar->k_full[x & 1]), (x >> 1) & 1);
+                for (int x = max(0, t - C::KST); x < t; x++) land(smem_u32(&bar->k_full[x % C::KST]), (x / C::KST) & 1);
             else if (t > 0)
                 land(smem_u32(&bar->v_full), (t - 1) & 1);
         }
     } else if (warp == kFwdWarps) {
         // ------------------------------------------------------- MMA issuer
         const uint32_t leader = elect_lane();
-        constexpr uint32_t idS = idesc_bf16(BT, BT, 0, 0), idO = idesc_bf16(BT, 64, 0, 1);
+        constexpr uint32_t idS = idesc_bf16(BT, BN, 0, 0), idO = idesc_bf16(BT, D, 0, 1);
         const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024), dK = desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t dV = desc_sw128(smem_u32(sV), kPlane, 1024);
+        const uint64_t dV = desc_sw128(smem_u32(sV), C::RK, 1024);
         auto issue_S = [&](int t) {
-            const int b = t & 1;
-            if (!warp_wait(smem_u32(&bar->k_full[b]), (t >> 1) & 1, abort_flag, a)) return false;
+            const int b = t & 1, st = t % C::KST;
+            if (!warp_wait(smem_u32(&bar->k_full[st]), (t / C::KST) & 1, abort_flag, a)) return false;
             if (t > 1 && !warp_wait(smem_u32(&bar->s_free[b]), ((t >> 1) - 1) & 1, abort_flag, a)) return false;
             tc_fence_after();
-            const uint64_t dT = dK + (b * kTile >> 4);
+            const uint64_t dT = dK + (st * 3 * C::PK >> 4);
 #pragma unroll
             for (int i = 0; i < 6; i++)
 #pragma unroll
-                for (int ks = 0; ks < 4; ks++)
-                    mma_ss(leader, tbase + b * 128, dQ + ((term_a(i) * kPlane + ks * 32) >> 4),
-                           dT + ((term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+                for (int ks = 0; ks < D / 16; ks++)
+                    mma_ss(leader, tbase + b * BN, dQ + ((term_a(i) * C::PQ + (ks / 4) * BT * 128 + (ks % 4) * 32) >> 4),
+                           dT + ((term_b(i) * C::PK + (ks / 4) * C::RK + (ks % 4) * 32) >> 4), idS, i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->s_full[b]));
-            commit(leader, smem_u32(&bar->k_empty[b]));
+            commit(leader, smem_u32(&bar->k_empty[st]));
             return true;
         };
         bool ok = n > 0 && warp_wait(smem_u32(&bar->q_full), 0, abort_flag, a) && issue_S(0);
@@ -204,11 +219,11 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             ok = ok && warp_wait(smem_u32(&bar->v_full), t & 1, abort_flag, a);
             if (!ok) break;
             // values behind the last valid key may be anything: their weights are 0, so they must be finite
-            const int live = sp.lk - (j_first + t * BT);
-            if (live < BT) {
-                for (int p = 0; p < 3; p++)
-                    for (int x = live * 8 + lane; x < BT * 8; x += 32)
-                        reinterpret_cast<uint4*>(sV + p * kPlane)[x] = make_uint4(0u, 0u, 0u, 0u);
+            const int live = sp.lk - (j_first + t * BN);
+            if (live < BN) {
+                for (int p = 0; p < 3 * C::NC; p++)
+                    for (int x = live * 8 + lane; x < BN * 8; x += 32)
+                        reinterpret_cast<uint4*>(sV + p * C::RK)[x] = make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
                 __syncwarp();
             }
@@ -216,8 +231,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 #pragma unroll
             for (int i = 0; i < 6; i++)
 #pragma unroll
-                for (int ks = 0; ks < 8; ks++)
-                    mma_ts(leader, tO, tP + term_a(i) * 64 + ks * 8, dV + ((term_b(i) * kPlane + ks * 2048) >> 4), idO,
+                for (int ks = 0; ks < BN / 16; ks++)
+                    mma_ts(leader, tO, tP + term_a(i) * (BN / 2) + ks * 8, dV + ((term_b(i) * C::PK + ks * 2048) >> 4), idO,
                            i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->o_done));
             commit(leader, smem_u32(&bar->v_empty));
@@ -233,28 +248,31 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const int r = r0 + lr;
         int lim = (r < a.R ? dense_kend(a, sp, r < a.nq ? r : r % a.nq) : 0) - j_first;
         const float sl2 = a.scale * kDenseLog2e;
-        float m = -INFINITY, l = 0.f, acc[32];  // l: of this half of the keys
+        float m = -INFINITY, l = 0.f, acc[D / 2];  // l: of this half of the keys
 #pragma unroll
-        for (int i = 0; i < 32; i++) acc[i] = 0.f;
+        for (int i = 0; i < D / 2; i++) acc[i] = 0.f;
         auto take_O = [&](int t) {  // adds the product of tile t to this row's sums
             bar_wait(smem_u32(&bar->o_done), t & 1, abort_flag, a);
             tc_fence_after();
-            uint32_t o[32];
-            tmem_ld32_nowait(tO + lanes + half * 32, o);
-            tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; i++) acc[i] += __uint_as_float(o[i]);
+            for (int c = 0; c < D / 2; c += 32) {
+                uint32_t o[32];
+                tmem_ld32_nowait(tO + lanes + half * (D / 2) + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; i++) acc[c + i] += __uint_as_float(o[i]);
+            }
             tc_fence_before();
         };
-        for (int t = 0; t < n; t++, lim -= BT) {
+        for (int t = 0; t < n; t++, lim -= BN) {
             const int b = t & 1;
-            const uint32_t tS = tbase + b * 128 + lanes;
+            const uint32_t tS = tbase + b * BN + lanes;
             bar_wait(smem_u32(&bar->s_full[b]), (t >> 1) & 1, abort_flag, a);
             tc_fence_after();
-            const bool cut = __any_sync(0xffffffffu, lim < BT);
+            const bool cut = __any_sync(0xffffffffu, lim < BN);
             float top = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < 128; c += 32) {
+            for (int c = 0; c < BN; c += 32) {
                 uint32_t s[32];
                 tmem_ld32_nowait(tS + c, s);
                 tmem_wait_ld();
@@ -269,12 +287,12 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             if (t > 0) {  // then the planes of P may be written again
                 take_O(t - 1);
 #pragma unroll
-                for (int i = 0; i < 32; i++) acc[i] *= f;
+                for (int i = 0; i < D / 2; i++) acc[i] *= f;
             }
             const float shift = m == -INFINITY ? 0.f : -m;
 #pragma unroll
-            for (int c0 = 0; c0 < 64; c0 += 32) {
-                const int c = half * 64 + c0;
+            for (int c0 = 0; c0 < BN / 2; c0 += 32) {
+                const int c = half * (BN / 2) + c0;
                 uint32_t s[32], p1[16], p2[16], p3[16];
                 tmem_ld32_nowait(tS + c, s);
                 tmem_wait_ld();
@@ -292,8 +310,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                 }
                 l += sum;
                 tmem_st16(tP + lanes + (c >> 1), p1);
-                tmem_st16(tP + lanes + 64 + (c >> 1), p2);
-                tmem_st16(tP + lanes + 128 + (c >> 1), p3);
+                tmem_st16(tP + lanes + BN / 2 + (c >> 1), p2);
+                tmem_st16(tP + lanes + BN + (c >> 1), p3);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -313,8 +331,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
         const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
         if (r < a.R) {
-            store_rowpart<32>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv, half * 32,
-                              a.d);
+            store_rowpart<D / 2>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv,
+                                 half * (D / 2), a.d);
             if (half == 0 && a.splits > 1)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
             else if (half == 0)
@@ -409,7 +427,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             // ----------------------------------------------------------- copies
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const int k = warp - kBwdWarps - 1;
-                load_planes(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
+                load_planes<BT, 64>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
                 const uint32_t full = smem_u32(&bar->y_full[k]);
                 int n = 0;
                 for (Items<KEYS> it = start; !it.done(); it.next(a)) {
@@ -422,7 +440,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
                         bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
                         bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
                     } else {
-                        load_planes(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                        load_planes<BT, 64>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
                     }
                     n++;
                 }
@@ -640,14 +658,15 @@ int write_planes(const float* const* x, const long long* elems, int n, void* ws,
 
 }  // namespace
 
-bool dense_split_bwd_supported(const DenseShape& s) {
-    return s.dtype == LLSA_DTYPE_F32 && s.d <= 64 && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
+static bool fits(const DenseShape& s, int most) {
+    return s.dtype == LLSA_DTYPE_F32 && s.d <= most && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
 }
+bool dense_split_bwd_supported(const DenseShape& s) { return fits(s, 64); }
 // The CUDA-core kernel is the faster one where the keys are one of its tiles and the
 // rows few (12 heads x 64 tokens 8.4 us against 9.5; 4 heads x 5 queries x 300 keys 26.6
 // against 13.8); backward it is not even there (28 against 14).
 bool dense_split_fwd_supported(const DenseShape& s) {
-    return dense_split_bwd_supported(s) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
+    return fits(s, 128) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
 }
 
 DenseSplit dense_split_fwd_split(const DenseShape& s) {
@@ -662,23 +681,29 @@ size_t dense_split_planes(const DenseShape& s, bool backward) {
     return backward ? 2 * q + 2 * k : q + 2 * k;
 }
 
+template <int D>
+static int launch_fwd(const DenseShape& s, const DenseArgs& a, __nv_bfloat16* const* p, cudaStream_t st) {
+    using C = FwdCfg<D>;
+    static_assert(C::SMEM <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
+    CUtensorMap mq, mk, mv;
+    LLSA_TRY(make_tmap_rows(&mq, p[0], 3LL * s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_rows(&mk, p[1], 3LL * s.slices, s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_rows(&mv, p[2], 3LL * s.slices, s.nk, s.d, C::BN));
+    cudaFuncSetAttribute(dense_fwd_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
+    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("dense_fwd_split", st,
+                dense_fwd_split_kernel<D><<<(unsigned)pieces, kFwdThreads, C::SMEM, st>>>(mq, mk, mv, a));
+    return LLSA_OK;
+}
+
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st) {
     const float* x[3] = {static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v)};
     const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
     const long long elems[3] = {nq, nk, nk};
     __nv_bfloat16* p[3];
     LLSA_TRY(write_planes(x, elems, 3, ws, p, st));
-    CUtensorMap mq, mk, mv;
-    LLSA_TRY(make_tmap_rows(&mq, p[0], 3LL * s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mk, p[1], 3LL * s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mv, p[2], 3LL * s.slices, s.nk, s.d, BT));
-    static_assert(kFwdSmem <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
-    cudaFuncSetAttribute(dense_fwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kFwdSmem);
-    const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
-    if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("dense_fwd_split", st,
-                dense_fwd_split_kernel<<<(unsigned)pieces, kFwdThreads, kFwdSmem, st>>>(mq, mk, mv, a));
-    return LLSA_OK;
+    return s.d <= 64 ? launch_fwd<64>(s, a, p, st) : launch_fwd<128>(s, a, p, st);
 }
 
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st) {
