@@ -166,6 +166,9 @@ DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st);
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st);
+// dense_split_wide_tc.cu: the backward pass at 64 < d <= 128.
+int launch_dense_split_wide_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
+                                cudaStream_t st);
 int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
                            cudaStream_t st);
 

@@ -1,0 +1,46 @@
+// dense_split.cuh -- fp32 operands as three bf16 planes: what the kernels on them share.
+#pragma once
+
+#include "dense_tc.cuh"
+
+namespace llsa {
+namespace tc {
+
+// The six terms, small ones first: plane of the first operand, of the second.
+__device__ __forceinline__ constexpr int term_a(int i) { return i == 0 ? 2 : i == 1 ? 0 : i == 2 ? 1 : i == 3 ? 1 : 0; }
+__device__ __forceinline__ constexpr int term_b(int i) { return i == 0 ? 0 : i == 1 ? 2 : i == 2 ? 1 : i == 3 ? 0 : i == 4 ? 1 : 0; }
+
+// Two fp32 values as three packed bf16 pairs.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
+    p1 = pack_bf16x2(x, y);
+    x -= __uint_as_float(p1 << 16);
+    y -= __uint_as_float(p1 & 0xffff0000u);
+    p2 = pack_bf16x2(x, y);
+    x -= __uint_as_float(p2 << 16);
+    y -= __uint_as_float(p2 & 0xffff0000u);
+    p3 = pack_bf16x2(x, y);
+}
+
+// One thread: the three planes of ROWS rows from `row` on of a tensor of `slices`
+// slices, as regions of 64 columns.
+template <int ROWS, int D>
+__device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, int slices,
+                                            uint32_t mbar) {
+    mbar_arrive_expect_tx(mbar, 3 * ROWS * D * 2);
+    for (int p = 0; p < 3; p++)
+        for (int c = 0; c < D / 64; c++)
+            tma_load_3d(smem_u32(dst + (p * (D / 64) + c) * ROWS * 128), map, c * 64, row, p * slices + slice, mbar);
+}
+
+template <int COLS>
+__device__ __forceinline__ void store_rowpart(float* dst, const float* o, float f, int c0, int d) {
+#pragma unroll
+    for (int c = 0; c < COLS; c += 4)
+        if (c0 + c < d) {
+            const float v[4] = {o[c] * f, o[c + 1] * f, o[c + 2] * f, o[c + 3] * f};
+            store4(dst + c0 + c, v);
+        }
+}
+
+}  // namespace tc
+}  // namespace llsa

@@ -23,7 +23,7 @@
 // (zeros behind d); a tile is three planes of 16 KB.
 #include <algorithm>
 
-#include "dense_tc.cuh"
+#include "dense_split.cuh"
 
 namespace llsa {
 namespace {
@@ -33,10 +33,6 @@ using namespace tc;
 constexpr int kPlane = kTileRows * 128;  // bytes of 128 rows x 64 bf16
 constexpr int kTile = 3 * kPlane;
 constexpr int BT = kTileRows;
-
-// The six terms, small ones first: plane of the first operand, of the second.
-__device__ __forceinline__ constexpr int term_a(int i) { return i == 0 ? 2 : i == 1 ? 0 : i == 2 ? 1 : i == 3 ? 1 : 0; }
-__device__ __forceinline__ constexpr int term_b(int i) { return i == 0 ? 0 : i == 1 ? 2 : i == 2 ? 1 : i == 3 ? 0 : i == 4 ? 1 : 0; }
 
 // ----------------------------------------------------------------- planes --
 
@@ -67,38 +63,6 @@ __global__ void __launch_bounds__(256) dense_planes_kernel(const __grid_constant
             *reinterpret_cast<uint4*>(a.out[t] + p * n + i) = u;
         }
     }
-}
-
-// Two fp32 values as three packed bf16 pairs.
-__device__ __forceinline__ void split2(float x, float y, uint32_t& p1, uint32_t& p2, uint32_t& p3) {
-    p1 = pack_bf16x2(x, y);
-    x -= __uint_as_float(p1 << 16);
-    y -= __uint_as_float(p1 & 0xffff0000u);
-    p2 = pack_bf16x2(x, y);
-    x -= __uint_as_float(p2 << 16);
-    y -= __uint_as_float(p2 & 0xffff0000u);
-    p3 = pack_bf16x2(x, y);
-}
-
-// One thread: the three planes of ROWS rows from `row` on of a tensor of `slices`
-// slices, as regions of 64 columns.
-template <int ROWS, int D>
-__device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, int slices,
-                                            uint32_t mbar) {
-    mbar_arrive_expect_tx(mbar, 3 * ROWS * D * 2);
-    for (int p = 0; p < 3; p++)
-        for (int c = 0; c < D / 64; c++)
-            tma_load_3d(smem_u32(dst + (p * (D / 64) + c) * ROWS * 128), map, c * 64, row, p * slices + slice, mbar);
-}
-
-template <int COLS>
-__device__ __forceinline__ void store_rowpart(float* dst, const float* o, float f, int c0, int d) {
-#pragma unroll
-    for (int c = 0; c < COLS; c += 4)
-        if (c0 + c < d) {
-            const float v[4] = {o[c] * f, o[c + 1] * f, o[c + 2] * f, o[c + 3] * f};
-            store4(dst + c0 + c, v);
-        }
 }
 
 // ---------------------------------------------------------------- forward --
@@ -658,15 +622,15 @@ int write_planes(const float* const* x, const long long* elems, int n, void* ws,
 
 }  // namespace
 
-static bool fits(const DenseShape& s, int most) {
-    return s.dtype == LLSA_DTYPE_F32 && s.d <= most && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
+static bool fits(const DenseShape& s) {
+    return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
 }
-bool dense_split_bwd_supported(const DenseShape& s) { return fits(s, 64); }
+bool dense_split_bwd_supported(const DenseShape& s) { return fits(s); }
 // The CUDA-core kernel is the faster one where the keys are one of its tiles and the
 // rows few (12 heads x 64 tokens 8.4 us against 9.5; 4 heads x 5 queries x 300 keys 26.6
 // against 13.8); backward it is not even there (28 against 14).
 bool dense_split_fwd_supported(const DenseShape& s) {
-    return fits(s, 128) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
+    return fits(s) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
 }
 
 DenseSplit dense_split_fwd_split(const DenseShape& s) {
@@ -719,6 +683,7 @@ int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, v
 
 int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
                            cudaStream_t st) {
+    if (s.d > 64) return launch_dense_split_wide_bwd(s, aq, ak, planes, st);
     CUtensorMap mq, mg, mk, mv;
     LLSA_TRY(make_tmap_rows(&mq, planes[0], 3LL * s.slices, s.R, s.d, BT));
     LLSA_TRY(make_tmap_rows(&mg, planes[1], 3LL * s.slices, s.R, s.d, BT));

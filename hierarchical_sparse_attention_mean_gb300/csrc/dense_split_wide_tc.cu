@@ -1,0 +1,348 @@
+// dense_split_wide_tc.cu -- dense attention backward in fp32 on the tcgen05 tensor
+// cores for 64 < d <= 128, operands as three bf16 planes and six products per term
+// as at d <= 64.
+//
+// Three kinds of blocks own 128 rows each and stream tiles of 64 rows of the other
+// side: dq (X1, X2, Y1, Y2 = Q, dO, K, V) and dk (K, V, Q, dO), which are the same
+// pass, and dv (K, -, Q, dO), which needs no dP. dk and dv apart cost S a second
+// time; together their sums would be 256 columns per row, half of the registers.
+//
+// The planes of X1 and X2 would fill 192 KB, so one buffer A holds them in turn: an
+// even item makes S, then dP, an odd one dP, then S, and A changes once per item,
+// after the item's first product. Y1 and Y2 take 48 KB each. Sums stay in tensor
+// memory for one item and are carried in registers.
+//
+// Bound by the chain of an item, some 10,000 clocks: a product of 128 x 64 x 128 is
+// 2,285 (S, dP) and 1,536 (sums), the change of A about 1,900. 4 heads x 2,048
+// tokens, d = 128: CUDA cores 1,065 us.
+//
+// Roles: warps 0-15 elementwise and epilogue, 16 issues the MMAs, 17 copies A, 18 and
+// 19 copy Y1 and Y2. Tensor memory: S at 0, dP at 64, planes 1 and 2 of dS (dv: P) over
+// S, 16 columns over the same 16, plane 3 at 128, the sums at 256.
+#include <algorithm>
+
+#include "dense_split.cuh"
+
+namespace llsa {
+namespace {
+
+using namespace tc;
+
+constexpr int BT = kTileRows, SN = 64, D = 128;  // stationary rows, streamed rows, columns
+constexpr int kRegionX = BT * 128, kRegionY = SN * 128;  // bytes of 64 columns
+constexpr int kPlaneX = BT * D * 2, kPlaneY = SN * D * 2;
+constexpr int kWarps = 16, kCols = SN / 4;
+// 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take
+// 104 of them, the 128 others keep 64.
+constexpr int kThreads = (kWarps + 4) * 32, kRegsElementwise = 104, kRegsOther = 64;
+constexpr int kSmem = 3 * kPlaneX + 6 * kPlaneY + 2 * SN * 4 + 512;
+
+enum Kind { kDq, kDk, kDv };
+
+struct Bars {
+    uint64_t a_full, a_empty, y_full[2], y_empty[2], s_full, dp_full, ds_ready, acc_full, acc_free, drain;
+    uint32_t tmem_slot;
+    int abort_flag;
+};
+
+template <Kind KIND>
+__device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensorMap& mx2, const CUtensorMap& my1,
+                                          const CUtensorMap& my2, const DenseArgs& a, int piece) {
+    constexpr bool KEYS = KIND != kDq, WITH_DP = KIND != kDv;
+    using List = Items<KEYS, SN>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    unsigned char *sA = sm, *sY = sm + 3 * kPlaneX;
+    float* stats = reinterpret_cast<float*>(sY + 6 * kPlaneY);  // KEYS: -l2 and -D of the item's rows
+    Bars* bar = reinterpret_cast<Bars*>(sY + 6 * kPlaneY + 2 * SN * 4);
+    volatile int* abort_flag = &bar->abort_flag;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
+        if (threadIdx.x == 0) set_status(a.status, LLSA_ERR_TIMEOUT);
+        return;
+    }
+    const int extent = KEYS ? a.nk : a.R;
+    const DenseWork work = dense_work(a, piece, (extent + BT - 1) / BT);
+    const int slice = work.slice, part = work.part;
+    const int x0 = (a.causal && !KEYS ? work.blocks - 1 - work.block : work.block) * BT;
+    const DenseSpan sp = dense_span(a, slice);
+    const int first = a.splits > 1 ? part * a.chunk : 0;
+    int stop;
+    if constexpr (KEYS) {
+        stop = x0 < sp.lk ? (a.splits > 1 ? min(a.R, first + a.chunk) : a.R) : 0;
+    } else {
+        stop = dense_tile_kend(a, sp, x0 < a.nq ? x0 : x0 % a.nq, BT);
+        if (a.splits > 1) stop = min(stop, first + a.chunk);
+    }
+    List start(a, sp, x0, first, 0, stop);
+    start.start(a);
+    const bool any = !start.done();
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&bar->a_full), 1);
+        mbar_init(smem_u32(&bar->a_empty), 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(smem_u32(&bar->y_full[i]), 1);
+            mbar_init(smem_u32(&bar->y_empty[i]), 1);
+        }
+        mbar_init(smem_u32(&bar->s_full), 1);
+        mbar_init(smem_u32(&bar->dp_full), 1);
+        mbar_init(smem_u32(&bar->ds_ready), kWarps);
+        mbar_init(smem_u32(&bar->acc_full), 1);
+        mbar_init(smem_u32(&bar->acc_free), kWarps);
+        mbar_init(smem_u32(&bar->drain), 1);
+        bar->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
+    const uint32_t tDP = tbase + 64, t3 = tbase + 128, tAcc = tbase + 256;
+
+    if (warp >= kWarps) {
+        regs_dec<kRegsOther>();
+        if (warp == kWarps + 1) {
+            // ------------------------------------------------------ copies of A
+            // X1 and X2 in turn, the next one behind the first product of every item
+            if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+                const uint32_t full = smem_u32(&bar->a_full);
+                load_planes<BT, D>(sA, &mx1, x0, slice, a.slices, full);
+                int n = 0;
+                if (WITH_DP)
+                    for (List it = start; !it.done(); it.next(a)) {
+                        if (!bar_wait(smem_u32(&bar->a_empty), n & 1, abort_flag, a)) break;
+                        load_planes<BT, D>(sA, n % 2 == 0 ? &mx2 : &mx1, x0, slice, a.slices, full);
+                        n++;
+                    }
+                land(full, n & 1);  // copies still in flight must land before the block exits
+            }
+        } else if (warp > kWarps + 1) {
+            // ------------------------------------------- copies of Y1, of Y2
+            if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+                const int k = warp - kWarps - 2;
+                const uint32_t full = smem_u32(&bar->y_full[k]);
+                int n = 0;
+                for (List it = start; !it.done(); it.next(a)) {
+                    if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
+                    if (KEYS && k == 0) {  // one phase for the tile and the rows' numbers
+                        const long long row = (long long)slice * a.Rp + it.pos;
+                        mbar_arrive_expect_tx(full, 3 * kPlaneY + 2 * SN * 4);
+                        for (int p = 0; p < 3; p++)
+                            for (int c = 0; c < 2; c++)
+                                tma_load_3d(smem_u32(sY + p * kPlaneY + c * kRegionY), &my1, c * 64, it.pos, p * a.slices + slice,
+                                            full);
+                        bulk_load(smem_u32(stats), a.nl2 + row, SN * 4, full);
+                        bulk_load(smem_u32(stats + SN), a.nd + row, SN * 4, full);
+                    } else {
+                        load_planes<SN, D>(sY + k * 3 * kPlaneY, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                    }
+                    n++;
+                }
+                if (n > 0) land(full, (n - 1) & 1);
+            }
+        } else {
+            // ------------------------------------------------------- MMA issuer
+            const uint32_t leader = elect_lane();
+            constexpr uint32_t idS = idesc_bf16(BT, SN, 0, 0), idA = idesc_bf16(BT, D, 0, 1);
+            const uint64_t dA = desc_sw128(smem_u32(sA), 16, 1024), dY = desc_sw128(smem_u32(sY), 16, 1024);
+            const uint64_t dM = desc_sw128(smem_u32(sY), kRegionY, 1024);  // the streamed tiles read along their rows
+            // rows whose P and dS are 0 by the lengths may hold anything: cleared, as they meet those zeros in the sums
+            auto clear_rows = [&](unsigned char* tile, const List& it) {
+                if constexpr (KEYS) {
+                    if (it.all || it.t0 + SN <= it.sp.lq) return;
+                    int t = it.t0 + lane;
+                    for (int x = lane; x < SN; x += 32, t += 32)
+                        if (t % a.nq >= it.sp.lq)
+                            for (int r = 0; r < 6; r++)
+                                for (int e = 0; e < 8; e++)
+                                    reinterpret_cast<uint4*>(tile + r * kRegionY + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
+                } else {
+                    const int live = it.sp.lk - it.pos;
+                    if (live >= SN) return;
+                    for (int r = 0; r < 6; r++)
+                        for (int x = live * 8 + lane; x < SN * 8; x += 32)
+                            reinterpret_cast<uint4*>(tile + r * kRegionY)[x] = make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_async_smem();
+                __syncwarp();
+            };
+            auto take_y = [&](const List& it, int k, int n) {
+                if (!warp_wait(smem_u32(&bar->y_full[k]), n & 1, abort_flag, a)) return false;
+                if (KEYS || k == 0) clear_rows(sY + k * 3 * kPlaneY, it);  // V only enters dP, which the mask covers
+                return true;
+            };
+            // S (k 0) or dP (k 1) of item n, of what A holds now
+            auto issue_tile = [&](const List& it, int k, int n) {
+                if (!take_y(it, k, n)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < 6; i++)
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ks++)
+                        mma_ss(leader, tbase + k * 64, dA + ((term_a(i) * kPlaneX + (ks / 4) * kRegionX + (ks % 4) * 32) >> 4),
+                               dY + ((k * 3 * kPlaneY + term_b(i) * kPlaneY + (ks / 4) * kRegionY + (ks % 4) * 32) >> 4), idS,
+                               i > 0 || ks > 0);
+                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+                if (k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
+                return true;
+            };
+            // sums = (dS or P) (streamed tile k, read along its rows)
+            auto issue_sum = [&](int k) {
+#pragma unroll
+                for (int i = 0; i < 6; i++) {
+                    const uint32_t op = term_a(i) == 2 ? t3 : tbase + term_a(i) * 8, step = term_a(i) == 2 ? 8 : 16;
+#pragma unroll
+                    for (int ks = 0; ks < SN / 16; ks++)
+                        mma_ts(leader, tAcc, op + ks * step, dM + ((k * 3 * kPlaneY + term_b(i) * kPlaneY + ks * 2048) >> 4), idA,
+                               i > 0 || ks > 0);
+                }
+                commit(leader, smem_u32(&bar->y_empty[0]));
+                if (k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
+                commit(leader, smem_u32(&bar->acc_full));
+            };
+            bool ok = any && warp_wait(smem_u32(&bar->a_full), 0, abort_flag, a);
+            int n = 0;
+            for (List it = start; ok && !it.done(); it.next(a), n++) {
+                if (WITH_DP) {
+                    ok = issue_tile(it, n & 1, n);
+                    if (!ok) break;
+                    commit(leader, smem_u32(&bar->a_empty));
+                    ok = warp_wait(smem_u32(&bar->a_full), (n + 1) & 1, abort_flag, a) && issue_tile(it, ~n & 1, n);
+                } else {
+                    ok = issue_tile(it, 0, n) && take_y(it, 1, n);
+                }
+                ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
+                if (ok && n > 0) ok = warp_wait(smem_u32(&bar->acc_free), (n - 1) & 1, abort_flag, a);
+                if (!ok) break;
+                tc_fence_after();
+                issue_sum(WITH_DP ? 0 : 1);
+            }
+            // no MMA may be in flight when tensor memory is released
+            commit(leader, smem_u32(&bar->drain));
+            if (lane == 0) land(smem_u32(&bar->drain), 0);
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------- elementwise, epilogue
+        regs_inc<kRegsElementwise>();
+        const int w = warp >> 2, q4 = warp & 3;  // quarter of the columns, of the rows
+        const uint32_t lanes = (uint32_t)(q4 * 32) << 16;
+        const int x = x0 + q4 * 32 + lane;       // stationary row
+        const float sl2 = a.scale * kDenseLog2e;
+        float nl2 = 0.f, nd = 0.f;
+        int kend = 0;
+        if constexpr (!KEYS) {
+            nl2 = a.nl2[(long long)slice * a.Rp + x];  // Rp is a multiple of 128
+            nd = a.nd[(long long)slice * a.Rp + x];
+            kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
+        }
+        float acc[32];  // this row's sums of 32 columns
+#pragma unroll
+        for (int i = 0; i < 32; i++) acc[i] = 0.f;
+        auto take_sums = [&](int item) {
+            bar_wait(smem_u32(&bar->acc_full), item & 1, abort_flag, a);
+            tc_fence_after();
+            uint32_t o[32];
+            tmem_ld32_nowait(tAcc + w * 32 + lanes, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i++) acc[i] += __uint_as_float(o[i]);
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->acc_free), lane);
+        };
+        int n = 0;
+        for (List it = start; !it.done(); it.next(a), n++) {
+            if (n > 0) take_sums(n - 1);  // while S and dP of this item are made
+            if (KEYS) bar_wait(smem_u32(&bar->y_full[0]), n & 1, abort_flag, a);  // the streamed rows' numbers
+            bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
+            if (WITH_DP) bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);
+            tc_fence_after();
+            const int lim = KEYS ? 0 : kend - it.pos - w * kCols;
+            const bool cut = KEYS ? a.causal && (it.t0 + SN > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)
+                                  : __any_sync(0xffffffffu, lim < kCols);
+            int t = KEYS && cut ? (it.t0 + w * kCols) % a.nq : 0;
+            const uint32_t at = lanes + w * kCols;
+            uint32_t s[16], g[16], p12[16], p3[8];
+            tmem_ld16_nowait(tbase + at, s);
+            if (WITH_DP) tmem_ld16_nowait(tDP + at, g);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 16; c++) {
+                const int col = w * kCols + c;
+                float p = ex2(fmaf(__uint_as_float(s[c]), sl2, KEYS ? stats[col] : nl2));
+                if (WITH_DP) p *= __uint_as_float(g[c]) + (KEYS ? stats[SN + col] : nd);
+                if (cut) {
+                    p = (KEYS ? x > t + sp.lk - sp.lq : c >= lim) ? 0.f : p;
+                    if (KEYS && ++t == a.nq) t = 0;
+                }
+                s[c] = __float_as_uint(p);
+            }
+#pragma unroll
+            for (int c = 0; c < 16; c += 2)
+                split2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]), p12[c >> 1], p12[8 + (c >> 1)], p3[c >> 1]);
+            tmem_st16(tbase + at, p12);
+            tmem_st8(t3 + lanes + w * kCols / 2, p3);
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(smem_u32(&bar->ds_ready), lane);
+        }
+        if (n > 0) take_sums(n - 1);
+        // rows without a gradient hold whatever their padding made: zero
+        const bool live = any && (KEYS ? x < sp.lk : kend > 0);
+        const long long row = (long long)slice * extent + x, all = (long long)a.slices * extent;
+#pragma unroll
+        for (int i = 0; i < 32; i++) acc[i] = live ? acc[i] : 0.f;
+        float* base = a.splits > 1 ? a.part + ((KIND == kDv ? a.splits : 0) + part) * all * a.d
+                                   : static_cast<float*>(KIND == kDq ? a.dq : KIND == kDk ? a.dk : a.dv);
+        if (x < extent) store_rowpart<32>(base + row * a.d, acc, KIND == kDv ? 1.f : a.scale, w * 32, a.d);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarps) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+// Tensor maps: of 128 rows for A, of 64 for the streamed tiles.
+struct Maps {
+    CUtensorMap q, g, k, v;
+};
+
+__global__ void __launch_bounds__(kThreads, 1)
+dense_bwd_wide_kernel(const __grid_constant__ Maps x, const __grid_constant__ Maps y, const __grid_constant__ DenseArgs aq,
+                      const __grid_constant__ DenseArgs ak, int key_pieces) {
+    const int piece = blockIdx.x;
+    if (piece < key_pieces)
+        wide_side<kDk>(x.k, x.v, y.q, y.g, ak, piece);
+    else if (piece < 2 * key_pieces)
+        wide_side<kDv>(x.k, x.k, y.q, y.g, ak, piece - key_pieces);
+    else
+        wide_side<kDq>(x.q, x.g, y.k, y.v, aq, piece - 2 * key_pieces);
+}
+
+}  // namespace
+
+int launch_dense_split_wide_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
+                                cudaStream_t st) {
+    Maps x, y;
+    for (int i = 0; i < 2; i++) {
+        Maps& m = i == 0 ? x : y;
+        const int rows = i == 0 ? BT : SN;
+        LLSA_TRY(make_tmap_rows(&m.q, planes[0], 3LL * s.slices, s.R, s.d, rows));
+        LLSA_TRY(make_tmap_rows(&m.g, planes[1], 3LL * s.slices, s.R, s.d, rows));
+        LLSA_TRY(make_tmap_rows(&m.k, planes[2], 3LL * s.slices, s.nk, s.d, rows));
+        LLSA_TRY(make_tmap_rows(&m.v, planes[3], 3LL * s.slices, s.nk, s.d, rows));
+    }
+    static_assert(kSmem <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
+    cudaFuncSetAttribute(dense_bwd_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;
+    const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.splits;
+    if (pq + 2 * pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("dense_bwd_split", st,
+                dense_bwd_wide_kernel<<<(unsigned)(pq + 2 * pk), kThreads, kSmem, st>>>(x, y, aq, ak, (int)pk));
+    return LLSA_OK;
+}
+
+}  // namespace llsa

@@ -81,9 +81,9 @@ struct Stage {
 
 constexpr int kTileRows = 128;  // rows of every tile of the backward kernels
 
-// The items of a block: tiles of 128 rows of the streamed side, those that the
+// The items of a block: tiles of ROWS rows of the streamed side, those that the
 // mask leaves nothing of skipped. Every role walks the same list.
-template <bool KEYS>
+template <bool KEYS, int ROWS = kTileRows>
 struct Items {
     int pos, t0, stop;  // first row of the tile; its token in its head (KEYS); end of the axis
     int x0;             // the block's first stationary row
@@ -99,7 +99,7 @@ struct Items {
     }
     __device__ __forceinline__ bool done() const { return pos >= stop; }
     __device__ __forceinline__ void next(const DenseArgs& a) {
-        pos += kTileRows;
+        pos += ROWS;
         if (all) return;
         turn(a);
         settle(a);
@@ -107,12 +107,12 @@ struct Items {
 
 private:
     __device__ __forceinline__ void turn(const DenseArgs& a) {
-        t0 += kTileRows;
+        t0 += ROWS;
         if (t0 >= a.nq) t0 = t0 - a.nq < a.nq ? t0 - a.nq : t0 % a.nq;
     }
     __device__ __forceinline__ void settle(const DenseArgs& a) {
-        while (pos < stop && dense_tile_kend(a, sp, t0, kTileRows) <= x0) {
-            pos += kTileRows;
+        while (pos < stop && dense_tile_kend(a, sp, t0, ROWS) <= x0) {
+            pos += ROWS;
             turn(a);
         }
     }

@@ -108,7 +108,7 @@ def test_scales(amp, scale, dtype):
         ref.check(n, got[n], want[n])
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("bf16", 200)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 128), ("bf16", 200)])
 @pytest.mark.parametrize("nq,nk,h,kv", [(1, 20000, 2, 2), (2, 9000, 8, 2), (5000, 33, 2, 1)])
 def test_long_axis_is_split(nq, nk, h, kv, dtype, d):
     """Few rows over many keys (and few keys under many rows): the long axis runs in parts."""
@@ -143,7 +143,7 @@ def test_bad_lengths_are_clamped_and_reported(dtype):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 104)])
 def test_repeats_are_bit_equal(dtype, d):
     x = make(2, 8, 2, 333, 450, d, dtype, q_len=[333, 200], k_len=[450, 77])
     a, b = (run(x, True, 0.0, [333, 200], [450, 77], dtype) for _ in range(2))
@@ -205,7 +205,7 @@ def test_other_stream_and_captured_graph(dtype):
             assert torch.equal(got[n], want[n]), n
 
 
-@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("fp32", 64, 300)])
+@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("fp32", 64, 300), ("fp32", 128, 300)])
 def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d, nq):
     """With the copying warps switched off every consumer's first wait runs out: the
     status reads TIMEOUT once, the kernels end, and the next calls are right."""
@@ -393,7 +393,7 @@ def test_few_rows(h, kv, nq, d, dtype):
         ref.check(n, got[n], want[n])
 
 
-@pytest.mark.parametrize("d", [8, 24, 40, 64])
+@pytest.mark.parametrize("d", [8, 24, 40, 64, 72, 128])
 @pytest.mark.parametrize("nq,nk", [(127, 129), (128, 128), (129, 128), (5, 3277), (3277, 5), (1, 16384)])
 def test_fp32_around_the_choice_of_kernels(nq, nk, d):
     """Pairs of a slice just below and above the number from which fp32 runs on the tensor cores."""
@@ -417,7 +417,7 @@ def test_fp32_magnitudes():
         ref.check(n, got[n], want[n])
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 128)])
 def test_two_streams_at_once(dtype, d):
     """Calls on two streams, workspaces of their own, give what they give alone."""
     xs = [make(2, 8, 4, 260, 3000, d, dtype, seed=s) for s in (20, 21)]
