@@ -157,7 +157,7 @@ DenseSplit dense_tc_dkv_split(const DenseShape& s);
 int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st);
 
-// dense_split_tc.cu: fp32 on the tensor cores, d <= 64 (planes: three bf16 planes
+// dense_split_tc.cu: fp32 on the tensor cores, d <= 128 (planes: three bf16 planes
 // of q, k, v, or of q, dout, k, v, at the start of the workspace).
 bool dense_split_fwd_supported(const DenseShape& s);
 bool dense_split_bwd_supported(const DenseShape& s);

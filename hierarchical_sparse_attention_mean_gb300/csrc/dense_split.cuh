@@ -21,15 +21,13 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& p1, uint32_t&
     p3 = pack_bf16x2(x, y);
 }
 
-// One thread: the three planes of ROWS rows from `row` on of a tensor of `slices`
-// slices, as regions of 64 columns.
+// One thread: the three planes of ROWS rows from `row` on, 64 columns after 64 columns,
+// in one copy each. `more` bytes come with them on the same barrier.
 template <int ROWS, int D>
-__device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, int slices,
-                                            uint32_t mbar) {
-    mbar_arrive_expect_tx(mbar, 3 * ROWS * D * 2);
-    for (int p = 0; p < 3; p++)
-        for (int c = 0; c < D / 64; c++)
-            tma_load_3d(smem_u32(dst + (p * (D / 64) + c) * ROWS * 128), map, c * 64, row, p * slices + slice, mbar);
+__device__ __forceinline__ void load_planes(unsigned char* dst, const CUtensorMap* map, int row, int slice, uint32_t mbar,
+                                            int more = 0) {
+    mbar_arrive_expect_tx(mbar, 3 * ROWS * D * 2 + more);
+    for (int c = 0; c < D / 64; c++) tma_load_4d(smem_u32(dst + c * 3 * ROWS * 128), map, c * 64, row, slice, 0, mbar);
 }
 
 template <int COLS>

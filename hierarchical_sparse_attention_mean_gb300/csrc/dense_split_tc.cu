@@ -1,5 +1,5 @@
-// dense_split_tc.cu -- dense attention in fp32 on the tcgen05 tensor cores (d <=
-// 64), forward and backward.
+// dense_split_tc.cu -- dense attention in fp32 on the tcgen05 tensor cores: forward up
+// to 128 columns, backward up to 64 (behind them: dense_split_wide_tc.cu).
 //
 // Mathematics. Each fp32 operand x is written as x1 + x2 + x3 with x1 = bf16(x),
 // x2 = bf16(x - x1), x3 = bf16(x - x1 - x2): 8 bits and a sign each, so what is
@@ -20,7 +20,7 @@
 //
 // A pass before writes the three planes of q, k, v (and dout) to the workspace,
 // plane by plane, where TMA fetches them as ordinary bf16 tiles of 64 columns
-// (zeros behind d); a tile is three planes of 16 KB.
+// (zeros behind d), the three planes of a tile in one copy.
 #include <algorithm>
 
 #include "dense_split.cuh"
@@ -76,7 +76,7 @@ constexpr int kFwdWarps = 8, kFwdThreads = (kFwdWarps + 3) * 32;
 template <int D>
 struct FwdCfg {
     static constexpr int BN = D == 64 ? 128 : 64, NC = D / 64;
-    static constexpr int PQ = BT * D * 2, PK = BN * D * 2, RK = BN * 128;  // bytes: a plane of Q, of K or V; 64 columns of that
+    static constexpr int PQ = BT * D * 2, PK = BN * D * 2, RQ = BT * 128, RK = BN * 128;  // bytes of a plane, of 64 columns of it
     static constexpr int KST = D == 64 ? 2 : 1;                           // K tiles
     static constexpr int SMEM = 3 * (PQ + (KST + 1) * PK) + 1024;
     static constexpr int TM_P = 2 * BN, TM_O = D == 64 ? 448 : 256;       // tensor memory: S at 0 and BN
@@ -139,13 +139,13 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         // ----------------------------------------------------------- copies
         if (lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
             const bool keys = warp == kFwdWarps + 1;
-            if (keys) load_planes<BT, D>(sQ, &mq, r0, slice, a.slices, smem_u32(&bar->q_full));
+            if (keys) load_planes<BT, D>(sQ, &mq, r0, slice, smem_u32(&bar->q_full));
             int t = 0;
             for (; t < n; t++) {
                 const int st = keys ? t % C::KST : 0, use = keys ? t / C::KST : t;
                 const uint32_t full = smem_u32(keys ? &bar->k_full[st] : &bar->v_full);
                 if (use > 0 && !bar_wait(smem_u32(keys ? &bar->k_empty[st] : &bar->v_empty), (use - 1) & 1, abort_flag, a)) break;
-                load_planes<BN, D>(keys ? sK + st * 3 * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, a.slices, full);
+                load_planes<BN, D>(keys ? sK + st * 3 * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, full);
             }
             // copies still in flight must land before the block exits
             if (keys) land(smem_u32(&bar->q_full), 0);
@@ -159,7 +159,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const uint32_t leader = elect_lane();
         constexpr uint32_t idS = idesc_bf16(BT, BN, 0, 0), idO = idesc_bf16(BT, D, 0, 1);
         const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024), dK = desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t dV = desc_sw128(smem_u32(sV), C::RK, 1024);
+        const uint64_t dV = desc_sw128(smem_u32(sV), 3 * C::RK, 1024);
         auto issue_S = [&](int t) {
             const int b = t & 1, st = t % C::KST;
             if (!warp_wait(smem_u32(&bar->k_full[st]), (t / C::KST) & 1, abort_flag, a)) return false;
@@ -170,8 +170,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             for (int i = 0; i < 6; i++)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++)
-                    mma_ss(leader, tbase + b * BN, dQ + ((term_a(i) * C::PQ + (ks / 4) * BT * 128 + (ks % 4) * 32) >> 4),
-                           dT + ((term_b(i) * C::PK + (ks / 4) * C::RK + (ks % 4) * 32) >> 4), idS, i > 0 || ks > 0);
+                    mma_ss(leader, tbase + b * BN, dQ + ((term_a(i) * C::RQ + (ks / 4) * 3 * C::RQ + (ks % 4) * 32) >> 4),
+                           dT + ((term_b(i) * C::RK + (ks / 4) * 3 * C::RK + (ks % 4) * 32) >> 4), idS, i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->s_full[b]));
             commit(leader, smem_u32(&bar->k_empty[st]));
             return true;
@@ -196,7 +196,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             for (int i = 0; i < 6; i++)
 #pragma unroll
                 for (int ks = 0; ks < BN / 16; ks++)
-                    mma_ts(leader, tO, tP + term_a(i) * (BN / 2) + ks * 8, dV + ((term_b(i) * C::PK + ks * 2048) >> 4), idO,
+                    mma_ts(leader, tO, tP + term_a(i) * (BN / 2) + ks * 8, dV + ((term_b(i) * C::RK + ks * 2048) >> 4), idO,
                            i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->o_done));
             commit(leader, smem_u32(&bar->v_empty));
@@ -391,20 +391,18 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             // ----------------------------------------------------------- copies
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const int k = warp - kBwdWarps - 1;
-                load_planes<BT, 64>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, a.slices, smem_u32(&bar->x_full[k]));
+                load_planes<BT, 64>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, smem_u32(&bar->x_full[k]));
                 const uint32_t full = smem_u32(&bar->y_full[k]);
                 int n = 0;
                 for (Items<KEYS> it = start; !it.done(); it.next(a)) {
                     if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
                     if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
                         const long long row = (long long)slice * a.Rp + it.pos;
-                        mbar_arrive_expect_tx(full, kTile + 2 * BT * 4);
-                        for (int p = 0; p < 3; p++)
-                            tma_load_3d(smem_u32(sY + kTile + p * kPlane), &my2, 0, it.pos, p * a.slices + slice, full);
+                        load_planes<BT, 64>(sY + kTile, &my2, it.pos, slice, full, 2 * BT * 4);
                         bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
                         bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
                     } else {
-                        load_planes<BT, 64>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                        load_planes<BT, 64>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, full);
                     }
                     n++;
                 }
@@ -623,7 +621,7 @@ int write_planes(const float* const* x, const long long* elems, int n, void* ws,
 }  // namespace
 
 static bool fits(const DenseShape& s) {
-    return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.R > 0 && s.nk > 0 && 3LL * s.slices <= kDenseMaxExtent;
+    return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.R > 0 && s.nk > 0;
 }
 bool dense_split_bwd_supported(const DenseShape& s) { return fits(s); }
 // The CUDA-core kernel is the faster one where the keys are one of its tiles and the
@@ -650,9 +648,9 @@ static int launch_fwd(const DenseShape& s, const DenseArgs& a, __nv_bfloat16* co
     using C = FwdCfg<D>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
     CUtensorMap mq, mk, mv;
-    LLSA_TRY(make_tmap_rows(&mq, p[0], 3LL * s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mk, p[1], 3LL * s.slices, s.nk, s.d, C::BN));
-    LLSA_TRY(make_tmap_rows(&mv, p[2], 3LL * s.slices, s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_planes(&mq, p[0], s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, p[1], s.slices, s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_planes(&mv, p[2], s.slices, s.nk, s.d, C::BN));
     cudaFuncSetAttribute(dense_fwd_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
     if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
@@ -685,10 +683,10 @@ int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const Dense
                            cudaStream_t st) {
     if (s.d > 64) return launch_dense_split_wide_bwd(s, aq, ak, planes, st);
     CUtensorMap mq, mg, mk, mv;
-    LLSA_TRY(make_tmap_rows(&mq, planes[0], 3LL * s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mg, planes[1], 3LL * s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mk, planes[2], 3LL * s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_rows(&mv, planes[3], 3LL * s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mq, planes[0], s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mg, planes[1], s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, planes[2], s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mv, planes[3], s.slices, s.nk, s.d, BT));
     static_assert(kBwdSmem <= 227 * 1024 && sizeof(BwdBars) <= 512, "shared memory budget");
     cudaFuncSetAttribute(dense_bwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;

@@ -8,17 +8,19 @@
 // time; together their sums would be 256 columns per row, half of the registers.
 //
 // The planes of X1 and X2 would fill 192 KB, so one buffer A holds them in turn: an
-// even item makes S, then dP, an odd one dP, then S, and A changes once per item,
-// after the item's first product. Y1 and Y2 take 48 KB each. Sums stay in tensor
-// memory for one item and are carried in registers.
+// even item makes S, then dP, and right behind it the next item's dP, for which
+// there is a second buffer; the odd item then only wants S. A changes once per item,
+// mostly while the threads or the sums are at work. Y1 and Y2 take 48 KB each. Sums
+// stay in tensor memory for one item and are carried in registers.
 //
-// Bound by the chain of an item, some 10,000 clocks: a product of 128 x 64 x 128 is
-// 2,285 (S, dP) and 1,536 (sums), the change of A about 1,900. 4 heads x 2,048
-// tokens, d = 128: CUDA cores 1,065 us.
+// Bound by the chain of an item, about 10,000 clocks: a product of 128 x 64 x 128 is
+// 2,285 (S, dP) and 1,536 (sums), and Y1 comes in between the sums and the next S. 4
+// heads x 2,048 tokens, d = 128: 268 us (80 TFLOP/s of the 10 d operations per
+// pair; CUDA cores 1,065 us).
 //
 // Roles: warps 0-15 elementwise and epilogue, 16 issues the MMAs, 17 copies A, 18 and
-// 19 copy Y1 and Y2. Tensor memory: S at 0, dP at 64, planes 1 and 2 of dS (dv: P) over
-// S, 16 columns over the same 16, plane 3 at 128, the sums at 256.
+// 19 copy Y1 and Y2. Tensor memory: S at 0, dP at 64 and 160, planes 1 and 2 of dS (dv:
+// P) over S, 16 columns over the same 16, plane 3 at 128, the sums at 256.
 #include <algorithm>
 
 #include "dense_split.cuh"
@@ -39,8 +41,10 @@ constexpr int kSmem = 3 * kPlaneX + 6 * kPlaneY + 2 * SN * 4 + 512;
 
 enum Kind { kDq, kDk, kDv };
 
+__device__ __forceinline__ uint32_t dp_column(int item) { return item & 1 ? 160 : 64; }
+
 struct Bars {
-    uint64_t a_full, a_empty, y_full[2], y_empty[2], s_full, dp_full, ds_ready, acc_full, acc_free, drain;
+    uint64_t a_full, a_empty, y_full[2], y_empty[2], s_full, dp_full[2], ds_ready, acc_full, acc_free, drain;
     uint32_t tmem_slot;
     int abort_flag;
 };
@@ -83,9 +87,9 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&bar->y_full[i]), 1);
             mbar_init(smem_u32(&bar->y_empty[i]), 1);
+            mbar_init(smem_u32(&bar->dp_full[i]), 1);
         }
         mbar_init(smem_u32(&bar->s_full), 1);
-        mbar_init(smem_u32(&bar->dp_full), 1);
         mbar_init(smem_u32(&bar->ds_ready), kWarps);
         mbar_init(smem_u32(&bar->acc_full), 1);
         mbar_init(smem_u32(&bar->acc_free), kWarps);
@@ -98,7 +102,7 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
-    const uint32_t tDP = tbase + 64, t3 = tbase + 128, tAcc = tbase + 256;
+    const uint32_t t3 = tbase + 128, tAcc = tbase + 256;
 
     if (warp >= kWarps) {
         regs_dec<kRegsOther>();
@@ -107,12 +111,12 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             // X1 and X2 in turn, the next one behind the first product of every item
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const uint32_t full = smem_u32(&bar->a_full);
-                load_planes<BT, D>(sA, &mx1, x0, slice, a.slices, full);
+                load_planes<BT, D>(sA, &mx1, x0, slice, full);
                 int n = 0;
                 if (WITH_DP)
                     for (List it = start; !it.done(); it.next(a)) {
                         if (!bar_wait(smem_u32(&bar->a_empty), n & 1, abort_flag, a)) break;
-                        load_planes<BT, D>(sA, n % 2 == 0 ? &mx2 : &mx1, x0, slice, a.slices, full);
+                        load_planes<BT, D>(sA, n % 2 == 0 ? &mx2 : &mx1, x0, slice, full);
                         n++;
                     }
                 land(full, n & 1);  // copies still in flight must land before the block exits
@@ -127,15 +131,11 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
                     if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
                     if (KEYS && k == 0) {  // one phase for the tile and the rows' numbers
                         const long long row = (long long)slice * a.Rp + it.pos;
-                        mbar_arrive_expect_tx(full, 3 * kPlaneY + 2 * SN * 4);
-                        for (int p = 0; p < 3; p++)
-                            for (int c = 0; c < 2; c++)
-                                tma_load_3d(smem_u32(sY + p * kPlaneY + c * kRegionY), &my1, c * 64, it.pos, p * a.slices + slice,
-                                            full);
+                        load_planes<SN, D>(sY, &my1, it.pos, slice, full, 2 * SN * 4);
                         bulk_load(smem_u32(stats), a.nl2 + row, SN * 4, full);
                         bulk_load(smem_u32(stats + SN), a.nd + row, SN * 4, full);
                     } else {
-                        load_planes<SN, D>(sY + k * 3 * kPlaneY, k == 0 ? &my1 : &my2, it.pos, slice, a.slices, full);
+                        load_planes<SN, D>(sY + k * 3 * kPlaneY, k == 0 ? &my1 : &my2, it.pos, slice, full);
                     }
                     n++;
                 }
@@ -146,7 +146,7 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             const uint32_t leader = elect_lane();
             constexpr uint32_t idS = idesc_bf16(BT, SN, 0, 0), idA = idesc_bf16(BT, D, 0, 1);
             const uint64_t dA = desc_sw128(smem_u32(sA), 16, 1024), dY = desc_sw128(smem_u32(sY), 16, 1024);
-            const uint64_t dM = desc_sw128(smem_u32(sY), kRegionY, 1024);  // the streamed tiles read along their rows
+            const uint64_t dM = desc_sw128(smem_u32(sY), 3 * kRegionY, 1024);  // the streamed tiles read along their rows
             // rows whose P and dS are 0 by the lengths may hold anything: cleared, as they meet those zeros in the sums
             auto clear_rows = [&](unsigned char* tile, const List& it) {
                 if constexpr (KEYS) {
@@ -180,10 +180,10 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
                 for (int i = 0; i < 6; i++)
 #pragma unroll
                     for (int ks = 0; ks < D / 16; ks++)
-                        mma_ss(leader, tbase + k * 64, dA + ((term_a(i) * kPlaneX + (ks / 4) * kRegionX + (ks % 4) * 32) >> 4),
-                               dY + ((k * 3 * kPlaneY + term_b(i) * kPlaneY + (ks / 4) * kRegionY + (ks % 4) * 32) >> 4), idS,
+                        mma_ss(leader, tbase + (k == 0 ? 0 : dp_column(n)), dA + ((term_a(i) * kRegionX + (ks / 4) * 3 * kRegionX + (ks % 4) * 32) >> 4),
+                               dY + ((k * 3 * kPlaneY + term_b(i) * kRegionY + (ks / 4) * 3 * kRegionY + (ks % 4) * 32) >> 4), idS,
                                i > 0 || ks > 0);
-                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
+                commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full[n & 1]));
                 if (k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
                 return true;
             };
@@ -194,7 +194,7 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
                     const uint32_t op = term_a(i) == 2 ? t3 : tbase + term_a(i) * 8, step = term_a(i) == 2 ? 8 : 16;
 #pragma unroll
                     for (int ks = 0; ks < SN / 16; ks++)
-                        mma_ts(leader, tAcc, op + ks * step, dM + ((k * 3 * kPlaneY + term_b(i) * kPlaneY + ks * 2048) >> 4), idA,
+                        mma_ts(leader, tAcc, op + ks * step, dM + ((k * 3 * kPlaneY + term_b(i) * kRegionY + ks * 2048) >> 4), idA,
                                i > 0 || ks > 0);
                 }
                 commit(leader, smem_u32(&bar->y_empty[0]));
@@ -204,13 +204,21 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             bool ok = any && warp_wait(smem_u32(&bar->a_full), 0, abort_flag, a);
             int n = 0;
             for (List it = start; ok && !it.done(); it.next(a), n++) {
-                if (WITH_DP) {
-                    ok = issue_tile(it, n & 1, n);
+                if (!WITH_DP) {
+                    ok = issue_tile(it, 0, n) && take_y(it, 1, n);
+                } else if (n & 1) {  // its dP is made
+                    ok = warp_wait(smem_u32(&bar->a_full), (n + 1) & 1, abort_flag, a) && issue_tile(it, 0, n);
+                } else {
+                    ok = issue_tile(it, 0, n);
                     if (!ok) break;
                     commit(leader, smem_u32(&bar->a_empty));
-                    ok = warp_wait(smem_u32(&bar->a_full), (n + 1) & 1, abort_flag, a) && issue_tile(it, ~n & 1, n);
-                } else {
-                    ok = issue_tile(it, 0, n) && take_y(it, 1, n);
+                    ok = warp_wait(smem_u32(&bar->a_full), (n + 1) & 1, abort_flag, a) && issue_tile(it, 1, n);
+                    List next = it;
+                    next.next(a);
+                    if (ok && !next.done()) {
+                        ok = issue_tile(next, 1, n + 1);
+                        if (ok) commit(leader, smem_u32(&bar->a_empty));
+                    }
                 }
                 ok = ok && warp_wait(smem_u32(&bar->ds_ready), n & 1, abort_flag, a);
                 if (ok && n > 0) ok = warp_wait(smem_u32(&bar->acc_free), (n - 1) & 1, abort_flag, a);
@@ -256,7 +264,7 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             if (n > 0) take_sums(n - 1);  // while S and dP of this item are made
             if (KEYS) bar_wait(smem_u32(&bar->y_full[0]), n & 1, abort_flag, a);  // the streamed rows' numbers
             bar_wait(smem_u32(&bar->s_full), n & 1, abort_flag, a);
-            if (WITH_DP) bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);
+            if (WITH_DP) bar_wait(smem_u32(&bar->dp_full[n & 1]), (n >> 1) & 1, abort_flag, a);
             tc_fence_after();
             const int lim = KEYS ? 0 : kend - it.pos - w * kCols;
             const bool cut = KEYS ? a.causal && (it.t0 + SN > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)
@@ -265,7 +273,7 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             const uint32_t at = lanes + w * kCols;
             uint32_t s[16], g[16], p12[16], p3[8];
             tmem_ld16_nowait(tbase + at, s);
-            if (WITH_DP) tmem_ld16_nowait(tDP + at, g);
+            if (WITH_DP) tmem_ld16_nowait(tbase + dp_column(n) + at, g);
             tmem_wait_ld();
 #pragma unroll
             for (int c = 0; c < 16; c++) {
@@ -330,10 +338,10 @@ int launch_dense_split_wide_bwd(const DenseShape& s, const DenseArgs& aq, const 
     for (int i = 0; i < 2; i++) {
         Maps& m = i == 0 ? x : y;
         const int rows = i == 0 ? BT : SN;
-        LLSA_TRY(make_tmap_rows(&m.q, planes[0], 3LL * s.slices, s.R, s.d, rows));
-        LLSA_TRY(make_tmap_rows(&m.g, planes[1], 3LL * s.slices, s.R, s.d, rows));
-        LLSA_TRY(make_tmap_rows(&m.k, planes[2], 3LL * s.slices, s.nk, s.d, rows));
-        LLSA_TRY(make_tmap_rows(&m.v, planes[3], 3LL * s.slices, s.nk, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.q, planes[0], s.slices, s.R, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.g, planes[1], s.slices, s.R, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.k, planes[2], s.slices, s.nk, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.v, planes[3], s.slices, s.nk, s.d, rows));
     }
     static_assert(kSmem <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
     cudaFuncSetAttribute(dense_bwd_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
