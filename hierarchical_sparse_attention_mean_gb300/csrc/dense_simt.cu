@@ -12,8 +12,8 @@
 // BM / 16 rows of the output. Operands sit in shared memory as fp32, rows of
 // DP + 4 floats: the 16 rows that a quarter warp reads then fall on distinct
 // banks. Bound by shared memory: per 4 columns of d a thread loads 8 vectors for 64
-// FMAs, which takes twice the FMAs' time (4 heads x 2,048 tokens in 128 columns of fp32:
-// forward 260 us, 33 TFLOP/s of 80; backward 1,065 us, 20).
+// FMAs, which takes twice the FMAs' time (4 heads x 2,048 tokens, d = 256, fp32:
+// forward 811 us, 21 TFLOP/s of 80; backward 3.5 ms, 12).
 #include <algorithm>
 
 #include "dense.h"
@@ -429,7 +429,7 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
 }
 
 // Pieces of keys first, they are the longer ones; those of rows fill up what they
-// leave (1 x 12 heads x 64 tokens at d = 128, fp32, 47.8 us in two launches, 28.4 in one).
+// leave (12 heads x 64 tokens of 128 columns in fp32 47.8 us in two launches, 28.4 in one).
 template <typename T, int DP, int BM>
 __global__ void __launch_bounds__(kThreads)
 dense_bwd_simt_kernel(const __grid_constant__ DenseArgs aq, const __grid_constant__ DenseArgs ak, int key_pieces) {
@@ -440,63 +440,57 @@ dense_bwd_simt_kernel(const __grid_constant__ DenseArgs aq, const __grid_constan
         rows_side<T, DP, BM>(aq, piece - key_pieces);
 }
 
-int block_rows(const DenseShape& s) { return s.d > 128 ? 32 : 64; }
+// Rows of a block. Tiles of 256 columns and 32 rows serve what has no tile of its
+// own: only the fp32 forward against a few keys comes here with fewer columns.
+int fwd_rows(const DenseShape& s) { return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.nk > 0 ? 64 : 32; }
+constexpr int kBwdRows = 32;
 
-struct Fwd {
-    template <typename T, int DP, int BM>
-    static int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-        constexpr int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * buffers<T, true>()) * tile + p;
-        static_assert(smem <= 227 * 1024, "shared memory budget");
-        const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
-        if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-        const dim3 grid((unsigned)blocks, a.splits);
-        cudaFuncSetAttribute(dense_fwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        LLSA_LAUNCH("dense_fwd_simt", st, dense_fwd_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
-        return LLSA_OK;
-    }
-};
+template <typename T, int DP, int BM>
+int launch_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    constexpr int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * buffers<T, true>()) * tile + p;
+    static_assert(smem <= 227 * 1024, "shared memory budget");
+    const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
+    if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, a.splits);
+    cudaFuncSetAttribute(dense_fwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    LLSA_LAUNCH("dense_fwd_simt", st, dense_fwd_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
+    return LLSA_OK;
+}
 
-struct Bwd {
-    template <typename T, int DP, int BM>
-    static int launch(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
-        constexpr int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (2 + 2 * buffers<T, false>()) * tile + 2 * p;
-        static_assert(smem <= 227 * 1024, "shared memory budget");
-        const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
-        const long long pk = (long long)((s.nk + BM - 1) / BM) * s.slices * ak.splits;
-        if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-        cudaFuncSetAttribute(dense_bwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        LLSA_LAUNCH("dense_bwd_simt", st,
-                    dense_bwd_simt_kernel<T, DP, BM><<<(unsigned)(pq + pk), kThreads, smem, st>>>(aq, ak, (int)pk));
-        return LLSA_OK;
-    }
-};
-
-template <typename Op, typename... Args>
-int launch_op(const DenseShape& s, const Args&... args) {
-    if (s.dtype == LLSA_DTYPE_F32)
-        return s.d <= 64    ? Op::template launch<float, 64, 64>(s, args...)
-               : s.d <= 128 ? Op::template launch<float, 128, 64>(s, args...)
-                            : Op::template launch<float, 256, 32>(s, args...);
-    return s.d <= 64    ? Op::template launch<__nv_bfloat16, 64, 64>(s, args...)
-           : s.d <= 128 ? Op::template launch<__nv_bfloat16, 128, 64>(s, args...)
-                        : Op::template launch<__nv_bfloat16, 256, 32>(s, args...);
+template <typename T>
+int launch_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
+    constexpr int BM = kBwdRows, DP = 256, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
+    constexpr int smem = (2 + 2 * buffers<T, false>()) * tile + 2 * p;
+    static_assert(smem <= 227 * 1024, "shared memory budget");
+    const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
+    const long long pk = (long long)((s.nk + BM - 1) / BM) * s.slices * ak.splits;
+    if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    cudaFuncSetAttribute(dense_bwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    LLSA_LAUNCH("dense_bwd_simt", st,
+                dense_bwd_simt_kernel<T, DP, BM><<<(unsigned)(pq + pk), kThreads, smem, st>>>(aq, ak, (int)pk));
+    return LLSA_OK;
 }
 
 }  // namespace
 
 DenseSplit dense_simt_fwd_split(const DenseShape& s) {
-    const int bm = block_rows(s);
+    const int bm = fwd_rows(s);
     return dense_make_split((long long)s.slices * ((s.R + bm - 1) / bm), s.nk, bm, 4);
 }
-DenseSplit dense_simt_dq_split(const DenseShape& s) { return dense_simt_fwd_split(s); }
+DenseSplit dense_simt_dq_split(const DenseShape& s) {
+    return dense_make_split((long long)s.slices * ((s.R + kBwdRows - 1) / kBwdRows), s.nk, kBwdRows, 4);
+}
 DenseSplit dense_simt_dkv_split(const DenseShape& s) {
-    const int bm = block_rows(s);
-    return dense_make_split((long long)s.slices * ((s.nk + bm - 1) / bm), s.R, bm, 4);
+    return dense_make_split((long long)s.slices * ((s.nk + kBwdRows - 1) / kBwdRows), s.R, kBwdRows, 4);
 }
 
-int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) { return launch_op<Fwd>(s, a, st); }
+int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    if (s.dtype == LLSA_DTYPE_BF16) return launch_fwd<__nv_bfloat16, 256, 32>(s, a, st);
+    if (fwd_rows(s) == 32) return launch_fwd<float, 256, 32>(s, a, st);
+    return s.d <= 64 ? launch_fwd<float, 64, 64>(s, a, st) : launch_fwd<float, 128, 64>(s, a, st);
+}
 int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
-    return launch_op<Bwd>(s, aq, ak, st);
+    return s.dtype == LLSA_DTYPE_BF16 ? launch_bwd<__nv_bfloat16>(s, aq, ak, st) : launch_bwd<float>(s, aq, ak, st);
 }
 
 }  // namespace llsa
