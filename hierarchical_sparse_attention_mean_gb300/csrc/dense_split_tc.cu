@@ -22,6 +22,7 @@
 // plane by plane, where TMA fetches them as ordinary bf16 tiles of 64 columns
 // (zeros behind d), the three planes of a tile in one copy.
 #include <algorithm>
+#include <type_traits>
 
 #include "dense_split.cuh"
 
@@ -71,14 +72,16 @@ __global__ void __launch_bounds__(256) dense_planes_kernel(const __grid_constant
 // at 64 columns and 64 keys at 128 columns. S has two buffers, so the next S runs
 // beside this one's softmax. Two threads share a row: each reads all of its scores
 // for the maximum, then takes half of the weights and half of the output.
-constexpr int kFwdWarps = 8, kFwdThreads = (kFwdWarps + 3) * 32;
+// 12 warps of 168 registers at launch = 64,512; at 256 columns the softmax warps take 216
+// of them and the others keep 72.
+constexpr int kFwdWarps = 8, kFwdThreads = (kFwdWarps + 4) * 32, kFwdRegsSoftmax = 216, kFwdRegsOther = 72;
 
-template <int D>
+template <int D, int PL>
 struct FwdCfg {
     static constexpr int BN = D == 64 ? 128 : 64, NC = D / 64;
     static constexpr int PQ = BT * D * 2, PK = BN * D * 2, RQ = BT * 128, RK = BN * 128;  // bytes of a plane, of 64 columns of it
-    static constexpr int KST = D == 64 ? 2 : 1;                           // K tiles
-    static constexpr int SMEM = 3 * (PQ + (KST + 1) * PK) + 1024;
+    static constexpr int KST = D * PL <= 256 ? 2 : 1;                     // K tiles
+    static constexpr int SMEM = PL * (PQ + (KST + 1) * PK) + 1024;
     static constexpr int TM_P = 2 * BN, TM_O = D == 64 ? 448 : 256;       // tensor memory: S at 0 and BN
 };
 
@@ -89,15 +92,16 @@ struct FwdBars {
     int abort_flag;
 };
 
-template <int D>
+template <int D, int PL>
 __global__ void __launch_bounds__(kFwdThreads, 1)
 dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const __grid_constant__ DenseArgs a) {
-    using C = FwdCfg<D>;
+    using C = FwdCfg<D, PL>;
+    using T = std::conditional_t<PL == 3, float, __nv_bfloat16>;
     constexpr int BN = C::BN;
     extern __shared__ __align__(1024) unsigned char sm[];
-    unsigned char *sQ = sm, *sK = sm + 3 * C::PQ, *sV = sK + C::KST * 3 * C::PK;
-    FwdBars* bar = reinterpret_cast<FwdBars*>(sV + 3 * C::PK);
+    unsigned char *sQ = sm, *sK = sm + PL * C::PQ, *sV = sK + C::KST * PL * C::PK;
+    FwdBars* bar = reinterpret_cast<FwdBars*>(sV + PL * C::PK);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
@@ -135,17 +139,21 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t tP = tbase + C::TM_P, tO = tbase + C::TM_O;
 
+    if constexpr (D == 256) {  // half an output row is 128 registers
+        if (warp >= kFwdWarps) regs_dec<kFwdRegsOther>();
+        else regs_inc<kFwdRegsSoftmax>();
+    }
     if (warp > kFwdWarps) {
         // ----------------------------------------------------------- copies
-        if (lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+        if (warp <= kFwdWarps + 2 && lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
             const bool keys = warp == kFwdWarps + 1;
-            if (keys) load_planes<BT, D>(sQ, &mq, r0, slice, smem_u32(&bar->q_full));
+            if (keys) load_planes<BT, D, PL>(sQ, &mq, r0, slice, smem_u32(&bar->q_full));
             int t = 0;
             for (; t < n; t++) {
                 const int st = keys ? t % C::KST : 0, use = keys ? t / C::KST : t;
                 const uint32_t full = smem_u32(keys ? &bar->k_full[st] : &bar->v_full);
                 if (use > 0 && !bar_wait(smem_u32(keys ? &bar->k_empty[st] : &bar->v_empty), (use - 1) & 1, abort_flag, a)) break;
-                load_planes<BN, D>(keys ? sK + st * 3 * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, full);
+                load_planes<BN, D, PL>(keys ? sK + st * PL * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, full);
             }
             // copies still in flight must land before the block exits
             if (keys) land(smem_u32(&bar->q_full), 0);
@@ -159,19 +167,19 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const uint32_t leader = elect_lane();
         constexpr uint32_t idS = idesc_bf16(BT, BN, 0, 0), idO = idesc_bf16(BT, D, 0, 1);
         const uint64_t dQ = desc_sw128(smem_u32(sQ), 16, 1024), dK = desc_sw128(smem_u32(sK), 16, 1024);
-        const uint64_t dV = desc_sw128(smem_u32(sV), 3 * C::RK, 1024);
+        const uint64_t dV = desc_sw128(smem_u32(sV), PL * C::RK, 1024);
         auto issue_S = [&](int t) {
             const int b = t & 1, st = t % C::KST;
             if (!warp_wait(smem_u32(&bar->k_full[st]), (t / C::KST) & 1, abort_flag, a)) return false;
             if (t > 1 && !warp_wait(smem_u32(&bar->s_free[b]), ((t >> 1) - 1) & 1, abort_flag, a)) return false;
             tc_fence_after();
-            const uint64_t dT = dK + (st * 3 * C::PK >> 4);
+            const uint64_t dT = dK + (st * PL * C::PK >> 4);
 #pragma unroll
-            for (int i = 0; i < 6; i++)
+            for (int i = 0; i < kTerms<PL>; i++)
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ks++)
-                    mma_ss(leader, tbase + b * BN, dQ + ((term_a(i) * C::RQ + (ks / 4) * 3 * C::RQ + (ks % 4) * 32) >> 4),
-                           dT + ((term_b(i) * C::RK + (ks / 4) * 3 * C::RK + (ks % 4) * 32) >> 4), idS, i > 0 || ks > 0);
+                    mma_ss(leader, tbase + b * BN, dQ + ((term_a<PL>(i) * C::RQ + (ks / 4) * PL * C::RQ + (ks % 4) * 32) >> 4),
+                           dT + ((term_b<PL>(i) * C::RK + (ks / 4) * PL * C::RK + (ks % 4) * 32) >> 4), idS, i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->s_full[b]));
             commit(leader, smem_u32(&bar->k_empty[st]));
             return true;
@@ -185,7 +193,7 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             // values behind the last valid key may be anything: their weights are 0, so they must be finite
             const int live = sp.lk - (j_first + t * BN);
             if (live < BN) {
-                for (int p = 0; p < 3 * C::NC; p++)
+                for (int p = 0; p < PL * C::NC; p++)
                     for (int x = live * 8 + lane; x < BN * 8; x += 32)
                         reinterpret_cast<uint4*>(sV + p * C::RK)[x] = make_uint4(0u, 0u, 0u, 0u);
                 fence_async_smem();
@@ -193,10 +201,10 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             }
             tc_fence_after();
 #pragma unroll
-            for (int i = 0; i < 6; i++)
+            for (int i = 0; i < kTerms<PL>; i++)
 #pragma unroll
                 for (int ks = 0; ks < BN / 16; ks++)
-                    mma_ts(leader, tO, tP + term_a(i) * (BN / 2) + ks * 8, dV + ((term_b(i) * C::RK + ks * 2048) >> 4), idO,
+                    mma_ts(leader, tO, tP + term_a<PL>(i) * (BN / 2) + ks * 8, dV + ((term_b<PL>(i) * C::RK + ks * 2048) >> 4), idO,
                            i > 0 || ks > 0);
             commit(leader, smem_u32(&bar->o_done));
             commit(leader, smem_u32(&bar->v_empty));
@@ -270,12 +278,15 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                         if (cut) e[k] = c + i + k < lim ? e[k] : 0.f;
                     }
                     sum += e[0] + e[1];
-                    split2(e[0], e[1], p1[i >> 1], p2[i >> 1], p3[i >> 1]);
+                    if constexpr (PL == 3) split2(e[0], e[1], p1[i >> 1], p2[i >> 1], p3[i >> 1]);
+                    else p1[i >> 1] = pack_bf16x2(e[0], e[1]);
                 }
                 l += sum;
                 tmem_st16(tP + lanes + (c >> 1), p1);
-                tmem_st16(tP + lanes + BN / 2 + (c >> 1), p2);
-                tmem_st16(tP + lanes + BN + (c >> 1), p3);
+                if constexpr (PL == 3) {
+                    tmem_st16(tP + lanes + BN / 2 + (c >> 1), p2);
+                    tmem_st16(tP + lanes + BN + (c >> 1), p3);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -295,8 +306,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
         const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
         if (r < a.R) {
-            store_rowpart<D / 2>(a.splits > 1 ? a.part + prow * a.d : static_cast<float*>(a.o_out) + row * a.d, acc, inv,
-                                 half * (D / 2), a.d);
+            if (a.splits > 1) store_rowpart<D / 2>(a.part + prow * a.d, acc, inv, half * (D / 2), a.d);
+            else store_rowpart<D / 2>(static_cast<T*>(a.o_out) + row * a.d, acc, inv, half * (D / 2), a.d);
             if (half == 0 && a.splits > 1)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
             else if (half == 0)
@@ -391,18 +402,18 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             // ----------------------------------------------------------- copies
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const int k = warp - kBwdWarps - 1;
-                load_planes<BT, 64>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, smem_u32(&bar->x_full[k]));
+                load_planes<BT, 64, 3>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, smem_u32(&bar->x_full[k]));
                 const uint32_t full = smem_u32(&bar->y_full[k]);
                 int n = 0;
                 for (Items<KEYS> it = start; !it.done(); it.next(a)) {
                     if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
                     if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
                         const long long row = (long long)slice * a.Rp + it.pos;
-                        load_planes<BT, 64>(sY + kTile, &my2, it.pos, slice, full, 2 * BT * 4);
+                        load_planes<BT, 64, 3>(sY + kTile, &my2, it.pos, slice, full, 2 * BT * 4);
                         bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
                         bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
                     } else {
-                        load_planes<BT, 64>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, full);
+                        load_planes<BT, 64, 3>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, full);
                     }
                     n++;
                 }
@@ -447,8 +458,8 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
                 for (int i = 0; i < 6; i++)
 #pragma unroll
                     for (int ks = 0; ks < 4; ks++)
-                        mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a(i) * kPlane + ks * 32) >> 4),
-                               dY + ((k * kTile + term_b(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
+                        mma_ss(leader, tbase + k * 128, dX + ((k * kTile + term_a<3>(i) * kPlane + ks * 32) >> 4),
+                               dY + ((k * kTile + term_b<3>(i) * kPlane + ks * 32) >> 4), idS, i > 0 || ks > 0);
                 commit(leader, smem_u32(k == 0 ? &bar->s_full : &bar->dp_full));
                 if (!KEYS && k == 1) commit(leader, smem_u32(&bar->y_empty[1]));
                 return true;
@@ -457,10 +468,10 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             auto issue_sum = [&](uint32_t acc, uint32_t t1, uint32_t t3, int k) {
 #pragma unroll
                 for (int i = 0; i < 6; i++) {
-                    const uint32_t op = term_a(i) == 2 ? t3 : t1 + term_a(i) * 8, step = term_a(i) == 2 ? 8 : 16;
+                    const uint32_t op = term_a<3>(i) == 2 ? t3 : t1 + term_a<3>(i) * 8, step = term_a<3>(i) == 2 ? 8 : 16;
 #pragma unroll
                     for (int ks = 0; ks < 8; ks++)
-                        mma_ts(leader, acc, op + ks * step, dM + ((k * kTile + term_b(i) * kPlane + ks * 2048) >> 4), idA,
+                        mma_ts(leader, acc, op + ks * step, dM + ((k * kTile + term_b<3>(i) * kPlane + ks * 2048) >> 4), idA,
                                i > 0 || ks > 0);
                 }
                 if (KEYS || k == 0) commit(leader, smem_u32(&bar->y_empty[k]));
@@ -621,7 +632,7 @@ int write_planes(const float* const* x, const long long* elems, int n, void* ws,
 }  // namespace
 
 static bool fits(const DenseShape& s) {
-    return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.R > 0 && s.nk > 0;
+    return (s.dtype == LLSA_DTYPE_F32 ? s.d <= 128 : s.d > 128) && s.R > 0 && s.nk > 0;
 }
 bool dense_split_bwd_supported(const DenseShape& s) { return fits(s); }
 // The CUDA-core kernel is the faster one where the keys are one of its tiles and the
@@ -639,36 +650,47 @@ DenseSplit dense_split_dkv_split(const DenseShape& s) {
 }
 
 size_t dense_split_planes(const DenseShape& s, bool backward) {
+    if (s.dtype == LLSA_DTYPE_BF16) return 0;  // read as they are
     const size_t q = up((size_t)s.slices * s.R * s.d * 6), k = up((size_t)s.slices * s.nk * s.d * 6);
     return backward ? 2 * q + 2 * k : q + 2 * k;
 }
 
-template <int D>
-static int launch_fwd(const DenseShape& s, const DenseArgs& a, __nv_bfloat16* const* p, cudaStream_t st) {
-    using C = FwdCfg<D>;
+template <int D, int PL>
+static int launch_fwd(const DenseShape& s, const DenseArgs& a, const void* const* p, cudaStream_t st) {
+    using C = FwdCfg<D, PL>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
     CUtensorMap mq, mk, mv;
-    LLSA_TRY(make_tmap_planes(&mq, p[0], s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mk, p[1], s.slices, s.nk, s.d, C::BN));
-    LLSA_TRY(make_tmap_planes(&mv, p[2], s.slices, s.nk, s.d, C::BN));
-    cudaFuncSetAttribute(dense_fwd_split_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    LLSA_TRY(make_tmap_planes(&mq, p[0], PL, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, p[1], PL, s.slices, s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_planes(&mv, p[2], PL, s.slices, s.nk, s.d, C::BN));
+    cudaFuncSetAttribute(dense_fwd_split_kernel<D, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
     if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("dense_fwd_split", st,
-                dense_fwd_split_kernel<D><<<(unsigned)pieces, kFwdThreads, C::SMEM, st>>>(mq, mk, mv, a));
+                dense_fwd_split_kernel<D, PL><<<(unsigned)pieces, kFwdThreads, C::SMEM, st>>>(mq, mk, mv, a));
     return LLSA_OK;
 }
 
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st) {
+    if (s.dtype == LLSA_DTYPE_BF16) {
+        const void* const x[3] = {a.q, a.k, a.v};
+        return launch_fwd<256, 1>(s, a, x, st);
+    }
     const float* x[3] = {static_cast<const float*>(a.q), static_cast<const float*>(a.k), static_cast<const float*>(a.v)};
     const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
     const long long elems[3] = {nq, nk, nk};
     __nv_bfloat16* p[3];
     LLSA_TRY(write_planes(x, elems, 3, ws, p, st));
-    return s.d <= 64 ? launch_fwd<64>(s, a, p, st) : launch_fwd<128>(s, a, p, st);
+    const void* const y[3] = {p[0], p[1], p[2]};
+    return s.d <= 64 ? launch_fwd<64, 3>(s, a, y, st) : launch_fwd<128, 3>(s, a, y, st);
 }
 
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st) {
+    if (s.dtype == LLSA_DTYPE_BF16) {
+        const void* const x[4] = {a.q, a.dout, a.k, a.v};
+        for (int i = 0; i < 4; i++) planes[i] = const_cast<void*>(x[i]);
+        return LLSA_OK;
+    }
     const float* x[4] = {static_cast<const float*>(a.q), static_cast<const float*>(a.dout), static_cast<const float*>(a.k),
                          static_cast<const float*>(a.v)};
     const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
@@ -683,10 +705,10 @@ int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const Dense
                            cudaStream_t st) {
     if (s.d > 64) return launch_dense_split_wide_bwd(s, aq, ak, planes, st);
     CUtensorMap mq, mg, mk, mv;
-    LLSA_TRY(make_tmap_planes(&mq, planes[0], s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mg, planes[1], s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mk, planes[2], s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mv, planes[3], s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mq, planes[0], 3, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mg, planes[1], 3, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, planes[2], 3, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mv, planes[3], 3, s.slices, s.nk, s.d, BT));
     static_assert(kBwdSmem <= 227 * 1024 && sizeof(BwdBars) <= 512, "shared memory budget");
     cudaFuncSetAttribute(dense_bwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;

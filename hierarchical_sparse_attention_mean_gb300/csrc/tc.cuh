@@ -421,7 +421,7 @@ int make_tmap_tokens(CUtensorMap* map, const void* base, const Shape& s);
 // multiple of 8.
 int make_tmap_rows(CUtensorMap* map, const void* base, long long slices, long long rows, int d, int box_rows);
 
-// Host: the same over three planes [3][slices][rows][d], a box of one slice's rows in all three.
-int make_tmap_planes(CUtensorMap* map, const void* base, long long slices, long long rows, int d, int box_rows);
+// Host: the same over `planes` planes [planes][slices][rows][d], a box of one slice's rows in all of them.
+int make_tmap_planes(CUtensorMap* map, const void* base, int planes, long long slices, long long rows, int d, int box_rows);
 
 }  // namespace llsa

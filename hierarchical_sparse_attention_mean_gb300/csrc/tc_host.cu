@@ -51,13 +51,13 @@ int make_tmap_rows(CUtensorMap* map, const void* base, long long slices, long lo
     return r == CUDA_SUCCESS ? LLSA_OK : LLSA_ERR_CUDA;
 }
 
-int make_tmap_planes(CUtensorMap* map, const void* base, long long slices, long long rows, int d, int box_rows) {
+int make_tmap_planes(CUtensorMap* map, const void* base, int planes, long long slices, long long rows, int d, int box_rows) {
     const PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
     if (!enc) return LLSA_ERR_CUDA;
     const cuuint64_t row = (cuuint64_t)d * 2;
-    cuuint64_t gdim[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slices, 3};
+    cuuint64_t gdim[4] = {(cuuint64_t)d, (cuuint64_t)rows, (cuuint64_t)slices, (cuuint64_t)planes};
     cuuint64_t gstride[3] = {row, row * rows, row * rows * slices};
-    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, 3};
+    cuuint32_t box[4] = {64, (cuuint32_t)box_rows, 1, (cuuint32_t)planes};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), gdim, gstride, box, estr,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

@@ -77,6 +77,8 @@ CASES = [
     (1, 2, 2, 150, 140, 96, False, None, None),
     (1, 2, 1, 70, 90, 136, True, None, None),             # behind 128 columns
     (1, 1, 1, 40, 65, 256, False, [33], [64]),
+    (2, 4, 2, 150, 270, 256, True, [150, 77], [201, 270]),
+    (1, 2, 1, 300, 333, 192, False, None, [260]),
     (1, 2, 2, 1000, 1100, 64, False, None, None),
     (1, 1, 1, 700, 900, 128, True, None, None),
 ]
@@ -143,7 +145,7 @@ def test_bad_lengths_are_clamped_and_reported(dtype):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
-@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 104)])
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("fp32", 64), ("fp32", 104)])
 def test_repeats_are_bit_equal(dtype, d):
     x = make(2, 8, 2, 333, 450, d, dtype, q_len=[333, 200], k_len=[450, 77])
     a, b = (run(x, True, 0.0, [333, 200], [450, 77], dtype) for _ in range(2))
@@ -205,7 +207,7 @@ def test_other_stream_and_captured_graph(dtype):
             assert torch.equal(got[n], want[n]), n
 
 
-@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("fp32", 64, 300), ("fp32", 128, 300)])
+@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("fp32", 64, 300), ("fp32", 128, 300), ("bf16", 256, 300)])
 def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d, nq):
     """With the copying warps switched off every consumer's first wait runs out: the
     status reads TIMEOUT once, the kernels end, and the next calls are right."""
@@ -363,6 +365,7 @@ SEVERAL = [
     (20, 16, 8, 70, 70, 40, True),
     (10, 16, 16, 150, 140, 128, True),
     (4, 40, 40, 260, 129, 96, False),
+    (4, 40, 20, 130, 200, 200, True),
 ]
 
 
