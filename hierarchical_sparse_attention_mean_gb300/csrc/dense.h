@@ -157,7 +157,7 @@ DenseSplit dense_tc_dkv_split(const DenseShape& s);
 int launch_dense_tc_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st);
 
-// dense_split_tc.cu: fp32 on the tensor cores, d <= 128 (planes: three bf16 planes
+// dense_split_tc.cu: fp32 up to 128 columns and bf16 behind 128 on the tensor cores (planes: fp32, three bf16 planes
 // of q, k, v, or of q, dout, k, v, at the start of the workspace).
 bool dense_split_fwd_supported(const DenseShape& s);
 bool dense_split_bwd_supported(const DenseShape& s);
@@ -166,7 +166,7 @@ DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st);
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st);
-// dense_split_wide_tc.cu: the backward pass at 64 < d <= 128.
+// dense_split_wide_tc.cu: the backward pass of fp32 behind 64 columns and of bf16.
 int launch_dense_split_wide_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,
                                 cudaStream_t st);
 int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,

@@ -1,6 +1,6 @@
 // dense_simt.cu -- dense attention on the CUDA cores: every type and head
-// dimension. What runs here: either type behind 128 columns, the fp32 forward of few
-// rows against a single tile of keys, and calls without rows or keys.
+// dimension. What runs here: fp32 behind 128 columns, the fp32 forward of few rows
+// against a single tile of keys, and calls without rows or keys.
 //
 // Forward: one pass over the keys with the running maximum and sum of the
 // softmax. Backward: probabilities recomputed from lse; dq by blocks of query

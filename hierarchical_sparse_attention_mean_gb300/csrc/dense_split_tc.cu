@@ -1,5 +1,8 @@
 // dense_split_tc.cu -- dense attention in fp32 on the tcgen05 tensor cores: forward up
-// to 128 columns, backward up to 64 (behind them: dense_split_wide_tc.cu).
+// to 128 columns, backward up to 64 (behind them: dense_split_wide_tc.cu). The
+// forward serves bf16 behind 128 columns too, as one plane that is read where it is
+// (4 heads x 2,048 tokens, d = 256 34 us, 500 TFLOP/s; 19 x 4,096 390 us, 837; there
+// the tensor cores' two products of 64 keys and the softmax between them alternate).
 //
 // Mathematics. Each fp32 operand x is written as x1 + x2 + x3 with x1 = bf16(x),
 // x2 = bf16(x - x1), x3 = bf16(x - x1 - x2): 8 bits and a sign each, so what is
@@ -635,11 +638,12 @@ static bool fits(const DenseShape& s) {
     return (s.dtype == LLSA_DTYPE_F32 ? s.d <= 128 : s.d > 128) && s.R > 0 && s.nk > 0;
 }
 bool dense_split_bwd_supported(const DenseShape& s) { return fits(s); }
-// The CUDA-core kernel is the faster one where the keys are one of its tiles and the
+// In fp32 the CUDA-core kernel is the faster one where the keys are one of its tiles and the
 // rows few (12 heads x 64 tokens 8.4 us against 9.5; 4 heads x 5 queries x 300 keys 26.6
-// against 13.8); backward it is not even there (28 against 14).
+// against 13.8); backward it is not even there (28 against 14), nor in bf16 (12 heads x 64
+// tokens, d = 256 19.2 against 7.8).
 bool dense_split_fwd_supported(const DenseShape& s) {
-    return fits(s) && (s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
+    return fits(s) && (s.dtype == LLSA_DTYPE_BF16 || s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
 }
 
 DenseSplit dense_split_fwd_split(const DenseShape& s) {
