@@ -23,7 +23,7 @@ import ctypes
 import functools
 import math
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, replace
 
 import torch
 
@@ -270,6 +270,13 @@ class RopeParams:
 
     def c(self, pos_batched: bool = False) -> _RopeParams:
         return self._c[1 if pos_batched else 0]
+
+    def in_fp32(self) -> "RopeParams":
+        """The same positions for fp32 tensors."""
+        got = self.__dict__.get("_fp32")
+        if got is None:
+            got = self.__dict__["_fp32"] = replace(self, dtype="fp32")
+        return got
 
     @staticmethod
     def like(q, k=None, **kw) -> "RopeParams":
@@ -787,6 +794,18 @@ def llsa_attention(q, k, v, block: int = 16, topk: int = 8, levels: int = 0, enr
     return _FN.apply(q, k, v, block, topk, levels, enrich_levels, scale, token_order, rope, pos)
 
 
+# dense_attention with rope= keeps bf16 operands in fp32 from the turn to the last
+# rounding up to this many columns or tokens: turned q and k in bf16 cost more there
+# than all other roundings (gradients against 64 bits, 2-norm: 256 tokens at d = 8
+# 0.0053 so, 0.0017 in fp32; four tokens at d = 64 up to 0.0058), while at 64 columns and
+# 64 tokens it is 0.004, and fp32 takes the GPU several times as long.
+_WIDE_COLUMNS, _WIDE_TOKENS = 32, 16
+
+
+def _wide(q, k):
+    return q.dtype == torch.bfloat16 and (q.shape[-1] <= _WIDE_COLUMNS or max(q.shape[-2], k.shape[-2]) <= _WIDE_TOKENS)
+
+
 def _dense_functions():
     from torch.autograd.function import once_differentiable
 
@@ -795,8 +814,14 @@ def _dense_functions():
 
         @staticmethod
         def forward(ctx, q, k, v, causal, scale, q_len, k_len, rope, pos):
+            ctx.dtype = dtype = q.dtype
             if rope is None:
                 q, k = q.contiguous(), k.contiguous()
+            elif _wide(q, k):
+                _check_rope(rope, q, k)
+                q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
+                rope = rope.in_fp32()
+                llsa_rope(rope, q, k, q, k, pos=pos)
             else:
                 q, k = _rotated(rope, q, k, pos)
             v = v.contiguous()
@@ -804,15 +829,17 @@ def _dense_functions():
             o, lse = dense_forward(p, q, k, v, q_len, k_len)
             ctx.p, ctx.rope = p, rope
             ctx.save_for_backward(q, k, v, o, lse, q_len, k_len, pos)
-            return o
+            return o.to(dtype)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, do):
             q, k, v, o, lse, q_len, k_len, pos = ctx.saved_tensors
-            dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, do.contiguous(), q_len, k_len)
+            dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, do.to(o.dtype).contiguous(), q_len, k_len)
             if ctx.rope is not None:
                 llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
+            if dq.dtype != ctx.dtype:
+                dq, dk, dv = dq.to(ctx.dtype), dk.to(ctx.dtype), dv.to(ctx.dtype)
             return dq, dk, dv, None, None, None, None, None, None
 
     class RotaryFunction(torch.autograd.Function):
@@ -849,7 +876,8 @@ def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=Non
     """Autograd entry point of dense attention: q [batch, heads, nq, d] over k, v
     [batch, kv_heads, nk, d]. q_len, k_len: int32 [batch] valid tokens of a
     padded batch. rope: rotary positions for q and k of the same tokens; the turned
-    q and k are rounded to their type before the scores, as rotary() returns them.
+    q and k are rounded to their type before the scores, as rotary() returns them,
+    but for bf16 of few columns or tokens, which stays in fp32 until the end.
     A backward pass that a CUDA graph captures wants leaves made inside the capture
     (x.detach().requires_grad_()), as every autograd function does."""
     return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)

@@ -469,3 +469,30 @@ def test_captured_autograd_step():
         for a, b in zip(got, w):
             assert torch.equal(a, b)
     assert torch.equal(alive, want[0][0])
+
+
+@pytest.mark.parametrize("b,h,kv,n,d", [(2, 2, 1, 2, 64), (1, 4, 2, 3, 128), (3, 3, 3, 16, 72), (1, 4, 2, 300, 8), (2, 2, 2, 129, 32)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_rotary_attention_of_few_columns_or_tokens(b, h, kv, n, d, causal):
+    """bf16 inputs with rope=: fp32 until the last rounding, against autograd of the
+    formulas in 64 bits on what the fp32 turn gives."""
+    x = make(b, h, kv, n, n, d, "bf16", seed=31)
+    leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v")]
+    rope = llsa.RopeParams.like(leaves[0], leaves[1])
+    o = llsa.dense_attention(*leaves, causal=causal, rope=rope)
+    got = dict(zip(("o", "dq", "dk", "dv"), (o, *torch.autograd.grad(o, leaves, x["dout"].cuda()))))
+    assert all(t.dtype == torch.bfloat16 for t in got.values())
+    turned = llsa.rotary(leaves[0].detach().float(), leaves[1].detach().float(), rope.in_fp32())
+    y = {m: t.float() for m, t in x.items()}
+    y["q"], y["k"] = (t.cpu() for t in turned)
+    want = ref.attention(**y, causal=causal, dtype=torch.float32)
+    u = ref.half_step(torch.bfloat16)
+    for m in ("o", "dv"):
+        value, bound = want[m]
+        ref.check(m, got[m], (value, bound + u * (value.abs() + bound)))
+    pos = torch.arange(n)[:, None]
+    for m in ("dq", "dk"):
+        value, bound = want[m]
+        back, turn = ref.rotary(value, pos[None], inverse=True)
+        bound = _pair_sum(bound, 1) * (1 + 2.0 ** -24) + turn + 2.0 ** -24 * back.abs()  # the turn's own rounding, in fp32
+        ref.check(m, got[m], (back, bound + u * (back.abs() + bound)))
