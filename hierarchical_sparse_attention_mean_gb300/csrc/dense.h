@@ -136,8 +136,7 @@ inline DenseSplit dense_make_split(long long blocks, int extent, int tile, int l
 }
 
 // dense_simt.cu: CUDA-core kernels (any type and head dimension).
-DenseSplit dense_simt_fwd_split(const DenseShape& s);
-DenseSplit dense_simt_dq_split(const DenseShape& s);
+DenseSplit dense_simt_fwd_split(const DenseShape& s);  // dq: the same
 DenseSplit dense_simt_dkv_split(const DenseShape& s);
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st);
@@ -149,6 +148,10 @@ DenseSplit dense_few_split(const DenseShape& s);  // of the keys, in both direct
 int launch_dense_few(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 int launch_dense_few_bwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
 
+// dense_keys.cu: forward of fp32 against a handful of keys.
+bool dense_keys_supported(const DenseShape& s);
+int launch_dense_keys(const DenseShape& s, const DenseArgs& a, cudaStream_t st);
+
 // dense_fwd_tc.cu, dense_bwd_tc.cu: tensor-core kernels (bf16, d <= 128).
 bool dense_tc_supported(const DenseShape& s);
 DenseSplit dense_tc_fwd_split(const DenseShape& s);
@@ -159,8 +162,7 @@ int launch_dense_tc_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArg
 
 // dense_split_tc.cu: fp32 up to 128 columns and bf16 behind 128 on the tensor cores (planes: fp32, three bf16 planes
 // of q, k, v, or of q, dout, k, v, at the start of the workspace).
-bool dense_split_fwd_supported(const DenseShape& s);
-bool dense_split_bwd_supported(const DenseShape& s);
+bool dense_split_supported(const DenseShape& s);
 DenseSplit dense_split_fwd_split(const DenseShape& s);  // dq: the same
 DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes

@@ -224,24 +224,26 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
 }
 
 // Which kernels take a call.
-enum class Path { kFew, kTc, kSplit, kSimt };
+enum class Path { kFew, kKeys, kTc, kSplit, kSimt };
 
 Path fwd_path(const DenseShape& s) {
-    return dense_few_supported(s)         ? Path::kFew
-           : dense_tc_supported(s)        ? Path::kTc
-           : dense_split_fwd_supported(s) ? Path::kSplit
-                                          : Path::kSimt;
+    return dense_few_supported(s)     ? Path::kFew
+           : dense_keys_supported(s)  ? Path::kKeys
+           : dense_tc_supported(s)    ? Path::kTc
+           : dense_split_supported(s) ? Path::kSplit
+                                      : Path::kSimt;
 }
 Path bwd_path(const DenseShape& s) {
-    return dense_few_bwd_supported(s)     ? Path::kFew
-           : dense_tc_supported(s)        ? Path::kTc
-           : dense_split_bwd_supported(s) ? Path::kSplit
-                                          : Path::kSimt;
+    return dense_few_bwd_supported(s) ? Path::kFew
+           : dense_tc_supported(s)    ? Path::kTc
+           : dense_split_supported(s) ? Path::kSplit
+                                      : Path::kSimt;
 }
 
 DenseSplit fwd_split(const DenseShape& s) {
     switch (fwd_path(s)) {
         case Path::kFew: return dense_few_split(s);
+        case Path::kKeys: return {1, s.nk};
         case Path::kTc: return dense_tc_fwd_split(s);
         case Path::kSplit: return dense_split_fwd_split(s);
         default: return dense_simt_fwd_split(s);
@@ -252,7 +254,7 @@ DenseSplit dq_split(const DenseShape& s) {
         case Path::kFew: return dense_few_split(s);
         case Path::kTc: return dense_tc_dq_split(s);
         case Path::kSplit: return dense_split_fwd_split(s);
-        default: return dense_simt_dq_split(s);
+        default: return dense_simt_fwd_split(s);
     }
 }
 DenseSplit dkv_split(const DenseShape& s) {
@@ -295,6 +297,7 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + (path == Path::kSplit ? dense_split_planes(s, false) : 0));
     switch (path) {
         case Path::kFew: LLSA_TRY(launch_dense_few(s, a, st)); break;
+        case Path::kKeys: LLSA_TRY(launch_dense_keys(s, a, st)); break;
         case Path::kTc: LLSA_TRY(launch_dense_tc_fwd(s, a, st)); break;
         case Path::kSplit: LLSA_TRY(launch_dense_split_fwd(s, a, ws, st)); break;
         default: LLSA_TRY(launch_dense_simt_fwd(s, a, st));

@@ -1,6 +1,6 @@
 // dense_simt.cu -- dense attention on the CUDA cores: every type and head
-// dimension. What runs here: fp32 behind 128 columns, the fp32 forward of few rows
-// against a single tile of keys, and calls without rows or keys.
+// dimension. What runs here: fp32 behind 128 columns, and calls of either type without
+// rows or keys, for which it writes what is left.
 //
 // Forward: one pass over the keys with the running maximum and sum of the
 // softmax. Backward: probabilities recomputed from lse; dq by blocks of query
@@ -68,8 +68,8 @@ __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group
 
 // The forward keeps two buffers for the tiles of the streamed side where the type
 // needs no conversion on the way: the next tile comes in during this one's work (4
-// heads x 200 queries x 8,000 keys 92 -> 73 us). The backward kernels, with four
-// operands, have no room for it at 128 columns.
+// heads x 200 queries x 8,000 keys of 64 columns 92 -> 73 us). The backward kernels have
+// four operands, and two buffers would leave one block per SM.
 template <typename T, bool FWD>
 constexpr int buffers() {
     return sizeof(T) == 4 && FWD ? 2 : 1;
@@ -440,14 +440,11 @@ dense_bwd_simt_kernel(const __grid_constant__ DenseArgs aq, const __grid_constan
         rows_side<T, DP, BM>(aq, piece - key_pieces);
 }
 
-// Rows of a block. Tiles of 256 columns and 32 rows serve what has no tile of its
-// own: only the fp32 forward against a few keys comes here with fewer columns.
-int fwd_rows(const DenseShape& s) { return s.dtype == LLSA_DTYPE_F32 && s.d <= 128 && s.nk > 0 ? 64 : 32; }
-constexpr int kBwdRows = 32;
+constexpr int kColumns = 256, kRows = 32;  // of a tile
 
-template <typename T, int DP, int BM>
+template <typename T>
 int launch_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    constexpr int tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * buffers<T, true>()) * tile + p;
+    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * buffers<T, true>()) * tile + p;
     static_assert(smem <= 227 * 1024, "shared memory budget");
     const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
     if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
@@ -459,7 +456,7 @@ int launch_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
 
 template <typename T>
 int launch_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
-    constexpr int BM = kBwdRows, DP = 256, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
+    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
     constexpr int smem = (2 + 2 * buffers<T, false>()) * tile + 2 * p;
     static_assert(smem <= 227 * 1024, "shared memory budget");
     const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
@@ -473,21 +470,15 @@ int launch_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cu
 
 }  // namespace
 
-DenseSplit dense_simt_fwd_split(const DenseShape& s) {
-    const int bm = fwd_rows(s);
-    return dense_make_split((long long)s.slices * ((s.R + bm - 1) / bm), s.nk, bm, 4);
-}
-DenseSplit dense_simt_dq_split(const DenseShape& s) {
-    return dense_make_split((long long)s.slices * ((s.R + kBwdRows - 1) / kBwdRows), s.nk, kBwdRows, 4);
+DenseSplit dense_simt_fwd_split(const DenseShape& s) {  // dq: the same
+    return dense_make_split((long long)s.slices * ((s.R + kRows - 1) / kRows), s.nk, kRows, 4);
 }
 DenseSplit dense_simt_dkv_split(const DenseShape& s) {
-    return dense_make_split((long long)s.slices * ((s.nk + kBwdRows - 1) / kBwdRows), s.R, kBwdRows, 4);
+    return dense_make_split((long long)s.slices * ((s.nk + kRows - 1) / kRows), s.R, kRows, 4);
 }
 
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    if (s.dtype == LLSA_DTYPE_BF16) return launch_fwd<__nv_bfloat16, 256, 32>(s, a, st);
-    if (fwd_rows(s) == 32) return launch_fwd<float, 256, 32>(s, a, st);
-    return s.d <= 64 ? launch_fwd<float, 64, 64>(s, a, st) : launch_fwd<float, 128, 64>(s, a, st);
+    return s.dtype == LLSA_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(s, a, st) : launch_fwd<float>(s, a, st);
 }
 int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
     return s.dtype == LLSA_DTYPE_BF16 ? launch_bwd<__nv_bfloat16>(s, aq, ak, st) : launch_bwd<float>(s, aq, ak, st);

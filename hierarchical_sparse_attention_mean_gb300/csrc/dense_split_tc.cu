@@ -634,16 +634,8 @@ int write_planes(const float* const* x, const long long* elems, int n, void* ws,
 
 }  // namespace
 
-static bool fits(const DenseShape& s) {
+bool dense_split_supported(const DenseShape& s) {
     return (s.dtype == LLSA_DTYPE_F32 ? s.d <= 128 : s.d > 128) && s.R > 0 && s.nk > 0;
-}
-bool dense_split_bwd_supported(const DenseShape& s) { return fits(s); }
-// In fp32 the CUDA-core kernel is the faster one where the keys are one of its tiles and the
-// rows few (12 heads x 64 tokens 8.4 us against 9.5; 4 heads x 5 queries x 300 keys 26.6
-// against 13.8); backward it is not even there (28 against 14), nor in bf16 (12 heads x 64
-// tokens, d = 256 19.2 against 7.8).
-bool dense_split_fwd_supported(const DenseShape& s) {
-    return fits(s) && (s.dtype == LLSA_DTYPE_BF16 || s.nk > 64 || (long long)s.R * s.nk >= (1 << 14));
 }
 
 DenseSplit dense_split_fwd_split(const DenseShape& s) {

@@ -496,3 +496,16 @@ def test_rotary_attention_of_few_columns_or_tokens(b, h, kv, n, d, causal):
         back, turn = ref.rotary(value, pos[None], inverse=True)
         bound = _pair_sum(bound, 1) * (1 + 2.0 ** -24) + turn + 2.0 ** -24 * back.abs()  # the turn's own rounding, in fp32
         ref.check(m, got[m], (back, bound + u * (back.abs() + bound)))
+
+
+@pytest.mark.parametrize("d", [8, 32, 40, 64, 72, 128, 136, 256])
+@pytest.mark.parametrize("nq,nk,causal,k_len", [(300, 4, False, None), (777, 7, True, [7, 0]), (9, 20, True, None), (130, 33, False, [33, 2]),
+                                                (300, 41, False, [40, 41])])
+def test_fp32_few_keys(nq, nk, causal, k_len, d):
+    """Many rows against a handful of keys, on both sides of where the kernels change;
+    with 7 keys most rows of the causal order see none."""
+    x = make(2, 4, 2, nq, nk, d, "fp32", None, k_len, seed=41)
+    want = ref.attention(**x, causal=causal, k_len=k_len, dtype=torch.float32)
+    got = run(x, causal, 0.0, None, k_len, "fp32")
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        ref.check(n, got[n], want[n])
