@@ -637,7 +637,7 @@ int launch(const DenseShape& s, DenseArgs aq, DenseArgs ak, cudaStream_t st) {
     // piece about three items' time more (152 slices with one item per piece), and
     // a second launch that of seven.
     const long long ck = 16 * ((std::min(ak.chunk, s.R) + BT - 1) / BT + 3), cq = 15 * ((std::min(aq.chunk, s.nk) + BT - 1) / BT + 3);
-    const int grid = (int)std::min<long long>(pq + pk, sm_count());
+    const int grid = resident_blocks(pq + pk);
     const int share = share_blocks(pk, ck, pq, cq, 7 * 16, grid, s.causal);
     LLSA_LAUNCH("dense_bwd_tc", st,
                 dense_bwd_tc_kernel<D><<<grid, kThreads, smem, st>>>(mq, mg, mk, mv, zq, zk, zv, aq, ak, share));

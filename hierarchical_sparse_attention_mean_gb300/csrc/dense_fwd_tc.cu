@@ -191,7 +191,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                     if (keys)
 #pragma unroll
                         for (int w = 0; w < 2; w++) {
-                            if (!ok || pc.n[w] == 0) continue;
+                            if (!ok || pc.n[w] <= 0) continue;  // no keys, or half a piece: no query tile
                             const int q = v[w] % C::NQ, use = v[w] / C::NQ;
                             if (use > 0) ok = bar_wait(smem_u32(&bar->q_free[w][q]), (use - 1) & 1, abort_flag, a);
                             if (!ok) continue;
@@ -516,13 +516,14 @@ int launch(const DenseShape& s, DenseArgs a, cudaStream_t st) {
     if (pieces > kDenseMaxPieces / 2) return LLSA_ERR_UNSUPPORTED;
     // A last round that leaves half of the SMs idle is dealt out in halves: a row
     // tile alone takes about 3/4 of the time of two.
-    const long long rest = pieces % kDenseSms;
-    a.whole = (int)(2 * rest <= kDenseSms && a.splits == 1 ? pieces - rest : pieces);
+    const int sms = sm_count();
+    const long long rest = pieces % sms;
+    a.whole = (int)(2 * rest <= sms && a.splits == 1 ? pieces - rest : pieces);
     pieces += pieces - a.whole;
     a.pieces = (int)pieces;
     // resident blocks against one per piece: 12 heads x 4,096 tokens 61.0 us and 63.3, 4 x 12 heads x 4,096
     // queries x 333 keys 33.7 and 43.1; at 128 columns 88.0 and 88.7, 50.6 and 58.0
-    const int grid = (int)std::min<long long>(pieces, sm_count());
+    const int grid = resident_blocks(pieces);
     LLSA_LAUNCH("dense_fwd_tc", st, dense_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(mq, mk, mv, mo, a));
     return LLSA_OK;
 }

@@ -130,6 +130,12 @@ __device__ __forceinline__ int dealt_pieces(const DenseArgs& a, int block, int b
     return full + (dealt(a, full, block, blocks) < a.pieces ? 1 : 0);
 }
 
+// Host: resident blocks of a call, one per SM.
+inline int resident_blocks(long long pieces) {
+    const int most = test_flags() & LLSA_TEST_FEW_BLOCKS ? 3 : sm_count();
+    return (int)(pieces < most ? pieces : most);
+}
+
 // The pieces of a resident block, worked out by one copying thread (divisions and
 // loads of the lengths: some 1,500 clocks) ahead of the roles that read them.
 constexpr int kPieceSlots = 4;

@@ -227,12 +227,17 @@ int llsa_bwd(const llsa_params *p, const void *q, const void *k, const void *v, 
  *                              runs when its groups hold at least 4.5 query
  *                              blocks on average); results agree either way
  *                              within rounding.
+ *   LLSA_TEST_FEW_BLOCKS       the dense tensor-core kernels whose blocks stay
+ *                              resident run on three blocks instead of one per
+ *                              SM, so that every block takes pieces of each
+ *                              kind in turn; results stay bit for bit.
  * Process-wide; applies to calls made after it; (0, 0) is the default state.
  * Host-side only, no device work. Unknown flag bits, or both FORCE bits:
  * LLSA_ERR_INVALID_ARG. */
 #define LLSA_TEST_NO_COPIES 1
 #define LLSA_TEST_FORCE_GROUPED 2
 #define LLSA_TEST_FORCE_PER_BLOCK 4
+#define LLSA_TEST_FEW_BLOCKS 16
 int llsa_test_set_wait_limit(int polls, int flags);
 
 /* Sparse index transpose for callers that cannot allocate device memory.

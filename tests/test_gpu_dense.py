@@ -509,3 +509,27 @@ def test_fp32_few_keys(nq, nk, causal, k_len, d):
     got = run(x, causal, 0.0, None, k_len, "fp32")
     for n in ("o", "lse", "dq", "dk", "dv"):
         ref.check(n, got[n], want[n])
+
+
+@pytest.mark.parametrize("b,h,kv,nq,nk,d,causal,ql,kl", [
+    (2, 6, 6, 700, 333, 64, False, None, None),            # 36 pieces, each of them in halves
+    (2, 6, 3, 300, 270, 64, True, None, None),
+    (3, 4, 2, 640, 200, 64, False, [640, 0, 129], [200, 77, 0]),
+    (2, 6, 6, 700, 333, 128, False, None, None),
+    (3, 4, 2, 330, 200, 128, True, [330, 129, 1], [200, 77, 0]),
+    (1, 8, 8, 256, 140, 96, False, None, [131]),
+])
+def test_blocks_take_several_halves(b, h, kv, nq, nk, d, causal, ql, kl):
+    """On three blocks each block takes many halved pieces, whatever the device's number of
+    SMs; what a piece gives does not depend on the block that takes it."""
+    x = make(b, h, kv, nq, nk, d, "bf16", ql, kl, seed=51)
+    want = run(x, causal, 0.0, ql, kl)
+    ref_want = ref.attention(**x, causal=causal, q_len=ql, k_len=kl, dtype=torch.bfloat16)
+    llsa.test_set_wait_limit(0, llsa.LLSA_TEST_FEW_BLOCKS)
+    try:
+        got = run(x, causal, 0.0, ql, kl)
+    finally:
+        llsa.test_set_wait_limit(0, 0)
+    for n in ("o", "lse", "dq", "dk", "dv"):
+        assert torch.equal(got[n], want[n]), n
+        ref.check(n, got[n], ref_want[n])
