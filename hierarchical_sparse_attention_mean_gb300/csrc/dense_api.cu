@@ -195,7 +195,8 @@ int derive_dense(const llsa_dense_params* p, DenseShape* s) {
     s->slices = (int)slices;
     s->R = (int)R;
     s->Rp = (s->R + kDenseRowPad - 1) / kDenseRowPad * kDenseRowPad;
-    if (slices * std::max<long long>(s->Rp, s->nk) * s->d > (1LL << 40)) return LLSA_ERR_UNSUPPORTED;
+    // up to 2^68: more than 64 bits hold
+    if ((double)slices * std::max(s->Rp, s->nk) * s->d > (double)(1LL << 40)) return LLSA_ERR_UNSUPPORTED;
     return LLSA_OK;
 }
 

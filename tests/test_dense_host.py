@@ -182,3 +182,17 @@ def test_parameters_copy_and_pickle(lib):
 def test_rope_sizes_refused(lib, kw):
     p = llsa.RopeParams(**{**dict(batch=2, heads=4, n=100, d=64, kv_heads=2), **kw})
     assert rope(lib, p) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("kw", [
+    dict(batch=1 << 28, heads=1, nk=1 << 30),                # 2^64 elements of k
+    dict(batch=1 << 30, heads=1, nk=1 << 30, d=16),          # again
+    dict(batch=1 << 28, heads=1, nq=1 << 30),                # of q
+    dict(batch=1 << 29, heads=1, nk=1 << 29, d=256),
+    dict(batch=3 << 20, heads=10, nk=(1 << 30) - 5, d=248),
+])
+def test_dense_sizes_behind_64_bits_refused(lib, kw):
+    p = llsa.DenseParams(**{**dict(batch=2, heads=4, nq=100, nk=100, d=64), **kw})
+    assert fwd(lib, p) == UNSUPPORTED and bwd(lib, p) == UNSUPPORTED
+    assert llsa.dense_workspace_bytes(p, llsa.OP_DENSE_FWD) == 0
+    assert llsa.dense_workspace_bytes(p, llsa.OP_DENSE_BWD) == 0
