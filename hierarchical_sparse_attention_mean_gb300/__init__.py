@@ -731,14 +731,20 @@ def _check_rope(p: RopeParams, q, k, name="rope"):
                          + ("" if k is None else f" and k {tuple(k.shape)}"))
 
 
+def _contiguous(t):
+    """t, or a copy where it is not contiguous or does not start on 16 bytes (a view into a flat buffer)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone(memory_format=torch.contiguous_format)
+
+
 def _rope_view(t):
-    """t, or a contiguous copy where its strides are none that llsa_rope takes."""
-    if t.is_contiguous() and t.data_ptr() % 16 == 0:
-        return t
+    """t, or a contiguous copy where its strides or its first byte are none that llsa_rope takes."""
+    if t.is_contiguous():
+        return _contiguous(t)
     unit = 16 // t.element_size()
     ok = any(t.stride()[:3]) and t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(
         t.stride(i) % unit == 0 for i in range(3) if t.shape[i] > 1)
-    return t if ok else t.contiguous()
+    return t if ok else _contiguous(t)
 
 
 def _autograd_function():
@@ -750,10 +756,10 @@ def _autograd_function():
         def forward(ctx, q, k, v, block, topk, levels, enrich_levels, scale, token_order, rope, pos):
             ctx.rope = rope
             if rope is None:
-                q, k = q.contiguous(), k.contiguous()
+                q, k = _contiguous(q), _contiguous(k)
             else:
                 q, k = _rotated(rope, q, k, pos)
-            v = v.contiguous()
+            v = _contiguous(v)
             p = Params.like(q, block=block, topk=topk, levels=levels, enrich_levels=enrich_levels, scale=scale,
                             token_order=token_order)
             b = forward(p, q, k, v)
@@ -764,7 +770,7 @@ def _autograd_function():
         @staticmethod
         def backward(ctx, do):
             q, k, v, *pos = ctx.saved_tensors
-            dq, dk, dv = backward(ctx.p, q, k, v, do.contiguous(), ctx.b)
+            dq, dk, dv = backward(ctx.p, q, k, v, _contiguous(do), ctx.b)
             if ctx.rope is not None:
                 llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos[0] if pos else None, inverse=True)
             return dq, dk, dv, None, None, None, None, None, None, None, None
@@ -818,7 +824,7 @@ def _dense_functions():
         def forward(ctx, q, k, v, causal, scale, q_len, k_len, rope, pos):
             ctx.dtype = dtype = q.dtype
             if rope is None:
-                q, k = q.contiguous(), k.contiguous()
+                q, k = _contiguous(q), _contiguous(k)
             elif _wide(q, k):
                 _check_rope(rope, q, k)
                 q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
@@ -826,7 +832,7 @@ def _dense_functions():
                 llsa_rope(rope, q, k, q, k, pos=pos)
             else:
                 q, k = _rotated(rope, q, k, pos)
-            v = v.contiguous()
+            v = _contiguous(v)
             p = DenseParams.like(q, k, causal=causal, scale=scale)
             o, lse = dense_forward(p, q, k, v, q_len, k_len)
             ctx.p, ctx.rope = p, rope
@@ -837,7 +843,7 @@ def _dense_functions():
         @once_differentiable
         def backward(ctx, do):
             q, k, v, o, lse, q_len, k_len, pos = ctx.saved_tensors
-            dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, do.to(o.dtype).contiguous(), q_len, k_len)
+            dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, _contiguous(do.to(o.dtype)), q_len, k_len)
             if ctx.rope is not None:
                 llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
             if dq.dtype != ctx.dtype:

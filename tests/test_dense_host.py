@@ -196,3 +196,18 @@ def test_dense_sizes_behind_64_bits_refused(lib, kw):
     assert fwd(lib, p) == UNSUPPORTED and bwd(lib, p) == UNSUPPORTED
     assert llsa.dense_workspace_bytes(p, llsa.OP_DENSE_FWD) == 0
     assert llsa.dense_workspace_bytes(p, llsa.OP_DENSE_BWD) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_off_16_bytes_are_copied(dtype):
+    """A contiguous view that starts inside a vector is no input of the kernels: a copy is."""
+    flat = torch.arange(1 + 2 * 3 * 5 * 8, dtype=dtype)
+    for take in (llsa._contiguous, llsa._rope_view):
+        view = flat[1:].view(2, 3, 5, 8)
+        assert view.is_contiguous() and view.data_ptr() % 16 != 0
+        got = take(view)
+        assert got.data_ptr() % 16 == 0 and got.is_contiguous() and torch.equal(got, view)
+        whole = flat[:-1].view(2, 3, 5, 8)
+        assert take(whole) is whole
+        turned = take(flat[1:].view(2, 5, 3, 8).transpose(1, 2))
+        assert turned.data_ptr() % 16 == 0 and torch.equal(turned, flat[1:].view(2, 5, 3, 8).transpose(1, 2))

@@ -533,3 +533,43 @@ def test_blocks_take_several_halves(b, h, kv, nq, nk, d, causal, ql, kl):
     for n in ("o", "lse", "dq", "dk", "dv"):
         assert torch.equal(got[n], want[n]), n
         ref.check(n, got[n], ref_want[n])
+
+
+def off_16_bytes(t):
+    """The same values in a contiguous view that starts one element into its storage."""
+    flat = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+    view = flat[1:].view(t.shape)
+    view.copy_(t)
+    assert view.is_contiguous() and view.data_ptr() % 16 != 0
+    return view
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_inputs_and_gradients_off_16_bytes(dtype):
+    """q, k, v and the gradient that comes in may be views into flat buffers: dense and
+    sparse attention and rotary positions give what aligned copies give."""
+    n = 256 if dtype == "fp32" else 4096
+    x = {m: t.cuda() for m, t in make(1, 2, 2, n, n, 64, dtype, seed=61).items()}
+    y = {m: off_16_bytes(t) for m, t in x.items()}
+    rope = llsa.RopeParams.like(x["q"], x["k"])
+    calls = [lambda q, k, v: llsa.dense_attention(q, k, v), lambda q, k, v: llsa.dense_attention(q, k, v, rope=rope),
+             lambda q, k, v: llsa.llsa_attention(q, k, v, topk=4), lambda q, k, v: llsa.llsa_attention(q, k, v, topk=4, rope=rope),
+             lambda q, k, v: torch.cat(llsa.rotary(q, k, rope)) + 0 * v]
+    for call in calls:
+        out = []
+        for z in (x, y):
+            leaves = [z[m].detach().requires_grad_() for m in ("q", "k", "v")]
+            o = call(*leaves)
+            g = z["dout"] if o.shape == z["dout"].shape else torch.cat([z["dout"]] * 2)
+            out.append((o.detach(), *torch.autograd.grad(o, leaves, g)))
+        for a, b in zip(*out):
+            assert torch.equal(a, b)
+    # the gradient's place is the engine's: a slice of a concatenation that starts with an odd number of values
+    leaves = [x[m].detach().requires_grad_() for m in ("q", "k", "v")]
+    lead = torch.zeros(3, dtype=x["q"].dtype, device="cuda", requires_grad=True)
+    w = off_16_bytes(torch.cat([lead.detach(), x["dout"].flatten()]))
+    o = llsa.dense_attention(*leaves)
+    got = torch.autograd.grad(torch.cat([lead, o.flatten()]), leaves, w)
+    want = torch.autograd.grad(llsa.dense_attention(*leaves), leaves, x["dout"])
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
