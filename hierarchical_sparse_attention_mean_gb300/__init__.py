@@ -795,23 +795,31 @@ def llsa_attention(q, k, v, block: int = 16, topk: int = 8, levels: int = 0, enr
     """Autograd entry point: o = LLSA(q, k, v). token_order "raster": q, k, v
     (and o, the gradients) are in the raster order of a square image, reordered
     inside the kernels. rope: rotary positions for q and k (with `pos`, or the
-    positions that the parameters imply; its token_order is its own)."""
+    positions that the parameters imply; its token_order is its own); the turned q and k
+    are rounded to their type, and so are their gradients before they are turned back."""
     global _FN
     if _FN is None:
         _FN = _autograd_function()
     return _FN.apply(q, k, v, block, topk, levels, enrich_levels, scale, token_order, rope, pos)
 
 
-# dense_attention with rope= keeps bf16 operands in fp32 from the turn to the last
-# rounding up to this many columns or tokens: turned q and k in bf16 cost more there
-# than all other roundings (gradients against 64 bits, 2-norm: 256 tokens at d = 8
-# 0.0053 so, 0.0017 in fp32; four tokens at d = 64 up to 0.0058), while at 64 columns and
-# 64 tokens it is 0.004, and fp32 takes the GPU several times as long.
-_WIDE_COLUMNS, _WIDE_TOKENS = 32, 16
+# Where dense_attention with rope= keeps bf16 operands in fp32 from the turn to the last
+# rounding. Turned q and k rounded to bf16 are the largest error of a step's gradients
+# (against 64 bits, 2-norm, 12 heads; in fp32 all are 0.0017): 0.0042 to 0.0044 at 40 columns and
+# more whatever the length, 0.0052 to 0.0061 at 8 from 256 to 4,096 tokens, and up to 0.0058
+# with four tokens of 64 columns, whose gradients cancel. So those two are always wide.
+# Between them it is 0.0047 to 0.0050 at 16 columns and 0.0043 to 0.0047 at 24 and 32, and fp32 takes the
+# GPU 5 times as long (12 heads x 4,096 tokens, d = 32 233 us and 1,180): wide where that
+# hides behind the call itself, some 300 us of the host (12 heads x 512 tokens 41 us and 107).
+_WIDE_TOKENS, _WIDE_ALWAYS, _WIDE_COLUMNS, _WIDE_PAIRS = 16, 8, 32, 1 << 22
 
 
 def _wide(q, k):
-    return q.dtype == torch.bfloat16 and (q.shape[-1] <= _WIDE_COLUMNS or max(q.shape[-2], k.shape[-2]) <= _WIDE_TOKENS)
+    if q.dtype != torch.bfloat16:
+        return False
+    d, nk = q.shape[-1], k.shape[-2]
+    return (d <= _WIDE_ALWAYS or max(q.shape[-2], nk) <= _WIDE_TOKENS
+            or (d <= _WIDE_COLUMNS and q.numel() * nk <= _WIDE_PAIRS * d))  # pairs of a query and a key
 
 
 def _dense_functions():
@@ -885,7 +893,10 @@ def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=Non
     [batch, kv_heads, nk, d]. q_len, k_len: int32 [batch] valid tokens of a
     padded batch. rope: rotary positions for q and k of the same tokens; the turned
     q and k are rounded to their type before the scores, as rotary() returns them,
-    but for bf16 of few columns or tokens, which stays in fp32 until the end.
+    and their gradients before they are turned back. bf16 of up to 8 columns or 16
+    tokens stays in fp32 from the turn to the last rounding instead, and so does bf16
+    of up to 32 columns and 2^22 pairs of a query and a key. rotary() and
+    dense_attention() one after the other round to their type at any size.
     A backward pass that a CUDA graph captures wants leaves made inside the capture
     (x.detach().requires_grad_()), as every autograd function does."""
     return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)

@@ -211,3 +211,15 @@ def test_tensors_off_16_bytes_are_copied(dtype):
         assert take(whole) is whole
         turned = take(flat[1:].view(2, 5, 3, 8).transpose(1, 2))
         assert turned.data_ptr() % 16 == 0 and torch.equal(turned, flat[1:].view(2, 5, 3, 8).transpose(1, 2))
+
+
+@pytest.mark.parametrize("b,h,n,d,wide", [
+    (1, 12, 16, 64, True), (1, 12, 17, 64, False), (64, 16, 16, 128, True),    # a handful of tokens
+    (1, 12, 16384, 8, True),                                                    # a handful of columns
+    (1, 12, 512, 32, True), (1, 12, 600, 32, False), (48, 12, 256, 16, False),  # up to what hides behind the call
+    (1, 12, 16384, 32, False), (1, 4, 1024, 32, True), (1, 4, 1025, 24, False), (1, 1, 100, 40, False),
+])
+def test_where_rotary_attention_stays_in_fp32(b, h, n, d, wide):
+    q = torch.empty(b, h, n, d, dtype=torch.bfloat16, device="meta")
+    assert llsa._wide(q, q) is wide
+    assert llsa._wide(q.float(), q.float()) is False

@@ -573,3 +573,22 @@ def test_inputs_and_gradients_off_16_bytes(dtype):
     want = torch.autograd.grad(llsa.dense_attention(*leaves), leaves, x["dout"])
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n,d,causal", [(2048, 32, False), (1500, 24, True), (2000, 16, False)])
+def test_rotary_attention_of_many_tokens_stays_in_bf16(n, d, causal):
+    """Behind a handful of columns, dense_attention(rope=) on many tokens is rotary() and
+    dense_attention() bit for bit, in both directions."""
+    x = {m: t.cuda() for m, t in make(1, 2, 2, n, n, d, "bf16", seed=71).items()}
+    rope = llsa.RopeParams.like(x["q"], x["k"])
+    leaves = [x[m].requires_grad_() for m in ("q", "k", "v")]
+    o = llsa.dense_attention(*leaves, causal=causal, rope=rope)
+    got = torch.autograd.grad(o, leaves, x["dout"])
+    qr, kr = (t.detach().requires_grad_() for t in llsa.rotary(leaves[0], leaves[1], rope))
+    o2 = llsa.dense_attention(qr, kr, leaves[2], causal=causal)
+    dqr, dkr, dv = torch.autograd.grad(o2, (qr, kr, leaves[2]), x["dout"])
+    dq, dk = torch.empty_like(dqr), torch.empty_like(dkr)
+    llsa.llsa_rope(rope, dqr, dkr, dq, dk, inverse=True)
+    assert torch.equal(o, o2)
+    for a, b in zip(got, (dq, dk, dv)):
+        assert torch.equal(a, b)
