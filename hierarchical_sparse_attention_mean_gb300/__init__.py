@@ -835,6 +835,9 @@ def _dense_functions():
                 q, k = _contiguous(q), _contiguous(k)
             elif _wide(q, k):
                 _check_rope(rope, q, k)
+                for name, t, want in (("q", q, _tok_dtype(rope)), ("k", k, dtype), ("v", v, dtype)):
+                    if t.dtype != want:
+                        raise ValueError(f"{name} must be {want}, got {t.dtype}")
                 q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
                 rope = rope.in_fp32()
                 llsa_rope(rope, q, k, q, k, pos=pos)

@@ -592,3 +592,18 @@ def test_rotary_attention_of_many_tokens_stays_in_bf16(n, d, causal):
     assert torch.equal(o, o2)
     for a, b in zip(got, (dq, dk, dv)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("n", [8, 100])
+def test_rotary_attention_refuses_mixed_types(n):
+    """Also where bf16 stays in fp32 in between: k, v and the positions' parameters are of q's type."""
+    d = 8 if n == 100 else 64
+    q, k, v = (torch.zeros(1, 2, n, d, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    assert llsa._wide(q, k)
+    rope = llsa.RopeParams.like(q, k)
+    llsa.dense_attention(q, k, v, rope=rope)
+    for args in ((q, k.float(), v), (q, k, v.float()), (q, k, v.half())):
+        with pytest.raises(ValueError, match="must be torch.bfloat16"):
+            llsa.dense_attention(*args, rope=rope)
+    with pytest.raises(ValueError, match="must be torch.float32"):
+        llsa.dense_attention(q, k, v, rope=rope.in_fp32())
