@@ -8,7 +8,8 @@
 // 0.06 rad), so the frequency is held as f = w / 2 pi turns in a 64-bit
 // fraction: the integer product p f modulo 2^64 is the turn's fraction itself,
 // with no range reduction left to do, and its top 32 bits as a signed number
-// of half turns are what sincospif takes.
+// of half turns are what sincospif takes, rounded to fp32: 2^-26 turns. The frequency
+// comes from double precision and adds up to 2^-54 turns per position (w <= 1).
 //
 // Bound by HBM: every element is read and written once. The angles depend on
 // the token and the pair alone, so a thread takes one 16-byte unit of a token

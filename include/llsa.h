@@ -371,8 +371,11 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  *                              orig_len positions, orig_len * w / 2 pi, go
  *                              from `low` to `high`
  * amplitude 0 selects 1, or 0.1 ln(factor) + 1 under WAVELENGTH.
- * Angles are exact to 2^-31 turns at every int32 position (the frequency is a
- * 64-bit fraction of a turn, and the product keeps its fractional part).
+ * An angle is within 2^-26 + 2^-32 turns of position * w_i (what its fp32 form
+ * rounds off), plus |position| * max(1, w_i) * 2^-54 turns (frequencies are worked
+ * out in double precision): 2^-23 turns at the farthest int32 position. The
+ * frequency is a 64-bit fraction of a turn, and the product keeps its fractional
+ * part, so no bits are lost to the turns before it.
  * `inverse` turns by the negative angles: with amplitude 1 the inverse, and
  * with any amplitude the gradient of the call.
  *

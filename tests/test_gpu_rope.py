@@ -215,3 +215,51 @@ def test_one_token_positions():
         out = torch.empty_like(qc)
         llsa.llsa_rope(p, qc, None, out, None, pos=torch.tensor(pos, dtype=torch.int32, device="cuda"))
         ref.check("out", out, ref.rotary(q, torch.tensor(full), dtype=torch.float32))
+
+
+PI = "3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803"
+
+
+def turns_per_position(seg, i, base=10000.0, scaling="none", factor=1.0, orig_len=0, low=1.0, high=32.0):
+    """A pair's frequency in turns, to 60 digits."""
+    from decimal import Decimal, localcontext
+    with localcontext() as c:
+        c.prec = 60
+        b, f, two_pi = Decimal(base), Decimal(factor), 2 * Decimal(PI)
+        if scaling == "base":
+            b *= f ** (Decimal(seg) / (seg - 2))
+        w = b ** (Decimal(-2 * i) / seg)
+        if scaling == "linear":
+            w /= f
+        if scaling == "wavelength":
+            g = min(Decimal(1), max(Decimal(0), (orig_len * w / two_pi - Decimal(low)) / (Decimal(high) - Decimal(low))))
+            w *= g + (1 - g) / f
+        return w / two_pi
+
+
+@pytest.mark.parametrize("d,kw", [(64, {}), (128, {"base": 500000.0}), (64, {"scaling": "linear", "factor": 8.0}),
+                                  (64, {"scaling": "linear", "factor": 0.05}), (72, {"scaling": "base", "factor": 16.0}),
+                                  (64, {"scaling": "wavelength", "factor": 8.0, "orig_len": 4096, "amplitude": 1.0})])
+def test_angles_are_as_good_as_stated(d, kw):
+    """Unit vectors, so that the outputs are cosine and sine: off by the stated error of the
+    angle and by 2 ulp of sincospif."""
+    import math
+    from decimal import Decimal, localcontext
+    at = [0, 1, -1, 2, 3, 37, 1000, 4095, -99999, 777777, 1 << 24, (1 << 24) + 1, 123456789, -(1 << 30), (1 << 31) - 1, -(1 << 31)]
+    x = torch.zeros(1, 1, len(at), d)
+    x[..., :d // 2] = 1.0
+    out = torch.empty_like(x, device="cuda")
+    p = llsa.RopeParams(1, 1, len(at), d, dtype="fp32", **kw)
+    llsa.llsa_rope(p, x.cuda(), None, out, None, pos=torch.tensor(at, dtype=torch.int32, device="cuda"))
+    got = out.cpu().double()[0, 0]
+    kw = {k: v for k, v in kw.items() if k != "amplitude"}
+    for i in range(d // 2):
+        f = turns_per_position(d, i, **kw)
+        for t, pos in enumerate(at):
+            with localcontext() as c:
+                c.prec = 60
+                turn = f * pos
+                turn = float(turn - turn.to_integral_value())
+            far = 2.0 ** -26 + 2.0 ** -32 + abs(pos) * max(1.0, 2 * math.pi * float(f)) * 2.0 ** -54
+            for value, want in ((got[t, i], math.cos(2 * math.pi * turn)), (got[t, i + d // 2], math.sin(2 * math.pi * turn))):
+                assert abs(float(value) - want) <= 2 * math.pi * far + 2.0 ** -23 * abs(want) + 2.0 ** -40, (i, pos)
