@@ -293,12 +293,14 @@ int launch_rope(const llsa_rope_params* p, RopeArgs& a, cudaStream_t st) {
     const long long threads = a.rows * units;
     // As many heads per thread (the sines are computed once for them) as leave
     // one wave of resident threads (6 heads x 10,785 tokens in fp32 14 us; two waves, 22).
+    // 65,535 blocks is the most that the grid's second dimension takes.
     const long long want = (long long)sm_count() * 2048;
-    a.heads_per_thread = (int)std::min<long long>(total, std::max<long long>(1, threads * total / want));
+    const long long least = (total + 65534) / 65535;
+    a.heads_per_thread = (int)std::min<long long>(total, std::max(least, threads * total / want));
     const long long gx = (threads + kThreads - 1) / kThreads;
     const int gy = (total + a.heads_per_thread - 1) / a.heads_per_thread;
     a.heads_per_thread = (total + gy - 1) / gy;  // the same share for all
-    if (gx > 2147483647LL || gy > 65535) return LLSA_ERR_UNSUPPORTED;
+    if (gx > 2147483647LL) return LLSA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)gx, (unsigned)gy);
     if (mode == kInterleaved) LLSA_LAUNCH("rope", st, rope_kernel<T, kInterleaved><<<grid, kThreads, 0, st>>>(a));
     else if (mode == kHalfVector) LLSA_LAUNCH("rope", st, rope_kernel<T, kHalfVector><<<grid, kThreads, 0, st>>>(a));
@@ -324,7 +326,7 @@ extern "C" int llsa_rope(const llsa_rope_params* p, const llsa_rope_strides* str
     LLSA_TRY(derive_rope(p, &a));
     const long long total = (long long)p->heads + p->kv_heads;
     if (p->batch == 0 || p->n == 0 || total == 0) return LLSA_OK;
-    if ((double)p->batch * p->n * total * p->d > (double)(1LL << 40)) return LLSA_ERR_UNSUPPORTED;
+    if (total > (1 << 30) || (double)p->batch * p->n * total * p->d > (double)(1LL << 40)) return LLSA_ERR_UNSUPPORTED;
     if (p->heads > 0) LLSA_TRY(check_ptrs({q, q_out}));
     if (p->kv_heads > 0) LLSA_TRY(check_ptrs({k, k_out}));
     if (pos && (reinterpret_cast<uintptr_t>(pos) & 3u)) return LLSA_ERR_ALIGN;

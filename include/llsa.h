@@ -394,7 +394,7 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  *                  contiguous; every stride that is used spans a multiple of
  *                  16 bytes (LLSA_ERR_ALIGN otherwise), and an output's are
  *                  not 0 (LLSA_ERR_INVALID_ARG): its rows must not overlap.
- * Limits: 2^40 elements of q and k together, 65,535 heads (LLSA_ERR_UNSUPPORTED). */
+ * Limits: 2^40 elements and 2^30 heads of q and k together (LLSA_ERR_UNSUPPORTED). */
 enum { LLSA_ROPE_HALF = 0, LLSA_ROPE_INTERLEAVED = 1 };
 enum { LLSA_ROPE_SCALE_NONE = 0, LLSA_ROPE_SCALE_LINEAR = 1, LLSA_ROPE_SCALE_BASE = 2, LLSA_ROPE_SCALE_WAVELENGTH = 3 };
 

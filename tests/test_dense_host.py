@@ -223,3 +223,10 @@ def test_where_rotary_attention_stays_in_fp32(b, h, n, d, wide):
     q = torch.empty(b, h, n, d, dtype=torch.bfloat16, device="meta")
     assert llsa._wide(q, q) is wide
     assert llsa._wide(q.float(), q.float()) is False
+
+
+@pytest.mark.parametrize("heads,kv", [((1 << 31) - 1, (1 << 31) - 1), ((1 << 30) + 1, 0), (1 << 30, 1)])
+def test_rope_heads_refused(lib, heads, kv):
+    """Few elements, but more heads than a launch counts."""
+    p = llsa.RopeParams(1, heads, 1, 8, kv_heads=kv)
+    assert rope(lib, p) == UNSUPPORTED

@@ -263,3 +263,16 @@ def test_angles_are_as_good_as_stated(d, kw):
             far = 2.0 ** -26 + 2.0 ** -32 + abs(pos) * max(1.0, 2 * math.pi * float(f)) * 2.0 ** -54
             for value, want in ((got[t, i], math.cos(2 * math.pi * turn)), (got[t, i + d // 2], math.sin(2 * math.pi * turn))):
                 assert abs(float(value) - want) <= 2 * math.pi * far + 2.0 ** -23 * abs(want) + 2.0 ** -40, (i, pos)
+
+
+@pytest.mark.parametrize("h,kv,n", [(65536, 0, 1), (65535, 1, 1), (50000, 90000, 3), (131072, 3, 1)])
+def test_many_heads(h, kv, n):
+    """More heads than a grid has blocks in its second dimension."""
+    q, k = rand((1, h, n, 8), "fp32", 40), rand((1, kv, n, 8), "fp32", 41)
+    qc, kc = q.cuda(), k.cuda() if kv else None
+    p = llsa.RopeParams.like(qc, kc, pos_offset=5)
+    pos = (torch.arange(n) + 5)[None, :, None]
+    out = llsa.rotary(qc, kc, p)
+    ref.check("q", out[0] if kv else out, ref.rotary(q, pos, dtype=torch.float32))
+    if kv:
+        ref.check("k", out[1], ref.rotary(k, pos, dtype=torch.float32))
