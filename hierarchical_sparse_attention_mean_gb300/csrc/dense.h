@@ -9,7 +9,9 @@
 // over those heads in one place.
 //
 // Mask. Every rule of the call (lengths, padding, causal order) leaves row r
-// the keys 0 .. kend(r) - 1, so one number per row is the mask.
+// the keys 0 .. kend(r) - 1, so one number per row is the mask. A row without keys is
+// known by its sum of weights, 0 (o = 0, lse = -infinity); the sum of a row with a NaN
+// among its scores is NaN, and so are its o and lse.
 #pragma once
 
 #include "internal.h"

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(const __grid_c
         l = fmaf(x.y, exp2f(x.x - shift), l);
     }
     l = warp_sum(l);
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     const int at_once = a.d <= 64 ? 2 : 1, sub = at_once == 2 ? lane >> 4 : 0;
     const int c = (at_once == 2 ? lane & 15 : lane) * 4;  // and c + 128 behind 128 columns
     float acc[2][4] = {};
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(const __grid_c
         }
         if (sub == 0 && c + 128 * k < a.d) store4(static_cast<T*>(a.o_out) + row * a.d + c + 128 * k, acc[k]);
     }
-    if (lane == 0) a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+    if (lane == 0) a.lse_out[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
 // Sums of `parts` fp32 arrays of n values, in ascending order, for up to three

@@ -200,10 +200,10 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_few_kernel(DenseArgs a) {
             if (c == 0)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(top, sum);
         } else {
-            out = sum > 0.f ? out / sum : 0.f;
+            out = sum == 0.f ? 0.f : out / sum;
             if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(a.o_out)[row * a.d + c] = __float2bfloat16_rn(out);
             else static_cast<float*>(a.o_out)[row * a.d + c] = out;
-            if (c == 0) a.lse_out[row] = sum > 0.f ? (top + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+            if (c == 0) a.lse_out[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         }
     }
 }

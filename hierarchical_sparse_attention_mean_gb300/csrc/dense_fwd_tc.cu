@@ -428,7 +428,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
             unpack2(l4[0], l0, l1);
             unpack2(l4[1], l2, l3);
             const float l = (l0 + l1) + (l2 + l3);
-            const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
+            const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
             const int4 piece = bar->pieces.slot[slot][0];  // slice, first row, part
             const int r = piece.y + w * BM + lr;
             const long long row = (long long)piece.x * a.R + r, prow = (long long)piece.z * a.slices * a.R + row;
@@ -438,7 +438,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constan
                 if (a.splits > 1)
                     reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
                 else
-                    a.lse_out[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+                    a.lse_out[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             }
             if (n == 0) {  // no key for these rows
                 if (r < a.R)

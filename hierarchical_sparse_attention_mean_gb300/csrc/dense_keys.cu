@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_keys_kernel(const __grid_c
             }
         }
         if (r >= a.R) continue;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
         for (int i = 0; i < kChunks; i++) {
             const int c = (i * LPR + sub) * 4;
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_keys_kernel(const __grid_c
             for (int e = 0; e < 4; e++) o[e] *= inv;
             if (c < a.d) store4(static_cast<float*>(a.o_out) + row * a.d + c, o);
         }
-        if (sub == 0) a.lse_out[row] = l > 0.f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        if (sub == 0) a.lse_out[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
     }
 }
 

@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
             float2* ml = reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d);
             if (tx == 0) ml[prow] = make_float2(m[i], l[i]);
         } else {
-            store_row<T, DP>(static_cast<T*>(a.o_out) + row * a.d, acc[i], l[i] > 0.f ? 1.f / l[i] : 0.f, a.d, tx);
-            if (tx == 0) a.lse_out[row] = l[i] > 0.f ? m[i] * 0.6931471805599453f + logf(l[i]) : -INFINITY;
+            store_row<T, DP>(static_cast<T*>(a.o_out) + row * a.d, acc[i], l[i] == 0.f ? 0.f : 1.f / l[i], a.d, tx);
+            if (tx == 0) a.lse_out[row] = l[i] == 0.f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
         }
     }
 }

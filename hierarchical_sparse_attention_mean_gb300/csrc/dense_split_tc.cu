@@ -307,14 +307,14 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         named_barrier(1, kFwdWarps * 32);
         l = bar->l[lr];
         const long long row = (long long)slice * a.R + r, prow = (long long)part * a.slices * a.R + row;
-        const float inv = l > 0.f ? (a.splits > 1 ? 1.f : 1.f / l) : 0.f;
+        const float inv = l == 0.f ? 0.f : a.splits > 1 ? 1.f : 1.f / l;
         if (r < a.R) {
             if (a.splits > 1) store_rowpart<D / 2>(a.part + prow * a.d, acc, inv, half * (D / 2), a.d);
             else store_rowpart<D / 2>(static_cast<T*>(a.o_out) + row * a.d, acc, inv, half * (D / 2), a.d);
             if (half == 0 && a.splits > 1)
                 reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d)[prow] = make_float2(m, l);
             else if (half == 0)
-                a.lse_out[row] = l > 0.f ? m * 0.6931471805599453f + logf(l) : -INFINITY;
+                a.lse_out[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
         }
     }
     tc_fence_before();

@@ -310,7 +310,8 @@ int llsa_reorder(const llsa_params *p, int height, int width, const void *in, vo
  * Tokens at or beyond a length may hold anything, NaN and infinities included;
  * what is stored for them (o, dq, dk, dv) is zero. Values of tokens inside
  * the lengths must be finite and below 2^127 in magnitude (fp32 operands are cut
- * into bf16 pieces). A length outside [0, nq] or [0, nk] is clamped
+ * into bf16 pieces); a query with a NaN among its scores gets NaN in o and lse, and
+ * its gradients pass NaN on. Outputs must not overlap inputs. A length outside [0, nq] or [0, nk] is clamped
  * and reported through llsa_get_status (LLSA_ERR_BAD_INDEX). */
 typedef struct llsa_dense_params {
     int batch;

@@ -607,3 +607,42 @@ def test_rotary_attention_refuses_mixed_types(n):
             llsa.dense_attention(*args, rope=rope)
     with pytest.raises(ValueError, match="must be torch.float32"):
         llsa.dense_attention(q, k, v, rope=rope.in_fp32())
+
+
+@pytest.mark.parametrize("dtype,d,nq,nk", [
+    ("bf16", 64, 300, 333), ("bf16", 128, 300, 333), ("bf16", 200, 300, 333), ("fp32", 64, 300, 333), ("fp32", 128, 300, 333),
+    ("fp32", 136, 300, 333), ("fp32", 64, 300, 9), ("fp32", 128, 300, 9),      # a handful of keys
+    ("bf16", 64, 2, 90), ("fp32", 64, 2, 90), ("bf16", 256, 4, 90),            # a handful of rows, one part
+    ("bf16", 64, 2, 20000), ("fp32", 128, 2, 20000), ("bf16", 64, 100, 20000), ("fp32", 64, 100, 20000),  # keys in parts
+])
+def test_scores_that_are_no_numbers_show(dtype, d, nq, nk):
+    """A NaN in a query makes its row's o and lse NaN and no other row's; a NaN in a key
+    those of every row that sees it. -infinity stays the mark of a row without keys."""
+    x = {m: t.cuda() for m, t in make(1, 2, 2, nq, nk, d, dtype, seed=81).items()}
+    q, k, v = x["q"], x["k"], x["v"]
+    p = llsa.DenseParams.like(q, k)
+    o, lse = llsa.dense_forward(p, q, k, v)
+    assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+    clean = llsa.dense_backward(p, q, k, v, o, lse, x["dout"])
+    row = nq // 2
+    bad = q.clone()
+    bad[0, 1, row, d - 1] = float("nan")
+    o2, lse2 = llsa.dense_forward(p, bad, k, v)
+    assert bool(o2[0, 1, row].isnan().all()) and bool(lse2[0, 1, row].isnan())
+    for got, want in zip(llsa.dense_backward(p, bad, k, v, o2, lse2, x["dout"]), clean):
+        assert bool(got[0, 1].isnan().any()) and torch.equal(got[0, 0], want[0, 0])
+    o2[0, 1, row], lse2[0, 1, row] = o[0, 1, row], lse[0, 1, row]
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+    bad = k.clone()
+    bad[0, 0, nk - 1, 0] = float("nan")
+    o2, lse2 = llsa.dense_forward(p, q, bad, v)
+    assert bool(o2[0, 0].isnan().all()) and bool(lse2[0, 0].isnan().all())
+    assert torch.equal(o2[0, 1], o[0, 1]) and torch.equal(lse2[0, 1], lse[0, 1])
+    # causal order: rows that do not see the key stay as they were; lengths that leave nothing give -infinity
+    if nq == nk - 33:
+        pc = llsa.DenseParams.like(q, k, causal=True)
+        o, lse = llsa.dense_forward(pc, q, k, v)
+        o2, lse2 = llsa.dense_forward(pc, q, bad, v)
+        assert bool(lse2[0, 0, -1].isnan()) and torch.equal(o2[0, 0, :-1], o[0, 0, :-1]) and torch.equal(lse2[0, 0, :-1], lse[0, 0, :-1])
+    o2, lse2 = llsa.dense_forward(p, q, bad, v, k_len=lens([0]))
+    assert not o2.any() and bool((lse2 == -math.inf).all())
