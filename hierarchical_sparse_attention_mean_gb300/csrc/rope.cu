@@ -215,9 +215,8 @@ int derive_rope(const llsa_rope_params* p, RopeArgs* a) {
     }
     if (p->scaling == LLSA_ROPE_SCALE_WAVELENGTH) amplitude = 0.1 * log(p->factor) + 1.0;
     if (p->amplitude != 0.0) amplitude = p->amplitude;
-    if (!isfinite(amplitude)) return LLSA_ERR_INVALID_ARG;
     a->amplitude = (float)amplitude;
-    return LLSA_OK;
+    return isfinite(a->amplitude) ? LLSA_OK : LLSA_ERR_INVALID_ARG;
 }
 
 int check_rope(const llsa_rope_params* p, int has_pos) {

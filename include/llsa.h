@@ -418,7 +418,7 @@ typedef struct llsa_rope_params {
     double base;        /* > 1 */
     double factor;      /* > 0 (ignored by SCALE_NONE) */
     double low, high;   /* WAVELENGTH: low < high */
-    double amplitude;   /* 0 selects the default */
+    double amplitude;   /* 0 selects the default; finite in fp32 */
 } llsa_rope_params;
 
 typedef struct llsa_rope_strides {

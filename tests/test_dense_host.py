@@ -230,3 +230,10 @@ def test_rope_heads_refused(lib, heads, kv):
     """Few elements, but more heads than a launch counts."""
     p = llsa.RopeParams(1, heads, 1, 8, kv_heads=kv)
     assert rope(lib, p) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("amplitude", [1e39, -1e300])
+def test_rope_amplitudes_refused(lib, amplitude):
+    """Finite, but not in the kernel's fp32."""
+    assert rope(lib, llsa.RopeParams(2, 4, 100, 64, kv_heads=2, amplitude=amplitude)) == INVALID
+    assert rope(lib, llsa.RopeParams(2, 4, 100, 64, kv_heads=2, amplitude=amplitude * 1e-30 if amplitude > 0 else -1e38), pos=6) == ALIGN
