@@ -259,7 +259,7 @@ class RopeParams:
     orig_len: int = 0            # "wavelength": positions the model was trained on
     low: float = 1.0             # "wavelength": turns over orig_len below which a pair is stretched fully
     high: float = 32.0           # and above which it is kept
-    amplitude: float = 0.0       # 0: 1, or 0.1 ln(factor) + 1 for "wavelength"
+    amplitude: float = 0.0       # 0: 1, or 0.1 ln(factor) + 1 for "wavelength" with a factor above 1
     dtype: str = "bf16"
 
     def __post_init__(self):

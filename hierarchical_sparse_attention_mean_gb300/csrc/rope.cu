@@ -213,7 +213,8 @@ int derive_rope(const llsa_rope_params* p, RopeArgs* a) {
         // below 2^-11 the fraction has bits behind 2^-64: rounded there
         a->freq[i] = (uint64_t)(f * 18446744073709551616.0 + (f < 4.8828125e-4 ? 0.5 : 0.0));
     }
-    if (p->scaling == LLSA_ROPE_SCALE_WAVELENGTH) amplitude = 0.1 * log(p->factor) + 1.0;
+    // stretched positions ask for sharper scores; the logarithm would turn them flat and at last around below 1
+    if (p->scaling == LLSA_ROPE_SCALE_WAVELENGTH && p->factor > 1.0) amplitude = 0.1 * log(p->factor) + 1.0;
     if (p->amplitude != 0.0) amplitude = p->amplitude;
     a->amplitude = (float)amplitude;
     return isfinite(a->amplitude) ? LLSA_OK : LLSA_ERR_INVALID_ARG;

@@ -371,7 +371,7 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  *                              to 1 as the turns that the pair makes over
  *                              orig_len positions, orig_len * w / 2 pi, go
  *                              from `low` to `high`
- * amplitude 0 selects 1, or 0.1 ln(factor) + 1 under WAVELENGTH.
+ * amplitude 0 selects 1, or 0.1 ln(factor) + 1 under WAVELENGTH with a factor above 1.
  * An angle is within 2^-26 + 2^-32 turns of position * w_i (what its fp32 form
  * rounds off), plus |position| * max(1, w_i) * 2^-54 turns (frequencies are worked
  * out in double precision): 2^-23 turns at the farthest int32 position. The

@@ -276,3 +276,17 @@ def test_many_heads(h, kv, n):
     ref.check("q", out[0] if kv else out, ref.rotary(q, pos, dtype=torch.float32))
     if kv:
         ref.check("k", out[1], ref.rotary(k, pos, dtype=torch.float32))
+
+
+@pytest.mark.parametrize("factor", [1.0, 0.5, 1e-5])
+def test_wavelength_scaling_that_stretches_nothing_keeps_lengths(factor):
+    """The amplitude follows the logarithm of the factor above 1 alone."""
+    x = rand((1, 2, 50, 64), "fp32", 50)
+    xc, out = x.cuda(), torch.empty(1, 2, 50, 64, device="cuda")
+    pos = (torch.arange(50, dtype=torch.int32) * 7)[:, None]
+    kw = dict(scaling="wavelength", factor=factor, orig_len=64)
+    llsa.llsa_rope(llsa.RopeParams.like(xc, **kw), xc, None, out, None, pos=pos.cuda())
+    value, bound = ref.rotary(x, pos[None], amplitude=1.0, dtype=torch.float32, **kw)
+    if factor < 1e-3:  # frequencies of up to 1 / factor radians: their 2^-50 counts as many times
+        bound = bound + 2.0 ** -50 * 350 / factor * 2 * x.double().abs().amax()
+    ref.check("out", out, (value, bound))
