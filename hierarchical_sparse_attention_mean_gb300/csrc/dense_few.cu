@@ -371,17 +371,25 @@ int launch(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
 
 template <typename T>
 int launch_rows(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    return s.R <= 1 ? launch<T, 1>(s, a, st) : s.R <= 2 ? launch<T, 2>(s, a, st) : launch<T, 4>(s, a, st);
+    if (s.R <= 1) return launch<T, 1>(s, a, st);
+    if constexpr (sizeof(T) == 4)
+        if (s.R > 2) return launch<T, 4>(s, a, st);
+    return launch<T, 2>(s, a, st);
 }
 
 }  // namespace
 
-// Two rows where the tensor cores could take them (12 heads x 65,536 keys 49 us
-// against 61; at four rows their kernel is the faster one, 61 us against 72, and 57
-// against 91 at 8 x 4 key heads x 16,383 keys of 128 columns), four where the other choice is the CUDA-core kernel with its 64-row tiles.
-bool dense_few_supported(const DenseShape& s) { return s.R > 0 && s.R <= (dense_tc_supported(s) ? 2 : 4); }
+// bf16: two rows. 12 heads x 65,536 keys 49 us against 61 on the tensor cores; at four
+// rows their kernels are the faster ones, 61 us against 72, and 57 against 91 at 8 x 4 key
+// heads x 16,383 keys of 128 columns (256 columns: two rows 100 against 131, four 203).
+// fp32: four rows, 68 us against 205 at 64 columns there and 121 against 403 at 128.
+bool dense_few_supported(const DenseShape& s) { return s.R > 0 && s.R <= (s.dtype == LLSA_DTYPE_BF16 ? 2 : 4); }
 
-// One round of two blocks per SM; a part has at least 256 keys, two rounds of its warps' loads.
+// Parts for two blocks per SM; a part has at least 256 keys, two rounds of its warps' loads.
+// Three and four rows, and two in the backward pass, take 155 to 197 registers a thread, so
+// that an SM holds one block and the parts run in two rounds: as fast as half as many parts
+// or faster (8 x 4 key heads x 16,383 keys of 128 columns, fp32: four rows backward 289 us
+// and 315, two rows forward 99 and 129).
 DenseSplit dense_few_split(const DenseShape& s) {
     DenseSplit p;
     long long n = 2 * kDenseSms / std::max(1, s.slices);
@@ -391,8 +399,9 @@ DenseSplit dense_few_split(const DenseShape& s) {
     return p;
 }
 
-// Four rows in either type: 8 x 4 key heads x 16,383 keys at 128 columns 139 us
-// against 255 on the tensor cores (one row 90).
+// Four rows in either type: 8 x 4 key heads x 16,383 keys at 128 columns 139 us in bf16
+// against 255 on the tensor cores (one row 90), fp32 289 against 1,170; bf16 at 256
+// columns 272 against 762.
 bool dense_few_bwd_supported(const DenseShape& s) { return s.R > 0 && s.R <= 4 && s.nk > 0; }
 
 int launch_dense_few_bwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {

@@ -646,3 +646,23 @@ def test_scores_that_are_no_numbers_show(dtype, d, nq, nk):
         assert bool(lse2[0, 0, -1].isnan()) and torch.equal(o2[0, 0, :-1], o[0, 0, :-1]) and torch.equal(lse2[0, 0, :-1], lse[0, 0, :-1])
     o2, lse2 = llsa.dense_forward(p, q, bad, v, k_len=lens([0]))
     assert not o2.any() and bool((lse2 == -math.inf).all())
+
+
+@pytest.mark.parametrize("dtype,d,rows,few", [
+    ("bf16", 64, 2, True), ("bf16", 64, 3, False), ("bf16", 256, 2, True), ("bf16", 256, 3, False), ("bf16", 136, 4, False),
+    ("fp32", 64, 4, True), ("fp32", 64, 5, False), ("fp32", 256, 4, True), ("fp32", 256, 5, False),
+])
+def test_which_kernel_takes_a_handful_of_rows(dtype, d, rows, few):
+    """Forward: up to two rows in bf16 and four in fp32 in one pass over the keys."""
+    x = {m: t.cuda() for m, t in make(1, 2 * rows, 2, 1, 700, d, dtype, seed=91).items()}
+    p = llsa.DenseParams.like(x["q"], x["k"])
+    llsa.profile_reset()
+    llsa.profile_enable(True)
+    try:
+        llsa.dense_forward(p, x["q"], x["k"], x["v"])
+        torch.cuda.synchronize()
+        launched = {n for n, _ in llsa.profile_read()}
+    finally:
+        llsa.profile_enable(False)
+        llsa.profile_reset()
+    assert ("dense_fwd_few" in launched) is few, launched
