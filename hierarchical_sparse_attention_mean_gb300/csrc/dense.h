@@ -137,7 +137,7 @@ inline DenseSplit dense_make_split(long long blocks, int extent, int tile, int l
     return p;
 }
 
-// dense_simt.cu: CUDA-core kernels (any type and head dimension).
+// dense_simt.cu: fp32 behind 128 columns on the CUDA cores.
 DenseSplit dense_simt_fwd_split(const DenseShape& s);  // dq: the same
 DenseSplit dense_simt_dkv_split(const DenseShape& s);
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st);

@@ -167,6 +167,20 @@ __global__ void __launch_bounds__(kThreads) dense_join_sum_kernel(const __grid_c
     store4(static_cast<T*>(a.out[t]) + i, acc);
 }
 
+// What is left of a call without rows or without keys: `n` 16-byte units of zeros in
+// one or two outputs, lse of `rows` rows that see nothing, and the report of lengths
+// outside their range.
+__global__ void __launch_bounds__(kThreads)
+dense_nothing_kernel(const __grid_constant__ DenseArgs a, uint4* x, uint4* y, long long n, float* lse, long long rows) {
+    const long long first = (long long)blockIdx.x * kThreads + threadIdx.x, step = (long long)gridDim.x * kThreads;
+    for (long long s = first * a.kv_heads; s < a.slices; s += step * a.kv_heads) dense_span(a, (int)s);
+    for (long long i = first; i < n; i += step) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (y) y[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    for (long long i = first; i < rows; i += step) lse[i] = -INFINITY;
+}
+
 int derive_dense(const llsa_dense_params* p, DenseShape* s) {
     if (!p) return LLSA_ERR_INVALID_ARG;
     if (p->batch < 0 || p->heads < 0 || p->kv_heads < 0 || p->nq < 0 || p->nk < 0) return LLSA_ERR_INVALID_ARG;
@@ -225,26 +239,29 @@ int check_lens(const int32_t* q_len, const int32_t* k_len) {
 }
 
 // Which kernels take a call.
-enum class Path { kFew, kKeys, kTc, kSplit, kSimt };
+enum class Path { kNone, kFew, kKeys, kTc, kSplit, kSimt };
 
 Path fwd_path(const DenseShape& s) {
-    return dense_few_supported(s)     ? Path::kFew
+    return s.R == 0 || s.nk == 0      ? Path::kNone
+           : dense_few_supported(s)   ? Path::kFew
            : dense_keys_supported(s)  ? Path::kKeys
            : dense_tc_supported(s)    ? Path::kTc
            : dense_split_supported(s) ? Path::kSplit
                                       : Path::kSimt;
 }
 Path bwd_path(const DenseShape& s) {
-    return dense_few_bwd_supported(s) ? Path::kFew
-           : dense_tc_supported(s)    ? Path::kTc
-           : dense_split_supported(s) ? Path::kSplit
-                                      : Path::kSimt;
+    return s.R == 0 || s.nk == 0        ? Path::kNone
+           : dense_few_bwd_supported(s) ? Path::kFew
+           : dense_tc_supported(s)      ? Path::kTc
+           : dense_split_supported(s)   ? Path::kSplit
+                                        : Path::kSimt;
 }
 
 DenseSplit fwd_split(const DenseShape& s) {
     switch (fwd_path(s)) {
-        case Path::kFew: return dense_few_split(s);
+        case Path::kNone:
         case Path::kKeys: return {1, s.nk};
+        case Path::kFew: return dense_few_split(s);
         case Path::kTc: return dense_tc_fwd_split(s);
         case Path::kSplit: return dense_split_fwd_split(s);
         default: return dense_simt_fwd_split(s);
@@ -252,6 +269,7 @@ DenseSplit fwd_split(const DenseShape& s) {
 }
 DenseSplit dq_split(const DenseShape& s) {
     switch (bwd_path(s)) {
+        case Path::kNone: return {1, s.nk};
         case Path::kFew: return dense_few_split(s);
         case Path::kTc: return dense_tc_dq_split(s);
         case Path::kSplit: return dense_split_fwd_split(s);
@@ -260,6 +278,7 @@ DenseSplit dq_split(const DenseShape& s) {
 }
 DenseSplit dkv_split(const DenseShape& s) {
     switch (bwd_path(s)) {
+        case Path::kNone:
         case Path::kFew: return {1, s.nk};  // dk, dv: of the blocks that own the keys
         case Path::kTc: return dense_tc_dkv_split(s);
         case Path::kSplit: return dense_split_dkv_split(s);
@@ -278,7 +297,19 @@ size_t dense_fwd_workspace(const DenseShape& s) {
 // The per-row numbers of the backward pass, one array of the two (the kernels for
 // a handful of rows work them out).
 static size_t dense_rows_bytes(const DenseShape& s) {
-    return bwd_path(s) == Path::kFew ? 0 : align_up((size_t)s.slices * s.Rp * sizeof(float));
+    const Path path = bwd_path(s);
+    return path == Path::kNone || path == Path::kFew ? 0 : align_up((size_t)s.slices * s.Rp * sizeof(float));
+}
+
+// A call without rows or without keys: zeros in x and y (or NULL) of `elems` elements, and
+// lse (or NULL).
+static int launch_dense_nothing(const DenseShape& s, const DenseArgs& a, void* x, void* y, long long elems, float* lse,
+                                cudaStream_t st) {
+    const long long n = elems / (s.dtype == LLSA_DTYPE_BF16 ? 8 : 4), rows = lse ? (long long)s.slices * s.R : 0;
+    const int blocks = (int)std::min<long long>((n + kThreads - 1) / kThreads, 8LL * kDenseSms);
+    LLSA_LAUNCH("dense_nothing", st,
+                dense_nothing_kernel<<<blocks, kThreads, 0, st>>>(a, static_cast<uint4*>(x), static_cast<uint4*>(y), n, lse, rows));
+    return LLSA_OK;
 }
 
 size_t dense_bwd_workspace(const DenseShape& s) {
@@ -295,6 +326,7 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     a.splits = p.splits;
     a.chunk = p.chunk;
     const Path path = fwd_path(s);
+    if (path == Path::kNone) return launch_dense_nothing(s, a, a.o_out, nullptr, (long long)s.slices * s.R * s.d, a.lse_out, st);
     a.part = reinterpret_cast<float*>(static_cast<char*>(ws) + (path == Path::kSplit ? dense_split_planes(s, false) : 0));
     switch (path) {
         case Path::kFew: LLSA_TRY(launch_dense_few(s, a, st)); break;
@@ -317,6 +349,9 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
     const Path path = bwd_path(s);
+    if (path == Path::kNone)
+        return s.R > 0 ? launch_dense_nothing(s, a, a.dq, nullptr, (long long)s.slices * s.R * s.d, nullptr, st)
+                       : launch_dense_nothing(s, a, a.dk, a.dv, (long long)s.slices * s.nk * s.d, nullptr, st);
     const size_t rows = dense_rows_bytes(s);
     void* planes[4];
     if (path == Path::kSplit) {
@@ -325,7 +360,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     }
     a.nl2 = static_cast<float*>(ws);
     a.nd = reinterpret_cast<float*>(static_cast<char*>(ws) + rows);
-    if (s.R > 0 && path != Path::kFew) {
+    if (path != Path::kFew) {
         const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
         if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
         if (bf16)

@@ -1,6 +1,5 @@
-// dense_simt.cu -- dense attention on the CUDA cores: every type and head
-// dimension. What runs here: fp32 behind 128 columns, and calls of either type without
-// rows or keys, for which it writes what is left.
+// dense_simt.cu -- dense attention on the CUDA cores: fp32 behind 128 columns, where the
+// three bf16 planes of a tile of 128 rows would fill shared memory by themselves.
 //
 // Forward: one pass over the keys with the running maximum and sum of the
 // softmax. Backward: probabilities recomputed from lse; dq by blocks of query
@@ -9,11 +8,11 @@
 //
 // A block takes BM rows against tiles of BM rows of the other side, 256
 // threads as 16 x 16, each with an (BM / 16)^2 piece of the score tile and
-// BM / 16 rows of the output. Operands sit in shared memory as fp32, rows of
+// BM / 16 rows of the output. Operands sit in shared memory, rows of
 // DP + 4 floats: the 16 rows that a quarter warp reads then fall on distinct
-// banks. Bound by shared memory: per 4 columns of d a thread loads 8 vectors for 64
-// FMAs, which takes twice the FMAs' time (4 heads x 2,048 tokens, d = 256, fp32:
-// forward 811 us, 21 TFLOP/s of 80; backward 3.5 ms, 12).
+// banks. Bound by shared memory: per 4 columns of d a thread loads 4 vectors for 16
+// FMAs (4 heads x 2,048 tokens, d = 256: forward 827 us, 21 TFLOP/s of 80; backward
+// 3.7 ms, 12).
 #include <algorithm>
 
 #include "dense.h"
@@ -23,34 +22,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
-    return __ldg(reinterpret_cast<const float4*>(p));
-}
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
-    const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
-    const float2 y = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
-    return make_float4(x.x, x.y, y.x, y.y);
-}
+__device__ __forceinline__ float4 load4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
 
 // BM rows of a [rows][d] matrix from row r0 on into shared memory, zeros where
 // valid(row) fails and behind column d.
-template <typename T, int DP, int BM, typename F>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, int r0, int d, F valid) {
+template <int DP, int BM, typename F>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, int r0, int d, F valid) {
     constexpr int C = DP / 4;
     for (int x = threadIdx.x; x < BM * C; x += kThreads) {
         const int r = x / C, c = (x - r * C) * 4;
         float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < d && valid(r0 + r)) f = load4<T>(src + (long long)(r0 + r) * d + c);
+        if (c < d && valid(r0 + r)) f = load4(src + (long long)(r0 + r) * d + c);
         *reinterpret_cast<float4*>(dst + r * (DP + 4) + c) = f;
     }
 }
 
-// The same, fp32, through asynchronous copies: in shared memory after async_wait
+// The same through asynchronous copies: in shared memory after async_wait
 // and a barrier.
 template <int DP, int BM, typename F>
 __device__ __forceinline__ void fetch_tile(float* dst, const float* src, int r0, int d, F valid) {
@@ -66,20 +53,16 @@ __device__ __forceinline__ void fetch_tile(float* dst, const float* src, int r0,
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group 0;\n" ::: "memory"); }
 
-// The forward keeps two buffers for the tiles of the streamed side where the type
-// needs no conversion on the way: the next tile comes in during this one's work (4
-// heads x 200 queries x 8,000 keys of 64 columns 92 -> 73 us). The backward kernels have
-// four operands, and two buffers would leave one block per SM.
-template <typename T, bool FWD>
-constexpr int buffers() {
-    return sizeof(T) == 4 && FWD ? 2 : 1;
-}
+// Buffers for the tiles of the streamed side. The forward keeps two: the next tile comes
+// in during this one's work (8 heads x 300 queries x 5,000 keys of 256 columns 1,006 us,
+// with one 1,911).
+constexpr int kFwdBuffers = 2, kBwdBuffers = 1;
 
 // Tiles of two streamed operands, one after the other.
-template <typename T, int DP, int BM, int NBUF, typename F>
+template <int DP, int BM, int NBUF, typename F>
 struct Stream {
     float *x, *y;  // NBUF tiles each
-    const T *gx, *gy;
+    const float *gx, *gy;
     int d, buf;
     F valid;
 
@@ -99,8 +82,8 @@ struct Stream {
             if (next >= 0) fetch(next);
         } else {
             __syncthreads();
-            load_tile<T, DP, BM>(x, gx, r0, d, valid);
-            load_tile<T, DP, BM>(y, gy, r0, d, valid);
+            load_tile<DP, BM>(x, gx, r0, d, valid);
+            load_tile<DP, BM>(y, gy, r0, d, valid);
             __syncthreads();
         }
     }
@@ -168,8 +151,8 @@ __device__ __forceinline__ void store_p(float* P, const float (&v)[N][N], int ty
 }
 
 // One row's columns of the result, times f.
-template <typename T, int DP>
-__device__ __forceinline__ void store_row(T* dst, const float4 (&acc)[DP / 64], float f, int d, int tx) {
+template <int DP>
+__device__ __forceinline__ void store_row(float* dst, const float4 (&acc)[DP / 64], float f, int d, int tx) {
 #pragma unroll
     for (int c = 0; c < DP / 64; c++)
         if (4 * tx + 64 * c < d) {
@@ -182,9 +165,9 @@ __device__ __forceinline__ void store_row(T* dst, const float4 (&acc)[DP / 64], 
 
 // Partial results of a split over the keys: o unnormalised [split][slice][R][d],
 // then (maximum, sum) pairs [split][slice][R].
-template <typename T, int DP, int BM>
+template <int DP, int BM>
 __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
-    constexpr int N = BM / 16, NBUF = buffers<T, true>();
+    constexpr int N = BM / 16, NBUF = kFwdBuffers;
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sK = sQ + BM * (DP + 4);
@@ -194,10 +177,10 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
     const int tiles = (a.R + BM - 1) / BM;
     const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
     const DenseSpan sp = dense_span(a, slice);
-    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
-    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
-    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
-    load_tile<T, DP, BM>(sQ, q, r0, a.d, [&](int r) { return r < a.R; });
+    const float* q = static_cast<const float*>(a.q) + (long long)slice * a.R * a.d;
+    const float* k = static_cast<const float*>(a.k) + (long long)slice * a.nk * a.d;
+    const float* v = static_cast<const float*>(a.v) + (long long)slice * a.nk * a.d;
+    load_tile<DP, BM>(sQ, q, r0, a.d, [&](int r) { return r < a.R; });
     int kend[N];
 #pragma unroll
     for (int i = 0; i < N; i++) {
@@ -217,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto key_ok = [&](int j) { return j < sp.lk; };
-    Stream<T, DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    Stream<DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
     if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
         stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
@@ -264,11 +247,11 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
         const long long row = (long long)slice * a.R + r;
         if (a.splits > 1) {
             const long long prow = (long long)part * a.slices * a.R + row;
-            store_row<float, DP>(a.part + prow * a.d, acc[i], 1.f, a.d, tx);
+            store_row<DP>(a.part + prow * a.d, acc[i], 1.f, a.d, tx);
             float2* ml = reinterpret_cast<float2*>(a.part + (long long)a.splits * a.slices * a.R * a.d);
             if (tx == 0) ml[prow] = make_float2(m[i], l[i]);
         } else {
-            store_row<T, DP>(static_cast<T*>(a.o_out) + row * a.d, acc[i], l[i] == 0.f ? 0.f : 1.f / l[i], a.d, tx);
+            store_row<DP>(static_cast<float*>(a.o_out) + row * a.d, acc[i], l[i] == 0.f ? 0.f : 1.f / l[i], a.d, tx);
             if (tx == 0) a.lse_out[row] = l[i] == 0.f ? -INFINITY : m[i] * 0.6931471805599453f + logf(l[i]);
         }
     }
@@ -277,9 +260,9 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
 // --------------------------------------------------------------- backward --
 
 // dq of BM query rows. Partial sums of a split over the keys: [split][slice][R][d].
-template <typename T, int DP, int BM>
+template <int DP, int BM>
 __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
-    constexpr int N = BM / 16, NBUF = buffers<T, false>();
+    constexpr int N = BM / 16, NBUF = kBwdBuffers;
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sG = sQ + BM * (DP + 4);
@@ -291,13 +274,13 @@ __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
     const int part = piece / (tiles * a.slices), rest = piece - part * (tiles * a.slices);
     const int slice = rest / tiles, r0 = (rest - slice * tiles) * BM;
     const DenseSpan sp = dense_span(a, slice);
-    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
-    const T* g = static_cast<const T*>(a.dout) + (long long)slice * a.R * a.d;
-    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
-    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
+    const float* q = static_cast<const float*>(a.q) + (long long)slice * a.R * a.d;
+    const float* g = static_cast<const float*>(a.dout) + (long long)slice * a.R * a.d;
+    const float* k = static_cast<const float*>(a.k) + (long long)slice * a.nk * a.d;
+    const float* v = static_cast<const float*>(a.v) + (long long)slice * a.nk * a.d;
     auto row_ok = [&](int r) { return r < a.R && r % a.nq < sp.lq; };
-    load_tile<T, DP, BM>(sQ, q, r0, a.d, row_ok);
-    load_tile<T, DP, BM>(sG, g, r0, a.d, row_ok);
+    load_tile<DP, BM>(sQ, q, r0, a.d, row_ok);
+    load_tile<DP, BM>(sG, g, r0, a.d, row_ok);
     int kend[N];
     float nl2[N], nd[N];
 #pragma unroll
@@ -316,7 +299,7 @@ __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
 #pragma unroll
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto key_ok = [&](int j) { return j < sp.lk; };
-    Stream<T, DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    Stream<DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
     if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
         stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
@@ -340,17 +323,17 @@ __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
         if (r >= a.R) continue;
         const long long row = (long long)slice * a.R + r;
         if (a.splits > 1)
-            store_row<float, DP>(a.part + ((long long)part * a.slices * a.R + row) * a.d, acc[i], a.scale, a.d, tx);
+            store_row<DP>(a.part + ((long long)part * a.slices * a.R + row) * a.d, acc[i], a.scale, a.d, tx);
         else
-            store_row<T, DP>(static_cast<T*>(a.dq) + row * a.d, acc[i], a.scale, a.d, tx);
+            store_row<DP>(static_cast<float*>(a.dq) + row * a.d, acc[i], a.scale, a.d, tx);
     }
 }
 
 // dk and dv of BM keys, over the query rows of all heads that share them.
 // Partial sums of a split over the rows: dk [split][slice][nk][d], then dv.
-template <typename T, int DP, int BM>
+template <int DP, int BM>
 __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
-    constexpr int N = BM / 16, NBUF = buffers<T, false>();
+    constexpr int N = BM / 16, NBUF = kBwdBuffers;
     extern __shared__ float4 smem4[];
     float* sK = reinterpret_cast<float*>(smem4);
     float* sV = sK + BM * (DP + 4);
@@ -363,14 +346,14 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
     const int part = piece / (tiles * a.slices), rest = piece - part * (tiles * a.slices);
     const int slice = rest / tiles, j0 = (rest - slice * tiles) * BM;
     const DenseSpan sp = dense_span(a, slice);
-    const T* q = static_cast<const T*>(a.q) + (long long)slice * a.R * a.d;
-    const T* g = static_cast<const T*>(a.dout) + (long long)slice * a.R * a.d;
-    const T* k = static_cast<const T*>(a.k) + (long long)slice * a.nk * a.d;
-    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * a.d;
+    const float* q = static_cast<const float*>(a.q) + (long long)slice * a.R * a.d;
+    const float* g = static_cast<const float*>(a.dout) + (long long)slice * a.R * a.d;
+    const float* k = static_cast<const float*>(a.k) + (long long)slice * a.nk * a.d;
+    const float* v = static_cast<const float*>(a.v) + (long long)slice * a.nk * a.d;
     auto key_ok = [&](int j) { return j < sp.lk; };
     auto row_ok = [&](int r) { return r < a.R && r % a.nq < sp.lq; };
-    load_tile<T, DP, BM>(sK, k, j0, a.d, key_ok);
-    load_tile<T, DP, BM>(sV, v, j0, a.d, key_ok);
+    load_tile<DP, BM>(sK, k, j0, a.d, key_ok);
+    load_tile<DP, BM>(sV, v, j0, a.d, key_ok);
     const int r_first = a.splits > 1 ? part * a.chunk : 0;
     const int r_last = a.splits > 1 ? min(a.R, r_first + a.chunk) : a.R;
     const float sl2 = a.scale * kDenseLog2e;
@@ -383,7 +366,7 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
         while (r0 < r_last && dense_tile_kend(a, sp, r0 % a.nq, BM) <= j0) r0 += BM;
         return r0 < r_last ? r0 : -1;
     };
-    Stream<T, DP, BM, NBUF, decltype(row_ok)> stream{sQ, sG, q, g, a.d, 0, row_ok};
+    Stream<DP, BM, NBUF, decltype(row_ok)> stream{sQ, sG, q, g, a.d, 0, row_ok};
     int next = settle(r_first);
     if (next >= 0) stream.fetch(next);
     while (next >= 0) {
@@ -419,54 +402,28 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
         const long long row = (long long)slice * a.nk + j;
         if (a.splits > 1) {
             const long long all = (long long)a.slices * a.nk;
-            store_row<float, DP>(a.part + (part * all + row) * a.d, dk[i], a.scale, a.d, tx);
-            store_row<float, DP>(a.part + ((a.splits + part) * all + row) * a.d, dv[i], 1.f, a.d, tx);
+            store_row<DP>(a.part + (part * all + row) * a.d, dk[i], a.scale, a.d, tx);
+            store_row<DP>(a.part + ((a.splits + part) * all + row) * a.d, dv[i], 1.f, a.d, tx);
         } else {
-            store_row<T, DP>(static_cast<T*>(a.dk) + row * a.d, dk[i], a.scale, a.d, tx);
-            store_row<T, DP>(static_cast<T*>(a.dv) + row * a.d, dv[i], 1.f, a.d, tx);
+            store_row<DP>(static_cast<float*>(a.dk) + row * a.d, dk[i], a.scale, a.d, tx);
+            store_row<DP>(static_cast<float*>(a.dv) + row * a.d, dv[i], 1.f, a.d, tx);
         }
     }
 }
 
 // Pieces of keys first, they are the longer ones; those of rows fill up what they
-// leave (12 heads x 64 tokens of 128 columns in fp32 47.8 us in two launches, 28.4 in one).
-template <typename T, int DP, int BM>
+// leave (12 heads x 64 tokens of 256 columns 94 us in two launches, 55 in one).
+template <int DP, int BM>
 __global__ void __launch_bounds__(kThreads)
 dense_bwd_simt_kernel(const __grid_constant__ DenseArgs aq, const __grid_constant__ DenseArgs ak, int key_pieces) {
     const int piece = blockIdx.x;
     if (piece < key_pieces)
-        keys_side<T, DP, BM>(ak, piece);
+        keys_side<DP, BM>(ak, piece);
     else
-        rows_side<T, DP, BM>(aq, piece - key_pieces);
+        rows_side<DP, BM>(aq, piece - key_pieces);
 }
 
 constexpr int kColumns = 256, kRows = 32;  // of a tile
-
-template <typename T>
-int launch_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * buffers<T, true>()) * tile + p;
-    static_assert(smem <= 227 * 1024, "shared memory budget");
-    const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
-    if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    const dim3 grid((unsigned)blocks, a.splits);
-    cudaFuncSetAttribute(dense_fwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    LLSA_LAUNCH("dense_fwd_simt", st, dense_fwd_simt_kernel<T, DP, BM><<<grid, kThreads, smem, st>>>(a));
-    return LLSA_OK;
-}
-
-template <typename T>
-int launch_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
-    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
-    constexpr int smem = (2 + 2 * buffers<T, false>()) * tile + 2 * p;
-    static_assert(smem <= 227 * 1024, "shared memory budget");
-    const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
-    const long long pk = (long long)((s.nk + BM - 1) / BM) * s.slices * ak.splits;
-    if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    cudaFuncSetAttribute(dense_bwd_simt_kernel<T, DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    LLSA_LAUNCH("dense_bwd_simt", st,
-                dense_bwd_simt_kernel<T, DP, BM><<<(unsigned)(pq + pk), kThreads, smem, st>>>(aq, ak, (int)pk));
-    return LLSA_OK;
-}
 
 }  // namespace
 
@@ -478,10 +435,27 @@ DenseSplit dense_simt_dkv_split(const DenseShape& s) {
 }
 
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    return s.dtype == LLSA_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(s, a, st) : launch_fwd<float>(s, a, st);
+    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * kFwdBuffers) * tile + p;
+    static_assert(smem <= 227 * 1024, "shared memory budget");
+    const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
+    if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    const dim3 grid((unsigned)blocks, a.splits);
+    cudaFuncSetAttribute(dense_fwd_simt_kernel<DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    LLSA_LAUNCH("dense_fwd_simt", st, dense_fwd_simt_kernel<DP, BM><<<grid, kThreads, smem, st>>>(a));
+    return LLSA_OK;
 }
+
 int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
-    return s.dtype == LLSA_DTYPE_BF16 ? launch_bwd<__nv_bfloat16>(s, aq, ak, st) : launch_bwd<float>(s, aq, ak, st);
+    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
+    constexpr int smem = (2 + 2 * kBwdBuffers) * tile + 2 * p;
+    static_assert(smem <= 227 * 1024, "shared memory budget");
+    const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
+    const long long pk = (long long)((s.nk + BM - 1) / BM) * s.slices * ak.splits;
+    if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
+    cudaFuncSetAttribute(dense_bwd_simt_kernel<DP, BM>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    LLSA_LAUNCH("dense_bwd_simt", st,
+                dense_bwd_simt_kernel<DP, BM><<<(unsigned)(pq + pk), kThreads, smem, st>>>(aq, ak, (int)pk));
+    return LLSA_OK;
 }
 
 }  // namespace llsa

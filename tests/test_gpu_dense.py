@@ -666,3 +666,18 @@ def test_which_kernel_takes_a_handful_of_rows(dtype, d, rows, few):
         llsa.profile_enable(False)
         llsa.profile_reset()
     assert ("dense_fwd_few" in launched) is few, launched
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("fp32", 40), ("fp32", 256), ("bf16", 136)])
+@pytest.mark.parametrize("nq,nk", [(7, 0), (300, 0), (0, 300)])
+def test_empty_sides_report_bad_lengths(nq, nk, dtype, d):
+    """Without rows or keys the outputs are zeros and -infinity, and a length that does not fit still shows."""
+    x = {m: t.cuda() for m, t in make(5, 4, 2, nq, nk, d, dtype).items()}
+    p = llsa.DenseParams.like(x["q"], x["k"])
+    for ql, kl, status in (([nq] * 5, [nk] * 5, 0), ([nq] * 4 + [nq + 1], None, BAD_INDEX), (None, [nk] * 4 + [-1], BAD_INDEX)):
+        o, lse = llsa.dense_forward(p, x["q"], x["k"], x["v"], lens(ql), lens(kl), o=torch.full_like(x["q"], 7.0))
+        assert llsa.llsa_get_status() == (status if nq else 0)   # no row: no work
+        full = [torch.full_like(x[n], 7.0) for n in ("q", "k", "v")]
+        llsa.dense_backward(p, x["q"], x["k"], x["v"], o, lse, x["dout"], lens(ql), lens(kl), *full)
+        assert llsa.llsa_get_status() == status
+        assert not o.any() and bool((lse == -math.inf).all()) and not any(t.any() for t in full)
