@@ -12,7 +12,7 @@
 // DP + 4 floats: the 16 rows that a quarter warp reads then fall on distinct
 // banks. Bound by shared memory: per 4 columns of d a thread loads 4 vectors for 16
 // FMAs (4 heads x 2,048 tokens, d = 256: forward 827 us, 21 TFLOP/s of 80; backward
-// 3.7 ms, 12).
+// 3.0 ms, 14).
 #include <algorithm>
 
 #include "dense.h"
@@ -53,42 +53,31 @@ __device__ __forceinline__ void fetch_tile(float* dst, const float* src, int r0,
 __device__ __forceinline__ void async_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 __device__ __forceinline__ void async_wait() { asm volatile("cp.async.wait_group 0;\n" ::: "memory"); }
 
-// Buffers for the tiles of the streamed side. The forward keeps two: the next tile comes
-// in during this one's work (8 heads x 300 queries x 5,000 keys of 256 columns 1,006 us,
-// with one 1,911).
-constexpr int kFwdBuffers = 2, kBwdBuffers = 1;
-
-// Tiles of two streamed operands, one after the other.
-template <int DP, int BM, int NBUF, typename F>
+// Tiles of two streamed operands, one after the other, in two buffers: the next tile
+// comes in during this one's work. With one buffer 8 heads x 300 queries x 5,000 keys of
+// 256 columns took 1,911 us forward instead of 1,006, and 4 heads x 2,048 tokens 3,677
+// backward instead of 2,993 (one block per SM either way).
+template <int DP, int BM, typename F>
 struct Stream {
-    float *x, *y;  // NBUF tiles each
+    float *x, *y;  // two tiles each
     const float *gx, *gy;
     int d, buf;
     F valid;
 
-    __device__ __forceinline__ void fetch(int r0) {  // NBUF 2: into the buffer that is not in use
-        if constexpr (NBUF == 2) {
-            fetch_tile<DP, BM>(x + buf * BM * (DP + 4), gx, r0, d, valid);
-            fetch_tile<DP, BM>(y + buf * BM * (DP + 4), gy, r0, d, valid);
-            async_commit();
-        }
+    __device__ __forceinline__ void fetch(int r0) {  // into the buffer that is not in use
+        fetch_tile<DP, BM>(x + buf * BM * (DP + 4), gx, r0, d, valid);
+        fetch_tile<DP, BM>(y + buf * BM * (DP + 4), gy, r0, d, valid);
+        async_commit();
     }
-    // The tile at r0 becomes the current one; `next` (or -1) is asked for. Ends with a barrier.
-    __device__ __forceinline__ void turn(int r0, int next) {
-        if constexpr (NBUF == 2) {
-            async_wait();
-            __syncthreads();
-            buf ^= 1;
-            if (next >= 0) fetch(next);
-        } else {
-            __syncthreads();
-            load_tile<DP, BM>(x, gx, r0, d, valid);
-            load_tile<DP, BM>(y, gy, r0, d, valid);
-            __syncthreads();
-        }
+    // The tile that was asked for becomes the current one, and the one at `next` (or -1) is asked for.
+    __device__ __forceinline__ void turn(int next) {
+        async_wait();
+        __syncthreads();
+        buf ^= 1;
+        if (next >= 0) fetch(next);
     }
-    __device__ __forceinline__ const float* cx() const { return x + (NBUF == 2 ? (buf ^ 1) * BM * (DP + 4) : 0); }
-    __device__ __forceinline__ const float* cy() const { return y + (NBUF == 2 ? (buf ^ 1) * BM * (DP + 4) : 0); }
+    __device__ __forceinline__ const float* cx() const { return x + (buf ^ 1) * BM * (DP + 4); }
+    __device__ __forceinline__ const float* cy() const { return y + (buf ^ 1) * BM * (DP + 4); }
 };
 
 // acc[i][j] = A row (ty * N + i) . B row (tx + 16 j)
@@ -167,12 +156,12 @@ __device__ __forceinline__ void store_row(float* dst, const float4 (&acc)[DP / 6
 // then (maximum, sum) pairs [split][slice][R].
 template <int DP, int BM>
 __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
-    constexpr int N = BM / 16, NBUF = kFwdBuffers;
+    constexpr int N = BM / 16;
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sK = sQ + BM * (DP + 4);
-    float* sV = sK + NBUF * BM * (DP + 4);
-    float* sP = sV + NBUF * BM * (DP + 4);
+    float* sV = sK + 2 * BM * (DP + 4);
+    float* sP = sV + 2 * BM * (DP + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.R + BM - 1) / BM;
     const int slice = blockIdx.x / tiles, r0 = (blockIdx.x - slice * tiles) * BM, part = blockIdx.y;
@@ -200,10 +189,10 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     auto key_ok = [&](int j) { return j < sp.lk; };
-    Stream<DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    Stream<DP, BM, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
     if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
-        stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
+        stream.turn(j0 + BM < j_last ? j0 + BM : -1);
         float s[N][N];
         tile_dot<N, DP>(s, sQ, stream.cx(), ty, tx);
 #pragma unroll
@@ -262,13 +251,13 @@ __global__ void __launch_bounds__(kThreads) dense_fwd_simt_kernel(DenseArgs a) {
 // dq of BM query rows. Partial sums of a split over the keys: [split][slice][R][d].
 template <int DP, int BM>
 __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
-    constexpr int N = BM / 16, NBUF = kBwdBuffers;
+    constexpr int N = BM / 16;
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sG = sQ + BM * (DP + 4);
     float* sK = sG + BM * (DP + 4);
-    float* sV = sK + NBUF * BM * (DP + 4);
-    float* sP = sV + NBUF * BM * (DP + 4);
+    float* sV = sK + 2 * BM * (DP + 4);
+    float* sP = sV + 2 * BM * (DP + 4);
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.R + BM - 1) / BM;
     const int part = piece / (tiles * a.slices), rest = piece - part * (tiles * a.slices);
@@ -299,10 +288,10 @@ __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
 #pragma unroll
         for (int c = 0; c < DP / 64; c++) acc[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
     auto key_ok = [&](int j) { return j < sp.lk; };
-    Stream<DP, BM, NBUF, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
+    Stream<DP, BM, decltype(key_ok)> stream{sK, sV, k, v, a.d, 0, key_ok};
     if (j_first < j_last) stream.fetch(j_first);
     for (int j0 = j_first; j0 < j_last; j0 += BM) {
-        stream.turn(j0, j0 + BM < j_last ? j0 + BM : -1);
+        stream.turn(j0 + BM < j_last ? j0 + BM : -1);
         float s[N][N], dp[N][N];
         tile_dot<N, DP>(s, sQ, stream.cx(), ty, tx);
         tile_dot<N, DP>(dp, sG, stream.cy(), ty, tx);
@@ -333,13 +322,13 @@ __device__ __forceinline__ void rows_side(const DenseArgs& a, int piece) {
 // Partial sums of a split over the rows: dk [split][slice][nk][d], then dv.
 template <int DP, int BM>
 __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
-    constexpr int N = BM / 16, NBUF = kBwdBuffers;
+    constexpr int N = BM / 16;
     extern __shared__ float4 smem4[];
     float* sK = reinterpret_cast<float*>(smem4);
     float* sV = sK + BM * (DP + 4);
     float* sQ = sV + BM * (DP + 4);
-    float* sG = sQ + NBUF * BM * (DP + 4);
-    float* sP = sG + NBUF * BM * (DP + 4);  // P^T
+    float* sG = sQ + 2 * BM * (DP + 4);
+    float* sP = sG + 2 * BM * (DP + 4);  // P^T
     float* sS = sP + BM * (BM + 4);  // dS^T
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     const int tiles = (a.nk + BM - 1) / BM;
@@ -366,13 +355,13 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
         while (r0 < r_last && dense_tile_kend(a, sp, r0 % a.nq, BM) <= j0) r0 += BM;
         return r0 < r_last ? r0 : -1;
     };
-    Stream<DP, BM, NBUF, decltype(row_ok)> stream{sQ, sG, q, g, a.d, 0, row_ok};
+    Stream<DP, BM, decltype(row_ok)> stream{sQ, sG, q, g, a.d, 0, row_ok};
     int next = settle(r_first);
     if (next >= 0) stream.fetch(next);
     while (next >= 0) {
         const int r0 = next;
         next = settle(r0 + BM);
-        stream.turn(r0, next);
+        stream.turn(next);
         float s[N][N], dp[N][N];
         tile_dot<N, DP>(s, sK, stream.cx(), ty, tx);
         tile_dot<N, DP>(dp, sV, stream.cy(), ty, tx);
@@ -412,7 +401,7 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
 }
 
 // Pieces of keys first, they are the longer ones; those of rows fill up what they
-// leave (12 heads x 64 tokens of 256 columns 94 us in two launches, 55 in one).
+// leave (12 heads x 64 tokens of 256 columns, with one buffer 94 us in two launches and 55 in one).
 template <int DP, int BM>
 __global__ void __launch_bounds__(kThreads)
 dense_bwd_simt_kernel(const __grid_constant__ DenseArgs aq, const __grid_constant__ DenseArgs ak, int key_pieces) {
@@ -435,7 +424,7 @@ DenseSplit dense_simt_dkv_split(const DenseShape& s) {
 }
 
 int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
-    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = (1 + 2 * kFwdBuffers) * tile + p;
+    constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4, smem = 5 * tile + p;
     static_assert(smem <= 227 * 1024, "shared memory budget");
     const long long blocks = (long long)((s.R + BM - 1) / BM) * s.slices;
     if (blocks > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
@@ -447,7 +436,7 @@ int launch_dense_simt_fwd(const DenseShape& s, const DenseArgs& a, cudaStream_t 
 
 int launch_dense_simt_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, cudaStream_t st) {
     constexpr int BM = kRows, DP = kColumns, tile = BM * (DP + 4) * 4, p = BM * (BM + 4) * 4;
-    constexpr int smem = (2 + 2 * kBwdBuffers) * tile + 2 * p;
+    constexpr int smem = 6 * tile + 2 * p;
     static_assert(smem <= 227 * 1024, "shared memory budget");
     const long long pq = (long long)((s.R + BM - 1) / BM) * s.slices * aq.splits;
     const long long pk = (long long)((s.nk + BM - 1) / BM) * s.slices * ak.splits;
