@@ -191,6 +191,13 @@ def _dtype_name(t):
     return name
 
 
+def _int32(**fields):
+    """Refuses what a C int would cut to its low bits."""
+    for name, value in fields.items():
+        if not -(1 << 31) <= value < 1 << 31:
+            raise ValueError(f"{name} must fit 32 bits, not {value}")
+
+
 @dataclass(frozen=True)
 class DenseParams:
     """A dense-attention problem; mirrors llsa_dense_params of include/llsa.h."""
@@ -228,6 +235,7 @@ class DenseParams:
 @functools.lru_cache(maxsize=256)
 def _dense_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, scale):
     """What equal parameters share: the C structure, the workspace sizes, the tensors' shapes."""
+    _int32(batch=batch, heads=heads, kv_heads=kv_heads, nq=nq, nk=nk, d=d)
     c = _DenseParams(batch, heads, kv_heads, nq, nk, d, _choice(_DTYPES, dtype, "dtype"), 1 if causal else 0, scale)
     return {"_c": c, "_ref": ctypes.byref(c), "_ws": {},
             "_shapes": ((batch, heads, nq, d), (batch, kv_heads or heads, nk, d), (batch, heads, nq))}
@@ -287,6 +295,8 @@ class RopeParams:
 @functools.lru_cache(maxsize=256)
 def _rope_native(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, order, offset, dtype, scaling, orig_len, *real):
     """The C structures of equal parameters, for positions without and with a batch dimension."""
+    _int32(batch=batch, heads=heads, kv_heads=kv_heads, n=n, d=d, rot_dim=rot_dim, axes=axes, width=width, pos_offset=offset,
+           orig_len=orig_len)
     layout, order = _choice(_ROPE_LAYOUTS, layout, "layout"), _choice(_ORDERS, order, "token_order")
     dtype, scaling = _choice(_DTYPES, dtype, "dtype"), _choice(_ROPE_SCALINGS, scaling, "scaling")
     return tuple(_RopeParams(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, order, offset, batched, dtype,

@@ -237,3 +237,22 @@ def test_rope_amplitudes_refused(lib, amplitude):
     """Finite, but not in the kernel's fp32."""
     assert rope(lib, llsa.RopeParams(2, 4, 100, 64, kv_heads=2, amplitude=amplitude)) == INVALID
     assert rope(lib, llsa.RopeParams(2, 4, 100, 64, kv_heads=2, amplitude=amplitude * 1e-30 if amplitude > 0 else -1e38), pos=6) == ALIGN
+
+
+WRAPS = [(1 << 32) + 100, 1 << 31, -(1 << 31) - 1, (1 << 32) + 2]
+
+
+@pytest.mark.parametrize("value", WRAPS)
+def test_parameters_behind_32_bits_refused(value):
+    """Not cut to their low bits: 2^32 + 100 tokens are not 100, position 2^32 + 2 is not 2."""
+    for field in ("batch", "heads", "kv_heads", "nq", "nk", "d"):
+        with pytest.raises(ValueError, match=field):
+            llsa.DenseParams(**{**dict(batch=2, heads=4, nq=100, nk=100, d=64), field: value})
+    for field in ("batch", "heads", "kv_heads", "n", "d", "rot_dim", "axes", "width", "pos_offset", "orig_len"):
+        with pytest.raises(ValueError, match=field):
+            llsa.RopeParams(**{**dict(batch=2, heads=4, n=100, d=64), field: value})
+    q = torch.empty(1, 1, abs(value), 8, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        llsa.DenseParams.like(q, q)
+    with pytest.raises(ValueError, match="32 bits"):
+        llsa.RopeParams.like(q)
