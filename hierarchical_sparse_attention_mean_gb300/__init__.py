@@ -467,6 +467,13 @@ def dense_workspace_bytes(p: DenseParams, op: int) -> int:
     return got
 
 
+def _ws_on(ws, device):
+    """The workspace's pointer and bytes, on device number `device`."""
+    if ws is not None and isinstance(ws, torch.Tensor) and ws.is_cuda and ws.get_device() != device:
+        raise ValueError(f"ws must be on cuda:{device}, got {ws.device}")
+    return _ws(ws)
+
+
 def _lens(p, q_len, k_len, device):
     return tuple(None if x is None else _like(x, name, (p.batch,), torch.int32, device)
                  for x, name in ((q_len, "q_len"), (k_len, "k_len")))
@@ -477,7 +484,7 @@ def llsa_dense_fwd(p: DenseParams, q, k, v, o, lse, q_len=None, k_len=None, ws=N
     with _on(q, "q"):
         td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
-        w, wb = _ws(ws)
+        w, wb = _ws_on(ws, dev)
         _check(_load().llsa_dense_fwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
                                       _like(v, "v", sk, td, dev), ql, kl, _like(o, "o", sq, td, dev),
                                       _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_dense_fwd")
@@ -488,7 +495,7 @@ def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None
     with _on(q, "q"):
         td, dev, (sq, sk, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
-        w, wb = _ws(ws)
+        w, wb = _ws_on(ws, dev)
         _check(_load().llsa_dense_bwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev),
                                       _like(v, "v", sk, td, dev), _like(o, "o", sq, td, dev),
                                       _like(lse, "lse", sl, torch.float32, dev), _like(dout, "dout", sq, td, dev), ql, kl,

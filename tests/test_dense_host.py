@@ -256,3 +256,18 @@ def test_parameters_behind_32_bits_refused(value):
         llsa.DenseParams.like(q, q)
     with pytest.raises(ValueError, match="32 bits"):
         llsa.RopeParams.like(q)
+
+
+def test_a_workspace_on_another_device_is_refused():
+    class Far(torch.Tensor):  # stands for a tensor on a second GPU
+        is_cuda = property(lambda self: True)
+
+        def get_device(self):
+            return 1
+
+    ws = torch.zeros(64, dtype=torch.uint8).as_subclass(Far)
+    assert llsa._ws_on(ws, 1) == (ws.data_ptr(), 64) and llsa._ws_on(None, 0) == (None, 0)
+    with pytest.raises(ValueError, match="ws must be on cuda:0"):
+        llsa._ws_on(ws, 0)
+    with pytest.raises(TypeError):
+        llsa._ws_on(64, 0)
