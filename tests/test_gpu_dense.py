@@ -681,3 +681,27 @@ def test_empty_sides_report_bad_lengths(nq, nk, dtype, d):
         llsa.dense_backward(p, x["q"], x["k"], x["v"], o, lse, x["dout"], lens(ql), lens(kl), *full)
         assert llsa.llsa_get_status() == status
         assert not o.any() and bool((lse == -math.inf).all()) and not any(t.any() for t in full)
+
+
+def test_rows_behind_32_bits_on_the_tensor_cores():
+    """2^31 elements and more in each of q, o, dout and dq, 130 keys; dout is zero but for the
+    last 300 rows, so that those are the whole backward problem."""
+    d, nk, last = 64, 130, 300
+    n = (1 << 25) + 77
+    q = torch.empty(1, 1, n, d, dtype=torch.bfloat16, device="cuda").normal_()
+    assert q.numel() > 1 << 31
+    k, v = (torch.randn(1, 1, nk, d, device="cuda").bfloat16() for _ in range(2))
+    dout = torch.zeros_like(q)
+    dout[:, :, -last:].normal_()
+    p = llsa.DenseParams.like(q, k)
+    o, lse = llsa.dense_forward(p, q, k, v)
+    dq, dk, dv = llsa.dense_backward(p, q, k, v, o, lse, dout)
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    want = ref.attention(q[:, :, -last:].cpu(), k.cpu(), v.cpu(), dout[:, :, -last:].cpu())
+    got = {"o": o[:, :, -last:], "lse": lse[:, :, -last:], "dq": dq[:, :, -last:], "dk": dk, "dv": dv}
+    for m in got:
+        ref.check(m, got[m], want[m])
+    assert not dq[:, :, :-last].any()
+    half = q[:, :, n // 2:n // 2 + 99]
+    ref.check("o", o[:, :, n // 2:n // 2 + 99], ref.attention(half.cpu(), k.cpu(), v.cpu())["o"])

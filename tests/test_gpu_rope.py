@@ -290,3 +290,16 @@ def test_wavelength_scaling_that_stretches_nothing_keeps_lengths(factor):
     if factor < 1e-3:  # frequencies of up to 1 / factor radians: their 2^-50 counts as many times
         bound = bound + 2.0 ** -50 * 350 / factor * 2 * x.double().abs().amax()
     ref.check("out", out, (value, bound))
+
+
+def test_more_threads_than_32_bits_count():
+    """8.6 GB, a thread per pair: the index arithmetic in 64 bits; in place, against calls on a part."""
+    n, d = (1 << 31) // 20 + 77, 40
+    x = torch.empty(1, 1, n, d, dtype=torch.bfloat16, device="cuda").normal_()
+    parts = {a: x[:, :, a:a + 200].clone() for a in (0, n // 2, n - 200)}
+    p = llsa.RopeParams.like(x)
+    llsa.llsa_rope(p, x, None, x, None)
+    for a, y in parts.items():
+        want = torch.empty_like(y)
+        llsa.llsa_rope(llsa.RopeParams.like(y, pos_offset=a), y, None, want, None)
+        assert torch.equal(x[:, :, a:a + 200], want), a
