@@ -705,3 +705,29 @@ def test_rows_behind_32_bits_on_the_tensor_cores():
     assert not dq[:, :, :-last].any()
     half = q[:, :, n // 2:n // 2 + 99]
     ref.check("o", o[:, :, n // 2:n // 2 + 99], ref.attention(half.cpu(), k.cpu(), v.cpu())["o"])
+
+
+@pytest.mark.parametrize("dtype,nq,d", [("bf16", 260, 64), ("fp32", 260, 64), ("bf16", 1, 64), ("bf16", 100, 256)])
+def test_two_captured_graphs_at_once(dtype, nq, d):
+    """Graphs with splits and workspaces of their own, replayed side by side."""
+    xs = [make(2, 8, 4, nq, 3000, d, dtype, seed=s) for s in (95, 96)]
+    want = [run(x, dtype=dtype) for x in xs]
+    cs = [{n: t.cuda() for n, t in x.items()} for x in xs]  # alive as long as the graphs
+    p = llsa.DenseParams.like(cs[0]["q"], cs[0]["k"])
+    graphs, got = [], []
+    for c in cs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            o, lse = llsa.dense_forward(p, c["q"], c["k"], c["v"])
+            got.append((o, lse, *llsa.dense_backward(p, c["q"], c["k"], c["v"], o, lse, c["dout"])))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    for outs, w in zip(got, want):
+        for t, n in zip(outs, ("o", "lse", "dq", "dk", "dv")):
+            assert torch.equal(t, w[n]), n
