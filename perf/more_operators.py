@@ -181,7 +181,8 @@ def prepare(case, seed):
     def rows(b, h, n, d):
         return torch.randn((b, h, n, d), generator=g, device="cuda").to(t)
 
-    st = {"case": case, "table": _table(case) if case["kind"] in ("rope", "step") else None}
+    st = {"case": case, "table": _table(case) if case["kind"] in ("rope", "step") else None,
+          "params": _params(case) if own else None}
     b, h, kv, d = case["batch"], case["heads"], case["kv_heads"], case["d"]
     if case["kind"] == "rope":
         n = case["n"]
@@ -424,19 +425,26 @@ def _grid_params(llsa, case, n, heads, kv_heads):
                                dtype=case["dtype"])
 
 
+def _params(case):
+    """The description of the call that a layer keeps."""
+    import hierarchical_sparse_attention_mean_gb300 as llsa
+    if case["kind"] == "rope":
+        return _grid_params(llsa, case, case["n"], case["heads"], case["kv_heads"])
+    if case["kind"] == "step":
+        return _grid_params(llsa, case, case["nq"], 2 * case["heads"], 2 * case["kv_heads"])
+    return llsa.DiffParams(case["batch"], case["heads"], case["nq"], case["nk"], case["d"], kv_heads=case["kv_heads"],
+                           causal=case["causal"], dtype=case["dtype"], lam_dtype=case["dtype"])
+
+
 def _call(st):
     import hierarchical_sparse_attention_mean_gb300 as llsa
-    case = st["case"]
+    case, p = st["case"], st["params"]
     if case["kind"] == "rope":
-        llsa.llsa_rope_grid(_grid_params(llsa, case, case["n"], case["heads"], case["kv_heads"]), st["q"], st["k"], st["q_out"],
-                            st["k_out"], pos=st["pos"], inverse=case["inverse"])
+        llsa.llsa_rope_grid(p, st["q"], st["k"], st["q_out"], st["k_out"], pos=st["pos"], inverse=case["inverse"])
         return st["q_out"], st["k_out"]
     if case["kind"] == "step":
-        rope = _grid_params(llsa, case, case["nq"], 2 * case["heads"], 2 * case["kv_heads"])
-        o = llsa.diff_attention(st["q"], st["k"], st["v"], st["lam"], causal=case["causal"], rope=rope)
+        o = llsa.diff_attention(st["q"], st["k"], st["v"], st["lam"], causal=case["causal"], rope=p)
         return (o.detach(), *torch.autograd.grad(o, (st["q"], st["k"], st["v"], st["lam"]), st["dout"]))
-    p = llsa.DiffParams(case["batch"], case["heads"], case["nq"], case["nk"], case["d"], kv_heads=case["kv_heads"],
-                        causal=case["causal"], dtype=case["dtype"], lam_dtype=case["dtype"])
     if case["kind"] == "forward":
         return llsa.diff_forward(p, st["q"], st["k"], st["v"], st["lam"], q_len=st["q_len"], k_len=st["k_len"])[:2]
     return llsa.diff_backward(p, st["q"], st["k"], st["v"], st["lam"], st["o"], st["o2"], st["lse"], st["dout"],
