@@ -9,8 +9,9 @@ device memory and streams. There is no CPU fallback: if the library is not
 built or the device is not a GB300, calls raise.
 
 Beside the sparse path: dense attention (``llsa_dense_fwd``, ``llsa_dense_bwd``;
-``dense_attention`` with autograd) and rotary positions (``llsa_rope``;
-``rotary``, or ``rope=`` of either attention).
+``dense_attention`` with autograd) and rotary positions on one or two axes
+(``llsa_rope``) or up to four (``llsa_rope_grid``): ``rotary``, or ``rope=`` of any
+attention.
 
 Method: "Trainable Log-linear Sparse Attention for Efficient Diffusion
 Transformers" (arXiv 2512.16615), as described on its Pith review page
@@ -42,6 +43,9 @@ OP_POOL, OP_SELECT, OP_FWD, OP_TRANSPOSE, OP_BWD, OP_DENSE_FWD, OP_DENSE_BWD = r
 LLSA_ROPE_HALF, LLSA_ROPE_INTERLEAVED = 0, 1
 _ROPE_LAYOUTS = {"half": LLSA_ROPE_HALF, "interleaved": LLSA_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3}
+LLSA_ROPE_SPAN_AXIS, LLSA_ROPE_SPAN_HEAD, LLSA_ROPE_SPAN_DEALT = 0, 1, 2
+_ROPE_SPANS = {"axis": LLSA_ROPE_SPAN_AXIS, "head": LLSA_ROPE_SPAN_HEAD, "dealt": LLSA_ROPE_SPAN_DEALT}
+ROPE_MAX_AXES = 4
 MAX_LEVELS = 8
 
 
@@ -85,6 +89,13 @@ class _RopeStrides(ctypes.Structure):
     _fields_ = [(n, ctypes.c_longlong * 3) for n in ("q", "k", "q_out", "k_out")]
 
 
+class _RopeGridParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "n", "d", "layout", "span", "axes")] + [
+        (n, ctypes.c_int * ROPE_MAX_AXES) for n in ("columns", "extent", "offset")] + [
+        (n, ctypes.c_int) for n in ("token_order", "pos_batched", "dtype", "scaling", "orig_len")] + [
+        (n, ctypes.c_double) for n in ("base", "factor", "low", "high", "amplitude")] + [("step", ctypes.c_double * ROPE_MAX_AXES)]
+
+
 def lib_path() -> str:
     return _LIB_PATH
 
@@ -115,6 +126,7 @@ def _load():
     lib.llsa_dense_fwd.argtypes = [DP] + [vp] * 8 + [sz, vp]
     lib.llsa_dense_bwd.argtypes = [DP] + [vp] * 12 + [sz, vp]
     lib.llsa_rope.argtypes = [ctypes.POINTER(_RopeParams), ctypes.POINTER(_RopeStrides)] + [vp] * 5 + [ctypes.c_int, vp]
+    lib.llsa_rope_grid.argtypes = [ctypes.POINTER(_RopeGridParams), ctypes.POINTER(_RopeStrides)] + [vp] * 5 + [ctypes.c_int, vp]
     lib.llsa_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     lib.llsa_strerror.argtypes = [ctypes.c_int]
     lib.llsa_strerror.restype = ctypes.c_char_p
@@ -301,6 +313,86 @@ def _rope_native(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, ord
     dtype, scaling = _choice(_DTYPES, dtype, "dtype"), _choice(_ROPE_SCALINGS, scaling, "scaling")
     return tuple(_RopeParams(batch, heads, kv_heads, n, d, rot_dim, layout, axes, width, order, offset, batched, dtype,
                              scaling, orig_len, *real) for batched in (0, 1))
+
+
+@dataclass(frozen=True)
+class RopeGridParams:
+    """Rotary positions on up to four axes; mirrors llsa_rope_grid_params of include/llsa.h.
+
+    The tokens are a grid of `extent` entries, the last axis fastest, or have their
+    positions in `pos` (extent None)."""
+    batch: int
+    heads: int
+    n: int
+    d: int
+    kv_heads: int = 0            # heads of k; 0: no k
+    columns: tuple = ()          # columns turned by each axis; one entry per axis
+    extent: tuple | None = None  # entries of the grid on each axis; None: positions are given
+    offset: tuple = ()           # position of the grid's first entry on each axis; (): 0
+    step: tuple = ()             # positions per entry on each axis; (): 1
+    span: str = "axis"           # frequencies: a ladder per "axis", one over the "head", or that one "dealt" in turn
+    layout: str = "half"         # pairs: "half" (i, i + h) or "interleaved" (2i, 2i + 1)
+    token_order: str = "raster"  # "raster", or "tile": the last two axes are a frame in tile order
+    base: float = 10000.0
+    scaling: str = "none"        # "none", "linear", "base" or "wavelength"
+    factor: float = 1.0
+    orig_len: int = 0            # "wavelength": positions the model was trained on
+    low: float = 1.0             # "wavelength": as RopeParams
+    high: float = 32.0
+    amplitude: float = 0.0       # 0: 1, or 0.1 ln(factor) + 1 for "wavelength" with a factor above 1
+    dtype: str = "bf16"
+
+    def __post_init__(self):
+        for name in ("columns", "extent", "offset", "step"):
+            value = getattr(self, name)
+            if value is not None:
+                self.__dict__[name] = tuple(value)
+        axes = len(self.columns)
+        if not 1 <= axes <= ROPE_MAX_AXES:
+            raise ValueError(f"columns must have 1 to {ROPE_MAX_AXES} entries, one per axis, not {axes}")
+        for name in ("extent", "offset", "step"):
+            value = getattr(self, name)
+            if value and len(value) != axes:
+                raise ValueError(f"{name} must have an entry for each of the {axes} axes, not {len(value)}")
+        self.__dict__["_c"] = _rope_grid_native(
+            self.batch, self.heads, self.kv_heads, self.n, self.d, self.columns, self.extent or (), self.offset,
+            tuple(float(x) for x in self.step), self.span, self.layout, self.token_order, self.dtype, self.scaling, self.orig_len,
+            float(self.base), float(self.factor), float(self.low), float(self.high), float(self.amplitude))
+
+    @property
+    def axes(self) -> int:
+        return len(self.columns)
+
+    def c(self, pos_batched: bool = False) -> _RopeGridParams:
+        return self._c[1 if pos_batched else 0]
+
+    def in_fp32(self) -> "RopeGridParams":
+        """The same positions for fp32 tensors."""
+        got = self.__dict__.get("_fp32")
+        if got is None:
+            got = self.__dict__["_fp32"] = replace(self, dtype="fp32")
+        return got
+
+    @staticmethod
+    def like(q, k=None, **kw) -> "RopeGridParams":
+        b, h, n, d = q.shape
+        return RopeGridParams(b, h, n, d, kv_heads=0 if k is None else k.shape[1], dtype=_dtype_name(q), **kw)
+
+
+@functools.lru_cache(maxsize=256)
+def _rope_grid_native(batch, heads, kv_heads, n, d, columns, extent, offset, step, span, layout, order, dtype, scaling, orig_len,
+                      *real):
+    """The C structures of equal parameters, for positions without and with a batch dimension."""
+    _int32(batch=batch, heads=heads, kv_heads=kv_heads, n=n, d=d, orig_len=orig_len)
+    for name, values in (("columns", columns), ("extent", extent), ("offset", offset)):
+        for value in values:
+            _int32(**{name: value})
+    four = [(ctypes.c_int * ROPE_MAX_AXES)(*x) for x in (columns, extent, offset)]
+    span, layout = _choice(_ROPE_SPANS, span, "span"), _choice(_ROPE_LAYOUTS, layout, "layout")
+    order = _choice(_ORDERS, order, "token_order")
+    dtype, scaling = _choice(_DTYPES, dtype, "dtype"), _choice(_ROPE_SCALINGS, scaling, "scaling")
+    return tuple(_RopeGridParams(batch, heads, kv_heads, n, d, layout, span, len(columns), *four, order, batched, dtype, scaling,
+                                 orig_len, *real, (ctypes.c_double * ROPE_MAX_AXES)(*step)) for batched in (0, 1))
 
 
 @dataclass(frozen=True)
@@ -540,6 +632,19 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
     k_out, in one launch. All may be strided views with contiguous columns, and
     a tensor may be its own output. pos: int32 [n], [n, axes], or either with a
     leading batch dimension. inverse: the negative angles (the gradient)."""
+    _rope_call("llsa_rope", p, q, k, q_out, k_out, pos, inverse, stream)
+
+
+def llsa_rope_grid(p: RopeGridParams, q, k, q_out, k_out, pos=None, inverse: bool = False, stream=None):
+    """Rotary positions on up to four axes: llsa_rope's call with the positions,
+    columns and frequencies of llsa_rope_grid_params. pos: int32 [n, axes] or
+    [batch, n, axes] ([n] or [batch, n] for one axis)."""
+    if pos is None and p.extent is None:
+        raise ValueError("without an extent positions must be given")
+    _rope_call("llsa_rope_grid", p, q, k, q_out, k_out, pos, inverse, stream)
+
+
+def _rope_call(entry, p, q, k, q_out, k_out, pos, inverse, stream):
     with _on(q, "q"):
         td, dev = _tok_dtype(p), q.get_device()
         shape = (p.batch, p.heads, p.n, p.d)
@@ -562,8 +667,8 @@ def llsa_rope(p: RopeParams, q, k, q_out, k_out, pos=None, inverse: bool = False
             elif shape != (p.n, p.axes):
                 raise ValueError(f"pos must have shape [n, axes] or [batch, n, axes], got {tuple(pos.shape)}")
             at = _like(pos, "pos", pos.shape, torch.int32, dev)
-        _check(_load().llsa_rope(p.c(batched), _rope_strides((sa, sb, sc, sd)), a, b, at, c, d, 1 if inverse else 0,
-                                 _stream(stream)), "llsa_rope")
+        _check(getattr(_load(), entry)(p.c(batched), _rope_strides((sa, sb, sc, sd)), a, b, at, c, d, 1 if inverse else 0,
+                                       _stream(stream)), entry)
 
 
 def llsa_get_status(stream=None) -> int:
@@ -741,7 +846,12 @@ def dense_backward(p: DenseParams, q, k, v, o, lse, dout, q_len=None, k_len=None
     return dq, dk, dv
 
 
-def _check_rope(p: RopeParams, q, k, name="rope"):
+def _turn(rope, *args, **kw):
+    """llsa_rope or llsa_rope_grid, by the parameters."""
+    (llsa_rope_grid if isinstance(rope, RopeGridParams) else llsa_rope)(rope, *args, **kw)
+
+
+def _check_rope(p, q, k, name="rope"):
     want = (p.batch, p.heads, p.n, p.d)
     if tuple(q.shape) != want or (k is not None and tuple(k.shape) != (p.batch, p.kv_heads, p.n, p.d)):
         raise ValueError(f"{name} is for q {want} and {p.kv_heads} heads of k, got q {tuple(q.shape)}"
@@ -789,7 +899,7 @@ def _autograd_function():
             q, k, v, *pos = ctx.saved_tensors
             dq, dk, dv = backward(ctx.p, q, k, v, _contiguous(do), ctx.b)
             if ctx.rope is not None:
-                llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos[0] if pos else None, inverse=True)
+                _turn(ctx.rope, dq, dk, dq, dk, pos=pos[0] if pos else None, inverse=True)
             return dq, dk, dv, None, None, None, None, None, None, None, None
 
     return LLSAFunction
@@ -800,7 +910,7 @@ def _rotated(rope, q, k, pos, inverse=False):
     _check_rope(rope, q, k)
     q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    llsa_rope(rope, _rope_view(q), None if k is None else _rope_view(k), q_out, k_out, pos=pos, inverse=inverse)
+    _turn(rope, _rope_view(q), None if k is None else _rope_view(k), q_out, k_out, pos=pos, inverse=inverse)
     return q_out, k_out
 
 
@@ -808,7 +918,7 @@ _FN = None
 
 
 def llsa_attention(q, k, v, block: int = 16, topk: int = 8, levels: int = 0, enrich_levels: int = -1,
-                   scale: float = 0.0, token_order: str = "tile", rope: RopeParams | None = None, pos=None):
+                   scale: float = 0.0, token_order: str = "tile", rope: RopeParams | RopeGridParams | None = None, pos=None):
     """Autograd entry point: o = LLSA(q, k, v). token_order "raster": q, k, v
     (and o, the gradients) are in the raster order of a square image, reordered
     inside the kernels. rope: rotary positions for q and k (with `pos`, or the
@@ -857,7 +967,7 @@ def _dense_functions():
                         raise ValueError(f"{name} must be {want}, got {t.dtype}")
                 q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
                 rope = rope.in_fp32()
-                llsa_rope(rope, q, k, q, k, pos=pos)
+                _turn(rope, q, k, q, k, pos=pos)
             else:
                 q, k = _rotated(rope, q, k, pos)
             v = _contiguous(v)
@@ -873,7 +983,7 @@ def _dense_functions():
             q, k, v, o, lse, q_len, k_len, pos = ctx.saved_tensors
             dq, dk, dv = dense_backward(ctx.p, q, k, v, o, lse, _contiguous(do.to(o.dtype)), q_len, k_len)
             if ctx.rope is not None:
-                llsa_rope(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
+                _turn(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
             if dq.dtype != ctx.dtype:
                 dq, dk, dv = dq.to(ctx.dtype), dk.to(ctx.dtype), dv.to(ctx.dtype)
             return dq, dk, dv, None, None, None, None, None, None
@@ -908,7 +1018,7 @@ def _dense_fns():
 
 
 def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=None, k_len=None,
-                    rope: RopeParams | None = None, pos=None):
+                    rope: RopeParams | RopeGridParams | None = None, pos=None):
     """Autograd entry point of dense attention: q [batch, heads, nq, d] over k, v
     [batch, kv_heads, nk, d]. q_len, k_len: int32 [batch] valid tokens of a
     padded batch. rope: rotary positions for q and k of the same tokens; the turned
@@ -922,7 +1032,7 @@ def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=Non
     return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)
 
 
-def rotary(q, k=None, rope: RopeParams | None = None, pos=None):
+def rotary(q, k=None, rope: RopeParams | RopeGridParams | None = None, pos=None):
     """Autograd entry point of rotary positions: (q, k) turned, head-major and
     contiguous (k None: q alone). Strided inputs are read in place."""
     if rope is None:

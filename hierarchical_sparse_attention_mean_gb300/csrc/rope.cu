@@ -20,15 +20,12 @@
 
 #include <algorithm>
 
-#include "entry.h"
-#include "internal.h"
+#include "rope.cuh"
 
 namespace llsa {
 namespace {
 
-constexpr int kMaxPairs = 128;  // d <= 256
-constexpr int kThreads = 256;
-constexpr double kPi = 3.14159265358979323846;
+constexpr int kMaxPairs = kRopeMaxPairs, kThreads = kRopeThreads;
 
 struct RopeArgs {
     const void* in[2];
@@ -62,21 +59,6 @@ __device__ __forceinline__ void turn(const RopeArgs& a, int pos, int pair, float
     c *= a.amplitude;
     s *= a.amplitude * a.sign;
 }
-
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ float from_float<float>(float x) { return x; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
-
-template <typename T>
-union Vec {
-    uint4 u;
-    T e[16 / sizeof(T)];
-};
 
 // One thread: unit u of one token, for heads h0 .. h0 + heads_per_thread - 1 of
 // the q heads followed by the k heads.
@@ -201,17 +183,8 @@ int derive_rope(const llsa_rope_params* p, RopeArgs* a) {
     }
     for (int i = 0; i < h; i++) {
         double w = pow(base, -2.0 * i / seg);
-        if (p->scaling == LLSA_ROPE_SCALE_LINEAR) w /= p->factor;
-        if (p->scaling == LLSA_ROPE_SCALE_WAVELENGTH) {
-            const double turns = p->orig_len * w / (2 * kPi);
-            const double g = std::min(1.0, std::max(0.0, (turns - p->low) / (p->high - p->low)));
-            w *= g + (1 - g) / p->factor;
-        }
-        double f = w / (2 * kPi);
-        f -= floor(f);
-        if (!(f >= 0.0 && f < 1.0)) return LLSA_ERR_INVALID_ARG;  // not a number
-        // below 2^-11 the fraction has bits behind 2^-64: rounded there
-        a->freq[i] = (uint64_t)(f * 18446744073709551616.0 + (f < 4.8828125e-4 ? 0.5 : 0.0));
+        w = rope_scaled(*p, w);
+        if (!rope_turns(w, &a->freq[i])) return LLSA_ERR_INVALID_ARG;
     }
     // stretched positions ask for sharper scores; the logarithm would turn them flat and at last around below 1
     if (p->scaling == LLSA_ROPE_SCALE_WAVELENGTH && p->factor > 1.0) amplitude = 0.1 * log(p->factor) + 1.0;
@@ -250,25 +223,6 @@ int check_rope(const llsa_rope_params* p, int has_pos) {
             while (side < p->width) side *= 4;
             if (side != p->width || side * side != p->n) return LLSA_ERR_SHAPE;
         }
-    }
-    return LLSA_OK;
-}
-
-// The strides of one tensor: the caller's, or the contiguous ones. An output's
-// rows must not lie over one another.
-int take_strides(const long long* given, const llsa_rope_params* p, int heads, bool output, long long* out) {
-    const long long want = p->dtype == LLSA_DTYPE_BF16 ? 8 : 4;  // elements in 16 bytes
-    if (!given || (given[0] == 0 && given[1] == 0 && given[2] == 0)) {
-        out[0] = (long long)heads * p->n * p->d;
-        out[1] = (long long)p->n * p->d;
-        out[2] = p->d;
-        return LLSA_OK;
-    }
-    const int extent[3] = {p->batch, heads, p->n};
-    for (int i = 0; i < 3; i++) {
-        out[i] = extent[i] > 1 ? given[i] : 0;  // one entry: the stride is never walked
-        if (out[i] % want != 0) return LLSA_ERR_ALIGN;
-        if (output && extent[i] > 1 && out[i] == 0) return LLSA_ERR_INVALID_ARG;
     }
     return LLSA_OK;
 }
@@ -330,10 +284,10 @@ extern "C" int llsa_rope(const llsa_rope_params* p, const llsa_rope_strides* str
     if (p->heads > 0) LLSA_TRY(check_ptrs({q, q_out}));
     if (p->kv_heads > 0) LLSA_TRY(check_ptrs({k, k_out}));
     if (pos && (reinterpret_cast<uintptr_t>(pos) & 3u)) return LLSA_ERR_ALIGN;
-    LLSA_TRY(take_strides(strides ? strides->q : nullptr, p, p->heads, false, a.in_stride[0]));
-    LLSA_TRY(take_strides(strides ? strides->k : nullptr, p, p->kv_heads, false, a.in_stride[1]));
-    LLSA_TRY(take_strides(strides ? strides->q_out : nullptr, p, p->heads, true, a.out_stride[0]));
-    LLSA_TRY(take_strides(strides ? strides->k_out : nullptr, p, p->kv_heads, true, a.out_stride[1]));
+    LLSA_TRY(rope_strides(strides ? strides->q : nullptr, *p, p->heads, false, a.in_stride[0]));
+    LLSA_TRY(rope_strides(strides ? strides->k : nullptr, *p, p->kv_heads, false, a.in_stride[1]));
+    LLSA_TRY(rope_strides(strides ? strides->q_out : nullptr, *p, p->heads, true, a.out_stride[0]));
+    LLSA_TRY(rope_strides(strides ? strides->k_out : nullptr, *p, p->kv_heads, true, a.out_stride[1]));
     // a tensor may be its own output only if every element goes back to its own place
     if (p->heads > 0 && q == q_out && memcmp(a.in_stride[0], a.out_stride[0], sizeof(a.in_stride[0])) != 0)
         return LLSA_ERR_INVALID_ARG;

@@ -428,6 +428,61 @@ typedef struct llsa_rope_strides {
 int llsa_rope(const llsa_rope_params *p, const llsa_rope_strides *strides, const void *q, const void *k,
               const int32_t *pos, void *q_out, void *k_out, int inverse, void *stream);
 
+/* Rotary positions on up to four axes (time, height and width of a clip; text
+ * mixed with frames), in one launch.
+ *
+ * Axis a turns columns[a] columns of a head; the columns behind all of them are
+ * copied. The turn of a pair, its layouts, scalings and accuracy are llsa_rope's, with
+ * the angle position_a * step[a] * w; the fraction of a turn is then good to
+ * |position| * max(1, step[a] * w) * 2^-54. With c = columns[a], R the sum of all
+ * columns and T = R / 2 pairs, `span` says which columns and frequencies an axis has:
+ *   LLSA_ROPE_SPAN_AXIS   the next c columns, paired among themselves ((2i, 2i + 1),
+ *                         or (i, i + c / 2)), pair i with w = base^(-2i / c)
+ *   LLSA_ROPE_SPAN_HEAD   the next c / 2 of the head's pairs: all R columns are paired
+ *                         ((2i, 2i + 1), or (i, i + T)), pair i with w = base^(-2i / R)
+ *   LLSA_ROPE_SPAN_DEALT  the same pairs and frequencies, dealt to the axes in turn
+ *                         (pair 0 to axis 0, pair 1 to axis 1, ...); an axis that has its
+ *                         c / 2 pairs is passed over
+ * llsa_rope with equal segments is SPAN_AXIS with equal columns; every factor means
+ * what it means there, SCALE_BASE with seg = c (SPAN_AXIS) or R.
+ *
+ *   pos          : int32 [n][axes] on the device, or [batch][n][axes] with
+ *                  pos_batched; NULL: the tokens are a grid of extent[0] x extent[1] x
+ *                  ... entries, n in all, the last axis fastest, and a token's position
+ *                  on axis a is its place there + offset[a]. Under LLSA_ORDER_TILE the
+ *                  last two axes are a square frame whose tokens are in tile order
+ *                  (llsa_reorder with B = 16; sides a power of 4).
+ *   q, k, q_out, k_out, strides, inverse, limits : as in llsa_rope. */
+enum { LLSA_ROPE_SPAN_AXIS = 0, LLSA_ROPE_SPAN_HEAD = 1, LLSA_ROPE_SPAN_DEALT = 2 };
+#define LLSA_ROPE_MAX_AXES 4
+
+typedef struct llsa_rope_grid_params {
+    int batch;
+    int heads;          /* heads of q */
+    int kv_heads;       /* heads of k; 0: no k */
+    int n;              /* tokens per slice */
+    int d;              /* head dimension: multiple of 8, at most 256 */
+    int layout;         /* LLSA_ROPE_HALF or LLSA_ROPE_INTERLEAVED */
+    int span;           /* LLSA_ROPE_SPAN_* */
+    int axes;           /* 1 to LLSA_ROPE_MAX_AXES; entries behind them are not read */
+    int columns[LLSA_ROPE_MAX_AXES]; /* even, at least 2, at most d in all */
+    int extent[LLSA_ROPE_MAX_AXES];  /* of the grid; ignored with pos */
+    int offset[LLSA_ROPE_MAX_AXES];  /* position of the grid's first entry; ignored with pos */
+    int token_order;    /* LLSA_ORDER_RASTER or LLSA_ORDER_TILE (at least 2 axes); ignored with pos */
+    int pos_batched;    /* pos holds batch * n rows instead of n */
+    int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int scaling;        /* LLSA_ROPE_SCALE_* */
+    int orig_len;       /* WAVELENGTH: positions that the model was trained on */
+    double base;        /* > 1 */
+    double factor;      /* > 0 (ignored by SCALE_NONE) */
+    double low, high;   /* WAVELENGTH: low < high */
+    double amplitude;   /* 0 selects the default; finite in fp32 */
+    double step[LLSA_ROPE_MAX_AXES]; /* positions per entry, > 0; 0 selects 1 */
+} llsa_rope_grid_params;
+
+int llsa_rope_grid(const llsa_rope_grid_params *p, const llsa_rope_strides *strides, const void *q, const void *k,
+                   const int32_t *pos, void *q_out, void *k_out, int inverse, void *stream);
+
 /* Reads (after synchronising `stream`) and clears the device status word of
  * the current device: LLSA_OK, LLSA_ERR_TIMEOUT or LLSA_ERR_BAD_INDEX. */
 int llsa_get_status(void *stream, int *device_status);
