@@ -9,7 +9,8 @@ device memory and streams. There is no CPU fallback: if the library is not
 built or the device is not a GB300, calls raise.
 
 Beside the sparse path: dense attention (``llsa_dense_fwd``, ``llsa_dense_bwd``;
-``dense_attention`` with autograd) and rotary positions on one or two axes
+``dense_attention`` with autograd), differential attention (``llsa_diff_fwd``,
+``llsa_diff_bwd``; ``diff_attention`` with autograd) and rotary positions on one or two axes
 (``llsa_rope``) or up to four (``llsa_rope_grid``): ``rotary``, or ``rope=`` of any
 attention.
 
@@ -39,7 +40,7 @@ LLSA_ENRICH_ALLK = 2
 _RULES = {"top1": LLSA_ENRICH_TOP1, "ancestor": LLSA_ENRICH_ANCESTOR, "allk": LLSA_ENRICH_ALLK}
 LLSA_ORDER_TILE, LLSA_ORDER_RASTER = 0, 1
 _ORDERS = {"tile": LLSA_ORDER_TILE, "raster": LLSA_ORDER_RASTER}
-OP_POOL, OP_SELECT, OP_FWD, OP_TRANSPOSE, OP_BWD, OP_DENSE_FWD, OP_DENSE_BWD = range(7)
+OP_POOL, OP_SELECT, OP_FWD, OP_TRANSPOSE, OP_BWD, OP_DENSE_FWD, OP_DENSE_BWD, OP_DIFF_FWD, OP_DIFF_BWD = range(9)
 LLSA_ROPE_HALF, LLSA_ROPE_INTERLEAVED = 0, 1
 _ROPE_LAYOUTS = {"half": LLSA_ROPE_HALF, "interleaved": LLSA_ROPE_INTERLEAVED}
 _ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "wavelength": 3}
@@ -76,6 +77,11 @@ class _Sizes(ctypes.Structure):
 
 class _DenseParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d", "dtype", "causal")] + [
+        ("scale", ctypes.c_float)]
+
+
+class _DiffParams(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d", "dtype", "lam_dtype", "causal")] + [
         ("scale", ctypes.c_float)]
 
 
@@ -125,6 +131,11 @@ def _load():
     lib.llsa_dense_workspace_bytes.restype = sz
     lib.llsa_dense_fwd.argtypes = [DP] + [vp] * 8 + [sz, vp]
     lib.llsa_dense_bwd.argtypes = [DP] + [vp] * 12 + [sz, vp]
+    FP = ctypes.POINTER(_DiffParams)
+    lib.llsa_diff_workspace_bytes.argtypes = [FP, ctypes.c_int]
+    lib.llsa_diff_workspace_bytes.restype = sz
+    lib.llsa_diff_fwd.argtypes = [FP] + [vp] * 10 + [sz, vp]
+    lib.llsa_diff_bwd.argtypes = [FP] + [vp] * 15 + [sz, vp]
     lib.llsa_rope.argtypes = [ctypes.POINTER(_RopeParams), ctypes.POINTER(_RopeStrides)] + [vp] * 5 + [ctypes.c_int, vp]
     lib.llsa_rope_grid.argtypes = [ctypes.POINTER(_RopeGridParams), ctypes.POINTER(_RopeStrides)] + [vp] * 5 + [ctypes.c_int, vp]
     lib.llsa_get_status.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
@@ -196,10 +207,10 @@ def _choice(table, value, name):
     return got
 
 
-def _dtype_name(t):
+def _dtype_name(t, what="q"):
     name = {torch.bfloat16: "bf16", torch.float32: "fp32"}.get(t.dtype)
     if name is None:
-        raise ValueError("q must be bfloat16 or float32")
+        raise ValueError(f"{what} must be bfloat16 or float32")
     return name
 
 
@@ -257,6 +268,62 @@ def _dense_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, scale):
 def _dense_params(q, k, dtype, causal, scale):
     b, h, n, d = q
     return DenseParams(b, h, n, k[2], d, kv_heads=k[1], causal=causal, dtype=dtype, scale=scale)
+
+
+@dataclass(frozen=True)
+class DiffParams:
+    """A differential-attention problem; mirrors llsa_diff_params of include/llsa.h."""
+    batch: int
+    heads: int                 # differential heads: q has twice as many
+    nq: int
+    nk: int
+    d: int                     # columns of q and k; v and o have twice as many
+    kv_heads: int = 0          # value heads, and key heads of each map; 0: as many as heads
+    causal: bool = False       # the last query sees the last key
+    dtype: str = "bf16"        # "bf16" or "fp32"
+    lam_dtype: str = ""        # of lam and its gradient; "": dtype
+    scale: float = 0.0         # 0: 1/sqrt(d)
+
+    def __post_init__(self):
+        self.__dict__.update(_diff_native(self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, bool(self.causal),
+                                          self.dtype, self.lam_dtype or self.dtype, float(self.scale)))
+
+    def __reduce__(self):  # copies and pickles build their own C structure
+        return DiffParams, (self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, self.causal, self.dtype,
+                            self.lam_dtype, self.scale)
+
+    def c(self) -> _DiffParams:
+        return self._c
+
+    @staticmethod
+    def like(q, k, lam=None, causal: bool = False, scale: float = 0.0) -> "DiffParams":
+        """The parameters of a call on q, k and lam (equal calls share one object)."""
+        return _diff_params(tuple(q.shape), tuple(k.shape), _dtype_name(q), "" if lam is None else _dtype_name(lam, "lam"),
+                            bool(causal), float(scale))
+
+    def shapes(self):
+        """Shapes of q (and dq), of k (and dk), of v (and dv), of o (and o2, dout) and of lse."""
+        return self._shapes
+
+
+@functools.lru_cache(maxsize=256)
+def _diff_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, lam_dtype, scale):
+    """What equal parameters share: the C structure, the workspace sizes, the tensors' shapes."""
+    _int32(batch=batch, heads=heads, kv_heads=kv_heads, nq=nq, nk=nk, d=d)
+    c = _DiffParams(batch, heads, kv_heads, nq, nk, d, _choice(_DTYPES, dtype, "dtype"), _choice(_DTYPES, lam_dtype, "lam_dtype"),
+                    1 if causal else 0, scale)
+    kv = kv_heads or heads
+    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {}, "_lam": torch.bfloat16 if lam_dtype == "bf16" else torch.float32,
+            "_shapes": ((batch, 2 * heads, nq, d), (batch, 2 * kv, nk, d), (batch, kv, nk, 2 * d), (batch, heads, nq, 2 * d),
+                        (batch, 2 * heads, nq))}
+
+
+@functools.lru_cache(maxsize=256)
+def _diff_params(q, k, dtype, lam_dtype, causal, scale):
+    b, h, n, d = q
+    if h % 2 or k[1] % 2:
+        raise ValueError(f"q and k must have two heads for each differential one, got {h} and {k[1]}")
+    return DiffParams(b, h // 2, n, k[2], d, kv_heads=k[1] // 2, causal=causal, dtype=dtype, lam_dtype=lam_dtype, scale=scale)
 
 
 @dataclass(frozen=True)
@@ -595,6 +662,40 @@ def llsa_dense_bwd(p: DenseParams, q, k, v, o, lse, dout, dq, dk, dv, q_len=None
                                       _like(dv, "dv", sk, td, dev), w, wb, _stream(stream)), "llsa_dense_bwd")
 
 
+def diff_workspace_bytes(p: DiffParams, op: int) -> int:
+    """Workspace of llsa_diff_fwd (OP_DIFF_FWD) or llsa_diff_bwd (OP_DIFF_BWD)."""
+    got = p._ws.get(op)
+    if got is None:
+        got = p._ws[op] = int(_load().llsa_diff_workspace_bytes(p._ref, op))
+    return got
+
+
+def llsa_diff_fwd(p: DiffParams, q, k, v, lam, o, o2, lse, q_len=None, k_len=None, ws=None, stream=None):
+    """Differential attention: o, o2 (None: not kept) and lse of q over k, v (llsa_diff_fwd of include/llsa.h)."""
+    with _on(q, "q"):
+        td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
+        w, wb = _ws_on(ws, dev)
+        _check(_load().llsa_diff_fwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev), _like(v, "v", sv, td, dev),
+                                     _like(lam, "lam", (p.heads,), p._lam, dev), ql, kl, _like(o, "o", so, td, dev),
+                                     None if o2 is None else _like(o2, "o2", so, td, dev),
+                                     _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_diff_fwd")
+
+
+def llsa_diff_bwd(p: DiffParams, q, k, v, lam, o, o2, lse, dout, dq, dk, dv, dlam, q_len=None, k_len=None, ws=None, stream=None):
+    """Gradients of differential attention (llsa_diff_bwd of include/llsa.h)."""
+    with _on(q, "q"):
+        td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
+        w, wb = _ws_on(ws, dev)
+        _check(_load().llsa_diff_bwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev), _like(v, "v", sv, td, dev),
+                                     _like(lam, "lam", (p.heads,), p._lam, dev), _like(o, "o", so, td, dev),
+                                     _like(o2, "o2", so, td, dev), _like(lse, "lse", sl, torch.float32, dev),
+                                     _like(dout, "dout", so, td, dev), ql, kl, _like(dq, "dq", sq, td, dev),
+                                     _like(dk, "dk", sk, td, dev), _like(dv, "dv", sv, td, dev),
+                                     _like(dlam, "dlam", (p.heads,), p._lam, dev), w, wb, _stream(stream)), "llsa_diff_bwd")
+
+
 def _strided(t, name, shape, dtype, device):
     """Pointer of a [batch, heads, n, d] tensor whose columns are contiguous, and
     its batch, head and token strides (None: contiguous throughout)."""
@@ -809,9 +910,9 @@ def backward(p: Params, q, k, v, dout, b: Buffers, dq=None, dk=None, dv=None, st
     return dq, dk, dv
 
 
-def _dense_ws(p: DenseParams, op: int, device):
+def _dense_ws(p, op: int, device):
     """The workspace of one call (None where it needs none)."""
-    need = dense_workspace_bytes(p, op)
+    need = (diff_workspace_bytes if isinstance(p, DiffParams) else dense_workspace_bytes)(p, op)
     if need == 0:
         return None
     return torch.empty(need, dtype=torch.uint8, device=device)
@@ -844,6 +945,34 @@ def dense_backward(p: DenseParams, q, k, v, o, lse, dout, q_len=None, k_len=None
         ws = _dense_ws(p, OP_DENSE_BWD, q.device) if ws is None else ws
         llsa_dense_bwd(p, q, k, v, o, lse, dout, dq, dk, dv, q_len, k_len, ws, stream)
     return dq, dk, dv
+
+
+def diff_forward(p: DiffParams, q, k, v, lam, q_len=None, k_len=None, o=None, o2=None, lse=None, ws=None, stream=None,
+                 backward: bool = False):
+    """Differential attention of q over k, v. Returns (o, lse, o2); what is not given is
+    allocated here, on `stream` (None: the current one), o2 only if `backward` says
+    that diff_backward() will need it (else it is None)."""
+    with _under(stream, q.device):
+        so, sl = p.shapes()[3:]
+        o = torch.empty(so, dtype=q.dtype, device=q.device) if o is None else o
+        o2 = torch.empty(so, dtype=q.dtype, device=q.device) if o2 is None and backward else o2
+        lse = torch.empty(sl, dtype=torch.float32, device=q.device) if lse is None else lse
+        ws = _dense_ws(p, OP_DIFF_FWD, q.device) if ws is None else ws
+        llsa_diff_fwd(p, q, k, v, lam, o, o2, lse, q_len, k_len, ws, stream)
+    return o, lse, o2
+
+
+def diff_backward(p: DiffParams, q, k, v, lam, o, o2, lse, dout, q_len=None, k_len=None, dq=None, dk=None, dv=None, dlam=None,
+                  ws=None, stream=None):
+    """Gradients of diff_forward(). Returns (dq, dk, dv, dlam)."""
+    with _under(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        dlam = torch.empty_like(lam) if dlam is None else dlam
+        ws = _dense_ws(p, OP_DIFF_BWD, q.device) if ws is None else ws
+        llsa_diff_bwd(p, q, k, v, lam, o, o2, lse, dout, dq, dk, dv, dlam, q_len, k_len, ws, stream)
+    return dq, dk, dv, dlam
 
 
 def _turn(rope, *args, **kw):
@@ -949,6 +1078,24 @@ def _wide(q, k):
             or (d <= _WIDE_COLUMNS and q.numel() * nk <= _WIDE_PAIRS * d))  # pairs of a query and a key
 
 
+def _positioned(rope, q, k, v, pos):
+    """Contiguous q, k, v with the positions of `rope` (None: none) turned in, and the
+    parameters that turn their gradients back."""
+    if rope is None:
+        q, k = _contiguous(q), _contiguous(k)
+    elif _wide(q, k):
+        _check_rope(rope, q, k)
+        for name, t, want in (("q", q, _tok_dtype(rope)), ("k", k, q.dtype), ("v", v, q.dtype)):
+            if t.dtype != want:
+                raise ValueError(f"{name} must be {want}, got {t.dtype}")
+        q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
+        rope = rope.in_fp32()
+        _turn(rope, q, k, q, k, pos=pos)
+    else:
+        q, k = _rotated(rope, q, k, pos)
+    return q, k, _contiguous(v), rope
+
+
 def _dense_functions():
     from torch.autograd.function import once_differentiable
 
@@ -958,19 +1105,7 @@ def _dense_functions():
         @staticmethod
         def forward(ctx, q, k, v, causal, scale, q_len, k_len, rope, pos):
             ctx.dtype = dtype = q.dtype
-            if rope is None:
-                q, k = _contiguous(q), _contiguous(k)
-            elif _wide(q, k):
-                _check_rope(rope, q, k)
-                for name, t, want in (("q", q, _tok_dtype(rope)), ("k", k, dtype), ("v", v, dtype)):
-                    if t.dtype != want:
-                        raise ValueError(f"{name} must be {want}, got {t.dtype}")
-                q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
-                rope = rope.in_fp32()
-                _turn(rope, q, k, q, k, pos=pos)
-            else:
-                q, k = _rotated(rope, q, k, pos)
-            v = _contiguous(v)
+            q, k, v, rope = _positioned(rope, q, k, v, pos)
             p = DenseParams.like(q, k, causal=causal, scale=scale)
             o, lse = dense_forward(p, q, k, v, q_len, k_len)
             ctx.p, ctx.rope = p, rope
@@ -988,6 +1123,31 @@ def _dense_functions():
                 dq, dk, dv = dq.to(ctx.dtype), dk.to(ctx.dtype), dv.to(ctx.dtype)
             return dq, dk, dv, None, None, None, None, None, None
 
+    class DiffFunction(torch.autograd.Function):
+        """Differentiable differential attention, with rotary positions if asked."""
+
+        @staticmethod
+        def forward(ctx, q, k, v, lam, causal, scale, q_len, k_len, rope, pos):
+            ctx.dtype = dtype = q.dtype
+            q, k, v, rope = _positioned(rope, q, k, v, pos)
+            lam = _contiguous(lam)
+            p = DiffParams.like(q, k, lam, causal=causal, scale=scale)
+            o, lse, o2 = diff_forward(p, q, k, v, lam, q_len, k_len, backward=any(ctx.needs_input_grad))
+            ctx.p, ctx.rope = p, rope
+            ctx.save_for_backward(q, k, v, lam, o, o2, lse, q_len, k_len, pos)
+            return o.to(dtype)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, do):
+            q, k, v, lam, o, o2, lse, q_len, k_len, pos = ctx.saved_tensors
+            dq, dk, dv, dlam = diff_backward(ctx.p, q, k, v, lam, o, o2, lse, _contiguous(do.to(o.dtype)), q_len, k_len)
+            if ctx.rope is not None:
+                _turn(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
+            if dq.dtype != ctx.dtype:
+                dq, dk, dv = dq.to(ctx.dtype), dk.to(ctx.dtype), dv.to(ctx.dtype)
+            return dq, dk, dv, dlam, None, None, None, None, None, None
+
     class RotaryFunction(torch.autograd.Function):
         """Differentiable rotary positions of q and k."""
 
@@ -1004,7 +1164,7 @@ def _dense_functions():
             dq, dk = _rotated(ctx.rope, dq, dk, pos, inverse=True)
             return dq, dk, None, None
 
-    return DenseFunction, RotaryFunction
+    return DenseFunction, RotaryFunction, DiffFunction
 
 
 _DENSE_FNS = None
@@ -1030,6 +1190,19 @@ def dense_attention(q, k, v, causal: bool = False, scale: float = 0.0, q_len=Non
     A backward pass that a CUDA graph captures wants leaves made inside the capture
     (x.detach().requires_grad_()), as every autograd function does."""
     return _dense_fns()[0].apply(q, k, v, causal, scale, q_len, k_len, rope, pos)
+
+
+def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len=None, k_len=None,
+                   rope: RopeParams | RopeGridParams | None = None, pos=None):
+    """Autograd entry point of differential attention: o [batch, heads, nq, 2d] =
+    (softmax(q1 k1) - lam softmax(q2 k2)) v. q [batch, 2 heads, nq, d] and k [batch,
+    2 kv_heads, nk, d] hold the first maps' heads, then the second maps'; v [batch,
+    kv_heads, nk, 2d]; lam [heads], bf16 or fp32 whatever the type of the others, or
+    one number for all heads. q_len, k_len, rope, pos, roundings and captured backward
+    passes: as dense_attention (rope is for the heads of q and k as they are)."""
+    if isinstance(lam, torch.Tensor) and lam.numel() == 1 and q.shape[1] != 2:
+        lam = lam.reshape(1).expand(q.shape[1] // 2)
+    return _dense_fns()[2].apply(q, k, v, lam, causal, scale, q_len, k_len, rope, pos)
 
 
 def rotary(q, k=None, rope: RopeParams | RopeGridParams | None = None, pos=None):

@@ -114,6 +114,11 @@ __device__ __forceinline__ DenseWork dense_work(const DenseArgs& a, int id, int 
     return w;
 }
 
+int derive_dense(const llsa_dense_params* p, DenseShape* s);  // checks the parameters
+DenseArgs dense_args(const DenseShape& s);                     // what a launch needs besides its pointers
+inline int dense_check_lens(const int32_t* q_len, const int32_t* k_len) {
+    return (reinterpret_cast<uintptr_t>(q_len) | reinterpret_cast<uintptr_t>(k_len)) & 3u ? LLSA_ERR_ALIGN : LLSA_OK;
+}
 size_t dense_fwd_workspace(const DenseShape& s);
 size_t dense_bwd_workspace(const DenseShape& s);
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);

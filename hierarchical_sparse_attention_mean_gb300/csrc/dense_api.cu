@@ -181,6 +181,56 @@ dense_nothing_kernel(const __grid_constant__ DenseArgs a, uint4* x, uint4* y, lo
     for (long long i = first; i < rows; i += step) lse[i] = -INFINITY;
 }
 
+// Which kernels take a call.
+enum class Path { kNone, kFew, kKeys, kTc, kSplit, kSimt };
+
+Path fwd_path(const DenseShape& s) {
+    return s.R == 0 || s.nk == 0      ? Path::kNone
+           : dense_few_supported(s)   ? Path::kFew
+           : dense_keys_supported(s)  ? Path::kKeys
+           : dense_tc_supported(s)    ? Path::kTc
+           : dense_split_supported(s) ? Path::kSplit
+                                      : Path::kSimt;
+}
+Path bwd_path(const DenseShape& s) {
+    return s.R == 0 || s.nk == 0        ? Path::kNone
+           : dense_few_bwd_supported(s) ? Path::kFew
+           : dense_tc_supported(s)      ? Path::kTc
+           : dense_split_supported(s)   ? Path::kSplit
+                                        : Path::kSimt;
+}
+
+DenseSplit fwd_split(const DenseShape& s) {
+    switch (fwd_path(s)) {
+        case Path::kNone:
+        case Path::kKeys: return {1, s.nk};
+        case Path::kFew: return dense_few_split(s);
+        case Path::kTc: return dense_tc_fwd_split(s);
+        case Path::kSplit: return dense_split_fwd_split(s);
+        default: return dense_simt_fwd_split(s);
+    }
+}
+DenseSplit dq_split(const DenseShape& s) {
+    switch (bwd_path(s)) {
+        case Path::kNone: return {1, s.nk};
+        case Path::kFew: return dense_few_split(s);
+        case Path::kTc: return dense_tc_dq_split(s);
+        case Path::kSplit: return dense_split_fwd_split(s);
+        default: return dense_simt_fwd_split(s);
+    }
+}
+DenseSplit dkv_split(const DenseShape& s) {
+    switch (bwd_path(s)) {
+        case Path::kNone:
+        case Path::kFew: return {1, s.nk};  // dk, dv: of the blocks that own the keys
+        case Path::kTc: return dense_tc_dkv_split(s);
+        case Path::kSplit: return dense_split_dkv_split(s);
+        default: return dense_simt_dkv_split(s);
+    }
+}
+
+}  // namespace
+
 int derive_dense(const llsa_dense_params* p, DenseShape* s) {
     if (!p) return LLSA_ERR_INVALID_ARG;
     if (p->batch < 0 || p->heads < 0 || p->kv_heads < 0 || p->nq < 0 || p->nk < 0) return LLSA_ERR_INVALID_ARG;
@@ -232,61 +282,6 @@ DenseArgs dense_args(const DenseShape& s) {
     a.test_flags = test_flags();
     return a;
 }
-
-int check_lens(const int32_t* q_len, const int32_t* k_len) {
-    if ((reinterpret_cast<uintptr_t>(q_len) | reinterpret_cast<uintptr_t>(k_len)) & 3u) return LLSA_ERR_ALIGN;
-    return LLSA_OK;
-}
-
-// Which kernels take a call.
-enum class Path { kNone, kFew, kKeys, kTc, kSplit, kSimt };
-
-Path fwd_path(const DenseShape& s) {
-    return s.R == 0 || s.nk == 0      ? Path::kNone
-           : dense_few_supported(s)   ? Path::kFew
-           : dense_keys_supported(s)  ? Path::kKeys
-           : dense_tc_supported(s)    ? Path::kTc
-           : dense_split_supported(s) ? Path::kSplit
-                                      : Path::kSimt;
-}
-Path bwd_path(const DenseShape& s) {
-    return s.R == 0 || s.nk == 0        ? Path::kNone
-           : dense_few_bwd_supported(s) ? Path::kFew
-           : dense_tc_supported(s)      ? Path::kTc
-           : dense_split_supported(s)   ? Path::kSplit
-                                        : Path::kSimt;
-}
-
-DenseSplit fwd_split(const DenseShape& s) {
-    switch (fwd_path(s)) {
-        case Path::kNone:
-        case Path::kKeys: return {1, s.nk};
-        case Path::kFew: return dense_few_split(s);
-        case Path::kTc: return dense_tc_fwd_split(s);
-        case Path::kSplit: return dense_split_fwd_split(s);
-        default: return dense_simt_fwd_split(s);
-    }
-}
-DenseSplit dq_split(const DenseShape& s) {
-    switch (bwd_path(s)) {
-        case Path::kNone: return {1, s.nk};
-        case Path::kFew: return dense_few_split(s);
-        case Path::kTc: return dense_tc_dq_split(s);
-        case Path::kSplit: return dense_split_fwd_split(s);
-        default: return dense_simt_fwd_split(s);
-    }
-}
-DenseSplit dkv_split(const DenseShape& s) {
-    switch (bwd_path(s)) {
-        case Path::kNone:
-        case Path::kFew: return {1, s.nk};  // dk, dv: of the blocks that own the keys
-        case Path::kTc: return dense_tc_dkv_split(s);
-        case Path::kSplit: return dense_split_dkv_split(s);
-        default: return dense_simt_dkv_split(s);
-    }
-}
-
-}  // namespace
 
 size_t dense_fwd_workspace(const DenseShape& s) {
     const DenseSplit p = fwd_split(s);
@@ -433,7 +428,7 @@ int llsa_dense_fwd(const llsa_dense_params* p, const void* q, const void* k, con
     if (s.slices == 0 || s.R == 0) return LLSA_OK;
     LLSA_TRY(check_ptrs({q, o, lse}));
     if (s.nk > 0) LLSA_TRY(check_ptrs({k, v}));
-    LLSA_TRY(check_lens(q_len, k_len));
+    LLSA_TRY(dense_check_lens(q_len, k_len));
     const size_t need = dense_fwd_workspace(s);
     if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
     if (need > 0) LLSA_TRY(check_ptrs({ws}));
@@ -458,7 +453,7 @@ int llsa_dense_bwd(const llsa_dense_params* p, const void* q, const void* k, con
     if (s.slices == 0 || (s.R == 0 && s.nk == 0)) return LLSA_OK;
     if (s.R > 0) LLSA_TRY(check_ptrs({q, o, lse, dout, dq}));
     if (s.nk > 0) LLSA_TRY(check_ptrs({k, v, dk, dv}));
-    LLSA_TRY(check_lens(q_len, k_len));
+    LLSA_TRY(dense_check_lens(q_len, k_len));
     const size_t need = dense_bwd_workspace(s);
     if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
     if (need > 0) LLSA_TRY(check_ptrs({ws}));

@@ -1,0 +1,46 @@
+// diff.h -- what the differential attention kernels share.
+//
+// o = P1 V - lam P2 V with P_i = softmax(scale Q_i K_i^T): two maps with query and key
+// heads of d columns over one value head of 2 d. Rows, slices and the mask are those of
+// dense attention (dense.h): a slice is a batch entry and value head, its R = G nq rows
+// are the tokens of the G heads that share it, and map i of slice (b, g) is matrix
+// (2 b + i) kv_heads + g of q and of k. Both maps see the same mask.
+#pragma once
+
+#include "dense.h"
+
+namespace llsa {
+
+struct DiffShape {
+    int batch, heads, kv_heads, G, nq, nk, d, dtype, lam_dtype, causal;
+    int slices;  // batch * kv_heads
+    int R, Rp;   // rows per slice, and padded to kDenseRowPad
+    float scale;
+    DenseShape four;  // the same call as four dense ones (diff_api.cu)
+};
+
+struct DiffArgs {
+    DenseArgs d;  // slices, rows, lengths, mask, status; q, k, v, dout, and o of the call
+    const void* lam;
+    int lam_bf16, heads;
+    const void* o2;  // the second map's output (backward)
+    void* o2_out;    // or NULL (forward)
+};
+
+// Weight of the second map in the rows of head h.
+__device__ __forceinline__ float diff_lam(const DiffArgs& a, int h) {
+    return a.lam_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.lam)[h]) : static_cast<const float*>(a.lam)[h];
+}
+
+// Head of row r of a slice.
+__device__ __forceinline__ int diff_head(const DiffArgs& a, int slice, int r) {
+    return slice % a.d.kv_heads * (a.heads / a.d.kv_heads) + r / a.d.nq;
+}
+
+// Row r of map i of a slice in an array over [batch][2 heads][nq].
+__device__ __forceinline__ long long diff_row(const DiffArgs& a, int slice, int i, int r) {
+    const int b = slice / a.d.kv_heads, g = slice - b * a.d.kv_heads;
+    return ((long long)(2 * b + i) * a.d.kv_heads + g) * a.d.R + r;
+}
+
+}  // namespace llsa

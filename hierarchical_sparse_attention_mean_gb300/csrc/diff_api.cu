@@ -1,0 +1,442 @@
+// diff_api.cu -- the C entries of differential attention: validation, workspace, choice
+// of kernels, the gradient of lam, and the form that serves every call.
+//
+// That form. With V in halves V_1, V_2 of d columns, map i against half j is a dense
+// attention of d columns: o's half j is A_1j - lam A_2j, and since a row's dS is linear in
+// dout, dQ_i and dK_i are the sums over j, dV_j the sum over i, of the gradients of the
+// four calls with dout_1j = dO_j and dout_2j = -lam dO_j. So the call runs as one dense
+// call of four times as many slices on fp32 copies in the workspace, on the kernels for
+// fp32, and is rounded once where the four are joined. Per pair of a query and a key it
+// takes 16 d operations forward and 40 d backward where 12 d and 20 d are needed.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "diff.h"
+#include "entry.h"
+
+namespace llsa {
+namespace {
+
+constexpr int kThreads = 256;
+
+size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+template <typename T>
+__device__ __forceinline__ void load4f(const T* p, float* f) {
+    if constexpr (sizeof(T) == 2) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        f[0] = __uint_as_float(u.x << 16);
+        f[1] = __uint_as_float(u.x & 0xffff0000u);
+        f[2] = __uint_as_float(u.y << 16);
+        f[3] = __uint_as_float(u.y & 0xffff0000u);
+    } else {
+        const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+    }
+}
+
+// The fp32 operands of the four calls: slice ((2 b + i) 2 + j) kv_heads + g.
+struct FourArgs {
+    DiffArgs a;
+    float *q, *k, *v;           // [4 slices][R or nk][d]
+    float *o, *dout, *lse;      // of the rows (backward)
+    const float *dq, *dk, *dv;  // gradients of the four (backward)
+    void *dq_out, *dk_out, *dv_out;
+};
+
+struct Place {
+    int b, i, j, g;
+};
+__device__ __forceinline__ Place four_place(const FourArgs& f, long long slice4) {
+    const int kv = f.a.d.kv_heads;
+    const int g = (int)(slice4 % kv), rest = (int)(slice4 / kv);
+    return {rest >> 2, (rest >> 1) & 1, rest & 1, g};
+}
+
+// blockIdx.y 0: what has query rows, 1: what has keys. Four values per thread.
+template <typename T, bool BACKWARD>
+__global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_constant__ FourArgs f) {
+    const DenseArgs& a = f.a.d;
+    const bool keys = blockIdx.y == 1;
+    const int rows = keys ? a.nk : a.R, per = a.d / 4;
+    const long long n = 4LL * a.slices * rows * per;
+    for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
+        const long long row4 = x / per;
+        const int c = (int)(x - row4 * per) * 4;
+        const long long slice4 = row4 / rows;
+        const int r = (int)(row4 - slice4 * rows);
+        const Place p = four_place(f, slice4);
+        const long long one = (((long long)(2 * p.b + p.i) * a.kv_heads + p.g) * rows + r) * a.d + c;  // in q or k
+        const long long slice = (long long)p.b * a.kv_heads + p.g;
+        const long long two = (slice * rows + r) * 2 * a.d + p.j * a.d + c;                            // in v, o, dout
+        const long long to = row4 * a.d + c;
+        float y[4];
+        if (keys) {
+            load4f(static_cast<const T*>(a.k) + one, y);
+            store4(f.k + to, y);
+            load4f(static_cast<const T*>(a.v) + two, y);
+            store4(f.v + to, y);
+            continue;
+        }
+        load4f(static_cast<const T*>(a.q) + one, y);
+        store4(f.q + to, y);
+        if (!BACKWARD) continue;
+        const float lam = diff_lam(f.a, diff_head(f.a, (int)slice, r));
+        float o[4], o2[4];
+        load4f(static_cast<const T*>(a.dout) + two, y);
+        load4f(static_cast<const T*>(f.a.o2) + two, o2);
+        if (p.i == 0) load4f(static_cast<const T*>(a.o) + two, o);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            o2[e] = p.i == 0 ? fmaf(lam, o2[e], o[e]) : o2[e];
+            y[e] = p.i == 0 ? y[e] : -lam * y[e];
+        }
+        store4(f.dout + to, y);
+        store4(f.o + to, o2);
+        if (c == 0) f.lse[row4] = a.lse[diff_row(f.a, (int)slice, p.i, r)];
+    }
+}
+
+// o, o2 and the log-sum-exp of both maps from the four calls' (in f.o and f.lse).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_constant__ FourArgs f) {
+    const DenseArgs& a = f.a.d;
+    const int per = a.d / 2;  // vectors of 4 of a row of 2 d
+    const long long n = (long long)a.slices * a.R * per, step = (long long)a.kv_heads * a.R;
+    for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
+        const long long row = x / per;
+        const int col = (int)(x - row * per) * 4, j = col >= a.d ? 1 : 0;
+        const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
+        const int b = slice / a.kv_heads, g = slice - b * a.kv_heads;
+        const long long first = ((4LL * b + j) * a.kv_heads + g) * a.R + r, second = first + 2 * step;
+        const float lam = diff_lam(f.a, diff_head(f.a, slice, r));
+        float y[4], z[4];
+        load4f(f.o + first * a.d + col - j * a.d, y);
+        load4f(f.o + second * a.d + col - j * a.d, z);
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] = fmaf(-lam, z[e], y[e]);
+        store4(static_cast<T*>(a.o_out) + row * 2 * a.d + col, y);
+        if (f.a.o2_out) store4(static_cast<T*>(f.a.o2_out) + row * 2 * a.d + col, z);
+        if (col == 0) {
+            a.lse_out[diff_row(f.a, slice, 0, r)] = f.lse[first];
+            a.lse_out[diff_row(f.a, slice, 1, r)] = f.lse[second];
+        }
+    }
+}
+
+// dq, dk, dv (blockIdx.y) as sums of two of the four calls' gradients.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_constant__ FourArgs f) {
+    const DenseArgs& a = f.a.d;
+    const int which = blockIdx.y, rows = which == 0 ? a.R : a.nk;
+    const int per = which == 2 ? a.d / 2 : a.d / 4;
+    const long long n = (which == 2 ? 1LL : 2LL) * a.slices * rows * per, step = (long long)a.kv_heads * rows * a.d;
+    const float* from = which == 0 ? f.dq : which == 1 ? f.dk : f.dv;
+    T* out = static_cast<T*>(which == 0 ? f.dq_out : which == 1 ? f.dk_out : f.dv_out);
+    for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
+        const long long row = x / per;
+        int c = (int)(x - row * per) * 4;
+        const long long m = row / rows;  // matrix of the output
+        const int r = (int)(row - m * rows);
+        const long long to = row * 4 * per + c;
+        const long long outer = m / a.kv_heads;  // 2 b + i, or b
+        const int g = (int)(m - outer * a.kv_heads);
+        long long matrix;
+        int j = 0;
+        if (which == 2) {
+            j = c >= a.d ? 1 : 0;
+            c -= j * a.d;
+            matrix = (4 * outer + j) * a.kv_heads + g;
+        } else {
+            matrix = 2 * outer * a.kv_heads + g;
+        }
+        const long long at = (matrix * rows + r) * a.d + c, other = at + (which == 2 ? 2 * step : step);
+        float y[4], z[4];
+        load4f(from + at, y);
+        load4f(from + other, z);
+#pragma unroll
+        for (int e = 0; e < 4; e++) y[e] += z[e];
+        store4(out + to, y);
+    }
+}
+
+// ------------------------------------------------------ gradient of lam --
+
+// dlam of a head: -sum of dout . o2 over its rows that see a key, in two steps of fixed
+// order. Bound by HBM: dout and o2 are read once.
+constexpr int kLamRows = 64;    // rows that a block takes at least
+constexpr int kLamParts = 512;  // most blocks per head
+
+int lam_parts(const DiffShape& s) {
+    const long long rows = (long long)s.batch * s.nq;
+    return (int)std::max<long long>(1, std::min<long long>({(rows + kLamRows - 1) / kLamRows, kLamParts, 8LL * kDenseSms / s.heads + 1}));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constant__ DiffArgs f, float* part, int parts) {
+    const DenseArgs& a = f.d;
+    const int h = blockIdx.x / parts, p = blockIdx.x - h * parts;
+    const int G = f.heads / a.kv_heads, g = h / G, batch = a.slices / a.kv_heads;
+    const long long rows = (long long)batch * a.nq, first = rows * p / parts, last = rows * (p + 1) / parts;
+    const int lanes = a.d / 2;  // vectors of 4 in a row of 2 d: 4 to 64 a row
+    float sum = 0.f;
+    for (long long x = first * lanes + threadIdx.x; x < last * lanes; x += kThreads) {
+        const long long row = x / lanes;
+        const int c = (int)(x - row * lanes) * 4;
+        const int b = (int)(row / a.nq), t = (int)(row - (long long)b * a.nq);
+        const int slice = b * a.kv_heads + g;
+        if (dense_kend(a, dense_span(a, slice), t) == 0) continue;
+        const long long at = ((long long)slice * a.R + (long long)(h - g * G) * a.nq + t) * 2 * a.d + c;
+        float y[4], z[4];
+        load4f(static_cast<const T*>(a.dout) + at, y);
+        load4f(static_cast<const T*>(f.o2) + at, z);
+#pragma unroll
+        for (int e = 0; e < 4; e++) sum = fmaf(y[e], z[e], sum);
+    }
+    __shared__ float warps[kThreads / 32];
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int i = 1; i < kThreads / 32; i++) sum += warps[i];
+        part[blockIdx.x] = sum;
+    }
+}
+
+// A warp per head.
+__global__ void __launch_bounds__(32) diff_lam_sum_kernel(const float* part, int parts, void* out, int bf16) {
+    const int h = blockIdx.x;
+    float sum = 0.f;
+    for (int p = threadIdx.x; p < parts; p += 32) sum += part[(long long)h * parts + p];
+    sum = warp_sum(sum);
+    if (threadIdx.x != 0) return;
+    if (bf16) static_cast<__nv_bfloat16*>(out)[h] = __float2bfloat16_rn(-sum);
+    else static_cast<float*>(out)[h] = -sum;
+}
+
+int launch_lam(const DiffShape& s, const DiffArgs& a, void* dlam, float* part, cudaStream_t st) {
+    const int parts = lam_parts(s);
+    const unsigned blocks = (unsigned)s.heads * parts;
+    if (s.dtype == LLSA_DTYPE_BF16)
+        LLSA_LAUNCH("diff_lam", st, diff_lam_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a, part, parts));
+    else
+        LLSA_LAUNCH("diff_lam", st, diff_lam_kernel<float><<<blocks, kThreads, 0, st>>>(a, part, parts));
+    LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(part, parts, dlam, s.lam_dtype == LLSA_DTYPE_BF16));
+    return LLSA_OK;
+}
+
+// ------------------------------------------------------------ parameters --
+
+int derive_diff(const llsa_diff_params* p, DiffShape* s) {
+    if (!p) return LLSA_ERR_INVALID_ARG;
+    if (p->lam_dtype != LLSA_DTYPE_BF16 && p->lam_dtype != LLSA_DTYPE_F32) return LLSA_ERR_DTYPE;
+    if (p->heads < 0 || p->kv_heads < 0) return LLSA_ERR_INVALID_ARG;
+    if (p->d > 128) return LLSA_ERR_SHAPE;
+    const int kv = p->kv_heads ? p->kv_heads : p->heads;
+    if (p->heads > kDenseMaxExtent / 4 || kv > kDenseMaxExtent / 4) return LLSA_ERR_UNSUPPORTED;
+    memset(s, 0, sizeof(*s));
+    llsa_dense_params four = {p->batch, 4 * p->heads, 4 * kv, p->nq, p->nk, p->d, p->dtype, p->causal, p->scale};
+    LLSA_TRY(derive_dense(&four, &s->four));
+    s->batch = p->batch;
+    s->heads = p->heads;
+    s->kv_heads = kv;
+    s->G = s->four.G;
+    s->nq = p->nq;
+    s->nk = p->nk;
+    s->d = p->d;
+    s->dtype = p->dtype;
+    s->lam_dtype = p->lam_dtype;
+    s->causal = p->causal;
+    s->scale = s->four.scale;
+    s->slices = s->four.slices / 4;
+    s->R = s->four.R;
+    s->Rp = s->four.Rp;
+    s->four.dtype = LLSA_DTYPE_F32;
+    return LLSA_OK;
+}
+
+DiffArgs diff_args(const DiffShape& s) {
+    DiffArgs a;
+    memset(&a, 0, sizeof(a));
+    a.d = dense_args(s.four);
+    a.d.slices = s.slices;
+    a.d.kv_heads = s.kv_heads;
+    a.lam_bf16 = s.lam_dtype == LLSA_DTYPE_BF16;
+    a.heads = s.heads;
+    return a;
+}
+
+// -------------------------------------------------- the form for every call --
+
+size_t four_rows(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.d * sizeof(float)); }
+size_t four_keys(const DiffShape& s) { return up((size_t)4 * s.slices * s.nk * s.d * sizeof(float)); }
+size_t four_lse(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * sizeof(float)); }
+
+size_t four_workspace(const DiffShape& s, bool backward) {
+    return backward ? 4 * four_rows(s) + 4 * four_keys(s) + four_lse(s) + up(dense_bwd_workspace(s.four))
+                    : 2 * four_rows(s) + 2 * four_keys(s) + four_lse(s) + up(dense_fwd_workspace(s.four));
+}
+
+DenseArgs four_args(const DiffShape& s, const DiffArgs& a, const FourArgs& f) {
+    DenseArgs d = a.d;
+    d.slices = s.four.slices;
+    d.kv_heads = s.four.kv_heads;
+    d.q = f.q;
+    d.k = f.k;
+    d.v = f.v;
+    return d;
+}
+
+unsigned blocks_for(long long n) { return (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 16LL * kDenseSms); }
+
+template <typename T>
+int launch_four_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStream_t st) {
+    FourArgs f;
+    memset(&f, 0, sizeof(f));
+    f.a = a;
+    char* at = static_cast<char*>(ws);
+    auto take = [&](size_t bytes) { char* p = at; at += bytes; return reinterpret_cast<float*>(p); };
+    f.q = take(four_rows(s));
+    f.o = take(four_rows(s));
+    f.k = take(four_keys(s));
+    f.v = take(four_keys(s));
+    f.lse = take(four_lse(s));
+    const dim3 grid(blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4)), s.nk > 0 ? 2 : 1);
+    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, false><<<grid, kThreads, 0, st>>>(f));
+    DenseArgs d = four_args(s, a, f);
+    d.o_out = f.o;
+    d.lse_out = f.lse;
+    LLSA_TRY(launch_dense_fwd(s.four, d, at, st));
+    LLSA_LAUNCH("diff_combine", st,
+                diff_combine_kernel<T><<<blocks_for((long long)s.slices * s.R * (s.d / 2)), kThreads, 0, st>>>(f));
+    return LLSA_OK;
+}
+
+template <typename T>
+int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, void* dv, void* ws, cudaStream_t st) {
+    FourArgs f;
+    memset(&f, 0, sizeof(f));
+    f.a = a;
+    char* at = static_cast<char*>(ws);
+    auto take = [&](size_t bytes) { char* p = at; at += bytes; return reinterpret_cast<float*>(p); };
+    f.q = take(four_rows(s));
+    f.dout = take(four_rows(s));
+    f.o = take(four_rows(s));
+    float* gq = take(four_rows(s));
+    f.k = take(four_keys(s));
+    f.v = take(four_keys(s));
+    float *gk = take(four_keys(s)), *gv = take(four_keys(s));
+    f.lse = take(four_lse(s));
+    const dim3 grid(blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4)), s.nk > 0 ? 2 : 1);
+    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, true><<<grid, kThreads, 0, st>>>(f));
+    DenseArgs d = four_args(s, a, f);
+    d.o = f.o;
+    d.lse = f.lse;
+    d.dout = f.dout;
+    d.dq = gq;
+    d.dk = gk;
+    d.dv = gv;
+    LLSA_TRY(launch_dense_bwd(s.four, d, at, st));
+    f.dq = gq;
+    f.dk = gk;
+    f.dv = gv;
+    f.dq_out = dq;
+    f.dk_out = dk;
+    f.dv_out = dv;
+    LLSA_LAUNCH("diff_collapse", st, diff_collapse_kernel<T><<<dim3(grid.x, s.nk > 0 ? 3 : 1), kThreads, 0, st>>>(f));
+    return LLSA_OK;
+}
+
+size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam_parts(s) * sizeof(float)) : 0; }
+
+size_t fwd_workspace(const DiffShape& s) { return s.R == 0 ? 0 : four_workspace(s, false); }
+size_t bwd_workspace(const DiffShape& s) { return lam_bytes(s) + four_workspace(s, true); }
+
+}  // namespace
+}  // namespace llsa
+
+using namespace llsa;
+
+extern "C" {
+
+size_t llsa_diff_workspace_bytes(const llsa_diff_params* p, int op) {
+    DiffShape s;
+    if (derive_diff(p, &s) != LLSA_OK || s.slices == 0) return 0;
+    switch (op) {
+        case LLSA_OP_DIFF_FWD: return fwd_workspace(s);
+        case LLSA_OP_DIFF_BWD: return bwd_workspace(s);
+        default: return 0;
+    }
+}
+
+int llsa_diff_fwd(const llsa_diff_params* p, const void* q, const void* k, const void* v, const void* lam,
+                  const int32_t* q_len, const int32_t* k_len, void* o, void* o2, float* lse, void* ws, size_t ws_bytes,
+                  void* stream) {
+    CallRange range("llsa_diff_fwd");
+    DiffShape s;
+    LLSA_TRY(derive_diff(p, &s));
+    if (s.slices == 0 || s.R == 0) return LLSA_OK;
+    LLSA_TRY(check_ptrs({q, lam, o, lse}));
+    if (o2) LLSA_TRY(check_ptrs({o2}));
+    if (s.nk > 0) LLSA_TRY(check_ptrs({k, v}));
+    LLSA_TRY(dense_check_lens(q_len, k_len));
+    const size_t need = fwd_workspace(s);
+    if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
+    if (need > 0) LLSA_TRY(check_ptrs({ws}));
+    LLSA_TRY(device_ready());
+    DiffArgs a = diff_args(s);
+    a.d.q = q;
+    a.d.k = k;
+    a.d.v = v;
+    a.d.q_len = q_len;
+    a.d.k_len = k_len;
+    a.d.o_out = o;
+    a.d.lse_out = lse;
+    a.lam = lam;
+    a.o2_out = o2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return s.dtype == LLSA_DTYPE_BF16 ? launch_four_fwd<__nv_bfloat16>(s, a, ws, st) : launch_four_fwd<float>(s, a, ws, st);
+}
+
+int llsa_diff_bwd(const llsa_diff_params* p, const void* q, const void* k, const void* v, const void* lam, const void* o,
+                  const void* o2, const float* lse, const void* dout, const int32_t* q_len, const int32_t* k_len, void* dq,
+                  void* dk, void* dv, void* dlam, void* ws, size_t ws_bytes, void* stream) {
+    CallRange range("llsa_diff_bwd");
+    DiffShape s;
+    LLSA_TRY(derive_diff(p, &s));
+    if (s.heads == 0) return LLSA_OK;
+    LLSA_TRY(check_ptrs({lam, dlam}));
+    const bool rows = s.slices > 0 && s.R > 0, keys = s.slices > 0 && s.nk > 0;
+    if (rows) LLSA_TRY(check_ptrs({q, o, o2, lse, dout, dq}));
+    if (keys) LLSA_TRY(check_ptrs({k, v, dk, dv}));
+    LLSA_TRY(dense_check_lens(q_len, k_len));
+    const size_t need = s.slices > 0 ? bwd_workspace(s) : 0;
+    if (need > 0 && (!ws || ws_bytes < need)) return LLSA_ERR_WORKSPACE;
+    if (need > 0) LLSA_TRY(check_ptrs({ws}));
+    LLSA_TRY(device_ready());
+    DiffArgs a = diff_args(s);
+    a.d.q = q;
+    a.d.k = k;
+    a.d.v = v;
+    a.d.q_len = q_len;
+    a.d.k_len = k_len;
+    a.d.o = o;
+    a.d.lse = lse;
+    a.d.dout = dout;
+    a.lam = lam;
+    a.o2 = o2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (s.slices == 0) {  // an empty batch: nothing to add up
+        LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(nullptr, 0, dlam, s.lam_dtype == LLSA_DTYPE_BF16));
+        return LLSA_OK;
+    }
+    LLSA_TRY(launch_lam(s, a, dlam, static_cast<float*>(ws), st));
+    if (!rows && !keys) return LLSA_OK;
+    void* rest = static_cast<char*>(ws) + lam_bytes(s);
+    return s.dtype == LLSA_DTYPE_BF16 ? launch_four_bwd<__nv_bfloat16>(s, a, dq, dk, dv, rest, st)
+                                      : launch_four_bwd<float>(s, a, dq, dk, dv, rest, st);
+}
+
+}  // extern "C"

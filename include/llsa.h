@@ -354,6 +354,63 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
                    const float *lse, const void *dout, const int32_t *q_len, const int32_t *k_len, void *dq,
                    void *dk, void *dv, void *ws, size_t ws_bytes, void *stream);
 
+/* Differential attention: the difference of two softmax maps over shared values, the
+ * second one weighed by a learned number per head, so that what both maps attend to
+ * alike cancels. For query token t of head h in batch entry b, with value head
+ * g = h / (heads / kv_heads) and the keys that llsa_dense_fwd's rules (lengths, causal
+ * order) allow,
+ *   s^i_tj = scale * q^i_t . k^i_j,  lse^i_t = ln sum_j exp(s^i_tj),
+ *   a^i_t = sum_j exp(s^i_tj - lse^i_t) v_j,  o_t = a^1_t - lam_h a^2_t.
+ * Map i of head h has its queries in head i * heads + h of q, and its keys in head
+ * i * kv_heads + g of k (i = 0, 1): the first maps' heads lie before the second maps', as
+ * one projection after the other writes them, and rotary positions turn q and k as
+ * they are. Values have 2 d columns. A query without an allowed key gets o = 0 and
+ * lse = -infinity and adds nothing to any gradient; tokens behind a length, NaN,
+ * clamped lengths: as in llsa_dense_fwd. Outputs must not overlap inputs. */
+typedef struct llsa_diff_params {
+    int batch;
+    int heads;          /* differential heads: a multiple of kv_heads */
+    int kv_heads;       /* value heads, and key heads of each map; 0 selects heads */
+    int nq, nk;         /* query and key tokens per slice, padding included; 0 is allowed */
+    int d;              /* columns of q and k: multiple of 8, at most 128; v and o have 2 d */
+    int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int lam_dtype;      /* of lam and dlam, on its own: LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int causal;         /* 0 or 1 */
+    float scale;        /* softmax scale; 0 selects 1/sqrt(d) */
+} llsa_diff_params;
+
+/* Workspace of llsa_diff_fwd (op LLSA_OP_DIFF_FWD) or llsa_diff_bwd
+ * (LLSA_OP_DIFF_BWD) in bytes; 0 when none, or when the parameters are invalid. Two
+ * calls that may run at the same time need a workspace each. */
+enum { LLSA_OP_DIFF_FWD = 7, LLSA_OP_DIFF_BWD = 8 };
+size_t llsa_diff_workspace_bytes(const llsa_diff_params *p, int op);
+
+/* Differential attention, forward.
+ *   q     : [batch, 2 heads, nq, d]; k : [batch, 2 kv_heads, nk, d];
+ *   v     : [batch, kv_heads, nk, 2 d] (p->dtype); lam : [heads] (p->lam_dtype).
+ *   q_len, k_len : int32 [batch] on the device, or NULL (all tokens valid).
+ *   o     : output [batch, heads, nq, 2 d] (p->dtype).
+ *   o2    : output [batch, heads, nq, 2 d] (p->dtype), a^2, which the backward pass
+ *           needs; NULL where there will be none.
+ *   lse   : output fp32 [batch, 2 heads, nq] (natural log), heads as in q.
+ * Limits: those of llsa_dense_fwd for four times as many heads. Deterministic. */
+int llsa_diff_fwd(const llsa_diff_params *p, const void *q, const void *k, const void *v, const void *lam,
+                  const int32_t *q_len, const int32_t *k_len, void *o, void *o2, float *lse, void *ws, size_t ws_bytes,
+                  void *stream);
+
+/* Differential attention, backward: gradients of sum_t dout_t . o_t, the
+ * probabilities P^i recomputed from lse. With D^i_t = dout_t . a^i_t and w_1 = 1,
+ * w_2 = -lam_h:
+ *   dS^i = w_i P^i (dout_t . v_j - D^i_t),  dq^i_t = scale sum_j dS^i k^i_j,
+ *   dk^i_j = scale sum_t dS^i q^i_t,  dv_j = sum_t (P^1 - lam_h P^2) dout_t,
+ *   dlam_h = -sum_{b,t} dout_t . a^2_t.
+ *   o, o2, lse : from llsa_diff_fwd on the same inputs and lengths.
+ *   dout  : [batch, heads, nq, 2 d]; dq, dk, dv, dlam : outputs, overwritten.
+ * Deterministic: every sum has one owner and a fixed order. */
+int llsa_diff_bwd(const llsa_diff_params *p, const void *q, const void *k, const void *v, const void *lam, const void *o,
+                  const void *o2, const float *lse, const void *dout, const int32_t *q_len, const int32_t *k_len,
+                  void *dq, void *dk, void *dv, void *dlam, void *ws, size_t ws_bytes, void *stream);
+
 /* Rotary positions of q and k, in one launch.
  *
  * The first rot_dim columns of a head are `axes` equal segments; segment a is

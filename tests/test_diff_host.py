@@ -1,0 +1,126 @@
+"""Differential attention: what the host refuses, and the sizes it computes, without a
+GPU (these calls fail or return before any device work)."""
+import copy
+import ctypes
+import dataclasses
+import pickle
+
+import pytest
+import torch
+
+import hierarchical_sparse_attention_mean_gb300 as llsa
+from hierarchical_sparse_attention_mean_gb300 import build
+
+INVALID, SHAPE, DTYPE, ALIGN, WORKSPACE, UNSUPPORTED = -1, -2, -3, -4, -6, -8
+BASE = dict(batch=2, heads=4, nq=100, nk=100, d=64)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return llsa._load()
+
+
+def fwd(lib, p, ptrs=(16,) * 4, lens=(None, None), outs=(16, None, 16), ws=(None, 0)):
+    c = p.c() if isinstance(p, llsa.DiffParams) else p
+    return lib.llsa_diff_fwd(ctypes.byref(c), *ptrs, *lens, *outs, *ws, None)
+
+
+def bwd(lib, p, ptrs=(16,) * 8, lens=(None, None), outs=(16,) * 4, ws=(None, 0)):
+    c = p.c() if isinstance(p, llsa.DiffParams) else p
+    return lib.llsa_diff_bwd(ctypes.byref(c), *ptrs, *lens, *outs, *ws, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(d=60), SHAPE), (dict(d=136), SHAPE), (dict(d=0), SHAPE), (dict(d=-8), SHAPE),
+    (dict(heads=6, kv_heads=4), SHAPE), (dict(heads=2, kv_heads=4), SHAPE), (dict(heads=0, kv_heads=2), SHAPE),
+    (dict(batch=-1), INVALID), (dict(nq=-1), INVALID), (dict(nk=-1), INVALID), (dict(kv_heads=-1), INVALID), (dict(heads=-1), INVALID),
+    (dict(scale=-1.0), INVALID), (dict(scale=float("inf")), INVALID), (dict(scale=float("nan")), INVALID),
+    (dict(nq=(1 << 30) + 1), UNSUPPORTED), (dict(nk=(1 << 30) + 1), UNSUPPORTED),
+    (dict(heads=(1 << 31) - 1), UNSUPPORTED), (dict(heads=1 << 29, kv_heads=1), UNSUPPORTED),
+    (dict(heads=1024, kv_heads=1, nq=1 << 21), UNSUPPORTED),
+    (dict(batch=1 << 28, heads=1, nk=1 << 30), UNSUPPORTED), (dict(batch=1 << 20, heads=1 << 10), UNSUPPORTED),
+])
+def test_parameters_refused(lib, kw, code):
+    p = llsa.DiffParams(**{**BASE, **kw})
+    assert fwd(lib, p) == code and bwd(lib, p) == code
+    assert llsa.diff_workspace_bytes(p, llsa.OP_DIFF_FWD) == 0 and llsa.diff_workspace_bytes(p, llsa.OP_DIFF_BWD) == 0
+
+
+def test_raw_fields_refused(lib):
+    for field, value, code in (("dtype", 2, DTYPE), ("lam_dtype", 2, DTYPE), ("causal", 2, INVALID)):
+        c = llsa._DiffParams(2, 4, 4, 100, 100, 64, 0, 0, 0, 0.0)
+        setattr(c, field, value)
+        assert fwd(lib, c) == code and bwd(lib, c) == code
+    assert lib.llsa_diff_fwd(None, *([16] * 4), None, None, 16, None, 16, None, 0, None) == INVALID
+    assert lib.llsa_diff_workspace_bytes(None, 7) == 0
+
+
+def test_pointers_refused(lib):
+    p = llsa.DiffParams(**BASE)
+    for f, count, outs in ((fwd, 4, 3), (bwd, 8, 4)):
+        for i in range(count):
+            ptrs = [16] * count
+            ptrs[i] = None
+            assert f(lib, p, ptrs) == INVALID
+            ptrs[i] = 24
+            assert f(lib, p, ptrs) == ALIGN
+        for i in range(outs):
+            got = [16] * outs
+            got[i] = 8
+            assert f(lib, p, outs=got) == ALIGN
+            if f is bwd or i != 1:  # o2 need not be kept
+                got[i] = None
+                assert f(lib, p, outs=got) == INVALID
+        assert f(lib, p, lens=(6, None)) == ALIGN and f(lib, p, lens=(None, 2)) == ALIGN
+
+
+def test_nothing_to_do(lib):
+    none = dict(ptrs=(None,) * 4, outs=(None,) * 3)
+    assert fwd(lib, llsa.DiffParams(0, 4, 100, 100, 64), **none) == 0
+    assert fwd(lib, llsa.DiffParams(2, 0, 100, 100, 64), **none) == 0
+    assert fwd(lib, llsa.DiffParams(2, 4, 0, 100, 64), **none) == 0
+    assert bwd(lib, llsa.DiffParams(2, 0, 100, 100, 64), ptrs=(None,) * 8, outs=(None,) * 4) == 0
+    # no keys: k and v may be NULL, q may not; no tokens: dlam is written all the same
+    assert fwd(lib, llsa.DiffParams(2, 4, 10, 0, 64), ptrs=(None,) * 4) == INVALID
+    assert bwd(lib, llsa.DiffParams(2, 4, 0, 0, 64), ptrs=(None,) * 8, outs=(None,) * 4) == INVALID
+
+
+def test_workspace(lib):
+    one = llsa.DiffParams(1, 6, 1, 65536, 64)
+    for f, op in ((fwd, llsa.OP_DIFF_FWD), (bwd, llsa.OP_DIFF_BWD)):
+        need = llsa.diff_workspace_bytes(one, op)
+        assert need > 0 and f(lib, one) == WORKSPACE
+        assert f(lib, one, ws=(16, need - 1)) == WORKSPACE and f(lib, one, ws=(24, need)) == ALIGN
+    assert llsa.diff_workspace_bytes(one, 6) == 0 and llsa.diff_workspace_bytes(one, 9) == 0
+
+
+def test_binding_refuses(lib):
+    for kw in (dict(dtype="fp16"), dict(lam_dtype="fp16")):
+        with pytest.raises(ValueError):
+            llsa.DiffParams(**{**BASE, **kw})
+    for value in ((1 << 32) + 100, 1 << 31, -(1 << 31) - 1):
+        for field in ("batch", "heads", "kv_heads", "nq", "nk", "d"):
+            with pytest.raises(ValueError, match=field):
+                llsa.DiffParams(**{**BASE, field: value})
+    x = torch.zeros(1, 2, 4, 64)
+    with pytest.raises(ValueError, match="two heads"):
+        llsa.DiffParams.like(x[:, :1], x)
+    with pytest.raises(ValueError, match="two heads"):
+        llsa.DiffParams.like(x, torch.zeros(1, 3, 4, 64))
+    with pytest.raises(ValueError, match="lam must be"):
+        llsa.DiffParams.like(x, x, torch.zeros(1, dtype=torch.float16))
+    v, lam = torch.zeros(1, 1, 4, 128), torch.zeros(1)
+    with pytest.raises(ValueError, match="CUDA"):
+        llsa.diff_attention(x, x, v, lam)
+    with pytest.raises(ValueError, match="CUDA"):
+        llsa.llsa_diff_fwd(llsa.DiffParams.like(x, x, lam), x, x, v, lam, v, None, torch.zeros(1, 2, 4))
+
+
+def test_parameters_copy_and_pickle(lib):
+    p = llsa.DiffParams(2, 4, 100, 90, 64, kv_heads=2, causal=True, lam_dtype="fp32", scale=0.5)
+    llsa.diff_workspace_bytes(p, llsa.OP_DIFF_BWD)
+    assert p.shapes() == ((2, 8, 100, 64), (2, 4, 90, 64), (2, 2, 90, 128), (2, 4, 100, 128), (2, 8, 100))
+    for y in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
+        assert y == p and bytes(y.c()) == bytes(p.c())
+    assert dataclasses.replace(p, nq=7).c().nq == 7 and p.c().nq == 100

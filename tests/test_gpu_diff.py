@@ -1,0 +1,458 @@
+"""Differential attention on the GPU against its formulas in 64 bits: values and
+gradients over types, head layouts, lengths, masks and padding, within bounds that count
+roundings; plus streams, captured graphs, splits of a long axis, offsets behind 32 bits,
+and a run together with rotary positions."""
+import math
+
+import pytest
+import torch
+
+import hierarchical_sparse_attention_mean_gb300 as llsa
+from hierarchical_sparse_attention_mean_gb300 import build
+
+import dense_ref
+import diff_ref as ref
+import grid_ref as grid
+
+pytestmark = pytest.mark.gpu
+T = {"bf16": torch.bfloat16, "fp32": torch.float32}
+NAMES = ("o", "o2", "lse", "dq", "dk", "dv", "dlam")
+TIMEOUT, BAD_INDEX = -9, -10
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+
+
+def make(b, h, kv, nq, nk, d, dtype, q_len=None, k_len=None, seed=0, pad=float("nan"), lam_dtype=None):
+    g = torch.Generator().manual_seed(seed * 1000 + nq * 7 + nk * 3 + d)
+    x = {n: torch.randn(b, hh, nn, c, generator=g).to(T[dtype])
+         for n, hh, nn, c in (("q", 2 * h, nq, d), ("k", 2 * kv, nk, d), ("v", kv, nk, 2 * d), ("dout", h, nq, 2 * d))}
+    x["lam"] = (0.2 + 0.6 * torch.rand(h, generator=g)).to(T[lam_dtype or dtype])
+    for e in range(b):  # what lies behind the lengths must not matter
+        if q_len is not None:
+            x["q"][e, :, q_len[e]:] = pad
+            x["dout"][e, :, q_len[e]:] = pad
+        if k_len is not None:
+            x["k"][e, :, k_len[e]:] = pad
+            x["v"][e, :, k_len[e]:] = -pad
+    return x
+
+
+def lens(x):
+    return None if x is None else torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def run(x, causal=False, scale=0.0, q_len=None, k_len=None):
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], causal=causal, scale=scale)
+    ql, kl = lens(q_len), lens(k_len)
+    full = lambda n: torch.full_like(c[n], 7.0)  # every row is written
+    o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], ql, kl, o=full("dout"), o2=full("dout"))
+    dq, dk, dv, dlam = llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], ql, kl,
+                                          full("q"), full("k"), full("v"), full("lam"))
+    alone, lse_alone, none = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], ql, kl)
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0 and none is None
+    assert torch.equal(alone, o) and torch.equal(lse_alone, lse)  # o2 is no more than kept or not
+    return {"o": o, "o2": o2, "lse": lse, "dq": dq, "dk": dk, "dv": dv, "dlam": dlam}
+
+
+def both(x, dtype, names=NAMES, causal=False, scale=0.0, q_len=None, k_len=None):
+    want = ref.attention(**x, causal=causal, scale=scale, q_len=q_len, k_len=k_len, dtype=T[dtype], lam_dtype=x["lam"].dtype)
+    got = run(x, causal, scale, q_len, k_len)
+    for n in names:
+        ref.check(n, got[n], want[n])
+
+
+CASES = [
+    # b, h, kv, nq, nk, d, causal, q_len, k_len
+    (1, 1, 1, 1, 1, 8, False, None, None),
+    (2, 3, 3, 5, 1, 64, False, None, None),
+    (1, 2, 1, 1, 300, 64, False, None, None),             # one token, shared keys
+    (2, 8, 2, 3, 67, 128, True, None, None),
+    (1, 2, 2, 64, 64, 64, False, None, None),
+    (1, 2, 2, 128, 128, 64, True, None, None),
+    (1, 4, 2, 130, 129, 64, False, None, None),
+    (2, 2, 2, 257, 255, 128, True, None, None),
+    (1, 2, 2, 200, 77, 64, True, None, None),             # 123 rows see nothing
+    (1, 2, 1, 77, 200, 64, True, None, None),
+    (1, 6, 2, 100, 150, 64, True, None, None),            # tiles run over the ends of heads
+    (1, 6, 2, 100, 150, 128, True, [61], [149]),
+    (1, 8, 1, 17, 90, 64, False, [9], None),              # padding inside a tile, head after head
+    (3, 2, 2, 140, 190, 64, False, [140, 65, 1], [190, 1, 129]),
+    (3, 2, 2, 140, 190, 64, True, [140, 65, 0], [100, 0, 190]),
+    (2, 4, 4, 300, 333, 64, False, None, [333, 0]),       # one entry without keys
+    (2, 2, 1, 260, 270, 128, False, [0, 259], [270, 131]),
+    (1, 2, 2, 90, 100, 40, False, None, None),
+    (2, 2, 1, 90, 140, 32, True, None, [97, 140]),
+    (1, 2, 2, 90, 100, 72, True, None, [97]),
+    (1, 2, 2, 150, 140, 96, False, None, None),
+    (1, 2, 2, 1000, 1100, 64, False, None, None),
+    (1, 1, 1, 700, 900, 128, True, None, None),
+    (1, 2, 2, 383, 513, 8, False, None, None),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v) for v in c[:6]) + ("-causal" if c[6] else "") +
+                         ("-len" if c[7] or c[8] else ""))
+def test_forward_and_backward(case, dtype):
+    b, h, kv, nq, nk, d, causal, ql, kl = case
+    both(make(b, h, kv, nq, nk, d, dtype, ql, kl), dtype, causal=causal, q_len=ql, k_len=kl)
+
+
+@pytest.mark.parametrize("dtype,lam_dtype", [("bf16", "fp32"), ("fp32", "bf16")])
+def test_lam_has_a_type_of_its_own(dtype, lam_dtype):
+    both(make(2, 4, 2, 70, 200, 64, dtype, lam_dtype=lam_dtype), dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("value", [0.0, 1.0, -1.5, 30.0])
+def test_any_lam(value, dtype):
+    x = make(1, 2, 2, 140, 150, 64, dtype, seed=2)
+    x["lam"][:] = value
+    both(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_equal_maps_cancel(dtype):
+    """With lam 1 and both maps the same, o is a difference of equal numbers: only what one map's roundings leave."""
+    x = make(1, 2, 2, 150, 300, 64, dtype, seed=4)
+    x["q"][:, 2:], x["k"][:, 2:] = x["q"][:, :2], x["k"][:, :2]
+    x["lam"][:] = 1.0
+    got = run(x)
+    assert not got["o"].any() and torch.equal(got["lse"][:, :2], got["lse"][:, 2:])
+    both(x, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("amp,scale", [(8.0, 0.0), (1.0, 1.0), (0.01, 0.3)])
+def test_scales(amp, scale, dtype):
+    """Sharp and flat softmax: scores up to hundreds, where rows pass through many maxima."""
+    x = make(1, 2, 2, 150, 400, 64, dtype, seed=3)
+    x["q"] = (x["q"].float() * amp).to(T[dtype])
+    # keys that grow along the sequence in one map and shrink in the other
+    grow = torch.linspace(0.1, 2.0, 400)[:, None]
+    x["k"] = torch.cat([x["k"][:, :2].float() * grow, x["k"][:, 2:].float() * grow.flip(0)], 1).to(T[dtype])
+    both(x, dtype, scale=scale)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 128), ("bf16", 40)])
+@pytest.mark.parametrize("nq,nk,h,kv", [(1, 20000, 2, 2), (2, 9000, 8, 2), (5000, 33, 2, 1)])
+def test_long_axis_is_split(nq, nk, h, kv, dtype, d):
+    """Few rows over many keys (and few keys under many rows): the long axis runs in parts."""
+    both(make(1, h, kv, nq, nk, d, dtype, k_len=[nk - 3], seed=5), dtype, k_len=[nk - 3])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("b,nq,nk", [(2, 0, 5), (2, 5, 0), (2, 0, 0), (0, 5, 5)])
+def test_empty_sides(b, nq, nk, dtype):
+    got = run(make(b, 2, 2, nq, nk, 64, dtype))
+    assert got["o"].shape == (b, 2, nq, 128) and not got["o"].any() and not got["o2"].any()
+    assert bool((got["lse"] == -math.inf).all())
+    for n in ("dq", "dk", "dv", "dlam"):
+        assert not got[n].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_bad_lengths_are_clamped_and_reported(dtype):
+    x = {n: t.cuda() for n, t in make(2, 2, 2, 70, 80, 64, dtype).items()}
+    p = llsa.DiffParams.like(x["q"], x["k"], x["lam"])
+    args = (p, x["q"], x["k"], x["v"], x["lam"])
+    o, lse, _ = llsa.diff_forward(*args, lens([75, 70]), lens([80, -4]))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == BAD_INDEX
+    o2, lse2, _ = llsa.diff_forward(*args, lens([70, 70]), lens([80, 0]))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64), ("fp32", 104)])
+def test_repeats_are_bit_equal(dtype, d):
+    x = make(2, 8, 2, 333, 450, d, dtype, q_len=[333, 200], k_len=[450, 77])
+    a, b = (run(x, True, 0.0, [333, 200], [450, 77]) for _ in range(2))
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_gradients_against_differences():
+    """Directional derivatives of the 64-bit loss sum(o dout), by central differences."""
+    x = make(1, 4, 2, 50, 60, 64, "fp32", seed=9)
+    got = run(x, causal=True)
+
+    def loss(**kw):
+        y = {n: t.double() for n, t in {**x, **kw}.items()}
+        return float((ref.attention(y["q"], y["k"], y["v"], y["lam"], causal=True)["o"][0] * y["dout"]).sum())
+
+    for n in ("q", "k", "v", "lam"):
+        u = torch.randn(x[n].shape, generator=torch.Generator().manual_seed(1), dtype=torch.float64)
+        u /= u.norm()
+        h = 1e-4  # truncation h^2, cancellation 2^-53 |loss| / h: both far below the fp32 gradient's error
+        diff = (loss(**{n: x[n].double() + h * u}) - loss(**{n: x[n].double() - h * u})) / (2 * h)
+        g = got["d" + n].double().cpu()
+        assert abs(float((g * u).sum()) - diff) <= 1e-5 * float(g.norm()) + 1e-6
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_other_stream_and_captured_graph(dtype, d):
+    """The call on a stream of its own, and captured with its backward pass and
+    replayed on new inputs, gives what it gives on the current stream."""
+    ql, kl = [200, 130], [190, 260]
+    x = make(2, 4, 2, 200, 260, d, dtype, ql, kl)
+    y = make(2, 4, 2, 200, 260, d, dtype, ql, kl, seed=4)
+    want_x, want_y = run(x, True, 0.0, ql, kl), run(y, True, 0.0, ql, kl)
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], causal=True)
+    a, b = lens(ql), lens(kl)
+
+    def step():
+        o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], a, b, backward=True)
+        return dict(zip(NAMES, (o, o2, lse, *llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], a, b))))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = step()
+    torch.cuda.synchronize()
+    for n in got:
+        assert torch.equal(got[n], want_x[n]), n
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for source, want in ((x, want_x), (y, want_y)):
+        for n in c:
+            c[n].copy_(source[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for n in got:
+            assert torch.equal(got[n], want[n]), n
+
+
+def test_two_captured_graphs_at_once():
+    """Each graph has a workspace of its own, so that replays on two streams do not meet."""
+    graphs, outs, wants = [], [], []
+    for seed in (1, 2):
+        x = make(1, 2, 1, 2, 9000, 64, "bf16", seed=seed)
+        want = run(x)
+        c = {n: t.cuda() for n, t in x.items()}
+        p = llsa.DiffParams.like(c["q"], c["k"], c["lam"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], backward=True)
+            grads = llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"])
+        graphs.append((g, c))
+        outs.append(dict(zip(NAMES, (o, o2, lse, *grads))))
+        wants.append(want)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (g, _c) in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for got, want in zip(outs, wants):
+        for n in want:
+            assert torch.equal(got[n], want[n]), n
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d):
+    """With the copying warps switched off every consumer's first wait runs out: the
+    status reads TIMEOUT once, the kernels end, and the next calls are right."""
+    x = make(1, 2, 2, 300, 400, d, dtype, seed=12)
+    want = run(x)
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"])
+    args = (p, c["q"], c["k"], c["v"], c["lam"])
+    for call in (lambda: llsa.diff_forward(*args),
+                 lambda: llsa.diff_backward(*args, want["o"], want["o2"], want["lse"], c["dout"])):
+        llsa.test_set_wait_limit(256, llsa.LLSA_TEST_NO_COPIES)
+        try:
+            call()
+            torch.cuda.synchronize()
+        finally:
+            llsa.test_set_wait_limit(0, 0)
+        assert llsa.llsa_get_status() == TIMEOUT
+        assert llsa.llsa_get_status() == 0
+    got = run(x)
+    for n in got:
+        assert torch.equal(got[n], want[n]), n
+
+
+def test_a_given_stream_orders_the_call():
+    """stream=: the work goes there, workspace included, whatever the current stream is."""
+    x = {n: t.cuda() for n, t in make(1, 2, 2, 1, 20000, 64, "bf16").items()}
+    p = llsa.DiffParams.like(x["q"], x["k"], x["lam"])
+    want = llsa.diff_forward(p, x["q"], x["k"], x["v"], x["lam"])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = llsa.diff_forward(p, x["q"], x["k"], x["v"], x["lam"], stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_autograd_matches_the_calls(dtype):
+    x = make(2, 4, 2, 64, 96, 64, dtype, seed=2)
+    want = run(x, causal=True)
+    leaves = [x[n].cuda().transpose(1, 2).contiguous().transpose(1, 2).requires_grad_() for n in ("q", "k", "v")]
+    lam = x["lam"].cuda().requires_grad_()
+    o = llsa.diff_attention(*leaves, lam, causal=True)
+    grads = torch.autograd.grad(o, (*leaves, lam), x["dout"].cuda())
+    assert torch.equal(o, want["o"])
+    for g, n in zip(grads, ("dq", "dk", "dv", "dlam")):
+        assert torch.equal(g, want[n]), n
+    with torch.no_grad():
+        assert torch.equal(llsa.diff_attention(*leaves, lam, causal=True), want["o"])
+
+
+def test_one_lam_for_all_heads_and_expanded_values():
+    """What is broadcast collects the gradients of every entry."""
+    x = make(3, 2, 2, 40, 50, 64, "fp32", seed=8)
+    k1, v1 = (x[n][:1].cuda().requires_grad_() for n in ("k", "v"))
+    lam = x["lam"][:1].clone().cuda().requires_grad_()
+    o = llsa.diff_attention(x["q"].cuda(), k1.expand(3, -1, -1, -1), v1.expand(3, -1, -1, -1), lam)
+    dk, dv, dlam = torch.autograd.grad(o, (k1, v1, lam), x["dout"].cuda())
+    x["k"], x["v"] = (x[n][:1].expand(3, -1, -1, -1) for n in ("k", "v"))
+    x["lam"] = x["lam"][:1].expand(2)
+    want = ref.attention(**x, dtype=torch.float32)
+    for n, g in (("dk", dk), ("dv", dv), ("dlam", dlam)):
+        value, bound = (t.sum(0, keepdim=True) for t in want[n])
+        ref.check(n, g, (value, bound + 4 * 2.0 ** -24 * value.abs()))
+
+
+def _columns_sum(t, pairs):
+    """For each column, its value plus its partner's."""
+    got = t.clone()
+    for _, _, _, ia, ib in pairs:
+        got[..., ia] = got[..., ib] = t[..., ia] + t[..., ib]
+    return got
+
+
+@pytest.mark.parametrize("extent,order,span", [((4, 8, 8), "raster", "axis"), ((1, 16, 16), "tile", "axis"), ((8, 4, 8), "raster", "dealt")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_positions_attention_and_gradients_together(dtype, extent, order, span):
+    """Positions of a clip -> differential attention -> both backward passes, against the formulas in 64 bits."""
+    b, h, kv, n, d, columns = 2, 4, 2, 256, 64, (16, 24, 24)
+    x = make(b, h, kv, n, n, d, dtype, seed=6)
+    leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v", "lam")]
+    rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=columns, extent=extent, token_order=order, span=span)
+    o = llsa.diff_attention(*leaves, rope=rope)
+    got = dict(zip(("o", "dq", "dk", "dv", "dlam"), (o, *torch.autograd.grad(o, leaves, x["dout"].cuda()))))
+    turned = llsa.rotary(leaves[0].detach(), leaves[1].detach(), rope)
+    pos = grid.places(extent, None, order)[None]
+    y = dict(x)
+    for m, z in zip(("q", "k"), turned):  # the attention sees them rounded to the type
+        ref.check(m, z, grid.turned(x[m], pos, columns, span, dtype=T[dtype]))
+        y[m] = z.cpu()
+    want = ref.attention(**y, dtype=T[dtype])
+    for m in ("o", "dv", "dlam"):
+        ref.check(m, got[m], want[m])
+    u = ref.half_step(T[dtype])
+    for m in ("dq", "dk"):
+        value, bound = want[m]
+        back, turn = grid.turned(value, pos, columns, span, inverse=True)
+        # |cos|, |sin| <= 1: an error of either column of a pair reaches both, and the result is rounded once more
+        bound = _columns_sum(bound, grid.pairs(columns, span, "half")) * (1 + u) + turn + u * back.abs()
+        ref.check(m, got[m], (back, bound))
+
+
+def test_few_tokens_with_positions_stay_in_fp32():
+    """bf16 of up to 16 tokens is turned, attended and turned back in fp32, and rounded once."""
+    x = make(1, 2, 2, 12, 12, 64, "bf16", seed=16)
+    leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v", "lam")]
+    rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=(32, 32), extent=(3, 4))
+    o = llsa.diff_attention(*leaves, rope=rope)
+    got = torch.autograd.grad(o, leaves, x["dout"].cuda())
+    wide = [x[m].float().cuda().requires_grad_() for m in ("q", "k", "v")] + [x["lam"].cuda().requires_grad_()]
+    o32 = llsa.diff_attention(*wide, rope=rope.in_fp32())
+    want = torch.autograd.grad(o32, wide, x["dout"].float().cuda())
+    assert torch.equal(o, o32.bfloat16())
+    for a, b in zip(got, want):
+        assert torch.equal(a, b.bfloat16())
+
+
+SEVERAL = [
+    # b, h, kv, nq, nk, d, causal: more pieces of work than SMs, so resident blocks take several one after the other
+    (8, 16, 16, 300, 333, 64, False),
+    (16, 12, 12, 200, 260, 64, True),
+    (10, 16, 16, 256, 130, 64, False),
+    (20, 16, 8, 70, 70, 40, True),
+    (10, 16, 16, 150, 140, 128, True),
+    (4, 40, 40, 260, 129, 96, False),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("ragged", [False, True])
+@pytest.mark.parametrize("b,h,kv,nq,nk,d,causal", SEVERAL)
+def test_blocks_take_several_pieces(b, h, kv, nq, nk, d, causal, ragged, dtype):
+    """Also with lengths that leave pieces of every kind between the full ones:
+    empty ones, ones without queries or without keys, and partial tiles."""
+    ql = [(nq, 0, 1, nq - 1, nq // 2)[e % 5] for e in range(b)] if ragged else None
+    kl = [(nk - 1, nk, nk // 3, 0, nk, 1, nk)[e % 7] for e in range(b)] if ragged else None
+    both(make(b, h, kv, nq, nk, d, dtype, ql, kl, seed=11), dtype, causal=causal, q_len=ql, k_len=kl)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [8, 64, 72, 128])
+@pytest.mark.parametrize("h,kv,nq", [(1, 1, 1), (2, 2, 1), (2, 1, 1), (3, 1, 1), (4, 2, 2), (5, 1, 1), (2, 1, 4), (3, 1, 3)])
+def test_few_rows(h, kv, nq, d, dtype):
+    """One to nine rows per key head, where the choice of kernels changes."""
+    both(make(2, h, kv, nq, 700, d, dtype, None, [700, 531], seed=13), dtype, causal=True, k_len=[700, 531])
+
+
+def test_nan_among_the_scores_stays_in_its_row():
+    """A query with a NaN gets NaN in o and lse of that map; its neighbours do not."""
+    for nq in (1, 130):
+        x = make(1, 2, 2, nq, 200, 64, "bf16", seed=17)
+        x["q"][0, 1, nq // 2, 3] = float("nan")  # first map of head 1
+        c = {n: t.cuda() for n, t in x.items()}
+        p = llsa.DiffParams.like(c["q"], c["k"], c["lam"])
+        o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], backward=True)
+        bad = torch.zeros(1, 4, nq, dtype=torch.bool)
+        bad[0, 1, nq // 2] = True
+        assert torch.equal(lse.isnan().cpu(), bad) and not o2.isnan().any()
+        assert torch.equal(o.isnan().all(-1).cpu(), bad[:, :2]) and torch.equal(o.isnan().any(-1).cpu(), bad[:, :2])
+
+
+def test_fp32_magnitudes():
+    """Large, small and mixed values of fp32 keep their exponents."""
+    x = make(1, 2, 2, 200, 150, 64, "fp32", seed=15)
+    big = torch.tensor([2.0 ** 60, 2.0 ** -60]).repeat(75)[:, None]
+    x["v"] = x["v"] * big
+    x["q"], x["k"] = x["q"] * 2.0 ** 40, x["k"] * 2.0 ** -40
+    x["dout"] = x["dout"] * 2.0 ** -20
+    both(x, "fp32")
+
+
+def test_offsets_behind_32_bits():
+    """2^31 elements and more in k and in v; the weight lies on the last keys."""
+    d, nk = 64, (1 << 24) + 77
+    k = torch.zeros(1, 2, nk, d, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros(1, 1, nk, 2 * d, dtype=torch.bfloat16, device="cuda")
+    assert k.numel() > 1 << 31 and v.numel() > 1 << 31
+    q = torch.ones(1, 2, 1, d, dtype=torch.bfloat16, device="cuda")
+    lam = torch.full((1,), 0.5, device="cuda")
+    k[0, 0, -3:] = 8.0                  # first map: scores 64 against 0, e^64 >> the number of keys
+    k[0, 1, -1:] = 8.0                  # second map: on the last key alone
+    v[0, 0, -3:] = torch.tensor([[1.0], [2.0], [4.0]], device="cuda")
+    p = llsa.DiffParams.like(q, k, lam)
+    o, lse, o2 = llsa.diff_forward(p, q, k, v, lam, backward=True)
+    grads = llsa.diff_backward(p, q, k, v, lam, o, o2, lse, torch.ones_like(o))
+    torch.cuda.synchronize()
+    assert llsa.llsa_get_status() == 0
+    assert torch.allclose(o.float(), torch.full_like(o, 7 / 3 - 2.0).float(), rtol=0, atol=2.0 ** -6)  # P rounded: 2^-8 of 7/3 and 4 / 2
+    assert abs(float(lse[0, 0]) - (64 + math.log(3))) < 1e-3 and abs(float(lse[0, 1]) - 64) < 1e-3
+    dv = grads[2][0, 0, -3:].float().cpu()
+    want = torch.tensor([1 / 3, 1 / 3, 1 / 3 - 0.5])[:, None].expand(3, 2 * d)
+    assert torch.allclose(dv, want, rtol=0, atol=2.0 ** -8)
+    assert abs(float(grads[3]) + 4.0 * 2 * d) < 4.0 * 2 * d * 2.0 ** -7
+    few = grads[2][0, 0, : nk // 2]     # a zero key's weight: e^-64 / 3 - 0.5 e^-64 = -2.67e-29
+    lo, hi = float(few.min()), float(few.max())
+    # the difference of two weights, each good to 2^-8 (as bf16, if it was rounded before) and 2^-15 (exp2 and lse)
+    small = math.exp(-64)
+    assert lo == hi and abs(lo - small * (1 / 3 - 0.5)) < small * (1 / 3 + 0.5) * (2.0 ** -8 + 2.0 ** -15)
