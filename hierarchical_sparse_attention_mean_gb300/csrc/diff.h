@@ -43,4 +43,21 @@ __device__ __forceinline__ long long diff_row(const DiffArgs& a, int slice, int 
     return ((long long)(2 * b + i) * a.d.kv_heads + g) * a.d.R + r;
 }
 
+// A split of the keys leaves, per part, O unnormalised [splits][2][slices R][2 d] and then
+// (maximum in units of log2, sum) pairs [splits][2][slices R], in DenseArgs::part.
+__device__ __forceinline__ long long diff_part(const DenseArgs& a, int part, int i, long long row) {
+    return ((long long)part * 2 + i) * a.slices * a.R + row;
+}
+__device__ __forceinline__ float2* diff_part_ml(const DenseArgs& a) {
+    return reinterpret_cast<float2*>(a.part + (long long)a.splits * 2 * a.slices * a.R * 2 * a.d);
+}
+inline size_t diff_part_bytes(const DiffShape& s, int splits) {
+    return splits > 1 ? (size_t)splits * 2 * s.slices * s.R * (2 * s.d + 2) * sizeof(float) : 0;
+}
+
+// diff_fwd_tc.cu: forward on the tensor cores (bf16).
+bool diff_tc_supported(const DiffShape& s);
+DenseSplit diff_tc_fwd_split(const DiffShape& s);
+int launch_diff_tc_fwd(const DiffShape& s, const DiffArgs& a, cudaStream_t st);
+
 }  // namespace llsa

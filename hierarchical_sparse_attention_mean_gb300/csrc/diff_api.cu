@@ -162,6 +162,69 @@ __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_co
     }
 }
 
+// ------------------------------------------------------ join of a split --
+
+// o, o2 and lse of every row from the parts of a split over the keys: a warp per row, the
+// weights of 32 parts worked out at once, a lane each, then part after part with the
+// loads of several in flight.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_constant__ DiffArgs f) {
+    const DenseArgs& a = f.d;
+    const long long rows = (long long)a.slices * a.R;
+    const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+    const int lane = threadIdx.x & 31, dv = 2 * a.d;
+    if (row >= rows) return;
+    const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
+    const float2* ml = diff_part_ml(a);
+    float acc[2][2][4] = {};
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        float m = -INFINITY, l = 0.f;
+        for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[diff_part(a, p, i, row)].x);
+        m = warp_max(m);
+        const float shift = m == -INFINITY ? 0.f : m;
+        for (int p = lane; p < a.splits; p += 32) {
+            const float2 x = ml[diff_part(a, p, i, row)];
+            l = fmaf(x.y, exp2f(x.x - shift), l);
+        }
+        l = warp_sum(l);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        for (int p0 = 0; p0 < a.splits; p0 += 32) {
+            const float w = p0 + lane < a.splits ? exp2f(ml[diff_part(a, p0 + lane, i, row)].x - shift) : 0.f;
+            const int n = min(32, a.splits - p0);
+#pragma unroll 8
+            for (int x = 0; x < n; x++) {
+                const float wx = __shfl_sync(0xffffffffu, w, x);
+                const float* from = a.part + diff_part(a, p0 + x, i, row) * dv + lane * 4;
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    if (lane * 4 + 128 * k < dv) {
+                        const float4 y = *reinterpret_cast<const float4*>(from + 128 * k);
+                        acc[i][k][0] = fmaf(wx, y.x, acc[i][k][0]);
+                        acc[i][k][1] = fmaf(wx, y.y, acc[i][k][1]);
+                        acc[i][k][2] = fmaf(wx, y.z, acc[i][k][2]);
+                        acc[i][k][3] = fmaf(wx, y.w, acc[i][k][3]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) acc[i][k][e] *= inv;
+        if (lane == 0) a.lse_out[diff_row(f, slice, i, r)] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    }
+    const float lam = diff_lam(f, diff_head(f, slice, r));
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const int c = lane * 4 + 128 * k;
+        if (c >= dv) break;
+        if (f.o2_out) store4(static_cast<T*>(f.o2_out) + row * dv + c, acc[1][k]);
+#pragma unroll
+        for (int e = 0; e < 4; e++) acc[0][k][e] = fmaf(-lam, acc[1][k][e], acc[0][k][e]);
+        store4(static_cast<T*>(a.o_out) + row * dv + c, acc[0][k]);
+    }
+}
+
 // ------------------------------------------------------ gradient of lam --
 
 // dlam of a head: -sum of dout . o2 over its rows that see a key, in two steps of fixed
@@ -351,7 +414,35 @@ int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, v
 
 size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam_parts(s) * sizeof(float)) : 0; }
 
-size_t fwd_workspace(const DiffShape& s) { return s.R == 0 ? 0 : four_workspace(s, false); }
+// Which kernels take a call.
+enum class Path { kTc, kFour };
+
+Path fwd_path(const DiffShape& s) { return diff_tc_supported(s) ? Path::kTc : Path::kFour; }
+
+DenseSplit fwd_split(const DiffShape& s) { return fwd_path(s) == Path::kTc ? diff_tc_fwd_split(s) : DenseSplit{1, s.nk}; }
+
+size_t fwd_workspace(const DiffShape& s) {
+    if (s.R == 0) return 0;
+    return fwd_path(s) == Path::kFour ? four_workspace(s, false) : diff_part_bytes(s, fwd_split(s).splits);
+}
+
+int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
+    const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
+    const Path path = fwd_path(s);
+    if (path == Path::kFour) return bf16 ? launch_four_fwd<__nv_bfloat16>(s, a, ws, st) : launch_four_fwd<float>(s, a, ws, st);
+    const DenseSplit p = fwd_split(s);
+    a.d.splits = p.splits;
+    a.d.chunk = p.chunk;
+    a.d.part = static_cast<float*>(ws);
+    LLSA_TRY(launch_diff_tc_fwd(s, a, st));
+    if (p.splits > 1) {
+        const unsigned blocks = (unsigned)(((long long)s.slices * s.R + kThreads / 32 - 1) / (kThreads / 32));
+        if (bf16) LLSA_LAUNCH("diff_join", st, diff_join_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
+        else LLSA_LAUNCH("diff_join", st, diff_join_kernel<float><<<blocks, kThreads, 0, st>>>(a));
+    }
+    return LLSA_OK;
+}
+
 size_t bwd_workspace(const DiffShape& s) { return lam_bytes(s) + four_workspace(s, true); }
 
 }  // namespace
@@ -396,8 +487,7 @@ int llsa_diff_fwd(const llsa_diff_params* p, const void* q, const void* k, const
     a.d.lse_out = lse;
     a.lam = lam;
     a.o2_out = o2;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return s.dtype == LLSA_DTYPE_BF16 ? launch_four_fwd<__nv_bfloat16>(s, a, ws, st) : launch_four_fwd<float>(s, a, ws, st);
+    return launch_diff_fwd(s, a, ws, static_cast<cudaStream_t>(stream));
 }
 
 int llsa_diff_bwd(const llsa_diff_params* p, const void* q, const void* k, const void* v, const void* lam, const void* o,
