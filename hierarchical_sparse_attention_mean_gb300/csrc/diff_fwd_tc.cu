@@ -34,9 +34,9 @@ namespace {
 
 using namespace tc;
 
-// 12 warps of 168 registers at launch = 64,512: 256 softmax threads take 216 of
-// them, the 128 others keep 72.
-constexpr int kThreads = 384, kRegsSoftmax = 216, kRegsOther = 72;
+// 12 warps of 168 registers at launch = 64,512: 256 softmax threads take 232 of
+// them, the 128 others keep 40 (with 216, a row of S spills).
+constexpr int kThreads = 384, kRegsSoftmax = 232, kRegsOther = 40;
 constexpr int BM = 128, BN = 128, VC = 128;  // rows, keys, columns of V of a piece
 
 template <int D>
