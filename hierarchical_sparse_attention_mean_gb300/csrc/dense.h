@@ -124,6 +124,22 @@ size_t dense_bwd_workspace(const DenseShape& s);
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
 
+// Sums of the parts of up to three outputs, in ascending order: out = sum_p part[p n ..], rounded to `dtype`.
+struct DenseSums {
+    const float* part[3];
+    void* out[3];
+    long long n[3];
+    int parts[3];
+    int outs = 0;
+    void add(const float* p, void* o, long long count, int splits) {
+        part[outs] = p;
+        out[outs] = o;
+        n[outs] = count;
+        parts[outs++] = splits;
+    }
+};
+int launch_dense_sums(int dtype, const DenseSums& sums, cudaStream_t st);
+
 struct DenseSplit {
     int splits, chunk;  // parts, and elements of the split axis per part (a multiple of `tile`)
 };

@@ -140,17 +140,9 @@ __global__ void __launch_bounds__(kThreads) dense_join_fwd_kernel(const __grid_c
     if (lane == 0) a.lse_out[row] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
 }
 
-// Sums of `parts` fp32 arrays of n values, in ascending order, for up to three
-// outputs (blockIdx.y).
-struct JoinArgs {
-    const float* part[3];
-    void* out[3];
-    long long n[3];
-    int parts[3];
-};
-
+// Sums of the parts of up to three outputs (blockIdx.y).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) dense_join_sum_kernel(const __grid_constant__ JoinArgs a) {
+__global__ void __launch_bounds__(kThreads) dense_join_sum_kernel(const __grid_constant__ DenseSums a) {
     const int t = blockIdx.y;
     const long long n = a.n[t], i = ((long long)blockIdx.x * kThreads + threadIdx.x) * 4;
     if (i >= n) return;
@@ -379,28 +371,24 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         case Path::kSplit: LLSA_TRY(launch_dense_split_bwd(s, aq, ak, planes, st)); break;
         default: LLSA_TRY(launch_dense_simt_bwd(s, aq, ak, st));
     }
-    JoinArgs join;
-    int outs = 0;
-    long long most = 0;
-    auto add = [&](const float* part, void* out, long long n, int parts) {
-        join.part[outs] = part;
-        join.out[outs] = out;
-        join.n[outs] = n;
-        join.parts[outs++] = parts;
-        most = std::max(most, n);
-    };
-    if (pq.splits > 1) add(aq.part, a.dq, nq, pq.splits);
+    DenseSums sums;
+    if (pq.splits > 1) sums.add(aq.part, a.dq, nq, pq.splits);
     if (pk.splits > 1) {
-        add(ak.part, a.dk, nk, pk.splits);
-        add(ak.part + pk.splits * nk, a.dv, nk, pk.splits);
+        sums.add(ak.part, a.dk, nk, pk.splits);
+        sums.add(ak.part + pk.splits * nk, a.dv, nk, pk.splits);
     }
-    if (outs > 0) {
-        const dim3 grid((unsigned)((most / 4 + kThreads - 1) / kThreads), (unsigned)outs);
-        if (bf16)
-            LLSA_LAUNCH("dense_join_sum", st, dense_join_sum_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(join));
-        else
-            LLSA_LAUNCH("dense_join_sum", st, dense_join_sum_kernel<float><<<grid, kThreads, 0, st>>>(join));
-    }
+    return launch_dense_sums(s.dtype, sums, st);
+}
+
+int launch_dense_sums(int dtype, const DenseSums& sums, cudaStream_t st) {
+    if (sums.outs == 0) return LLSA_OK;
+    long long most = 0;
+    for (int i = 0; i < sums.outs; i++) most = std::max(most, sums.n[i]);
+    const dim3 grid((unsigned)((most / 4 + kThreads - 1) / kThreads), (unsigned)sums.outs);
+    if (dtype == LLSA_DTYPE_BF16)
+        LLSA_LAUNCH("dense_join_sum", st, dense_join_sum_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(sums));
+    else
+        LLSA_LAUNCH("dense_join_sum", st, dense_join_sum_kernel<float><<<grid, kThreads, 0, st>>>(sums));
     return LLSA_OK;
 }
 

@@ -11,6 +11,8 @@
 
 namespace llsa {
 
+constexpr int kDiffStats = 5;  // numbers per query row in the backward pass: -lse log2(e) and -D of both maps, lam
+
 struct DiffShape {
     int batch, heads, kv_heads, G, nq, nk, d, dtype, lam_dtype, causal;
     int slices;  // batch * kv_heads
@@ -25,6 +27,9 @@ struct DiffArgs {
     int lam_bf16, heads;
     const void* o2;  // the second map's output (backward)
     void* o2_out;    // or NULL (forward)
+    // Backward: nl2 of DenseArgs holds kDiffStats arrays [slices][Rp], -lse log2(e) and -D of
+    // both maps and lam; d2 takes sums of P_2 dP of every row, [parts of dq][4][slices][Rp].
+    float* d2;
 };
 
 // Weight of the second map in the rows of head h.
@@ -59,5 +64,11 @@ inline size_t diff_part_bytes(const DiffShape& s, int splits) {
 bool diff_tc_supported(const DiffShape& s);
 DenseSplit diff_tc_fwd_split(const DiffShape& s);
 int launch_diff_tc_fwd(const DiffShape& s, const DiffArgs& a, cudaStream_t st);
+
+// diff_bwd_tc.cu: backward on the tensor cores (bf16 up to 64 columns).
+bool diff_tc_bwd_supported(const DiffShape& s);
+DenseSplit diff_tc_dq_split(const DiffShape& s);
+DenseSplit diff_tc_dkv_split(const DiffShape& s);
+int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st);
 
 }  // namespace llsa

@@ -225,6 +225,83 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
     }
 }
 
+// ------------------------------------------------------ per-row numbers --
+
+// The numbers that the backward pass needs of every query row: -lse log2(e) and -D of both
+// maps, D_1 = dout . (o + lam o2) and D_2 = dout . o2, and lam. Rows that see no key (and
+// the padding to Rp) get -infinity and 0, so that their probabilities are 2^(s - inf) = 0.
+// A block per 128 rows, eight lanes per row, four rows each at a time. Bound by HBM: dout,
+// o and o2 are read once.
+constexpr int kRowsEach = kDenseRowPad / (kThreads / 8);
+
+__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
+    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
+        sum = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), sum);
+    }
+    return sum;
+}
+
+__global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_constant__ DiffArgs f) {
+    const DenseArgs& a = f.d;
+    const unsigned per = (unsigned)a.Rp / kDenseRowPad, slice = blockIdx.x / per;
+    const int r0 = (int)(blockIdx.x - slice * per) * kDenseRowPad + (threadIdx.x >> 3), part = threadIdx.x & 7;
+    const DenseSpan sp = dense_span(a, (int)slice);
+    const int dv = 2 * a.d;
+    float one[kRowsEach], two[kRowsEach];
+    bool on[kRowsEach];
+#pragma unroll
+    for (int u = 0; u < kRowsEach; u++) {
+        const int r = r0 + u * (kThreads / 8);
+        on[u] = r < a.R && dense_kend(a, sp, r < a.nq ? r : r % a.nq) > 0;
+        one[u] = two[u] = 0.f;
+    }
+    for (int c = part * 8; c < dv; c += 64) {
+        uint4 g[kRowsEach], x[kRowsEach], y[kRowsEach];
+        const long long at = ((long long)slice * a.R + r0) * dv + c;
+#pragma unroll
+        for (int u = 0; u < kRowsEach; u++) {
+            g[u] = x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+            if (on[u]) {
+                const long long to = at + (long long)u * (kThreads / 8) * dv;
+                g[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + to));
+                x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + to));
+                y[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(f.o2) + to));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRowsEach; u++) {
+            one[u] += dot8(g[u], x[u]);
+            two[u] += dot8(g[u], y[u]);
+        }
+    }
+    const long long all = (long long)a.slices * a.Rp;
+#pragma unroll
+    for (int u = 0; u < kRowsEach; u++) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) {
+            one[u] += __shfl_xor_sync(0xffffffffu, one[u], o);
+            two[u] += __shfl_xor_sync(0xffffffffu, two[u], o);
+        }
+        if (part == 0) {
+            const int r = r0 + u * (kThreads / 8);
+            const long long idx = (long long)slice * a.Rp + r;
+            const float lam = on[u] ? diff_lam(f, diff_head(f, (int)slice, r)) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const float lse = on[u] ? __ldg(a.lse + diff_row(f, (int)slice, i, r)) : -INFINITY;
+                a.nl2[i * all + idx] = lse == -INFINITY ? -INFINITY : -lse * kDenseLog2e;
+            }
+            a.nl2[2 * all + idx] = on[u] ? -fmaf(lam, two[u], one[u]) : 0.f;
+            a.nl2[3 * all + idx] = on[u] ? -two[u] : 0.f;
+            a.nl2[4 * all + idx] = lam;
+        }
+    }
+}
+
 // ------------------------------------------------------ gradient of lam --
 
 // dlam of a head: -sum of dout . o2 over its rows that see a key, in two steps of fixed
@@ -266,6 +343,33 @@ __global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constan
         for (int i = 1; i < kThreads / 32; i++) sum += warps[i];
         part[blockIdx.x] = sum;
     }
+}
+
+// dlam of a head from d2, `sets` sums of P_2 dP of every row: part p of `parts` of its
+// rows to part[h parts + p], or with one part to dlam itself.
+__global__ void __launch_bounds__(kThreads) diff_lam_rows_kernel(const __grid_constant__ DiffArgs f, float* part, int parts, int sets,
+                                                                 void* out) {
+    const DenseArgs& a = f.d;
+    const int h = blockIdx.x / parts, p = blockIdx.x - h * parts;
+    const int G = f.heads / a.kv_heads, g = h / G, batch = a.slices / a.kv_heads;
+    const long long rows = (long long)batch * a.nq, first = rows * p / parts, last = rows * (p + 1) / parts;
+    const long long all = (long long)a.slices * a.Rp;
+    float sum = 0.f;
+    for (long long row = first + threadIdx.x; row < last; row += kThreads) {
+        const int b = (int)(row / a.nq), t = (int)(row - (long long)b * a.nq);
+        const float* from = f.d2 + ((long long)b * a.kv_heads + g) * a.Rp + (long long)(h - g * G) * a.nq + t;
+#pragma unroll 4
+        for (int i = 0; i < sets; i++) sum += from[i * all];
+    }
+    __shared__ float warps[kThreads / 32];
+    sum = warp_sum(sum);
+    if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < kThreads / 32; i++) sum += warps[i];
+    if (parts > 1) part[blockIdx.x] = sum;
+    else if (f.lam_bf16) static_cast<__nv_bfloat16*>(out)[h] = __float2bfloat16_rn(-sum);
+    else static_cast<float*>(out)[h] = -sum;
 }
 
 // A warp per head.
@@ -443,7 +547,72 @@ int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     return LLSA_OK;
 }
 
-size_t bwd_workspace(const DiffShape& s) { return lam_bytes(s) + four_workspace(s, true); }
+Path bwd_path(const DiffShape& s) { return s.nk > 0 && diff_tc_bwd_supported(s) ? Path::kTc : Path::kFour; }
+
+// Workspace of the tensor-core backward pass, in order: the rows' numbers, the sums of
+// P_2 dP, parts of those over a head's rows, parts of dq, of dk, of dv.
+struct TcBwd {
+    DenseSplit q, k;
+    long long nq, nk;  // elements of dq, and of dk or dv
+    int lam_parts;
+    size_t stats, d2, lam, dq, dkv;
+    size_t bytes() const { return stats + d2 + lam + dq + dkv; }
+};
+
+TcBwd tc_bwd(const DiffShape& s) {
+    TcBwd t;
+    t.q = diff_tc_dq_split(s);
+    t.k = diff_tc_dkv_split(s);
+    t.nq = 2LL * s.slices * s.R * s.d;
+    t.nk = 2LL * s.slices * s.nk * s.d;
+    const size_t rows = (size_t)s.slices * s.Rp * sizeof(float);
+    t.stats = up(kDiffStats * rows);
+    t.d2 = up(4 * t.q.splits * rows);
+    // one block per head up to 4,096 of its rows: a second launch costs more than a long loop
+    t.lam_parts = (int)std::min<long long>(64, ((long long)s.batch * s.nq + 4095) / 4096);
+    t.lam = up((size_t)s.heads * t.lam_parts * sizeof(float));
+    t.dq = t.q.splits > 1 ? up(t.q.splits * t.nq * sizeof(float)) : 0;
+    t.dkv = t.k.splits > 1 ? up(2 * t.k.splits * t.nk * sizeof(float)) : 0;
+    return t;
+}
+
+int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, void* dlam, void* ws, cudaStream_t st) {
+    const TcBwd t = tc_bwd(s);
+    char* at = static_cast<char*>(ws);
+    auto take = [&](size_t bytes) { char* p = at; at += bytes; return reinterpret_cast<float*>(p); };
+    a.d.nl2 = take(t.stats);
+    a.d2 = take(t.d2);
+    float* lam = take(t.lam);
+    a.d.dq = dq;
+    a.d.dk = dk;
+    a.d.dv = dv;
+    DiffArgs aq = a, ak = a;
+    aq.d.splits = t.q.splits;
+    aq.d.chunk = t.q.chunk;
+    aq.d.part = take(t.dq);
+    ak.d.splits = t.k.splits;
+    ak.d.chunk = t.k.chunk;
+    ak.d.part = take(t.dkv);
+    const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
+    if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("diff_rows", st, diff_rows_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a));
+    LLSA_TRY(launch_diff_tc_bwd(s, aq, ak, st));
+    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * t.lam_parts, kThreads, 0, st>>>(a, lam, t.lam_parts,
+                                                                                                                 4 * t.q.splits, dlam));
+    if (t.lam_parts > 1)
+        LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(lam, t.lam_parts, dlam, a.lam_bf16));
+    DenseSums sums;
+    if (t.q.splits > 1) sums.add(aq.d.part, dq, t.nq, t.q.splits);
+    if (t.k.splits > 1) {
+        sums.add(ak.d.part, dk, t.nk, t.k.splits);
+        sums.add(ak.d.part + t.k.splits * t.nk, dv, t.nk, t.k.splits);
+    }
+    return launch_dense_sums(s.dtype, sums, st);
+}
+
+size_t bwd_workspace(const DiffShape& s) {
+    return bwd_path(s) == Path::kTc ? tc_bwd(s).bytes() : lam_bytes(s) + four_workspace(s, true);
+}
 
 }  // namespace
 }  // namespace llsa
@@ -522,6 +691,7 @@ int llsa_diff_bwd(const llsa_diff_params* p, const void* q, const void* k, const
         LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(nullptr, 0, dlam, s.lam_dtype == LLSA_DTYPE_BF16));
         return LLSA_OK;
     }
+    if (bwd_path(s) == Path::kTc) return launch_tc_bwd(s, a, dq, dk, dv, dlam, ws, st);
     LLSA_TRY(launch_lam(s, a, dlam, static_cast<float*>(ws), st));
     if (!rows && !keys) return LLSA_OK;
     void* rest = static_cast<char*>(ws) + lam_bytes(s);
