@@ -65,10 +65,10 @@ bool diff_tc_supported(const DiffShape& s);
 DenseSplit diff_tc_fwd_split(const DiffShape& s);
 int launch_diff_tc_fwd(const DiffShape& s, const DiffArgs& a, cudaStream_t st);
 
-// diff_bwd_tc.cu: backward on the tensor cores (bf16 up to 64 columns).
-bool diff_tc_bwd_supported(const DiffShape& s);
+// diff_bwd_tc.cu: backward on the tensor cores (bf16); diff_bwd_wide_tc.cu: behind 64 columns.
 DenseSplit diff_tc_dq_split(const DiffShape& s);
 DenseSplit diff_tc_dkv_split(const DiffShape& s);
 int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st);
+int launch_diff_tc_bwd_wide(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st);
 
 }  // namespace llsa

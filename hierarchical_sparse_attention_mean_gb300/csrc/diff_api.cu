@@ -547,7 +547,7 @@ int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     return LLSA_OK;
 }
 
-Path bwd_path(const DiffShape& s) { return s.nk > 0 && diff_tc_bwd_supported(s) ? Path::kTc : Path::kFour; }
+Path bwd_path(const DiffShape& s) { return diff_tc_supported(s) ? Path::kTc : Path::kFour; }
 
 // Workspace of the tensor-core backward pass, in order: the rows' numbers, the sums of
 // P_2 dP, parts of those over a head's rows, parts of dq, of dk, of dv.

@@ -549,16 +549,16 @@ diff_bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 
 }  // namespace
 
-bool diff_tc_bwd_supported(const DiffShape& s) { return diff_tc_supported(s) && s.d <= D; }
-
+// Behind 64 columns a row or key block is several pieces of work.
 DenseSplit diff_tc_dq_split(const DiffShape& s) {
-    return dense_make_split((long long)s.slices * ((s.R + BT - 1) / BT), s.nk, BT, 2);
+    return dense_make_split((long long)s.slices * ((s.R + BT - 1) / BT) * (s.d > D ? 2 : 1), s.nk, BT, 2);
 }
 DenseSplit diff_tc_dkv_split(const DiffShape& s) {
-    return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT), s.R, BT, 2);
+    return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT) * (s.d > D ? 3 : 1), s.R, BT, 2);
 }
 
 int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st) {
+    if (s.d > D) return launch_diff_tc_bwd_wide(s, aq, ak, st);
     constexpr int smem = Cfg<true>::SMEM > Cfg<false>::SMEM ? Cfg<true>::SMEM : Cfg<false>::SMEM;
     static_assert(smem <= 227 * 1024 && sizeof(Bars) <= 1024, "shared memory budget");
     const DenseArgs& a = aq.d;
