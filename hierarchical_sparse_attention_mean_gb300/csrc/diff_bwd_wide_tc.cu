@@ -45,9 +45,10 @@ enum Kind { kDq = 0, kDk = 1, kDv = 2 };
 template <Kind KIND>
 struct Cfg {
     static constexpr int NX = KIND == kDv ? 2 : 3;   // HALVES of stationary tiles: X1, X2 of two; or both maps' keys
-    static constexpr int N1 = KIND == kDv ? 3 : 2, N2 = 2;
+    static constexpr int N1 = 3, N2 = 2;                 // stages of the two streams
+    static constexpr int CH = KIND == kDv ? 2 : 1;       // 64-column regions of a stage of stream 2
     static constexpr int NS = KIND == kDq ? 0 : 2;   // stages of the rows' numbers, two of 128 each
-    static constexpr int SMEM = (NX + N1 + N2) * HALF + NS * 2 * BT * 4 + 1024;
+    static constexpr int SMEM = (NX + N1) * HALF + N2 * CH * REGION + NS * 2 * BT * 4 + 1024;
     static constexpr int TM_DP = 128, TM_ACC = KIND == kDv ? 256 : 384;
 };
 
@@ -83,8 +84,8 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
     unsigned char* sX = sm;
     unsigned char* ring1 = sm + C::NX * HALF;
     unsigned char* ring2 = ring1 + C::N1 * HALF;
-    float* stats = reinterpret_cast<float*>(ring2 + C::N2 * HALF);
-    Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * HALF + C::NS * 2 * BT * 4);
+    float* stats = reinterpret_cast<float*>(ring2 + C::N2 * C::CH * REGION);
+    Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * C::CH * REGION + C::NS * 2 * BT * 4);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
@@ -180,15 +181,15 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                         bulk_load(smem_u32(stats + k * 2 * BT), a.nl2 + (KIND == kDv ? 0 : map) * all + row, BT * 4, fs);
                         bulk_load(smem_u32(stats + k * 2 * BT + BT), a.nl2 + (KIND == kDv ? 1 : 2 + map) * all + row, BT * 4, fs);
                     }
-                    const int tiles = one ? (KIND == kDv ? 2 : 1) : 2;
+                    const int regions = one ? 2 : C::CH, tiles = one ? (KIND == kDv ? 2 : 1) : 4 / C::CH;
                     for (int t = 0; t < tiles; t++) {
                         if (n >= ns) ok = bar_wait(smem_u32(&empty[st]), parity, abort_flag, a);
                         if (!ok) break;
                         const uint32_t fb = smem_u32(&full[st]);
-                        mbar_arrive_expect_tx(fb, HALF);
-                        for (int c = 0; c < 2; c++)
-                            tma_load_3d(smem_u32(ring + st * HALF + c * REGION), one ? map1 : map2, (one ? 0 : t * 128) + c * 64, it.pos,
-                                        one ? m0 + t * a.kv_heads : slice, fb);
+                        mbar_arrive_expect_tx(fb, regions * REGION);
+                        for (int c = 0; c < regions; c++)
+                            tma_load_3d(smem_u32(ring + (st * regions + c) * REGION), one ? map1 : map2,
+                                        ((one ? 0 : t * regions) + c) * 64, it.pos, one ? m0 + t * a.kv_heads : slice, fb);
                         n++;
                         if (++st == ns) {
                             st = 0;
@@ -212,32 +213,34 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
             const uint64_t dM2 = desc_sw128(smem_u32(ring2), REGION, 1024);
             // Rows of the streamed tiles whose P and dS are 0 by the mask of the lengths may
             // hold anything: they meet those zeros in the sums, so they are cleared.
-            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
+            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it, int regions = 2) {
                 if constexpr (KEYS) {
                     if (it.all || it.t0 + BT <= it.sp.lq) return;
                     int t = it.t0 + lane;
                     for (int x = lane; x < BT; x += 32, t += 32)
                         if (t % a.nq >= it.sp.lq)
-                            for (int c = 0; c < 2; c++)
+                            for (int c = 0; c < regions; c++)
                                 for (int e = 0; e < 8; e++)
                                     reinterpret_cast<uint4*>(tile + c * REGION + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
                 } else {
                     const int live = it.sp.lk - it.pos;
                     if (live >= BT) return;
-                    for (int c = 0; c < 2; c++)
+                    for (int c = 0; c < regions; c++)
                         for (int x = live * 8 + lane; x < BT * 8; x += 32)
                             reinterpret_cast<uint4*>(tile + c * REGION)[x] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
                 __syncwarp();
             };
-            // acc (+)= A B^T over 128 columns
-            auto mma_half = [&](uint32_t acc, uint64_t dA, uint64_t dB, bool fresh) {
+            // acc (+)= A B^T over 64 columns
+            auto mma_cols = [&](uint32_t acc, uint64_t dA, uint64_t dB, bool fresh) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ks++) {
-                    const uint32_t off = (ks / 4) * REGION + (ks % 4) * 32;
-                    mma_ss(leader, tbase + acc, dA + (off >> 4), dB + (off >> 4), idS, !fresh || ks > 0);
-                }
+                for (int ks = 0; ks < 4; ks++)
+                    mma_ss(leader, tbase + acc, dA + (ks * 32 >> 4), dB + (ks * 32 >> 4), idS, !fresh || ks > 0);
+            };
+            auto mma_half = [&](uint32_t acc, uint64_t dA, uint64_t dB) {
+                mma_cols(acc, dA, dB, true);
+                mma_cols(acc, dA + (REGION >> 4), dB + (REGION >> 4), false);
             };
             // acc += A B with A in tensor memory, 16 words of every 32 columns
             auto issue_sum = [&](uint32_t acc, uint32_t op, uint64_t dB, bool fresh) {
@@ -260,16 +263,16 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                         if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
                         if (!ok) break;
                         tc_fence_after();
-                        mma_half(0, dX, dY1 + (s1.st * HALF >> 4), true);
+                        mma_half(0, dX, dY1 + (s1.st * HALF >> 4));
                         commit(leader, smem_u32(&bar->s_full[0]));
                         s1.next();
                         if (n >= 2) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
-                        for (int h = 0; ok && h < 2; h++) {
+                        for (int h = 0; ok && h < 4; h++) {
                             ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
                             if (!ok) break;
-                            if (KEYS) clear_rows(ring2 + s2.st * HALF, it);  // v only enters dP, which the mask covers
+                            if (KEYS) clear_rows(ring2 + s2.st * REGION, it, 1);  // v only enters dP, which the mask covers
                             tc_fence_after();
-                            mma_half(C::TM_DP + sb.st * 128, dX + ((1 + h) * HALF >> 4), dY2 + (s2.st * HALF >> 4), h == 0);
+                            mma_cols(C::TM_DP + sb.st * 128, dX + ((2 + h) * REGION >> 4), dY2 + (s2.st * REGION >> 4), h == 0);
                             commit(leader, smem_u32(&bar->y2_empty[s2.st]));
                             s2.next();
                         }
@@ -303,7 +306,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                     if (!warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a)) return false;
                     clear_rows(ring1 + s1.st * HALF, it);
                     tc_fence_after();
-                    mma_half(i * 128, dX + (i * HALF >> 4), dY1 + (s1.st * HALF >> 4), true);
+                    mma_half(i * 128, dX + (i * HALF >> 4), dY1 + (s1.st * HALF >> 4));
                     commit(leader, smem_u32(&bar->s_full[i]));
                     commit(leader, smem_u32(&bar->y1_empty[s1.st]));
                     s1.next();
@@ -565,17 +568,18 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
     }
 }
 
-// Pieces in the order of their length: dk, dq, dv.
+// Longer pieces first: those of keys have R / 128 tiles, those of rows nk / 128.
 __global__ void __launch_bounds__(kThreads, 1)
 diff_bwd_wide_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
                         const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                         const __grid_constant__ CUtensorMap zq, const __grid_constant__ CUtensorMap zk,
                         const __grid_constant__ CUtensorMap zv, const __grid_constant__ DiffArgs aq,
-                        const __grid_constant__ DiffArgs ak, int row_pieces, int key_pieces) {
+                        const __grid_constant__ DiffArgs ak, int row_pieces, int key_pieces, int keys_first) {
     const Maps maps = {mq, mg, mk, mv, zq, zk, zv};
-    const int piece = blockIdx.x;
-    if (piece < 2 * key_pieces) bwd_piece<kDk>(maps, ak, piece);
-    else if (piece < 2 * (key_pieces + row_pieces)) bwd_piece<kDq>(maps, aq, piece - 2 * key_pieces);
+    int piece = blockIdx.x;
+    if (keys_first) piece = piece < 3 * key_pieces ? piece + 2 * row_pieces : piece - 3 * key_pieces;
+    if (piece < 2 * row_pieces) bwd_piece<kDq>(maps, aq, piece);
+    else if (piece < 2 * (key_pieces + row_pieces)) bwd_piece<kDk>(maps, ak, piece - 2 * row_pieces);
     else bwd_piece<kDv>(maps, ak, piece - 2 * (key_pieces + row_pieces));
 }
 
@@ -598,7 +602,8 @@ int launch_diff_tc_bwd_wide(const DiffShape& s, const DiffArgs& aq, const DiffAr
     const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.d.splits;
     if (2 * pq + 3 * pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("diff_bwd_wide_tc", st, diff_bwd_wide_tc_kernel<<<(unsigned)(2 * pq + 3 * pk), kThreads, smem, st>>>(
-                                            mq, mg, mk, mv, zq, zk, zv, aq, ak, (int)pq, (int)pk));
+                                            mq, mg, mk, mv, zq, zk, zv, aq, ak, (int)pq, (int)pk,
+                                            std::min(ak.d.chunk, s.R) >= std::min(a.chunk, s.nk)));
     return LLSA_OK;
 }
 
