@@ -21,9 +21,13 @@
 // columns each) and both dq; dS_i lies over S_i, and the maps take turns, so that one's
 // products run beside the other's exponentials. Keys: one place for S_1 and S_2 after
 // each other, over which P_1 - lam P_2 is written, dP, over which both dS are, and
-// the sums of dv, dk_1, dk_2. The tensor cores run dv, the next S_1, both dk, the next
-// S_2, the next dP; the exponentials of one map fall beside dk, those of the other
-// beside dP, dS beside dv.
+// the sums of dv, dk_1, dk_2. The tensor cores run dv, the next S_1, dk_1, the next S_2,
+// dk_2, the next dP; the exponentials fall beside dk and dP, dS beside dv.
+//
+// For keys, the numbers that go with a column (l2, D and lam of its row) come from shared
+// memory, which the products of two shared-memory operands keep busy by themselves. There
+// the threads read tensor memory as fragments, 8 columns of 4 rows each, and need a
+// quarter as many of those numbers as with a row of 32 columns each.
 //
 // All sixteen elementwise warps take a tile together, a thread per row and quarter of the
 // columns. Shared memory holds one set of stationary tiles, and every piece of work gets a
@@ -288,14 +292,14 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
                     tc_fence_after();
                     if constexpr (KEYS) {
                         issue_sum(C::TM_ACC + 128, C::TM_DP, 8, dT1, idA, fresh);                          // dk_1
-                        issue_sum(C::TM_ACC + 192, C::TM_DP + 8, 8, dT1 + (REGION >> 4), idA, fresh);      // dk_2
-                        commit(leader, smem_u32(&bar->y1_empty[t1.st]));
                         if (more) {
                             ok = warp_wait(smem_u32(&bar->s_read), (n + 1) & 1, abort_flag, a);
                             if (!ok) break;
                             issue_S(1);
-                            ok = issue_dP(it);
                         }
+                        issue_sum(C::TM_ACC + 192, C::TM_DP + 8, 8, dT1 + (REGION >> 4), idA, fresh);      // dk_2
+                        commit(leader, smem_u32(&bar->y1_empty[t1.st]));
+                        if (more) ok = issue_dP(it);
                     } else {
                         if (more) ok = issue_dP(it);
                         issue_sum(C::TM_ACC + 64, 128, 16, dT1 + (REGION >> 4), idA, fresh);               // dq_2
@@ -393,83 +397,100 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
             if (x < a.Rp) f.d2[((long long)(part * 4 + w) * a.slices + slice) * a.Rp + x] = kend > 0 ? d2 : 0.f;
         } else {
             Stage<C::N1> s1;
+            const int fr = (warp & 3) * 32 + (lane >> 2), fc = 2 * (lane & 3);  // first row and column of the fragments
+            const uint32_t low = 16u << 16;                                    // the second 16 lanes
             for (Items<KEYS> it = first; !it.done(); it.next(a), n++) {
-                const float* st = stats + s1.st * kStats * BT + w * kCols;  // of these columns' rows
+                // of these columns' rows; registers 16 h + 4 i + 2 e + k: column fc + 8 i + k, row fr + 16 h + 8 e
+                const float* st = stats + s1.st * kStats * BT + w * kCols + fc;
                 bar_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a);
                 uint32_t p[kCols], s[kCols];
+                auto pair = [](const uint32_t* v) { return pack2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+                auto put = [](uint32_t* v, uint64_t x) {
+                    float e0, e1;
+                    unpack2(x, e0, e1);
+                    v[0] = __float_as_uint(e0);
+                    v[1] = __float_as_uint(e1);
+                };
                 auto weights = [&](uint32_t* v, int i) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 4) {
-                        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + i * BT + c);
-                        float e0, e1, e2, e3;
-                        unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sl2x2, u.x), e0, e1);
-                        unpack2(fma2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sl2x2, u.y), e2, e3);
-                        v[c] = __float_as_uint(ex2(e0));
-                        v[c + 1] = __float_as_uint(ex2(e1));
-                        v[c + 2] = __float_as_uint(ex2(e2));
-                        v[c + 3] = __float_as_uint(ex2(e3));
+                    for (int c = 0; c < 16; c += 4) {
+                        const uint64_t l = *reinterpret_cast<const uint64_t*>(st + i * BT + 2 * c);
+#pragma unroll
+                        for (int x = c; x < 32; x += (x & 2) ? 14 : 2) {
+                            float e0, e1;
+                            unpack2(fma2(pair(v + x), sl2x2, l), e0, e1);
+                            v[x] = __float_as_uint(ex2(e0));
+                            v[x + 1] = __float_as_uint(ex2(e1));
+                        }
                     }
                 };
                 bar_wait(smem_u32(&bar->s_full[0]), n & 1, abort_flag, a);
                 tc_fence_after();
-                tmem_ld32_nowait(tS, p);
+                tmem_ld_frag(tS, p);
+                tmem_ld_frag(tS + low, p + 16);
                 tmem_wait_ld();
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->s_read), lane);
                 weights(p, 0);
                 bar_wait(smem_u32(&bar->s_full[1]), n & 1, abort_flag, a);
                 tc_fence_after();
-                tmem_ld32_nowait(tS, s);
+                tmem_ld_frag(tS, s);
+                tmem_ld_frag(tS + low, s + 16);
                 tmem_wait_ld();
                 weights(s, 1);
                 // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
                 if (a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)) {
-                    int t = (it.t0 + w * kCols) % a.nq;
 #pragma unroll
-                    for (int c = 0; c < kCols; c++) {
-                        if (x > t + sp.lk - sp.lq) p[c] = s[c] = 0u;
-                        if (++t == a.nq) t = 0;
-                    }
+                    for (int c = 0; c < 16; c += 4)
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const int last = (it.t0 + w * kCols + fc + 2 * c + k) % a.nq + sp.lk - sp.lq;  // key that this column's row sees last
+#pragma unroll
+                            for (int x = 0; x < 4; x++)
+                                if (x0 + fr + 8 * x > last) p[16 * (x >> 1) + c + 2 * (x & 1) + k] = s[16 * (x >> 1) + c + 2 * (x & 1) + k] = 0u;
+                        }
                 }
                 uint32_t o[kCols / 2];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 4) {
-                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + 4 * BT + c);  // lam
-                    float e0, e1;
+                for (int c = 0; c < 16; c += 4) {
+                    const uint64_t lam2 = *reinterpret_cast<const uint64_t*>(st + 4 * BT + 2 * c);
 #pragma unroll
-                    for (int h = 0; h < 4; h += 2) {
-                        unpack2(mul2(pack2(__uint_as_float(s[c + h]), __uint_as_float(s[c + h + 1])), h ? u.y : u.x), e0, e1);
-                        s[c + h] = __float_as_uint(e0);
-                        s[c + h + 1] = __float_as_uint(e1);
-                        o[(c + h) >> 1] = pack_bf16x2(__uint_as_float(p[c + h]) - e0, __uint_as_float(p[c + h + 1]) - e1);
+                    for (int x = c; x < 32; x += (x & 2) ? 14 : 2) {
+                        put(s + x, mul2(pair(s + x), lam2));
+                        o[x >> 1] = pack_bf16x2(__uint_as_float(p[x]) - __uint_as_float(s[x]), __uint_as_float(p[x + 1]) - __uint_as_float(s[x + 1]));
                     }
                 }
-                tmem_st16(tS, o);
+                tmem_st_frag16(tS, o);
+                tmem_st_frag16(tS + low, o + 8);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->ready[0]), lane);
                 bar_wait(smem_u32(&bar->dp_full), n & 1, abort_flag, a);
                 tc_fence_after();
+                uint32_t o2[kCols / 2];
 #pragma unroll
-                for (int q = 0; q < kCols; q += 16) {
+                for (int h = 0; h < 2; h++) {
                     uint32_t g[16];
-                    tmem_ld16_nowait(tG + q, g);
+                    tmem_ld_frag(tG + h * low, g);
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < 16; c += 4) {
-                        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + 2 * BT + q + c);
-                        const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(st + 3 * BT + q + c);
+                        const uint64_t d1 = *reinterpret_cast<const uint64_t*>(st + 2 * BT + 2 * c);
+                        const uint64_t d2x = *reinterpret_cast<const uint64_t*>(st + 3 * BT + 2 * c);
 #pragma unroll
-                        for (int h = 0; h < 4; h += 2) {
-                            const uint64_t g2 = pack2(__uint_as_float(g[c + h]), __uint_as_float(g[c + h + 1]));
-                            float e0, e1, y0, y1;
-                            unpack2(mul2(add2(g2, h ? u.y : u.x), pack2(__uint_as_float(p[q + c + h]), __uint_as_float(p[q + c + h + 1]))), e0, e1);
-                            unpack2(mul2(add2(g2, h ? v.y : v.x), pack2(__uint_as_float(s[q + c + h]), __uint_as_float(s[q + c + h + 1]))), y0, y1);
-                            o[(c + h) >> 1] = pack_bf16x2(e0, e1);
-                            o[8 + ((c + h) >> 1)] = pack_bf16x2(y0, y1);
+                        for (int x = c; x < c + 4; x += 2) {
+                            float e0, e1;
+                            unpack2(mul2(add2(pair(g + x), d1), pair(p + 16 * h + x)), e0, e1);
+                            o[8 * h + (x >> 1)] = pack_bf16x2(e0, e1);
+                            unpack2(mul2(add2(pair(g + x), d2x), pair(s + 16 * h + x)), e0, e1);
+                            o2[8 * h + (x >> 1)] = pack_bf16x2(e0, e1);
                         }
                     }
-                    tmem_st16(tG + q, o);  // 8 words of each dS where their 16 rows' dP were
+                    // 8 words of each dS where their 16 columns of dP were
+                    tmem_st_frag8(tG + h * low, o + 8 * h);
+                    tmem_st_frag8(tG + h * low + 8, o2 + 8 * h);
+                    tmem_st_frag8(tG + h * low + 16, o + 8 * h + 4);
+                    tmem_st_frag8(tG + h * low + 24, o2 + 8 * h + 4);
                 }
                 tmem_wait_st();
                 tc_fence_before();

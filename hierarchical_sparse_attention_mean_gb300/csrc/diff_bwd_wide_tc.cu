@@ -16,7 +16,7 @@
 // rows a tile, X2 and Y2 of 256 columns and Y2 fetched in halves. S is free as soon as it is
 // read and dP has two buffers, so the tensor cores, 2,048 clocks per 128 x 128 pairs, run the
 // next tile's S and dP while the threads make this one's dS, which is written over dP.
-// dv: P_1 - lam P_2 is written over S_1, S_2 of the next tile is made meanwhile; 2,048
+// dv: P_1 - lam P_2 is written over S_2, S_1 of the next tile is made meanwhile; 2,048
 // clocks too.
 //
 // Roles: warps 0-15 elementwise and epilogue (a thread per row and quarter of the columns),
@@ -45,10 +45,9 @@ enum Kind { kDq = 0, kDk = 1, kDv = 2 };
 template <Kind KIND>
 struct Cfg {
     static constexpr int NX = KIND == kDv ? 2 : 3;   // HALVES of stationary tiles: X1, X2 of two; or both maps' keys
-    static constexpr int N1 = 3, N2 = 2;                 // stages of the two streams
-    static constexpr int CH = KIND == kDv ? 2 : 1;       // 64-column regions of a stage of stream 2
+    static constexpr int N1 = KIND == kDv ? 3 : 2, N2 = 2;
     static constexpr int NS = KIND == kDq ? 0 : 2;   // stages of the rows' numbers, two of 128 each
-    static constexpr int SMEM = (NX + N1) * HALF + N2 * CH * REGION + NS * 2 * BT * 4 + 1024;
+    static constexpr int SMEM = (NX + N1 + N2) * HALF + NS * 2 * BT * 4 + 1024;
     static constexpr int TM_DP = 128, TM_ACC = KIND == kDv ? 256 : 384;
 };
 
@@ -84,8 +83,8 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
     unsigned char* sX = sm;
     unsigned char* ring1 = sm + C::NX * HALF;
     unsigned char* ring2 = ring1 + C::N1 * HALF;
-    float* stats = reinterpret_cast<float*>(ring2 + C::N2 * C::CH * REGION);
-    Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * C::CH * REGION + C::NS * 2 * BT * 4);
+    float* stats = reinterpret_cast<float*>(ring2 + C::N2 * HALF);
+    Bars* bar = reinterpret_cast<Bars*>(ring2 + C::N2 * HALF + C::NS * 2 * BT * 4);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     if (smem_u32(sm) & 1023u) {  // the swizzled layouts need it; the whole block leaves
@@ -181,15 +180,15 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                         bulk_load(smem_u32(stats + k * 2 * BT), a.nl2 + (KIND == kDv ? 0 : map) * all + row, BT * 4, fs);
                         bulk_load(smem_u32(stats + k * 2 * BT + BT), a.nl2 + (KIND == kDv ? 1 : 2 + map) * all + row, BT * 4, fs);
                     }
-                    const int regions = one ? 2 : C::CH, tiles = one ? (KIND == kDv ? 2 : 1) : 4 / C::CH;
+                    const int tiles = one ? (KIND == kDv ? 2 : 1) : 2;
                     for (int t = 0; t < tiles; t++) {
                         if (n >= ns) ok = bar_wait(smem_u32(&empty[st]), parity, abort_flag, a);
                         if (!ok) break;
                         const uint32_t fb = smem_u32(&full[st]);
-                        mbar_arrive_expect_tx(fb, regions * REGION);
-                        for (int c = 0; c < regions; c++)
-                            tma_load_3d(smem_u32(ring + (st * regions + c) * REGION), one ? map1 : map2,
-                                        ((one ? 0 : t * regions) + c) * 64, it.pos, one ? m0 + t * a.kv_heads : slice, fb);
+                        mbar_arrive_expect_tx(fb, HALF);
+                        for (int c = 0; c < 2; c++)
+                            tma_load_3d(smem_u32(ring + st * HALF + c * REGION), one ? map1 : map2, (one ? 0 : t * 128) + c * 64, it.pos,
+                                        one ? m0 + t * a.kv_heads : slice, fb);
                         n++;
                         if (++st == ns) {
                             st = 0;
@@ -213,34 +212,32 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
             const uint64_t dM2 = desc_sw128(smem_u32(ring2), REGION, 1024);
             // Rows of the streamed tiles whose P and dS are 0 by the mask of the lengths may
             // hold anything: they meet those zeros in the sums, so they are cleared.
-            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it, int regions = 2) {
+            auto clear_rows = [&](unsigned char* tile, const Items<KEYS>& it) {
                 if constexpr (KEYS) {
                     if (it.all || it.t0 + BT <= it.sp.lq) return;
                     int t = it.t0 + lane;
                     for (int x = lane; x < BT; x += 32, t += 32)
                         if (t % a.nq >= it.sp.lq)
-                            for (int c = 0; c < regions; c++)
+                            for (int c = 0; c < 2; c++)
                                 for (int e = 0; e < 8; e++)
                                     reinterpret_cast<uint4*>(tile + c * REGION + x * 128)[e] = make_uint4(0u, 0u, 0u, 0u);
                 } else {
                     const int live = it.sp.lk - it.pos;
                     if (live >= BT) return;
-                    for (int c = 0; c < regions; c++)
+                    for (int c = 0; c < 2; c++)
                         for (int x = live * 8 + lane; x < BT * 8; x += 32)
                             reinterpret_cast<uint4*>(tile + c * REGION)[x] = make_uint4(0u, 0u, 0u, 0u);
                 }
                 fence_async_smem();
                 __syncwarp();
             };
-            // acc (+)= A B^T over 64 columns
-            auto mma_cols = [&](uint32_t acc, uint64_t dA, uint64_t dB, bool fresh) {
+            // acc (+)= A B^T over 128 columns
+            auto mma_half = [&](uint32_t acc, uint64_t dA, uint64_t dB, bool fresh) {
 #pragma unroll
-                for (int ks = 0; ks < 4; ks++)
-                    mma_ss(leader, tbase + acc, dA + (ks * 32 >> 4), dB + (ks * 32 >> 4), idS, !fresh || ks > 0);
-            };
-            auto mma_half = [&](uint32_t acc, uint64_t dA, uint64_t dB) {
-                mma_cols(acc, dA, dB, true);
-                mma_cols(acc, dA + (REGION >> 4), dB + (REGION >> 4), false);
+                for (int ks = 0; ks < 8; ks++) {
+                    const uint32_t off = (ks / 4) * REGION + (ks % 4) * 32;
+                    mma_ss(leader, tbase + acc, dA + (off >> 4), dB + (off >> 4), idS, !fresh || ks > 0);
+                }
             };
             // acc += A B with A in tensor memory, 16 words of every 32 columns
             auto issue_sum = [&](uint32_t acc, uint32_t op, uint64_t dB, bool fresh) {
@@ -263,16 +260,16 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                         if (n > 0) ok = warp_wait(smem_u32(&bar->s_free), (n - 1) & 1, abort_flag, a);
                         if (!ok) break;
                         tc_fence_after();
-                        mma_half(0, dX, dY1 + (s1.st * HALF >> 4));
+                        mma_half(0, dX, dY1 + (s1.st * HALF >> 4), true);
                         commit(leader, smem_u32(&bar->s_full[0]));
                         s1.next();
                         if (n >= 2) ok = warp_wait(smem_u32(&bar->dp_free[sb.st]), sb.parity ^ 1, abort_flag, a);
-                        for (int h = 0; ok && h < 4; h++) {
+                        for (int h = 0; ok && h < 2; h++) {
                             ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
                             if (!ok) break;
-                            if (KEYS) clear_rows(ring2 + s2.st * REGION, it, 1);  // v only enters dP, which the mask covers
+                            if (KEYS) clear_rows(ring2 + s2.st * HALF, it);  // v only enters dP, which the mask covers
                             tc_fence_after();
-                            mma_cols(C::TM_DP + sb.st * 128, dX + ((2 + h) * REGION >> 4), dY2 + (s2.st * REGION >> 4), h == 0);
+                            mma_half(C::TM_DP + sb.st * 128, dX + ((1 + h) * HALF >> 4), dY2 + (s2.st * HALF >> 4), h == 0);
                             commit(leader, smem_u32(&bar->y2_empty[s2.st]));
                             s2.next();
                         }
@@ -297,8 +294,8 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                     if (ok) commit(leader, smem_u32(&bar->acc_full));
                 }
             } else if (warp == kWarps) {
-                // S of the first map waits for the product that uses up what lies over it;
-                // S of the second is made as soon as the last one is read.
+                // S of the first map is made as soon as the last one is read, S of the second behind
+                // the product that uses up what lies over it.
                 Stage<C::N1> s1;
                 Stage<C::N2> s2;
                 ok = ok && warp_wait(smem_u32(&bar->x_full), 0, abort_flag, a);
@@ -306,7 +303,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                     if (!warp_wait(smem_u32(&bar->y1_full[s1.st]), s1.parity, abort_flag, a)) return false;
                     clear_rows(ring1 + s1.st * HALF, it);
                     tc_fence_after();
-                    mma_half(i * 128, dX + (i * HALF >> 4), dY1 + (s1.st * HALF >> 4));
+                    mma_half(i * 128, dX + (i * HALF >> 4), dY1 + (s1.st * HALF >> 4), true);
                     commit(leader, smem_u32(&bar->s_full[i]));
                     commit(leader, smem_u32(&bar->y1_empty[s1.st]));
                     s1.next();
@@ -318,19 +315,19 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                 for (bool fresh = true; ok; fresh = false, n++) {
                     ahead.next(a);
                     const bool more = !ahead.done();
-                    ok = warp_wait(smem_u32(&bar->ready[0]), n & 1, abort_flag, a);
+                    if (more) ok = warp_wait(smem_u32(&bar->s_free), n & 1, abort_flag, a) && issue_S(0, ahead);
+                    ok = ok && warp_wait(smem_u32(&bar->ready[0]), n & 1, abort_flag, a);
                     for (int h = 0; ok && h < 2; h++) {
                         ok = warp_wait(smem_u32(&bar->y2_full[s2.st]), s2.parity, abort_flag, a);
                         if (!ok) break;
                         clear_rows(ring2 + s2.st * HALF, it);
                         tc_fence_after();
-                        issue_sum(C::TM_ACC + 128 * h, 0, dM2 + (s2.st * HALF >> 4), fresh);
+                        issue_sum(C::TM_ACC + 128 * h, 128, dM2 + (s2.st * HALF >> 4), fresh);
                         commit(leader, smem_u32(&bar->y2_empty[s2.st]));
                         s2.next();
                     }
                     if (!ok || !more) break;
-                    // both scores of this tile were read before `ready`
-                    ok = issue_S(0, ahead) && issue_S(1, ahead);
+                    ok = issue_S(1, ahead);
                     it = ahead;
                 }
                 if (ok) commit(leader, smem_u32(&bar->acc_full));
@@ -409,6 +406,8 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                 tc_fence_after();
                 tmem_ld32_nowait(tS, p);
                 tmem_wait_ld();
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->s_free), lane);
                 weights(p, 0ull, st);
                 bar_wait(smem_u32(&bar->s_full[1]), n & 1, abort_flag, a);
                 tc_fence_after();
@@ -428,7 +427,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
 #pragma unroll
                 for (int c = 0; c < kCols; c += 2)
                     o[c >> 1] = pack_bf16x2(__uint_as_float(p[c]) - __uint_as_float(s[c]), __uint_as_float(p[c + 1]) - __uint_as_float(s[c + 1]));
-                tmem_st16(tS, o);
+                tmem_st16(tS + 128, o);
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->ready[0]), lane);
