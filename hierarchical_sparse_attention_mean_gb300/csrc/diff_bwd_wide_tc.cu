@@ -353,164 +353,180 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
         uint32_t n = 0;
         float lam = 0.f;
         int kend = 0;
-        // 2^(scale log2(e) s + nl2) in place
-        auto weights = [&](uint32_t* v, uint64_t l0, const float* st) {
+        // Keys read tensor memory as fragments: registers 16 h + 4 i + 2 e + k of a tile are column
+        // w kCols + fc + 8 i + k, row fr + 16 h + 8 e, so that a thread needs the numbers of 8
+        // columns and not of 32: shared memory, where they are, is kept busy by the products.
+        const int fr = (warp & 3) * 32 + (lane >> 2), fc = 2 * (lane & 3);
+        const uint32_t low = 16u << 16;  // the second 16 lanes
+        auto pair = [](const uint32_t* v) { return pack2(__uint_as_float(v[0]), __uint_as_float(v[1])); };
+        auto put = [](uint32_t* v, uint64_t y) {
+            float e0, e1;
+            unpack2(y, e0, e1);
+            v[0] = __float_as_uint(e0);
+            v[1] = __float_as_uint(e1);
+        };
+        auto read = [&](uint32_t at, uint32_t* v) {
+            tmem_ld_frag(at, v);
+            tmem_ld_frag(at + low, v + 16);
+            tmem_wait_ld();
+        };
+        auto write = [&](uint32_t at, const uint32_t* v) {
+            tmem_st_frag16(at, v);
+            tmem_st_frag16(at + low, v + 8);
+            tmem_wait_st();
+        };
+        // 2^(scale log2(e) s + nl2) in place, nl2 of the tile's rows from `st` on
+        auto weights = [&](uint32_t* v, const float* st) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                uint64_t la = l0, lb = l0;
-                if (KEYS) {
-                    const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + c);
-                    la = u.x;
-                    lb = u.y;
+            for (int c = 0; c < 16; c += 4) {
+                const uint64_t l = *reinterpret_cast<const uint64_t*>(st + 2 * c);
+#pragma unroll
+                for (int x = c; x < 32; x += (x & 2) ? 14 : 2) {
+                    float e0, e1;
+                    unpack2(fma2(pair(v + x), sl2x2, l), e0, e1);
+                    v[x] = __float_as_uint(ex2(e0));
+                    v[x + 1] = __float_as_uint(ex2(e1));
                 }
-                float e0, e1, e2, e3;
-                unpack2(fma2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sl2x2, la), e0, e1);
-                unpack2(fma2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), sl2x2, lb), e2, e3);
-                v[c] = __float_as_uint(ex2(e0));
-                v[c + 1] = __float_as_uint(ex2(e1));
-                v[c + 2] = __float_as_uint(ex2(e2));
-                v[c + 3] = __float_as_uint(ex2(e3));
             }
         };
-        // v times lam of these columns' rows, from row `pos` on
+        // v times lam of the tile's rows, from row `pos` on
         auto times_lam = [&](uint32_t* v, int pos) {
 #pragma unroll
-            for (int c = 0; c < kCols; c += 4) {
-                uint64_t la = pack2(lam, lam), lb = la;
+            for (int c = 0; c < 16; c += 4) {
+                uint64_t l = pack2(lam, lam);
                 if (!one_head) {
-                    const float4 u = __ldg(reinterpret_cast<const float4*>(lams + pos + w * kCols + c));
-                    la = pack2(u.x, u.y);
-                    lb = pack2(u.z, u.w);
+                    const float2 u = __ldg(reinterpret_cast<const float2*>(lams + pos + w * kCols + fc + 2 * c));
+                    l = pack2(u.x, u.y);
                 }
-                float e0, e1, e2, e3;
-                unpack2(mul2(pack2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), la), e0, e1);
-                unpack2(mul2(pack2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])), lb), e2, e3);
-                v[c] = __float_as_uint(e0);
-                v[c + 1] = __float_as_uint(e1);
-                v[c + 2] = __float_as_uint(e2);
-                v[c + 3] = __float_as_uint(e3);
+#pragma unroll
+                for (int x = c; x < 32; x += (x & 2) ? 14 : 2) put(v + x, mul2(pair(v + x), l));
             }
         };
-        // the lengths are in l2; causal order cuts where a row's keys end inside the block's keys
-        auto cut = [&](const Items<KEYS>& it) {
-            return a.causal && (it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT);
+        // The lengths are in l2; causal order cuts where a row's keys end inside the block's keys.
+        auto cut = [&](const Items<KEYS>& it, uint32_t* v, uint32_t* u) {
+            if (!a.causal || !(it.t0 + BT > a.nq || dense_kend(a, sp, it.t0) < x0 + BT)) return;
+#pragma unroll
+            for (int c = 0; c < 16; c += 4)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    const int last = (it.t0 + w * kCols + fc + 2 * c + k) % a.nq + sp.lk - sp.lq;  // key that this column's row sees last
+#pragma unroll
+                    for (int y = 0; y < 4; y++)
+                        if (x0 + fr + 8 * y > last) v[16 * (y >> 1) + c + 2 * (y & 1) + k] = u[16 * (y >> 1) + c + 2 * (y & 1) + k] = 0u;
+                }
         };
         if (KEYS && one_head) lam = diff_lam(f, diff_head(f, slice, 0));
         if constexpr (KIND == kDv) {
             for (Items<KEYS> it = first; !it.done(); it.next(a), n++) {
                 const int k = n & 1;
-                const float* st = stats + k * 2 * BT + w * kCols;
+                const float* st = stats + k * 2 * BT + w * kCols + fc;
                 bar_wait(smem_u32(&bar->st_full[k]), (n / 2) & 1, abort_flag, a);
                 uint32_t p[kCols], s[kCols], o[kCols / 2];
                 bar_wait(smem_u32(&bar->s_full[0]), n & 1, abort_flag, a);
                 tc_fence_after();
-                tmem_ld32_nowait(tS, p);
-                tmem_wait_ld();
+                read(tS, p);
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->s_free), lane);
-                weights(p, 0ull, st);
+                weights(p, st);
                 bar_wait(smem_u32(&bar->s_full[1]), n & 1, abort_flag, a);
                 tc_fence_after();
-                tmem_ld32_nowait(tS + 128, s);
-                tmem_wait_ld();
-                weights(s, 0ull, st + BT);
+                read(tS + 128, s);
+                weights(s, st + BT);
                 warp_arrive(smem_u32(&bar->st_empty[k]), lane);
                 times_lam(s, it.pos);
-                if (cut(it)) {
-                    int t = (it.t0 + w * kCols) % a.nq;
-#pragma unroll
-                    for (int c = 0; c < kCols; c++) {
-                        if (x > t + sp.lk - sp.lq) p[c] = s[c] = 0u;
-                        if (++t == a.nq) t = 0;
-                    }
-                }
+                cut(it, p, s);
 #pragma unroll
                 for (int c = 0; c < kCols; c += 2)
                     o[c >> 1] = pack_bf16x2(__uint_as_float(p[c]) - __uint_as_float(s[c]), __uint_as_float(p[c + 1]) - __uint_as_float(s[c + 1]));
-                tmem_st16(tS + 128, o);
-                tmem_wait_st();
+                write(tS + 128, o);
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->ready[0]), lane);
             }
-        } else {
-            uint64_t nl2x2 = 0ull, ndx2 = 0ull, sum2 = 0ull;
-            if constexpr (!KEYS) {
-                const long long row = (long long)slice * a.Rp + x;  // Rp is a multiple of 128
-                const float nl = a.nl2[map * all + row], nd = a.nl2[(2 + map) * all + row];
-                nl2x2 = pack2(nl, nl);
-                ndx2 = pack2(nd, nd);
-                lam = a.nl2[4 * all + row];
-                kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
-            }
+        } else if constexpr (KIND == kDk) {
             Stage<2> sb;
             for (Items<KEYS> it = first; !it.done(); it.next(a), n++) {
                 const int k = n & 1;
-                const float* st = stats + k * 2 * BT + w * kCols;  // KEYS: -l2 of these columns' rows; -D BT further
+                const float* st = stats + k * 2 * BT + w * kCols + fc;  // -l2 of these columns' rows; -D BT further
                 const uint32_t tG = tS + C::TM_DP + sb.st * 128;
-                uint32_t s[kCols], g[kCols];
-                if (KEYS) bar_wait(smem_u32(&bar->st_full[k]), (n / 2) & 1, abort_flag, a);
+                uint32_t s[kCols], g[kCols], o[kCols / 2];
+                bar_wait(smem_u32(&bar->st_full[k]), (n / 2) & 1, abort_flag, a);
+                bar_wait(smem_u32(&bar->s_full[0]), n & 1, abort_flag, a);
+                tc_fence_after();
+                read(tS, s);
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->s_free), lane);
+                weights(s, st);
+                if (map == 1 && !one_head) times_lam(s, it.pos);
+                cut(it, s, s);
+                bar_wait(smem_u32(&bar->dp_full[sb.st]), sb.parity, abort_flag, a);
+                tc_fence_after();
+                read(tG, g);
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                    const uint64_t nd = *reinterpret_cast<const uint64_t*>(st + BT + 2 * c);
+#pragma unroll
+                    for (int x = c; x < 32; x += (x & 2) ? 14 : 2) {
+                        float e0, e1;
+                        unpack2(mul2(add2(pair(g + x), nd), pair(s + x)), e0, e1);
+                        o[x >> 1] = pack_bf16x2(e0, e1);
+                    }
+                }
+                write(tG, o);
+                tc_fence_before();
+                warp_arrive(smem_u32(&bar->st_empty[k]), lane);
+                warp_arrive(smem_u32(&bar->ready[sb.st]), lane);
+                sb.next();
+            }
+        } else {
+            const long long row = (long long)slice * a.Rp + x;  // Rp is a multiple of 128
+            const float nl = a.nl2[map * all + row], nd = a.nl2[(2 + map) * all + row];
+            const uint64_t nl2x2 = pack2(nl, nl), ndx2 = pack2(nd, nd);
+            uint64_t sum2 = 0ull;
+            lam = a.nl2[4 * all + row];
+            kend = x < a.R ? dense_kend(a, sp, x < a.nq ? x : x % a.nq) : 0;
+            Stage<2> sb;
+            for (Items<KEYS> it = first; !it.done(); it.next(a), n++) {
+                const uint32_t tG = tS + C::TM_DP + sb.st * 128;
+                uint32_t s[kCols], g[kCols], o[kCols / 2];
                 bar_wait(smem_u32(&bar->s_full[0]), n & 1, abort_flag, a);
                 tc_fence_after();
                 tmem_ld32_nowait(tS, s);
                 tmem_wait_ld();
                 tc_fence_before();
                 warp_arrive(smem_u32(&bar->s_free), lane);
-                weights(s, nl2x2, st);
-                bool masked = false;
-                int lim = 0;
-                if constexpr (KEYS) {
-                    if (map == 1 && !one_head) times_lam(s, it.pos);
-                    if (cut(it)) {
-                        int t = (it.t0 + w * kCols) % a.nq;
 #pragma unroll
-                        for (int c = 0; c < kCols; c++) {
-                            if (x > t + sp.lk - sp.lq) s[c] = 0u;
-                            if (++t == a.nq) t = 0;
-                        }
-                    }
-                } else {
-                    masked = __any_sync(0xffffffffu, kend - it.pos < BT);
-                    lim = kend - it.pos - w * kCols;
+                for (int c = 0; c < kCols; c += 2) {
+                    float e0, e1;
+                    unpack2(fma2(pair(s + c), sl2x2, nl2x2), e0, e1);
+                    s[c] = __float_as_uint(ex2(e0));
+                    s[c + 1] = __float_as_uint(ex2(e1));
                 }
                 bar_wait(smem_u32(&bar->dp_full[sb.st]), sb.parity, abort_flag, a);
                 tc_fence_after();
                 tmem_ld32_nowait(tG, g);
                 tmem_wait_ld();
-                if (masked) {  // S and dP of a key behind the lengths may be anything
+                if (__any_sync(0xffffffffu, kend - it.pos < BT)) {  // S and dP of a key behind the lengths may be anything
+                    const int lim = kend - it.pos - w * kCols;
 #pragma unroll
                     for (int c = 0; c < kCols; c++) {
                         s[c] = c < lim ? s[c] : 0u;
                         g[c] = c < lim ? g[c] : 0u;
                     }
                 }
-                uint32_t o[kCols / 2];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 4) {
-                    uint64_t d0 = ndx2, d1 = ndx2;
-                    if (KEYS) {
-                        const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(st + BT + c);
-                        d0 = u.x;
-                        d1 = u.y;
-                    }
-                    const uint64_t p0 = pack2(__uint_as_float(s[c]), __uint_as_float(s[c + 1]));
-                    const uint64_t p1 = pack2(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
-                    const uint64_t g0 = pack2(__uint_as_float(g[c]), __uint_as_float(g[c + 1]));
-                    const uint64_t g1 = pack2(__uint_as_float(g[c + 2]), __uint_as_float(g[c + 3]));
-                    if (!KEYS && map == 1) sum2 = fma2(p0, g0, fma2(p1, g1, sum2));
-                    float e0, e1, e2, e3;
-                    unpack2(mul2(add2(g0, d0), p0), e0, e1);
-                    unpack2(mul2(add2(g1, d1), p1), e2, e3);
+                for (int c = 0; c < kCols; c += 2) {
+                    if (map == 1) sum2 = fma2(pair(s + c), pair(g + c), sum2);
+                    float e0, e1;
+                    unpack2(mul2(add2(pair(g + c), ndx2), pair(s + c)), e0, e1);
                     o[c >> 1] = pack_bf16x2(e0, e1);
-                    o[(c >> 1) + 1] = pack_bf16x2(e2, e3);
                 }
                 tmem_st16(tG, o);
                 tmem_wait_st();
                 tc_fence_before();
-                if (KEYS) warp_arrive(smem_u32(&bar->st_empty[k]), lane);
                 warp_arrive(smem_u32(&bar->ready[sb.st]), lane);
                 sb.next();
             }
-            if (!KEYS && map == 1) {
+            if (map == 1) {
                 // P_2 dP of this part's keys, a quarter of the columns each
                 float u0, u1;
                 unpack2(sum2, u0, u1);
