@@ -164,65 +164,75 @@ __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_co
 
 // ------------------------------------------------------ join of a split --
 
-// o, o2 and lse of every row from the parts of a split over the keys: a warp per row, the
-// weights of 32 parts worked out at once, a lane each, then part after part with the
-// loads of several in flight.
+// o, o2 and lse of every row from the parts of a split over the keys: a block per row, four
+// warps per map, each with every fourth part. Rows are few where keys are split, so it is
+// the latency of the parts that this costs (a warp per row, part after part: 35 us for 6 rows
+// of 50 parts).
+constexpr int kJoinSets = kThreads / 64;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_constant__ DiffArgs f) {
     const DenseArgs& a = f.d;
-    const long long rows = (long long)a.slices * a.R;
-    const long long row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-    const int lane = threadIdx.x & 31, dv = 2 * a.d;
-    if (row >= rows) return;
+    const long long row = blockIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp & 1, set = warp >> 1, dv = 2 * a.d;
     const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
     const float2* ml = diff_part_ml(a);
-    float acc[2][2][4] = {};
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        float m = -INFINITY, l = 0.f;
-        for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[diff_part(a, p, i, row)].x);
-        m = warp_max(m);
-        const float shift = m == -INFINITY ? 0.f : m;
-        for (int p = lane; p < a.splits; p += 32) {
-            const float2 x = ml[diff_part(a, p, i, row)];
-            l = fmaf(x.y, exp2f(x.x - shift), l);
-        }
-        l = warp_sum(l);
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        for (int p0 = 0; p0 < a.splits; p0 += 32) {
-            const float w = p0 + lane < a.splits ? exp2f(ml[diff_part(a, p0 + lane, i, row)].x - shift) : 0.f;
-            const int n = min(32, a.splits - p0);
+    __shared__ float4 sums[2][kJoinSets][64];
+    float m = -INFINITY, l = 0.f;
+    for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[diff_part(a, p, i, row)].x);
+    m = warp_max(m);
+    const float shift = m == -INFINITY ? 0.f : m;
+    for (int p = lane; p < a.splits; p += 32) {
+        const float2 x = ml[diff_part(a, p, i, row)];
+        l = fmaf(x.y, exp2f(x.x - shift), l);
+    }
+    l = warp_sum(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    float acc[2][4] = {};
+    for (int p0 = set; p0 < a.splits; p0 += 32 * kJoinSets) {
+        const int mine = p0 + lane * kJoinSets;
+        const float w = mine < a.splits ? exp2f(ml[diff_part(a, mine, i, row)].x - shift) * inv : 0.f;
+        const int n = min(32, (a.splits - p0 + kJoinSets - 1) / kJoinSets);
 #pragma unroll 8
-            for (int x = 0; x < n; x++) {
-                const float wx = __shfl_sync(0xffffffffu, w, x);
-                const float* from = a.part + diff_part(a, p0 + x, i, row) * dv + lane * 4;
+        for (int x = 0; x < n; x++) {
+            const float wx = __shfl_sync(0xffffffffu, w, x);
+            const float* from = a.part + diff_part(a, p0 + x * kJoinSets, i, row) * dv + lane * 4;
 #pragma unroll
-                for (int k = 0; k < 2; k++)
-                    if (lane * 4 + 128 * k < dv) {
-                        const float4 y = *reinterpret_cast<const float4*>(from + 128 * k);
-                        acc[i][k][0] = fmaf(wx, y.x, acc[i][k][0]);
-                        acc[i][k][1] = fmaf(wx, y.y, acc[i][k][1]);
-                        acc[i][k][2] = fmaf(wx, y.z, acc[i][k][2]);
-                        acc[i][k][3] = fmaf(wx, y.w, acc[i][k][3]);
-                    }
-            }
+            for (int k = 0; k < 2; k++)
+                if (lane * 4 + 128 * k < dv) {
+                    const float4 y = *reinterpret_cast<const float4*>(from + 128 * k);
+                    acc[k][0] = fmaf(wx, y.x, acc[k][0]);
+                    acc[k][1] = fmaf(wx, y.y, acc[k][1]);
+                    acc[k][2] = fmaf(wx, y.z, acc[k][2]);
+                    acc[k][3] = fmaf(wx, y.w, acc[k][3]);
+                }
         }
-#pragma unroll
-        for (int k = 0; k < 2; k++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) acc[i][k][e] *= inv;
-        if (lane == 0) a.lse_out[diff_row(f, slice, i, r)] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
     }
+#pragma unroll
+    for (int k = 0; k < 2; k++) sums[i][set][lane + 32 * k] = make_float4(acc[k][0], acc[k][1], acc[k][2], acc[k][3]);
+    if (set == 0 && lane == 0) a.lse_out[diff_row(f, slice, i, r)] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
+    __syncthreads();
+    const int c = threadIdx.x * 4;
+    if (c >= dv) return;
     const float lam = diff_lam(f, diff_head(f, slice, r));
+    float y[2][4];
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
-        const int c = lane * 4 + 128 * k;
-        if (c >= dv) break;
-        if (f.o2_out) store4(static_cast<T*>(f.o2_out) + row * dv + c, acc[1][k]);
+    for (int i2 = 0; i2 < 2; i2++) {
+        float4 t = sums[i2][0][threadIdx.x];
 #pragma unroll
-        for (int e = 0; e < 4; e++) acc[0][k][e] = fmaf(-lam, acc[1][k][e], acc[0][k][e]);
-        store4(static_cast<T*>(a.o_out) + row * dv + c, acc[0][k]);
+        for (int s = 1; s < kJoinSets; s++) {
+            const float4 u = sums[i2][s][threadIdx.x];
+            t.x += u.x;
+            t.y += u.y;
+            t.z += u.z;
+            t.w += u.w;
+        }
+        y[i2][0] = t.x, y[i2][1] = t.y, y[i2][2] = t.z, y[i2][3] = t.w;
     }
+    if (f.o2_out) store4(static_cast<T*>(f.o2_out) + row * dv + c, y[1]);
+#pragma unroll
+    for (int e = 0; e < 4; e++) y[0][e] = fmaf(-lam, y[1][e], y[0][e]);
+    store4(static_cast<T*>(a.o_out) + row * dv + c, y[0]);
 }
 
 // ------------------------------------------------------ per-row numbers --
@@ -347,7 +357,9 @@ __global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constan
 
 // dlam of a head from d2, `sets` sums of P_2 dP of every row: part p of `parts` of its
 // rows to part[h parts + p], or with one part to dlam itself.
-__global__ void __launch_bounds__(kThreads) diff_lam_rows_kernel(const __grid_constant__ DiffArgs f, float* part, int parts, int sets,
+constexpr int kLamThreads = 1024;
+
+__global__ void __launch_bounds__(kLamThreads) diff_lam_rows_kernel(const __grid_constant__ DiffArgs f, float* part, int parts, int sets,
                                                                  void* out) {
     const DenseArgs& a = f.d;
     const int h = blockIdx.x / parts, p = blockIdx.x - h * parts;
@@ -355,18 +367,18 @@ __global__ void __launch_bounds__(kThreads) diff_lam_rows_kernel(const __grid_co
     const long long rows = (long long)batch * a.nq, first = rows * p / parts, last = rows * (p + 1) / parts;
     const long long all = (long long)a.slices * a.Rp;
     float sum = 0.f;
-    for (long long row = first + threadIdx.x; row < last; row += kThreads) {
+    for (long long row = first + threadIdx.x; row < last; row += kLamThreads) {
         const int b = (int)(row / a.nq), t = (int)(row - (long long)b * a.nq);
         const float* from = f.d2 + ((long long)b * a.kv_heads + g) * a.Rp + (long long)(h - g * G) * a.nq + t;
 #pragma unroll 4
         for (int i = 0; i < sets; i++) sum += from[i * all];
     }
-    __shared__ float warps[kThreads / 32];
+    __shared__ float warps[kLamThreads / 32];
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
     __syncthreads();
     if (threadIdx.x != 0) return;
-    for (int i = 1; i < kThreads / 32; i++) sum += warps[i];
+    for (int i = 1; i < kLamThreads / 32; i++) sum += warps[i];
     if (parts > 1) part[blockIdx.x] = sum;
     else if (f.lam_bf16) static_cast<__nv_bfloat16*>(out)[h] = __float2bfloat16_rn(-sum);
     else static_cast<float*>(out)[h] = -sum;
@@ -519,11 +531,19 @@ int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, v
 size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam_parts(s) * sizeof(float)) : 0; }
 
 // Which kernels take a call.
-enum class Path { kTc, kFour };
+enum class Path { kFew, kTc, kFour };
 
-Path fwd_path(const DiffShape& s) { return diff_tc_supported(s) ? Path::kTc : Path::kFour; }
+Path fwd_path(const DiffShape& s) {
+    return diff_few_supported(s) ? Path::kFew : diff_tc_supported(s) ? Path::kTc : Path::kFour;
+}
 
-DenseSplit fwd_split(const DiffShape& s) { return fwd_path(s) == Path::kTc ? diff_tc_fwd_split(s) : DenseSplit{1, s.nk}; }
+DenseSplit fwd_split(const DiffShape& s) {
+    switch (fwd_path(s)) {
+        case Path::kFew: return diff_few_split(s);
+        case Path::kTc: return diff_tc_fwd_split(s);
+        default: return {1, s.nk};
+    }
+}
 
 size_t fwd_workspace(const DiffShape& s) {
     if (s.R == 0) return 0;
@@ -538,9 +558,9 @@ int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     a.d.splits = p.splits;
     a.d.chunk = p.chunk;
     a.d.part = static_cast<float*>(ws);
-    LLSA_TRY(launch_diff_tc_fwd(s, a, st));
+    LLSA_TRY(path == Path::kFew ? launch_diff_few(s, a, st) : launch_diff_tc_fwd(s, a, st));
     if (p.splits > 1) {
-        const unsigned blocks = (unsigned)(((long long)s.slices * s.R + kThreads / 32 - 1) / (kThreads / 32));
+        const unsigned blocks = (unsigned)((long long)s.slices * s.R);  // few: blocks would do without a split otherwise
         if (bf16) LLSA_LAUNCH("diff_join", st, diff_join_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
         else LLSA_LAUNCH("diff_join", st, diff_join_kernel<float><<<blocks, kThreads, 0, st>>>(a));
     }
@@ -597,7 +617,7 @@ int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, 
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("diff_rows", st, diff_rows_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a));
     LLSA_TRY(launch_diff_tc_bwd(s, aq, ak, st));
-    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * t.lam_parts, kThreads, 0, st>>>(a, lam, t.lam_parts,
+    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * t.lam_parts, kLamThreads, 0, st>>>(a, lam, t.lam_parts,
                                                                                                                  4 * t.q.splits, dlam));
     if (t.lam_parts > 1)
         LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(lam, t.lam_parts, dlam, a.lam_bf16));

@@ -432,7 +432,6 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                 tc_fence_after();
                 read(tS + 128, s);
                 weights(s, st + BT);
-                warp_arrive(smem_u32(&bar->st_empty[k]), lane);
                 times_lam(s, it.pos);
                 cut(it, p, s);
 #pragma unroll
@@ -440,6 +439,9 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                     o[c >> 1] = pack_bf16x2(__uint_as_float(p[c]) - __uint_as_float(s[c]), __uint_as_float(p[c + 1]) - __uint_as_float(s[c + 1]));
                 write(tS + 128, o);
                 tc_fence_before();
+                // only now: an arrival right behind the loads has overtaken the last of them, and
+                // the next copy was there first
+                warp_arrive(smem_u32(&bar->st_empty[k]), lane);
                 warp_arrive(smem_u32(&bar->ready[0]), lane);
             }
         } else if constexpr (KIND == kDk) {
