@@ -60,7 +60,7 @@ inline size_t diff_part_bytes(const DiffShape& s, int splits) {
     return splits > 1 ? (size_t)splits * 2 * s.slices * s.R * (2 * s.d + 2) * sizeof(float) : 0;
 }
 
-// diff_few.cu: forward of one or two rows per value head.
+// diff_few.cu: forward of a few rows per value head.
 bool diff_few_supported(const DiffShape& s);
 DenseSplit diff_few_split(const DiffShape& s);
 int launch_diff_few(const DiffShape& s, const DiffArgs& a, cudaStream_t st);

@@ -1,6 +1,6 @@
-// diff_few.cu -- differential attention forward for one or two query rows per value head
-// (single tokens, pooling queries): both maps' keys and the values are read once, on the
-// CUDA cores.
+// diff_few.cu -- differential attention forward for a few query rows per value head (single
+// tokens, their shared-value heads, pooling queries): both maps' keys and the values are read
+// once, on the CUDA cores.
 //
 // Mathematics: one pass over the keys with a running maximum and sum for each map; a key's
 // two weights meet its value while that is in registers. The keys of a slice are split
@@ -8,200 +8,234 @@
 // maxima, sums and outputs, joined at the end in a fixed order, and the maps' difference
 // is formed in fp32 there.
 //
-// Bound by HBM: 12 d flops per key and row against 8 d bytes per key (bf16). A group of 8 or
-// 16 lanes holds one key, 8 columns of each map's key and 16 of the value per lane, and
-// the next keys are in flight while these are used.
+// Bound by HBM: 12 d flops per key and row against 8 d bytes per key (bf16). Keys and values
+// of consecutive tokens lie next to each other, so a stage of 32 KB is three bulk copies,
+// and a block per SM keeps six of them in flight; with the loads in registers instead, as
+// many as fit, 6 heads x 65,536 keys of 64 columns took 49 us. A group of 8 or 16 lanes
+// takes one key, 8 columns of each map's key and 16 of the value per lane.
 #include <algorithm>
 
+#include "dense_tc.cuh"
 #include "diff.h"
 
 namespace llsa {
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+using namespace tc;
 
-// Eight values as they lie in memory, and as fp32.
-template <typename T>
-struct Raw {
-    uint4 w[sizeof(T) / 2];
-    __device__ __forceinline__ void load(const T* p) {
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); i++) w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
-    }
-    __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (int i = 0; i < (int)(sizeof(T) / 2); i++) w[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    __device__ __forceinline__ void get(float* f) const {
-        if constexpr (sizeof(T) == 2) {
-            const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                f[2 * i] = __uint_as_float(u[i] << 16);
-                f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
-        } else {
-            const float* h = reinterpret_cast<const float*>(w);
-#pragma unroll
-            for (int i = 0; i < 8; i++) f[i] = h[i];
-        }
-    }
+// Warps that take keys (one more copies): what hides the latency of a key's chain of
+// products, shuffles and exponentials. Two rows take 153 registers a thread.
+template <int RR>
+constexpr int kFewWarps = RR == 1 ? 16 : 8;
+constexpr int kStage = 32 * 1024, kStages = 6;
+
+struct FewBars {
+    uint64_t full[kStages], empty[kStages];
+    int abort_flag;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
+// Eight values from shared memory as fp32.
+__device__ __forceinline__ void get8(const __nv_bfloat16* p, float* f) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void get8(const float* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + i);
+        f[i] = x.x;
+        f[i + 1] = x.y;
+        f[i + 2] = x.z;
+        f[i + 3] = x.w;
+    }
 }
 
 template <typename T, int RR, int LANES>
-__global__ void __launch_bounds__(kThreads) diff_few_kernel(const __grid_constant__ DiffArgs f) {
+__global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(const __grid_constant__ DiffArgs f) {
     const DenseArgs& a = f.d;
-    constexpr int GROUPS = 32 / LANES;
-    constexpr int U = (sizeof(T) == 2 ? 8 : 4) / RR;  // keys per group of lanes in flight
-    constexpr int VC = LANES * 8;                     // columns of half a value
-    extern __shared__ float sm[];
-    float* sO = sm;                                                           // [kWarps][RR][2][2 VC]
-    float2* sML = reinterpret_cast<float2*>(sm + kWarps * RR * 2 * 2 * VC);  // [kWarps][RR][2]
+    constexpr int kWarps = kFewWarps<RR>, kThreads = (kWarps + 1) * 32;
+    constexpr int GROUPS = 32 / LANES, VC = LANES * 8;      // keys of a warp at a time; columns of half a value
+    constexpr int KS = kStage / (4 * VC * (int)sizeof(T));  // keys of a stage
+    extern __shared__ __align__(128) unsigned char sm[];
+    T* ring = reinterpret_cast<T*>(sm);  // per stage: KS rows of each map's keys, then of the values
+    FewBars* bar = reinterpret_cast<FewBars*>(sm + kStages * kStage);
+    volatile int* abort_flag = &bar->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int grp = lane / LANES, col = (lane % LANES) * 8;
     const int slice = blockIdx.x / a.splits, part = blockIdx.x - slice * a.splits;
     const DenseSpan sp = dense_span(a, slice);
     const int dv = 2 * a.d;
-    const bool on = col < a.d, on1 = col < dv, on2 = VC + col < dv;
-    const float sl2 = a.scale * kDenseLog2e;
-    float q[RR][2][8], acc[RR][2][16], m[RR][2], l[RR][2];
     int kend[RR], most = 0;
 #pragma unroll
     for (int r = 0; r < RR; r++) {
         kend[r] = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
         most = max(most, kend[r]);
-#pragma unroll
-        for (int i = 0; i < 2; i++) {
-            m[r][i] = -INFINITY;
-            l[r][i] = 0.f;
-#pragma unroll
-            for (int c = 0; c < 8; c++) q[r][i][c] = acc[r][i][c] = acc[r][i][c + 8] = 0.f;
-            if (on && kend[r] > 0) {
-                load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r) * a.d + col, q[r][i]);
-#pragma unroll
-                for (int c = 0; c < 8; c++) q[r][i][c] *= sl2;
-            }
-        }
     }
     const int first = part * a.chunk;
     const int stop = min(most, a.splits > 1 ? first + a.chunk : a.nk);
-    const int b = slice / a.kv_heads;
-    const T* k0 = static_cast<const T*>(a.k) + ((long long)slice + (long long)b * a.kv_heads) * a.nk * a.d + col;
-    const T* k1 = k0 + (long long)a.kv_heads * a.nk * a.d;
-    const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * dv + col;
-    constexpr int STEP = kWarps * GROUPS;  // keys between a group's keys
-    Raw<T> kr[U][2], vr[U][2];
-    auto fetch = [&](int u, int j) {
-        const bool here = j < stop;
-        if (here && on) {
-            kr[u][0].load(k0 + (long long)j * a.d);
-            kr[u][1].load(k1 + (long long)j * a.d);
-        } else {
-            kr[u][0].zero();
-            kr[u][1].zero();
+    const int n = stop > first ? (stop - first + KS - 1) / KS : 0;  // stages
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; i++) {
+            mbar_init(smem_u32(&bar->full[i]), 1);
+            mbar_init(smem_u32(&bar->empty[i]), kWarps);
         }
-        if (here && on1) vr[u][0].load(v + (long long)j * dv);
-        else vr[u][0].zero();
-        if (here && on2) vr[u][1].load(v + (long long)j * dv + VC);
-        else vr[u][1].zero();
-    };
-    const int mine = first + warp * GROUPS + grp;
+        bar->abort_flag = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const int grp = lane / LANES, col = (lane % LANES) * 8;
+    float acc[RR][2][16], m[RR][2], l[RR][2];
+    if (warp == kWarps) {
+        // ----------------------------------------------------------- copies
+        if (lane == 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
+            const int b = slice / a.kv_heads;
+            const T* k0 = static_cast<const T*>(a.k) + ((long long)slice + (long long)b * a.kv_heads) * a.nk * a.d;
+            const T* k1 = k0 + (long long)a.kv_heads * a.nk * a.d;
+            const T* v = static_cast<const T*>(a.v) + (long long)slice * a.nk * dv;
+            Stage<kStages> s;
+            int filled = 0;
+            for (; filled < n; filled++, s.next()) {
+                if (filled >= kStages && !bar_wait(smem_u32(&bar->empty[s.st]), s.parity ^ 1, abort_flag, a)) break;
+                const long long j = first + filled * KS;
+                const uint32_t bytes = (uint32_t)(min(KS, stop - (int)j) * a.d * (int)sizeof(T));
+                const uint32_t to = smem_u32(sm + s.st * kStage), fb = smem_u32(&bar->full[s.st]);
+                mbar_arrive_expect_tx(fb, 4 * bytes);
+                bulk_load(to, k0 + j * a.d, bytes, fb);
+                bulk_load(to + kStage / 4, k1 + j * a.d, bytes, fb);
+                bulk_load(to + kStage / 2, v + j * dv, 2 * bytes, fb);
+            }
+            // copies still in flight must land before the block exits
+            for (int x = max(0, filled - kStages); x < filled; x++) land(smem_u32(&bar->full[x % kStages]), (x / kStages) & 1);
+        }
+    } else {
+        const bool on = col < a.d, on1 = col < dv, on2 = VC + col < dv;
+        const float sl2 = a.scale * kDenseLog2e;
+        float q[RR][2][8];
 #pragma unroll
-    for (int u = 0; u < U; u++) fetch(u, mine + u * STEP);
-    // Key after key, and each one's registers take its successor U keys further at once.
-    for (int j0 = mine; __any_sync(0xffffffffu, j0 < stop); j0 += U * STEP) {
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            const int j = j0 + u * STEP;
-            float s[RR][2], x[8];
+        for (int r = 0; r < RR; r++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                kr[u][i].get(x);
+                m[r][i] = -INFINITY;
+                l[r][i] = 0.f;
 #pragma unroll
-                for (int r = 0; r < RR; r++) {
-                    float t = q[r][i][0] * x[0];
+                for (int c = 0; c < 8; c++) q[r][i][c] = acc[r][i][c] = acc[r][i][c + 8] = 0.f;
+                if (on && kend[r] > 0) {
+                    load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r) * a.d + col, q[r][i]);
 #pragma unroll
-                    for (int c = 1; c < 8; c++) t = fmaf(q[r][i][c], x[c], t);
-                    s[r][i] = t;
+                    for (int c = 0; c < 8; c++) q[r][i][c] *= sl2;
                 }
             }
+        Stage<kStages> st;
+        int last = 0;
+        for (int t = 0; t < n; t++, st.next()) {
+            if (!warp_wait(smem_u32(&bar->full[st.st]), st.parity, abort_flag, a)) break;
+            const T* k0 = ring + (size_t)st.st * (kStage / sizeof(T));
+            const T *k1 = k0 + kStage / 4 / sizeof(T), *v = k0 + kStage / 2 / sizeof(T);
+            const int j0 = first + t * KS;
 #pragma unroll
-            for (int o = 1; o < LANES; o <<= 1)
-#pragma unroll
-                for (int r = 0; r < RR; r++)
-#pragma unroll
-                    for (int i = 0; i < 2; i++) s[r][i] += __shfl_xor_sync(0xffffffffu, s[r][i], o);
-            bool grow = false;
-#pragma unroll
-            for (int r = 0; r < RR; r++)
+            for (int x0 = 0; x0 < KS; x0 += kWarps * GROUPS) {
+                const int x = x0 + warp * GROUPS + grp, j = j0 + x;
+                const bool here = x < KS && j < stop;  // what lies behind it in the stage is of other keys
+                float s[RR][2], y[8];
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    if (j >= min(kend[r], stop)) s[r][i] = -INFINITY;
-                    grow |= s[r][i] > m[r][i];
+#pragma unroll
+                    for (int c = 0; c < 8; c++) y[c] = 0.f;
+                    if (here && on) get8((i ? k1 : k0) + x * a.d + col, y);
+#pragma unroll
+                    for (int r = 0; r < RR; r++) {
+                        float u = q[r][i][0] * y[0];
+#pragma unroll
+                        for (int c = 1; c < 8; c++) u = fmaf(q[r][i][c], y[c], u);
+                        s[r][i] = u;
+                    }
                 }
-            if (__any_sync(0xffffffffu, grow)) {  // rare behind the first keys
+#pragma unroll
+                for (int o = 1; o < LANES; o <<= 1)
+#pragma unroll
+                    for (int r = 0; r < RR; r++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++) s[r][i] += __shfl_xor_sync(0xffffffffu, s[r][i], o);
+                bool grow = false;
 #pragma unroll
                 for (int r = 0; r < RR; r++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const float top = fmaxf(m[r][i], s[r][i]), g = ex2(m[r][i] - (top == -INFINITY ? 0.f : top));
-                        m[r][i] = top;
-                        l[r][i] *= g;
-#pragma unroll
-                        for (int c = 0; c < 16; c++) acc[r][i][c] *= g;
+                        if (!here || j >= kend[r]) s[r][i] = -INFINITY;
+                        grow |= s[r][i] > m[r][i];
                     }
-            }
+                if (__any_sync(0xffffffffu, grow)) {  // rare behind the first keys
 #pragma unroll
-            for (int r = 0; r < RR; r++)
+                    for (int r = 0; r < RR; r++)
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    s[r][i] = ex2(s[r][i] - (m[r][i] == -INFINITY ? 0.f : m[r][i]));
-                    l[r][i] += s[r][i];
+                        for (int i = 0; i < 2; i++) {
+                            const float top = fmaxf(m[r][i], s[r][i]), g = ex2(m[r][i] - (top == -INFINITY ? 0.f : top));
+                            m[r][i] = top;
+                            l[r][i] *= g;
+#pragma unroll
+                            for (int c = 0; c < 16; c++) acc[r][i][c] *= g;
+                        }
                 }
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                vr[u][h].get(x);
 #pragma unroll
                 for (int r = 0; r < RR; r++)
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
+                    for (int i = 0; i < 2; i++) {
+                        s[r][i] = ex2(s[r][i] - (m[r][i] == -INFINITY ? 0.f : m[r][i]));
+                        l[r][i] += s[r][i];
+                    }
 #pragma unroll
-                        for (int c = 0; c < 8; c++) acc[r][i][8 * h + c] = fmaf(s[r][i], x[c], acc[r][i][8 * h + c]);
+                for (int h = 0; h < 2; h++) {
+#pragma unroll
+                    for (int c = 0; c < 8; c++) y[c] = 0.f;
+                    if (here && (h ? on2 : on1)) get8(v + x * dv + h * VC + col, y);
+#pragma unroll
+                    for (int r = 0; r < RR; r++)
+#pragma unroll
+                        for (int i = 0; i < 2; i++)
+#pragma unroll
+                            for (int c = 0; c < 8; c++) acc[r][i][8 * h + c] = fmaf(s[r][i], y[c], acc[r][i][8 * h + c]);
+                }
             }
-            fetch(u, j + U * STEP);
+            // An arrival right behind loads can overtake the last of them. So a stage is released in
+            // the next round, when what was read from it has been used.
+            if (t > 0) warp_arrive(smem_u32(&bar->empty[last]), lane);
+            last = st.st;
         }
     }
+    __syncthreads();  // the ring has been read: its place takes what is joined
+    float* sO = reinterpret_cast<float*>(sm);                                 // [kWarps][RR][2][2 VC]
+    float2* sML = reinterpret_cast<float2*>(sO + kWarps * RR * 2 * 2 * VC);  // [kWarps][RR][2]
     // the groups of a warp, then the warps, in a fixed order
+    if (warp < kWarps) {
 #pragma unroll
-    for (int r = 0; r < RR; r++)
+        for (int r = 0; r < RR; r++)
 #pragma unroll
-        for (int i = 0; i < 2; i++) {
+            for (int i = 0; i < 2; i++) {
 #pragma unroll
-            for (int o = LANES; o < 32; o <<= 1) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, m[r][i], o), l2 = __shfl_xor_sync(0xffffffffu, l[r][i], o);
-                const float top = fmaxf(m[r][i], m2), shift = top == -INFINITY ? 0.f : top;
-                const float f1 = ex2(m[r][i] - shift), f2 = ex2(m2 - shift);
-                m[r][i] = top;
-                l[r][i] = l[r][i] * f1 + l2 * f2;
+                for (int o = LANES; o < 32; o <<= 1) {
+                    const float m2 = __shfl_xor_sync(0xffffffffu, m[r][i], o), l2 = __shfl_xor_sync(0xffffffffu, l[r][i], o);
+                    const float top = fmaxf(m[r][i], m2), shift = top == -INFINITY ? 0.f : top;
+                    const float f1 = ex2(m[r][i] - shift), f2 = ex2(m2 - shift);
+                    m[r][i] = top;
+                    l[r][i] = l[r][i] * f1 + l2 * f2;
 #pragma unroll
-                for (int c = 0; c < 16; c++) acc[r][i][c] = acc[r][i][c] * f1 + __shfl_xor_sync(0xffffffffu, acc[r][i][c], o) * f2;
-            }
-            if (grp == 0) {
-                float* to = sO + ((warp * RR + r) * 2 + i) * 2 * VC;
-#pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    to[col + c] = acc[r][i][c];
-                    to[VC + col + c] = acc[r][i][8 + c];
+                    for (int c = 0; c < 16; c++) acc[r][i][c] = acc[r][i][c] * f1 + __shfl_xor_sync(0xffffffffu, acc[r][i][c], o) * f2;
                 }
-                if (lane == 0) sML[(warp * RR + r) * 2 + i] = make_float2(m[r][i], l[r][i]);
+                if (grp == 0) {
+                    float* to = sO + ((warp * RR + r) * 2 + i) * 2 * VC;
+#pragma unroll
+                    for (int c = 0; c < 8; c++) {
+                        to[col + c] = acc[r][i][c];
+                        to[VC + col + c] = acc[r][i][8 + c];
+                    }
+                    if (lane == 0) sML[(warp * RR + r) * 2 + i] = make_float2(m[r][i], l[r][i]);
+                }
             }
-        }
+    }
     __syncthreads();
     for (int x = threadIdx.x; x < RR * dv; x += kThreads) {
         const int r = x / dv, c = x - r * dv;
@@ -247,9 +281,10 @@ template <typename T, int RR, int LANES>
 int launch_lanes(const DiffArgs& a, cudaStream_t st) {
     const long long blocks = (long long)a.d.slices * a.d.splits;
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
-    constexpr int smem = kWarps * RR * 2 * (2 * LANES * 8 * (int)sizeof(float) + (int)sizeof(float2));
-    static_assert(smem <= 48 * 1024, "shared memory budget");
-    LLSA_LAUNCH("diff_few", st, diff_few_kernel<T, RR, LANES><<<(unsigned)blocks, kThreads, smem, st>>>(a));
+    constexpr int smem = kStages * kStage + (int)sizeof(FewBars);
+    static_assert(smem <= 227 * 1024 && kFewWarps<RR> * RR * 2 * (2 * LANES * 8 + 2) * 4 <= kStages * kStage, "shared memory budget");
+    cudaFuncSetAttribute(diff_few_kernel<T, RR, LANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    LLSA_LAUNCH("diff_few", st, diff_few_kernel<T, RR, LANES><<<(unsigned)blocks, (kFewWarps<RR> + 1) * 32, smem, st>>>(a));
     return LLSA_OK;
 }
 
@@ -263,10 +298,10 @@ int launch(const DiffShape& s, const DiffArgs& a, cudaStream_t st) {
 
 bool diff_few_supported(const DiffShape& s) { return s.R > 0 && s.R <= 2 && s.nk > 0; }
 
-// Parts for two blocks per SM; a part has at least 128 keys, a few rounds of its warps' loads.
+// Parts for one block per SM; a part has at least 128 keys, a few rounds of its warps.
 DenseSplit diff_few_split(const DiffShape& s) {
     DenseSplit p;
-    long long n = 2 * kDenseSms / std::max(1, s.slices);
+    long long n = kDenseSms / std::max(1, s.slices);
     n = std::max<long long>(1, std::min<long long>(n, s.nk / 128));
     p.chunk = (int)((s.nk + n - 1) / n);
     p.splits = (s.nk + p.chunk - 1) / p.chunk;
