@@ -1078,12 +1078,23 @@ def _wide(q, k):
             or (d <= _WIDE_COLUMNS and q.numel() * nk <= _WIDE_PAIRS * d))  # pairs of a query and a key
 
 
-def _positioned(rope, q, k, v, pos):
+# diff_attention with rope= is wide wherever that hides behind the call, whatever the columns: lam's
+# gradient is a sum of terms of both signs over all tokens, and with few heads it can come out as
+# small as what the rounding of turned q and k makes of it (0.007 to 0.011 off where the other
+# outputs are 0.003; in fp32 all are 0.0017). 2^23 pairs of 64 columns take the GPU 170 us.
+_WIDE_DIFF = (1 << 23) * 64
+
+
+def _wide_diff(q, k):
+    return _wide(q, k) or (q.dtype == torch.bfloat16 and q.numel() * k.shape[-2] <= _WIDE_DIFF)
+
+
+def _positioned(rope, q, k, v, pos, wide=_wide):
     """Contiguous q, k, v with the positions of `rope` (None: none) turned in, and the
     parameters that turn their gradients back."""
     if rope is None:
         q, k = _contiguous(q), _contiguous(k)
-    elif _wide(q, k):
+    elif wide(q, k):
         _check_rope(rope, q, k)
         for name, t, want in (("q", q, _tok_dtype(rope)), ("k", k, q.dtype), ("v", v, q.dtype)):
             if t.dtype != want:
@@ -1129,7 +1140,7 @@ def _dense_functions():
         @staticmethod
         def forward(ctx, q, k, v, lam, causal, scale, q_len, k_len, rope, pos):
             ctx.dtype = dtype = q.dtype
-            q, k, v, rope = _positioned(rope, q, k, v, pos)
+            q, k, v, rope = _positioned(rope, q, k, v, pos, _wide_diff)
             lam = _contiguous(lam)
             p = DiffParams.like(q, k, lam, causal=causal, scale=scale)
             o, lse, o2 = diff_forward(p, q, k, v, lam, q_len, k_len, backward=any(ctx.needs_input_grad))
@@ -1198,8 +1209,10 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     (softmax(q1 k1) - lam softmax(q2 k2)) v. q [batch, 2 heads, nq, d] and k [batch,
     2 kv_heads, nk, d] hold the first maps' heads, then the second maps'; v [batch,
     kv_heads, nk, 2d]; lam [heads], bf16 or fp32 whatever the type of the others, or
-    one number for all heads. q_len, k_len, rope, pos, roundings and captured backward
-    passes: as dense_attention (rope is for the heads of q and k as they are)."""
+    one number for all heads. q_len, k_len, rope, pos and captured backward passes: as
+    dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
+    in fp32 from the turn to the last rounding where that call's does, and up to 2^29
+    products of a pair of a query and a key (both maps' pairs times d)."""
     if isinstance(lam, torch.Tensor) and lam.numel() == 1 and q.shape[1] != 2:
         lam = lam.reshape(1).expand(q.shape[1] // 2)
     return _dense_fns()[2].apply(q, k, v, lam, causal, scale, q_len, k_len, rope, pos)

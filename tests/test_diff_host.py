@@ -124,3 +124,13 @@ def test_parameters_copy_and_pickle(lib):
     for y in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
         assert y == p and bytes(y.c()) == bytes(p.c())
     assert dataclasses.replace(p, nq=7).c().nq == 7 and p.c().nq == 100
+
+
+@pytest.mark.parametrize("b,h,n,d,wide", [
+    (1, 6, 64, 64, True), (1, 1, 2048, 64, True), (1, 1, 2049, 64, False), (1, 1, 1448, 128, True), (1, 1, 1449, 128, False),
+    (4, 16, 16, 128, True), (2, 6, 4096, 64, False), (1, 1, 16384, 8, True),
+])
+def test_where_positions_stay_in_fp32(b, h, n, d, wide):
+    q = torch.empty(b, 2 * h, n, d, dtype=torch.bfloat16, device="meta")
+    assert llsa._wide_diff(q, q) is wide
+    assert llsa._wide_diff(q.float(), q.float()) is False

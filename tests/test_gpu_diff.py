@@ -334,12 +334,13 @@ def _columns_sum(t, pairs):
 
 @pytest.mark.parametrize("extent,order,span", [((4, 8, 8), "raster", "axis"), ((1, 16, 16), "tile", "axis"), ((8, 4, 8), "raster", "dealt")])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
-def test_positions_attention_and_gradients_together(dtype, extent, order, span):
+def test_positions_attention_and_gradients_together(dtype, extent, order, span, monkeypatch):
     """Positions of a clip -> differential attention -> both backward passes, against the formulas in 64 bits."""
     b, h, kv, n, d, columns = 2, 4, 2, 256, 64, (16, 24, 24)
     x = make(b, h, kv, n, n, d, dtype, seed=6)
     leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v", "lam")]
     rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=columns, extent=extent, token_order=order, span=span)
+    monkeypatch.setattr(llsa, "_WIDE_DIFF", 0)  # bf16 in bf16, as at larger sizes
     o = llsa.diff_attention(*leaves, rope=rope)
     got = dict(zip(("o", "dq", "dk", "dv", "dlam"), (o, *torch.autograd.grad(o, leaves, x["dout"].cuda()))))
     turned = llsa.rotary(leaves[0].detach(), leaves[1].detach(), rope)
@@ -360,11 +361,13 @@ def test_positions_attention_and_gradients_together(dtype, extent, order, span):
         ref.check(m, got[m], (back, bound))
 
 
-def test_few_tokens_with_positions_stay_in_fp32():
-    """bf16 of up to 16 tokens is turned, attended and turned back in fp32, and rounded once."""
-    x = make(1, 2, 2, 12, 12, 64, "bf16", seed=16)
+@pytest.mark.parametrize("extent", [(3, 4), (40, 20)])
+def test_small_steps_with_positions_stay_in_fp32(extent):
+    """bf16 is turned, attended and turned back in fp32, and rounded once."""
+    n = extent[0] * extent[1]
+    x = make(1, 2, 2, n, n, 64, "bf16", seed=16)
     leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v", "lam")]
-    rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=(32, 32), extent=(3, 4))
+    rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=(32, 32), extent=extent)
     o = llsa.diff_attention(*leaves, rope=rope)
     got = torch.autograd.grad(o, leaves, x["dout"].cuda())
     wide = [x[m].float().cuda().requires_grad_() for m in ("q", "k", "v")] + [x["lam"].cuda().requires_grad_()]
