@@ -81,7 +81,7 @@ class _DenseParams(ctypes.Structure):
 
 
 class _DiffParams(ctypes.Structure):
-    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d", "dtype", "lam_dtype", "causal")] + [
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "nq", "nk", "d", "dtype", "lam_dtype", "qk_fp32", "causal")] + [
         ("scale", ctypes.c_float)]
 
 
@@ -98,7 +98,7 @@ class _RopeStrides(ctypes.Structure):
 class _RopeGridParams(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("batch", "heads", "kv_heads", "n", "d", "layout", "span", "axes")] + [
         (n, ctypes.c_int * ROPE_MAX_AXES) for n in ("columns", "extent", "offset")] + [
-        (n, ctypes.c_int) for n in ("token_order", "pos_batched", "dtype", "scaling", "orig_len")] + [
+        (n, ctypes.c_int) for n in ("token_order", "pos_batched", "dtype", "out_other", "scaling", "orig_len")] + [
         (n, ctypes.c_double) for n in ("base", "factor", "low", "high", "amplitude")] + [("step", ctypes.c_double * ROPE_MAX_AXES)]
 
 
@@ -283,23 +283,25 @@ class DiffParams:
     dtype: str = "bf16"        # "bf16" or "fp32"
     lam_dtype: str = ""        # of lam and its gradient; "": dtype
     scale: float = 0.0         # 0: 1/sqrt(d)
+    qk_dtype: str = ""         # of q, k, their gradients and o2; "": dtype, else "fp32"
 
     def __post_init__(self):
         self.__dict__.update(_diff_native(self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, bool(self.causal),
-                                          self.dtype, self.lam_dtype or self.dtype, float(self.scale)))
+                                          self.dtype, self.lam_dtype or self.dtype, float(self.scale), self.qk_dtype or self.dtype))
 
     def __reduce__(self):  # copies and pickles build their own C structure
         return DiffParams, (self.batch, self.heads, self.nq, self.nk, self.d, self.kv_heads, self.causal, self.dtype,
-                            self.lam_dtype, self.scale)
+                            self.lam_dtype, self.scale, self.qk_dtype)
 
     def c(self) -> _DiffParams:
         return self._c
 
     @staticmethod
-    def like(q, k, lam=None, causal: bool = False, scale: float = 0.0) -> "DiffParams":
-        """The parameters of a call on q, k and lam (equal calls share one object)."""
+    def like(q, k, lam=None, causal: bool = False, scale: float = 0.0, v=None) -> "DiffParams":
+        """The parameters of a call on q, k and lam (equal calls share one object); with v, its type
+        may be another than q's."""
         return _diff_params(tuple(q.shape), tuple(k.shape), _dtype_name(q), "" if lam is None else _dtype_name(lam, "lam"),
-                            bool(causal), float(scale))
+                            bool(causal), float(scale), _dtype_name(q if v is None else v))
 
     def shapes(self):
         """Shapes of q (and dq), of k (and dk), of v (and dv), of o (and o2, dout) and of lse."""
@@ -307,23 +309,27 @@ class DiffParams:
 
 
 @functools.lru_cache(maxsize=256)
-def _diff_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, lam_dtype, scale):
+def _diff_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, lam_dtype, scale, qk_dtype):
     """What equal parameters share: the C structure, the workspace sizes, the tensors' shapes."""
     _int32(batch=batch, heads=heads, kv_heads=kv_heads, nq=nq, nk=nk, d=d)
+    if qk_dtype != dtype and qk_dtype != "fp32":
+        raise ValueError(f"qk_dtype must be dtype or 'fp32', not {qk_dtype!r}")
     c = _DiffParams(batch, heads, kv_heads, nq, nk, d, _choice(_DTYPES, dtype, "dtype"), _choice(_DTYPES, lam_dtype, "lam_dtype"),
-                    1 if causal else 0, scale)
+                    1 if qk_dtype != dtype else 0, 1 if causal else 0, scale)
     kv = kv_heads or heads
-    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {}, "_lam": torch.bfloat16 if lam_dtype == "bf16" else torch.float32,
+    types = {"bf16": torch.bfloat16, "fp32": torch.float32}
+    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {}, "_lam": types[lam_dtype], "_qk": types[qk_dtype],
             "_shapes": ((batch, 2 * heads, nq, d), (batch, 2 * kv, nk, d), (batch, kv, nk, 2 * d), (batch, heads, nq, 2 * d),
                         (batch, 2 * heads, nq))}
 
 
 @functools.lru_cache(maxsize=256)
-def _diff_params(q, k, dtype, lam_dtype, causal, scale):
+def _diff_params(q, k, qk_dtype, lam_dtype, causal, scale, dtype):
     b, h, n, d = q
     if h % 2 or k[1] % 2:
         raise ValueError(f"q and k must have two heads for each differential one, got {h} and {k[1]}")
-    return DiffParams(b, h // 2, n, k[2], d, kv_heads=k[1] // 2, causal=causal, dtype=dtype, lam_dtype=lam_dtype, scale=scale)
+    return DiffParams(b, h // 2, n, k[2], d, kv_heads=k[1] // 2, causal=causal, dtype=dtype, lam_dtype=lam_dtype, scale=scale,
+                      qk_dtype=qk_dtype)
 
 
 @dataclass(frozen=True)
@@ -357,6 +363,30 @@ class RopeParams:
 
     def c(self, pos_batched: bool = False) -> _RopeParams:
         return self._c[1 if pos_batched else 0]
+
+    def grid(self, has_pos: bool = False) -> "RopeGridParams | None":
+        """The same positions as parameters of llsa_rope_grid; None where it has none (an image whose
+        last row is not full)."""
+        got = self.__dict__.get("_grid", {}).get(has_pos, self)
+        if got is not self:
+            return got
+        rot = self.rot_dim or self.d
+        if has_pos:
+            extent = None
+        elif self.axes == 1:
+            extent = (self.n,)
+        else:
+            extent = (self.n // self.width, self.width) if self.width > 0 and self.n % self.width == 0 else 0
+        if extent == 0 or rot % (2 * self.axes):
+            got = None
+        else:
+            got = RopeGridParams(self.batch, self.heads, self.n, self.d, kv_heads=self.kv_heads, columns=(rot // self.axes,) * self.axes,
+                                 extent=extent, offset=() if self.axes == 2 or has_pos else (self.pos_offset,), layout=self.layout,
+                                 token_order=self.token_order if self.axes == 2 else "raster", base=self.base, scaling=self.scaling,
+                                 factor=self.factor, orig_len=self.orig_len, low=self.low, high=self.high, amplitude=self.amplitude,
+                                 dtype=self.dtype)
+        self.__dict__.setdefault("_grid", {})[has_pos] = got
+        return got
 
     def in_fp32(self) -> "RopeParams":
         """The same positions for fp32 tensors."""
@@ -408,6 +438,7 @@ class RopeGridParams:
     high: float = 32.0
     amplitude: float = 0.0       # 0: 1, or 0.1 ln(factor) + 1 for "wavelength" with a factor above 1
     dtype: str = "bf16"
+    out_dtype: str = ""          # of q_out and k_out; "": dtype
 
     def __post_init__(self):
         for name in ("columns", "extent", "offset", "step"):
@@ -423,8 +454,9 @@ class RopeGridParams:
                 raise ValueError(f"{name} must have an entry for each of the {axes} axes, not {len(value)}")
         self.__dict__["_c"] = _rope_grid_native(
             self.batch, self.heads, self.kv_heads, self.n, self.d, self.columns, self.extent or (), self.offset,
-            tuple(float(x) for x in self.step), self.span, self.layout, self.token_order, self.dtype, self.scaling, self.orig_len,
-            float(self.base), float(self.factor), float(self.low), float(self.high), float(self.amplitude))
+            tuple(float(x) for x in self.step), self.span, self.layout, self.token_order, self.dtype, self.out_dtype or self.dtype,
+            self.scaling, self.orig_len, float(self.base), float(self.factor), float(self.low), float(self.high),
+            float(self.amplitude))
 
     @property
     def axes(self) -> int:
@@ -435,10 +467,24 @@ class RopeGridParams:
 
     def in_fp32(self) -> "RopeGridParams":
         """The same positions for fp32 tensors."""
-        got = self.__dict__.get("_fp32")
+        return self._kept("_fp32", dtype="fp32", out_dtype="")
+
+    def to_fp32(self) -> "RopeGridParams":
+        """The same positions, from bf16 into fp32."""
+        return self._kept("_up", dtype="bf16", out_dtype="fp32")
+
+    def from_fp32(self) -> "RopeGridParams":
+        """The same positions, from fp32 into bf16."""
+        return self._kept("_down", dtype="fp32", out_dtype="bf16")
+
+    def _kept(self, name, **kw):
+        got = self.__dict__.get(name)
         if got is None:
-            got = self.__dict__["_fp32"] = replace(self, dtype="fp32")
+            got = self.__dict__[name] = replace(self, **kw)
         return got
+
+    def grid(self, has_pos: bool = False) -> "RopeGridParams":
+        return self
 
     @staticmethod
     def like(q, k=None, **kw) -> "RopeGridParams":
@@ -447,8 +493,8 @@ class RopeGridParams:
 
 
 @functools.lru_cache(maxsize=256)
-def _rope_grid_native(batch, heads, kv_heads, n, d, columns, extent, offset, step, span, layout, order, dtype, scaling, orig_len,
-                      *real):
+def _rope_grid_native(batch, heads, kv_heads, n, d, columns, extent, offset, step, span, layout, order, dtype, out_dtype, scaling,
+                      orig_len, *real):
     """The C structures of equal parameters, for positions without and with a batch dimension."""
     _int32(batch=batch, heads=heads, kv_heads=kv_heads, n=n, d=d, orig_len=orig_len)
     for name, values in (("columns", columns), ("extent", extent), ("offset", offset)):
@@ -458,8 +504,9 @@ def _rope_grid_native(batch, heads, kv_heads, n, d, columns, extent, offset, ste
     span, layout = _choice(_ROPE_SPANS, span, "span"), _choice(_ROPE_LAYOUTS, layout, "layout")
     order = _choice(_ORDERS, order, "token_order")
     dtype, scaling = _choice(_DTYPES, dtype, "dtype"), _choice(_ROPE_SCALINGS, scaling, "scaling")
-    return tuple(_RopeGridParams(batch, heads, kv_heads, n, d, layout, span, len(columns), *four, order, batched, dtype, scaling,
-                                 orig_len, *real, (ctypes.c_double * ROPE_MAX_AXES)(*step)) for batched in (0, 1))
+    other = 1 if _choice(_DTYPES, out_dtype, "out_dtype") != dtype else 0
+    return tuple(_RopeGridParams(batch, heads, kv_heads, n, d, layout, span, len(columns), *four, order, batched, dtype, other,
+                                 scaling, orig_len, *real, (ctypes.c_double * ROPE_MAX_AXES)(*step)) for batched in (0, 1))
 
 
 @dataclass(frozen=True)
@@ -676,9 +723,9 @@ def llsa_diff_fwd(p: DiffParams, q, k, v, lam, o, o2, lse, q_len=None, k_len=Non
         td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws_on(ws, dev)
-        _check(_load().llsa_diff_fwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev), _like(v, "v", sv, td, dev),
+        _check(_load().llsa_diff_fwd(p._ref, _like(q, "q", sq, p._qk, dev), _like(k, "k", sk, p._qk, dev), _like(v, "v", sv, td, dev),
                                      _like(lam, "lam", (p.heads,), p._lam, dev), ql, kl, _like(o, "o", so, td, dev),
-                                     None if o2 is None else _like(o2, "o2", so, td, dev),
+                                     None if o2 is None else _like(o2, "o2", so, p._qk, dev),
                                      _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_diff_fwd")
 
 
@@ -688,11 +735,11 @@ def llsa_diff_bwd(p: DiffParams, q, k, v, lam, o, o2, lse, dout, dq, dk, dv, dla
         td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws_on(ws, dev)
-        _check(_load().llsa_diff_bwd(p._ref, _like(q, "q", sq, td, dev), _like(k, "k", sk, td, dev), _like(v, "v", sv, td, dev),
+        _check(_load().llsa_diff_bwd(p._ref, _like(q, "q", sq, p._qk, dev), _like(k, "k", sk, p._qk, dev), _like(v, "v", sv, td, dev),
                                      _like(lam, "lam", (p.heads,), p._lam, dev), _like(o, "o", so, td, dev),
-                                     _like(o2, "o2", so, td, dev), _like(lse, "lse", sl, torch.float32, dev),
-                                     _like(dout, "dout", so, td, dev), ql, kl, _like(dq, "dq", sq, td, dev),
-                                     _like(dk, "dk", sk, td, dev), _like(dv, "dv", sv, td, dev),
+                                     _like(o2, "o2", so, p._qk, dev), _like(lse, "lse", sl, torch.float32, dev),
+                                     _like(dout, "dout", so, td, dev), ql, kl, _like(dq, "dq", sq, p._qk, dev),
+                                     _like(dk, "dk", sk, p._qk, dev), _like(dv, "dv", sv, td, dev),
                                      _like(dlam, "dlam", (p.heads,), p._lam, dev), w, wb, _stream(stream)), "llsa_diff_bwd")
 
 
@@ -748,14 +795,15 @@ def llsa_rope_grid(p: RopeGridParams, q, k, q_out, k_out, pos=None, inverse: boo
 def _rope_call(entry, p, q, k, q_out, k_out, pos, inverse, stream):
     with _on(q, "q"):
         td, dev = _tok_dtype(p), q.get_device()
+        to = {"": td, "bf16": torch.bfloat16, "fp32": torch.float32}[getattr(p, "out_dtype", "")]
         shape = (p.batch, p.heads, p.n, p.d)
         a, sa = _strided(q, "q", shape, td, dev)
-        c, sc = _strided(q_out, "q_out", shape, td, dev)
+        c, sc = _strided(q_out, "q_out", shape, to, dev)
         b = d = sb = sd = None
         if p.kv_heads:
             shape = (p.batch, p.kv_heads, p.n, p.d)
             b, sb = _strided(k, "k", shape, td, dev)
-            d, sd = _strided(k_out, "k_out", shape, td, dev)
+            d, sd = _strided(k_out, "k_out", shape, to, dev)
         elif k is not None or k_out is not None:
             raise ValueError("k and k_out must be None where kv_heads is 0")
         at, batched = None, False
@@ -954,7 +1002,7 @@ def diff_forward(p: DiffParams, q, k, v, lam, q_len=None, k_len=None, o=None, o2
     that diff_backward() will need it (else it is None)."""
     with _under(stream, q.device):
         so, sl = p.shapes()[3:]
-        o = torch.empty(so, dtype=q.dtype, device=q.device) if o is None else o
+        o = torch.empty(so, dtype=v.dtype, device=q.device) if o is None else o
         o2 = torch.empty(so, dtype=q.dtype, device=q.device) if o2 is None and backward else o2
         lse = torch.empty(sl, dtype=torch.float32, device=q.device) if lse is None else lse
         ws = _dense_ws(p, OP_DIFF_FWD, q.device) if ws is None else ws
@@ -1081,8 +1129,8 @@ def _wide(q, k):
 # diff_attention with rope= is wide wherever that hides behind the call, whatever the columns: lam's
 # gradient is a sum of terms of both signs over all tokens, and with few heads it can come out as
 # small as what the rounding of turned q and k makes of it (0.007 to 0.011 off where the other
-# outputs are 0.003; in fp32 all are 0.0017). 2^23 pairs of 64 columns take the GPU 170 us.
-_WIDE_DIFF = (1 << 23) * 64
+# outputs are 0.003; in fp32 all are 0.0017). 2^24 pairs of 64 columns take the GPU 350 us.
+_WIDE_DIFF = (1 << 24) * 64
 
 
 def _wide_diff(q, k):
@@ -1139,21 +1187,34 @@ def _dense_functions():
 
         @staticmethod
         def forward(ctx, q, k, v, lam, causal, scale, q_len, k_len, rope, pos):
-            ctx.dtype = dtype = q.dtype
-            q, k, v, rope = _positioned(rope, q, k, v, pos, _wide_diff)
+            ctx.dtype = q.dtype
+            ctx.narrow = grid = None if rope is None or not _wide_diff(q, k) else rope.grid(pos is not None)
+            if grid is not None:  # turned into fp32, and the gradients back out of it
+                _check_rope(rope, q, k)
+                x, y = (torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in (q, k))
+                llsa_rope_grid(grid.to_fp32(), _rope_view(q), _rope_view(k), x, y, pos=pos)
+                if v.dtype != q.dtype:
+                    raise ValueError(f"v must be {q.dtype}, got {v.dtype}")
+                q, k, v = x, y, _contiguous(v)
+            else:
+                q, k, v, rope = _positioned(rope, q, k, v, pos, _wide_diff)
             lam = _contiguous(lam)
-            p = DiffParams.like(q, k, lam, causal=causal, scale=scale)
+            p = DiffParams.like(q, k, lam, causal, scale, v)
             o, lse, o2 = diff_forward(p, q, k, v, lam, q_len, k_len, backward=any(ctx.needs_input_grad))
             ctx.p, ctx.rope = p, rope
             ctx.save_for_backward(q, k, v, lam, o, o2, lse, q_len, k_len, pos)
-            return o.to(dtype)
+            return o.to(ctx.dtype)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, do):
             q, k, v, lam, o, o2, lse, q_len, k_len, pos = ctx.saved_tensors
             dq, dk, dv, dlam = diff_backward(ctx.p, q, k, v, lam, o, o2, lse, _contiguous(do.to(o.dtype)), q_len, k_len)
-            if ctx.rope is not None:
+            if ctx.narrow is not None:
+                x, y = (torch.empty(t.shape, dtype=ctx.dtype, device=t.device) for t in (dq, dk))
+                llsa_rope_grid(ctx.narrow.from_fp32(), dq, dk, x, y, pos=pos, inverse=True)
+                dq, dk = x, y
+            elif ctx.rope is not None:
                 _turn(ctx.rope, dq, dk, dq, dk, pos=pos, inverse=True)
             if dq.dtype != ctx.dtype:
                 dq, dk, dv = dq.to(ctx.dtype), dk.to(ctx.dtype), dv.to(ctx.dtype)
@@ -1211,7 +1272,7 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     kv_heads, nk, 2d]; lam [heads], bf16 or fp32 whatever the type of the others, or
     one number for all heads. q_len, k_len, rope, pos and captured backward passes: as
     dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
-    in fp32 from the turn to the last rounding where that call's does, and up to 2^29
+    in fp32 from the turn to the last rounding where that call's does, and up to 2^30
     products of a pair of a query and a key (both maps' pairs times d)."""
     if isinstance(lam, torch.Tensor) and lam.numel() == 1 and q.shape[1] != 2:
         lam = lam.reshape(1).expand(q.shape[1] // 2)

@@ -15,6 +15,7 @@ constexpr int kDiffStats = 5;  // numbers per query row in the backward pass: -l
 
 struct DiffShape {
     int batch, heads, kv_heads, G, nq, nk, d, dtype, lam_dtype, causal;
+    int wide;    // q, k, dq, dk and o2 are fp32, whatever dtype
     int slices;  // batch * kv_heads
     int R, Rp;   // rows per slice, and padded to kDenseRowPad
     float scale;

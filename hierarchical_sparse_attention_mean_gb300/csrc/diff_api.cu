@@ -55,8 +55,9 @@ __device__ __forceinline__ Place four_place(const FourArgs& f, long long slice4)
     return {rest >> 2, (rest >> 1) & 1, rest & 1, g};
 }
 
-// blockIdx.y 0: what has query rows, 1: what has keys. Four values per thread.
-template <typename T, bool BACKWARD>
+// blockIdx.y 0: what has query rows, 1: what has keys. Four values per thread. Q: the type of
+// q, k and o2.
+template <typename T, typename Q, bool BACKWARD>
 __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     const bool keys = blockIdx.y == 1;
@@ -74,19 +75,19 @@ __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_cons
         const long long to = row4 * a.d + c;
         float y[4];
         if (keys) {
-            load4f(static_cast<const T*>(a.k) + one, y);
+            load4f(static_cast<const Q*>(a.k) + one, y);
             store4(f.k + to, y);
             load4f(static_cast<const T*>(a.v) + two, y);
             store4(f.v + to, y);
             continue;
         }
-        load4f(static_cast<const T*>(a.q) + one, y);
+        load4f(static_cast<const Q*>(a.q) + one, y);
         store4(f.q + to, y);
         if (!BACKWARD) continue;
         const float lam = diff_lam(f.a, diff_head(f.a, (int)slice, r));
         float o[4], o2[4];
         load4f(static_cast<const T*>(a.dout) + two, y);
-        load4f(static_cast<const T*>(f.a.o2) + two, o2);
+        load4f(static_cast<const Q*>(f.a.o2) + two, o2);
         if (p.i == 0) load4f(static_cast<const T*>(a.o) + two, o);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_cons
 }
 
 // o, o2 and the log-sum-exp of both maps from the four calls' (in f.o and f.lse).
-template <typename T>
+template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     const int per = a.d / 2;  // vectors of 4 of a row of 2 d
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < 4; e++) y[e] = fmaf(-lam, z[e], y[e]);
         store4(static_cast<T*>(a.o_out) + row * 2 * a.d + col, y);
-        if (f.a.o2_out) store4(static_cast<T*>(f.a.o2_out) + row * 2 * a.d + col, z);
+        if (f.a.o2_out) store4(static_cast<Q*>(f.a.o2_out) + row * 2 * a.d + col, z);
         if (col == 0) {
             a.lse_out[diff_row(f.a, slice, 0, r)] = f.lse[first];
             a.lse_out[diff_row(f.a, slice, 1, r)] = f.lse[second];
@@ -127,14 +128,13 @@ __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_con
 }
 
 // dq, dk, dv (blockIdx.y) as sums of two of the four calls' gradients.
-template <typename T>
+template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     const int which = blockIdx.y, rows = which == 0 ? a.R : a.nk;
     const int per = which == 2 ? a.d / 2 : a.d / 4;
     const long long n = (which == 2 ? 1LL : 2LL) * a.slices * rows * per, step = (long long)a.kv_heads * rows * a.d;
     const float* from = which == 0 ? f.dq : which == 1 ? f.dk : f.dv;
-    T* out = static_cast<T*>(which == 0 ? f.dq_out : which == 1 ? f.dk_out : f.dv_out);
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
         const long long row = x / per;
         int c = (int)(x - row * per) * 4;
@@ -158,7 +158,8 @@ __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_co
         load4f(from + other, z);
 #pragma unroll
         for (int e = 0; e < 4; e++) y[e] += z[e];
-        store4(out + to, y);
+        if (which == 2) store4(static_cast<T*>(f.dv_out) + to, y);
+        else store4(static_cast<Q*>(which == 0 ? f.dq_out : f.dk_out) + to, y);
     }
 }
 
@@ -324,7 +325,7 @@ int lam_parts(const DiffShape& s) {
     return (int)std::max<long long>(1, std::min<long long>({(rows + kLamRows - 1) / kLamRows, kLamParts, 8LL * kDenseSms / s.heads + 1}));
 }
 
-template <typename T>
+template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constant__ DiffArgs f, float* part, int parts) {
     const DenseArgs& a = f.d;
     const int h = blockIdx.x / parts, p = blockIdx.x - h * parts;
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constan
         const long long at = ((long long)slice * a.R + (long long)(h - g * G) * a.nq + t) * 2 * a.d + c;
         float y[4], z[4];
         load4f(static_cast<const T*>(a.dout) + at, y);
-        load4f(static_cast<const T*>(f.o2) + at, z);
+        load4f(static_cast<const Q*>(f.o2) + at, z);
 #pragma unroll
         for (int e = 0; e < 4; e++) sum = fmaf(y[e], z[e], sum);
     }
@@ -395,13 +396,11 @@ __global__ void __launch_bounds__(32) diff_lam_sum_kernel(const float* part, int
     else static_cast<float*>(out)[h] = -sum;
 }
 
+template <typename T, typename Q>
 int launch_lam(const DiffShape& s, const DiffArgs& a, void* dlam, float* part, cudaStream_t st) {
     const int parts = lam_parts(s);
     const unsigned blocks = (unsigned)s.heads * parts;
-    if (s.dtype == LLSA_DTYPE_BF16)
-        LLSA_LAUNCH("diff_lam", st, diff_lam_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a, part, parts));
-    else
-        LLSA_LAUNCH("diff_lam", st, diff_lam_kernel<float><<<blocks, kThreads, 0, st>>>(a, part, parts));
+    LLSA_LAUNCH("diff_lam", st, diff_lam_kernel<T, Q><<<blocks, kThreads, 0, st>>>(a, part, parts));
     LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(part, parts, dlam, s.lam_dtype == LLSA_DTYPE_BF16));
     return LLSA_OK;
 }
@@ -411,6 +410,7 @@ int launch_lam(const DiffShape& s, const DiffArgs& a, void* dlam, float* part, c
 int derive_diff(const llsa_diff_params* p, DiffShape* s) {
     if (!p) return LLSA_ERR_INVALID_ARG;
     if (p->lam_dtype != LLSA_DTYPE_BF16 && p->lam_dtype != LLSA_DTYPE_F32) return LLSA_ERR_DTYPE;
+    if (p->qk_fp32 != 0 && p->qk_fp32 != 1) return LLSA_ERR_INVALID_ARG;
     if (p->heads < 0 || p->kv_heads < 0) return LLSA_ERR_INVALID_ARG;
     if (p->d > 128) return LLSA_ERR_SHAPE;
     const int kv = p->kv_heads ? p->kv_heads : p->heads;
@@ -426,6 +426,7 @@ int derive_diff(const llsa_diff_params* p, DiffShape* s) {
     s->nk = p->nk;
     s->d = p->d;
     s->dtype = p->dtype;
+    s->wide = p->qk_fp32 && p->dtype == LLSA_DTYPE_BF16;
     s->lam_dtype = p->lam_dtype;
     s->causal = p->causal;
     s->scale = s->four.scale;
@@ -470,7 +471,7 @@ DenseArgs four_args(const DiffShape& s, const DiffArgs& a, const FourArgs& f) {
 
 unsigned blocks_for(long long n) { return (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 16LL * kDenseSms); }
 
-template <typename T>
+template <typename T, typename Q>
 int launch_four_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStream_t st) {
     FourArgs f;
     memset(&f, 0, sizeof(f));
@@ -483,22 +484,26 @@ int launch_four_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStream_
     f.v = take(four_keys(s));
     f.lse = take(four_lse(s));
     const dim3 grid(blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4)), s.nk > 0 ? 2 : 1);
-    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, false><<<grid, kThreads, 0, st>>>(f));
+    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, Q, false><<<grid, kThreads, 0, st>>>(f));
     DenseArgs d = four_args(s, a, f);
     d.o_out = f.o;
     d.lse_out = f.lse;
     LLSA_TRY(launch_dense_fwd(s.four, d, at, st));
     LLSA_LAUNCH("diff_combine", st,
-                diff_combine_kernel<T><<<blocks_for((long long)s.slices * s.R * (s.d / 2)), kThreads, 0, st>>>(f));
+                diff_combine_kernel<T, Q><<<blocks_for((long long)s.slices * s.R * (s.d / 2)), kThreads, 0, st>>>(f));
     return LLSA_OK;
 }
 
-template <typename T>
-int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, void* dv, void* ws, cudaStream_t st) {
+size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam_parts(s) * sizeof(float)) : 0; }
+
+template <typename T, typename Q>
+int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, void* dv, void* dlam, void* ws, cudaStream_t st) {
+    LLSA_TRY((launch_lam<T, Q>(s, a, dlam, static_cast<float*>(ws), st)));
+    if (s.R == 0 && s.nk == 0) return LLSA_OK;
     FourArgs f;
     memset(&f, 0, sizeof(f));
     f.a = a;
-    char* at = static_cast<char*>(ws);
+    char* at = static_cast<char*>(ws) + lam_bytes(s);
     auto take = [&](size_t bytes) { char* p = at; at += bytes; return reinterpret_cast<float*>(p); };
     f.q = take(four_rows(s));
     f.dout = take(four_rows(s));
@@ -509,7 +514,7 @@ int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, v
     float *gk = take(four_keys(s)), *gv = take(four_keys(s));
     f.lse = take(four_lse(s));
     const dim3 grid(blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4)), s.nk > 0 ? 2 : 1);
-    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, true><<<grid, kThreads, 0, st>>>(f));
+    LLSA_LAUNCH("diff_expand", st, diff_expand_kernel<T, Q, true><<<grid, kThreads, 0, st>>>(f));
     DenseArgs d = four_args(s, a, f);
     d.o = f.o;
     d.lse = f.lse;
@@ -524,17 +529,16 @@ int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, v
     f.dq_out = dq;
     f.dk_out = dk;
     f.dv_out = dv;
-    LLSA_LAUNCH("diff_collapse", st, diff_collapse_kernel<T><<<dim3(grid.x, s.nk > 0 ? 3 : 1), kThreads, 0, st>>>(f));
+    LLSA_LAUNCH("diff_collapse", st, diff_collapse_kernel<T, Q><<<dim3(grid.x, s.nk > 0 ? 3 : 1), kThreads, 0, st>>>(f));
     return LLSA_OK;
 }
 
-size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam_parts(s) * sizeof(float)) : 0; }
 
 // Which kernels take a call.
 enum class Path { kFew, kTc, kFour };
 
 Path fwd_path(const DiffShape& s) {
-    return diff_few_supported(s) ? Path::kFew : diff_tc_supported(s) ? Path::kTc : Path::kFour;
+    return s.wide ? Path::kFour : diff_few_supported(s) ? Path::kFew : diff_tc_supported(s) ? Path::kTc : Path::kFour;
 }
 
 DenseSplit fwd_split(const DiffShape& s) {
@@ -553,7 +557,10 @@ size_t fwd_workspace(const DiffShape& s) {
 int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
     const Path path = fwd_path(s);
-    if (path == Path::kFour) return bf16 ? launch_four_fwd<__nv_bfloat16>(s, a, ws, st) : launch_four_fwd<float>(s, a, ws, st);
+    if (path == Path::kFour)
+        return s.wide ? launch_four_fwd<__nv_bfloat16, float>(s, a, ws, st)
+               : bf16 ? launch_four_fwd<__nv_bfloat16, __nv_bfloat16>(s, a, ws, st)
+                      : launch_four_fwd<float, float>(s, a, ws, st);
     const DenseSplit p = fwd_split(s);
     a.d.splits = p.splits;
     a.d.chunk = p.chunk;
@@ -567,7 +574,7 @@ int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     return LLSA_OK;
 }
 
-Path bwd_path(const DiffShape& s) { return diff_tc_supported(s) ? Path::kTc : Path::kFour; }
+Path bwd_path(const DiffShape& s) { return !s.wide && diff_tc_supported(s) ? Path::kTc : Path::kFour; }
 
 // Workspace of the tensor-core backward pass, in order: the rows' numbers, the sums of
 // P_2 dP, parts of those over a head's rows, parts of dq, of dk, of dv.
@@ -712,11 +719,9 @@ int llsa_diff_bwd(const llsa_diff_params* p, const void* q, const void* k, const
         return LLSA_OK;
     }
     if (bwd_path(s) == Path::kTc) return launch_tc_bwd(s, a, dq, dk, dv, dlam, ws, st);
-    LLSA_TRY(launch_lam(s, a, dlam, static_cast<float*>(ws), st));
-    if (!rows && !keys) return LLSA_OK;
-    void* rest = static_cast<char*>(ws) + lam_bytes(s);
-    return s.dtype == LLSA_DTYPE_BF16 ? launch_four_bwd<__nv_bfloat16>(s, a, dq, dk, dv, rest, st)
-                                      : launch_four_bwd<float>(s, a, dq, dk, dv, rest, st);
+    return s.wide                       ? launch_four_bwd<__nv_bfloat16, float>(s, a, dq, dk, dv, dlam, ws, st)
+           : s.dtype == LLSA_DTYPE_BF16 ? launch_four_bwd<__nv_bfloat16, __nv_bfloat16>(s, a, dq, dk, dv, dlam, ws, st)
+                                        : launch_four_bwd<float, float>(s, a, dq, dk, dv, dlam, ws, st);
 }
 
 }  // extern "C"

@@ -100,6 +100,9 @@ struct Word<4> { using type = uint32_t; };
 template <>
 struct Word<2> { using type = uint16_t; };
 
+template <>
+struct Word<32> { struct type { uint4 a, b; }; };
+
 template <typename T, int W>
 union Few {
     typename Word<W * sizeof(T)>::type u;
@@ -109,8 +112,8 @@ union Few {
 
 // One thread: unit u of one token, for heads h0 .. h0 + heads_per_thread - 1 of the q
 // heads followed by the k heads. W elements per vector; PAIRED: neighbouring columns
-// are a pair, else two vectors hold W pairs.
-template <typename T, int W, bool PAIRED>
+// are a pair, else two vectors hold W pairs. T: the inputs' type, O: the outputs'.
+template <typename T, typename O, int W, bool PAIRED>
 __global__ void __launch_bounds__(kThreads) rope_grid_kernel(const __grid_constant__ GridArgs a) {
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
     if (idx >= a.rows * a.units) return;
@@ -164,33 +167,40 @@ __global__ void __launch_bounds__(kThreads) rope_grid_kernel(const __grid_consta
     }
     const int total = a.heads[0] + a.heads[1];
     const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(h0 + a.heads_per_thread, total);
-    auto place = [&](int h, const T*& in, T*& out) {
+    auto place = [&](int h, const T*& in, O*& out) {
         const int w = h >= a.heads[0] ? 1 : 0;
         const int hh = h - w * a.heads[0];
         in = static_cast<const T*>(a.in[w]) + b * a.in_stride[w][0] + hh * a.in_stride[w][1] + t * a.in_stride[w][2];
-        out = static_cast<T*>(a.out[w]) + b * a.out_stride[w][0] + hh * a.out_stride[w][1] + t * a.out_stride[w][2];
+        out = static_cast<O*>(a.out[w]) + b * a.out_stride[w][0] + hh * a.out_stride[w][1] + t * a.out_stride[w][2];
     };
     using V = typename Word<W * sizeof(T)>::type;
+    using VO = typename Word<W * sizeof(O)>::type;
     for (int h = h0; h < h1; h++) {
         const T* in;
-        T* out;
+        O* out;
         place(h, in, out);
         Few<T, W> x, y;
+        Few<O, W> xo, yo;
         x.u = *reinterpret_cast<const V*>(in + col0);
+        if (!copy && !PAIRED) y.u = *reinterpret_cast<const V*>(in + col1);
+        // same type: what is not turned keeps its bits, NaN payloads among them
+        if constexpr (sizeof(T) == sizeof(O)) {
+            xo.u = x.u;
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; i++) xo.e[i] = from_float<O>(to_float(x.e[i]));
+        }
         if (!copy) {
-            if (!PAIRED) y.u = *reinterpret_cast<const V*>(in + col1);
 #pragma unroll
             for (int i = 0; i < P; i++) {
-                T& one = x.e[PAIRED ? 2 * i : i];
-                T& two = PAIRED ? x.e[2 * i + 1] : y.e[i];
                 if (PAIRED && col0 + 2 * i >= a.rot) break;  // the turned columns may end inside the vector
-                const float f = to_float(one), g = to_float(two);
-                one = from_float<T>(f * c[i] - g * s[i]);
-                two = from_float<T>(f * s[i] + g * c[i]);
+                const float f = to_float(x.e[PAIRED ? 2 * i : i]), g = to_float(PAIRED ? x.e[2 * i + 1] : y.e[i]);
+                xo.e[PAIRED ? 2 * i : i] = from_float<O>(f * c[i] - g * s[i]);
+                (PAIRED ? xo.e[2 * i + 1] : yo.e[i]) = from_float<O>(f * s[i] + g * c[i]);
             }
-            if (!PAIRED) *reinterpret_cast<V*>(out + col1) = y.u;
+            if (!PAIRED) *reinterpret_cast<VO*>(out + col1) = yo.u;
         }
-        *reinterpret_cast<V*>(out + col0) = x.u;
+        *reinterpret_cast<VO*>(out + col0) = xo.u;
     }
 }
 
@@ -198,6 +208,7 @@ int check_grid(const llsa_rope_grid_params* p, bool has_pos) {
     if (!p) return LLSA_ERR_INVALID_ARG;
     if (p->batch < 0 || p->heads < 0 || p->kv_heads < 0 || p->n < 0) return LLSA_ERR_INVALID_ARG;
     if (p->dtype != LLSA_DTYPE_BF16 && p->dtype != LLSA_DTYPE_F32) return LLSA_ERR_DTYPE;
+    if (p->out_other != 0 && p->out_other != 1) return LLSA_ERR_INVALID_ARG;
     if (p->layout != LLSA_ROPE_HALF && p->layout != LLSA_ROPE_INTERLEAVED) return LLSA_ERR_INVALID_ARG;
     if (p->span < LLSA_ROPE_SPAN_AXIS || p->span > LLSA_ROPE_SPAN_DEALT) return LLSA_ERR_INVALID_ARG;
     if (p->axes < 1 || p->axes > kAxes) return LLSA_ERR_INVALID_ARG;
@@ -274,7 +285,7 @@ int derive_grid(const llsa_rope_grid_params* p, GridArgs* a) {
     return isfinite(a->amplitude) ? LLSA_OK : LLSA_ERR_INVALID_ARG;
 }
 
-template <typename T>
+template <typename T, typename O>
 int launch_grid(const llsa_rope_grid_params* p, GridArgs& a, cudaStream_t st) {
     constexpr int V = 16 / sizeof(T);
     int w = V;
@@ -298,13 +309,13 @@ int launch_grid(const llsa_rope_grid_params* p, GridArgs& a, cudaStream_t st) {
     if (gx > 2147483647LL) return LLSA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)gx, (unsigned)gy);
     if (p->layout == LLSA_ROPE_INTERLEAVED)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, V, true><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V, true><<<grid, kThreads, 0, st>>>(a));
     else if (w == V)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, V, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V, false><<<grid, kThreads, 0, st>>>(a));
     else if (w == V / 2)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, V / 2, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V / 2, false><<<grid, kThreads, 0, st>>>(a));
     else
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, 1, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, 1, false><<<grid, kThreads, 0, st>>>(a));
     return LLSA_OK;
 }
 
@@ -329,9 +340,12 @@ extern "C" int llsa_rope_grid(const llsa_rope_grid_params* p, const llsa_rope_st
     if (pos && (reinterpret_cast<uintptr_t>(pos) & 3u)) return LLSA_ERR_ALIGN;
     LLSA_TRY(rope_strides(strides ? strides->q : nullptr, *p, p->heads, false, a.in_stride[0]));
     LLSA_TRY(rope_strides(strides ? strides->k : nullptr, *p, p->kv_heads, false, a.in_stride[1]));
-    LLSA_TRY(rope_strides(strides ? strides->q_out : nullptr, *p, p->heads, true, a.out_stride[0]));
-    LLSA_TRY(rope_strides(strides ? strides->k_out : nullptr, *p, p->kv_heads, true, a.out_stride[1]));
+    llsa_rope_grid_params outs = *p;
+    if (p->out_other) outs.dtype = p->dtype == LLSA_DTYPE_BF16 ? LLSA_DTYPE_F32 : LLSA_DTYPE_BF16;
+    LLSA_TRY(rope_strides(strides ? strides->q_out : nullptr, outs, p->heads, true, a.out_stride[0]));
+    LLSA_TRY(rope_strides(strides ? strides->k_out : nullptr, outs, p->kv_heads, true, a.out_stride[1]));
     // a tensor may be its own output only if every element goes back to its own place
+    if (p->out_other && ((p->heads > 0 && q == q_out) || (p->kv_heads > 0 && k == k_out))) return LLSA_ERR_INVALID_ARG;
     if (p->heads > 0 && q == q_out && memcmp(a.in_stride[0], a.out_stride[0], sizeof(a.in_stride[0])) != 0)
         return LLSA_ERR_INVALID_ARG;
     if (p->kv_heads > 0 && k == k_out && memcmp(a.in_stride[1], a.out_stride[1], sizeof(a.in_stride[1])) != 0)
@@ -356,5 +370,7 @@ extern "C" int llsa_rope_grid(const llsa_rope_grid_params* p, const llsa_rope_st
     }
     a.sign = inverse ? -1.0f : 1.0f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return p->dtype == LLSA_DTYPE_BF16 ? launch_grid<__nv_bfloat16>(p, a, st) : launch_grid<float>(p, a, st);
+    if (p->dtype == LLSA_DTYPE_BF16)
+        return p->out_other ? launch_grid<__nv_bfloat16, float>(p, a, st) : launch_grid<__nv_bfloat16, __nv_bfloat16>(p, a, st);
+    return p->out_other ? launch_grid<float, __nv_bfloat16>(p, a, st) : launch_grid<float, float>(p, a, st);
 }

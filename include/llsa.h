@@ -375,6 +375,8 @@ typedef struct llsa_diff_params {
     int d;              /* columns of q and k: multiple of 8, at most 128; v and o have 2 d */
     int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
     int lam_dtype;      /* of lam and dlam, on its own: LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int qk_fp32;        /* 1: q, k, dq, dk and o2 are fp32 beside tensors of type `dtype`, as llsa_rope_grid with
+                           out_other turns them without rounding; computed in fp32 throughout */
     int causal;         /* 0 or 1 */
     float scale;        /* softmax scale; 0 selects 1/sqrt(d) */
 } llsa_diff_params;
@@ -387,7 +389,8 @@ size_t llsa_diff_workspace_bytes(const llsa_diff_params *p, int op);
 
 /* Differential attention, forward.
  *   q     : [batch, 2 heads, nq, d]; k : [batch, 2 kv_heads, nk, d];
- *   v     : [batch, kv_heads, nk, 2 d] (p->dtype); lam : [heads] (p->lam_dtype).
+ *   v     : [batch, kv_heads, nk, 2 d] (p->dtype; q, k and o2 fp32 with qk_fp32);
+ *   lam   : [heads] (p->lam_dtype).
  *   q_len, k_len : int32 [batch] on the device, or NULL (all tokens valid).
  *   o     : output [batch, heads, nq, 2 d] (p->dtype).
  *   o2    : output [batch, heads, nq, 2 d] (p->dtype), a^2, which the backward pass
@@ -527,7 +530,8 @@ typedef struct llsa_rope_grid_params {
     int offset[LLSA_ROPE_MAX_AXES];  /* position of the grid's first entry; ignored with pos */
     int token_order;    /* LLSA_ORDER_RASTER or LLSA_ORDER_TILE (at least 2 axes); ignored with pos */
     int pos_batched;    /* pos holds batch * n rows instead of n */
-    int dtype;          /* LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int dtype;          /* of q and k: LLSA_DTYPE_BF16 or LLSA_DTYPE_F32 */
+    int out_other;      /* 1: q_out and k_out have the other type of the two (no tensor is its own output) */
     int scaling;        /* LLSA_ROPE_SCALE_* */
     int orig_len;       /* WAVELENGTH: positions that the model was trained on */
     double base;        /* > 1 */

@@ -48,8 +48,8 @@ def test_parameters_refused(lib, kw, code):
 
 
 def test_raw_fields_refused(lib):
-    for field, value, code in (("dtype", 2, DTYPE), ("lam_dtype", 2, DTYPE), ("causal", 2, INVALID)):
-        c = llsa._DiffParams(2, 4, 4, 100, 100, 64, 0, 0, 0, 0.0)
+    for field, value, code in (("dtype", 2, DTYPE), ("lam_dtype", 2, DTYPE), ("qk_fp32", 2, INVALID), ("causal", 2, INVALID)):
+        c = llsa._DiffParams(2, 4, 4, 100, 100, 64, 0, 0, 0, 0, 0.0)
         setattr(c, field, value)
         assert fwd(lib, c) == code and bwd(lib, c) == code
     assert lib.llsa_diff_fwd(None, *([16] * 4), None, None, 16, None, 16, None, 0, None) == INVALID
@@ -96,7 +96,7 @@ def test_workspace(lib):
 
 
 def test_binding_refuses(lib):
-    for kw in (dict(dtype="fp16"), dict(lam_dtype="fp16")):
+    for kw in (dict(dtype="fp16"), dict(lam_dtype="fp16"), dict(dtype="fp32", qk_dtype="bf16"), dict(qk_dtype="fp16")):
         with pytest.raises(ValueError):
             llsa.DiffParams(**{**BASE, **kw})
     for value in ((1 << 32) + 100, 1 << 31, -(1 << 31) - 1):
@@ -118,7 +118,7 @@ def test_binding_refuses(lib):
 
 
 def test_parameters_copy_and_pickle(lib):
-    p = llsa.DiffParams(2, 4, 100, 90, 64, kv_heads=2, causal=True, lam_dtype="fp32", scale=0.5)
+    p = llsa.DiffParams(2, 4, 100, 90, 64, kv_heads=2, causal=True, lam_dtype="fp32", scale=0.5, qk_dtype="fp32")
     llsa.diff_workspace_bytes(p, llsa.OP_DIFF_BWD)
     assert p.shapes() == ((2, 8, 100, 64), (2, 4, 90, 64), (2, 2, 90, 128), (2, 4, 100, 128), (2, 8, 100))
     for y in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
@@ -127,7 +127,7 @@ def test_parameters_copy_and_pickle(lib):
 
 
 @pytest.mark.parametrize("b,h,n,d,wide", [
-    (1, 6, 64, 64, True), (1, 1, 2048, 64, True), (1, 1, 2049, 64, False), (1, 1, 1448, 128, True), (1, 1, 1449, 128, False),
+    (1, 6, 64, 64, True), (1, 1, 2896, 64, True), (1, 1, 2897, 64, False), (1, 1, 2048, 128, True), (1, 1, 2049, 128, False),
     (4, 16, 16, 128, True), (2, 6, 4096, 64, False), (1, 1, 16384, 8, True),
 ])
 def test_where_positions_stay_in_fp32(b, h, n, d, wide):

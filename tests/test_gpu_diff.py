@@ -361,21 +361,81 @@ def test_positions_attention_and_gradients_together(dtype, extent, order, span, 
         ref.check(m, got[m], (back, bound))
 
 
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("kind", ["grid", "image", "ragged image"])
 @pytest.mark.parametrize("extent", [(3, 4), (40, 20)])
-def test_small_steps_with_positions_stay_in_fp32(extent):
-    """bf16 is turned, attended and turned back in fp32, and rounded once."""
-    n = extent[0] * extent[1]
-    x = make(1, 2, 2, n, n, 64, "bf16", seed=16)
+def test_small_steps_with_positions_stay_in_fp32(extent, kind, given):
+    """bf16 is turned into fp32 and attended in it, and every result is rounded once."""
+    b, h, kv, n, d = 2, 4, 2, extent[0] * extent[1], 64
+    x = make(b, h, kv, n, n, d, "bf16", seed=16)
     leaves = [x[m].cuda().requires_grad_() for m in ("q", "k", "v", "lam")]
-    rope = llsa.RopeGridParams.like(leaves[0], leaves[1], columns=(32, 32), extent=extent)
-    o = llsa.diff_attention(*leaves, rope=rope)
-    got = torch.autograd.grad(o, leaves, x["dout"].cuda())
-    wide = [x[m].float().cuda().requires_grad_() for m in ("q", "k", "v")] + [x["lam"].cuda().requires_grad_()]
-    o32 = llsa.diff_attention(*wide, rope=rope.in_fp32())
-    want = torch.autograd.grad(o32, wide, x["dout"].float().cuda())
-    assert torch.equal(o, o32.bfloat16())
-    for a, b in zip(got, want):
-        assert torch.equal(a, b.bfloat16())
+    q, k = leaves[:2]
+    if kind == "grid":
+        rope = llsa.RopeGridParams.like(q, k, columns=(32, 32), extent=extent)
+    else:  # a ragged image has no grid: its positions go through fp32 copies
+        rope = llsa.RopeParams.like(q, k, axes=2, width=extent[1] if kind == "image" else 7)
+    pos = torch.randint(0, 99, (b, n, 2), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda() if given else None
+    o = llsa.diff_attention(*leaves, rope=rope, pos=pos)
+    got = dict(zip(("o", "dq", "dk", "dv", "dlam"), (o, *torch.autograd.grad(o, leaves, x["dout"].cuda()))))
+    y = dict(x)
+    for m, z in zip(("q", "k"), llsa.rotary(q.detach().float(), k.detach().float(), rope.in_fp32(), pos=pos)):
+        y[m] = z.cpu()
+    # fp32 inside: the bounds of fp32 (o is rounded before D is formed: a half step of bf16 of it more), and one rounding to bf16
+    want = ref.attention(**y, dtype=torch.float32, lam_dtype=torch.float32)
+    u = ref.half_step(torch.bfloat16)
+    D = u * (x["dout"].double().abs() * want["o"][0].abs()).sum(-1, keepdim=True)  # what that makes of D
+    for m in ("o", "dv", "dlam"):
+        value, bound = want[m]
+        ref.check(m, got[m], (value, bound + u * value.abs()))
+    P = _weights(y, h, kv)
+    scale = 1 / math.sqrt(d)
+    where = rope.grid(given) if kind != "ragged image" or given else None
+    at = pos.cpu() if given else grid.places(extent)[None] if kind != "ragged image" else torch.stack([torch.arange(n) // 7, torch.arange(n) % 7], -1)[None]
+    for m in ("dq", "dk"):
+        value, bound = (t.clone() for t in want[m])
+        for e in range(b):
+            for hh in range(h):
+                g = hh // (h // kv)
+                # of both maps D carries it: D_1 through o, D_2 through nothing (o2 is fp32)
+                err = scale * P[e, hh] * D[e, hh]
+                if m == "dq":
+                    bound[e, hh] += err @ y["k"][e, g].double().abs()
+                else:
+                    bound[e, g] += err.T @ y["q"][e, hh].double().abs()
+        back, turn = grid.turned(value, at, (32, 32), inverse=True)
+        bound = _columns_sum(bound, grid.pairs((32, 32), "axis", "half")) + turn + u * back.abs()
+        ref.check(m, got[m], (back, bound))
+    assert where is None or where.out_dtype == ""
+
+
+def _weights(y, h, kv):
+    """The first map's softmax, [batch, heads, nq, nk]."""
+    q, k = y["q"][:, :h].double(), y["k"][:, :kv].double().repeat_interleave(h // kv, 1)
+    return torch.softmax(q @ k.transpose(-1, -2) / math.sqrt(q.shape[-1]), -1)
+
+
+@pytest.mark.parametrize("d", [64, 72])
+def test_fp32_queries_and_keys_beside_bf16_values(d):
+    """qk_dtype: the call of fp32 on the same values, with v, o, dout and dv rounded."""
+    x = make(2, 4, 2, 70, 90, d, "bf16", [70, 33], [90, 61], seed=18)
+    g = torch.Generator().manual_seed(4)
+    for m in ("q", "k"):
+        x[m] = x[m].float() * (1 + 0.01 * torch.randn(x[m].shape, generator=g))  # no values of bf16
+    c = {n: t.cuda() for n, t in x.items()}
+    a, b = lens([70, 33]), lens([90, 61])
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], True, v=c["v"])
+    assert p.qk_dtype == "fp32" and p.dtype == "bf16"
+    o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], a, b, backward=True)
+    w = llsa.DiffParams.like(c["q"], c["k"], c["lam"], True)
+    full = (c["q"], c["k"], c["v"].float(), c["lam"])
+    o_w, lse_w, o2_w = llsa.diff_forward(w, *full, a, b, backward=True)
+    assert o2.dtype == torch.float32 and torch.equal(o, o_w.bfloat16()) and torch.equal(lse, lse_w) and torch.equal(o2, o2_w)
+    got = llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], a, b)
+    want = llsa.diff_backward(w, *full, o.float(), o2, lse, c["dout"].float(), a, b)
+    torch.cuda.synchronize()
+    for m, y, z in zip(("dq", "dk", "dv", "dlam"), got, want):
+        assert y.dtype == (torch.float32 if m in ("dq", "dk") else torch.bfloat16), m
+        assert torch.equal(y, z.to(y.dtype)), m
 
 
 SEVERAL = [

@@ -217,3 +217,27 @@ def test_more_threads_than_32_bits_count():
     for f, y in parts.items():
         want = llsa.rotary(y, rope=llsa.RopeGridParams.like(y, extent=(1, 32, 32), offset=(f, 0, 0), **kw))
         assert torch.equal(x[:, :, f * 1024:(f + 1) * 1024], want), f
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,columns", [(64, (16, 24, 24)), (8, (2, 2, 4)), (40, (10, 2, 6)), (256, (2, 100, 154)), (32, (16, 16))])
+def test_into_the_other_type(d, columns, layout):
+    """bf16 in and fp32 out is fp32's result on the same values; fp32 in and bf16 out is that rounded."""
+    x = rand((2, 3, 37, d), "bf16", d).cuda()
+    pos = torch.randint(-5000, 5000, (2, 37, len(columns)), generator=torch.Generator().manual_seed(3), dtype=torch.int32).cuda()
+    p = llsa.RopeGridParams.like(x, columns=columns, layout=layout)
+    want = llsa.rotary(x.float(), rope=p.in_fp32(), pos=pos)
+    up = torch.full((2, 3, 37, d), 7.0, device="cuda")
+    llsa.llsa_rope_grid(p.to_fp32(), x, None, up, None, pos=pos)
+    assert torch.equal(up, want)
+    down = torch.full_like(x, 7.0)
+    llsa.llsa_rope_grid(p.from_fp32(), x.float(), None, down, None, pos=pos)
+    assert torch.equal(down, want.bfloat16())
+
+
+@pytest.mark.parametrize("kw", [dict(pos_offset=9), dict(axes=2, width=6), dict(axes=2, width=10, rot_dim=16, layout="interleaved"),
+                                dict(scaling="base", factor=3.0)])
+def test_the_grid_of_one_and_two_axes(kw):
+    x = rand((1, 2, 60, 32), "bf16", 5).cuda()
+    p = llsa.RopeParams.like(x, **kw)
+    assert torch.equal(llsa.rotary(x, rope=p), llsa.rotary(x, rope=p.grid()))

@@ -48,7 +48,7 @@ def test_parameters_refused(lib, kw, code):
 
 def test_raw_fields_refused(lib):
     for field, value, code in (("dtype", 2, DTYPE), ("layout", 2, INVALID), ("span", 3, INVALID), ("axes", 0, INVALID), ("axes", 5, INVALID),
-                               ("token_order", 2, INVALID), ("pos_batched", 2, INVALID), ("scaling", 4, INVALID)):
+                               ("token_order", 2, INVALID), ("pos_batched", 2, INVALID), ("out_other", 2, INVALID), ("scaling", 4, INVALID)):
         c = llsa._RopeGridParams.from_buffer_copy(bytes(llsa.RopeGridParams(**BASE).c()))
         setattr(c, field, value)
         assert rope(lib, c) == code, field
@@ -62,6 +62,12 @@ def test_pointers_and_strides_refused(lib):
     assert rope(lib, p, pos=6) == ALIGN and rope(lib, p, inverse=2) == INVALID
     # with positions given, what would imply them is ignored: the call gets as far as the device
     assert rope(lib, llsa.RopeGridParams(**{**BASE, "extent": (7, 7, 7), "token_order": "tile"}), pos=6) == ALIGN
+    # into the other type: no tensor is its own output, and strides are in elements of its own type
+    up = llsa.RopeGridParams(**{**BASE, "out_dtype": "fp32"})
+    assert rope(lib, up, outs=(16, 32)) == INVALID and rope(lib, up, outs=(32, 16)) == INVALID
+    st = llsa._RopeStrides()
+    st.q_out[:] = [15364, 3840, 64]  # 4 elements more: 16 bytes of fp32, 8 of bf16
+    assert rope(lib, p, strides=ctypes.byref(st)) == ALIGN and rope(lib, up, outs=(32, 40), strides=ctypes.byref(st)) == ALIGN
     st = llsa._RopeStrides()
     st.q[:] = [15360, 3840, 60]
     assert rope(lib, p, strides=ctypes.byref(st)) == ALIGN
@@ -77,7 +83,7 @@ def test_pointers_and_strides_refused(lib):
 
 def test_binding_refuses(lib):
     for kw in (dict(columns=()), dict(columns=(8,) * 5), dict(extent=(3, 4)), dict(offset=(1,)), dict(step=(1.0, 1.0)),
-               dict(span="both"), dict(layout="pairs"), dict(token_order="z"), dict(dtype="fp16"), dict(scaling="ntk")):
+               dict(span="both"), dict(layout="pairs"), dict(token_order="z"), dict(dtype="fp16"), dict(out_dtype="fp16"), dict(scaling="ntk")):
         with pytest.raises(ValueError):
             llsa.RopeGridParams(**{**BASE, **kw})
     for value in ((1 << 32) + 2, -(1 << 31) - 1):
@@ -103,3 +109,20 @@ def test_parameters_copy_and_pickle():
     for y in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
         assert y == p and bytes(y.c()) == bytes(p.c()) and bytes(y.c(True)) == bytes(p.c(True)) and y.c(True).pos_batched == 1
     assert p.in_fp32().dtype == "fp32" and list(p.c().offset) == [1, 2, 3, 0]
+
+
+@pytest.mark.parametrize("kw,extent", [
+    (dict(pos_offset=5), (60,)), (dict(axes=2, width=6), (10, 6)), (dict(axes=2, width=7), None), (dict(axes=2, width=60, rot_dim=32), (1, 60)),
+    (dict(rot_dim=20, layout="interleaved", scaling="wavelength", factor=2.0, orig_len=9, low=0.5, amplitude=1.5), (60,)),
+])
+def test_one_and_two_axes_as_a_grid(lib, kw, extent):
+    p = llsa.RopeParams(2, 4, 60, 64, kv_heads=2, **kw)
+    g = p.grid()
+    if extent is None:
+        assert g is None and p.grid(True).extent is None
+        return
+    assert g is p.grid() and g.extent == extent and g.grid() is g
+    assert rope(lib, g, pos=6) == ALIGN and rope(lib, p.grid(True), pos=6) == ALIGN  # checked and found right
+    for name in ("layout", "base", "scaling", "factor", "orig_len", "low", "high", "amplitude", "dtype", "batch", "heads", "kv_heads", "n", "d"):
+        assert getattr(g, name) == getattr(p, name)
+    assert sum(g.columns) == (p.rot_dim or p.d) and g.to_fp32().out_dtype == "fp32" and g.from_fp32().dtype == "fp32"
