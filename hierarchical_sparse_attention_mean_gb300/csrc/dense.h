@@ -123,6 +123,14 @@ size_t dense_fwd_workspace(const DenseShape& s);
 size_t dense_bwd_workspace(const DenseShape& s);
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st);
+// Whether a call in fp32 runs on planes, and its passes behind those that make them: forward with
+// `part` for a split's parts; backward also behind the rows' numbers (nl2, nd of `a`).
+bool dense_fwd_on_planes(const DenseShape& s);
+bool dense_bwd_on_planes(const DenseShape& s);
+size_t dense_fwd_parts(const DenseShape& s);
+size_t dense_bwd_parts(const DenseShape& s);
+int launch_dense_fwd_planes(const DenseShape& s, DenseArgs a, const void* const* planes, void* part, cudaStream_t st);
+int launch_dense_bwd_planes(const DenseShape& s, DenseArgs a, void* const* planes, void* part, cudaStream_t st);
 
 // Sums of the parts of up to three outputs, in ascending order: out = sum_p part[p n ..], rounded to `dtype`.
 struct DenseSums {
@@ -190,6 +198,8 @@ DenseSplit dense_split_fwd_split(const DenseShape& s);  // dq: the same
 DenseSplit dense_split_dkv_split(const DenseShape& s);
 size_t dense_split_planes(const DenseShape& s, bool backward);  // bytes
 int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cudaStream_t st);
+// fp32, from planes that are there already ([3][slices][R or nk][d] each of q, k, v).
+int launch_dense_split_fwd_planes(const DenseShape& s, const DenseArgs& a, const void* const* planes, cudaStream_t st);
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st);
 // dense_split_wide_tc.cu: the backward pass of fp32 behind 64 columns and of bf16.
 int launch_dense_split_wide_bwd(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* const* planes,

@@ -275,10 +275,16 @@ DenseArgs dense_args(const DenseShape& s) {
     return a;
 }
 
-size_t dense_fwd_workspace(const DenseShape& s) {
+bool dense_fwd_on_planes(const DenseShape& s) { return s.dtype == LLSA_DTYPE_F32 && fwd_path(s) == Path::kSplit; }
+bool dense_bwd_on_planes(const DenseShape& s) { return s.dtype == LLSA_DTYPE_F32 && bwd_path(s) == Path::kSplit; }
+
+size_t dense_fwd_parts(const DenseShape& s) {
     const DenseSplit p = fwd_split(s);
-    return (fwd_path(s) == Path::kSplit ? dense_split_planes(s, false) : 0) +
-           (p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0);
+    return p.splits > 1 ? (size_t)p.splits * s.slices * s.R * (s.d + 2) * sizeof(float) : 0;
+}
+
+size_t dense_fwd_workspace(const DenseShape& s) {
+    return (fwd_path(s) == Path::kSplit ? dense_split_planes(s, false) : 0) + dense_fwd_parts(s);
 }
 
 // The per-row numbers of the backward pass, one array of the two (the kernels for
@@ -299,12 +305,26 @@ static int launch_dense_nothing(const DenseShape& s, const DenseArgs& a, void* x
     return LLSA_OK;
 }
 
-size_t dense_bwd_workspace(const DenseShape& s) {
+size_t dense_bwd_parts(const DenseShape& s) {
     const DenseSplit pq = dq_split(s), pk = dkv_split(s);
     const size_t dq = pq.splits > 1 ? (size_t)pq.splits * s.slices * s.R * s.d * sizeof(float) : 0;
     const size_t dkv = pk.splits > 1 ? (size_t)pk.splits * 2 * s.slices * s.nk * s.d * sizeof(float) : 0;
-    return (bwd_path(s) == Path::kSplit ? dense_split_planes(s, true) : 0) +
-           2 * dense_rows_bytes(s) + align_up(dq) + dkv;
+    return align_up(dq) + dkv;
+}
+
+size_t dense_bwd_workspace(const DenseShape& s) {
+    return (bwd_path(s) == Path::kSplit ? dense_split_planes(s, true) : 0) + 2 * dense_rows_bytes(s) + dense_bwd_parts(s);
+}
+
+static int launch_dense_join(const DenseShape& s, const DenseArgs& a, cudaStream_t st) {
+    if (a.splits == 1) return LLSA_OK;
+    const long long rows = (long long)s.slices * s.R;
+    const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+    if (s.dtype == LLSA_DTYPE_BF16)
+        LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
+    else
+        LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<float><<<blocks, kThreads, 0, st>>>(a));
+    return LLSA_OK;
 }
 
 int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
@@ -322,16 +342,19 @@ int launch_dense_fwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         case Path::kSplit: LLSA_TRY(launch_dense_split_fwd(s, a, ws, st)); break;
         default: LLSA_TRY(launch_dense_simt_fwd(s, a, st));
     }
-    if (p.splits > 1) {
-        const long long rows = (long long)s.slices * s.R;
-        const unsigned blocks = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
-        if (s.dtype == LLSA_DTYPE_BF16)
-            LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
-        else
-            LLSA_LAUNCH("dense_join_fwd", st, dense_join_fwd_kernel<float><<<blocks, kThreads, 0, st>>>(a));
-    }
-    return LLSA_OK;
+    return launch_dense_join(s, a, st);
 }
+
+int launch_dense_fwd_planes(const DenseShape& s, DenseArgs a, const void* const* planes, void* part, cudaStream_t st) {
+    const DenseSplit p = fwd_split(s);
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.part = static_cast<float*>(part);
+    LLSA_TRY(launch_dense_split_fwd_planes(s, a, planes, st));
+    return launch_dense_join(s, a, st);
+}
+
+static int launch_dense_bwd_sides(const DenseShape& s, DenseArgs a, void* const* planes, void* part, cudaStream_t st);
 
 int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st) {
     const bool bf16 = s.dtype == LLSA_DTYPE_BF16;
@@ -355,6 +378,15 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
         else
             LLSA_LAUNCH("dense_rows", st, dense_rows_kernel<float><<<(unsigned)blocks, kThreads, 0, st>>>(a));
     }
+    return launch_dense_bwd_sides(s, a, path == Path::kSplit ? planes : nullptr, static_cast<char*>(ws) + 2 * rows, st);
+}
+
+int launch_dense_bwd_planes(const DenseShape& s, DenseArgs a, void* const* planes, void* part, cudaStream_t st) {
+    return launch_dense_bwd_sides(s, a, planes, part, st);
+}
+
+static int launch_dense_bwd_sides(const DenseShape& s, DenseArgs a, void* const* planes, void* part, cudaStream_t st) {
+    const Path path = bwd_path(s);
     // dq by blocks of query rows (aq), dk and dv by blocks of keys (ak)
     const DenseSplit pq = dq_split(s), pk = dkv_split(s);
     const long long nq = (long long)s.slices * s.R * s.d, nk = (long long)s.slices * s.nk * s.d;
@@ -363,7 +395,7 @@ int launch_dense_bwd(const DenseShape& s, DenseArgs a, void* ws, cudaStream_t st
     aq.chunk = pq.chunk;
     ak.splits = pk.splits;
     ak.chunk = pk.chunk;
-    aq.part = reinterpret_cast<float*>(static_cast<char*>(ws) + 2 * rows);
+    aq.part = static_cast<float*>(part);
     ak.part = aq.part + (pq.splits > 1 ? align_up((size_t)pq.splits * nq * sizeof(float)) / sizeof(float) : 0);
     switch (path) {
         case Path::kFew: LLSA_TRY(launch_dense_few_bwd(s, aq, st)); break;

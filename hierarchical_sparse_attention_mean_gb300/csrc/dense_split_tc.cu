@@ -678,7 +678,11 @@ int launch_dense_split_fwd(const DenseShape& s, const DenseArgs& a, void* ws, cu
     __nv_bfloat16* p[3];
     LLSA_TRY(write_planes(x, elems, 3, ws, p, st));
     const void* const y[3] = {p[0], p[1], p[2]};
-    return s.d <= 64 ? launch_fwd<64, 3>(s, a, y, st) : launch_fwd<128, 3>(s, a, y, st);
+    return launch_dense_split_fwd_planes(s, a, y, st);
+}
+
+int launch_dense_split_fwd_planes(const DenseShape& s, const DenseArgs& a, const void* const* planes, cudaStream_t st) {
+    return s.d <= 64 ? launch_fwd<64, 3>(s, a, planes, st) : launch_fwd<128, 3>(s, a, planes, st);
 }
 
 int make_dense_split_planes(const DenseShape& s, const DenseArgs& a, void* ws, void** planes, cudaStream_t st) {

@@ -100,6 +100,65 @@ __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_cons
     }
 }
 
+// The four calls' operands at once as the three bf16 planes that the fp32 kernels read:
+// blockIdx.y q, k, v, dout. Eight values per thread, written to both calls that share them
+// (dout: as it is, and times -lam). Bound by HBM: 4 bytes in, 12 out.
+struct PlanesArgs {
+    DiffArgs a;
+    __nv_bfloat16* out[4];  // plane p of tensor t at out[t] + p * n[t]
+    long long n[4];
+};
+
+__device__ __forceinline__ void put_planes(__nv_bfloat16* out, long long n, const float* y) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++) f[e] = y[e];
+#pragma unroll
+    for (int p = 0; p < 3; p++) {
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+            __nv_bfloat162 h = __floats2bfloat162_rn(f[c], f[c + 1]);
+            w[c >> 1] = *reinterpret_cast<uint32_t*>(&h);
+            f[c] -= __uint_as_float(w[c >> 1] << 16);
+            f[c + 1] -= __uint_as_float(w[c >> 1] & 0xffff0000u);
+        }
+        *reinterpret_cast<uint4*>(out + p * n) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <typename T, typename Q>
+__global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_constant__ PlanesArgs f) {
+    const DenseArgs& a = f.a.d;
+    const int t = blockIdx.y;
+    const bool one = t < 2;  // a matrix of d columns per map, or of 2 d for both
+    const int rows = t == 0 || t == 3 ? a.R : a.nk, cols = one ? a.d : 2 * a.d, per = cols / 8;
+    const long long total = (long long)a.slices * (one ? 2 : 1) * rows * per, step = (long long)a.kv_heads * rows * a.d;
+    for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < total; x += (long long)gridDim.x * kThreads) {
+        const long long row = x / per;
+        int c = (int)(x - row * per) * 8;
+        const long long m = row / rows, outer = m / a.kv_heads;  // outer: 2 b + i, or b
+        const int r = (int)(row - m * rows), g = (int)(m - outer * a.kv_heads);
+        float y[8];
+        if (one) load8(static_cast<const Q*>(t == 0 ? a.q : a.k) + x * 8, y);
+        else load8(static_cast<const T*>(t == 2 ? a.v : a.dout) + x * 8, y);
+        int j = 0;
+        if (!one && c >= a.d) {
+            j = 1;
+            c -= a.d;
+        }
+        const long long matrix = one ? 2 * outer * a.kv_heads + g : (4 * outer + j) * a.kv_heads + g;
+        const long long at = (matrix * rows + r) * a.d + c;
+        put_planes(f.out[t] + at, f.n[t], y);
+        if (t == 3) {
+            const float lam = diff_lam(f.a, diff_head(f.a, (int)m, r));
+#pragma unroll
+            for (int e = 0; e < 8; e++) y[e] *= -lam;
+        }
+        put_planes(f.out[t] + at + (one ? step : 2 * step), f.n[t], y);
+    }
+}
+
 // o, o2 and the log-sum-exp of both maps from the four calls' (in f.o and f.lse).
 template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_constant__ FourArgs f) {
@@ -242,20 +301,10 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
 // maps, D_1 = dout . (o + lam o2) and D_2 = dout . o2, and lam. Rows that see no key (and
 // the padding to Rp) get -infinity and 0, so that their probabilities are 2^(s - inf) = 0.
 // A block per 128 rows, eight lanes per row, four rows each at a time. Bound by HBM: dout,
-// o and o2 are read once.
+// o and o2 are read once. FOUR: the same for the four calls of the form above, and D_2 itself.
 constexpr int kRowsEach = kDenseRowPad / (kThreads / 8);
 
-__device__ __forceinline__ float dot8(const uint4& x, const uint4& y) {
-    const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        sum = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), sum);
-        sum = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u), sum);
-    }
-    return sum;
-}
-
+template <typename T, typename Q, bool FOUR>
 __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_constant__ DiffArgs f) {
     const DenseArgs& a = f.d;
     const unsigned per = (unsigned)a.Rp / kDenseRowPad, slice = blockIdx.x / per;
@@ -270,24 +319,34 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
         on[u] = r < a.R && dense_kend(a, sp, r < a.nq ? r : r % a.nq) > 0;
         one[u] = two[u] = 0.f;
     }
-    for (int c = part * 8; c < dv; c += 64) {
-        uint4 g[kRowsEach], x[kRowsEach], y[kRowsEach];
+    constexpr int E = sizeof(T) == 2 && sizeof(Q) == 2 ? 8 : 4;
+    for (int c = part * E; c < dv; c += 8 * E) {
         const long long at = ((long long)slice * a.R + r0) * dv + c;
+        float g[kRowsEach][E], x[kRowsEach][E], y[kRowsEach][E];
 #pragma unroll
         for (int u = 0; u < kRowsEach; u++) {
-            g[u] = x[u] = y[u] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int e = 0; e < E; e++) g[u][e] = x[u][e] = y[u][e] = 0.f;
             if (on[u]) {
                 const long long to = at + (long long)u * (kThreads / 8) * dv;
-                g[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + to));
-                x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.o) + to));
-                y[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(f.o2) + to));
+                if constexpr (E == 8) {
+                    load8(static_cast<const T*>(a.dout) + to, g[u]);
+                    load8(static_cast<const T*>(a.o) + to, x[u]);
+                    load8(static_cast<const Q*>(f.o2) + to, y[u]);
+                } else {
+                    load4f(static_cast<const T*>(a.dout) + to, g[u]);
+                    load4f(static_cast<const T*>(a.o) + to, x[u]);
+                    load4f(static_cast<const Q*>(f.o2) + to, y[u]);
+                }
             }
         }
 #pragma unroll
-        for (int u = 0; u < kRowsEach; u++) {
-            one[u] += dot8(g[u], x[u]);
-            two[u] += dot8(g[u], y[u]);
-        }
+        for (int u = 0; u < kRowsEach; u++)
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                one[u] = fmaf(g[u][e], x[u][e], one[u]);
+                two[u] = fmaf(g[u][e], y[u][e], two[u]);
+            }
     }
     const long long all = (long long)a.slices * a.Rp;
 #pragma unroll
@@ -297,19 +356,29 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
             one[u] += __shfl_xor_sync(0xffffffffu, one[u], o);
             two[u] += __shfl_xor_sync(0xffffffffu, two[u], o);
         }
-        if (part == 0) {
-            const int r = r0 + u * (kThreads / 8);
-            const long long idx = (long long)slice * a.Rp + r;
-            const float lam = on[u] ? diff_lam(f, diff_head(f, (int)slice, r)) : 0.f;
+        if (part != 0) continue;
+        const int r = r0 + u * (kThreads / 8);
+        const long long idx = (long long)slice * a.Rp + r;
+        const float lam = on[u] ? diff_lam(f, diff_head(f, (int)slice, r)) : 0.f;
+        const float D[2] = {on[u] ? -fmaf(lam, two[u], one[u]) : 0.f, on[u] ? -two[u] : 0.f};
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const float lse = on[u] ? __ldg(a.lse + diff_row(f, (int)slice, i, r)) : -INFINITY;
-                a.nl2[i * all + idx] = lse == -INFINITY ? -INFINITY : -lse * kDenseLog2e;
+        for (int i = 0; i < 2; i++) {
+            const float lse = on[u] ? __ldg(a.lse + diff_row(f, (int)slice, i, r)) : -INFINITY;
+            const float l2 = lse == -INFINITY ? -INFINITY : -lse * kDenseLog2e;
+            if constexpr (FOUR) {
+                // both halves' calls of map i; only the sum of their D counts, weighed as their dout is
+                const int b = (int)slice / a.kv_heads, gg = (int)slice - b * a.kv_heads;
+                const long long first = ((4LL * b + 2 * i) * a.kv_heads + gg) * a.Rp + r, second = first + (long long)a.kv_heads * a.Rp;
+                a.nl2[first] = a.nl2[second] = l2;
+                a.nd[first] = i == 0 ? D[0] : -lam * D[1];
+                a.nd[second] = 0.f;
+            } else {
+                a.nl2[i * all + idx] = l2;
+                a.nl2[(2 + i) * all + idx] = D[i];
             }
-            a.nl2[2 * all + idx] = on[u] ? -fmaf(lam, two[u], one[u]) : 0.f;
-            a.nl2[3 * all + idx] = on[u] ? -two[u] : 0.f;
-            a.nl2[4 * all + idx] = lam;
         }
+        if constexpr (FOUR) f.d2[idx] = -D[1];
+        else a.nl2[4 * all + idx] = lam;
     }
 }
 
@@ -454,7 +523,27 @@ size_t four_rows(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.
 size_t four_keys(const DiffShape& s) { return up((size_t)4 * s.slices * s.nk * s.d * sizeof(float)); }
 size_t four_lse(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * sizeof(float)); }
 
+size_t plane_rows(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.d * 6); }
+size_t plane_keys(const DiffShape& s) { return up((size_t)4 * s.slices * s.nk * s.d * 6); }
+size_t padded_rows(const DiffShape& s) { return up((size_t)s.slices * s.Rp * sizeof(float)); }
+
+// One block per head up to 4,096 of its rows: a second launch costs more than a long loop.
+int row_parts(const DiffShape& s) { return (int)std::min<long long>(64, ((long long)s.batch * s.nq + 4095) / 4096); }
+size_t row_parts_bytes(const DiffShape& s) { return up((size_t)s.heads * row_parts(s) * sizeof(float)); }
+
+int launch_lam_rows(const DiffShape& s, const DiffArgs& a, int sets, float* part, void* dlam, cudaStream_t st) {
+    const int parts = row_parts(s);
+    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * parts, kLamThreads, 0, st>>>(a, part, parts, sets, dlam));
+    if (parts > 1) LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(part, parts, dlam, a.lam_bf16));
+    return LLSA_OK;
+}
+
 size_t four_workspace(const DiffShape& s, bool backward) {
+    if (!backward && dense_fwd_on_planes(s.four))
+        return plane_rows(s) + 2 * plane_keys(s) + four_rows(s) + four_lse(s) + up(dense_fwd_parts(s.four));
+    if (backward && dense_bwd_on_planes(s.four))
+        return 2 * plane_rows(s) + 2 * plane_keys(s) + four_rows(s) + 2 * four_keys(s) + 9 * padded_rows(s) + row_parts_bytes(s) +
+               up(dense_bwd_parts(s.four));
     return backward ? 4 * four_rows(s) + 4 * four_keys(s) + four_lse(s) + up(dense_bwd_workspace(s.four))
                     : 2 * four_rows(s) + 2 * four_keys(s) + four_lse(s) + up(dense_fwd_workspace(s.four));
 }
@@ -471,8 +560,83 @@ DenseArgs four_args(const DiffShape& s, const DiffArgs& a, const FourArgs& f) {
 
 unsigned blocks_for(long long n) { return (unsigned)std::min<long long>((n + kThreads - 1) / kThreads, 16LL * kDenseSms); }
 
+// Planes of q, k, v and (backward) dout, one after the other from `at` on.
+template <typename T, typename Q>
+int launch_planes(const DiffShape& s, const DiffArgs& a, bool backward, char*& at, void** planes, cudaStream_t st) {
+    PlanesArgs f;
+    memset(&f, 0, sizeof(f));
+    f.a = a;
+    const long long nq = 4LL * s.slices * s.R * s.d, nk = 4LL * s.slices * s.nk * s.d;
+    for (int t = 0; t < (backward ? 4 : 3); t++) {
+        const bool rows = t == 0 || t == 3;
+        f.out[t] = reinterpret_cast<__nv_bfloat16*>(at);
+        f.n[t] = rows ? nq : nk;
+        planes[t] = at;
+        at += rows ? plane_rows(s) : plane_keys(s);
+    }
+    const dim3 grid((unsigned)std::min<long long>((std::max(nq, nk) / 16 + kThreads - 1) / kThreads, 8LL * kDenseSms), backward ? 4 : 3);
+    LLSA_LAUNCH("diff_planes", st, (diff_planes_kernel<T, Q><<<grid, kThreads, 0, st>>>(f)));
+    return LLSA_OK;
+}
+
+template <typename T, typename Q>
+int launch_planes_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStream_t st) {
+    FourArgs f;
+    memset(&f, 0, sizeof(f));
+    f.a = a;
+    char* at = static_cast<char*>(ws);
+    void* planes[4];
+    LLSA_TRY((launch_planes<T, Q>(s, a, false, at, planes, st)));
+    f.o = reinterpret_cast<float*>(at);
+    at += four_rows(s);
+    f.lse = reinterpret_cast<float*>(at);
+    at += four_lse(s);
+    DenseArgs d = four_args(s, a, f);
+    d.o_out = f.o;
+    d.lse_out = f.lse;
+    LLSA_TRY(launch_dense_fwd_planes(s.four, d, planes, at, st));
+    LLSA_LAUNCH("diff_combine", st,
+                (diff_combine_kernel<T, Q><<<blocks_for((long long)s.slices * s.R * (s.d / 2)), kThreads, 0, st>>>(f)));
+    return LLSA_OK;
+}
+
+template <typename T, typename Q>
+int launch_planes_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, void* dlam, void* ws, cudaStream_t st) {
+    char* at = static_cast<char*>(ws);
+    auto take = [&](size_t bytes) { char* p = at; at += bytes; return reinterpret_cast<float*>(p); };
+    void* planes[4];
+    LLSA_TRY((launch_planes<T, Q>(s, a, true, at, planes, st)));
+    void* const order[4] = {planes[0], planes[3], planes[1], planes[2]};  // q, dout, k, v
+    FourArgs f;
+    memset(&f, 0, sizeof(f));
+    float *gq = take(four_rows(s)), *gk = take(four_keys(s)), *gv = take(four_keys(s));
+    a.d.nl2 = take(4 * padded_rows(s));
+    a.d.nd = take(4 * padded_rows(s));
+    a.d2 = take(padded_rows(s));
+    float* part = take(row_parts_bytes(s));
+    const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
+    if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
+    LLSA_LAUNCH("diff_rows", st, (diff_rows_kernel<T, Q, true><<<(unsigned)blocks, kThreads, 0, st>>>(a)));
+    f.a = a;
+    DenseArgs d = four_args(s, a, f);
+    d.dq = gq;
+    d.dk = gk;
+    d.dv = gv;
+    LLSA_TRY(launch_dense_bwd_planes(s.four, d, order, at, st));
+    f.dq = gq;
+    f.dk = gk;
+    f.dv = gv;
+    f.dq_out = dq;
+    f.dk_out = dk;
+    f.dv_out = dv;
+    const unsigned grid = blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4));
+    LLSA_LAUNCH("diff_collapse", st, (diff_collapse_kernel<T, Q><<<dim3(grid, 3), kThreads, 0, st>>>(f)));
+    return launch_lam_rows(s, a, 1, part, dlam, st);
+}
+
 template <typename T, typename Q>
 int launch_four_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStream_t st) {
+    if (dense_fwd_on_planes(s.four)) return launch_planes_fwd<T, Q>(s, a, ws, st);
     FourArgs f;
     memset(&f, 0, sizeof(f));
     f.a = a;
@@ -498,6 +662,7 @@ size_t lam_bytes(const DiffShape& s) { return s.heads ? up((size_t)s.heads * lam
 
 template <typename T, typename Q>
 int launch_four_bwd(const DiffShape& s, const DiffArgs& a, void* dq, void* dk, void* dv, void* dlam, void* ws, cudaStream_t st) {
+    if (dense_bwd_on_planes(s.four)) return launch_planes_bwd<T, Q>(s, a, dq, dk, dv, dlam, ws, st);
     LLSA_TRY((launch_lam<T, Q>(s, a, dlam, static_cast<float*>(ws), st)));
     if (s.R == 0 && s.nk == 0) return LLSA_OK;
     FourArgs f;
@@ -581,7 +746,6 @@ Path bwd_path(const DiffShape& s) { return !s.wide && diff_tc_supported(s) ? Pat
 struct TcBwd {
     DenseSplit q, k;
     long long nq, nk;  // elements of dq, and of dk or dv
-    int lam_parts;
     size_t stats, d2, lam, dq, dkv;
     size_t bytes() const { return stats + d2 + lam + dq + dkv; }
 };
@@ -595,9 +759,7 @@ TcBwd tc_bwd(const DiffShape& s) {
     const size_t rows = (size_t)s.slices * s.Rp * sizeof(float);
     t.stats = up(kDiffStats * rows);
     t.d2 = up(4 * t.q.splits * rows);
-    // one block per head up to 4,096 of its rows: a second launch costs more than a long loop
-    t.lam_parts = (int)std::min<long long>(64, ((long long)s.batch * s.nq + 4095) / 4096);
-    t.lam = up((size_t)s.heads * t.lam_parts * sizeof(float));
+    t.lam = row_parts_bytes(s);
     t.dq = t.q.splits > 1 ? up(t.q.splits * t.nq * sizeof(float)) : 0;
     t.dkv = t.k.splits > 1 ? up(2 * t.k.splits * t.nk * sizeof(float)) : 0;
     return t;
@@ -622,12 +784,9 @@ int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, 
     ak.d.part = take(t.dkv);
     const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("diff_rows", st, diff_rows_kernel<<<(unsigned)blocks, kThreads, 0, st>>>(a));
+    LLSA_LAUNCH("diff_rows", st, (diff_rows_kernel<__nv_bfloat16, __nv_bfloat16, false><<<(unsigned)blocks, kThreads, 0, st>>>(a)));
     LLSA_TRY(launch_diff_tc_bwd(s, aq, ak, st));
-    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * t.lam_parts, kLamThreads, 0, st>>>(a, lam, t.lam_parts,
-                                                                                                                 4 * t.q.splits, dlam));
-    if (t.lam_parts > 1)
-        LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(lam, t.lam_parts, dlam, a.lam_bf16));
+    LLSA_TRY(launch_lam_rows(s, a, 4 * t.q.splits, lam, dlam, st));
     DenseSums sums;
     if (t.q.splits > 1) sums.add(aq.d.part, dq, t.nq, t.q.splits);
     if (t.k.splits > 1) {
@@ -638,7 +797,7 @@ int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, 
 }
 
 size_t bwd_workspace(const DiffShape& s) {
-    return bwd_path(s) == Path::kTc ? tc_bwd(s).bytes() : lam_bytes(s) + four_workspace(s, true);
+    return bwd_path(s) == Path::kTc ? tc_bwd(s).bytes() : (dense_bwd_on_planes(s.four) ? 0 : lam_bytes(s)) + four_workspace(s, true);
 }
 
 }  // namespace
