@@ -12,6 +12,7 @@
 #include <string.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "diff.h"
 #include "entry.h"
@@ -304,6 +305,24 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
 // o and o2 are read once. FOUR: the same for the four calls of the form above, and D_2 itself.
 constexpr int kRowsEach = kDenseRowPad / (kThreads / 8);
 
+// A vector's values as fp32.
+__device__ __forceinline__ void unpack(const uint2& v, float* f, const __nv_bfloat16*) {
+    f[0] = __uint_as_float(v.x << 16);
+    f[1] = __uint_as_float(v.x & 0xffff0000u);
+    f[2] = __uint_as_float(v.y << 16);
+    f[3] = __uint_as_float(v.y & 0xffff0000u);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float* f, const __nv_bfloat16* t) {
+    unpack(make_uint2(v.x, v.y), f, t);
+    unpack(make_uint2(v.z, v.w), f + 4, t);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float* f, const float*) {
+    f[0] = __uint_as_float(v.x);
+    f[1] = __uint_as_float(v.y);
+    f[2] = __uint_as_float(v.z);
+    f[3] = __uint_as_float(v.w);
+}
+
 template <typename T, typename Q, bool FOUR>
 __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_constant__ DiffArgs f) {
     const DenseArgs& a = f.d;
@@ -319,34 +338,35 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
         on[u] = r < a.R && dense_kend(a, sp, r < a.nq ? r : r % a.nq) > 0;
         one[u] = two[u] = 0.f;
     }
-    constexpr int E = sizeof(T) == 2 && sizeof(Q) == 2 ? 8 : 4;
+    // vectors as they lie in memory: as fp32 four rows of three would not fit the registers
+    using VT = std::conditional_t<sizeof(T) == sizeof(Q), uint4, uint2>;  // of dout and o
+    constexpr int E = sizeof(VT) / sizeof(T);                             // elements; o2's vector is 16 bytes in any case
     for (int c = part * E; c < dv; c += 8 * E) {
+        VT g[kRowsEach], x[kRowsEach];
+        uint4 y[kRowsEach];
         const long long at = ((long long)slice * a.R + r0) * dv + c;
-        float g[kRowsEach][E], x[kRowsEach][E], y[kRowsEach][E];
 #pragma unroll
         for (int u = 0; u < kRowsEach; u++) {
-#pragma unroll
-            for (int e = 0; e < E; e++) g[u][e] = x[u][e] = y[u][e] = 0.f;
+            g[u] = x[u] = VT{};
+            y[u] = uint4{};
             if (on[u]) {
                 const long long to = at + (long long)u * (kThreads / 8) * dv;
-                if constexpr (E == 8) {
-                    load8(static_cast<const T*>(a.dout) + to, g[u]);
-                    load8(static_cast<const T*>(a.o) + to, x[u]);
-                    load8(static_cast<const Q*>(f.o2) + to, y[u]);
-                } else {
-                    load4f(static_cast<const T*>(a.dout) + to, g[u]);
-                    load4f(static_cast<const T*>(a.o) + to, x[u]);
-                    load4f(static_cast<const Q*>(f.o2) + to, y[u]);
-                }
+                g[u] = __ldg(reinterpret_cast<const VT*>(static_cast<const T*>(a.dout) + to));
+                x[u] = __ldg(reinterpret_cast<const VT*>(static_cast<const T*>(a.o) + to));
+                y[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const Q*>(f.o2) + to));
             }
         }
 #pragma unroll
-        for (int u = 0; u < kRowsEach; u++)
+        for (int u = 0; u < kRowsEach; u++) {
+            float p[E], q[E];
+            unpack(g[u], p, static_cast<const T*>(nullptr));
+            unpack(x[u], q, static_cast<const T*>(nullptr));
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                one[u] = fmaf(g[u][e], x[u][e], one[u]);
-                two[u] = fmaf(g[u][e], y[u][e], two[u]);
-            }
+            for (int e = 0; e < E; e++) one[u] = fmaf(p[e], q[e], one[u]);
+            unpack(y[u], q, static_cast<const Q*>(nullptr));
+#pragma unroll
+            for (int e = 0; e < E; e++) two[u] = fmaf(p[e], q[e], two[u]);
+        }
     }
     const long long all = (long long)a.slices * a.Rp;
 #pragma unroll
