@@ -1274,7 +1274,7 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
     in fp32 from the turn to the last rounding where that call's does, and up to 2^30
     products of a pair of a query and a key (both maps' pairs times d)."""
-    if isinstance(lam, torch.Tensor) and lam.numel() == 1 and q.shape[1] != 2:
+    if isinstance(lam, torch.Tensor) and lam.numel() == 1:
         lam = lam.reshape(1).expand(q.shape[1] // 2)
     return _dense_fns()[2].apply(q, k, v, lam, causal, scale, q_len, k_len, rope, pos)
 

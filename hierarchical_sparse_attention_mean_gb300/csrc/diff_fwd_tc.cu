@@ -403,7 +403,8 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             const float l = (l0 + l1) + (l2 + l3);
             Piece pc;
             pc.take(bar->pieces.slot[slot][0], bar->pieces.slot[slot][1]);
-            warp_arrive(smem_u32(&bar->pieces.free[slot]), lane);
+            // the slot is free when its numbers have come: an arrival could overtake loads that nothing waits for
+            if (__all_sync(0xffffffffu, (pc.col | pc.slice) >= 0)) warp_arrive(smem_u32(&bar->pieces.free[slot]), lane);
             const int r = pc.r0 + lr, dv = 2 * a.d;
             const bool here = r < a.R;
             const long long row = (long long)pc.slice * a.R + r, prow = diff_part(a, pc.part, w, row);

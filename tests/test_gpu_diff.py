@@ -468,6 +468,97 @@ def test_few_rows(h, kv, nq, d, dtype):
     both(make(2, h, kv, nq, 700, d, dtype, None, [700, 531], seed=13), dtype, causal=True, k_len=[700, 531])
 
 
+@pytest.mark.parametrize("cfg,ql,kl,causal", [
+    ((2, 8, 2, 333, 450, 128), [333, 200], [450, 77], True),   # stages of the rows' numbers that come round
+    ((2, 8, 2, 333, 450, 64), [333, 200], [450, 77], True),
+    ((3, 4, 2, 500, 700, 96), [500, 200, 3], [450, 77, 700], False),
+    ((3, 4, 2, 500, 700, 40), [500, 200, 3], [450, 77, 700], False),
+    ((1, 2, 2, 1, 20000, 64), None, None, False),              # a ring of copies that comes round
+    ((1, 4, 2, 1, 20000, 128), None, None, False),
+    ((16, 12, 12, 200, 260, 64), None, None, True),            # several pieces per block
+])
+def test_many_repeats_are_bit_equal(cfg, ql, kl, causal):
+    """A buffer that is handed on too early shows now and then: 60 runs give one result."""
+    c = {n: t.cuda() for n, t in make(*cfg, "bf16", ql, kl, seed=19).items()}
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], causal=causal)
+    a, b = lens(ql), lens(kl)
+    busy = torch.empty(1 << 24, device="cuda")
+    want = None
+    for i in range(60):
+        if i % 3 == 0:
+            busy.normal_()  # other contents of the caches
+        o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], a, b, backward=True)
+        got = (o, o2, lse, *llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], a, b))
+        want = want or got
+        for n, x, y in zip(NAMES, got, want):
+            assert torch.equal(x, y), (i, n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("b,h,kv,nq,nk,causal,ql,kl", [
+    (2, 6, 6, 700, 333, False, None, None), (3, 4, 2, 500, 600, True, [500, 0, 77], [1, 600, 300]), (2, 4, 1, 300, 200, False, None, [200, 0])])
+def test_three_resident_blocks_take_everything(b, h, kv, nq, nk, causal, ql, kl, d):
+    """The forward's blocks take many pieces of each kind in turn; results stay bit for bit."""
+    x = make(b, h, kv, nq, nk, d, "bf16", ql, kl, seed=20)
+    want = run(x, causal, 0.0, ql, kl)
+    llsa.test_set_wait_limit(0, llsa.LLSA_TEST_FEW_BLOCKS)
+    try:
+        got = run(x, causal, 0.0, ql, kl)
+    finally:
+        llsa.test_set_wait_limit(0, 0)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+def test_inputs_and_gradients_off_16_bytes():
+    """Views into flat buffers, as a packed set of parameters gives them: copied, not refused."""
+    x = make(1, 2, 2, 40, 50, 64, "bf16", seed=21)
+    want = run(x)
+
+    def off(t):  # two bytes behind a 16-byte boundary
+        flat = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")
+        view = flat[1:].view(t.shape)
+        view.copy_(t)
+        return view.requires_grad_()
+
+    leaves = [off(x[n]) for n in ("q", "k", "v", "lam")]
+    o = llsa.diff_attention(*leaves)
+    got = torch.autograd.grad(o, leaves, off(x["dout"]).detach())
+    assert torch.equal(o, want["o"])
+    for n, g in zip(("dq", "dk", "dv", "dlam"), got):
+        assert torch.equal(g, want[n]), n
+
+
+def test_a_number_for_one_head():
+    """lam without a dimension, one head: its gradient comes back in its shape."""
+    x = make(1, 1, 1, 30, 40, 64, "fp32", seed=22)
+    lam = x["lam"][0].cuda().requires_grad_()
+    o = llsa.diff_attention(x["q"].cuda(), x["k"].cuda(), x["v"].cuda(), lam)
+    (g,) = torch.autograd.grad(o, lam, x["dout"].cuda())
+    want = run(x)
+    assert g.shape == () and torch.equal(g, want["dlam"][0]) and torch.equal(o, want["o"])
+
+
+def test_types_that_do_not_go_together_are_refused():
+    x = {n: t.cuda() for n, t in make(1, 2, 2, 30, 40, 64, "bf16").items()}
+    for n in ("q", "k"):
+        y = {**x, n: x[n].float()}
+        with pytest.raises(ValueError):
+            llsa.diff_attention(y["q"], y["k"], y["v"], y["lam"])
+    with pytest.raises(ValueError):
+        llsa.diff_attention(x["q"], x["k"], x["v"].float(), x["lam"])
+    with pytest.raises(ValueError, match="lam"):
+        llsa.diff_attention(x["q"], x["k"], x["v"], x["lam"].half())
+    with pytest.raises(ValueError, match="v must have shape"):
+        llsa.diff_attention(x["q"], x["k"], x["v"][..., :64].contiguous(), x["lam"])
+    with pytest.raises(ValueError, match="lam must have shape"):
+        llsa.diff_attention(x["q"], x["k"], x["v"], x["lam"].repeat(2))
+    rope = llsa.RopeGridParams.like(x["q"], x["k"], columns=(64,))
+    with pytest.raises(ValueError):
+        llsa.diff_attention(x["q"], x["k"], x["v"], x["lam"], rope=rope)  # other tokens in q and k
+    assert llsa.llsa_get_status() == 0
+
+
 def test_nan_among_the_scores_stays_in_its_row():
     """A query with a NaN gets NaN in o and lse of that map; its neighbours do not."""
     for nq in (1, 130):
