@@ -1,6 +1,6 @@
 // diff_few.cu -- differential attention forward for a few query rows per value head (single
 // tokens, their shared-value heads, pooling queries): both maps' keys and the values are read
-// once, on the CUDA cores.
+// once per two rows, on the CUDA cores.
 //
 // Mathematics: one pass over the keys with a running maximum and sum for each map; a key's
 // two weights meet its value while that is in registers. The keys of a slice are split
@@ -8,11 +8,13 @@
 // maxima, sums and outputs, joined at the end in a fixed order, and the maps' difference
 // is formed in fp32 there.
 //
-// Bound by HBM: 12 d flops per key and row against 8 d bytes per key (bf16). Keys and values
-// of consecutive tokens lie next to each other, so a stage of 32 KB is three bulk copies,
-// and a block per SM keeps six of them in flight; with the loads in registers instead, as
-// many as fit, 6 heads x 65,536 keys of 64 columns took 49 us. A group of 8 or 16 lanes
-// takes one key, 8 columns of each map's key and 16 of the value per lane.
+// Bound by HBM with one row: 12 d flops per key and row against 8 d bytes per key (bf16). Keys
+// and values of consecutive tokens lie next to each other, so a stage of 32 KB is three bulk
+// copies, and a block per SM keeps six of them in flight: 6 heads x 65,536 keys of 64 columns,
+// 201 MB, in 37 us (5.4 TB/s), the join of the parts 5 more; with the loads in registers instead,
+// as many as fit, the kernel took 4 more. A group of 8 or 16 lanes takes one key, 8
+// columns of each map's key and 16 of the value per lane. Further rows go in pairs, blocks
+// side by side that read the same keys: the second pair finds them in L2.
 #include <algorithm>
 
 #include "dense_tc.cuh"
@@ -68,11 +70,11 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int slice = blockIdx.x / a.splits, part = blockIdx.x - slice * a.splits;
     const DenseSpan sp = dense_span(a, slice);
-    const int dv = 2 * a.d;
+    const int dv = 2 * a.d, r0 = blockIdx.y * RR;
     int kend[RR], most = 0;
 #pragma unroll
     for (int r = 0; r < RR; r++) {
-        kend[r] = r < a.R ? dense_kend(a, sp, r % a.nq) : 0;
+        kend[r] = r0 + r < a.R ? dense_kend(a, sp, (r0 + r) % a.nq) : 0;
         most = max(most, kend[r]);
     }
     const int first = part * a.chunk;
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
 #pragma unroll
                 for (int c = 0; c < 8; c++) q[r][i][c] = acc[r][i][c] = acc[r][i][c + 8] = 0.f;
                 if (on && kend[r] > 0) {
-                    load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r) * a.d + col, q[r][i]);
+                    load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r0 + r) * a.d + col, q[r][i]);
 #pragma unroll
                     for (int c = 0; c < 8; c++) q[r][i][c] *= sl2;
                 }
@@ -239,9 +241,9 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
     __syncthreads();
     for (int x = threadIdx.x; x < RR * dv; x += kThreads) {
         const int r = x / dv, c = x - r * dv;
-        if (r >= a.R) break;
+        if (r0 + r >= a.R) break;
         float out[2];
-        const long long row = (long long)slice * a.R + r;
+        const long long row = (long long)slice * a.R + r0 + r;
 #pragma unroll
         for (int i = 0; i < 2; i++) {
             float top = -INFINITY;
@@ -262,11 +264,11 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
                 if (c == 0) diff_part_ml(a)[prow] = make_float2(top, sum);
             } else {
                 out[i] = sum == 0.f ? 0.f : o / sum;
-                if (c == 0) a.lse_out[diff_row(f, slice, i, r)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                if (c == 0) a.lse_out[diff_row(f, slice, i, r0 + r)] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
             }
         }
         if (a.splits > 1) continue;
-        const float o = fmaf(-diff_lam(f, diff_head(f, slice, r)), out[1], out[0]);
+        const float o = fmaf(-diff_lam(f, diff_head(f, slice, r0 + r)), out[1], out[0]);
         if constexpr (sizeof(T) == 2) {
             static_cast<__nv_bfloat16*>(a.o_out)[row * dv + c] = __float2bfloat16_rn(o);
             if (f.o2_out) static_cast<__nv_bfloat16*>(f.o2_out)[row * dv + c] = __float2bfloat16_rn(out[1]);
@@ -284,7 +286,7 @@ int launch_lanes(const DiffArgs& a, cudaStream_t st) {
     constexpr int smem = kStages * kStage + (int)sizeof(FewBars);
     static_assert(smem <= 227 * 1024 && kFewWarps<RR> * RR * 2 * (2 * LANES * 8 + 2) * 4 <= kStages * kStage, "shared memory budget");
     cudaFuncSetAttribute(diff_few_kernel<T, RR, LANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    LLSA_LAUNCH("diff_few", st, diff_few_kernel<T, RR, LANES><<<(unsigned)blocks, (kFewWarps<RR> + 1) * 32, smem, st>>>(a));
+    LLSA_LAUNCH("diff_few", st, (diff_few_kernel<T, RR, LANES><<<dim3((unsigned)blocks, (a.d.R + RR - 1) / RR), (kFewWarps<RR> + 1) * 32, smem, st>>>(a)));
     return LLSA_OK;
 }
 
@@ -296,12 +298,28 @@ int launch(const DiffShape& s, const DiffArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-bool diff_few_supported(const DiffShape& s) { return s.R > 0 && s.R <= 2 && s.nk > 0; }
+// Where this is the faster way, times in us here and there (head columns d = 64):
+// bf16 against the tensor cores, which read rows by 128. One row: 8 x 4 heads x 16,383 keys 66
+//   and 70, d = 128 109 and 121; 6 heads x 65,536 keys 56 and 60; 16 heads x 256 keys 17 and 13. A
+//   pair of rows is bound by instructions (88 and 70; 156 and 121), and only where the other way
+//   needs a split and a join for little work, up to 2^22 key elements that the pairs read, are
+//   up to eight rows better off here: 4 heads x 2,048 keys 20 and 27.
+// fp32 against three planes of every operand, which are written first: 8 x 4 heads x 16,383 keys
+//   two rows 109 and 513, four 156 and 574, eight 281 and 640, sixteen 550 and 639; 64 x 16 heads
+//   x 64 keys four 101 and 156, eight 187 and 255, sixteen 357 and 261; x 16 keys four 87 and 104,
+//   eight 163 and 81.
+bool diff_few_supported(const DiffShape& s) {
+    if (s.R <= 0 || s.R > 8 || s.nk <= 0) return false;
+    if (s.dtype == LLSA_DTYPE_F32) return s.R <= 4 || s.nk >= 64;
+    const long long read = (s.R + 1LL) / 2 * s.slices * s.nk;
+    return s.R == 1 || (read <= (1 << 22) / s.d && diff_tc_fwd_split(s).splits > 1);
+}
 
-// Parts for one block per SM; a part has at least 128 keys, a few rounds of its warps.
+// Parts for one block per SM (more, shorter ones cost their beginnings and ends: 6 heads x 65,536
+// keys 57 us, 64 with twice as many); a part has at least 128 keys, a few rounds of its warps.
 DenseSplit diff_few_split(const DiffShape& s) {
     DenseSplit p;
-    long long n = kDenseSms / std::max(1, s.slices);
+    long long n = kDenseSms / std::max(1LL, s.slices * ((s.R + 1LL) / 2));
     n = std::max<long long>(1, std::min<long long>(n, s.nk / 128));
     p.chunk = (int)((s.nk + n - 1) / n);
     p.splits = (s.nk + p.chunk - 1) / p.chunk;

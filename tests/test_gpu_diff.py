@@ -468,6 +468,16 @@ def test_few_rows(h, kv, nq, d, dtype):
     both(make(2, h, kv, nq, 700, d, dtype, None, [700, 531], seed=13), dtype, causal=True, k_len=[700, 531])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [24, 64, 128])
+@pytest.mark.parametrize("h,kv,nq", [(2, 2, 1), (2, 1, 1), (6, 2, 1), (8, 2, 1), (2, 1, 4), (8, 1, 1), (1, 1, 9), (3, 1, 3)])
+def test_few_rows_over_many_keys(h, kv, nq, d, dtype):
+    """One to nine rows per key head over keys that are split: in pairs, the last of an odd
+    number by itself, a batch entry without keys and one whose last parts are empty."""
+    kl = [2100, 0, 1200]
+    both(make(3, h, kv, nq, 2100, d, dtype, None, kl, seed=14), dtype, causal=True, k_len=kl)
+
+
 @pytest.mark.parametrize("cfg,ql,kl,causal", [
     ((2, 8, 2, 333, 450, 128), [333, 200], [450, 77], True),   # stages of the rows' numbers that come round
     ((2, 8, 2, 333, 450, 64), [333, 200], [450, 77], True),
