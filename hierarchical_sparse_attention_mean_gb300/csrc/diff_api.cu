@@ -133,6 +133,7 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
     const DenseArgs& a = f.a.d;
     const int t = blockIdx.y;
     const bool one = t < 2;  // a matrix of d columns per map, or of 2 d for both
+    close_ahead();
     const int rows = t == 0 || t == 3 ? a.R : a.nk, cols = one ? a.d : 2 * a.d, per = cols / 8;
     const long long total = (long long)a.slices * (one ? 2 : 1) * rows * per, step = (long long)a.kv_heads * rows * a.d;
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < total; x += (long long)gridDim.x * kThreads) {
@@ -192,6 +193,7 @@ template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     const int which = blockIdx.y, rows = which == 0 ? a.R : a.nk;
+    close_ahead();
     const int per = which == 2 ? a.d / 2 : a.d / 4;
     const long long n = (which == 2 ? 1LL : 2LL) * a.slices * rows * per, step = (long long)a.kv_heads * rows * a.d;
     const float* from = which == 0 ? f.dq : which == 1 ? f.dk : f.dv;
@@ -238,6 +240,7 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp & 1, set = warp >> 1, dv = 2 * a.d;
     const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
     const float2* ml = diff_part_ml(a);
+    close_wait();
     __shared__ float4 sums[2][kJoinSets][64];
     float m = -INFINITY, l = 0.f;
     for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[diff_part(a, p, i, row)].x);
@@ -369,6 +372,7 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
         }
     }
     const long long all = (long long)a.slices * a.Rp;
+    close_ahead();
 #pragma unroll
     for (int u = 0; u < kRowsEach; u++) {
 #pragma unroll
@@ -400,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
         if constexpr (FOUR) f.d2[idx] = -D[1];
         else a.nl2[4 * all + idx] = lam;
     }
+    close_wait();  // FOUR: reads nothing that the kernel before it writes
 }
 
 // ------------------------------------------------------ gradient of lam --
@@ -446,16 +451,17 @@ __global__ void __launch_bounds__(kThreads) diff_lam_kernel(const __grid_constan
 }
 
 // dlam of a head from d2, `sets` sums of P_2 dP of every row: part p of `parts` of its
-// rows to part[h parts + p], or with one part to dlam itself.
+// rows to part[h parts + p], or with one part to dlam itself. fresh: the kernel before it writes d2.
 constexpr int kLamThreads = 1024;
 
 __global__ void __launch_bounds__(kLamThreads) diff_lam_rows_kernel(const __grid_constant__ DiffArgs f, float* part, int parts, int sets,
-                                                                 void* out) {
+                                                                 int fresh, void* out) {
     const DenseArgs& a = f.d;
     const int h = blockIdx.x / parts, p = blockIdx.x - h * parts;
     const int G = f.heads / a.kv_heads, g = h / G, batch = a.slices / a.kv_heads;
     const long long rows = (long long)batch * a.nq, first = rows * p / parts, last = rows * (p + 1) / parts;
     const long long all = (long long)a.slices * a.Rp;
+    if (fresh) close_wait();
     float sum = 0.f;
     for (long long row = first + threadIdx.x; row < last; row += kLamThreads) {
         const int b = (int)(row / a.nq), t = (int)(row - (long long)b * a.nq);
@@ -467,6 +473,7 @@ __global__ void __launch_bounds__(kLamThreads) diff_lam_rows_kernel(const __grid
     sum = warp_sum(sum);
     if ((threadIdx.x & 31) == 0) warps[threadIdx.x >> 5] = sum;
     __syncthreads();
+    close_wait();
     if (threadIdx.x != 0) return;
     for (int i = 1; i < kLamThreads / 32; i++) sum += warps[i];
     if (parts > 1) part[blockIdx.x] = sum;
@@ -551,9 +558,10 @@ size_t padded_rows(const DiffShape& s) { return up((size_t)s.slices * s.Rp * siz
 int row_parts(const DiffShape& s) { return (int)std::min<long long>(64, ((long long)s.batch * s.nq + 4095) / 4096); }
 size_t row_parts_bytes(const DiffShape& s) { return up((size_t)s.heads * row_parts(s) * sizeof(float)); }
 
-int launch_lam_rows(const DiffShape& s, const DiffArgs& a, int sets, float* part, void* dlam, cudaStream_t st) {
+int launch_lam_rows(const DiffShape& s, const DiffArgs& a, int sets, int fresh, float* part, void* dlam, cudaStream_t st) {
     const int parts = row_parts(s);
-    LLSA_LAUNCH("diff_lam_rows", st, diff_lam_rows_kernel<<<(unsigned)s.heads * parts, kLamThreads, 0, st>>>(a, part, parts, sets, dlam));
+    LLSA_LAUNCH("diff_lam_rows", st, launch_close(true, diff_lam_rows_kernel, dim3((unsigned)s.heads * parts), kLamThreads, 0, st, a, part, parts, sets,
+                                                    fresh, dlam));
     if (parts > 1) LLSA_LAUNCH("diff_lam_sum", st, diff_lam_sum_kernel<<<s.heads, 32, 0, st>>>(part, parts, dlam, a.lam_bf16));
     return LLSA_OK;
 }
@@ -636,7 +644,7 @@ int launch_planes_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* 
     float* part = take(row_parts_bytes(s));
     const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("diff_rows", st, (diff_rows_kernel<T, Q, true><<<(unsigned)blocks, kThreads, 0, st>>>(a)));
+    LLSA_LAUNCH("diff_rows", st, launch_close(true, diff_rows_kernel<T, Q, true>, dim3((unsigned)blocks), kThreads, 0, st, a));
     f.a = a;
     DenseArgs d = four_args(s, a, f);
     d.dq = gq;
@@ -651,7 +659,7 @@ int launch_planes_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* 
     f.dv_out = dv;
     const unsigned grid = blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4));
     LLSA_LAUNCH("diff_collapse", st, (diff_collapse_kernel<T, Q><<<dim3(grid, 3), kThreads, 0, st>>>(f)));
-    return launch_lam_rows(s, a, 1, part, dlam, st);
+    return launch_lam_rows(s, a, 1, 0, part, dlam, st);
 }
 
 template <typename T, typename Q>
@@ -753,8 +761,8 @@ int launch_diff_fwd(const DiffShape& s, DiffArgs a, void* ws, cudaStream_t st) {
     LLSA_TRY(path == Path::kFew ? launch_diff_few(s, a, st) : launch_diff_tc_fwd(s, a, st));
     if (p.splits > 1) {
         const unsigned blocks = (unsigned)((long long)s.slices * s.R);  // few: blocks would do without a split otherwise
-        if (bf16) LLSA_LAUNCH("diff_join", st, diff_join_kernel<__nv_bfloat16><<<blocks, kThreads, 0, st>>>(a));
-        else LLSA_LAUNCH("diff_join", st, diff_join_kernel<float><<<blocks, kThreads, 0, st>>>(a));
+        if (bf16) LLSA_LAUNCH("diff_join", st, launch_close(true, diff_join_kernel<__nv_bfloat16>, dim3(blocks), kThreads, 0, st, a));
+        else LLSA_LAUNCH("diff_join", st, launch_close(true, diff_join_kernel<float>, dim3(blocks), kThreads, 0, st, a));
     }
     return LLSA_OK;
 }
@@ -806,7 +814,7 @@ int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, 
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("diff_rows", st, (diff_rows_kernel<__nv_bfloat16, __nv_bfloat16, false><<<(unsigned)blocks, kThreads, 0, st>>>(a)));
     LLSA_TRY(launch_diff_tc_bwd(s, aq, ak, st));
-    LLSA_TRY(launch_lam_rows(s, a, 4 * t.q.splits, lam, dlam, st));
+    LLSA_TRY(launch_lam_rows(s, a, 4 * t.q.splits, 1, lam, dlam, st));
     DenseSums sums;
     if (t.q.splits > 1) sums.add(aq.d.part, dq, t.nq, t.q.splits);
     if (t.k.splits > 1) {

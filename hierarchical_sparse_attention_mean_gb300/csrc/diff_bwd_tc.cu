@@ -145,6 +145,8 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
     }
     if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
+    close_ahead();
+    close_wait();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
@@ -595,8 +597,8 @@ int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& a
     const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
     const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.d.splits;
     if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("diff_bwd_tc", st, diff_bwd_tc_kernel<<<(unsigned)(pq + pk), kThreads, smem, st>>>(mq, mg, mk, mv, zq, zk, zv, aq,
-                                                                                                   ak, (int)pk));
+    LLSA_LAUNCH("diff_bwd_tc", st, launch_close(true, diff_bwd_tc_kernel, dim3((unsigned)(pq + pk)), kThreads, smem, st, mq, mg, mk, mv, zq,
+                                                zk, zv, aq, ak, (int)pk));
     return LLSA_OK;
 }
 

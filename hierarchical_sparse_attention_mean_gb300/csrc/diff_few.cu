@@ -88,6 +88,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
         bar->abort_flag = 0;
         fence_mbar_init();
     }
+    close_ahead();
     __syncthreads();
     const int grp = lane / LANES, col = (lane % LANES) * 8;
     float acc[RR][2][16], m[RR][2], l[RR][2];

@@ -157,6 +157,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         prefetch_map(&mo2);
     }
     tc_fence_before();
+    close_ahead();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);

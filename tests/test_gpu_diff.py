@@ -258,6 +258,42 @@ def test_two_captured_graphs_at_once():
             assert torch.equal(got[n], want[n]), n
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("dtype,d,nq,nk,causal", [("bf16", 64, 130, 300, True), ("bf16", 64, 2, 9000, False), ("bf16", 128, 300, 300, False),
+                                                  ("fp32", 64, 130, 300, True), ("fp32", 64, 300, 40, False), ("fp32", 72, 5, 2000, False)])
+def test_calls_behind_each_other_share_workspaces(dtype, d, nq, nk, causal, captured):
+    """A call's kernels start while the one before them ends; so many calls of two inputs in
+    one set of workspaces and outputs, with copies of the outputs between them, give what
+    each gives by itself."""
+    xs = [{n: t.cuda() for n, t in make(2, 4, 2, nq, nk, d, dtype, seed=s).items()} for s in (21, 22)]
+    x = xs[0]
+    p = llsa.DiffParams.like(x["q"], x["k"], x["lam"], causal=causal)
+    ws = [torch.empty(max(16, llsa.diff_workspace_bytes(p, op)), dtype=torch.uint8, device="cuda") for op in (llsa.OP_DIFF_FWD, llsa.OP_DIFF_BWD)]
+    o, o2, lse = torch.empty_like(x["dout"]), torch.empty_like(x["dout"]), torch.empty(2, 8, nq, device="cuda")
+    grads = [torch.empty_like(x[n]) for n in ("q", "k", "v", "lam")]
+
+    def call(c):
+        llsa.llsa_diff_fwd(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, ws=ws[0])
+        llsa.llsa_diff_bwd(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], *grads, ws=ws[1])
+        return [t.clone() for t in (o, o2, lse, *grads)]
+
+    want = []
+    for c in xs:
+        want.append(call(c))
+        torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [call(xs[i & 1]) for i in range(12)]
+        graph.replay()
+    else:
+        got = [call(xs[i & 1]) for i in range(12)]
+    torch.cuda.synchronize()
+    for i, ts in enumerate(got):
+        for t, w in zip(ts, want[i & 1]):
+            assert torch.equal(t, w), i
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
 def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d):
     """With the copying warps switched off every consumer's first wait runs out: the
