@@ -29,6 +29,12 @@
 // the threads read tensor memory as fragments, 8 columns of 4 rows each, and need a
 // quarter as many of those numbers as with a row of 32 columns each.
 //
+// Bound by issue: exponentials, dS, and moves between tensor memory and registers take 2,925
+// clocks per tile pair for rows and 3,785 for keys, whatever runs on the tensor cores beside them.
+// 6 heads x 16,384 tokens: 2,188 us (1,320 TFLOP/s of the 28 d), the rows' numbers 27 before that.
+// Eight warps of 64 columns took 2,225; two teams of eight warps, a map each, 2,649; a ring of
+// single map tiles 2,387; S and dP loaded together 2,244.
+//
 // All sixteen elementwise warps take a tile together, a thread per row and quarter of the
 // columns. Shared memory holds one set of stationary tiles, and every piece of work gets a
 // block of its own.

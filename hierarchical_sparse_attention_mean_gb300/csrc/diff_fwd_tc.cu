@@ -17,7 +17,11 @@
 // and a key instead of 12 d.
 //
 // Bound by the tensor cores: 1,536 clocks per 128 x 128 pairs at 64 columns, where the
-// exponentials of both maps take 1,024.
+// exponentials of both maps take 1,024. 19 heads x 16,384 tokens of 64 columns: 2,383 us, 1,643
+// TFLOP/s, 84 % of what a large matrix product was measured at; of 128 columns 6,340 us, 1,648
+// TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 124 us, 384 pieces in three rounds of 152.
+// S and P of 64 keys in two places per map, so that a map's products run beside its own
+// exponentials, took 138: S of 64 keys reads shared memory 1.5 times as much as S of 128.
 //
 // One block per SM stays for the whole call and takes its share of the pieces: while
 // the softmax warps finish one, the others load for the next.
