@@ -258,6 +258,37 @@ def test_two_captured_graphs_at_once():
             assert torch.equal(got[n], want[n]), n
 
 
+@pytest.mark.parametrize("wide", [True, False])
+def test_captured_autograd_step(wide, monkeypatch):
+    """Positions, attention and gradients captured on leaves of the capture's own, replayed
+    on new inputs, while an eager graph of the same tensors lives."""
+    if not wide:
+        monkeypatch.setattr(llsa, "_WIDE_DIFF", 0)
+    x, y = (make(2, 4, 2, 256, 256, 64, "bf16", seed=s) for s in (22, 23))
+    c = {n: t.cuda() for n, t in x.items()}
+    rope = llsa.RopeGridParams.like(c["q"], c["k"], columns=(16, 24, 24), extent=(4, 8, 8))
+
+    def step(c):
+        leaves = [c[n].detach().requires_grad_() for n in ("q", "k", "v", "lam")]
+        o = llsa.diff_attention(*leaves, rope=rope)
+        return (o, *torch.autograd.grad(o, leaves, c["dout"]))
+
+    want = [[t.detach().clone() for t in step({n: t.cuda() for n, t in z.items()})] for z in (x, y)]
+    alive = llsa.diff_attention(*(c[n].detach().requires_grad_() for n in ("q", "k", "v", "lam")), rope=rope)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(c)
+    for z, w in zip((x, y), want):
+        for n in c:
+            c[n].copy_(z[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, w):
+            assert torch.equal(a, b)
+    assert torch.equal(alive, want[0][0])
+
+
 @pytest.mark.parametrize("captured", [False, True])
 @pytest.mark.parametrize("dtype,d,nq,nk,causal", [("bf16", 64, 130, 300, True), ("bf16", 64, 2, 9000, False), ("bf16", 128, 300, 300, False),
                                                   ("fp32", 64, 130, 300, True), ("fp32", 64, 300, 40, False), ("fp32", 72, 5, 2000, False)])
