@@ -31,6 +31,11 @@ struct DiffArgs {
     // Backward: nl2 of DenseArgs holds kDiffStats arrays [slices][Rp], -lse log2(e) and -D of
     // both maps and lam; d2 takes sums of P_2 dP of every row, [parts of dq][4][slices][Rp].
     float* d2;
+    // Of a small call, the last block of dq sums d2 to dlam: *lam_ticket counts the lam_pieces
+    // of them. NULL: a kernel after it does.
+    int* lam_ticket;
+    void* dlam;
+    int lam_pieces, lam_sets;
 };
 
 // Weight of the second map in the rows of head h.
@@ -57,6 +62,36 @@ __device__ __forceinline__ long long diff_part(const DenseArgs& a, int part, int
 __device__ __forceinline__ float2* diff_part_ml(const DenseArgs& a) {
     return reinterpret_cast<float2*>(a.part + (long long)a.splits * 2 * a.slices * a.R * 2 * a.d);
 }
+// Writes dlam where lam_ticket asks for it, by 512 threads of a block that has written its part of
+// d2. A warp per head, so every sum has a fixed order whichever block is the last. `last`:
+// shared memory of the block.
+__device__ __forceinline__ void diff_lam_last(const DiffArgs& f, int* last) {
+    if (!f.lam_ticket) return;
+    const DenseArgs& a = f.d;
+    __threadfence();
+    asm volatile("bar.sync 5, 512;" ::: "memory");
+    if (threadIdx.x == 0) *last = atomicAdd(f.lam_ticket, 1) == f.lam_pieces - 1;
+    asm volatile("bar.sync 5, 512;" ::: "memory");
+    if (!*last) return;
+    __threadfence();
+    const int lane = threadIdx.x & 31, G = f.heads / a.kv_heads, rows = a.slices / a.kv_heads * a.nq;
+    const long long all = (long long)a.slices * a.Rp;
+    for (int h = threadIdx.x >> 5; h < f.heads; h += 16) {
+        const int g = h / G;
+        float sum = 0.f;
+        for (int row = lane; row < rows; row += 32) {
+            const int b = row / a.nq, t = row - b * a.nq;
+            const float* from = f.d2 + ((long long)b * a.kv_heads + g) * a.Rp + (h - g * G) * a.nq + t;
+#pragma unroll 4
+            for (int i = 0; i < f.lam_sets; i++) sum += __ldcg(from + i * all);
+        }
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane != 0) continue;
+        if (f.lam_bf16) static_cast<__nv_bfloat16*>(f.dlam)[h] = __float2bfloat16_rn(-sum);
+        else static_cast<float*>(f.dlam)[h] = -sum;
+    }
+}
+
 inline size_t diff_part_bytes(const DiffShape& s, int splits) {
     return splits > 1 ? (size_t)splits * 2 * s.slices * s.R * (2 * s.d + 2) * sizeof(float) : 0;
 }

@@ -72,7 +72,7 @@ struct Bars {
     uint64_t x_full, y1_full[3], y1_empty[3], y2_full[2], y2_empty[2];
     uint64_t s_full[2], s_read, dp_full, ready[2], acc_full, drain;
     uint32_t tmem_slot;
-    int abort_flag;
+    int abort_flag, last;
 };
 
 // Matrix of map i of a slice in q, k, dq and dk.
@@ -554,6 +554,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
                 bulk_wait_read();
             }
         }
+        if constexpr (!KEYS) diff_lam_last(f, &bar->last);
     }
     tc_fence_before();
     __syncthreads();

@@ -60,7 +60,7 @@ struct Bars {
     uint64_t x_full, y1_full[3], y1_empty[3], y2_full[2], y2_empty[2], st_full[2], st_empty[2];
     uint64_t s_full[2], s_free, dp_full[2], ready[2], dp_free[2], acc_full, drain[2];
     uint32_t tmem_slot;
-    int abort_flag;
+    int abort_flag, last;
 };
 
 __device__ __forceinline__ int map_slice(const DenseArgs& a, int slice, int i) {
@@ -583,6 +583,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                 bulk_wait_read();
             }
         }
+        if (KIND == kDq && map == 1) diff_lam_last(f, &bar->last);
     }
     tc_fence_before();
     __syncthreads();
