@@ -42,6 +42,7 @@ struct DenseArgs {
     int splits, chunk;  // parts of the split axis, and how many of its elements each takes
     int pieces;         // pieces of work that the resident blocks share (tensor-core kernels)
     int whole;          // of them, those before the halved ones (forward)
+    int four;           // slices share planes of q, k and v, as diff_api.cu lays them out
     int slices, kv_heads, nq, nk, R, Rp, d, causal;
     float scale;
     int* status;
@@ -51,6 +52,22 @@ struct DenseArgs {
 struct DenseSpan {
     int lq, lk;
 };
+
+// Where the planes of a slice's q and k, and of its v, lie among those of all slices. Four calls
+// as one (diff_api.cu): slice ((2 b + i) 2 + j) kv + g has the q and k of (2 b + i) kv + g and the v of
+// (2 b + j) kv + g.
+__device__ __forceinline__ int dense_qk_slice(const DenseArgs& a, int slice) {
+    if (!a.four) return slice;
+    const int kv = a.kv_heads / 4, x = slice / kv;
+    return (x >> 1) * kv + slice - x * kv;
+}
+__device__ __forceinline__ int dense_v_slice(const DenseArgs& a, int slice) {
+    if (!a.four) return slice;
+    const int kv = a.kv_heads / 4, x = slice / kv;
+    return ((x >> 2) * 2 + (x & 1)) * kv + slice - x * kv;
+}
+// Slices of those planes.
+inline long long dense_plane_slices(const DenseArgs& a) { return a.four ? a.slices / 2 : a.slices; }
 
 // Valid query and key tokens of a slice's batch entry.
 __device__ __forceinline__ DenseSpan dense_span(const DenseArgs& a, int slice) {

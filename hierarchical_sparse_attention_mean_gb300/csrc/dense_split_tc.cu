@@ -150,13 +150,14 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         // ----------------------------------------------------------- copies
         if (warp <= kFwdWarps + 2 && lane == 0 && n > 0 && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
             const bool keys = warp == kFwdWarps + 1;
-            if (keys) load_planes<BT, D, PL>(sQ, &mq, r0, slice, smem_u32(&bar->q_full));
+            const int at = keys ? dense_qk_slice(a, slice) : dense_v_slice(a, slice);
+            if (keys) load_planes<BT, D, PL>(sQ, &mq, r0, at, smem_u32(&bar->q_full));
             int t = 0;
             for (; t < n; t++) {
                 const int st = keys ? t % C::KST : 0, use = keys ? t / C::KST : t;
                 const uint32_t full = smem_u32(keys ? &bar->k_full[st] : &bar->v_full);
                 if (use > 0 && !bar_wait(smem_u32(keys ? &bar->k_empty[st] : &bar->v_empty), (use - 1) & 1, abort_flag, a)) break;
-                load_planes<BN, D, PL>(keys ? sK + st * PL * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, slice, full);
+                load_planes<BN, D, PL>(keys ? sK + st * PL * C::PK : sV, keys ? &mk : &mv, j_first + t * BN, at, full);
             }
             // copies still in flight must land before the block exits
             if (keys) land(smem_u32(&bar->q_full), 0);
@@ -405,18 +406,21 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
             // ----------------------------------------------------------- copies
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const int k = warp - kBwdWarps - 1;
-                load_planes<BT, 64, 3>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, slice, smem_u32(&bar->x_full[k]));
+                // q and k; of v and dout, keys have v stationary
+                const int qk = dense_qk_slice(a, slice), v = dense_v_slice(a, slice);
+                const int at_x = k == 0 ? qk : KEYS ? v : slice, at_y = k == 0 ? qk : KEYS ? slice : v;
+                load_planes<BT, 64, 3>(sX + k * kTile, k == 0 ? &mx1 : &mx2, x0, at_x, smem_u32(&bar->x_full[k]));
                 const uint32_t full = smem_u32(&bar->y_full[k]);
                 int n = 0;
                 for (Items<KEYS> it = start; !it.done(); it.next(a)) {
                     if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
                     if (KEYS && k == 1) {  // one phase for the tile and the rows' numbers
                         const long long row = (long long)slice * a.Rp + it.pos;
-                        load_planes<BT, 64, 3>(sY + kTile, &my2, it.pos, slice, full, 2 * BT * 4);
+                        load_planes<BT, 64, 3>(sY + kTile, &my2, it.pos, at_y, full, 2 * BT * 4);
                         bulk_load(smem_u32(stats), a.nl2 + row, BT * 4, full);
                         bulk_load(smem_u32(stats + BT), a.nd + row, BT * 4, full);
                     } else {
-                        load_planes<BT, 64, 3>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, slice, full);
+                        load_planes<BT, 64, 3>(sY + k * kTile, k == 0 ? &my1 : &my2, it.pos, at_y, full);
                     }
                     n++;
                 }
@@ -656,9 +660,9 @@ static int launch_fwd(const DenseShape& s, const DenseArgs& a, const void* const
     using C = FwdCfg<D, PL>;
     static_assert(C::SMEM <= 227 * 1024 && sizeof(FwdBars) <= 1024, "shared memory budget");
     CUtensorMap mq, mk, mv;
-    LLSA_TRY(make_tmap_planes(&mq, p[0], PL, s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mk, p[1], PL, s.slices, s.nk, s.d, C::BN));
-    LLSA_TRY(make_tmap_planes(&mv, p[2], PL, s.slices, s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_planes(&mq, p[0], PL, dense_plane_slices(a), s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, p[1], PL, dense_plane_slices(a), s.nk, s.d, C::BN));
+    LLSA_TRY(make_tmap_planes(&mv, p[2], PL, dense_plane_slices(a), s.nk, s.d, C::BN));
     cudaFuncSetAttribute(dense_fwd_split_kernel<D, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
     if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
@@ -705,10 +709,10 @@ int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const Dense
                            cudaStream_t st) {
     if (s.d > 64) return launch_dense_split_wide_bwd(s, aq, ak, planes, st);
     CUtensorMap mq, mg, mk, mv;
-    LLSA_TRY(make_tmap_planes(&mq, planes[0], 3, s.slices, s.R, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mq, planes[0], 3, dense_plane_slices(aq), s.R, s.d, BT));
     LLSA_TRY(make_tmap_planes(&mg, planes[1], 3, s.slices, s.R, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mk, planes[2], 3, s.slices, s.nk, s.d, BT));
-    LLSA_TRY(make_tmap_planes(&mv, planes[3], 3, s.slices, s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mk, planes[2], 3, dense_plane_slices(aq), s.nk, s.d, BT));
+    LLSA_TRY(make_tmap_planes(&mv, planes[3], 3, dense_plane_slices(aq), s.nk, s.d, BT));
     static_assert(kBwdSmem <= 227 * 1024 && sizeof(BwdBars) <= 512, "shared memory budget");
     cudaFuncSetAttribute(dense_bwd_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
     const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;

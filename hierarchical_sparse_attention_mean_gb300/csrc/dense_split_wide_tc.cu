@@ -123,13 +123,14 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             // X1 and X2 in turn, the next one behind the first product of every item
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const uint32_t full = smem_u32(&bar->a_full);
-                load_planes<BT, D, PL>(sA, &mx1, x0, slice, full);
-                if (BOTH && WITH_DP) load_planes<BT, D, PL>(sA + C::X, &mx2, x0, slice, full);
+                const int qk = dense_qk_slice(a, slice), second = KEYS ? dense_v_slice(a, slice) : slice;  // of v or dout
+                load_planes<BT, D, PL>(sA, &mx1, x0, qk, full);
+                if (BOTH && WITH_DP) load_planes<BT, D, PL>(sA + C::X, &mx2, x0, second, full);
                 int n = 0;
                 if (WITH_DP && !BOTH)
                     for (List it = start; !it.done(); it.next(a)) {
                         if (!bar_wait(smem_u32(&bar->a_empty), n & 1, abort_flag, a)) break;
-                        load_planes<BT, D, PL>(sA, n % 2 == 0 ? &mx2 : &mx1, x0, slice, full);
+                        load_planes<BT, D, PL>(sA, n % 2 == 0 ? &mx2 : &mx1, x0, n % 2 == 0 ? second : qk, full);
                         n++;
                     }
                 land(full, n & 1);  // copies still in flight must land before the block exits
@@ -139,16 +140,17 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
             if (lane == 0 && any && !(a.test_flags & LLSA_TEST_NO_COPIES)) {
                 const int k = warp - kWarps - 2;
                 const uint32_t full = smem_u32(&bar->y_full[k]);
+                const int at = k == 0 ? dense_qk_slice(a, slice) : KEYS ? slice : dense_v_slice(a, slice);
                 int n = 0;
                 for (List it = start; !it.done(); it.next(a)) {
                     if (n > 0 && !bar_wait(smem_u32(&bar->y_empty[k]), (n - 1) & 1, abort_flag, a)) break;
                     if (KEYS && k == 0) {  // one phase for the tile and the rows' numbers
                         const long long row = (long long)slice * a.Rp + it.pos;
-                        load_planes<SN, D, PL>(sY, &my1, it.pos, slice, full, 2 * SN * 4);
+                        load_planes<SN, D, PL>(sY, &my1, it.pos, at, full, 2 * SN * 4);
                         bulk_load(smem_u32(stats), a.nl2 + row, SN * 4, full);
                         bulk_load(smem_u32(stats + SN), a.nd + row, SN * 4, full);
                     } else {
-                        load_planes<SN, D, PL>(sY + k * C::Y, k == 0 ? &my1 : &my2, it.pos, slice, full);
+                        load_planes<SN, D, PL>(sY + k * C::Y, k == 0 ? &my1 : &my2, it.pos, at, full);
                     }
                     n++;
                 }
@@ -379,10 +381,10 @@ int launch(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* 
     for (int i = 0; i < 2; i++) {
         Maps& m = i == 0 ? x : y;
         const int rows = i == 0 ? BT : SN;
-        LLSA_TRY(make_tmap_planes(&m.q, planes[0], PL, s.slices, s.R, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.q, planes[0], PL, dense_plane_slices(aq), s.R, s.d, rows));
         LLSA_TRY(make_tmap_planes(&m.g, planes[1], PL, s.slices, s.R, s.d, rows));
-        LLSA_TRY(make_tmap_planes(&m.k, planes[2], PL, s.slices, s.nk, s.d, rows));
-        LLSA_TRY(make_tmap_planes(&m.v, planes[3], PL, s.slices, s.nk, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.k, planes[2], PL, dense_plane_slices(aq), s.nk, s.d, rows));
+        LLSA_TRY(make_tmap_planes(&m.v, planes[3], PL, dense_plane_slices(aq), s.nk, s.d, rows));
     }
     static_assert(C::SMEM <= 227 * 1024 && sizeof(Bars) <= 512, "shared memory budget");
     cudaFuncSetAttribute(dense_bwd_wide_kernel<D, PL>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);

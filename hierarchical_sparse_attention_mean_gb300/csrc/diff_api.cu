@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_cons
 }
 
 // The four calls' operands at once as the three bf16 planes that the fp32 kernels read:
-// blockIdx.y q, k, v, dout. Eight values per thread, written to both calls that share them
-// (dout: as it is, and times -lam). Bound by HBM: 4 bytes in, 12 out.
+// blockIdx.y q, k, v, dout. Eight values per thread, for both calls that share them at once
+// (dense_qk_slice, dense_v_slice), and dout as it is and times -lam. Bound by HBM: 4 bytes in, 6 or 12 out.
 struct PlanesArgs {
     DiffArgs a;
     __nv_bfloat16* out[4];  // plane p of tensor t at out[t] + p * n[t]
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
     const bool one = t < 2;  // a matrix of d columns per map, or of 2 d for both
     close_ahead();
     const int rows = t == 0 || t == 3 ? a.R : a.nk, cols = one ? a.d : 2 * a.d, per = cols / 8;
-    const long long total = (long long)a.slices * (one ? 2 : 1) * rows * per, step = (long long)a.kv_heads * rows * a.d;
+    const long long total = (long long)a.slices * (one ? 2 : 1) * rows * per;
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < total; x += (long long)gridDim.x * kThreads) {
         const long long row = x / per;
         int c = (int)(x - row * per) * 8;
@@ -149,15 +149,16 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
             j = 1;
             c -= a.d;
         }
-        const long long matrix = one ? 2 * outer * a.kv_heads + g : (4 * outer + j) * a.kv_heads + g;
-        const long long at = (matrix * rows + r) * a.d + c;
-        put_planes(f.out[t] + at, f.n[t], y);
-        if (t == 3) {
-            const float lam = diff_lam(f.a, diff_head(f.a, (int)m, r));
-#pragma unroll
-            for (int e = 0; e < 8; e++) y[e] *= -lam;
+        if (t < 3) {
+            put_planes(f.out[t] + (one ? x * 8 : (((2 * outer + j) * a.kv_heads + g) * rows + r) * a.d + c), f.n[t], y);
+            continue;
         }
-        put_planes(f.out[t] + at + (one ? step : 2 * step), f.n[t], y);
+        const long long at = (((4 * outer + j) * a.kv_heads + g) * rows + r) * a.d + c;
+        put_planes(f.out[t] + at, f.n[t], y);
+        const float lam = diff_lam(f.a, diff_head(f.a, (int)m, r));
+#pragma unroll
+        for (int e = 0; e < 8; e++) y[e] *= -lam;
+        put_planes(f.out[t] + at + 2LL * a.kv_heads * rows * a.d, f.n[t], y);
     }
 }
 
@@ -551,8 +552,10 @@ size_t four_rows(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.
 size_t four_keys(const DiffShape& s) { return up((size_t)4 * s.slices * s.nk * s.d * sizeof(float)); }
 size_t four_lse(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * sizeof(float)); }
 
-size_t plane_rows(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.d * 6); }
-size_t plane_keys(const DiffShape& s) { return up((size_t)4 * s.slices * s.nk * s.d * 6); }
+// Planes of q (two calls share them) and of dout, and of k or v.
+size_t plane_q(const DiffShape& s) { return up((size_t)2 * s.slices * s.R * s.d * 6); }
+size_t plane_dout(const DiffShape& s) { return up((size_t)4 * s.slices * s.R * s.d * 6); }
+size_t plane_keys(const DiffShape& s) { return up((size_t)2 * s.slices * s.nk * s.d * 6); }
 size_t padded_rows(const DiffShape& s) { return up((size_t)s.slices * s.Rp * sizeof(float)); }
 
 // One block per head up to 4,096 of its rows: a second launch costs more than a long loop.
@@ -569,16 +572,17 @@ int launch_lam_rows(const DiffShape& s, const DiffArgs& a, int sets, int fresh, 
 
 size_t four_workspace(const DiffShape& s, bool backward) {
     if (!backward && dense_fwd_on_planes(s.four))
-        return plane_rows(s) + 2 * plane_keys(s) + four_rows(s) + four_lse(s) + up(dense_fwd_parts(s.four));
+        return plane_q(s) + 2 * plane_keys(s) + four_rows(s) + four_lse(s) + up(dense_fwd_parts(s.four));
     if (backward && dense_bwd_on_planes(s.four))
-        return 2 * plane_rows(s) + 2 * plane_keys(s) + four_rows(s) + 2 * four_keys(s) + 9 * padded_rows(s) + row_parts_bytes(s) +
+        return plane_q(s) + plane_dout(s) + 2 * plane_keys(s) + four_rows(s) + 2 * four_keys(s) + 9 * padded_rows(s) + row_parts_bytes(s) +
                up(dense_bwd_parts(s.four));
     return backward ? 4 * four_rows(s) + 4 * four_keys(s) + four_lse(s) + up(dense_bwd_workspace(s.four))
                     : 2 * four_rows(s) + 2 * four_keys(s) + four_lse(s) + up(dense_fwd_workspace(s.four));
 }
 
-DenseArgs four_args(const DiffShape& s, const DiffArgs& a, const FourArgs& f) {
+DenseArgs four_args(const DiffShape& s, const DiffArgs& a, const FourArgs& f, bool planes = false) {
     DenseArgs d = a.d;
+    d.four = planes;
     d.slices = s.four.slices;
     d.kv_heads = s.four.kv_heads;
     d.q = f.q;
@@ -595,15 +599,14 @@ int launch_planes(const DiffShape& s, const DiffArgs& a, bool backward, char*& a
     PlanesArgs f;
     memset(&f, 0, sizeof(f));
     f.a = a;
-    const long long nq = 4LL * s.slices * s.R * s.d, nk = 4LL * s.slices * s.nk * s.d;
+    const long long nq = 2LL * s.slices * s.R * s.d, nk = 2LL * s.slices * s.nk * s.d;
     for (int t = 0; t < (backward ? 4 : 3); t++) {
-        const bool rows = t == 0 || t == 3;
         f.out[t] = reinterpret_cast<__nv_bfloat16*>(at);
-        f.n[t] = rows ? nq : nk;
+        f.n[t] = t == 0 ? nq : t == 3 ? 2 * nq : nk;
         planes[t] = at;
-        at += rows ? plane_rows(s) : plane_keys(s);
+        at += t == 0 ? plane_q(s) : t == 3 ? plane_dout(s) : plane_keys(s);
     }
-    const dim3 grid((unsigned)std::min<long long>((std::max(nq, nk) / 16 + kThreads - 1) / kThreads, 8LL * kDenseSms), backward ? 4 : 3);
+    const dim3 grid((unsigned)std::min<long long>((std::max(nq, nk) / 8 + kThreads - 1) / kThreads, 8LL * kDenseSms), backward ? 4 : 3);
     LLSA_LAUNCH("diff_planes", st, (diff_planes_kernel<T, Q><<<grid, kThreads, 0, st>>>(f)));
     return LLSA_OK;
 }
@@ -620,7 +623,7 @@ int launch_planes_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStrea
     at += four_rows(s);
     f.lse = reinterpret_cast<float*>(at);
     at += four_lse(s);
-    DenseArgs d = four_args(s, a, f);
+    DenseArgs d = four_args(s, a, f, true);
     d.o_out = f.o;
     d.lse_out = f.lse;
     LLSA_TRY(launch_dense_fwd_planes(s.four, d, planes, at, st));
@@ -647,7 +650,7 @@ int launch_planes_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* 
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("diff_rows", st, launch_close(true, diff_rows_kernel<T, Q, true>, dim3((unsigned)blocks), kThreads, 0, st, a));
     f.a = a;
-    DenseArgs d = four_args(s, a, f);
+    DenseArgs d = four_args(s, a, f, true);
     d.dq = gq;
     d.dk = gk;
     d.dv = gv;
