@@ -137,6 +137,8 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     }
     if (warp == kFwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
+    close_wait();
+    close_ahead();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
@@ -395,6 +397,8 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
     }
     if (warp == kBwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
+    close_wait();
+    close_ahead();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
@@ -667,7 +671,7 @@ static int launch_fwd(const DenseShape& s, const DenseArgs& a, const void* const
     const long long pieces = (long long)((s.R + BT - 1) / BT) * s.slices * a.splits;
     if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("dense_fwd_split", st,
-                dense_fwd_split_kernel<D, PL><<<(unsigned)pieces, kFwdThreads, C::SMEM, st>>>(mq, mk, mv, a));
+                launch_close(a.four, dense_fwd_split_kernel<D, PL>, dim3((unsigned)pieces), kFwdThreads, C::SMEM, st, mq, mk, mv, a));
     return LLSA_OK;
 }
 
@@ -719,7 +723,8 @@ int launch_dense_split_bwd(const DenseShape& s, const DenseArgs& aq, const Dense
     const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.splits;
     if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("dense_bwd_split", st,
-                dense_bwd_split_kernel<<<(unsigned)(pq + pk), kBwdThreads, kBwdSmem, st>>>(mq, mg, mk, mv, aq, ak, (int)pk));
+                launch_close(aq.four, dense_bwd_split_kernel, dim3((unsigned)(pq + pk)), kBwdThreads, kBwdSmem, st, mq, mg, mk, mv, aq, ak,
+                             (int)pk));
     return LLSA_OK;
 }
 

@@ -111,6 +111,8 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
     }
     if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
+    close_wait();
+    close_ahead();
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
@@ -391,8 +393,8 @@ int launch(const DenseShape& s, const DenseArgs& aq, const DenseArgs& ak, void* 
     const long long pq = (long long)((s.R + BT - 1) / BT) * s.slices * aq.splits;
     const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.splits;
     if (pq + 2 * pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("dense_bwd_split", st, dense_bwd_wide_kernel<D, PL><<<(unsigned)(pq + 2 * pk), kThreads, C::SMEM, st>>>(
-                                           x, y, aq, ak, (int)pk));
+    LLSA_LAUNCH("dense_bwd_split", st, launch_close(aq.four, dense_bwd_wide_kernel<D, PL>, dim3((unsigned)(pq + 2 * pk)), kThreads,
+                                                    C::SMEM, st, x, y, aq, ak, (int)pk));
     return LLSA_OK;
 }
 

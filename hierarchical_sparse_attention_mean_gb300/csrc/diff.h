@@ -96,28 +96,6 @@ inline size_t diff_part_bytes(const DiffShape& s, int splits) {
     return splits > 1 ? (size_t)splits * 2 * s.slices * s.R * (2 * s.d + 2) * sizeof(float) : 0;
 }
 
-// A call's kernels follow each other closely: a kernel launched by launch_close may be set up while
-// the one before it still runs (from close_ahead there on), and reads what that one writes
-// behind close_wait. Every kernel so launched waits, if only at its end, so that
-// whatever comes after it comes after all of the call.
-__device__ __forceinline__ void close_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void close_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-template <typename... P, typename... A>
-void launch_close(bool close, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = close ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
 // diff_few.cu: forward of a few rows per value head.
 bool diff_few_supported(const DiffShape& s);
 DenseSplit diff_few_split(const DiffShape& s);

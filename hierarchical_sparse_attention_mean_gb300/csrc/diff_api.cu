@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
 template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
+    close_wait();
     const int per = a.d / 2;  // vectors of 4 of a row of 2 d
     const long long n = (long long)a.slices * a.R * per, step = (long long)a.kv_heads * a.R;
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
@@ -194,7 +195,8 @@ template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_collapse_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     const int which = blockIdx.y, rows = which == 0 ? a.R : a.nk;
-    close_ahead();
+    close_wait();
+    close_ahead();  // what does not wait behind this may read all but what this writes
     const int per = which == 2 ? a.d / 2 : a.d / 4;
     const long long n = (which == 2 ? 1LL : 2LL) * a.slices * rows * per, step = (long long)a.kv_heads * rows * a.d;
     const float* from = which == 0 ? f.dq : which == 1 ? f.dk : f.dv;
@@ -628,7 +630,7 @@ int launch_planes_fwd(const DiffShape& s, const DiffArgs& a, void* ws, cudaStrea
     d.lse_out = f.lse;
     LLSA_TRY(launch_dense_fwd_planes(s.four, d, planes, at, st));
     LLSA_LAUNCH("diff_combine", st,
-                (diff_combine_kernel<T, Q><<<blocks_for((long long)s.slices * s.R * (s.d / 2)), kThreads, 0, st>>>(f)));
+                launch_close(true, diff_combine_kernel<T, Q>, dim3(blocks_for((long long)s.slices * s.R * (s.d / 2))), kThreads, 0, st, f));
     return LLSA_OK;
 }
 
@@ -662,7 +664,7 @@ int launch_planes_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* 
     f.dk_out = dk;
     f.dv_out = dv;
     const unsigned grid = blocks_for((long long)s.four.slices * std::max(s.R, s.nk) * (s.d / 4));
-    LLSA_LAUNCH("diff_collapse", st, (diff_collapse_kernel<T, Q><<<dim3(grid, 3), kThreads, 0, st>>>(f)));
+    LLSA_LAUNCH("diff_collapse", st, launch_close(true, diff_collapse_kernel<T, Q>, dim3(grid, 3), kThreads, 0, st, f));
     return launch_lam_rows(s, a, 1, 0, part, dlam, st);
 }
 
