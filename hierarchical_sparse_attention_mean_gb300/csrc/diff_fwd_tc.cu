@@ -17,11 +17,13 @@
 // and a key instead of 12 d.
 //
 // Bound by the tensor cores: 1,536 clocks per 128 x 128 pairs at 64 columns, where the
-// exponentials of both maps take 1,024. 19 heads x 16,384 tokens of 64 columns: 2,383 us, 1,643
-// TFLOP/s, 84 % of what a large matrix product was measured at; of 128 columns 6,340 us, 1,648
+// exponentials of both maps take 1,024. 19 heads x 16,384 tokens of 64 columns: 2,359 us, 1,660
+// TFLOP/s, 85 % of what a large matrix product was measured at; of 128 columns 6,340 us, 1,648
 // TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 124 us, 384 pieces in three rounds of 152.
 // S and P of 64 keys in two places per map, so that a map's products run beside its own
 // exponentials, took 138: S of 64 keys reads shared memory 1.5 times as much as S of 128.
+// A piece's end behind the first tile of the next, with a place for the output rows taken from
+// the stages of K, took 134.
 //
 // One block per SM stays for the whole call and takes its share of the pieces: while
 // the softmax warps finish one, the others load for the next.
@@ -57,7 +59,7 @@ struct Cfg {
 struct Bars {
     float l[2][BM];  // the sums of both maps' rows, at the end of a piece
     uint64_t k_full[6], k_empty[6], v_full[2], v_empty[2], q_full[2], q_free[2];
-    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2], drain;
+    uint64_t s_full[2], p_full[2][2], o_done[2], o_free[2], l_ready, drain;
     PieceRing pieces;
     uint32_t tmem_slot;
     int abort_flag;
@@ -147,6 +149,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             mbar_init(smem_u32(&bar->o_done[i]), 1);
             mbar_init(smem_u32(&bar->o_free[i]), 8);
         }
+        mbar_init(smem_u32(&bar->l_ready), 8);
         mbar_init(smem_u32(&bar->drain), 1);
         piece_ring_init(&bar->pieces, 10);  // softmax warps, the issuer, the copies of V
         bar->abort_flag = 0;
@@ -433,6 +436,11 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 }
                 continue;
             }
+            const float lam = here ? diff_lam(f, diff_head(f, pc.slice, r)) : 0.f;  // comes while O is being finished
+            if (a.splits == 1) {
+                bar->l[w][lr] = l;
+                warp_arrive(smem_u32(&bar->l_ready), lane);
+            }
             bar_wait(smem_u32(&bar->o_done[w]), (u - 1) & 1, abort_flag, a);
             if (a.splits > 1) {
                 tc_fence_after();
@@ -457,13 +465,11 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             }
             // the sums of both maps, and both O; the query tiles have been used up: their place
             // takes the output rows, 32 rows and 64 columns per warp
-            bar->l[w][lr] = l;
             bar_wait(smem_u32(&bar->o_done[w ^ 1]), (u - 1) & 1, abort_flag, a);
             tc_fence_after();
-            named_barrier(1, 256);
+            bar_wait(smem_u32(&bar->l_ready), v & 1, abort_flag, a);
             const float la = bar->l[0][lr], lb = bar->l[1][lr];
             const float inv1 = la == 0.f ? 0.f : 1.f / la, inv2 = lb == 0.f ? 0.f : 1.f / lb;
-            const float lam = here ? diff_lam(f, diff_head(f, pc.slice, r)) : 0.f;
             unsigned char* out = sQ + 2 * (v % C::NQ) * C::TILE + w * C::REGION;
             unsigned char* out2 = D == 64 ? out : out + C::TILE;
             uint32_t kept[32];  // o2's row, packed
