@@ -318,9 +318,12 @@ def _diff_native(batch, heads, nq, nk, d, kv_heads, causal, dtype, lam_dtype, sc
                     1 if qk_dtype != dtype else 0, 1 if causal else 0, scale)
     kv = kv_heads or heads
     types = {"bf16": torch.bfloat16, "fp32": torch.float32}
-    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {}, "_lam": types[lam_dtype], "_qk": types[qk_dtype],
-            "_shapes": ((batch, 2 * heads, nq, d), (batch, 2 * kv, nk, d), (batch, kv, nk, 2 * d), (batch, heads, nq, 2 * d),
-                        (batch, 2 * heads, nq))}
+    shapes = ((batch, 2 * heads, nq, d), (batch, 2 * kv, nk, d), (batch, kv, nk, 2 * d), (batch, heads, nq, 2 * d), (batch, 2 * heads, nq))
+    (sq, sk, sv, so, sl), td, qk = shapes, types[dtype], types[qk_dtype]
+    given = (("q", qk, sq), ("k", qk, sk), ("v", td, sv), ("lam", types[lam_dtype], (heads,)))
+    o, o2, lse = ("o", td, so), ("o2", qk, so), ("lse", torch.float32, sl)
+    return {"_c": c, "_ref": ctypes.byref(c), "_ws": {}, "_shapes": shapes, "_fwd": (*given, o, lse, o2),
+            "_bwd": (*given, o, o2, lse, ("dout", td, so), *(("d" + name, t, x) for name, t, x in given))}
 
 
 @functools.lru_cache(maxsize=256)
@@ -653,6 +656,19 @@ def _like(t, name, shape, dtype, device):
     return ptr
 
 
+def _all_like(tensors, want, device):
+    """_like of each tensor and its (name, type, shape) in `want`, in one loop: small calls wait for the host."""
+    try:
+        for t, (_, dtype, shape) in zip(tensors, want):
+            if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+                break
+        else:
+            return [t.data_ptr() for t in tensors]
+    except AttributeError:  # no tensor
+        pass
+    return [_like(t, name, shape, dtype, device) for t, (name, dtype, shape) in zip(tensors, want)]
+
+
 _HERE = contextlib.nullcontext()
 
 
@@ -720,27 +736,22 @@ def diff_workspace_bytes(p: DiffParams, op: int) -> int:
 def llsa_diff_fwd(p: DiffParams, q, k, v, lam, o, o2, lse, q_len=None, k_len=None, ws=None, stream=None):
     """Differential attention: o, o2 (None: not kept) and lse of q over k, v (llsa_diff_fwd of include/llsa.h)."""
     with _on(q, "q"):
-        td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        dev = q.get_device()
+        q, k, v, lam, o, lse, *kept = _all_like((q, k, v, lam, o, lse) if o2 is None else (q, k, v, lam, o, lse, o2), p._fwd, dev)
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws_on(ws, dev)
-        _check(_load().llsa_diff_fwd(p._ref, _like(q, "q", sq, p._qk, dev), _like(k, "k", sk, p._qk, dev), _like(v, "v", sv, td, dev),
-                                     _like(lam, "lam", (p.heads,), p._lam, dev), ql, kl, _like(o, "o", so, td, dev),
-                                     None if o2 is None else _like(o2, "o2", so, p._qk, dev),
-                                     _like(lse, "lse", sl, torch.float32, dev), w, wb, _stream(stream)), "llsa_diff_fwd")
+        _check(_load().llsa_diff_fwd(p._ref, q, k, v, lam, ql, kl, o, kept[0] if kept else None, lse, w, wb, _stream(stream)),
+               "llsa_diff_fwd")
 
 
 def llsa_diff_bwd(p: DiffParams, q, k, v, lam, o, o2, lse, dout, dq, dk, dv, dlam, q_len=None, k_len=None, ws=None, stream=None):
     """Gradients of differential attention (llsa_diff_bwd of include/llsa.h)."""
     with _on(q, "q"):
-        td, dev, (sq, sk, sv, so, sl) = _tok_dtype(p), q.get_device(), p.shapes()
+        dev = q.get_device()
+        at = _all_like((q, k, v, lam, o, o2, lse, dout, dq, dk, dv, dlam), p._bwd, dev)
         ql, kl = (None, None) if q_len is None and k_len is None else _lens(p, q_len, k_len, dev)
         w, wb = _ws_on(ws, dev)
-        _check(_load().llsa_diff_bwd(p._ref, _like(q, "q", sq, p._qk, dev), _like(k, "k", sk, p._qk, dev), _like(v, "v", sv, td, dev),
-                                     _like(lam, "lam", (p.heads,), p._lam, dev), _like(o, "o", so, td, dev),
-                                     _like(o2, "o2", so, p._qk, dev), _like(lse, "lse", sl, torch.float32, dev),
-                                     _like(dout, "dout", so, td, dev), ql, kl, _like(dq, "dq", sq, p._qk, dev),
-                                     _like(dk, "dk", sk, p._qk, dev), _like(dv, "dv", sv, td, dev),
-                                     _like(dlam, "dlam", (p.heads,), p._lam, dev), w, wb, _stream(stream)), "llsa_diff_bwd")
+        _check(_load().llsa_diff_bwd(p._ref, *at[:8], ql, kl, *at[8:], w, wb, _stream(stream)), "llsa_diff_bwd")
 
 
 def _strided(t, name, shape, dtype, device):
