@@ -23,28 +23,6 @@ constexpr int kDenseRowPad = 128;  // rows of a slice in the per-row arrays: a m
 constexpr int kDenseMaxExtent = 1 << 30;  // rows of a slice, keys of a slice
 constexpr int kDenseSms = 152;  // splits, and so the workspace, go by the GB300's SMs
 
-// A call's kernels follow each other closely: a kernel launched by launch_close may be set up while
-// the one before it still runs (from close_ahead there on), and reads what that one writes
-// behind close_wait. Every kernel so launched waits, if only at its end, so that
-// whatever comes after it comes after all of the call.
-__device__ __forceinline__ void close_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void close_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
-template <typename... P, typename... A>
-void launch_close(bool close, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = close ? 1 : 0;
-    cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
-}
-
 struct DenseShape {
     int batch, heads, kv_heads, G, nq, nk, d, dtype, causal;
     int slices;   // batch * kv_heads
@@ -98,12 +76,12 @@ __device__ __forceinline__ DenseSpan dense_span(const DenseArgs& a, int slice) {
     s.lq = a.nq;
     s.lk = a.nk;
     if (a.q_len) {
-        const int v = __ldg(a.q_len + b);
+        const int v = a.q_len[b];
         s.lq = min(max(v, 0), a.nq);
         if (s.lq != v) set_status(a.status, LLSA_ERR_BAD_INDEX);
     }
     if (a.k_len) {
-        const int v = __ldg(a.k_len + b);
+        const int v = a.k_len[b];
         s.lk = min(max(v, 0), a.nk);
         if (s.lk != v) set_status(a.status, LLSA_ERR_BAD_INDEX);
     }

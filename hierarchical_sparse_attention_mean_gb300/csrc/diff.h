@@ -38,6 +38,28 @@ struct DiffArgs {
     int lam_pieces, lam_sets;
 };
 
+// Eight values as fp32, from memory that a kernel before this one may have written while this one
+// was set up (load8 reads through the cache for what stays as it is).
+__device__ __forceinline__ void diff_load8(const __nv_bfloat16* p, float* f) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        f[2 * i] = __uint_as_float(u[i] << 16);
+        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void diff_load8(const float* p, float* f) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p + i);
+        f[i] = x.x;
+        f[i + 1] = x.y;
+        f[i + 2] = x.z;
+        f[i + 3] = x.w;
+    }
+}
+
 // Weight of the second map in the rows of head h.
 __device__ __forceinline__ float diff_lam(const DiffArgs& a, int h) {
     return a.lam_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.lam)[h]) : static_cast<const float*>(a.lam)[h];

@@ -27,13 +27,13 @@ size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 template <typename T>
 __device__ __forceinline__ void load4f(const T* p, float* f) {
     if constexpr (sizeof(T) == 2) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
         f[0] = __uint_as_float(u.x << 16);
         f[1] = __uint_as_float(u.x & 0xffff0000u);
         f[2] = __uint_as_float(u.y << 16);
         f[3] = __uint_as_float(u.y & 0xffff0000u);
     } else {
-        const float4 u = __ldg(reinterpret_cast<const float4*>(p));
+        const float4 u = *reinterpret_cast<const float4*>(p);
         f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
     }
 }
@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
     const DenseArgs& a = f.a.d;
     const int t = blockIdx.y;
     const bool one = t < 2;  // a matrix of d columns per map, or of 2 d for both
-    close_ahead();
+    close_wait();
+    close_ahead();  // behind the wait: the rows' numbers are worked out beside this, from what was there before
     const int rows = t == 0 || t == 3 ? a.R : a.nk, cols = one ? a.d : 2 * a.d, per = cols / 8;
     const long long total = (long long)a.slices * (one ? 2 : 1) * rows * per;
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < total; x += (long long)gridDim.x * kThreads) {
@@ -142,8 +143,8 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
         const long long m = row / rows, outer = m / a.kv_heads;  // outer: 2 b + i, or b
         const int r = (int)(row - m * rows), g = (int)(m - outer * a.kv_heads);
         float y[8];
-        if (one) load8(static_cast<const Q*>(t == 0 ? a.q : a.k) + x * 8, y);
-        else load8(static_cast<const T*>(t == 2 ? a.v : a.dout) + x * 8, y);
+        if (one) diff_load8(static_cast<const Q*>(t == 0 ? a.q : a.k) + x * 8, y);
+        else diff_load8(static_cast<const T*>(t == 2 ? a.v : a.dout) + x * 8, y);
         int j = 0;
         if (!one && c >= a.d) {
             j = 1;
@@ -167,6 +168,7 @@ template <typename T, typename Q>
 __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_constant__ FourArgs f) {
     const DenseArgs& a = f.a.d;
     close_wait();
+    close_ahead();
     const int per = a.d / 2;  // vectors of 4 of a row of 2 d
     const long long n = (long long)a.slices * a.R * per, step = (long long)a.kv_heads * a.R;
     for (long long x = (long long)blockIdx.x * kThreads + threadIdx.x; x < n; x += (long long)gridDim.x * kThreads) {
@@ -244,6 +246,7 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
     const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
     const float2* ml = diff_part_ml(a);
     close_wait();
+    close_ahead();
     __shared__ float4 sums[2][kJoinSets][64];
     float m = -INFINITY, l = 0.f;
     for (int p = lane; p < a.splits; p += 32) m = fmaxf(m, ml[diff_part(a, p, i, row)].x);
@@ -334,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
     const DenseArgs& a = f.d;
     const unsigned per = (unsigned)a.Rp / kDenseRowPad, slice = blockIdx.x / per;
     const int r0 = (int)(blockIdx.x - slice * per) * kDenseRowPad + (threadIdx.x >> 3), part = threadIdx.x & 7;
+    if (!FOUR) close_wait();
     const DenseSpan sp = dense_span(a, (int)slice);
     const int dv = 2 * a.d;
     float one[kRowsEach], two[kRowsEach];
@@ -357,9 +361,9 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
             y[u] = uint4{};
             if (on[u]) {
                 const long long to = at + (long long)u * (kThreads / 8) * dv;
-                g[u] = __ldg(reinterpret_cast<const VT*>(static_cast<const T*>(a.dout) + to));
-                x[u] = __ldg(reinterpret_cast<const VT*>(static_cast<const T*>(a.o) + to));
-                y[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const Q*>(f.o2) + to));
+                g[u] = *reinterpret_cast<const VT*>(static_cast<const T*>(a.dout) + to);
+                x[u] = *reinterpret_cast<const VT*>(static_cast<const T*>(a.o) + to);
+                y[u] = *reinterpret_cast<const uint4*>(static_cast<const Q*>(f.o2) + to);
             }
         }
 #pragma unroll
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 4) diff_rows_kernel(const __grid_con
         const float D[2] = {on[u] ? -fmaf(lam, two[u], one[u]) : 0.f, on[u] ? -two[u] : 0.f};
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            const float lse = on[u] ? __ldg(a.lse + diff_row(f, (int)slice, i, r)) : -INFINITY;
+            const float lse = on[u] ? a.lse[diff_row(f, (int)slice, i, r)] : -INFINITY;
             const float l2 = lse == -INFINITY ? -INFINITY : -lse * kDenseLog2e;
             if constexpr (FOUR) {
                 // both halves' calls of map i; only the sum of their D counts, weighed as their dout is
@@ -466,6 +470,7 @@ __global__ void __launch_bounds__(kLamThreads) diff_lam_rows_kernel(const __grid
     const long long rows = (long long)batch * a.nq, first = rows * p / parts, last = rows * (p + 1) / parts;
     const long long all = (long long)a.slices * a.Rp;
     if (fresh) close_wait();
+    close_ahead();
     float sum = 0.f;
     for (long long row = first + threadIdx.x; row < last; row += kLamThreads) {
         const int b = (int)(row / a.nq), t = (int)(row - (long long)b * a.nq);
@@ -609,7 +614,7 @@ int launch_planes(const DiffShape& s, const DiffArgs& a, bool backward, char*& a
         at += t == 0 ? plane_q(s) : t == 3 ? plane_dout(s) : plane_keys(s);
     }
     const dim3 grid((unsigned)std::min<long long>((std::max(nq, nk) / 8 + kThreads - 1) / kThreads, 8LL * kDenseSms), backward ? 4 : 3);
-    LLSA_LAUNCH("diff_planes", st, (diff_planes_kernel<T, Q><<<grid, kThreads, 0, st>>>(f)));
+    LLSA_LAUNCH("diff_planes", st, launch_close(close_first(st), diff_planes_kernel<T, Q>, grid, kThreads, 0, st, f));
     return LLSA_OK;
 }
 
@@ -828,7 +833,8 @@ int launch_tc_bwd(const DiffShape& s, DiffArgs a, void* dq, void* dk, void* dv, 
     ak.d.part = take(t.dkv);
     const long long blocks = (long long)s.slices * (s.Rp / kDenseRowPad);
     if (blocks > 0x7fffffffLL) return LLSA_ERR_UNSUPPORTED;
-    LLSA_LAUNCH("diff_rows", st, (diff_rows_kernel<__nv_bfloat16, __nv_bfloat16, false><<<(unsigned)blocks, kThreads, 0, st>>>(a)));
+    LLSA_LAUNCH("diff_rows", st, launch_close(close_first(st), diff_rows_kernel<__nv_bfloat16, __nv_bfloat16, false>, dim3((unsigned)blocks), kThreads, 0, st,
+                                           a));
     LLSA_TRY(launch_diff_tc_bwd(s, aq, ak, st));
     if (!last) LLSA_TRY(launch_lam_rows(s, a, sets, 1, lam, dlam, st));
     DenseSums sums;

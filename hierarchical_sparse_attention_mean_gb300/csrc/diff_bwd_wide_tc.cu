@@ -402,7 +402,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
             for (int c = 0; c < 16; c += 4) {
                 uint64_t l = pack2(lam, lam);
                 if (!one_head) {
-                    const float2 u = __ldg(reinterpret_cast<const float2*>(lams + pos + w * kCols + fc + 2 * c));
+                    const float2 u = *reinterpret_cast<const float2*>(lams + pos + w * kCols + fc + 2 * c);
                     l = pack2(u.x, u.y);
                 }
 #pragma unroll

@@ -36,27 +36,6 @@ struct FewBars {
     int abort_flag;
 };
 
-// Eight values from shared memory as fp32.
-__device__ __forceinline__ void get8(const __nv_bfloat16* p, float* f) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        f[2 * i] = __uint_as_float(u[i] << 16);
-        f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void get8(const float* p, float* f) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p + i);
-        f[i] = x.x;
-        f[i + 1] = x.y;
-        f[i + 2] = x.z;
-        f[i + 3] = x.w;
-    }
-}
-
 template <typename T, int RR, int LANES>
 __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(const __grid_constant__ DiffArgs f) {
     const DenseArgs& a = f.d;
@@ -68,6 +47,8 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
     FewBars* bar = reinterpret_cast<FewBars*>(sm + kStages * kStage);
     volatile int* abort_flag = &bar->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    close_wait();
+    close_ahead();
     const int slice = blockIdx.x / a.splits, part = blockIdx.x - slice * a.splits;
     const DenseSpan sp = dense_span(a, slice);
     const int dv = 2 * a.d, r0 = blockIdx.y * RR;
@@ -88,7 +69,6 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
         bar->abort_flag = 0;
         fence_mbar_init();
     }
-    close_ahead();
     __syncthreads();
     const int grp = lane / LANES, col = (lane % LANES) * 8;
     float acc[RR][2][16], m[RR][2], l[RR][2];
@@ -127,7 +107,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
 #pragma unroll
                 for (int c = 0; c < 8; c++) q[r][i][c] = acc[r][i][c] = acc[r][i][c + 8] = 0.f;
                 if (on && kend[r] > 0) {
-                    load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r0 + r) * a.d + col, q[r][i]);
+                    diff_load8(static_cast<const T*>(a.q) + diff_row(f, slice, i, r0 + r) * a.d + col, q[r][i]);
 #pragma unroll
                     for (int c = 0; c < 8; c++) q[r][i][c] *= sl2;
                 }
@@ -148,7 +128,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
                 for (int i = 0; i < 2; i++) {
 #pragma unroll
                     for (int c = 0; c < 8; c++) y[c] = 0.f;
-                    if (here && on) get8((i ? k1 : k0) + x * a.d + col, y);
+                    if (here && on) diff_load8((i ? k1 : k0) + x * a.d + col, y);
 #pragma unroll
                     for (int r = 0; r < RR; r++) {
                         float u = q[r][i][0] * y[0];
@@ -194,7 +174,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
                 for (int h = 0; h < 2; h++) {
 #pragma unroll
                     for (int c = 0; c < 8; c++) y[c] = 0.f;
-                    if (here && (h ? on2 : on1)) get8(v + x * dv + h * VC + col, y);
+                    if (here && (h ? on2 : on1)) diff_load8(v + x * dv + h * VC + col, y);
 #pragma unroll
                     for (int r = 0; r < RR; r++)
 #pragma unroll
@@ -287,7 +267,8 @@ int launch_lanes(const DiffArgs& a, cudaStream_t st) {
     constexpr int smem = kStages * kStage + (int)sizeof(FewBars);
     static_assert(smem <= 227 * 1024 && kFewWarps<RR> * RR * 2 * (2 * LANES * 8 + 2) * 4 <= kStages * kStage, "shared memory budget");
     cudaFuncSetAttribute(diff_few_kernel<T, RR, LANES>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    LLSA_LAUNCH("diff_few", st, (diff_few_kernel<T, RR, LANES><<<dim3((unsigned)blocks, (a.d.R + RR - 1) / RR), (kFewWarps<RR> + 1) * 32, smem, st>>>(a)));
+    LLSA_LAUNCH("diff_few", st, launch_close(close_first(st), diff_few_kernel<T, RR, LANES>, dim3((unsigned)blocks, (a.d.R + RR - 1) / RR),
+                                              (kFewWarps<RR> + 1) * 32, smem, st, a));
     return LLSA_OK;
 }
 

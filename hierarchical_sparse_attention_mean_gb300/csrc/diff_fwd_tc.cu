@@ -19,11 +19,11 @@
 // Bound by the tensor cores: 1,536 clocks per 128 x 128 pairs at 64 columns, where the
 // exponentials of both maps take 1,024. 19 heads x 16,384 tokens of 64 columns: 2,359 us, 1,660
 // TFLOP/s, 85 % of what a large matrix product was measured at; of 128 columns 6,340 us, 1,648
-// TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 124 us, 384 pieces in three rounds of 152.
+// TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 120 us, 384 pieces in three rounds of 152.
 // S and P of 64 keys in two places per map, so that a map's products run beside its own
-// exponentials, took 138: S of 64 keys reads shared memory 1.5 times as much as S of 128.
+// exponentials, took 138 against 126 with cold caches: S of 64 keys reads shared memory 1.5 times as much as S of 128.
 // A piece's end behind the first tile of the next, with a place for the output rows taken from
-// the stages of K, took 134.
+// the stages of K, took 134 against 128.
 //
 // One block per SM stays for the whole call and takes its share of the pieces: while
 // the softmax warps finish one, the others load for the next.
@@ -164,6 +164,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
         prefetch_map(&mo2);
     }
     tc_fence_before();
+    close_wait();
     close_ahead();
     __syncthreads();
     tc_fence_after();
@@ -546,7 +547,7 @@ int launch(const DiffShape& s, DiffArgs f, cudaStream_t st) {
     if (pieces > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     a.pieces = (int)pieces;
     const int grid = resident_blocks(pieces);
-    LLSA_LAUNCH("diff_fwd_tc", st, diff_fwd_tc_kernel<D><<<grid, kThreads, C::SMEM, st>>>(mq, mk, mv, mo, mo2, f));
+    LLSA_LAUNCH("diff_fwd_tc", st, launch_close(close_first(st), diff_fwd_tc_kernel<D>, dim3(grid), kThreads, C::SMEM, st, mq, mk, mv, mo, mo2, f));
     return LLSA_OK;
 }
 

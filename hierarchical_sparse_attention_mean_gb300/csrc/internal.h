@@ -97,6 +97,35 @@ int launch_end(const char* name, cudaStream_t st);
         if (_llsa_rc != LLSA_OK) return _llsa_rc;               \
     } while (0)
 
+// Kernels that follow each other closely: one launched by launch_close may be set up while the one
+// before it in the stream still runs (from close_ahead there on, or as its blocks leave), and touches
+// memory behind close_wait alone, which waits until that one is done. Every kernel so launched
+// waits, if only at its end, so that what comes after it comes after all before it.
+__device__ __forceinline__ void close_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void close_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <typename... P, typename... A>
+void launch_close(bool close, void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = close ? 1 : 0;
+    cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// For the first kernel of a call, whatever is before it; in a captured graph that may be anything,
+// and an edge of the usual kind is taken.
+inline bool close_first(cudaStream_t st) {
+    cudaStreamCaptureStatus status;
+    return cudaStreamIsCapturing(st, &status) == cudaSuccess && status == cudaStreamCaptureStatusNone;
+}
+
 #define LLSA_TRY(expr)                                          \
     do {                                                        \
         int _llsa_rc = (expr);                                  \

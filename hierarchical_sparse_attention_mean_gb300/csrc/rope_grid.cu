@@ -8,7 +8,7 @@
 // frequencies to axes are one kernel.
 //
 // Bound by HBM: every element is read and written once, 2 x 12 heads x 65,536 tokens of 64
-// columns (403 MB) in 71 us, 5.7 TB/s. A thread takes one vector of a
+// columns (403 MB) in 67 us among others, 6.0 TB/s. A thread takes one vector of a
 // token (two a half apart in the half layout) and walks a run of heads with its sines
 // and cosines in registers. Segments of unequal axes need not be whole 16-byte vectors:
 // the half layout takes the widest vector that divides them all, so that 16 + 24 + 24
@@ -48,7 +48,7 @@ __device__ __forceinline__ void grid_position(const GridArgs& a, long long b, in
     if (a.pos) {
         const int* at = a.pos + ((a.batched ? b * a.n : 0) + t) * a.axes;
 #pragma unroll
-        for (int i = 0; i < kAxes; i++) p[i] = i < a.axes ? __ldg(at + i) : 0;
+        for (int i = 0; i < kAxes; i++) p[i] = i < a.axes ? at[i] : 0;
         return;
     }
     uint32_t rest = (uint32_t)t;
@@ -117,6 +117,7 @@ union Few {
 template <typename T, typename O, int W, bool PAIRED>
 __global__ void __launch_bounds__(kThreads) rope_grid_kernel(const __grid_constant__ GridArgs a) {
     const long long idx = (long long)blockIdx.x * kThreads + threadIdx.x;
+    close_ahead();
     if (idx >= a.rows * a.units) return;
     int u, t;
     long long b;
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kThreads) rope_grid_kernel(const __grid_consta
     }
     if (!copy) {
         int p[kAxes];
+        if (a.pos) close_wait();
         grid_position(a, b, t, p);
 #pragma unroll
         for (int i = 0; i < P; i++) {
@@ -166,6 +168,7 @@ __global__ void __launch_bounds__(kThreads) rope_grid_kernel(const __grid_consta
             if (!PAIRED || 2 * (first + i) < a.rot) grid_turn(a, p, first + i, c[i], s[i]);
         }
     }
+    close_wait();
     const int total = a.heads[0] + a.heads[1];
     const int h0 = blockIdx.y * a.heads_per_thread, h1 = min(h0 + a.heads_per_thread, total);
     auto place = [&](int h, const T*& in, O*& out) {
@@ -309,14 +312,15 @@ int launch_grid(const llsa_rope_grid_params* p, GridArgs& a, cudaStream_t st) {
     a.heads_per_thread = (total + gy - 1) / gy;  // the same share for all
     if (gx > 2147483647LL) return LLSA_ERR_UNSUPPORTED;
     const dim3 grid((unsigned)gx, (unsigned)gy);
+    const bool close = close_first(st);
     if (p->layout == LLSA_ROPE_INTERLEAVED)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V, true><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, launch_close(close, rope_grid_kernel<T, O, V, true>, grid, kThreads, 0, st, a));
     else if (w == V)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, launch_close(close, rope_grid_kernel<T, O, V, false>, grid, kThreads, 0, st, a));
     else if (w == V / 2)
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, V / 2, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, launch_close(close, rope_grid_kernel<T, O, V / 2, false>, grid, kThreads, 0, st, a));
     else
-        LLSA_LAUNCH("rope_grid", st, rope_grid_kernel<T, O, 1, false><<<grid, kThreads, 0, st>>>(a));
+        LLSA_LAUNCH("rope_grid", st, launch_close(close, rope_grid_kernel<T, O, 1, false>, grid, kThreads, 0, st, a));
     return LLSA_OK;
 }
 

@@ -325,6 +325,37 @@ def test_calls_behind_each_other_share_workspaces(dtype, d, nq, nk, causal, capt
             assert torch.equal(t, w), i
 
 
+@pytest.mark.parametrize("dtype,d,nq", [("bf16", 64, 300), ("bf16", 128, 300), ("bf16", 64, 1), ("fp32", 64, 300), ("fp32", 64, 2)])
+def test_inputs_written_right_before_the_call(dtype, d, nq):
+    """A call's first kernel may be set up while the kernel before it in the stream, whosever
+    it is, still writes what the call reads: copies of all inputs, the lengths among them."""
+    xs = [{n: t.cuda() for n, t in make(2, 4, 2, nq, 400, d, dtype, seed=s).items()} for s in (31, 32)]
+    ks = [lens([400, 200]), lens([77, 400])]
+    c, kl = {n: torch.empty_like(t) for n, t in xs[0].items()}, torch.empty_like(ks[0])
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"])
+    rope = llsa.RopeGridParams(2, 8, nq, d, columns=(d // 2, d // 2), dtype=dtype)
+    pos = torch.arange(2 * nq, dtype=torch.int32, device="cuda").view(nq, 2)
+
+    def call(i):
+        for n in c:
+            c[n].copy_(xs[i][n])
+        kl.copy_(ks[i])
+        o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], k_len=kl, backward=True)
+        got = [o, lse, o2, *llsa.diff_backward(p, c["q"], c["k"], c["v"], c["lam"], o, o2, lse, c["dout"], k_len=kl)]
+        c["q"].copy_(xs[1 - i]["q"])
+        return [*got, llsa.rotary(c["q"], None, rope, pos=pos.mul(i + 1))]
+
+    want = []
+    for i in (0, 1):
+        want.append(call(i))
+        torch.cuda.synchronize()
+    got = [call(i & 1) for i in range(20)]
+    torch.cuda.synchronize()
+    for i, ts in enumerate(got):
+        for t, w in zip(ts, want[i & 1]):
+            assert torch.equal(t, w), i
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
 def test_waits_that_run_out_are_reported_and_leave_no_trace(dtype, d):
     """With the copying warps switched off every consumer's first wait runs out: the
