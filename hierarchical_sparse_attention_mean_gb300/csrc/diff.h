@@ -129,8 +129,7 @@ DenseSplit diff_tc_fwd_split(const DiffShape& s);
 int launch_diff_tc_fwd(const DiffShape& s, const DiffArgs& a, cudaStream_t st);
 
 // diff_bwd_tc.cu: backward on the tensor cores (bf16); diff_bwd_wide_tc.cu: behind 64 columns.
-DenseSplit diff_tc_dq_split(const DiffShape& s);
-DenseSplit diff_tc_dkv_split(const DiffShape& s);
+void diff_tc_bwd_splits(const DiffShape& s, DenseSplit* rows, DenseSplit* keys);
 int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st);
 int launch_diff_tc_bwd_wide(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st);
 

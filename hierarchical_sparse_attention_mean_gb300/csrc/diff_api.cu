@@ -791,8 +791,7 @@ struct TcBwd {
 
 TcBwd tc_bwd(const DiffShape& s) {
     TcBwd t;
-    t.q = diff_tc_dq_split(s);
-    t.k = diff_tc_dkv_split(s);
+    diff_tc_bwd_splits(s, &t.q, &t.k);
     t.nq = 2LL * s.slices * s.R * s.d;
     t.nk = 2LL * s.slices * s.nk * s.d;
     const size_t rows = (size_t)s.slices * s.Rp * sizeof(float);

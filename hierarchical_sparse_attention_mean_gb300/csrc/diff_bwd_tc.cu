@@ -569,8 +569,10 @@ diff_bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                    const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
                    const __grid_constant__ CUtensorMap zq, const __grid_constant__ CUtensorMap zk,
                    const __grid_constant__ CUtensorMap zv, const __grid_constant__ DiffArgs aq,
-                   const __grid_constant__ DiffArgs ak, int key_pieces) {
-    const int piece = blockIdx.x;
+                   const __grid_constant__ DiffArgs ak, int row_pieces, int key_pieces, int keys_first) {
+    // longer pieces first
+    const int piece = blockIdx.x < (keys_first ? 0 : row_pieces) ? blockIdx.x + key_pieces
+                      : blockIdx.x - (keys_first ? 0 : row_pieces);
     if (piece < key_pieces)
         bwd_side<true>(mk, mv, mq, mg, zk, zv, ak, piece);
     else
@@ -579,12 +581,55 @@ diff_bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
 
 }  // namespace
 
-// Behind 64 columns a row or key block is several pieces of work.
-DenseSplit diff_tc_dq_split(const DiffShape& s) {
-    return dense_make_split((long long)s.slices * ((s.R + BT - 1) / BT) * (s.d > D ? 2 : 1), s.nk, BT, 2);
+// When the last of `first` pieces of `a` clocks and then `others` of `b` < a ends, one at a time on
+// every SM.
+static long long pieces_end(long long first, long long a, long long others, long long b) {
+    const long long sms = kDenseSms, rounds = first / sms, left = first % sms;
+    const long long even = (left * a + others * b + sms - 1) / sms;  // no sooner than this
+    long long end = -1;
+    for (int i = 0; i < 2; i++)
+        for (const long long from : {0LL, a}) {
+            const long long t = from + (std::max(0LL, even - from) + b - 1) / b * b + i * b;
+            const bool all = (left == 0 || t >= a) && (sms - left) * (t / b) + left * (std::max(0LL, t - a) / b) >= others;
+            if (all && (end < 0 || t < end)) end = t;
+        }
+    return rounds * a + std::max(end, even);
 }
-DenseSplit diff_tc_dkv_split(const DiffShape& s) {
-    return dense_make_split((long long)s.slices * ((s.nk + BT - 1) / BT) * (s.d > D ? 3 : 1), s.R, BT, 2);
+
+// Into how many parts the pieces of rows go along the keys and those of keys along the rows: what
+// ends first by a count of clocks, in tenths of what a tile of a rows' piece takes. A tile of a
+// keys' piece takes 13, a piece's beginning and end three tiles, joining parts 30 and what they
+// write and read; a few long pieces beside many short ones, which copy more, take twice as long. Longer pieces go first. One query, 6 heads x 8,192 keys: 41 us, 53 with as many
+// parts of either kind as SMs; 2 x 3 heads x 700 x 1,500, d = 96: 44 and 57.
+void diff_tc_bwd_splits(const DiffShape& s, DenseSplit* rows, DenseSplit* keys) {
+    constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+    const long long r = (s.R + BT - 1) / BT, k = (s.nk + BT - 1) / BT;
+    // behind 64 columns a row or key block is several pieces of work
+    const long long row_pieces = s.slices * r * (s.d > D ? 2 : 1), key_pieces = s.slices * k * (s.d > D ? 3 : 1);
+    const long long row_join = (long long)s.slices * s.R * s.d / 65536, key_join = (long long)s.slices * s.nk * s.d / 32768;
+    int best_r = 1, best_k = 1;
+    long long best = 0;
+    for (int nr : kParts) {
+        if (nr > 1 && nr * 2 > k) break;
+        for (int nk : kParts) {
+            if (nk > 1 && nk * 2 > r) break;
+            const long long lr = 10 * ((k + nr - 1) / nr + 3), lk = 13 * ((r + nk - 1) / nk + 3);
+            const long long cr = row_pieces * nr, ck = key_pieces * nk, first = lr > lk ? cr : ck, b = std::min(lr, lk);
+            long long a = std::max(lr, lk);
+            if (first <= kDenseSms / 2 && b < a / 3) a *= 2;
+            long long t = pieces_end(first, a, lr > lk ? ck : cr, b);
+            if (nr > 1 || nk > 1) t += 30 + (nr > 1 ? nr * row_join : 0) + (nk > 1 ? nk * key_join : 0);
+            if (best == 0 || t < best) {
+                best = t;
+                best_r = nr;
+                best_k = nk;
+            }
+        }
+    }
+    rows->chunk = (int)((k + best_r - 1) / best_r) * BT;
+    rows->splits = (s.nk + rows->chunk - 1) / rows->chunk;
+    keys->chunk = (int)((r + best_k - 1) / best_k) * BT;
+    keys->splits = (s.R + keys->chunk - 1) / keys->chunk;
 }
 
 int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& ak, cudaStream_t st) {
@@ -605,7 +650,7 @@ int launch_diff_tc_bwd(const DiffShape& s, const DiffArgs& aq, const DiffArgs& a
     const long long pk = (long long)((s.nk + BT - 1) / BT) * s.slices * ak.d.splits;
     if (pq + pk > kDenseMaxPieces) return LLSA_ERR_UNSUPPORTED;
     LLSA_LAUNCH("diff_bwd_tc", st, launch_close(true, diff_bwd_tc_kernel, dim3((unsigned)(pq + pk)), kThreads, smem, st, mq, mg, mk, mv, zq,
-                                                zk, zv, aq, ak, (int)pk));
+                                                zk, zv, aq, ak, (int)pq, (int)pk, (int)(std::min(ak.d.chunk, s.R) >= std::min(a.chunk, s.nk))));
     return LLSA_OK;
 }
 
