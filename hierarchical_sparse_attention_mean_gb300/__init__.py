@@ -1139,13 +1139,16 @@ def _wide(q, k):
 
 # diff_attention with rope= is wide wherever that hides behind the call, whatever the columns: lam's
 # gradient is a sum of terms of both signs over all tokens, and with few heads it can come out as
-# small as what the rounding of turned q and k makes of it (0.007 to 0.011 off where the other
-# outputs are 0.003; in fp32 all are 0.0017). 2^24 pairs of 64 columns take the GPU 350 us.
-_WIDE_DIFF = (1 << 24) * 64
+# small as what the rounding of turned q and k makes of it (one to four heads, worst of 24 inputs of
+# up to 4,000 tokens: 0.006 to 0.035 off where the other outputs are 0.003; in fp32 0.0036).
+# 2^24 pairs of 64 columns take the GPU 350 us. Up to four heads it is wide for four times as many.
+_WIDE_DIFF, _FEW_HEADS = (1 << 24) * 64, 4
 
 
 def _wide_diff(q, k):
-    return _wide(q, k) or (q.dtype == torch.bfloat16 and q.numel() * k.shape[-2] <= _WIDE_DIFF)
+    if q.dtype != torch.bfloat16:
+        return False
+    return _wide(q, k) or q.numel() * k.shape[-2] <= (4 if q.shape[1] <= 2 * _FEW_HEADS else 1) * _WIDE_DIFF
 
 
 def _positioned(rope, q, k, v, pos, wide=_wide):
@@ -1284,7 +1287,7 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     one number for all heads. q_len, k_len, rope, pos and captured backward passes: as
     dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
     in fp32 from the turn to the last rounding where that call's does, and up to 2^30
-    products of a pair of a query and a key (both maps' pairs times d)."""
+    products of a pair of a query and a key (both maps' pairs times d), 2^32 with up to four heads."""
     if isinstance(lam, torch.Tensor) and lam.numel() == 1:
         lam = lam.reshape(1).expand(q.shape[1] // 2)
     return _dense_fns()[2].apply(q, k, v, lam, causal, scale, q_len, k_len, rope, pos)

@@ -123,7 +123,9 @@ void launch_close(bool close, void (*kernel)(P...), dim3 grid, int threads, size
 // and an edge of the usual kind is taken.
 inline bool close_first(cudaStream_t st) {
     cudaStreamCaptureStatus status;
-    return cudaStreamIsCapturing(st, &status) == cudaSuccess && status == cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &status) == cudaSuccess) return status == cudaStreamCaptureStatusNone;
+    cudaGetLastError();  // the launch says whether it may run
+    return false;
 }
 
 #define LLSA_TRY(expr)                                          \

@@ -127,7 +127,9 @@ def test_parameters_copy_and_pickle(lib):
 
 
 @pytest.mark.parametrize("b,h,n,d,wide", [
-    (1, 6, 64, 64, True), (1, 1, 2896, 64, True), (1, 1, 2897, 64, False), (1, 1, 2048, 128, True), (1, 1, 2049, 128, False),
+    (1, 6, 64, 64, True), (1, 1, 5792, 64, True), (1, 1, 5793, 64, False), (1, 1, 4096, 128, True), (1, 1, 4097, 128, False),
+    (2, 2, 2048, 128, True), (2, 2, 2049, 128, False), (1, 4, 2896, 64, True), (1, 4, 2897, 64, False),
+    (1, 8, 1024, 64, True), (1, 8, 1025, 64, False), (2, 5, 1295, 32, True), (2, 5, 1296, 40, False),
     (4, 16, 16, 128, True), (2, 6, 4096, 64, False), (1, 1, 16384, 8, True),
 ])
 def test_where_positions_stay_in_fp32(b, h, n, d, wide):
