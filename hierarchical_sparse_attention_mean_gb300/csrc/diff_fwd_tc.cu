@@ -439,6 +439,9 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             }
             const float lam = here ? diff_lam(f, diff_head(f, pc.slice, r)) : 0.f;  // comes while O is being finished
             if (a.splits == 1) {
+                // l has one place: all warps have read the last piece's sums before they left its O. With one
+                // key tile nothing else holds this back, as S waits for no O.
+                if (v > 0) bar_wait(smem_u32(&bar->o_free[w]), (v - 1) & 1, abort_flag, a);
                 bar->l[w][lr] = l;
                 warp_arrive(smem_u32(&bar->l_ready), lane);
             }

@@ -618,6 +618,37 @@ def test_three_resident_blocks_take_everything(b, h, kv, nq, nk, causal, ql, kl,
         assert torch.equal(got[n], want[n]), n
 
 
+@pytest.mark.parametrize("few", [False, True])
+@pytest.mark.parametrize("cfg,ql,kl,causal", [
+    ((8, 16, 16, 300, 100, 64), None, None, False),
+    ((8, 16, 4, 140, 128, 64), None, None, False),
+    ((12, 16, 16, 260, 77, 40), [260, 3, 129] * 4, [77, 1, 50, 0] * 3, True),
+    ((16, 12, 12, 200, 700, 64), None, [700, 60, 128, 1] * 4, False),  # pieces of one key tile between longer ones
+])
+def test_pieces_of_one_key_tile_keep_their_sums(cfg, ql, kl, causal, few):
+    """The sums of a piece's rows pass from one map's warps to the other's through a place
+    that the next piece uses too; with one tile of keys a piece is over soon."""
+    x = make(*cfg, "bf16", ql, kl, seed=24)
+    if few:
+        llsa.test_set_wait_limit(0, llsa.LLSA_TEST_FEW_BLOCKS)
+    try:
+        c = {n: t.cuda() for n, t in x.items()}
+        p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], causal=causal)
+        a, b = lens(ql), lens(kl)
+        runs = [llsa.diff_forward(p, c["q"], c["k"], c["v"], c["lam"], a, b, backward=True) for _ in range(60)]
+        torch.cuda.synchronize()
+    finally:
+        llsa.test_set_wait_limit(0, 0)
+    assert llsa.llsa_get_status() == 0
+    y = {n: t for n, t in x.items() if n != "dout"}
+    want = ref.attention(**y, causal=causal, q_len=ql, k_len=kl)
+    for n, t in zip(("o", "lse", "o2"), runs[0]):
+        ref.check(n, t, want[n])
+    for i, got in enumerate(runs[1:]):
+        for s, t in zip(got, runs[0]):
+            assert torch.equal(s, t), i
+
+
 def test_inputs_and_gradients_off_16_bytes():
     """Views into flat buffers, as a packed set of parameters gives them: copied, not refused."""
     x = make(1, 2, 2, 40, 50, 64, "bf16", seed=21)
