@@ -138,9 +138,9 @@ dense_fwd_split_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     if (warp == kFwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
     close_wait();
-    close_ahead();
     __syncthreads();
     tc_fence_after();
+    close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t tP = tbase + C::TM_P, tO = tbase + C::TM_O;
 
@@ -398,9 +398,9 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mx1, const CUtensorM
     if (warp == kBwdWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
     close_wait();
-    close_ahead();
     __syncthreads();
     tc_fence_after();
+    close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t tDP = tbase + 128, tP3 = tbase + 256, tS3 = tbase + 320, tAcc = tbase + 384;
 

@@ -112,9 +112,9 @@ __device__ __forceinline__ void wide_side(const CUtensorMap& mx1, const CUtensor
     if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
     close_wait();
-    close_ahead();
     __syncthreads();
     tc_fence_after();
+    close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
     const uint32_t t3 = tbase + 128, tAcc = tbase + 256;
 

@@ -139,10 +139,10 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
     }
     if (warp == kWarps) tmem_alloc(smem_u32(&bar->tmem_slot), 512);
     tc_fence_before();
-    close_ahead();
     close_wait();
     __syncthreads();
     tc_fence_after();
+    close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
 
     if (warp >= kWarps) {

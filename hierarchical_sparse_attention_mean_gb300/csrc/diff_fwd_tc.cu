@@ -165,9 +165,9 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
     }
     tc_fence_before();
     close_wait();
-    close_ahead();
     __syncthreads();
     tc_fence_after();
+    close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
 
     // Every role walks the block's pieces. What is counted on through them: the rings'

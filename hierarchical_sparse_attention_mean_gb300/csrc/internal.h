@@ -100,7 +100,9 @@ int launch_end(const char* name, cudaStream_t st);
 // Kernels that follow each other closely: one launched by launch_close may be set up while the one
 // before it in the stream still runs (from close_ahead there on, or as its blocks leave), and touches
 // memory behind close_wait alone, which waits until that one is done. Every kernel so launched
-// waits, if only at its end, so that what comes after it comes after all before it.
+// waits, if only at its end, so that what comes after it comes after all before it. A kernel that
+// takes tensor memory calls close_ahead behind the barrier that follows the allocation: the next
+// one's blocks take theirs before they wait, and may share an SM with blocks that they wait for.
 __device__ __forceinline__ void close_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void close_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
