@@ -1044,6 +1044,11 @@ def _check_rope(p, q, k, name="rope"):
     if tuple(q.shape) != want or (k is not None and tuple(k.shape) != (p.batch, p.kv_heads, p.n, p.d)):
         raise ValueError(f"{name} is for q {want} and {p.kv_heads} heads of k, got q {tuple(q.shape)}"
                          + ("" if k is None else f" and k {tuple(k.shape)}"))
+    for what, t in (("q", q), ("k", k)):
+        if t is not None and t.dtype != _tok_dtype(p):
+            raise ValueError(f"{what} must be {_tok_dtype(p)}, as {name} says, got {t.dtype}")
+    if getattr(p, "out_dtype", "") not in ("", p.dtype):
+        raise ValueError(f"{name} must leave q and k their type: out_dtype is for llsa_rope_grid")
 
 
 def _contiguous(t):
@@ -1151,6 +1156,11 @@ def _wide_diff(q, k):
     return _wide(q, k) or q.numel() * k.shape[-2] <= (4 if q.shape[1] <= 2 * _FEW_HEADS else 1) * _WIDE_DIFF
 
 
+def _check_values(q, v):
+    if v.dtype != q.dtype:
+        raise ValueError(f"v must be {q.dtype}, got {v.dtype}")
+
+
 def _positioned(rope, q, k, v, pos, wide=_wide):
     """Contiguous q, k, v with the positions of `rope` (None: none) turned in, and the
     parameters that turn their gradients back."""
@@ -1158,9 +1168,7 @@ def _positioned(rope, q, k, v, pos, wide=_wide):
         q, k = _contiguous(q), _contiguous(k)
     elif wide(q, k):
         _check_rope(rope, q, k)
-        for name, t, want in (("q", q, _tok_dtype(rope)), ("k", k, q.dtype), ("v", v, q.dtype)):
-            if t.dtype != want:
-                raise ValueError(f"{name} must be {want}, got {t.dtype}")
+        _check_values(q, v)
         q, k, v = (t.to(torch.float32, memory_format=torch.contiguous_format) for t in (q, k, v))
         rope = rope.in_fp32()
         _turn(rope, q, k, q, k, pos=pos)
@@ -1205,10 +1213,9 @@ def _dense_functions():
             ctx.narrow = grid = None if rope is None or not _wide_diff(q, k) else rope.grid(pos is not None)
             if grid is not None:  # turned into fp32, and the gradients back out of it
                 _check_rope(rope, q, k)
+                _check_values(q, v)
                 x, y = (torch.empty(t.shape, dtype=torch.float32, device=t.device) for t in (q, k))
                 llsa_rope_grid(grid.to_fp32(), _rope_view(q), _rope_view(k), x, y, pos=pos)
-                if v.dtype != q.dtype:
-                    raise ValueError(f"v must be {q.dtype}, got {v.dtype}")
                 q, k, v = x, y, _contiguous(v)
             else:
                 q, k, v, rope = _positioned(rope, q, k, v, pos, _wide_diff)

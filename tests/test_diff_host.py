@@ -136,3 +136,36 @@ def test_where_positions_stay_in_fp32(b, h, n, d, wide):
     q = torch.empty(b, 2 * h, n, d, dtype=torch.bfloat16, device="meta")
     assert llsa._wide_diff(q, q) is wide
     assert llsa._wide_diff(q.float(), q.float()) is False
+
+
+@pytest.mark.parametrize("n", [60, 4096])  # in fp32 from the turn on, and not
+@pytest.mark.parametrize("entry", ["diff", "dense"])
+def test_positions_of_another_type_are_refused_at_any_size(entry, n):
+    """What the positions say of the types holds whether or not a call keeps bf16 in fp32."""
+    heads = 10 if entry == "diff" else 5
+    q = torch.zeros(1, heads, n, 64, dtype=torch.bfloat16)
+    v = torch.zeros(1, 5, n, 128 if entry == "diff" else 64, dtype=torch.bfloat16)
+    if entry == "dense":  # there few columns decide
+        q, v = q[..., :24], v[..., :24]
+    assert (llsa._wide_diff if entry == "diff" else llsa._wide)(q, q) is (n == 60)
+
+    def call(rope, k=q):
+        return llsa.diff_attention(q, k, v, torch.zeros(5), rope=rope) if entry == "diff" else llsa.dense_attention(q, k, v, rope=rope)
+
+    d = q.shape[-1]
+    kw = dict(kv_heads=heads, columns=(d - 8, 8), extent=(n // 4, 4))
+    grid = llsa.RopeGridParams(1, heads, n, d, **kw)
+    line = llsa.RopeParams(1, heads, n, d, kv_heads=heads)
+    for rope in (grid, line):
+        with pytest.raises(ValueError, match="CUDA"):  # found right up to the device
+            call(rope)
+        with pytest.raises(ValueError, match="q must be torch.float32"):
+            call(dataclasses.replace(rope, dtype="fp32"))
+        with pytest.raises(ValueError, match="k must be torch.bfloat16"):
+            call(rope, q.float())
+    for other in (dataclasses.replace(grid, out_dtype="fp32"), dataclasses.replace(grid, dtype="fp32", out_dtype="bf16")):
+        with pytest.raises(ValueError, match="must be torch.float32|out_dtype"):
+            call(other)
+    call_same = dataclasses.replace(grid, out_dtype="bf16")
+    with pytest.raises(ValueError, match="CUDA"):
+        call(call_same)
