@@ -369,7 +369,7 @@ class RopeParams:
 
     def grid(self, has_pos: bool = False) -> "RopeGridParams | None":
         """The same positions as parameters of llsa_rope_grid; None where it has none (an image whose
-        last row is not full)."""
+        last row is not full, fields that llsa_rope refuses)."""
         got = self.__dict__.get("_grid", {}).get(has_pos, self)
         if got is not self:
             return got
@@ -380,7 +380,8 @@ class RopeParams:
             extent = (self.n,)
         else:
             extent = (self.n // self.width, self.width) if self.width > 0 and self.n % self.width == 0 else 0
-        if extent == 0 or rot % (2 * self.axes):
+        stray = not has_pos and (self.width if self.axes == 1 else self.pos_offset)  # a field of the other kind of axes
+        if self.axes not in (1, 2) or extent == 0 or stray or rot % (2 * self.axes):
             got = None
         else:
             got = RopeGridParams(self.batch, self.heads, self.n, self.d, kv_heads=self.kv_heads, columns=(rot // self.axes,) * self.axes,

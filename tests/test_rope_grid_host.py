@@ -126,3 +126,14 @@ def test_one_and_two_axes_as_a_grid(lib, kw, extent):
     for name in ("layout", "base", "scaling", "factor", "orig_len", "low", "high", "amplitude", "dtype", "batch", "heads", "kv_heads", "n", "d"):
         assert getattr(g, name) == getattr(p, name)
     assert sum(g.columns) == (p.rot_dim or p.d) and g.to_fp32().out_dtype == "fp32" and g.from_fp32().dtype == "fp32"
+
+
+@pytest.mark.parametrize("kw", [dict(axes=2, width=6, pos_offset=3), dict(width=6), dict(axes=0), dict(axes=3, width=6)])
+def test_what_one_and_two_axes_refuse_has_no_grid(lib, kw):
+    """Positions that llsa_rope refuses do not become others on their way through a grid."""
+    p = llsa.RopeParams(2, 4, 60, 64, kv_heads=2, **kw)
+    assert p.grid() is None
+    assert lib.llsa_rope(ctypes.byref(p.c()), None, 16, 16, None, 32, 32, 0, None) == INVALID
+    given = p.grid(True)  # with positions given, what would imply them is ignored, as in llsa_rope
+    code = lib.llsa_rope(ctypes.byref(p.c()), None, 16, 16, 6, 32, 32, 0, None)
+    assert (given is None and code == INVALID) if p.axes not in (1, 2) else (given.extent is None and code == ALIGN)
