@@ -1292,11 +1292,13 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     (softmax(q1 k1) - lam softmax(q2 k2)) v. q [batch, 2 heads, nq, d] and k [batch,
     2 kv_heads, nk, d] hold the first maps' heads, then the second maps'; v [batch,
     kv_heads, nk, 2d]; lam [heads], bf16 or fp32 whatever the type of the others, or
-    one number for all heads. q_len, k_len, rope, pos and captured backward passes: as
+    a tensor of one element for all heads. q_len, k_len, rope, pos and captured backward passes: as
     dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
     in fp32 from the turn to the last rounding where that call's does, and up to 2^30
     products of a pair of a query and a key (both maps' pairs times d), 2^32 with up to four heads."""
-    if isinstance(lam, torch.Tensor) and lam.numel() == 1:
+    if not isinstance(lam, torch.Tensor):
+        raise TypeError(f"lam must be a torch.Tensor, of one element for all heads or of [heads], not {type(lam).__name__}")
+    if lam.numel() == 1:
         lam = lam.reshape(1).expand(q.shape[1] // 2)
     return _dense_fns()[2].apply(q, k, v, lam, causal, scale, q_len, k_len, rope, pos)
 

@@ -169,3 +169,10 @@ def test_positions_of_another_type_are_refused_at_any_size(entry, n):
     call_same = dataclasses.replace(grid, out_dtype="bf16")
     with pytest.raises(ValueError, match="CUDA"):
         call(call_same)
+
+
+@pytest.mark.parametrize("lam", [0.5, 1, None, [0.5]])
+def test_lam_that_is_no_tensor_is_refused_by_name(lam):
+    x, v = torch.zeros(1, 2, 4, 64), torch.zeros(1, 1, 4, 128)
+    with pytest.raises(TypeError, match="lam must be a torch.Tensor"):
+        llsa.diff_attention(x, x, v, lam)
