@@ -310,11 +310,17 @@ __global__ void __launch_bounds__(kThreads) dense_bwd_few_kernel(const __grid_co
                     acc[r][i] = fmaf(ds, kf[i], acc[r][i]);
                 }
             }
-            if (on && j < last) {  // keys that no row sees: zeros
+            if (on && j < stop) {
                 store4(dk + (long long)j * a.d, ok);
                 store4(dk + (long long)j * a.d + 4, ok + 4);
                 store4(dv + (long long)j * a.d, ov);
                 store4(dv + (long long)j * a.d + 4, ov + 4);
+            } else if (on && j < last) {  // keys that no row sees: zeros, also beside a row that is no number
+                const float none[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int c = 0; c < 8; c += 4) {
+                    store4(dk + (long long)j * a.d + c, none);
+                    store4(dv + (long long)j * a.d + c, none);
+                }
             }
         }
     }
@@ -399,8 +405,8 @@ DenseSplit dense_few_split(const DenseShape& s) {
     return p;
 }
 
-// Four rows in either type: 8 x 4 key heads x 16,383 keys at 128 columns 139 us in bf16
-// against 255 on the tensor cores (one row 90), fp32 289 against 1,170; bf16 at 256
+// Four rows in either type: 8 x 4 key heads x 16,383 keys at 128 columns 142 us in bf16
+// against 255 on the tensor cores (one row 99), fp32 254 against 1,170; bf16 at 256
 // columns 272 against 762.
 bool dense_few_bwd_supported(const DenseShape& s) { return s.R > 0 && s.R <= 4 && s.nk > 0; }
 

@@ -388,6 +388,10 @@ __device__ __forceinline__ void keys_side(const DenseArgs& a, int piece) {
     for (int i = 0; i < N; i++) {
         const int j = j0 + ty * N + i;
         if (j >= a.nk) continue;
+        if (j >= sp.lk) {  // zeros, also beside a row that is no number
+#pragma unroll
+            for (int c = 0; c < DP / 64; c++) dk[i][c] = dv[i][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
         const long long row = (long long)slice * a.nk + j;
         if (a.splits > 1) {
             const long long all = (long long)a.slices * a.nk;

@@ -731,3 +731,29 @@ def test_two_captured_graphs_at_once(dtype, nq, d):
     for outs, w in zip(got, want):
         for t, n in zip(outs, ("o", "lse", "dq", "dk", "dv")):
             assert torch.equal(t, w[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("nq,nk,d", [(1, 200, 64), (2, 700, 128), (4, 3000, 40), (9, 300, 64), (200, 260, 64), (200, 260, 128), (140, 190, 256), (1, 6000, 64), (3000, 100, 200)])
+def test_a_row_that_is_no_number_leaves_padding_alone(nq, nk, d, causal, dtype):
+    """Keys behind a length get zeros for gradients, and other heads, entries and rows what they get without it."""
+    kl = [nk - 77, nk, nk // 2]
+    x = make(3, 2, 2, nq, nk, d, dtype, None, kl, seed=31)
+    want = run(x, causal=causal, k_len=kl)
+    row = nq // 2
+    x["q"][0, 1, row, 3] = float("nan")
+    got = run(x, causal=causal, k_len=kl)
+    sees = kl[0] - nq + row + 1 if causal else kl[0]
+    if sees <= 0:  # no key for it
+        for n in got:
+            assert torch.equal(got[n], want[n]), n
+        return
+    for n in ("dk", "dv"):
+        assert bool(got[n][0, 1, :sees].isnan().any(-1).all()), n
+        for e in range(3):
+            assert not got[n][e, :, kl[e]:].any(), n
+        assert torch.equal(got[n][0, 0], want[n][0, 0]) and torch.equal(got[n][1:], want[n][1:]), n
+    others = [r for r in range(nq) if r != row]
+    assert bool(got["dq"][0, 1, row].isnan().any()) and torch.equal(got["dq"][0, 1, others], want["dq"][0, 1, others])
+    assert torch.equal(got["dq"][0, 0], want["dq"][0, 0]) and torch.equal(got["dq"][1:], want["dq"][1:])
