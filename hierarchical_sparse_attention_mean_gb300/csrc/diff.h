@@ -70,6 +70,13 @@ __device__ __forceinline__ int diff_head(const DiffArgs& a, int slice, int r) {
     return slice % a.d.kv_heads * (a.heads / a.d.kv_heads) + r / a.d.nq;
 }
 
+// The same for row r of a slice, and 0 where the row sees no key: it has o = 0 and no gradient
+// whatever lam is, infinite or no number.
+__device__ __forceinline__ float diff_lam_row(const DiffArgs& a, int slice, int r) {
+    const float lam = diff_lam(a, diff_head(a, slice, r));
+    return isfinite(lam) || dense_kend(a.d, dense_span(a.d, slice), r % a.d.nq) > 0 ? lam : 0.f;
+}
+
 // Row r of map i of a slice in an array over [batch][2 heads][nq].
 __device__ __forceinline__ long long diff_row(const DiffArgs& a, int slice, int i, int r) {
     const int b = slice / a.d.kv_heads, g = slice - b * a.d.kv_heads;

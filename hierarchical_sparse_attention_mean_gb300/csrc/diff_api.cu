@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) diff_expand_kernel(const __grid_cons
         load4f(static_cast<const Q*>(a.q) + one, y);
         store4(f.q + to, y);
         if (!BACKWARD) continue;
-        const float lam = diff_lam(f.a, diff_head(f.a, (int)slice, r));
+        const float lam = diff_lam_row(f.a, (int)slice, r);
         float o[4], o2[4];
         load4f(static_cast<const T*>(a.dout) + two, y);
         load4f(static_cast<const Q*>(f.a.o2) + two, o2);
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads) diff_planes_kernel(const __grid_cons
         }
         const long long at = (((4 * outer + j) * a.kv_heads + g) * rows + r) * a.d + c;
         put_planes(f.out[t] + at, f.n[t], y);
-        const float lam = diff_lam(f.a, diff_head(f.a, (int)m, r));
+        const float lam = diff_lam_row(f.a, (int)m, r);
 #pragma unroll
         for (int e = 0; e < 8; e++) y[e] *= -lam;
         put_planes(f.out[t] + at + 2LL * a.kv_heads * rows * a.d, f.n[t], y);
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) diff_combine_kernel(const __grid_con
         const int slice = (int)(row / a.R), r = (int)(row - (long long)slice * a.R);
         const int b = slice / a.kv_heads, g = slice - b * a.kv_heads;
         const long long first = ((4LL * b + j) * a.kv_heads + g) * a.R + r, second = first + 2 * step;
-        const float lam = diff_lam(f.a, diff_head(f.a, slice, r));
+        const float lam = diff_lam_row(f.a, slice, r);
         float y[4], z[4];
         load4f(f.o + first * a.d + col - j * a.d, y);
         load4f(f.o + second * a.d + col - j * a.d, z);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) diff_join_kernel(const __grid_consta
     __syncthreads();
     const int c = threadIdx.x * 4;
     if (c >= dv) return;
-    const float lam = diff_lam(f, diff_head(f, slice, r));
+    const float lam = diff_lam_row(f, slice, r);
     float y[2][4];
 #pragma unroll
     for (int i2 = 0; i2 < 2; i2++) {

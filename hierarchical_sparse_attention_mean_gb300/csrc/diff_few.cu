@@ -249,7 +249,7 @@ __global__ void __launch_bounds__((kFewWarps<RR> + 1) * 32, 1) diff_few_kernel(c
             }
         }
         if (a.splits > 1) continue;
-        const float o = fmaf(-diff_lam(f, diff_head(f, slice, r0 + r)), out[1], out[0]);
+        const float o = fmaf(-diff_lam_row(f, slice, r0 + r), out[1], out[0]);
         if constexpr (sizeof(T) == 2) {
             static_cast<__nv_bfloat16*>(a.o_out)[row * dv + c] = __float2bfloat16_rn(o);
             if (f.o2_out) static_cast<__nv_bfloat16*>(f.o2_out)[row * dv + c] = __float2bfloat16_rn(out[1]);

@@ -437,7 +437,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                 }
                 continue;
             }
-            const float lam = here ? diff_lam(f, diff_head(f, pc.slice, r)) : 0.f;  // comes while O is being finished
+            float lam = here ? diff_lam(f, diff_head(f, pc.slice, r)) : 0.f;  // comes while O is being finished
             if (a.splits == 1) {
                 // l has one place: all warps have read the last piece's sums before they left its O. With one
                 // key tile nothing else holds this back, as S waits for no O.
@@ -474,6 +474,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
             bar_wait(smem_u32(&bar->l_ready), v & 1, abort_flag, a);
             const float la = bar->l[0][lr], lb = bar->l[1][lr];
             const float inv1 = la == 0.f ? 0.f : 1.f / la, inv2 = lb == 0.f ? 0.f : 1.f / lb;
+            if (lb == 0.f) lam = 0.f;  // no key: o is 0 whatever lam is
             unsigned char* out = sQ + 2 * (v % C::NQ) * C::TILE + w * C::REGION;
             unsigned char* out2 = D == 64 ? out : out + C::TILE;
             uint32_t kept[32];  // o2's row, packed

@@ -712,6 +712,46 @@ def test_nan_among_the_scores_stays_in_its_row():
         assert torch.equal(o.isnan().all(-1).cpu(), bad[:, :2]) and torch.equal(o.isnan().any(-1).cpu(), bad[:, :2])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("nq,nk,d,causal,ql,kl", [
+    (140, 200, 64, False, [140, 70, 0], [200, 0, 90]),
+    (140, 200, 128, True, [140, 101, 50], [100, 1, 200]),   # rows before the first key in causal order
+    (1, 200, 64, False, None, [200, 0, 1]),
+    (4, 300, 64, True, [4, 3, 4], [300, 300, 2]),
+    (1, 9000, 64, False, None, [9000, 0, 8000]),            # parts of the keys, and their join
+    (40, 9000, 64, True, [40, 7, 40], [9000, 0, 20]),
+    (40, 8, 64, True, [40, 7, 40], [8, 0, 5]),
+])
+def test_rows_without_keys_are_zero_whatever_lam_is(nq, nk, d, causal, ql, kl, dtype):
+    """A lam that is infinite or no number stays in its head, and there in the rows that see a key."""
+    x = make(3, 3, 3, nq, nk, d, dtype, ql, kl, seed=25)
+    c = {n: t.cuda() for n, t in x.items()}
+    p = llsa.DiffParams.like(c["q"], c["k"], c["lam"], causal=causal)
+    a, b = lens(ql), lens(kl)
+
+    def call(lam):
+        lam = torch.tensor(lam).to(T[dtype]).cuda()
+        o, lse, o2 = llsa.diff_forward(p, c["q"], c["k"], c["v"], lam, a, b, backward=True)
+        alone = llsa.diff_forward(p, c["q"], c["k"], c["v"], lam, a, b)[0]
+        grads = llsa.diff_backward(p, c["q"], c["k"], c["v"], lam, o, o2, lse, c["dout"], a, b)
+        torch.cuda.synchronize()
+        assert llsa.llsa_get_status() == 0 and torch.equal(alone.nan_to_num(), o.nan_to_num())
+        return dict(zip(NAMES, (o, o2, lse, *grads)))
+
+    got, want = call([0.5, math.nan, math.inf]), call([0.5, 0.5, 0.5])
+    none = got["lse"][:, :3] == -math.inf
+    assert torch.equal(none, got["lse"][:, 3:] == -math.inf) and bool(none.any()) and not bool(none.all())
+    assert not got["o"][none].any() and not got["o2"][none].any()
+    assert bool(got["o"][:, 1][~none[:, 1]].isnan().all()) and not bool(got["o"][:, 2][~none[:, 2]].isfinite().any())
+    assert not got["dq"][torch.cat([none, none], 1)].any()
+    for e in range(3):
+        for n in ("dk", "dv"):
+            assert not got[n][e, :, kl[e]:].any(), n
+    for n, heads in (("o", [0]), ("o2", [0, 1, 2]), ("lse", list(range(6))), ("dq", [0, 3]), ("dk", [0, 3]), ("dv", [0])):
+        assert torch.equal(got[n][:, heads], want[n][:, heads]), n
+    assert torch.equal(got["dlam"][0], want["dlam"][0])
+
+
 def test_fp32_magnitudes():
     """Large, small and mixed values of fp32 keep their exponents."""
     x = make(1, 2, 2, 200, 150, 64, "fp32", seed=15)
