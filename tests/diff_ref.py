@@ -84,3 +84,40 @@ def attention(q, k, v, lam, dout=None, causal=False, scale=0.0, q_len=None, k_le
         ul = half_step(lam_dtype or dtype) if n == "dlam" else u
         out[n][1].add_(ul * out[n][0].abs())
     return out
+
+
+def lam_gradient(q, k, v, lam, dout, causal=False, scale=0.0, q_len=None, k_len=None, lam_dtype=torch.float32):
+    """(value, bound) of dlam where it is summed from P_2 dP in fp32, as the kernels for bf16 do.
+    A pair's term is off by the score's sums of d exact products, (d + 32) 2^-24 of their magnitude, by the
+    exponential, 2^-22, and its argument, 2^-23 of ln P, and by dP's sums of 2 d, (2 d + 32) 2^-24 of theirs; all
+    pairs of a row alike by lse and its product with log2 e, which so stands beside the row's D_2; and the
+    terms are added in chains of at most nk + rows + 700. Nothing is rounded to bf16 but the result to lam's type."""
+    b, h2, nq, d = q.shape
+    h, kv, nk = h2 // 2, v.shape[1], k.shape[2]
+    scale = scale or 1 / math.sqrt(d)
+    e24 = 2.0 ** -24
+    f = (2 * d + max(nq * h // kv, nk) + 32) * e24
+    value, bound = torch.zeros(h, dtype=torch.float64), torch.zeros(h, dtype=torch.float64)
+    for e in range(b):
+        lq = nq if q_len is None else int(q_len[e])
+        lk = nk if k_len is None else int(k_len[e])
+        if lq == 0 or lk == 0:
+            continue
+        ok = allowed(lq, lk, lq, lk, causal)
+        for hh in range(h):
+            g = hh // (h // kv)
+            Q, K, V = q[e, h + hh, :lq].double(), k[e, kv + g, :lk].double(), v[e, g, :lk].double()
+            G = dout[e, hh, :lq].double()
+            s = (scale * Q @ K.T).masked_fill(~ok, -INF)
+            mag = (scale * Q.abs() @ K.abs().T).masked_fill(~ok, 0.0)
+            lse = torch.logsumexp(s, -1)
+            live = lse > -INF
+            ln = s - lse.masked_fill(~live, 0.0)[:, None]
+            P, dP = torch.exp(ln), G @ V.T
+            D = (P * dP).sum(-1)
+            l_err = f * mag.amax(-1) + lk * e24 + 6 * e24 * lse.abs().nan_to_num(posinf=0) + 2.0 ** -20
+            rel = (d + 32) * e24 * (1 + mag) + 2.0 ** -22 + 2 * e24 * ln.abs().nan_to_num(posinf=0)
+            value[hh] -= D[live].sum()
+            bound[hh] += (l_err * D.abs())[live].sum() + (P * (rel * dP.abs() + (2 * d + 32) * e24 * (G.abs() @ V.abs().T))).sum()
+            bound[hh] += (nk + b * nq + 700) * e24 * (P * dP.abs()).sum()
+    return value, bound + half_step(lam_dtype) * value.abs()

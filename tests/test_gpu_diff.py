@@ -649,6 +649,37 @@ def test_pieces_of_one_key_tile_keep_their_sums(cfg, ql, kl, causal, few):
             assert torch.equal(s, t), i
 
 
+@pytest.mark.parametrize("b,h,kv,nq,nk,d,causal,ql,kl", [
+    (1, 2, 2, 64, 64, 64, False, None, None),                        # the last block of dq sums
+    (2, 4, 2, 130, 300, 64, True, [130, 61], [300, 290]),
+    (1, 2, 1, 20, 9000, 64, False, None, None),                      # over parts of the keys
+    (1, 2, 1, 100, 9000, 40, False, None, [8990]),
+    (1, 66, 66, 20, 40, 64, False, None, None),                      # many heads
+    (1, 2, 2, 1000, 1100, 64, False, None, None),                    # a kernel of its own
+    (3, 3, 3, 5000, 200, 64, False, [5000, 0, 4097], None),          # and one for its parts
+    (1, 2, 2, 64, 64, 128, False, None, None),
+    (2, 4, 2, 130, 300, 96, True, [130, 61], [300, 290]),
+    (1, 2, 1, 20, 9000, 128, False, None, None),
+    (1, 2, 1, 100, 9000, 72, False, None, [8990]),
+    (1, 66, 66, 20, 40, 80, False, None, None),
+    (1, 4, 2, 1000, 1100, 128, True, None, None),
+    (3, 3, 3, 5000, 200, 128, False, [5000, 0, 4097], None),
+])
+def test_lam_gradient_far_above_its_bound(b, h, kv, nq, nk, d, causal, ql, kl):
+    """dout along a^2, other weights and signs per head: dlam is hundreds of times what its
+    roundings may be, so a part that is lost, taken twice or given to another head shows."""
+    x = make(b, h, kv, nq, nk, d, "bf16", ql, kl, seed=26, lam_dtype="fp32")
+    y = {n: t for n, t in x.items() if n != "dout"}
+    a2 = ref.attention(**y, causal=causal, q_len=ql, k_len=kl)["o2"][0]
+    weight = torch.tensor([(1 + i % 5) * (-1) ** i for i in range(h)], dtype=torch.float64)[None, :, None, None]
+    along = a2 / a2.square().mean(-1, keepdim=True).sqrt().clamp(min=1e-6)
+    x["dout"] = (weight * (along + 0.25 * x["dout"].double())).to(torch.bfloat16)  # the padding stays no number
+    want = ref.lam_gradient(**x, causal=causal, q_len=ql, k_len=kl)
+    assert bool((want[0].abs() > 100 * want[1]).all())
+    got = run(x, causal, 0.0, ql, kl)
+    ref.check("dlam", got["dlam"], want)
+
+
 def test_inputs_and_gradients_off_16_bytes():
     """Views into flat buffers, as a packed set of parameters gives them: copied, not refused."""
     x = make(1, 2, 2, 40, 50, 64, "bf16", seed=21)
