@@ -241,3 +241,31 @@ def test_the_grid_of_one_and_two_axes(kw):
     x = rand((1, 2, 60, 32), "bf16", 5).cuda()
     p = llsa.RopeParams.like(x, **kw)
     assert torch.equal(llsa.rotary(x, rope=p), llsa.rotary(x, rope=p.grid()))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("entry", ["sparse", "dense"])
+@pytest.mark.parametrize("extent,order,given", [((16, 16, 16), "raster", False), ((16, 16, 16), "tile", False), ((8, 8, 64), "raster", False), (None, "raster", True)])
+def test_attention_takes_a_grid(extent, order, given, entry, dtype):
+    """rope= of the sparse and of dense attention: the attention of the turned q and k, and its gradients turned back."""
+    g = torch.Generator().manual_seed(41)
+    q, k, v, do = (torch.randn(2, 2, 4096, 64, generator=g).to(T[dtype]).cuda() for _ in range(4))
+    rope = llsa.RopeGridParams.like(q, k, columns=(16, 24, 16), extent=extent, token_order=order, span="head" if given else "axis")
+    pos = torch.randint(0, 999, (2, 4096, 3), generator=g, dtype=torch.int32).cuda() if given else None
+
+    def attend(q, k, v, **kw):
+        return llsa.llsa_attention(q, k, v, topk=4, **kw) if entry == "sparse" else llsa.dense_attention(q, k, v, **kw)
+
+    leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+    o = attend(*leaves, rope=rope, pos=pos)
+    got = torch.autograd.grad(o, leaves, do)
+    turned = [t.detach().requires_grad_() for t in (*llsa.rotary(q, k, rope, pos=pos), v)]
+    where = grid.places(extent, None, order)[None] if pos is None else pos.cpu()
+    for t, x in zip(turned, (q, k)):
+        ref.check("turned", t, grid.turned(x.cpu(), where, (16, 24, 16), rope.span, dtype=T[dtype]))
+    want = attend(*turned)
+    dq, dk, dv = torch.autograd.grad(want, turned, do)
+    llsa.llsa_rope_grid(rope, dq, dk, dq, dk, pos=pos, inverse=True)
+    assert torch.equal(o, want)
+    for a, b in zip(got, (dq, dk, dv)):
+        assert torch.equal(a, b)
