@@ -83,6 +83,19 @@ __device__ __forceinline__ long long diff_row(const DiffArgs& a, int slice, int 
     return ((long long)(2 * b + i) * a.d.kv_heads + g) * a.d.R + r;
 }
 
+// Matrix of map i of a slice in q, k, dq and dk.
+__device__ __forceinline__ int diff_matrix(const DenseArgs& a, int slice, int i) {
+    return slice + (slice / a.kv_heads + i) * a.kv_heads;  // (2 b + i) kv_heads + g
+}
+
+// 16 results of a row from column c on, of an output of `cols` columns.
+template <typename T>
+__device__ __forceinline__ void diff_store16(T* dst, const float* o, int c, int cols) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+        if (c + i < cols) store4(dst + i, o + i);
+}
+
 // A split of the keys leaves, per part, O unnormalised [splits][2][slices R][2 d] and then
 // (maximum in units of log2, sum) pairs [splits][2][slices R], in DenseArgs::part.
 __device__ __forceinline__ long long diff_part(const DenseArgs& a, int part, int i, long long row) {

@@ -75,24 +75,6 @@ struct Bars {
     int abort_flag, last;
 };
 
-// Matrix of map i of a slice in q, k, dq and dk.
-__device__ __forceinline__ int map_slice(const DenseArgs& a, int slice, int i) {
-    const int b = slice / a.kv_heads;
-    return slice + (b + i) * a.kv_heads;  // (2 b + i) kv_heads + g
-}
-
-// 16 results of a row, of matrix `slice` of an output of `cols` columns.
-__device__ __forceinline__ void store16(float* dst, const float* o, int c, int cols) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        if (c + i < cols) store4(dst + i, o + i);
-}
-__device__ __forceinline__ void store16(__nv_bfloat16* dst, const float* o, int c, int cols) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        if (c + i < cols) store4(dst + i, o + i);
-}
-
 // Piece `id`: 128 stationary rows of a slice against a part of the stream.
 template <bool KEYS>
 __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorMap& mgv, const CUtensorMap& syqk,
@@ -156,7 +138,7 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
     tc_fence_after();
     close_ahead();  // the block has its tensor memory
     const uint32_t tbase = __shfl_sync(0xffffffffu, bar->tmem_slot, 0);
-    const int m0 = map_slice(a, slice, 0), m1 = m0 + a.kv_heads;
+    const int m0 = diff_matrix(a, slice, 0), m1 = m0 + a.kv_heads;
 
     if (warp >= kWarps) {
         regs_dec<kRegsOther>();
@@ -530,14 +512,14 @@ __device__ __forceinline__ void bwd_side(const CUtensorMap& mqk, const CUtensorM
                 // parts: dq; or dk of all parts, then dv of all parts
                 float* dst = v ? a.part + a.splits * all2 * a.d + (part * (all2 / 2) + row) * cols
                                : a.part + (part * all2 + row) * cols;
-                if (x < extent) store16(dst + col, o, col, cols);
+                if (x < extent) diff_store16(dst + col, o, col, cols);
             } else if (any) {
                 // the stationary tiles have been used up: their place takes the results
                 unsigned char* out = sX + (v ? PAIR + k * REGION : i * REGION);
                 put_chunk(out, lr, w * 2, o);
                 put_chunk(out, lr, w * 2 + 1, o + 8);
             } else if (x < extent) {
-                store16(static_cast<__nv_bfloat16*>(v ? a.dv : KEYS ? a.dk : a.dq) + row * cols + col, o, col, cols);
+                diff_store16(static_cast<__nv_bfloat16*>(v ? a.dv : KEYS ? a.dk : a.dq) + row * cols + col, o, col, cols);
             }
         }
         if (any && a.splits == 1) {

@@ -63,18 +63,6 @@ struct Bars {
     int abort_flag, last;
 };
 
-__device__ __forceinline__ int map_slice(const DenseArgs& a, int slice, int i) {
-    const int b = slice / a.kv_heads;
-    return slice + (b + i) * a.kv_heads;  // (2 b + i) kv_heads + g
-}
-
-template <typename T>
-__device__ __forceinline__ void store16(T* dst, const float* o, int c, int cols) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        if (c + i < cols) store4(dst + i, o + i);
-}
-
 struct Maps {
     const CUtensorMap &q, &g, &k, &v, &zq, &zk, &zv;
 };
@@ -113,7 +101,7 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
     Items<KEYS> first(a, sp, x0, pos, 0, stop);
     first.start(a);
     const bool any = !first.done();
-    const int m0 = map_slice(a, slice, map);  // matrix of q and k (kDv: of the first map)
+    const int m0 = diff_matrix(a, slice, map);  // matrix of q and k (kDv: of the first map)
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&bar->x_full), 1);
@@ -563,13 +551,13 @@ __device__ __forceinline__ void bwd_piece(const Maps& maps, const DiffArgs& f, i
                 // parts: dq; or dk of all parts, then dv of all parts
                 float* dst = KIND == kDv ? a.part + a.splits * all2 * a.d + (part * (all2 / 2) + row) * cols
                                          : a.part + (part * all2 + row) * cols;
-                if (x < extent) store16(dst + c, o, c, cols);
+                if (x < extent) diff_store16(dst + c, o, c, cols);
             } else if (any) {
                 // the stationary tiles have been used up: their place takes the results
                 put_chunk(sX + k * REGION, lr, w * 2, o);
                 put_chunk(sX + k * REGION, lr, w * 2 + 1, o + 8);
             } else if (x < extent) {
-                store16(static_cast<__nv_bfloat16*>(KIND == kDv ? a.dv : KEYS ? a.dk : a.dq) + row * cols + c, o, c, cols);
+                diff_store16(static_cast<__nv_bfloat16*>(KIND == kDv ? a.dv : KEYS ? a.dk : a.dq) + row * cols + c, o, c, cols);
             }
         }
         if (any && a.splits == 1) {

@@ -108,12 +108,6 @@ struct Piece {
     }
 };
 
-// Matrix of map w of a slice in q and k.
-__device__ __forceinline__ int map_slice(const DenseArgs& a, int slice, int w) {
-    const int b = slice / a.kv_heads;
-    return slice + (b + w) * a.kv_heads;  // (2 b + w) kv_heads + g
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -192,7 +186,7 @@ diff_fwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant
                         ok = pc.get<1>(&bar->pieces, i, lane, abort_flag, a);
                     }
                     if (!ok || pc.n == 0) continue;
-                    const int m0 = map_slice(a, pc.slice, 0), m1 = m0 + a.kv_heads;
+                    const int m0 = diff_matrix(a, pc.slice, 0), m1 = m0 + a.kv_heads;
                     if (keys) {
                         const int q = v % C::NQ, use = v / C::NQ;
                         if (use > 0) ok = bar_wait(smem_u32(&bar->q_free[q]), (use - 1) & 1, abort_flag, a);
