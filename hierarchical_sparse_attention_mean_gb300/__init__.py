@@ -1295,7 +1295,8 @@ def diff_attention(q, k, v, lam, causal: bool = False, scale: float = 0.0, q_len
     a tensor of one element for all heads. q_len, k_len, rope, pos and captured backward passes: as
     dense_attention (rope is for the heads of q and k as they are); with rope, bf16 stays
     in fp32 from the turn to the last rounding where that call's does, and up to 2^30
-    products of a pair of a query and a key (both maps' pairs times d), 2^32 with up to four heads."""
+    products of a pair of a query and a key (both maps' pairs times d), 2^32 with up to four heads. The
+    backward pass forms dout . o from o as it was rounded."""
     if not isinstance(lam, torch.Tensor):
         raise TypeError(f"lam must be a torch.Tensor, of one element for all heads or of [heads], not {type(lam).__name__}")
     if lam.numel() == 1:

@@ -394,8 +394,8 @@ bool dense_few_supported(const DenseShape& s) { return s.R > 0 && s.R <= (s.dtyp
 // Parts for two blocks per SM; a part has at least 256 keys, two rounds of its warps' loads.
 // Three and four rows, and two in the backward pass, take 155 to 197 registers a thread, so
 // that an SM holds one block and the parts run in two rounds: as fast as half as many parts
-// or faster (8 x 4 key heads x 16,383 keys of 128 columns, fp32: four rows backward 289 us
-// and 315, two rows forward 99 and 129).
+// or faster (8 x 4 key heads x 16,383 keys of 128 columns, fp32: four rows backward 254 us
+// now, 289 and 315 when both were measured; two rows forward 99 and 129).
 DenseSplit dense_few_split(const DenseShape& s) {
     DenseSplit p;
     long long n = 2 * kDenseSms / std::max(1, s.slices);

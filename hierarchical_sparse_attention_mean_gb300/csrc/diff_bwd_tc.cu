@@ -29,9 +29,10 @@
 // the threads read tensor memory as fragments, 8 columns of 4 rows each, and need a
 // quarter as many of those numbers as with a row of 32 columns each.
 //
-// Bound by issue: exponentials, dS, and moves between tensor memory and registers take 2,925
-// clocks per tile pair for rows and 3,785 for keys, whatever runs on the tensor cores beside them.
-// 6 heads x 16,384 tokens: 2,188 us (1,320 TFLOP/s of the 28 d), the rows' numbers 27 before that.
+// Bound by the chain of a tile: products, exponentials, dS and the moves between tensor memory and
+// registers wait for each other, 2,925 clocks per tile pair for rows and 3,785 for keys, where the
+// counters have neither the issue slots (39 %) nor the tensor cores (43 %) full.
+// 6 heads x 16,384 tokens: 2,150 us (1,342 TFLOP/s of the 28 d), the rows' numbers 31 before that.
 // Eight warps of 64 columns took 2,225; two teams of eight warps, a map each, 2,649; a ring of
 // single map tiles 2,387; S and dP loaded together 2,244.
 //
@@ -53,7 +54,7 @@ using namespace tc;
 
 constexpr int kWarps = 16, kCols = 32;  // elementwise warps: a thread takes one row and kCols columns of a tile
 // 20 warps of 96 registers at launch = 61,440: the 512 elementwise threads take 112 of
-// them, the 128 others keep 32.
+// them, of which 60 bytes a thread spill, and the 128 others keep 32.
 constexpr int kThreads = (kWarps + 4) * 32, kRegsElementwise = 112, kRegsOther = 32;
 constexpr int BT = kTileRows, D = 64;
 constexpr int REGION = BT * 128;   // bytes of 128 rows x 64 columns

@@ -20,9 +20,9 @@
 // clocks too.
 //
 // Bound by the chain of a tile, 2,700 clocks for dq, 3,200 for dk, 4,100 for dv, which copies 128
-// KB a tile. 19 heads x 16,384 tokens of 128 columns: 16.6 ms (1,554 TFLOP/s of the 40 d); 8 heads
-// over 2, 4,095 tokens in causal order 285 us. Stream tiles of 64 rows took 1.2 times as
-// long, as more, smaller copies and products do.
+// KB a tile. 19 heads x 16,384 tokens of 128 columns: this kernel 16.6 ms (1,570 TFLOP/s of the
+// 40 d), the call 17.0; 8 heads over 2, 4,095 tokens in causal order 285 us by itself, 306 in the
+// call. Stream tiles of 64 rows took 1.2 times as long, as more, smaller copies and products do.
 //
 // Roles: warps 0-15 elementwise and epilogue (a thread per row and quarter of the columns),
 // warps 16 and 17 issue the MMAs, warps 18 and 19 the copies of the two streams. Every piece

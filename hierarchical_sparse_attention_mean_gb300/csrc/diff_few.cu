@@ -282,10 +282,12 @@ int launch(const DiffShape& s, const DiffArgs& a, cudaStream_t st) {
 
 // Where this is the faster way, times in us here and there (head columns d = 64):
 // bf16 against the tensor cores, which read rows by 128. One row: 8 x 4 heads x 16,383 keys 66
-//   and 70, d = 128 109 and 121; 6 heads x 65,536 keys 56 and 60; 16 heads x 256 keys 17 and 13. A
-//   pair of rows is bound by instructions (88 and 70; 156 and 121), and only where the other way
-//   needs a split and a join for little work, up to 2^22 key elements that the pairs read, are
-//   up to eight rows better off here: 4 heads x 2,048 keys 20 and 27.
+//   and 70, d = 128 109 and 121; 6 heads x 65,536 keys 56 and 60; 16 heads x 16 keys 4.9 and 6.7
+//   among others of their kind, x 256 keys 7.8 and 8.7, x 1,024 8.1 and 17.4 (from cold caches the
+//   two are closest at 256 keys: 16 heads 13 and 14, 64 heads 16 and 15). A pair of rows is bound by
+//   instructions (88 and 70; 156 and 121), and only where the other way needs a split and a join for
+//   little work, up to 2^22 key elements that the pairs read, are up to eight rows better off here:
+//   4 heads x 2,048 keys 20 and 27.
 // fp32 against three planes of every operand, which are written first: 8 x 4 heads x 16,383 keys
 //   two rows 109 and 513, four 156 and 574, eight 281 and 640, sixteen 550 and 639; 64 x 16 heads
 //   x 64 keys four 101 and 156, eight 187 and 255, sixteen 357 and 261; x 16 keys four 87 and 104,

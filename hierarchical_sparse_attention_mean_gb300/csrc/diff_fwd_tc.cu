@@ -19,7 +19,7 @@
 // Bound by the tensor cores: 1,536 clocks per 128 x 128 pairs at 64 columns, where the
 // exponentials of both maps take 1,024. 19 heads x 16,384 tokens of 64 columns: 2,359 us, 1,660
 // TFLOP/s, 85 % of what a large matrix product was measured at; of 128 columns 6,340 us, 1,648
-// TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 120 us, 384 pieces in three rounds of 152.
+// TFLOP/s of the 16 d. 2 x 6 x 4,096 tokens, d = 64: 121 us, 384 pieces in three rounds of 152.
 // S and P of 64 keys in two places per map, so that a map's products run beside its own
 // exponentials, took 138 against 126 with cold caches: S of 64 keys reads shared memory 1.5 times as much as S of 128.
 // A piece's end behind the first tile of the next, with a place for the output rows taken from
@@ -41,7 +41,8 @@ namespace {
 using namespace tc;
 
 // 12 warps of 168 registers at launch = 64,512: 256 softmax threads take 232 of
-// them, the 128 others keep 40 (with 216, a row of S spills).
+// them, the 128 others keep 40. Of a row of S 12 bytes still spill at 64 columns, 52 at 128; with 216
+// registers so much does that 2 x 6 x 4,096 tokens take 212 us.
 constexpr int kThreads = 384, kRegsSoftmax = 232, kRegsOther = 40;
 constexpr int BM = 128, BN = 128, VC = 128;  // rows, keys, columns of V of a piece
 

@@ -12,7 +12,8 @@
 // token (two a half apart in the half layout) and walks a run of heads with its sines
 // and cosines in registers. Segments of unequal axes need not be whole 16-byte vectors:
 // the half layout takes the widest vector that divides them all, so that 16 + 24 + 24
-// columns of bf16 (halves of 8, 12 and 12) still move 8 bytes at a time.
+// columns of bf16 (halves of 8, 12 and 12) still move 8 bytes at a time. A thread has one head
+// in flight: fp32 of 20 packed heads x 2 x 4,095 tokens, half layout, 33.6 us, 73 % of a copy's rate.
 #include <math.h>
 #include <string.h>
 
@@ -302,8 +303,10 @@ int launch_grid(const llsa_rope_grid_params* p, GridArgs& a, cudaStream_t st) {
     a.units = p->layout == LLSA_ROPE_INTERLEAVED ? a.d / V : a.rot / 2 / w + (a.d - a.rot) / w;
     const int total = a.heads[0] + a.heads[1];
     const long long threads = a.rows * a.units;
-    // As many heads per thread (the sines are computed once for them) as leave one wave
-    // of resident threads; 65,535 blocks is the most that the grid's second dimension takes.
+    // As many heads per thread (the sines are computed once for them) as leave about one wave of
+    // resident threads: 2,048 per SM with 32 registers, which the interleaved layout has; the
+    // half layout's whole vectors take 40 (fp32), 51 (bf16) and 56 (bf16 into fp32), so one and a
+    // half to two waves there. 65,535 blocks is the most that the grid's second dimension takes.
     const long long want = (long long)sm_count() * 2048;
     const long long least = (total + 65534) / 65535;
     a.heads_per_thread = (int)std::min<long long>(total, std::max(least, threads * total / want));
