@@ -31,7 +31,7 @@
 //
 // Bound by the chain of a tile: products, exponentials, dS and the moves between tensor memory and
 // registers wait for each other, 2,925 clocks per tile pair for rows and 3,785 for keys, where the
-// counters have neither the issue slots (39 %) nor the tensor cores (43 %) full.
+// counters have neither the issue slots (39 %) nor the tensor cores (42 %) full.
 // 6 heads x 16,384 tokens: 2,150 us (1,342 TFLOP/s of the 28 d), the rows' numbers 31 before that.
 // Eight warps of 64 columns took 2,225; two teams of eight warps, a map each, 2,649; a ring of
 // single map tiles 2,387; S and dP loaded together 2,244.

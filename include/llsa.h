@@ -365,7 +365,7 @@ int llsa_dense_bwd(const llsa_dense_params *p, const void *q, const void *k, con
  * i * kv_heads + g of k (i = 0, 1): the first maps' heads lie before the second maps', as
  * one projection after the other writes them, and rotary positions turn q and k as
  * they are. Values have 2 d columns. A query without an allowed key gets o = 0 and
- * lse = -infinity and adds nothing to any gradient; tokens behind a length, NaN,
+ * lse = -infinity and adds nothing to any gradient, whatever lam is; tokens behind a length, NaN,
  * clamped lengths: as in llsa_dense_fwd. Outputs must not overlap inputs. */
 typedef struct llsa_diff_params {
     int batch;
